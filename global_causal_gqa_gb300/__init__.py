@@ -25,6 +25,8 @@ __all__ = [
     "gqa_rope_apply", "gqa_prefill_workspace_bytes", "gqa_attn_prefill", "gqa_kv_append",
     "gqa_decode_workspace_bytes", "gqa_attn_decode", "gqa_attn_decode_static",
     "gqa_qk_norm_rope", "gqa_qk_norm_append", "gqa_prefill_gather", "gqa_kv_append_chunk",
+    "PAGED_KV_DTYPE", "make_paged_kv", "gqa_packed_rope_append", "gqa_attn_packed",
+    "gqa_attn_paged_workspace_bytes", "gqa_attn_paged",
     "gqa_get_device_status", "gqa_get_device_diag", "gqa_watchdog_selftest",
     "gqa_status_string", "gqa_last_error_string", "gqa_device_check",
 ]
@@ -68,6 +70,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P, I, D, Z, F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_double, ctypes.c_size_t,
                          ctypes.c_float)
+        L64 = ctypes.c_int64
         sig = {
             "gqa_rope_inv_freq": ([P, I, D, D, D, D, D, D], I),
             "gqa_yarn_amplitude": ([D], D),
@@ -88,6 +91,12 @@ def lib() -> ctypes.CDLL:
                                            I),
             "gqa_kv_shared_append": ([P, I, P, P, I, I, I, P, F, P, P, P], I),
             "gqa_attn_decode_kv_shared": ([P, P, I, I, I, I, F, P, I, P, P, P, Z, P], I),
+            "gqa_packed_rope_append": ([P, L64, P, L64, P, L64, P, I, I, I, I, I, P, P, F, P, I,
+                                        P, P, P, P], I),
+            "gqa_attn_packed": ([P, L64, P, L64, P, L64, P, L64, P, P, I, I, I, I, I, I, F, P],
+                                I),
+            "gqa_attn_paged_workspace_bytes": ([I, I, I, I, I, I, I], Z),
+            "gqa_attn_paged": ([P, L64, P, P, I, I, I, I, I, I, F, P, L64, P, P, Z, P], I),
             "gqa_get_device_status": ([P], I),
             "gqa_get_device_diag": ([P, P, I], I),
             "gqa_watchdog_selftest": ([ctypes.c_int64, P], I),
@@ -287,6 +296,74 @@ def gqa_attn_decode_kv_shared(q, descs, nseq: int, Hq: int, Hkv: int, d: int, sc
                                          _ptr(k_gamma), max_len, _ptr(o), _ptr(lse),
                                          _ptr(workspace), workspace_bytes, _stream(stream))
     return _check("gqa_attn_decode_kv_shared", st, check)
+
+
+# ---- packed sequences and the paged cache --------------------------------------------------
+
+# struct gqa_paged_kv { void *k, *v; const int32 *page_table, *kv_lens;
+#                       int32 num_pages, Hkv, page_size, d, max_pages, reserved; }
+PAGED_KV_DTYPE = np.dtype([("k", "<u8"), ("v", "<u8"), ("page_table", "<u8"),
+                           ("kv_lens", "<u8"), ("num_pages", "<i4"), ("Hkv", "<i4"),
+                           ("page_size", "<i4"), ("d", "<i4"), ("max_pages", "<i4"),
+                           ("reserved", "<i4")])
+assert PAGED_KV_DTYPE.itemsize == 56
+
+
+def make_paged_kv(k_pool, v_pool, page_table, kv_lens) -> np.ndarray:
+    """The host struct gqa_paged_kv of a paged cache: k_pool, v_pool [num_pages, Hkv,
+    page_size, d] bf16, page_table [nseq, max_pages] int32, kv_lens [nseq] int32, all
+    contiguous device tensors that the caller keeps alive; pass it as `cache`."""
+    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool"), (page_table, "page_table"),
+                 (kv_lens, "kv_lens")):
+        if not t.is_contiguous():
+            raise ValueError(f"make_paged_kv: {n} must be contiguous")
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+        raise ValueError("make_paged_kv: k_pool and v_pool are [num_pages, Hkv, page_size, d]")
+    if k_pool.element_size() != 2 or v_pool.dtype != k_pool.dtype:
+        raise ValueError("make_paged_kv: the pools are bfloat16")
+    if page_table.dim() != 2 or page_table.element_size() != 4 or kv_lens.element_size() != 4 \
+            or kv_lens.numel() != page_table.shape[0]:
+        raise ValueError("make_paged_kv: page_table is int32 [nseq, max_pages], kv_lens int32 "
+                         "[nseq]")
+    num_pages, Hkv, page_size, d = k_pool.shape
+    a = np.zeros(1, dtype=PAGED_KV_DTYPE)
+    a[0] = (_ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(kv_lens), num_pages, Hkv,
+            page_size, d, page_table.shape[1], 0)
+    return a
+
+
+def gqa_packed_rope_append(q, q_stride: int, k, k_stride: int, v, v_stride: int, cu_seqlens,
+                           nseq: int, total: int, Hq: int, Hkv: int, d: int, q_gamma, k_gamma,
+                           eps: float, table, table_len: int, q_out, k_out, cache=None,
+                           stream=None, check: bool = True) -> int:
+    st = lib().gqa_packed_rope_append(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                                      _ptr(cu_seqlens), nseq, total, Hq, Hkv, d, _ptr(q_gamma),
+                                      _ptr(k_gamma), eps, _ptr(table), table_len, _ptr(q_out),
+                                      _ptr(k_out), _ptr(cache), _stream(stream))
+    return _check("gqa_packed_rope_append", st, check)
+
+
+def gqa_attn_packed(q, q_stride: int, k, k_stride: int, v, v_stride: int, o, o_stride: int, lse,
+                    cu_seqlens, nseq: int, total: int, Hq: int, Hkv: int, d: int, window: int,
+                    scale: float, stream=None, check: bool = True) -> int:
+    st = lib().gqa_attn_packed(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(o),
+                               o_stride, _ptr(lse), _ptr(cu_seqlens), nseq, total, Hq, Hkv, d,
+                               window, scale, _stream(stream))
+    return _check("gqa_attn_packed", st, check)
+
+
+def gqa_attn_paged_workspace_bytes(nseq: int, total: int, max_q: int, max_kv: int, Hq: int,
+                                   Hkv: int, d: int) -> int:
+    return lib().gqa_attn_paged_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv, d)
+
+
+def gqa_attn_paged(q, q_stride: int, cache, cu_seqlens, nseq: int, total: int, max_q: int,
+                   max_kv: int, Hq: int, window: int, scale: float, o, o_stride: int, lse,
+                   workspace, workspace_bytes: int, stream=None, check: bool = True) -> int:
+    st = lib().gqa_attn_paged(_ptr(q), q_stride, _ptr(cache), _ptr(cu_seqlens), nseq, total,
+                              max_q, max_kv, Hq, window, scale, _ptr(o), o_stride, _ptr(lse),
+                              _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check("gqa_attn_paged", st, check)
 
 
 # ---- status ---------------------------------------------------------------------------------

@@ -406,6 +406,129 @@ gqa_status gqa_attn_decode_static(const void *q, const gqa_kv_desc *descs, int n
                                         scratch, st, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ---- packed sequences and the paged cache ------------------------------------------------
+// The host-side checks that every call with packed rows or a paged cache shares.
+static bool stride_ok(int64_t stride, int heads, int d) {
+    return stride >= static_cast<int64_t>(heads) * d && (stride & 7) == 0;
+}
+
+static gqa_status check_paged(const gqa_paged_kv *c) {
+    if (!c->k || !c->v || !c->page_table || !c->kv_lens || c->num_pages <= 0 || c->Hkv <= 0 ||
+        c->max_pages <= 0 || c->reserved != 0)
+        return GQA_ERR_INVALID_ARG;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return GQA_ERR_UNSUPPORTED;
+    if (!aligned16(c->k) || !aligned16(c->v) ||
+        ((reinterpret_cast<uintptr_t>(c->page_table) |
+          reinterpret_cast<uintptr_t>(c->kv_lens)) & 3u))
+        return GQA_ERR_ALIGNMENT;
+    return GQA_OK;
+}
+
+gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k,
+                                  int64_t k_stride, const void *v, int64_t v_stride,
+                                  const int32_t *cu_seqlens, int nseq, int total, int Hq,
+                                  int Hkv, int d, const float *q_gamma, const float *k_gamma,
+                                  float eps, const float *table, int table_len, void *q_out,
+                                  void *k_out, const gqa_paged_kv *cache, gqa_stream_t stream) {
+    const bool with_q = q != nullptr;
+    if (!k || !cu_seqlens || !table || with_q != (q_out != nullptr) ||
+        (!q_out && !k_out && !cache) || (cache && !v) || nseq <= 0 || total <= 0 ||
+        (with_q && Hq <= 0) || Hkv <= 0 || table_len <= 0 || !(eps >= 0.f) ||
+        !std::isfinite(eps))
+        return GQA_ERR_INVALID_ARG;
+    if (!rope_dim_ok(d)) return GQA_ERR_UNSUPPORTED;
+    if ((with_q && !stride_ok(q_stride, Hq, d)) || !stride_ok(k_stride, Hkv, d) ||
+        (cache && !stride_ok(v_stride, Hkv, d)))
+        return GQA_ERR_INVALID_ARG;
+    // in place only where the rows lie as the dense output's
+    if ((with_q && q_out == q && q_stride != static_cast<int64_t>(Hq) * d) ||
+        (k_out && k_out == k && k_stride != static_cast<int64_t>(Hkv) * d))
+        return GQA_ERR_INVALID_ARG;
+    if ((with_q && (!aligned16(q) || !aligned16(q_out))) || !aligned16(k) ||
+        (cache && !aligned16(v)) || (k_out && !aligned16(k_out)) ||
+        (q_gamma && !aligned16(q_gamma)) || (k_gamma && !aligned16(k_gamma)) ||
+        !aligned16(table) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
+        return GQA_ERR_ALIGNMENT;
+    if (cache) {
+        const gqa_status bad = check_paged(cache);
+        if (bad != GQA_OK) return bad;
+        if (cache->Hkv != Hkv || cache->d != d) return GQA_ERR_INVALID_ARG;
+    }
+    int *st = status_ptr();
+    if (!st) return GQA_ERR_CUDA;
+    return from_cuda(gqa::launch_packed_rope_append(
+        q, q_stride, k, k_stride, v, v_stride, cu_seqlens, nseq, total, with_q ? Hq : 0, Hkv, d,
+        q_gamma, k_gamma, eps, table, table_len, q_out, k_out, cache, st,
+        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, void *o, int64_t o_stride,
+                           float *lse, const int32_t *cu_seqlens, int nseq, int total, int Hq,
+                           int Hkv, int d, int window, float scale, gqa_stream_t stream) {
+    if (!q || !k || !v || !o || !cu_seqlens || nseq <= 0 || total <= 0 || Hq <= 0 || Hkv <= 0 ||
+        (Hq % Hkv) != 0 || !(scale > 0.f) || !std::isfinite(scale))
+        return GQA_ERR_INVALID_ARG;
+    if (d != 128 || Hq / Hkv > 64) return GQA_ERR_UNSUPPORTED;
+    if (!stride_ok(q_stride, Hq, d) || !stride_ok(k_stride, Hkv, d) ||
+        !stride_ok(v_stride, Hkv, d) || !stride_ok(o_stride, Hq, d) || o == q || o == k || o == v)
+        return GQA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+        ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_seqlens)) & 3u))
+        return GQA_ERR_ALIGNMENT;
+    int *st = status_ptr();
+    if (!st) return GQA_ERR_CUDA;
+    gqa::PackedAttn a{q, k, v, o, lse, q_stride, k_stride, v_stride, o_stride, cu_seqlens,
+                      nullptr, nseq, total, total, total, Hq, Hkv, window, scale};
+    const int rc =
+        gqa::launch_packed_attn(a, nullptr, st, reinterpret_cast<cudaStream_t>(stream));
+    if (rc == GQA_ERR_CUDA) t_last_cuda_error = cudaGetLastError();
+    return static_cast<gqa_status>(rc);
+}
+
+size_t gqa_attn_paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
+                                      int Hkv, int d) {
+    if (nseq <= 0 || total <= 0 || max_q <= 0 || max_kv <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 ||
+        (Hq % Hkv) != 0)
+        return 0;
+    return gqa::paged_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv, d);
+}
+
+gqa_status gqa_attn_paged(const void *q, int64_t q_stride, const gqa_paged_kv *cache,
+                          const int32_t *cu_seqlens, int nseq, int total, int max_q, int max_kv,
+                          int Hq, int window, float scale, void *o, int64_t o_stride,
+                          float *lse, void *workspace, size_t workspace_bytes,
+                          gqa_stream_t stream) {
+    if (!q || !cache || !o || !cu_seqlens || nseq <= 0 || total <= 0 || max_q <= 0 ||
+        max_kv < max_q || Hq <= 0 || !(scale > 0.f) || !std::isfinite(scale))
+        return GQA_ERR_INVALID_ARG;
+    const gqa_status bad = check_paged(cache);
+    if (bad != GQA_OK) return bad;
+    const int Hkv = cache->Hkv, d = cache->d;
+    if ((Hq % Hkv) != 0) return GQA_ERR_INVALID_ARG;
+    if (d != 128 || Hq / Hkv > 64) return GQA_ERR_UNSUPPORTED;
+    if (!stride_ok(q_stride, Hq, d) || !stride_ok(o_stride, Hq, d) || o == q)
+        return GQA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) ||
+        ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_seqlens)) & 3u))
+        return GQA_ERR_ALIGNMENT;
+    const size_t need =
+        gqa_attn_paged_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv, d);
+    if (need) {
+        if (!workspace || workspace_bytes < need) return GQA_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return GQA_ERR_ALIGNMENT;
+    }
+    int *st = status_ptr();
+    if (!st) return GQA_ERR_CUDA;
+    gqa::PackedAttn a{q, cache->k, cache->v, o, lse, q_stride, 0, 0, o_stride, cu_seqlens,
+                      cache, nseq, total, max_q, max_kv, Hq, Hkv, window, scale};
+    const int rc =
+        gqa::launch_packed_attn(a, workspace, st, reinterpret_cast<cudaStream_t>(stream));
+    if (rc == GQA_ERR_CUDA) t_last_cuda_error = cudaGetLastError();
+    return static_cast<gqa_status>(rc);
+}
+
 gqa_status gqa_get_device_status(gqa_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return GQA_ERR_CUDA;

@@ -124,6 +124,31 @@ cudaError_t launch_qk_norm_append(gqa_kv_desc *descs, int nseq, const void *q, c
                                   int v_norm, void *q_out, int32_t *slots, int *status,
                                   cudaStream_t s);
 
+// Packed sequences and the paged cache (packed_append.cu, packed_attn.cu).  `kv_lens`,
+// `pages` of an attention call: nullptr for packed prompts (keys are the packed rows).
+cudaError_t launch_packed_rope_append(const void *q, int64_t q_stride, const void *k,
+                                      int64_t k_stride, const void *v, int64_t v_stride,
+                                      const int32_t *cu, int nseq, int total, int Hq, int Hkv,
+                                      int d, const float *q_gamma, const float *k_gamma,
+                                      float eps, const float *table, int table_len, void *q_out,
+                                      void *k_out, const gqa_paged_kv *cache, int *status,
+                                      cudaStream_t s);
+
+// What the attention kernels take: token strides in elements; for a paged call k and v are
+// the pools and `cache` describes them (packed prompts: cache == nullptr).
+struct PackedAttn {
+    const void *q, *k, *v;
+    void *o;
+    float *lse;
+    int64_t q_stride, k_stride, v_stride, o_stride;
+    const int32_t *cu;
+    const gqa_paged_kv *cache;
+    int nseq, total, max_q, max_kv, Hq, Hkv, window;
+    float scale;
+};
+int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
+size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv, int d);
+
 // Bounded-wait self-test (watchdog.cu)
 cudaError_t launch_watchdog_selftest(int64_t limit_ns, int *status, cudaStream_t s);
 

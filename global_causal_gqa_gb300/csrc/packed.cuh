@@ -1,0 +1,64 @@
+// packed.cuh -- what the kernels over packed sequences and the paged cache share: a
+// sequence's rows and lengths, checked, and the sequence that owns a packed row.
+#pragma once
+#include <cstdint>
+
+#include "gqa_attn.h"
+#include "ptx.cuh"
+
+namespace gqa {
+
+// A sequence of a packed batch: its first row, its T new tokens and its S keys.  T = 0 where
+// there is nothing to do for it.
+struct PackedSeq {
+    int row0, T, S;
+};
+
+// Bounds on a batch's sequences: rows of the packed tensors, new tokens and keys of one
+// sequence (the host's bounds), and the keys that its pages can hold.
+struct PackedBounds {
+    int total, max_q, max_kv;
+    long cap;
+};
+
+// Sequence i.  kv_lens == nullptr: packed prompts, S = T.  Numbers that contradict one
+// another or exceed a bound give T = 0 and are recorded in `status` (nullable).
+__device__ __forceinline__ PackedSeq packed_seq(const int32_t *cu, const int32_t *kv_lens, int i,
+                                                const PackedBounds &b, int *status) {
+    PackedSeq s;
+    const int r0 = __ldg(cu + i), r1 = __ldg(cu + i + 1);
+    s.row0 = r0;
+    s.T = r1 - r0;
+    if (r0 < 0 || r1 < r0 || r1 > b.total) {
+        s.T = s.S = 0;
+        set_status(status, GQA_ERR_INVALID_ARG);
+        return s;
+    }
+    s.S = kv_lens ? __ldg(kv_lens + i) : s.T;
+    if (s.T > 0) {
+        if (s.S < s.T) {
+            s.T = 0;
+            set_status(status, GQA_ERR_INVALID_ARG);
+        } else if (s.T > b.max_q || s.S > b.max_kv || s.S > b.cap) {
+            s.T = 0;
+            set_status(status, GQA_ERR_CAPACITY);
+        }
+    }
+    return s;
+}
+
+// The sequence whose rows include packed row `row` (warp-collective: every lane gets it):
+// the number of entries cu[1 .. nseq] that are <= row.  The caller checks the row against
+// that sequence's bounds, which also rejects rows behind the last sequence (the result is
+// then nseq) and offsets that are not sorted.
+__device__ __forceinline__ int packed_row_seq(const int32_t *cu, int nseq, int row) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int base = 1; base <= nseq; base += 32) {
+        const int i = base + lane;
+        n += __popc(__ballot_sync(0xffffffffu, i <= nseq && __ldg(cu + i) <= row));
+    }
+    return n;
+}
+
+}  // namespace gqa

@@ -37,7 +37,9 @@ enum DiagKernel {
     kDiagDecode = 3,
     kDiagWatchdog = 4,
     kDiagPrefillPair = 5,
-    kDiagCache = 6   // cache append, chunk gather, RoPE pass, Q/K normalisation
+    kDiagCache = 6,  // cache append, chunk gather, RoPE pass, Q/K normalisation
+    kDiagPacked = 7,      // packed / paged prefill
+    kDiagPagedDecode = 8  // paged decode
 };
 __device__ __forceinline__ void set_timeout(int *status, int kernel, int role, int barrier,
                                             int tile) {

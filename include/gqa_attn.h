@@ -36,8 +36,9 @@
  *     predecessor before reading.  A caller's own kernel launched after them with that
  *     attribute must likewise execute griddepcontrol.wait (cudaGridDependencySynchronize)
  *     before it reads their outputs.
- *   - Head dims: prefill and decode d in {128, 256, 512}; kv_append, rope_apply and the
- *     Q/K normalisation d in {64, 128, 256, 512}.  Query group G = Hq/Hkv must be an
+ *   - Head dims: prefill and decode d in {128, 256, 512}, their packed and paged forms
+ *     d = 128; kv_append, rope_apply, the packed append and the Q/K normalisation d in
+ *     {64, 128, 256, 512}.  Query group G = Hq/Hkv must be an
  *     integer; decode needs G <= 8.  Other values return GQA_ERR_UNSUPPORTED.
  */
 #ifndef GQA_ATTN_H
@@ -299,6 +300,95 @@ gqa_status gqa_attn_decode_static(const void *q, const gqa_kv_desc *descs, int n
                                   int Hkv, int d, float scale, int max_len, void *o,
                                   float *lse, gqa_stream_t stream);
 
+/* ---- Packed sequences and the paged cache ------------------------------------------------
+ * A packed batch holds the tokens of nseq sequences of different lengths behind one another:
+ * sequence i owns rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 of token-major tensors
+ * [total, heads, d] (cu_seqlens: device int32[nseq + 1], non-decreasing, cu_seqlens[0] >= 0).
+ * `total` is the number of rows of the tensors, cu_seqlens[nseq] <= total; rows that belong to
+ * no sequence are neither read nor written.  A sequence may be empty.  Each tensor has a token
+ * stride in elements, a multiple of 8 and at least heads * d (heads are d apart), so that q, k
+ * and v may be column slices of the rows of one fused QKV projection (§4.1: 8192 q, 1024 k,
+ * 1024 v columns in PLaMo 3 31B).
+ *
+ * A paged cache keeps each sequence's keys and values in pages of page_size tokens of one
+ * pool: token j of sequence i lies in row j mod page_size of page page_table[i][j / page_size],
+ * for every KV head.  Unlike the caches of gqa_kv_desc it holds keys AFTER RoPE (a cache that
+ * stores rotated keys, as Gemma's does, §4.4): each key is rotated once, when it is written,
+ * and a page can be shared by sequences with a common prefix.  kv_lens[i] counts the tokens
+ * of sequence i with the new ones of this step: S = kv_lens[i], T = cu_seqlens[i+1] -
+ * cu_seqlens[i] new tokens at positions S - T .. S - 1, T <= S.  The struct lives in host
+ * memory and is read during the call; page_table and kv_lens are device memory and are read
+ * when the kernels run, so a captured call follows their later contents.
+ *
+ * A sequence whose numbers are inconsistent (offsets that decrease or pass `total`, T > S)
+ * is skipped, its outputs left as they were, and the status word records
+ * GQA_ERR_INVALID_ARG; one that exceeds a bound given by the host (max_q, max_kv, the pages
+ * of its table row) is skipped and records GQA_ERR_CAPACITY.  A page-table entry outside the
+ * pool records GQA_ERR_INVALID_ARG: nothing is written there, and zeros are read instead. */
+typedef struct gqa_paged_kv {
+    void *k;                    /* device [num_pages, Hkv, page_size, d] bf16, after RoPE */
+    void *v;                    /* device, the same shape */
+    const int32_t *page_table;  /* device [nseq, max_pages] */
+    const int32_t *kv_lens;     /* device [nseq] */
+    int32_t num_pages;
+    int32_t Hkv;
+    int32_t page_size;          /* 16, 32, 64 or 128 */
+    int32_t d;
+    int32_t max_pages;          /* entries of a page_table row */
+    int32_t reserved;           /* 0 */
+} gqa_paged_kv;
+
+/* What a step does to the new tokens between the QKV projection and attention (§4.3, §4.4):
+ * for each token at position p = S - T + t of its sequence
+ *   q_out = RoPE_p(N_{q_gamma}(q)),   key = RoPE_p(N_{k_gamma}(k)),   value = v,
+ * the key and the value written to the sequence's page, the key also to k_out.  N is the
+ * RMSNorm of the section above (fp32, gain device fp32 [d]); q_gamma NULL: q is not
+ * normalised, k_gamma likewise.  Everything between the load and the one rounding to bf16 is
+ * fp32.  q_out [total, Hq, d] and k_out [total, Hkv, d] are dense, either may be NULL; q_out
+ * may be q (k_out may be k) if that tensor's stride is dense.  q and q_out are NULL together
+ * (Hq ignored).  cache NULL: no cache is written, v is not read and may be NULL, and every
+ * sequence starts at position 0 (the prompts of gqa_attn_packed).  With a cache, Hkv and d
+ * must be the cache's.  A position at or past table_len records GQA_ERR_RANGE and its token
+ * is skipped.  d in {64, 128, 256, 512}.  One kernel.  Two sequences of one call must not
+ * append to the same page. */
+gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k,
+                                  int64_t k_stride, const void *v, int64_t v_stride,
+                                  const int32_t *cu_seqlens, int nseq, int total, int Hq,
+                                  int Hkv, int d, const float *q_gamma, const float *k_gamma,
+                                  float eps, const float *table, int table_len, void *q_out,
+                                  void *k_out, const gqa_paged_kv *cache,
+                                  gqa_stream_t stream);
+
+/* Attention over whole prompts of different lengths: within each sequence query t attends to
+ * keys j <= t (window > 0: also t - j < window).  q, k after RoPE, q [total, Hq, d], k, v
+ * [total, Hkv, d], o [total, Hq, d] with token strides; o may not alias an input.  lse
+ * [Hq, total] float32 natural-log sum of exp of the scaled scores, or NULL.  scale finite and
+ * > 0.  A row never depends on keys or values that its mask hides, not even through NaN or
+ * infinities in them.  d = 128; Hq / Hkv an integer of at most 64. */
+gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, void *o, int64_t o_stride,
+                           float *lse, const int32_t *cu_seqlens, int nseq, int total, int Hq,
+                           int Hkv, int d, int window, float scale, gqa_stream_t stream);
+
+/* Attention of each sequence's new tokens over its paged cache (which holds them already: call
+ * after gqa_packed_rope_append): T = 1 is a decode step, a few are a draft being checked, many
+ * a chunk of a prompt; a batch may mix them.  Query t sits at position S - T + t and attends
+ * to keys j <= S - T + t (window > 0: also with S - T + t - j < window; pages that lie wholly
+ * below every window are not read and their table entries may be stale).  q [total, Hq, d]
+ * after RoPE, o [total, Hq, d], lse as for gqa_attn_packed.  max_q and max_kv: upper bounds on
+ * T and S over the batch; they and the shape choose the kernel and its split of the keys, and
+ * size the workspace (gqa_attn_paged_workspace_bytes with the same arguments; 0 = none
+ * needed).  Its contents need no initialisation; calls that may overlap need one each.  Every
+ * result is the same on every run of the same call.  d = 128; Hq / Hkv an integer of at most
+ * 64; max_q <= max_kv. */
+size_t gqa_attn_paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
+                                      int Hkv, int d);
+gqa_status gqa_attn_paged(const void *q, int64_t q_stride, const gqa_paged_kv *cache,
+                          const int32_t *cu_seqlens, int nseq, int total, int max_q, int max_kv,
+                          int Hq, int window, float scale, void *o, int64_t o_stride,
+                          float *lse, void *workspace, size_t workspace_bytes,
+                          gqa_stream_t stream);
+
 /* ---- Status ----------------------------------------------------------------------------
  * Waits for `stream`, then returns and clears the current device's status word
  * (GQA_OK if no device-side error was recorded since the last call). */
@@ -310,7 +400,7 @@ gqa_status gqa_get_device_status(gqa_stream_t stream);
  * (kernel << 24) | (role << 20) | (barrier << 16) | (tile index & 0xffff), kernel 1 =
  * prefill d=128, 2 = prefill d=256, 3 = decode, 4 = gqa_watchdog_selftest,
  * 5 = prefill d=512 (a pair of CTAs), 6 = cache append, chunk gather, RoPE pass, Q/K
- * normalisation.  A library compiled with -DGQA_DEBUG_BOUNDS checks the indices of the
+ * normalisation, 7 = packed / paged prefill, 8 = paged decode.  A library compiled with -DGQA_DEBUG_BOUNDS checks the indices of the
  * global accesses it derives from device-side data; the first failed check records
  * GQA_ERR_DEVICE_BOUNDS and, in diag[0], (kernel << 24) | (1 << 23) | site, and the access
  * is skipped.  For diagnosing device-side errors; gqa_get_device_status leaves the codes
