@@ -124,7 +124,8 @@ cudaError_t launch_qk_norm_append(gqa_kv_desc *descs, int nseq, const void *q, c
                                   int v_norm, void *q_out, int32_t *slots, int *status,
                                   cudaStream_t s);
 
-// Packed sequences and the paged cache (packed_append.cu, packed_attn.cu).  `kv_lens`,
+// Packed sequences and the paged cache (packed_append.cu, packed_prefill.cu,
+// packed_attn.cu).  `kv_lens`,
 // `pages` of an attention call: nullptr for packed prompts (keys are the packed rows).
 cudaError_t launch_packed_rope_append(const void *q, int64_t q_stride, const void *k,
                                       int64_t k_stride, const void *v, int64_t v_stride,
@@ -146,6 +147,9 @@ struct PackedAttn {
     int nseq, total, max_q, max_kv, Hq, Hkv, window;
     float scale;
 };
+// the tensor-core kernel for prompts and chunks (packed_prefill.cu); returns a gqa_status
+int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
+size_t packed_prefill_workspace_bytes(int total, int max_kv, int Hq, int Hkv);
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
 size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv, int d);
 

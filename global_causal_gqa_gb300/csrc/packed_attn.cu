@@ -19,6 +19,9 @@ namespace {
 
 constexpr int kD = 128;
 
+// A paged call whose sequences bring at most 32 rows (tokens times heads of a group) each.
+bool few_rows(int max_q, int G) { return static_cast<long>(max_q) * G <= 32; }
+
 struct RowParams {
     const __nv_bfloat16 *q, *k, *v;
     __nv_bfloat16 *o;
@@ -86,9 +89,14 @@ __global__ void packed_attn_row_kernel(const RowParams p) {
 
 }  // namespace
 
-size_t paged_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
+size_t paged_workspace_bytes(int, int total, int max_q, int max_kv, int Hq, int Hkv, int) {
+    if (few_rows(max_q, Hq / Hkv)) return 0;
+    return packed_prefill_workspace_bytes(total, max_kv, Hq, Hkv);
+}
 
-int launch_packed_attn(const PackedAttn &a, void *, int *status, cudaStream_t s) {
+int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
+    if (!a.cache || !few_rows(a.max_q, a.Hq / a.Hkv))
+        return launch_packed_prefill(a, ws, status, s);
     RowParams p{};
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.k = static_cast<const __nv_bfloat16 *>(a.k);

@@ -1,0 +1,1166 @@
+// packed_prefill.cu -- tcgen05 attention over packed prompts, and of chunks of new tokens over
+// a paged cache (d = 128).
+//
+// Within a sequence of S keys whose last T tokens are queries ("PLaMo 3アーキテクチャ徹底解析"
+// §4.2, §4.5, §5.1), for query token t at position i = S - T + t and head h of KV head g:
+//   o = sum_j softmax_j(scale q . k_j) v_j  over j <= i (and i - j < W with a window).
+// S = Q K^T and O += P V run as 128 x 128 tiles on the tensor cores with fp32 accumulators in
+// tensor memory; the softmax is one online pass (running maximum and sum in fp32), and only
+// the key tiles that some query of the block sees are loaded.
+//
+// Rows.  A tile's 128 rows are 128/G tokens times the G = Hq/Hkv query heads that share a KV
+// head (row = token * G + head), so that a short chunk or a single token still fills rows
+// with everything its keys are read for, and the keys are read once for all of them.  A work
+// item is (sequence, KV head, two such tiles of consecutive tokens[, a span of the keys]): both
+// tiles share every K and V load.  Q, and O on its way out, are one TMA box of {64 dims, G
+// heads, 128/G tokens} per half of the head dimension.
+//
+// Keys come as TMA boxes of 128 rows of the packed tensor, or one box per page of a paged
+// cache; a box outside the tensor (a page that is not needed, or a bad entry) is zero fill.
+//
+// Items are claimed with cluster launch control: the grid has an upper bound of CTAs (the
+// lengths are known on the device only), the CTAs that get an SM take over the items of CTAs
+// not yet launched.  The producer warp turns an item's number into its sequence, rows and
+// key range (a scan over the sequences' item counts, resumed where the last one stopped,
+// since the numbers only grow) and publishes it through a 4-slot ring in shared memory.
+// Within a sequence the blocks with the most keys come first.
+//
+// Warp roles (12 warps; 96 registers for warps 0-3, 200 for the softmax warps):
+//   warp 0      work claiming and TMA loads: Q of the item, K and V through a 4-slot ring.
+//   warp 1      tensor-memory owner and the single MMA-issuing thread.
+//   warp 2      TMA stores of O.
+//   warp 3      the V guard (below).
+//   warps 4-7   softmax + epilogue of tile 0, warps 8-11 of tile 1: a thread per row.
+// Tensor memory: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512); P (bf16) overwrites
+// the first 64 columns of its S tile and is the PV product's operand from there; S_i(j+1) is
+// issued once PV_i(j) has completed.  O is rescaled only when a row's maximum grows by more
+// than 2^8 (exact: O and the sum share one reference maximum).
+//
+// The V guard.  A hidden key has weight 0, but 0 * NaN is NaN, so a value that no row may see
+// must not reach the product as NaN or infinity: rows past a sequence's end belong to another
+// sequence or to no one.  In the tiles that straddle an edge of the mask, warp 3 zeroes the
+// rows that no row of the item sees, and in those that only some rows see it replaces
+// non-finite elements by 0 and marks the key; the epilogue then adds a marked key's
+// non-finite elements to the rows that do see it.  Without such values the cost is reading
+// the edge rows of two tiles per item, off the critical path.
+//
+// Shared memory: Q 64 KB, ring 4 x 32 KB, O staging 2 x 16 KB (one half of the columns of
+// each tile at a time).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "internal.h"
+#include "packed.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kBM = 128;
+constexpr int kBN = 128;
+constexpr int kSlots = 4;                     // K/V ring depth
+constexpr int kBoxBytes = 128 * 128;          // 128 rows x 64 bf16 (one 128-byte swizzle span)
+constexpr int kTileBytes = 2 * kBoxBytes;     // 128 rows x 128 bf16
+constexpr int kSmemQ = 0;
+constexpr int kSmemRing = 2 * kTileBytes;
+constexpr int kSmemStage = kSmemRing + kSlots * kTileBytes;
+constexpr int kSmemBar = kSmemStage + 2 * kBoxBytes;
+constexpr int kSmemBytes = kSmemBar + 1024 + 1024;  // + barriers + alignment slack
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleThreshold = 8.0f;     // log2 units
+constexpr int kItemSlots = 4;
+constexpr int kItemReaders = 11;              // MMA thread, warps 2 and 3, 8 softmax warps
+constexpr int kSMs = 152;
+
+// A work item as the producer publishes it.  n_tiles < 0: no more items.
+struct ItemRec {
+    int row0;       // packed row of the item's first token
+    int ntok;       // its tokens
+    int qpos0;      // position of the first one
+    int g;          // KV head
+    int kt_first;   // first key tile
+    int n_tiles;
+    int seq;
+    int kv_row0;    // packed prompts: row of the sequence's key 0
+    int split;      // span of the keys, -1: all of them (the result is final)
+};
+
+struct Slot {
+    ItemRec it;
+    uint32_t any_bad;
+    uint32_t bad[16];   // marked keys: [0, 8) after qpos0, [8, 16) from the window's lower edge
+};
+
+struct Bars {
+    uint4 clc_resp;
+    Slot slot[kItemSlots];
+    uint64_t clc_full;
+    uint64_t item_full[kItemSlots], item_free[kItemSlots];
+    uint64_t q_full, q_free;
+    uint64_t full[kSlots], empty[kSlots];         // K/V ring
+    uint64_t guard_go[2], guard[2];               // a guarded V tile is there / is clean (alternate)
+    uint64_t s_full[2], p_full[2], o_done[2];     // per query tile
+    uint64_t o_final[2];                          // an item's last PV product of the tile
+    uint64_t o_free[2];                           // the epilogue has read O out of TMEM
+    uint64_t staged[2], stage_free[2];            // O halves in shared memory
+    uint64_t mma_done;
+    uint32_t tmem_base;
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block");
+
+struct Params {
+    __nv_bfloat16 *o;
+    const __nv_bfloat16 *v;        // for the marked keys of the V guard
+    float *lse;
+    float *ws_ml, *ws_o;           // partials of split items
+    const int32_t *cu, *kv_lens, *pages;
+    int *status;
+    long o_stride, v_stride;
+    PackedBounds bounds;
+    int nseq, Hq, Hkv, G, Mt, window;    // Mt = 128 / G tokens per tile
+    int num_pages, page_size, max_pages;
+    int split_tiles;               // key tiles of a span; 0: items are not split
+    int q_box_bytes;               // bytes of one Q box
+    float scale_log2;
+};
+
+// Key tiles of a block of tokens at positions [q_lo, q_hi].
+__host__ __device__ __forceinline__ int first_tile(int q_lo, int window) {
+    return window > 0 && q_lo - window + 1 > 0 ? (q_lo - window + 1) / kBN : 0;
+}
+// Most key tiles of any block of `ntok` tokens of a sequence with S keys.
+__host__ __device__ __forceinline__ int most_tiles(int S, int ntok, int window) {
+    const int all = (S + kBN - 1) / kBN;
+    // a span of window + ntok - 1 keys touches at most this many tiles
+    const long w = window > 0 ? ((long)window + ntok - 2) / kBN + 2 : all;
+    return w < all ? static_cast<int>(w) : all;
+}
+__host__ __device__ __forceinline__ int n_spans(int tiles, int split_tiles) {
+    return split_tiles > 0 ? (tiles + split_tiles - 1) / split_tiles : 1;
+}
+
+// A bounded wait whose outcome every lane of the warp agrees on.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+enum Role { kRoleProducer = 0, kRoleMma = 1, kRoleSoftmax = 2, kRoleAux = 3 };
+
+// The producer's walk over the sequences: one block of 32 in the lanes at a time.
+struct Walk {
+    int base = -32;        // first sequence of the block in the lanes
+    int before = 0, here = 0;   // items before the block, in the block
+    PackedSeq s{0, 0, 0};  // this lane's sequence
+    int count = 0, incl = 0;    // its items, and the inclusive sum over the lanes
+};
+
+__device__ __forceinline__ void walk_to(const Params &p, Walk &w, int base) {
+    const int lane = threadIdx.x & 31;
+    w.before += w.here;
+    w.base = base;
+    const int i = base + lane;
+    w.count = 0;
+    if (i < p.nseq) {
+        w.s = packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status);
+        if (w.s.T > 0) {
+            const int ntok = 2 * p.Mt;
+            w.count = (w.s.T + ntok - 1) / ntok * p.Hkv *
+                      n_spans(most_tiles(w.s.S, ntok, p.window), p.split_tiles);
+        }
+    }
+    w.incl = w.count;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, w.incl, d);
+        if (lane >= d) w.incl += x;
+    }
+    w.here = __shfl_sync(0xffffffffu, w.incl, 31);
+}
+
+// Item `idx` (not below the last one asked for): 1 and the item, 0 if that number has no
+// work (a span past the block's keys), -1 past the last item.  Warp-collective.
+__device__ int find_item(const Params &p, Walk &w, int idx, ItemRec &it) {
+    while (w.base < 0 || idx >= w.before + w.here) {
+        if (w.base + 32 >= p.nseq) return -1;
+        walk_to(p, w, w.base + 32);
+    }
+    const int rel = idx - w.before;
+    const int lane_s = __ffs(__ballot_sync(0xffffffffu, w.incl > rel)) - 1;
+    const int row0 = __shfl_sync(0xffffffffu, w.s.row0, lane_s);
+    const int T = __shfl_sync(0xffffffffu, w.s.T, lane_s);
+    const int S = __shfl_sync(0xffffffffu, w.s.S, lane_s);
+    int r = rel - __shfl_sync(0xffffffffu, w.incl - w.count, lane_s);
+    const int ntok = 2 * p.Mt, blocks = (T + ntok - 1) / ntok;
+    const int spans = n_spans(most_tiles(S, ntok, p.window), p.split_tiles);
+    const int split = r % spans;
+    r /= spans;
+    it.g = r % p.Hkv;
+    const int t0 = (blocks - 1 - r / p.Hkv) * ntok;
+    it.seq = w.base + lane_s;
+    it.row0 = row0 + t0;
+    it.ntok = min(ntok, T - t0);
+    it.qpos0 = S - T + t0;
+    it.kv_row0 = row0;
+    it.kt_first = first_tile(it.qpos0, p.window);
+    it.n_tiles = (it.qpos0 + it.ntok - 1) / kBN - it.kt_first + 1;
+    it.split = -1;
+    if (p.split_tiles > 0 && it.n_tiles > p.split_tiles) {
+        it.split = split;
+        it.kt_first += split * p.split_tiles;
+        it.n_tiles = min(p.split_tiles, it.n_tiles - split * p.split_tiles);
+        return it.n_tiles > 0 ? 1 : 0;
+    }
+    return split == 0 ? 1 : 0;
+}
+
+// Item k as a reader role sees it (false: the wait expired).
+__device__ __forceinline__ bool read_item(Bars *bars, int k, ItemRec &it) {
+    if (!mbar_wait(&bars->item_full[k & (kItemSlots - 1)], (k / kItemSlots) & 1)) return false;
+    it = bars->slot[k & (kItemSlots - 1)].it;
+    return true;
+}
+
+// What the mask makes of an item's keys: rows of V outside [lo, hi] are hidden from every
+// row, those in [lo, lo_all) and (hi_all, hi] from some.
+struct Edges {
+    int lo, lo_all, hi_all, hi;
+    __device__ Edges(const ItemRec &it, int window) {
+        hi_all = it.qpos0;
+        hi = it.qpos0 + it.ntok - 1;
+        lo = window > 0 ? max(0, it.qpos0 - window + 1) : 0;
+        lo_all = window > 0 ? max(0, hi - window + 1) : 0;
+    }
+    __device__ bool guarded(int n0) const { return n0 < lo_all || n0 + kBN - 1 > hi_all; }
+};
+
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {   // of the two bf16 in w
+    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// Adds the non-finite ones of 64 value elements to a row's staged half (bf16), row r at
+// `stage` + 128 r, 16-byte chunks swizzled or not.
+__device__ __noinline__ void add_marked(uint8_t *stage, int r, bool swizzled,
+                                        const __nv_bfloat16 *v) {
+    for (int c = 0; c < 64; ++c) {
+        const float x = __bfloat162float(v[c]);
+        if (isfinite(x)) continue;
+        const int chunk = swizzled ? (c >> 3) ^ (r & 7) : c >> 3;
+        __nv_bfloat16 *e = reinterpret_cast<__nv_bfloat16 *>(stage + r * 128 + chunk * 16) + (c & 7);
+        *e = __float2bfloat16_rn(__bfloat162float(*e) + x);
+    }
+}
+
+template <bool PAGED>
+__device__ __forceinline__ const __nv_bfloat16 *value_row(const Params &p, const ItemRec &it,
+                                                          int key) {
+    if constexpr (!PAGED) {
+        return p.v + (long)(it.kv_row0 + key) * p.v_stride + it.g * kD;
+    } else {
+        // a marked key came from a page inside the pool (anything else is read as zeros)
+        const int page = p.pages[(long)it.seq * p.max_pages + key / p.page_size];
+        return p.v + (((long)page * p.Hkv + it.g) * p.page_size + key % p.page_size) * kD;
+    }
+}
+
+template <bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_prefill_kernel(const __grid_constant__ CUtensorMap tmQ,
+                          const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV,
+                          const __grid_constant__ CUtensorMap tmO, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    // 1024-byte alignment for the 128-byte swizzle atoms
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    Bars *bars = reinterpret_cast<Bars *>(smem + kSmemBar);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&bars->clc_full, 1);
+        for (int i = 0; i < kItemSlots; ++i) {
+            mbar_init(&bars->item_full[i], 1);
+            mbar_init(&bars->item_free[i], kItemReaders);
+        }
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_free, 1);
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->guard_go[i], 1);
+            mbar_init(&bars->guard[i], 32);
+            mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_full[i], 128);
+            mbar_init(&bars->o_done[i], 1);
+            mbar_init(&bars->o_final[i], 1);
+            mbar_init(&bars->o_free[i], 128);
+            mbar_init(&bars->staged[i], 128);
+            mbar_init(&bars->stage_free[i], 1);
+        }
+        mbar_init(&bars->mma_done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&bars->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+
+    // Register split (launch: 384 threads x 168): 128 x 96 + 256 x 200 <= 384 x 168.
+    if (warp < 4) {
+        reg_dealloc<96>();
+        if (warp == 0) {
+            // ================= work claiming, TMA loads =================
+            if (lane == 0) {
+                tma_prefetch_desc(&tmQ);
+                tma_prefetch_desc(&tmK);
+                tma_prefetch_desc(&tmV);
+                tma_prefetch_desc(&tmO);
+            }
+            bool ok = true;
+            int u = 0;        // ring loads issued
+            int nq = 0;       // items whose Q tiles have been issued
+            int claims = 0;   // responses asked for
+            Walk walk;
+            auto fail = [&](int barrier, int at) {
+                ok = false;
+                set_timeout(p.status, kDiagPacked, kRoleProducer, barrier, at);
+            };
+            auto claim = [&]() {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars->clc_full, 16);
+                    clc_try_cancel(&bars->clc_resp, &bars->clc_full);
+                }
+                ++claims;
+            };
+            // the claimed number, -1 when nothing was left
+            auto claimed = [&]() {
+                if (!warp_wait(&bars->clc_full, (claims - 1) & 1)) {
+                    fail(3, claims);
+                    return -1;
+                }
+                const int x = clc_decode(&bars->clc_resp);
+                fence_proxy_async_smem();   // read before the next response overwrites it
+                __syncwarp();
+                return x;
+            };
+            // the next item from number `idx` on, claiming further numbers while they have no
+            // work; it.n_tiles = -1 when there is none
+            auto settle = [&](int idx, ItemRec &it) {
+                while (true) {
+                    const int r = idx < 0 ? -1 : find_item(p, walk, idx, it);
+                    if (r > 0) return;
+                    if (r < 0) break;
+                    claim();
+                    idx = claimed();
+                    if (!ok) break;
+                }
+                it.n_tiles = -1;
+            };
+            auto publish = [&](int k, const ItemRec &it) {
+                Slot &s = bars->slot[k & (kItemSlots - 1)];
+                if (k >= kItemSlots &&
+                    !warp_wait(&bars->item_free[k & (kItemSlots - 1)], (k / kItemSlots - 1) & 1)) {
+                    fail(2, k);
+                    return;
+                }
+                if (lane < 16) s.bad[lane] = 0;
+                if (lane == 0) {
+                    s.it = it;
+                    s.any_bad = 0;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->item_full[k & (kItemSlots - 1)]);
+            };
+            auto load_q = [&](int k, const ItemRec &it) {
+                if (k >= 1 && !warp_wait(&bars->q_free, (k - 1) & 1)) {
+                    fail(0, k);
+                    return;
+                }
+                const int ntile = it.ntok > p.Mt ? 2 : 1;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars->q_full, ntile * 2 * p.q_box_bytes);
+                    for (int i = 0; i < ntile; ++i)
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_3d(smem + kSmemQ + i * kTileBytes + h * kBoxBytes, &tmQ,
+                                        &bars->q_full, 64 * h, it.g * p.G, it.row0 + i * p.Mt);
+                }
+                __syncwarp();
+                nq = k + 1;
+            };
+            ItemRec it;
+            settle(blockIdx.x, it);
+            for (int k = 0; ok; ++k) {
+                publish(k, it);
+                if (!ok || it.n_tiles < 0) break;
+                claim();   // one item ahead
+                const Edges e(it, p.window);
+                // pages of a key tile: lane i holds the slab of the tile's i-th page, -1 for
+                // one that no row sees or that is not in the pool (its box is zero fill)
+                const int npg = PAGED ? kBN / p.page_size : 1;
+                auto slab_of = [&](int n0) {
+                    int slab = -1;
+                    if (lane < npg) {
+                        const int key0 = n0 + lane * p.page_size;
+                        if (key0 <= e.hi && key0 + p.page_size > e.lo) {
+                            const int pg = __ldg(p.pages + (long)it.seq * p.max_pages +
+                                                 key0 / p.page_size);
+                            if (pg >= 0 && pg < p.num_pages) slab = pg * p.Hkv + it.g;
+                            else set_status(p.status, GQA_ERR_INVALID_ARG);
+                        }
+                    }
+                    return slab;
+                };
+                int slab = 0, slab_next = 0;
+                if constexpr (PAGED) slab = slab_of(it.kt_first * kBN);
+                if (k == 0) load_q(k, it);
+                for (int l = 0; l < 2 * it.n_tiles && ok; ++l) {
+                    const int n0 = (it.kt_first + (l >> 1)) * kBN;
+                    if constexpr (PAGED)
+                        if (!(l & 1) && l + 2 < 2 * it.n_tiles) slab_next = slab_of(n0 + kBN);
+                    const int st = u % kSlots;
+                    if (u >= kSlots && !warp_wait(&bars->empty[st], (u / kSlots - 1) & 1)) {
+                        fail(1, u);
+                        break;
+                    }
+                    uint8_t *dst = smem + kSmemRing + st * kTileBytes;
+                    const CUtensorMap *map = (l & 1) ? &tmV : &tmK;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], kTileBytes);
+                    __syncwarp();
+                    if constexpr (PAGED) {
+                        if (lane < npg) {
+                            uint8_t *d = dst + lane * p.page_size * 128;
+                            tma_load_3d(d, map, &bars->full[st], 0, 0, slab);
+                            tma_load_3d(d + kBoxBytes, map, &bars->full[st], 64, 0, slab);
+                        }
+                    } else if (lane < 2) {
+                        tma_load_3d(dst + lane * kBoxBytes, map, &bars->full[st], 64 * lane, it.g,
+                                    it.kv_row0 + n0);
+                    }
+                    __syncwarp();
+                    ++u;
+                    if constexpr (PAGED)
+                        if (l & 1) slab = slab_next;
+                    // Q after the item's first K and V: by then the previous item's last
+                    // score products, which still read the buffer, are near
+                    if (l == 1 && k > 0) load_q(k, it);
+                }
+                if (!ok) break;
+                const int next = claimed();
+                if (!ok) break;
+                settle(next, it);
+            }
+            if (!ok) {
+                // never leave the CTA with copies in flight
+                for (int w = max(0, u - kSlots); w < u; ++w)
+                    mbar_wait(&bars->full[w % kSlots], (w / kSlots) & 1);
+                if (nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1);
+                if (claims > 0) mbar_wait(&bars->clc_full, (claims - 1) & 1);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ================= MMA issuer =================
+            if (lane == 0) {
+                const uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, 0, 0);
+                const uint32_t idesc_o = idesc_bf16_f32(kBM, kD, 0, 1);
+                const uint32_t ring0 = smem_u32(smem + kSmemRing);
+                const uint32_t q0 = smem_u32(smem + kSmemQ);
+                bool ok = true;
+                int u = 0;                 // ring slots consumed
+                int gc = 0;                // guarded V tiles consumed
+                int cpv[2] = {0, 0};       // PV products issued, per query tile (all items)
+                int nepi[2] = {0, 0};      // items finished, per query tile
+                auto fail = [&](int barrier, int at) {
+                    ok = false;
+                    set_timeout(p.status, kDiagPacked, kRoleMma, barrier, at);
+                };
+                auto take = [&](int &st) {
+                    st = u % kSlots;
+                    if (!mbar_wait(&bars->full[st], (u / kSlots) & 1)) {
+                        fail(1, u);
+                        return;
+                    }
+                    ++u;
+                    tc_fence_after();
+                };
+                auto issue_s = [&](int i, int st) {
+                    const uint32_t ka = ring0 + st * kTileBytes, qa = q0 + i * kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kD / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+                        umma_ss(tmem + i * 128, sdesc_sw128(qa + off, 16, 1024),
+                                sdesc_sw128(ka + off, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    umma_commit(&bars->s_full[i]);
+                };
+                auto issue_pv = [&](int i, int st, bool acc) {
+                    const uint32_t va = ring0 + st * kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kBN / 16; ++kk)
+                        umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8,
+                                sdesc_sw128(va + kk * 16 * 128, kBoxBytes, 1024), idesc_o,
+                                (acc || kk > 0) ? 1u : 0u);
+                    umma_commit(&bars->o_done[i]);
+                    ++cpv[i];
+                };
+                // waits until PV product number cpv[i] - 1 of tile i has completed
+                auto wait_last_pv = [&](int i, int where) {
+                    if (cpv[i] > 0 && !mbar_wait(&bars->o_done[i], (cpv[i] - 1) & 1))
+                        fail(where, cpv[i]);
+                    tc_fence_after();
+                };
+                for (int k = 0;; ++k) {
+                    ItemRec it;
+                    if (!read_item(bars, k, it)) {
+                        fail(6, k);
+                        break;
+                    }
+                    if (it.n_tiles < 0) break;
+                    mbar_arrive(&bars->item_free[k & (kItemSlots - 1)]);
+                    const int ntile = it.ntok > p.Mt ? 2 : 1, n = it.n_tiles;
+                    const Edges e(it, p.window);
+                    int kst = 0, vst = 0;
+                    if (!mbar_wait(&bars->q_full, k & 1)) {
+                        fail(0, k);
+                        break;
+                    }
+                    take(kst);
+                    for (int i = 0; i < ntile && ok; ++i) {
+                        // S_i(0) overwrites the columns the previous item's last P_i sits in
+                        wait_last_pv(i, 2);
+                        if (ok) issue_s(i, kst);
+                    }
+                    if (!ok) break;
+                    if (n == 1) umma_commit(&bars->q_free);
+                    umma_commit(&bars->empty[kst]);
+                    int kprev = kst;   // K slot of the last score products issued
+                    for (int j = 0; j < n && ok; ++j) {
+                        take(vst);
+                        if (!ok) break;
+                        // the guard works while the softmax does
+                        const bool guarded = e.guarded((it.kt_first + j) * kBN);
+                        if (guarded) mbar_arrive(&bars->guard_go[gc & 1]);
+                        for (int i = 0; i < ntile && ok; ++i) {
+                            if (!mbar_wait(&bars->p_full[i], cpv[i] & 1)) {
+                                fail(3, cpv[i]);
+                                break;
+                            }
+                            // the first PV of an item overwrites O_i: the previous item's
+                            // epilogue must have read it out
+                            if (j == 0 && nepi[i] > 0 &&
+                                !mbar_wait(&bars->o_free[i], (nepi[i] - 1) & 1)) {
+                                fail(4, nepi[i]);
+                                break;
+                            }
+                            if (guarded && i == 0) {
+                                if (!mbar_wait(&bars->guard[gc & 1], (gc >> 1) & 1)) {
+                                    fail(7, gc);
+                                    break;
+                                }
+                                ++gc;
+                            }
+                            tc_fence_after();
+                            issue_pv(i, vst, j > 0);
+                            if (j == n - 1) umma_commit(&bars->o_final[i]);
+                            if (j + 1 < n) {
+                                if (i == 0) take(kst);
+                                if (!ok) break;
+                                // S_i(j+1) overwrites the columns P_i(j) sits in
+                                wait_last_pv(i, 5);
+                                // PV_i(j) has completed, and with it every earlier product:
+                                // K(j) is free once PV_0(j) is, V(j) once the last tile's is
+                                if (i == 0 && j > 0) mbar_arrive(&bars->empty[kprev]);
+                                if (i == ntile - 1) mbar_arrive(&bars->empty[vst]);
+                                if (ok) issue_s(i, kst);
+                                if (j + 2 == n && i == ntile - 1) umma_commit(&bars->q_free);
+                            } else {
+                                // the item's last key tile: K and V go free when its products do
+                                if (i == 0 && j > 0) umma_commit(&bars->empty[kprev]);
+                                if (i == ntile - 1) umma_commit(&bars->empty[vst]);
+                            }
+                        }
+                        kprev = kst;
+                    }
+                    if (!ok) break;
+                    for (int i = 0; i < ntile; ++i) ++nepi[i];
+                }
+                if (!ok) set_status(p.status, GQA_ERR_DEVICE_TIMEOUT);
+                // every tcgen05 operation issued above completes before TMEM is released
+                umma_commit(&bars->mma_done);
+                mbar_wait(&bars->mma_done, 0);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ================= O stores =================
+            int done[2] = {0, 0};   // halves stored, per tile
+            for (int k = 0;; ++k) {
+                ItemRec it;
+                const bool got = read_item(bars, k, it);
+                if (!__all_sync(0xffffffffu, got)) {
+                    set_timeout(p.status, kDiagPacked, kRoleAux, 6, k);
+                    break;
+                }
+                __syncwarp();
+                if (it.n_tiles < 0) break;
+                if (lane == 0) mbar_arrive(&bars->item_free[k & (kItemSlots - 1)]);
+                // whole tiles only: the epilogue stores ragged ones and partials itself
+                int left[2];
+                left[0] = it.split < 0 && it.ntok >= p.Mt ? 2 : 0;
+                left[1] = it.split < 0 && it.ntok >= 2 * p.Mt ? 2 : 0;
+                if (lane == 0) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (left[0] + left[1] > 0) {
+                        for (int i = 0; i < 2; ++i) {
+                            if (left[i] == 0 || !mbar_try_wait(&bars->staged[i], done[i] & 1))
+                                continue;
+                            tma_store_3d(&tmO, smem + kSmemStage + i * kBoxBytes,
+                                         64 * (2 - left[i]), it.g * p.G, it.row0 + i * p.Mt);
+                            bulk_commit_group();
+                            bulk_wait_read_all();
+                            mbar_arrive(&bars->stage_free[i]);
+                            ++done[i];
+                            --left[i];
+                        }
+                        // a whole item may pass before its epilogue: the limit is generous,
+                        // but it is one
+                        if (globaltimer_ns() - t0 > 2 * GQA_WAIT_LIMIT_NS) {
+                            set_timeout(p.status, kDiagPacked, kRoleAux, 0, k);
+                            break;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (__any_sync(0xffffffffu, lane == 0 && left[0] + left[1] > 0)) break;
+            }
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
+        } else {
+            // ================= V guard =================
+            int u = 0, gc = 0;
+            for (int k = 0;; ++k) {
+                ItemRec it;
+                const bool got = read_item(bars, k, it);
+                if (!__all_sync(0xffffffffu, got)) {
+                    set_timeout(p.status, kDiagPacked, kRoleAux, 5, k);
+                    break;
+                }
+                __syncwarp();
+                if (it.n_tiles < 0) break;
+                const Edges e(it, p.window);
+                Slot &slot = bars->slot[k & (kItemSlots - 1)];
+                bool ok = true;
+                for (int j = 0; j < it.n_tiles; ++j) {
+                    const int n0 = (it.kt_first + j) * kBN;
+                    if (!e.guarded(n0)) continue;
+                    // the MMA thread has seen this V tile land and waits for the guard, so
+                    // the slot's phase cannot move on (waiting on it alone could take an
+                    // older phase of the same parity for this one)
+                    const int uu = u + 2 * j + 1, st = uu % kSlots;
+                    if (!warp_wait(&bars->guard_go[gc & 1], (gc >> 1) & 1) ||
+                        !warp_wait(&bars->full[st], (uu / kSlots) & 1)) {
+                        set_timeout(p.status, kDiagPacked, kRoleAux, 1, gc);
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *tile = smem + kSmemRing + st * kTileBytes;
+                    // rows [a, b) of the tile need a look: below the window's edge for some
+                    // row, or past the diagonal for some row
+                    auto look = [&](int a, int b) {
+                        // eight rows at a time, 4 lanes to a row of 16 16-byte chunks
+                        for (int r = a + (lane >> 2); r < b; r += 8) {
+                            const int key = n0 + r;
+                            const bool gone = key < e.lo || key > e.hi;
+                            bool marked = false;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const int cc = (lane & 3) + 4 * c;   // order does not matter
+                                uint4 *at = reinterpret_cast<uint4 *>(tile + (cc >> 3) * kBoxBytes +
+                                                                      r * 128 + (cc & 7) * 16);
+                                if (gone) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                    continue;
+                                }
+                                const uint4 x = *at;
+                                if (!(nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) ||
+                                      nonfinite2(x.w)))
+                                    continue;
+                                marked = true;
+                                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    if ((w[q] & 0x7f80u) == 0x7f80u) w[q] &= 0xffff0000u;
+                                    if ((w[q] & 0x7f800000u) == 0x7f800000u) w[q] &= 0xffffu;
+                                }
+                                *at = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                            if (marked) {
+                                const int b0 = key > e.hi_all ? key - e.hi_all - 1
+                                                              : 256 + key - e.lo;
+                                atomicOr(&slot.bad[b0 >> 5], 1u << (b0 & 31));
+                                atomicOr(&slot.any_bad, 1u);
+                            }
+                        }
+                    };
+                    const int below = min(kBN, max(0, e.lo_all - n0));
+                    const int above = min(kBN, max(below, e.hi_all + 1 - n0));
+                    look(0, below);
+                    look(above, kBN);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&bars->guard[gc & 1]);
+                    ++gc;
+                }
+                u += 2 * it.n_tiles;
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->item_free[k & (kItemSlots - 1)]);
+            }
+        }
+    } else {
+        reg_alloc<200>();
+        // ================= softmax / epilogue =================
+        const int wg = (warp - 4) >> 2;        // query tile
+        const int r = (warp & 3) * 32 + lane;  // row in tile == TMEM lane
+        const int rtok = r / p.G, rhead = r - rtok * p.G;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + wg * 128;
+        const uint32_t tO = tmem + lane_off + 256 + wg * 128;
+        uint8_t *stage = smem + kSmemStage + wg * kBoxBytes;
+        int cs = 0;    // score tiles consumed (all items)
+        int pvb = 0;   // PV products of the previous items
+        int ne = 0;    // items finished
+        int ns = 0;    // halves handed to the store warp
+        bool ok = true;
+        auto fail = [&](int barrier, int at) {
+            ok = false;
+            set_timeout(p.status, kDiagPacked, kRoleSoftmax, barrier, at);
+        };
+        for (int k = 0; ok; ++k) {
+            int n_tiles, n0, qpos, ntok;
+            {
+                ItemRec it;
+                const bool got = read_item(bars, k, it);
+                if (!__all_sync(0xffffffffu, got)) {
+                    fail(4, k);
+                    break;
+                }
+                n_tiles = it.n_tiles;
+                if (n_tiles < 0) break;
+                ntok = it.ntok - wg * p.Mt;    // tokens of this tile
+                n0 = it.kt_first * kBN;
+                // rows behind the last token compute what the last token's would
+                qpos = it.qpos0 + wg * p.Mt + min(rtok, min(ntok, p.Mt) - 1);
+            }
+            auto free_item = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->item_free[k & (kItemSlots - 1)]);
+            };
+            if (ntok <= 0) {
+                free_item();
+                continue;
+            }
+            const bool valid = rtok < min(ntok, p.Mt);
+            const bool warp_on = __any_sync(0xffffffffu, valid);
+            float m = -CUDART_INF_F, l = 0.f;
+            for (int j = 0; j < n_tiles; ++j, n0 += kBN) {
+                if (!warp_wait(&bars->s_full[wg], cs & 1)) {
+                    fail(0, cs);
+                    break;
+                }
+                ++cs;
+                if (!warp_on) {   // no row of this warp is stored: its P may be anything
+                    mbar_arrive(&bars->p_full[wg]);
+                    continue;
+                }
+                tc_fence_after();
+                const bool full = (n0 + kBN - 1 <= qpos) &&
+                                  (p.window <= 0 || n0 >= qpos - p.window + 1);
+                // Masking, decided per warp and 32-column chunk, applied in tensor memory
+                // before the row is loaded: a chunk visible in all 32 rows of the warp is
+                // left alone; one hidden in all of them gets -inf and is skipped below (P = 0,
+                // no exponentials); a mixed one is masked element by element.
+                uint32_t dead = 0;   // chunks hidden in every row of the warp
+                if (!__all_sync(0xffffffffu, full)) {
+                    // visible columns of this row in the tile: [c_lo, c_hi)
+                    const int c_hi = min(kBN, qpos - n0 + 1);
+                    const int c_lo = p.window > 0 ? max(0, qpos - p.window + 1 - n0) : 0;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const bool vis = c_lo <= 32 * c && 32 * c + 32 <= c_hi;
+                        const bool hid = c_hi <= 32 * c || 32 * c + 32 <= c_lo || c_hi <= c_lo;
+                        if (__all_sync(0xffffffffu, vis)) continue;
+                        uint32_t rr[32];
+                        if (__all_sync(0xffffffffu, hid)) {
+                            dead |= 1u << c;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(-CUDART_INF_F);
+                        } else {
+                            tmem_ld32(tS + 32 * c, rr);
+                            tmem_wait_ld();
+                            const int lo = c_lo - 32 * c, hi = c_hi - 32 * c;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < lo || i >= hi) rr[i] = __float_as_uint(-CUDART_INF_F);
+                        }
+                        tmem_st32(tS + 32 * c, rr);
+                    }
+                    tmem_wait_st();
+                }
+                // the whole S row in registers: four loads in flight, one wait
+                float x[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t rr[32];
+                    tmem_ld32(tS + 32 * c, rr);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[32 * c + i] = __uint_as_float(rr[i]);
+                }
+                tmem_wait_ld();
+                // row maximum of the raw scores: 3-input max, 8 independent chains of 16
+                float mx8[8];
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    mx8[kk] = fmax3(x[kk], x[kk + 8], x[kk + 16]);
+#pragma unroll
+                    for (int tt = 3; tt < 15; tt += 2)
+                        mx8[kk] = fmax3(mx8[kk], x[kk + 8 * tt], x[kk + 8 * tt + 8]);
+                    mx8[kk] = fmaxf(mx8[kk], x[kk + 120]);
+                }
+                const float mraw = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                         fmaxf(mx8[6], mx8[7]));
+                const float mx = mraw * p.scale_log2;   // scale > 0: max commutes with it
+                const float m_new = fmaxf(m, mx);
+                const bool grow = m_new > m + kRescaleThreshold;  // false while both -inf
+                const bool need_o = grow && j > 0 && m != -CUDART_INF_F;
+                const float f = grow ? ex2_approx(m - m_new) : 1.0f;  // 0 when m was -inf
+                if (grow) {
+                    l *= f;
+                    m = m_new;
+                }
+                const float nmref = (m == -CUDART_INF_F) ? 0.f : -m;
+                // P = 2^(s * scale * log2e - m) as bf16 over the first 64 columns of the S
+                // tile, 16 columns at a time (each piece lands on columns already read); the
+                // row sum takes the unrounded weights
+                float2 ls[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+                    if (dead & (1u << c)) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                        tmem_st16(tS + 16 * c, pk);
+                        continue;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 a = ffma2(make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]),
+                                               p.scale_log2, nmref);
+                        const float e0 = ex2_approx(a.x), e1 = ex2_approx(a.y);
+                        ls[i & 3] = fadd2(ls[i & 3], make_float2(e0, e1));
+                        pk[i] = pack_bf16x2(e0, e1);
+                    }
+                    tmem_st16(tS + 16 * c, pk);
+                }
+                l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) +
+                     ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
+                if (__any_sync(0xffffffffu, need_o)) {
+                    // O holds the product of tiles < j (already complete: S_i(j) was
+                    // issued after PV_i(j-1) finished); rescale it in TMEM before this
+                    // tile's PV is issued
+                    if (!warp_wait(&bars->o_done[wg], (pvb + j - 1) & 1)) fail(1, pvb + j);
+                    tc_fence_after();
+                    const float fo = need_o ? f : 1.0f;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t rr[32];
+                        tmem_ld32(tO + 32 * c, rr);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            rr[i] = __float_as_uint(__uint_as_float(rr[i]) * fo);
+                        tmem_st32(tO + 32 * c, rr);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&bars->p_full[wg]);
+                if (!ok) break;
+            }
+            if (!ok) break;
+            pvb += n_tiles;
+            // ---- epilogue: O out of TMEM first (frees it for the next item)
+            if (!warp_wait(&bars->o_final[wg], ne & 1)) {
+                fail(2, ne);
+                break;
+            }
+            ++ne;
+            tc_fence_after();
+            float x[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t rr[32];
+                tmem_ld32(tO + 32 * c, rr);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[32 * c + i] = __uint_as_float(rr[i]);
+            }
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(&bars->o_free[wg]);
+            Slot &slot = bars->slot[k & (kItemSlots - 1)];
+            const ItemRec it = slot.it;
+            const int row = it.row0 + wg * p.Mt + rtok, head = it.g * p.G + rhead;
+            // the marked keys that this row sees, one by one: `fn(value row)`
+            auto marked = [&](auto &&fn) {
+                for (int w = 0; w < 16; ++w) {
+                    for (uint32_t b = slot.bad[w]; b; b &= b - 1) {
+                        const int at = 32 * w + __ffs(b) - 1;
+                        const int key = at < 256 ? it.qpos0 + 1 + at
+                                                 : max(0, it.qpos0 - p.window + 1) + at - 256;
+                        if (key <= qpos && (p.window <= 0 || qpos - key < p.window))
+                            fn(value_row<PAGED>(p, it, key));
+                    }
+                }
+            };
+            if (it.split >= 0) {
+                // a span of the keys: the unnormalised row with its maximum (log2) and sum
+                if (valid) {
+                    const size_t rec = (size_t)it.split * p.bounds.total * p.Hq + (size_t)row * p.Hq + head;
+                    float4 *dst = reinterpret_cast<float4 *>(p.ws_o + rec * kD);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        dst[c] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+                    p.ws_ml[2 * rec] = m;
+                    p.ws_ml[2 * rec + 1] = l;
+                    if (slot.any_bad)
+                        marked([&](const __nv_bfloat16 *v) {
+                            for (int c = 0; c < kD; ++c) {
+                                const float y = __bfloat162float(v[c]);
+                                if (!isfinite(y)) p.ws_o[rec * kD + c] += y;
+                            }
+                        });
+                }
+            } else {
+                const float inv_l = l > 0.f || l != l ? 1.0f / l : 0.f;
+                const bool whole = ntok >= p.Mt;   // the tile's tokens are all there
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // the staging half's last store has read it
+                    if (ns > 0 && !warp_wait(&bars->stage_free[wg], (ns - 1) & 1)) {
+                        fail(3, ns);
+                        break;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const float *y = x + 64 * h + 8 * c;
+                        *reinterpret_cast<uint4 *>(stage + r * 128 +
+                                                   ((whole ? c ^ (r & 7) : c) << 4)) =
+                            make_uint4(pack_bf16x2(y[0] * inv_l, y[1] * inv_l),
+                                       pack_bf16x2(y[2] * inv_l, y[3] * inv_l),
+                                       pack_bf16x2(y[4] * inv_l, y[5] * inv_l),
+                                       pack_bf16x2(y[6] * inv_l, y[7] * inv_l));
+                    }
+                    if (valid && slot.any_bad)
+                        marked([&](const __nv_bfloat16 *v) {
+                            add_marked(stage, r, whole, v + 64 * h);
+                        });
+                    fence_proxy_async_smem();
+                    if (whole) {
+                        mbar_arrive(&bars->staged[wg]);
+                        ++ns;
+                    } else if (valid) {
+                        // a ragged tile: each row's 128 bytes by themselves
+                        bulk_store(p.o + (size_t)row * p.o_stride + head * kD + 64 * h,
+                                   stage + r * 128, 128);
+                        bulk_commit_group();
+                        bulk_wait_read_all();
+                    }
+                }
+                if (!ok) break;
+                if (valid && p.lse)
+                    p.lse[(size_t)head * p.bounds.total + row] =
+                        (m + __log2f(l)) * 0.69314718055994531f;
+            }
+            free_item();
+        }
+        bulk_wait_all();   // the stores complete before the CTA exits
+        if (!ok) set_status(p.status, GQA_ERR_DEVICE_TIMEOUT);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Merges the spans of split items: one warp per (token, query head), 4 dims per lane.
+__global__ void packed_combine_kernel(const Params p) {
+    const int row = blockIdx.x, lane = threadIdx.x & 31;
+    const int i = packed_row_seq(p.cu, p.nseq, row);
+    if (i >= p.nseq) return;
+    const PackedSeq s = packed_seq(p.cu, p.kv_lens, i, p.bounds, nullptr);
+    if (row < s.row0 || row >= s.row0 + s.T) return;
+    // the block of tokens that the row was computed in
+    const int ntok = 2 * p.Mt, t0 = (row - s.row0) / ntok * ntok;
+    const int q_lo = s.S - s.T + t0, q_hi = q_lo + min(ntok, s.T - t0) - 1;
+    const int spans = n_spans(q_hi / kBN - first_tile(q_lo, p.window) + 1, p.split_tiles);
+    if (spans <= 1) return;   // written by the attention kernel itself
+    const size_t step = (size_t)p.bounds.total * p.Hq;
+    for (int h = threadIdx.x >> 5; h < p.Hq; h += blockDim.x >> 5) {
+        const size_t rec = (size_t)row * p.Hq + h;
+        float M = -CUDART_INF_F;
+        for (int k = 0; k < spans; ++k) M = fmaxf(M, p.ws_ml[2 * (rec + k * step)]);
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < spans; ++k) {
+            const size_t at = rec + k * step;
+            const float m = p.ws_ml[2 * at];
+            if (m == -CUDART_INF_F && p.ws_ml[2 * at + 1] == 0.f) continue;   // a span with no visible key
+            const float f = ex2_approx(m - M);
+            const float4 o = reinterpret_cast<const float4 *>(p.ws_o + at * kD)[lane];
+            L = fmaf(p.ws_ml[2 * at + 1], f, L);
+            acc.x = fmaf(o.x, f, acc.x);
+            acc.y = fmaf(o.y, f, acc.y);
+            acc.z = fmaf(o.z, f, acc.z);
+            acc.w = fmaf(o.w, f, acc.w);
+        }
+        const float r = 1.0f / L;
+        reinterpret_cast<uint2 *>(p.o + (size_t)row * p.o_stride + h * kD)[lane] =
+            make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
+        if (p.lse && lane == 0)
+            p.lse[(size_t)h * p.bounds.total + row] = (M + __log2f(L)) * 0.69314718055994531f;
+    }
+}
+
+// How many key tiles a span of a split item has (0: items stay whole), and the most spans.
+// Items stay whole when there are enough of them for every SM; otherwise each is split so
+// that the grid has about two per SM, but no span is shorter than 4 tiles (512 keys).
+struct SpanRule {
+    int split_tiles, spans;
+    int most;   // spans of this shape with any window: a window only lowers it
+};
+SpanRule span_rule(int total, int max_kv, int Hkv, int G, int window) {
+    const int ntok = 2 * (kBM / G);
+    const long items = (long)((total + ntok - 1) / ntok) * Hkv;
+    const int tiles = most_tiles(max_kv, ntok, window);
+    long want = (2 * kSMs + items - 1) / items;
+    if (want > tiles / 4) want = tiles / 4;
+    if (want <= 1) return {0, 1, 1};
+    const int per = static_cast<int>((tiles + want - 1) / want);
+    return {per, n_spans(tiles, per), static_cast<int>(want)};
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// bf16 [n2, n1, 128] with strides s1, s2 in elements; boxes of b2 x b1 rows of 64, 128-byte
+// swizzle.
+bool make_map(CUtensorMap *map, const void *base, long n1, long s1, long n2, long s2, int b1,
+              int b2) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)n1, (cuuint64_t)n2};
+    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+size_t packed_prefill_workspace_bytes(int total, int max_kv, int Hq, int Hkv) {
+    const SpanRule r = span_rule(total, max_kv, Hkv, Hq / Hkv, 0);
+    return r.most <= 1 ? 0 : (size_t)r.most * total * Hq * (kD + 2) * sizeof(float);
+}
+
+int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
+    const bool paged = a.cache != nullptr;
+    Params p{};
+    p.o = static_cast<__nv_bfloat16 *>(a.o);
+    p.v = static_cast<const __nv_bfloat16 *>(a.v);
+    p.lse = a.lse;
+    p.cu = a.cu;
+    p.status = status;
+    p.o_stride = a.o_stride;
+    p.v_stride = a.v_stride;
+    p.nseq = a.nseq;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.Hq / a.Hkv;
+    p.Mt = kBM / p.G;
+    p.window = a.window;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.q_box_bytes = 64 * 2 * p.G * p.Mt;
+    p.bounds = {a.total, a.max_q, a.max_kv, 0x7fffffffL};
+    const int ntok = 2 * p.Mt;
+    int spans = 1;
+    CUtensorMap mq, mk, mv, mo;
+    if (!make_map(&mq, a.q, a.Hq, kD, a.total, a.q_stride, p.G, p.Mt) ||
+        !make_map(&mo, a.o, a.Hq, kD, a.total, a.o_stride, p.G, p.Mt))
+        return GQA_ERR_CUDA;
+    if (paged) {
+        const gqa_paged_kv &c = *a.cache;
+        p.kv_lens = c.kv_lens;
+        p.pages = c.page_table;
+        p.num_pages = c.num_pages;
+        p.page_size = c.page_size;
+        p.max_pages = c.max_pages;
+        p.bounds.cap = (long)c.max_pages * c.page_size;
+        const SpanRule r = span_rule(a.total, a.max_kv, a.Hkv, p.G, a.window);
+        p.split_tiles = r.split_tiles;
+        spans = r.spans;
+        if (spans > 1) {
+            // the outputs come first (16-byte aligned), then the maxima and sums
+            p.ws_o = static_cast<float *>(ws);
+            p.ws_ml = p.ws_o + (size_t)spans * a.total * a.Hq * kD;
+        }
+        const long slabs = (long)c.num_pages * c.Hkv, page = c.page_size;
+        if (!make_map(&mk, c.k, page, kD, slabs, page * kD, c.page_size, 1) ||
+            !make_map(&mv, c.v, page, kD, slabs, page * kD, c.page_size, 1))
+            return GQA_ERR_CUDA;
+    } else if (!make_map(&mk, a.k, a.Hkv, kD, a.total, a.k_stride, 1, kBN) ||
+               !make_map(&mv, a.v, a.Hkv, kD, a.total, a.v_stride, 1, kBN)) {
+        return GQA_ERR_CUDA;
+    }
+    auto kern = paged ? packed_prefill_kernel<true> : packed_prefill_kernel<false>;
+    if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes) != cudaSuccess)
+        return GQA_ERR_CUDA;
+    // an upper bound on the items: a sequence adds at most one block that is not full
+    const long blocks = (long)a.total / ntok + (a.nseq < a.total ? a.nseq : a.total);
+    const long grid = blocks * a.Hkv * spans;
+    if (grid > 0x7fffffffL) return GQA_ERR_UNSUPPORTED;
+    kern<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, s>>>(mq, mk, mv, mo, p);
+    if (cudaPeekAtLastError() != cudaSuccess) return GQA_ERR_CUDA;
+    if (spans > 1) {
+        packed_combine_kernel<<<a.total, 256, 0, s>>>(p);
+        if (cudaPeekAtLastError() != cudaSuccess) return GQA_ERR_CUDA;
+    }
+    return GQA_OK;
+}
+
+}  // namespace gqa
