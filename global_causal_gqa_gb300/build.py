@@ -28,7 +28,8 @@ BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libgqa_attn_debug.so")
 SOURCES = ["api.cu", "rope.cu", "kv.cu", "decode.cu", "prefill.cu", "prefill_stream.cu",
            "prefill_wide.cu", "prefill_pair.cu", "qknorm.cu", "chunk.cu", "watchdog.cu",
-           "packed_append.cu", "packed_prefill.cu", "packed_attn.cu"]
+           "packed_append.cu", "packed_prefill.cu", "paged_decode.cu",
+           "packed_attn.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "packed.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -416,6 +416,8 @@ static gqa_status check_paged(const gqa_paged_kv *c) {
     if (!c->k || !c->v || !c->page_table || !c->kv_lens || c->num_pages <= 0 || c->Hkv <= 0 ||
         c->max_pages <= 0 || c->reserved != 0)
         return GQA_ERR_INVALID_ARG;
+    // a (page, KV head) has a 32-bit number
+    if (static_cast<int64_t>(c->num_pages) * c->Hkv > 0x7fffffff) return GQA_ERR_UNSUPPORTED;
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
         return GQA_ERR_UNSUPPORTED;
     if (!aligned16(c->k) || !aligned16(c->v) ||

@@ -1,5 +1,6 @@
 // internal.h -- launchers shared between the kernel translation units and the C ABI.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -125,7 +126,7 @@ cudaError_t launch_qk_norm_append(gqa_kv_desc *descs, int nseq, const void *q, c
                                   cudaStream_t s);
 
 // Packed sequences and the paged cache (packed_append.cu, packed_prefill.cu,
-// packed_attn.cu).  `kv_lens`,
+// paged_decode.cu, packed_attn.cu).  `kv_lens`,
 // `pages` of an attention call: nullptr for packed prompts (keys are the packed rows).
 cudaError_t launch_packed_rope_append(const void *q, int64_t q_stride, const void *k,
                                       int64_t k_stride, const void *v, int64_t v_stride,
@@ -150,6 +151,14 @@ struct PackedAttn {
 // the tensor-core kernel for prompts and chunks (packed_prefill.cu); returns a gqa_status
 int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
 size_t packed_prefill_workspace_bytes(int total, int max_kv, int Hq, int Hkv);
+// the streaming kernel for a few rows per sequence (paged_decode.cu)
+bool paged_decode_fits(int max_q, int G);
+int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
+size_t paged_decode_workspace_bytes(int nseq, int max_kv);
+// bf16 [n2, n1, 128] with strides s1, s2 in elements, boxes of b2 x b1 rows of 64 elements,
+// 128-byte swizzle; false if the driver refuses it (packed_attn.cu)
+bool make_rows_map(CUtensorMap *map, const void *base, long n1, long s1, long n2, long s2, int b1,
+                   int b2);
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
 size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv, int d);
 

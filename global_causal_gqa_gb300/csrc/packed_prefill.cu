@@ -1057,40 +1057,6 @@ SpanRule span_rule(int total, int max_kv, int Hkv, int G, int window) {
     return {per, n_spans(tiles, per), static_cast<int>(want)};
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                             cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            ptr = nullptr;
-        return reinterpret_cast<EncodeTiledFn>(ptr);
-    }();
-    return fn;
-}
-
-// bf16 [n2, n1, 128] with strides s1, s2 in elements; boxes of b2 x b1 rows of 64, 128-byte
-// swizzle.
-bool make_map(CUtensorMap *map, const void *base, long n1, long s1, long n2, long s2, int b1,
-              int b2) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)n1, (cuuint64_t)n2};
-    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
-              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 
 size_t packed_prefill_workspace_bytes(int total, int max_kv, int Hq, int Hkv) {
@@ -1120,8 +1086,8 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
     const int ntok = 2 * p.Mt;
     int spans = 1;
     CUtensorMap mq, mk, mv, mo;
-    if (!make_map(&mq, a.q, a.Hq, kD, a.total, a.q_stride, p.G, p.Mt) ||
-        !make_map(&mo, a.o, a.Hq, kD, a.total, a.o_stride, p.G, p.Mt))
+    if (!make_rows_map(&mq, a.q, a.Hq, kD, a.total, a.q_stride, p.G, p.Mt) ||
+        !make_rows_map(&mo, a.o, a.Hq, kD, a.total, a.o_stride, p.G, p.Mt))
         return GQA_ERR_CUDA;
     if (paged) {
         const gqa_paged_kv &c = *a.cache;
@@ -1140,11 +1106,11 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
             p.ws_ml = p.ws_o + (size_t)spans * a.total * a.Hq * kD;
         }
         const long slabs = (long)c.num_pages * c.Hkv, page = c.page_size;
-        if (!make_map(&mk, c.k, page, kD, slabs, page * kD, c.page_size, 1) ||
-            !make_map(&mv, c.v, page, kD, slabs, page * kD, c.page_size, 1))
+        if (!make_rows_map(&mk, c.k, page, kD, slabs, page * kD, c.page_size, 1) ||
+            !make_rows_map(&mv, c.v, page, kD, slabs, page * kD, c.page_size, 1))
             return GQA_ERR_CUDA;
-    } else if (!make_map(&mk, a.k, a.Hkv, kD, a.total, a.k_stride, 1, kBN) ||
-               !make_map(&mv, a.v, a.Hkv, kD, a.total, a.v_stride, 1, kBN)) {
+    } else if (!make_rows_map(&mk, a.k, a.Hkv, kD, a.total, a.k_stride, 1, kBN) ||
+               !make_rows_map(&mv, a.v, a.Hkv, kD, a.total, a.v_stride, 1, kBN)) {
         return GQA_ERR_CUDA;
     }
     auto kern = paged ? packed_prefill_kernel<true> : packed_prefill_kernel<false>;

@@ -1,0 +1,690 @@
+// paged_decode.cu -- attention of a few new tokens per sequence over a paged cache (d = 128):
+// decode steps and short drafts, up to 16 rows (tokens x heads of a KV group) per sequence.
+//
+// For query token t of a sequence with S keys and T new tokens, at position i = S - T + t
+// ("PLaMo 3アーキテクチャ徹底解析" §4.5, §5.1):
+//   o = sum_j softmax_j(scale q . k_j) v_j  over j <= i (and i - j < W with a window).
+// Every key and value is read once for all rows of its KV head, 512 bytes per key and head,
+// and feeds 4 * 128 flops per row: the call is bound by memory, and the kernel is built to
+// keep HBM busy.
+//
+// Work split.  The unit is 64 keys of one (sequence, KV head).  All units of the batch, in
+// the order (sequence, KV head, keys), are cut into one equal run per SM, whatever the
+// lengths, so every SM streams the same number of bytes.  A pair of (sequence, KV head) that
+// lies within one CTA's run is finished there; one that spans several leaves a partial (m, l,
+// O) per CTA, at most two per CTA (its first and its last pair), and the combine kernel
+// merges them.  Calls whose keys are few per pair take one CTA per pair and no second kernel.
+// The lengths are read on the device: every CTA sums the units of all sequences (a thread per
+// sequence) and finds its own start.
+//
+// A producer warp streams K and V by TMA into a ring of 6 stages of 64 keys (192 KB in
+// flight per SM), one box per page and half of the head dimension, 128-byte swizzle; it runs
+// ahead over the ends of pairs.  Four consumer warps take 16 keys of each stage:
+// S = Q K^T and O += P V as m16n8k16 bf16 MMAs with the rows as M (P leaves the score
+// product in the layout of an A operand), fp32 accumulators and softmax statistics, the row
+// maximum updated only when a score exceeds it by 2^8 (exact: sum and O share the
+// reference).  At the end of a pair the four warps merge through shared memory.
+//
+// Hidden keys have weight 0, but 0 * NaN is NaN: in blocks that straddle an edge of the mask
+// the values of keys that no row sees are zeroed on their way into the product, and
+// non-finite ones that only some rows see are taken out and added to the rows that do.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "internal.h"
+#include "packed.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kUnit = 64;                       // keys of a stage
+constexpr int kStages = 6;
+constexpr int kHalfBytes = kUnit * 128;         // 64 keys x 64 dims
+constexpr int kStageBytes = 4 * kHalfBytes;     // K halves, V halves
+constexpr int kConsumers = 4;                   // warps, 16 keys of a stage each
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kMaxRows = 16;
+constexpr int kRowFloats = 132;                 // a row of the exchange, padded off its bank
+constexpr int kSmemXchg = kStages * kStageBytes;
+constexpr int kSmemBar = kSmemXchg + kConsumers * kMaxRows * kRowFloats * 4;
+constexpr int kSmemBytes = kSmemBar + 1024 + 1024;
+constexpr float kRescaleThreshold = 8.0f;       // log2 units
+constexpr int kSegSlots = 4;
+constexpr int kSMs = 152;
+
+// A run of stages of one (sequence, KV head).  stages < 0: no more.
+struct Segment {
+    int row0, T, S, seq, g, unit0, stages;
+    int slot;   // -1: all of the pair's keys; else the partial's place
+};
+
+struct Bars {
+    Segment seg[kSegSlots];
+    uint64_t full[kStages], empty[kStages];
+    uint64_t seg_full[kSegSlots], seg_free[kSegSlots];
+    uint64_t merge;                // the consumer warps meet (a barrier with a bounded wait)
+    float2 ml[kConsumers][kMaxRows];
+    int scan[kThreads / 32];
+    int start_seq, start_unit;
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block");
+
+struct Params {
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *o;
+    float *lse;
+    float *ws_o, *ws_ml;
+    int *ws_units;                 // units before each sequence, and in all
+    const int32_t *cu, *kv_lens, *pages;
+    int *status;
+    long q_stride, o_stride;
+    PackedBounds bounds;
+    int nseq, Hq, Hkv, G, window, num_pages, page_size, max_pages;
+    int whole;                     // 1: one CTA per pair
+    float scale_log2;
+};
+
+// Units of one (sequence, KV head): [first, first + count) of 64 keys each.
+__device__ __forceinline__ int first_unit(const PackedSeq &s, int window) {
+    return window > 0 && s.S - s.T - window + 1 > 0 ? (s.S - s.T - window + 1) / kUnit : 0;
+}
+__device__ __forceinline__ int count_units(const PackedSeq &s, int window) {
+    return s.T > 0 ? (s.S + kUnit - 1) / kUnit - first_unit(s, window) : 0;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Clears the non-finite ones of the two bf16 in w; true if there was one.
+__device__ __forceinline__ bool strip_nonfinite(uint32_t &w) {
+    const bool lo = (w & 0x7f80u) == 0x7f80u, hi = (w & 0x7f800000u) == 0x7f800000u;
+    if (lo) w &= 0xffff0000u;
+    if (hi) w &= 0x0000ffffu;
+    return lo || hi;
+}
+
+enum Role { kRoleProducer = 0, kRoleConsumer = 2 };
+
+// ROWS: 8 or 16 rows of the MMA in use (8: the upper half is zero and costs no exponentials).
+template <int ROWS>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const Params p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    Bars *bars = reinterpret_cast<Bars *>(smem + kSmemBar);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->empty[i], kConsumers);
+        }
+        for (int i = 0; i < kSegSlots; ++i) {
+            mbar_init(&bars->seg_full[i], 1);
+            mbar_init(&bars->seg_free[i], kConsumers);
+        }
+        mbar_init(&bars->merge, kConsumers);
+        fence_mbar_init();
+    }
+    // ---- this CTA's run of units
+    int run = 0, per = 0;          // units of the run; of every CTA's run
+    if (p.whole) {
+        if (threadIdx.x == 0) {
+            bars->start_seq = blockIdx.x / p.Hkv;
+            bars->start_unit = 0;
+        }
+        __syncthreads();
+    } else {
+        const int m = (p.nseq + kThreads - 1) / kThreads;   // sequences per thread
+        const int s0 = threadIdx.x * m;
+        int mine = 0;
+        for (int i = s0; i < s0 + m && i < p.nseq; ++i)
+            mine += p.Hkv * count_units(packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status),
+                                        p.window);
+        int incl = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += x;
+        }
+        if (lane == 31) bars->scan[warp] = incl;
+        if (threadIdx.x == 0) bars->start_seq = -1;
+        __syncthreads();
+        int all = 0, before = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += bars->scan[w];
+            all += bars->scan[w];
+        }
+        before += incl - mine;
+        per = (all + gridDim.x - 1) / gridDim.x;
+        const int u0 = blockIdx.x * per;
+        run = max(0, min(per, all - u0));
+        if (run > 0 && before <= u0 && u0 < before + mine) {
+            int at = before;
+            for (int i = s0; i < p.nseq; ++i) {
+                const int n = p.Hkv * count_units(
+                                          packed_seq(p.cu, p.kv_lens, i, p.bounds, nullptr), p.window);
+                if (u0 < at + n) {
+                    bars->start_seq = i;
+                    bars->start_unit = u0 - at;
+                    break;
+                }
+                at += n;
+            }
+        }
+        if (blockIdx.x == 0) {   // for the combine kernel
+            int at = before;
+            for (int i = s0; i < s0 + m && i < p.nseq; ++i) {
+                p.ws_units[i] = at;
+                at += p.Hkv * count_units(packed_seq(p.cu, p.kv_lens, i, p.bounds, nullptr), p.window);
+            }
+            if (threadIdx.x == 0) p.ws_units[p.nseq] = all;
+        }
+        __syncthreads();
+    }
+
+    if (warp == kConsumers) {
+        // ================= producer =================
+        if (lane == 0) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+        bool ok = true;
+        int u = 0;   // stages issued
+        int seq = bars->start_seq, off = bars->start_unit;   // off: units into the sequence
+        // boxes of a stage: one per page, or per 64 keys of a longer page
+        const int box = min(p.page_size, kUnit), boxes = kUnit / box;
+        for (int k = 0;; ++k) {
+            Segment sg;
+            sg.stages = -1;
+            while (p.whole ? k == 0 && sg.stages < 0 : run > 0) {
+                const PackedSeq s = packed_seq(p.cu, p.kv_lens, seq, p.bounds,
+                                               p.whole && lane == 0 ? p.status : nullptr);
+                const int n = count_units(s, p.window);
+                if (p.whole) {
+                    off = n * (blockIdx.x % p.Hkv);
+                    run = n;
+                    if (n == 0) break;
+                } else if (off >= n * p.Hkv) {
+                    ++seq;   // run > 0: a later sequence has units
+                    off = 0;
+                    continue;
+                }
+                sg.row0 = s.row0;
+                sg.T = s.T;
+                sg.S = s.S;
+                sg.seq = seq;
+                sg.g = off / n;
+                const int in = off - sg.g * n;
+                sg.unit0 = first_unit(s, p.window) + in;
+                sg.stages = min(run, n - in);
+                sg.slot = sg.stages == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (in == 0 ? 1 : 0);
+                off += sg.stages;
+                run -= sg.stages;
+                break;
+            }
+            const int slot = k & (kSegSlots - 1);
+            if (k >= kSegSlots && !warp_wait(&bars->seg_free[slot], (k / kSegSlots - 1) & 1)) {
+                set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 0, k);
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                bars->seg[slot] = sg;
+                mbar_arrive(&bars->seg_full[slot]);
+            }
+            __syncwarp();
+            if (sg.stages < 0) break;
+            const int lo = p.window > 0 ? max(0, sg.S - sg.T - p.window + 1) : 0;
+            // the slab of this lane's box of a stage; -1 for one that no row sees or that is
+            // not in the pool (its box is zero fill).  The next stage's entries are fetched
+            // one stage ahead.
+            auto slab_of = [&](int unit) {
+                int slab = -1;
+                if (lane < boxes) {
+                    const int key0 = unit * kUnit + lane * box;
+                    if (key0 < sg.S && key0 + box > lo) {
+                        const int pg = __ldg(p.pages + (long)sg.seq * p.max_pages + key0 / p.page_size);
+                        if (pg >= 0 && pg < p.num_pages) slab = pg * p.Hkv + sg.g;
+                        else set_status(p.status, GQA_ERR_INVALID_ARG);
+                    }
+                }
+                return slab;
+            };
+            int slab = slab_of(sg.unit0);
+            for (int j = 0; j < sg.stages; ++j, ++u) {
+                const int next = j + 1 < sg.stages ? slab_of(sg.unit0 + j + 1) : -1;
+                const int st = u % kStages;
+                if (u >= kStages && !warp_wait(&bars->empty[st], (u / kStages - 1) & 1)) {
+                    set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 1, u);
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], kStageBytes);
+                __syncwarp();
+                if (lane < boxes) {
+                    uint8_t *dst = smem + st * kStageBytes + lane * box * 128;
+                    const int row = p.page_size > kUnit ? ((sg.unit0 + j) * kUnit) % p.page_size : 0;
+                    tma_load_3d(dst, &tmK, &bars->full[st], 0, row, slab);
+                    tma_load_3d(dst + kHalfBytes, &tmK, &bars->full[st], 64, row, slab);
+                    tma_load_3d(dst + 2 * kHalfBytes, &tmV, &bars->full[st], 0, row, slab);
+                    tma_load_3d(dst + 3 * kHalfBytes, &tmV, &bars->full[st], 64, row, slab);
+                }
+                __syncwarp();
+                slab = next;
+            }
+            if (!ok) break;
+        }
+        if (!ok)   // never leave the CTA with copies in flight
+            for (int w = max(0, u - kStages); w < u; ++w)
+                mbar_wait(&bars->full[w % kStages], (w / kStages) & 1);
+        return;
+    }
+
+    // ================= consumers =================
+    const int gq = lane >> 2, tq = lane & 3;
+    constexpr int HR = ROWS / 8;                  // row halves in use
+    const uint32_t ring = smem_u32(smem);
+    float *xchg = reinterpret_cast<float *>(smem + kSmemXchg);
+    // ldmatrix rows: K: matrices (keys 0-7 | 8-15) x (chunk 2ks | 2ks + 1); V transposed:
+    // (dim chunk 2nn | 2nn + 1) x (keys 0-7 | 8-15)
+    const int mat = lane >> 3, l7 = lane & 7;
+    const uint32_t k_row = (16 * warp + ((mat >> 1) << 3) + l7) * 128;
+    const uint32_t v_row = 2 * kHalfBytes + (16 * warp + ((mat & 1) << 3) + l7) * 128;
+    int meets = 0;
+    auto meet = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->merge);
+        if (warp_wait(&bars->merge, meets++ & 1)) return true;
+        set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 2, meets);
+        return false;
+    };
+    int u = 0;
+    for (int k = 0;; ++k) {
+        const int slot = k & (kSegSlots - 1);
+        if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
+            set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 0, k);
+            return;
+        }
+        const Segment sg = bars->seg[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->seg_free[slot]);
+        if (sg.stages < 0) return;
+        const int rows = sg.T * p.G;              // <= ROWS (the host's rule on max_q)
+        // this thread's rows gq, gq + 8: their query and position (rows past the last one
+        // are zero queries at the last position)
+        uint32_t qa[8][2 * HR];
+        int qpos[HR];
+#pragma unroll
+        for (int h = 0; h < HR; ++h) {
+            const int r = gq + 8 * h, t = min(r, rows - 1) / p.G;
+            qpos[h] = sg.S - sg.T + t;
+            const __nv_bfloat16 *qr = p.q + (long)(sg.row0 + t) * p.q_stride +
+                                      (sg.g * p.G + (r - t * p.G)) * kD + 2 * tq;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                qa[ks][h] = qa[ks][HR + h] = 0u;
+                if (r < rows) {
+                    qa[ks][h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks));
+                    qa[ks][HR + h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks + 8));
+                }
+            }
+        }
+        const int q_first = sg.S - sg.T;          // hi_all: keys beyond are hidden from some
+        const int lo = p.window > 0 ? max(0, q_first - p.window + 1) : 0;
+        const int lo_all = p.window > 0 ? max(0, sg.S - p.window) : 0;
+        float o[16][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float m[HR], mr[HR], l[HR];               // mr: m, or 0 while m is -inf
+#pragma unroll
+        for (int h = 0; h < HR; ++h) {
+            m[h] = -CUDART_INF_F;
+            mr[h] = l[h] = 0.f;
+        }
+        for (int j = 0; j < sg.stages; ++j, ++u) {
+            const int st = u % kStages;
+            if (!warp_wait(&bars->full[st], (u / kStages) & 1)) {
+                set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 1, u);
+                return;
+            }
+            const int kb = (sg.unit0 + j) * kUnit + 16 * warp;   // this warp's 16 keys
+            if (kb < sg.S && kb + 15 >= lo) {
+                const uint32_t base = ring + st * kStageBytes;
+                // ---- scores: rows x 16 keys, two chains per 8 keys
+                float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+                float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    uint32_t b[4];
+                    const int c = 2 * ks + (mat & 1);
+                    ldsm4(b, base + (c >> 3) * kHalfBytes + k_row + (((c & 7) ^ l7) << 4));
+                    const uint32_t a0 = qa[ks][0], a1 = HR > 1 ? qa[ks][1] : 0u;
+                    const uint32_t a2 = qa[ks][HR], a3 = HR > 1 ? qa[ks][HR + 1] : 0u;
+                    mma16816(ks & 1 ? t0 : s0, a0, a1, a2, a3, b[0], b[1]);
+                    mma16816(ks & 1 ? t1 : s1, a0, a1, a2, a3, b[2], b[3]);
+                }
+                // x[h]: row gq + 8h, keys kb + 2tq, + 1, kb + 8 + 2tq, + 1
+                float x[HR][4];
+#pragma unroll
+                for (int h = 0; h < HR; ++h) {
+                    x[h][0] = s0[2 * h] + t0[2 * h];
+                    x[h][1] = s0[2 * h + 1] + t0[2 * h + 1];
+                    x[h][2] = s1[2 * h] + t1[2 * h];
+                    x[h][3] = s1[2 * h + 1] + t1[2 * h + 1];
+                }
+                const bool edge = kb + 15 > q_first || kb < lo_all;   // of the mask
+                if (edge) {
+#pragma unroll
+                    for (int h = 0; h < HR; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = kb + 2 * tq + (e & 1) + 8 * (e >> 1);
+                            if (key > qpos[h] || (p.window > 0 && qpos[h] - key >= p.window))
+                                x[h][e] = -CUDART_INF_F;
+                        }
+                }
+                // ---- online softmax: the maximum moves only when a score exceeds it by 2^8
+                bool grow = false;
+#pragma unroll
+                for (int h = 0; h < HR; ++h) {
+                    const float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+                    grow |= mx * p.scale_log2 > m[h] + kRescaleThreshold;
+                }
+                if (__any_sync(0xffffffffu, grow)) {
+                    float f[HR];
+#pragma unroll
+                    for (int h = 0; h < HR; ++h) {
+                        float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        const float mn = fmaxf(m[h], mx * p.scale_log2);
+                        f[h] = m[h] == -CUDART_INF_F ? 0.f : ex2_approx(m[h] - mn);
+                        m[h] = mn;
+                        mr[h] = mn == -CUDART_INF_F ? 0.f : mn;
+                        l[h] *= f[h];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+#pragma unroll
+                        for (int h = 0; h < HR; ++h) {
+                            o[i][2 * h] *= f[h];
+                            o[i][2 * h + 1] *= f[h];
+                        }
+                }
+                // P as the A operand: rows gq (+ 8), keys 2tq, + 1 and 8 + 2tq, + 1; the sum
+                // takes the unrounded weights
+                uint32_t pa[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int h = 0; h < HR; ++h) {
+                    const float e0 = ex2_approx(fmaf(x[h][0], p.scale_log2, -mr[h]));
+                    const float e1 = ex2_approx(fmaf(x[h][1], p.scale_log2, -mr[h]));
+                    const float e2 = ex2_approx(fmaf(x[h][2], p.scale_log2, -mr[h]));
+                    const float e3 = ex2_approx(fmaf(x[h][3], p.scale_log2, -mr[h]));
+                    l[h] += (e0 + e1) + (e2 + e3);
+                    pa[h] = pack_bf16x2(e0, e1);
+                    pa[2 + h] = pack_bf16x2(e2, e3);
+                }
+                // ---- O += P V
+                // masks of the B fragment's keys 2tq, + 1 (and + 8): those that some row sees
+                uint32_t seen0 = 0xffffffffu, seen1 = 0xffffffffu;
+                if (edge) {
+                    const int ka = kb + 2 * tq;
+                    auto in = [&](int key) { return key >= lo && key < sg.S; };
+                    seen0 = (in(ka) ? 0xffffu : 0u) | (in(ka + 1) ? 0xffff0000u : 0u);
+                    seen1 = (in(ka + 8) ? 0xffffu : 0u) | (in(ka + 9) ? 0xffff0000u : 0u);
+                }
+                bool stripped = false;
+#pragma unroll
+                for (int nn = 0; nn < 8; ++nn) {
+                    uint32_t b[4];
+                    const int c = 2 * nn + (mat >> 1);
+                    ldsm4_trans(b, base + (c >> 3) * kHalfBytes + v_row + (((c & 7) ^ l7) << 4));
+                    if (edge) {
+                        b[0] &= seen0;
+                        b[1] &= seen1;
+                        b[2] &= seen0;
+                        b[3] &= seen1;
+                        if (sg.T > 1) {   // some of the block's keys are hidden from some rows
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) stripped |= strip_nonfinite(b[i]);
+                        }
+                    }
+                    mma16816(o[2 * nn], pa[0], pa[1], pa[2], pa[3], b[0], b[1]);
+                    mma16816(o[2 * nn + 1], pa[0], pa[1], pa[2], pa[3], b[2], b[3]);
+                }
+                if (__any_sync(0xffffffffu, stripped)) {
+                    // add what was taken out to the rows that see it: this thread's elements
+                    // are rows gq (+ 8), dims 8 i + 2 tq, + 1
+                    for (int kk = 0; kk < 16; ++kk) {
+                        const int key = kb + kk;
+                        if (key < lo || key >= sg.S) continue;
+                        const uint8_t *vr = smem + st * kStageBytes + 2 * kHalfBytes +
+                                            (16 * warp + kk) * 128 + 4 * tq;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                                vr + (i >> 3) * kHalfBytes + (((i & 7) ^ (kk & 7)) << 4));
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float y = e ? bf16hi(w) : bf16lo(w);
+                                if (isfinite(y)) continue;
+#pragma unroll
+                                for (int h = 0; h < HR; ++h)
+                                    if (key <= qpos[h] && (p.window <= 0 || qpos[h] - key < p.window))
+                                        o[i][2 * h + e] += y;
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->empty[st]);
+        }
+        // ---- the pair's (or span's) result: merge the four warps
+#pragma unroll
+        for (int h = 0; h < HR; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            if (tq == 0) bars->ml[warp][gq + 8 * h] = make_float2(m[h], l[h]);
+        }
+        if (!meet()) return;
+        float *mine = xchg + warp * kMaxRows * kRowFloats;
+#pragma unroll
+        for (int h = 0; h < HR; ++h) {
+            float M = -CUDART_INF_F;
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, bars->ml[w][gq + 8 * h].x);
+            const float f = m[h] == -CUDART_INF_F && M != m[h] ? 0.f : ex2_approx(mr[h] - (M == -CUDART_INF_F ? 0.f : M));
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                *reinterpret_cast<float2 *>(mine + (gq + 8 * h) * kRowFloats + 8 * i + 2 * tq) =
+                    make_float2(o[i][2 * h] * f, o[i][2 * h + 1] * f);
+        }
+        // every thread: dims 2 dd, + 1 of every other row
+        const int dd = threadIdx.x & 63;
+        float Mr[ROWS / 2], Lr[ROWS / 2];
+#pragma unroll
+        for (int i = 0; i < ROWS / 2; ++i) {
+            const int r = (threadIdx.x >> 6) + 2 * i;
+            float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, bars->ml[w][r].x);
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) {
+                const float2 x = bars->ml[w][r];
+                if (x.x == -CUDART_INF_F && M != x.x) L += x.y * 0.f;   // a warp without keys
+                else L += x.y * ex2_approx(x.x == -CUDART_INF_F ? 0.f : x.x - M);
+            }
+            Mr[i] = M;
+            Lr[i] = L;
+        }
+        if (!meet()) return;
+#pragma unroll
+        for (int i = 0; i < ROWS / 2; ++i) {
+            const int r = (threadIdx.x >> 6) + 2 * i;
+            if (r >= rows) continue;
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kConsumers; ++w) {
+                const float2 y = *reinterpret_cast<const float2 *>(
+                    xchg + (w * kMaxRows + r) * kRowFloats + 2 * dd);
+                acc.x += y.x;
+                acc.y += y.y;
+            }
+            if (sg.slot >= 0) {
+                const size_t rec = (size_t)sg.slot * kMaxRows + r;
+                reinterpret_cast<float2 *>(p.ws_o + rec * kD)[dd] = acc;
+                if (dd == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(Mr[i], Lr[i]);
+            } else {
+                const int t = r / p.G, head = sg.g * p.G + r - t * p.G;
+                const long row = sg.row0 + t;
+                const float inv = 1.0f / Lr[i];
+                reinterpret_cast<uint32_t *>(p.o + row * p.o_stride + head * kD)[dd] =
+                    pack_bf16x2(acc.x * inv, acc.y * inv);
+                if (p.lse && dd == 0)
+                    p.lse[(long)head * p.bounds.total + row] =
+                        (Mr[i] + __log2f(Lr[i])) * 0.69314718055994531f;
+            }
+        }
+    }
+}
+
+// Merges the partials of pairs that span several CTAs: one warp per (token, query head),
+// 4 dims per lane.
+__global__ void __launch_bounds__(256) paged_decode_combine_kernel(const Params p, int ctas) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int row = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int i = packed_row_seq(p.cu, p.nseq, row);
+    if (i >= p.nseq || h >= p.Hq) return;
+    const PackedSeq s = packed_seq(p.cu, p.kv_lens, i, p.bounds, nullptr);
+    if (row < s.row0 || row >= s.row0 + s.T) return;
+    const int n = count_units(s, p.window), g = h / p.G;
+    const int per = (p.ws_units[p.nseq] + ctas - 1) / ctas;
+    const int a = p.ws_units[i] + g * n;
+    const int c0 = a / per, c1 = (a + n - 1) / per;
+    if (c0 == c1) return;   // finished by its CTA
+    const int r = (row - s.row0) * p.G + h - g * p.G;
+    auto rec = [&](int c) { return (size_t)(2 * c + (c == c0 ? 1 : 0)) * kMaxRows + r; };
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
+    float M = -CUDART_INF_F;
+    for (int c = c0; c <= c1; ++c) M = fmaxf(M, ml[rec(c)].x);
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+        const float2 x = ml[rec(c)];
+        const float4 y = reinterpret_cast<const float4 *>(p.ws_o + rec(c) * kD)[lane];
+        // a span none of whose keys this row sees: m = -inf, l = 0 and O = 0
+        const float f = x.x == -CUDART_INF_F ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx(x.x - M);
+        L = fmaf(x.y, f, L);
+        acc.x = fmaf(y.x, f, acc.x);
+        acc.y = fmaf(y.y, f, acc.y);
+        acc.z = fmaf(y.z, f, acc.z);
+        acc.w = fmaf(y.w, f, acc.w);
+    }
+    const float inv = 1.0f / L;
+    reinterpret_cast<uint2 *>(p.o + (long)row * p.o_stride + h * kD)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (p.lse && lane == 0)
+        p.lse[(long)h * p.bounds.total + row] = (M + __log2f(L)) * 0.69314718055994531f;
+}
+
+// One CTA per (sequence, KV head) and no combine: for short caches.
+bool whole_pairs(int max_kv) { return max_kv <= 8 * kUnit; }
+
+}  // namespace
+
+bool paged_decode_fits(int max_q, int G) { return static_cast<long>(max_q) * G <= kMaxRows; }
+
+size_t paged_decode_workspace_bytes(int nseq, int max_kv) {
+    if (whole_pairs(max_kv)) return 0;
+    const size_t rec = (size_t)2 * kSMs * kMaxRows;
+    return rec * (kD + 2) * sizeof(float) + ((size_t)nseq + 1) * sizeof(int);
+}
+
+int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
+    const gqa_paged_kv &c = *a.cache;
+    Params p{};
+    p.q = static_cast<const __nv_bfloat16 *>(a.q);
+    p.o = static_cast<__nv_bfloat16 *>(a.o);
+    p.lse = a.lse;
+    p.cu = a.cu;
+    p.kv_lens = c.kv_lens;
+    p.pages = c.page_table;
+    p.status = status;
+    p.q_stride = a.q_stride;
+    p.o_stride = a.o_stride;
+    p.bounds = {a.total, a.max_q, a.max_kv, (long)c.max_pages * c.page_size};
+    p.nseq = a.nseq;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.Hq / a.Hkv;
+    p.window = a.window;
+    p.num_pages = c.num_pages;
+    p.page_size = c.page_size;
+    p.max_pages = c.max_pages;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.whole = whole_pairs(a.max_kv);
+    // units are counted in 32 bits
+    if ((long)a.nseq * a.Hkv * ((a.max_kv + kUnit - 1) / kUnit) > 0x7fffffffL - kSMs)
+        return GQA_ERR_UNSUPPORTED;
+    if (!p.whole) {
+        const size_t rec = (size_t)2 * kSMs * kMaxRows;
+        p.ws_o = static_cast<float *>(ws);
+        p.ws_ml = p.ws_o + rec * kD;
+        p.ws_units = reinterpret_cast<int *>(p.ws_ml + rec * 2);
+    }
+    const long slabs = (long)c.num_pages * c.Hkv, page = c.page_size;
+    const int box = c.page_size < kUnit ? c.page_size : kUnit;
+    CUtensorMap mk, mv;
+    if (!make_rows_map(&mk, c.k, page, kD, slabs, page * kD, box, 1) ||
+        !make_rows_map(&mv, c.v, page, kD, slabs, page * kD, box, 1))
+        return GQA_ERR_CUDA;
+    const long grid = p.whole ? (long)a.nseq * a.Hkv : kSMs;
+    auto kern = static_cast<long>(a.max_q) * p.G <= 8 ? paged_decode_kernel<8>
+                                                      : paged_decode_kernel<16>;
+    if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes) != cudaSuccess)
+        return GQA_ERR_CUDA;
+    if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, mk, mv,
+                   p) != cudaSuccess)
+        return GQA_ERR_CUDA;
+    if (!p.whole &&
+        launch_pdl(paged_decode_combine_kernel, dim3(a.total, (a.Hq + 7) / 8), dim3(256), 0, s, p,
+                   kSMs) != cudaSuccess)
+        return GQA_ERR_CUDA;
+    return GQA_OK;
+}
+
+}  // namespace gqa
