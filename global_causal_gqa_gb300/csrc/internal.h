@@ -154,11 +154,14 @@ size_t packed_prefill_workspace_bytes(int total, int max_kv, int Hq, int Hkv);
 // the streaming kernel for a few rows per sequence (paged_decode.cu)
 bool paged_decode_fits(int max_q, int G);
 int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
-size_t paged_decode_workspace_bytes(int nseq, int max_kv);
+size_t paged_decode_workspace_bytes(int max_kv);
 // bf16 [n2, n1, 128] with strides s1, s2 in elements, boxes of b2 x b1 rows of 64 elements,
 // 128-byte swizzle; false if the driver refuses it (packed_attn.cu)
 bool make_rows_map(CUtensorMap *map, const void *base, long n1, long s1, long n2, long s2, int b1,
                    int b2);
+// the pages of a cache, bf16 [slabs, page, 128]: boxes of `rows` rows, all 128 elements, which
+// land as the rows' elements 0-63, then 64-127, each 128-byte swizzled
+bool make_page_map(CUtensorMap *map, const void *base, long page, long slabs, int rows);
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
 size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv, int d);
 

@@ -27,6 +27,7 @@ __device__ __forceinline__ PackedSeq packed_seq(const int32_t *cu, const int32_t
                                                 const PackedBounds &b, int *status) {
     PackedSeq s;
     const int r0 = __ldg(cu + i), r1 = __ldg(cu + i + 1);
+    const int keys = kv_lens ? __ldg(kv_lens + i) : r1 - r0;   // in flight with the offsets
     s.row0 = r0;
     s.T = r1 - r0;
     if (r0 < 0 || r1 < r0 || r1 > b.total) {
@@ -34,7 +35,7 @@ __device__ __forceinline__ PackedSeq packed_seq(const int32_t *cu, const int32_t
         set_status(status, GQA_ERR_INVALID_ARG);
         return s;
     }
-    s.S = kv_lens ? __ldg(kv_lens + i) : s.T;
+    s.S = keys;
     if (s.T > 0) {
         if (s.S < s.T) {
             s.T = 0;

@@ -43,9 +43,22 @@ bool make_rows_map(CUtensorMap *map, const void *base, long n1, long s1, long n2
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv, int) {
+bool make_page_map(CUtensorMap *map, const void *base, long page, long slabs, int rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)page, 2, (cuuint64_t)slabs};
+    const cuuint64_t strides[3] = {256, 128, (cuuint64_t)page * 256};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 2, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t paged_workspace_bytes(int, int total, int max_q, int max_kv, int Hq, int Hkv, int) {
     return paged_decode_fits(max_q, Hq / Hkv)
-               ? paged_decode_workspace_bytes(nseq, max_kv)
+               ? paged_decode_workspace_bytes(max_kv)
                : packed_prefill_workspace_bytes(total, max_kv, Hq, Hkv);
 }
 

@@ -18,12 +18,17 @@
 // sequence) and finds its own start.
 //
 // A producer warp streams K and V by TMA into a ring of 6 stages of 64 keys (192 KB in
-// flight per SM), one box per page and half of the head dimension, 128-byte swizzle; it runs
-// ahead over the ends of pairs.  Four consumer warps take 16 keys of each stage:
-// S = Q K^T and O += P V as m16n8k16 bf16 MMAs with the rows as M (P leaves the score
-// product in the layout of an A operand), fp32 accumulators and softmax statistics, the row
-// maximum updated only when a score exceeds it by 2^8 (exact: sum and O share the
-// reference).  At the end of a pair the four warps merge through shared memory.
+// flight per SM) and runs ahead over the ends of pairs.  A box is one page with both halves of
+// the head dimension (their rows 128-byte swizzled): for 64 windows of 2048 keys in pages of
+// 16, 98 us; with a box per half 121 us.  Four consumer warps take 16 keys of each stage
+// (eight, four to a stage in turn, were no faster; with nothing computed at all that batch
+// took 91 us).  S = Q K^T and O += P V are m16n8k16 bf16 MMAs with the rows as M, so that P
+// leaves the score product in the layout of an A operand; accumulators and softmax statistics
+// are fp32, P is rounded to bf16 for its product, and the row maximum moves only when a score
+// exceeds it by 2^8 (exact: sum and O share the reference).  At the end of a pair the warps
+// merge through shared memory.
+//
+// Measured (GB300): 32 caches of 8k-64k tokens, 8 KV heads, 64-token pages: 785 us, 6.9 TB/s.
 //
 // Hidden keys have weight 0, but 0 * NaN is NaN: in blocks that straddle an edge of the mask
 // the values of keys that no row sees are zeroed on their way into the product, and
@@ -42,14 +47,13 @@ namespace {
 constexpr int kD = 128;
 constexpr int kUnit = 64;                       // keys of a stage
 constexpr int kStages = 6;
-constexpr int kHalfBytes = kUnit * 128;         // 64 keys x 64 dims
-constexpr int kStageBytes = 4 * kHalfBytes;     // K halves, V halves
+constexpr int kTileBytes = kUnit * kD * 2;      // K or V of a stage
+constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kConsumers = 4;                   // warps, 16 keys of a stage each
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kMaxRows = 16;
-constexpr int kRowFloats = 132;                 // a row of the exchange, padded off its bank
 constexpr int kSmemXchg = kStages * kStageBytes;
-constexpr int kSmemBar = kSmemXchg + kConsumers * kMaxRows * kRowFloats * 4;
+constexpr int kSmemBar = kSmemXchg + kConsumers * kMaxRows * kD * 4;
 constexpr int kSmemBytes = kSmemBar + 1024 + 1024;
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
 constexpr int kSegSlots = 4;
@@ -59,6 +63,11 @@ constexpr int kSMs = 152;
 struct Segment {
     int row0, T, S, seq, g, unit0, stages;
     int slot;   // -1: all of the pair's keys; else the partial's place
+};
+
+// A pair whose keys begin in one CTA and go on in the next ones.  rows = 0: none.
+struct Joint {
+    int row0, g, rows, parts;
 };
 
 struct Bars {
@@ -77,13 +86,13 @@ struct Params {
     __nv_bfloat16 *o;
     float *lse;
     float *ws_o, *ws_ml;
-    int *ws_units;                 // units before each sequence, and in all
+    Joint *ws_joint;               // one per CTA
     const int32_t *cu, *kv_lens, *pages;
     int *status;
     long q_stride, o_stride;
     PackedBounds bounds;
     int nseq, Hq, Hkv, G, window, num_pages, page_size, max_pages;
-    int whole;                     // 1: one CTA per pair
+    int whole;                     // 1: CTAs take whole pairs, every gridDim.x-th one
     float scale_log2;
 };
 
@@ -158,10 +167,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- this CTA's run of units
     int run = 0, per = 0;          // units of the run; of every CTA's run
     if (p.whole) {
-        if (threadIdx.x == 0) {
-            bars->start_seq = blockIdx.x / p.Hkv;
-            bars->start_unit = 0;
-        }
         __syncthreads();
     } else {
         const int m = (p.nseq + kThreads - 1) / kThreads;   // sequences per thread
@@ -202,14 +207,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 at += n;
             }
         }
-        if (blockIdx.x == 0) {   // for the combine kernel
-            int at = before;
-            for (int i = s0; i < s0 + m && i < p.nseq; ++i) {
-                p.ws_units[i] = at;
-                at += p.Hkv * count_units(packed_seq(p.cu, p.kv_lens, i, p.bounds, nullptr), p.window);
-            }
-            if (threadIdx.x == 0) p.ws_units[p.nseq] = all;
-        }
         __syncthreads();
     }
 
@@ -222,19 +219,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         int u = 0;   // stages issued
         int seq = bars->start_seq, off = bars->start_unit;   // off: units into the sequence
+        int pair = blockIdx.x;                               // (whole pairs)
+        Joint joint{0, 0, 0, 0};
         // boxes of a stage: one per page, or per 64 keys of a longer page
         const int box = min(p.page_size, kUnit), boxes = kUnit / box;
         for (int k = 0;; ++k) {
             Segment sg;
             sg.stages = -1;
-            while (p.whole ? k == 0 && sg.stages < 0 : run > 0) {
+            while (p.whole ? pair < p.nseq * p.Hkv : run > 0) {
+                if (p.whole) seq = pair / p.Hkv;
                 const PackedSeq s = packed_seq(p.cu, p.kv_lens, seq, p.bounds,
                                                p.whole && lane == 0 ? p.status : nullptr);
                 const int n = count_units(s, p.window);
                 if (p.whole) {
-                    off = n * (blockIdx.x % p.Hkv);
+                    off = n * (pair - seq * p.Hkv);
                     run = n;
-                    if (n == 0) break;
+                    pair += gridDim.x;
+                    if (n == 0) continue;
                 } else if (off >= n * p.Hkv) {
                     ++seq;   // run > 0: a later sequence has units
                     off = 0;
@@ -251,6 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sg.slot = sg.stages == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (in == 0 ? 1 : 0);
                 off += sg.stages;
                 run -= sg.stages;
+                if (in == 0 && sg.stages < n)   // the rest of the pair's units, per CTA
+                    joint = {s.row0, sg.g, s.T * p.G, 1 + (n - sg.stages + per - 1) / per};
                 break;
             }
             const int slot = k & (kSegSlots - 1);
@@ -264,7 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars->seg_full[slot]);
             }
             __syncwarp();
-            if (sg.stages < 0) break;
+            if (sg.stages < 0) {
+                if (!p.whole && lane == 0) p.ws_joint[blockIdx.x] = joint;
+                break;
+            }
             const int lo = p.window > 0 ? max(0, sg.S - sg.T - p.window + 1) : 0;
             // the slab of this lane's box of a stage; -1 for one that no row sees or that is
             // not in the pool (its box is zero fill).  The next stage's entries are fetched
@@ -293,12 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], kStageBytes);
                 __syncwarp();
                 if (lane < boxes) {
-                    uint8_t *dst = smem + st * kStageBytes + lane * box * 128;
+                    uint8_t *dst = smem + st * kStageBytes + lane * box * kD * 2;
                     const int row = p.page_size > kUnit ? ((sg.unit0 + j) * kUnit) % p.page_size : 0;
-                    tma_load_3d(dst, &tmK, &bars->full[st], 0, row, slab);
-                    tma_load_3d(dst + kHalfBytes, &tmK, &bars->full[st], 64, row, slab);
-                    tma_load_3d(dst + 2 * kHalfBytes, &tmV, &bars->full[st], 0, row, slab);
-                    tma_load_3d(dst + 3 * kHalfBytes, &tmV, &bars->full[st], 64, row, slab);
+                    tma_load_4d(dst, &tmK, &bars->full[st], 0, row, 0, slab);
+                    tma_load_4d(dst + kTileBytes, &tmV, &bars->full[st], 0, row, 0, slab);
                 }
                 __syncwarp();
                 slab = next;
@@ -315,12 +319,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int gq = lane >> 2, tq = lane & 3;
     constexpr int HR = ROWS / 8;                  // row halves in use
     const uint32_t ring = smem_u32(smem);
-    float *xchg = reinterpret_cast<float *>(smem + kSmemXchg);
+    float2 *xchg = reinterpret_cast<float2 *>(smem + kSmemXchg);
     // ldmatrix rows: K: matrices (keys 0-7 | 8-15) x (chunk 2ks | 2ks + 1); V transposed:
     // (dim chunk 2nn | 2nn + 1) x (keys 0-7 | 8-15)
     const int mat = lane >> 3, l7 = lane & 7;
-    const uint32_t k_row = (16 * warp + ((mat >> 1) << 3) + l7) * 128;
-    const uint32_t v_row = 2 * kHalfBytes + (16 * warp + ((mat & 1) << 3) + l7) * 128;
+    const int box = min(p.page_size, kUnit);
+    const uint32_t half = box * 128;          // a box: its rows' dims 0-63, then 64-127
+    const int part = 16 * warp;               // first of this warp's keys in a stage
+    const uint32_t rows16 = part / box * 2 * half + part % box * 128;
+    const uint32_t k_row = rows16 + (((mat >> 1) << 3) + l7) * 128;
+    const uint32_t v_row = kTileBytes + rows16 + (((mat & 1) << 3) + l7) * 128;
     int meets = 0;
     auto meet = [&]() {
         __syncwarp();
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 1, u);
                 return;
             }
-            const int kb = (sg.unit0 + j) * kUnit + 16 * warp;   // this warp's 16 keys
+            const int kb = (sg.unit0 + j) * kUnit + part;   // this warp's 16 keys
             if (kb < sg.S && kb + 15 >= lo) {
                 const uint32_t base = ring + st * kStageBytes;
                 // ---- scores: rows x 16 keys, two chains per 8 keys
@@ -388,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int ks = 0; ks < 8; ++ks) {
                     uint32_t b[4];
                     const int c = 2 * ks + (mat & 1);
-                    ldsm4(b, base + (c >> 3) * kHalfBytes + k_row + (((c & 7) ^ l7) << 4));
+                    ldsm4(b, base + (c >> 3) * half + k_row + (((c & 7) ^ l7) << 4));
                     const uint32_t a0 = qa[ks][0], a1 = HR > 1 ? qa[ks][1] : 0u;
                     const uint32_t a2 = qa[ks][HR], a3 = HR > 1 ? qa[ks][HR + 1] : 0u;
                     mma16816(ks & 1 ? t0 : s0, a0, a1, a2, a3, b[0], b[1]);
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int nn = 0; nn < 8; ++nn) {
                     uint32_t b[4];
                     const int c = 2 * nn + (mat >> 1);
-                    ldsm4_trans(b, base + (c >> 3) * kHalfBytes + v_row + (((c & 7) ^ l7) << 4));
+                    ldsm4_trans(b, base + (c >> 3) * half + v_row + (((c & 7) ^ l7) << 4));
                     if (edge) {
                         b[0] &= seen0;
                         b[1] &= seen1;
@@ -489,12 +497,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 16; ++kk) {
                         const int key = kb + kk;
                         if (key < lo || key >= sg.S) continue;
-                        const uint8_t *vr = smem + st * kStageBytes + 2 * kHalfBytes +
-                                            (16 * warp + kk) * 128 + 4 * tq;
+                        const uint8_t *vr = smem + st * kStageBytes + kTileBytes + rows16 +
+                                            kk * 128 + 4 * tq;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                                vr + (i >> 3) * kHalfBytes + (((i & 7) ^ (kk & 7)) << 4));
+                                vr + (i >> 3) * half + (((i & 7) ^ (kk & 7)) << 4));
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const float y = e ? bf16hi(w) : bf16lo(w);
@@ -519,17 +527,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tq == 0) bars->ml[warp][gq + 8 * h] = make_float2(m[h], l[h]);
         }
         if (!meet()) return;
-        float *mine = xchg + warp * kMaxRows * kRowFloats;
+        // the exchange: [4][16 rows][64 pairs of dims], a row's pairs permuted so that the 16
+        // lanes of a half warp (4 rows x 4 pairs) meet 16 different places
+        auto place = [&](int i, int h) {
+            return xchg + (warp * kMaxRows + gq + 8 * h) * 64 + ((4 * i + tq) ^ ((gq & 3) << 2));
+        };
 #pragma unroll
         for (int h = 0; h < HR; ++h) {
             float M = -CUDART_INF_F;
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, bars->ml[w][gq + 8 * h].x);
-            const float f = m[h] == -CUDART_INF_F && M != m[h] ? 0.f : ex2_approx(mr[h] - (M == -CUDART_INF_F ? 0.f : M));
+            // this warp's outputs, relative to M (0 where it saw no key and another one did)
+            const float f = m[h] == -CUDART_INF_F && M != m[h]
+                                ? 0.f
+                                : ex2_approx(mr[h] - (M == -CUDART_INF_F ? 0.f : M));
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                *reinterpret_cast<float2 *>(mine + (gq + 8 * h) * kRowFloats + 8 * i + 2 * tq) =
-                    make_float2(o[i][2 * h] * f, o[i][2 * h + 1] * f);
+            for (int i = 0; i < 16; ++i) {
+                *place(i, h) = make_float2(o[i][2 * h] * f, o[i][2 * h + 1] * f);
+            }
         }
         // every thread: dims 2 dd, + 1 of every other row
         const int dd = threadIdx.x & 63;
@@ -543,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) {
                 const float2 x = bars->ml[w][r];
-                if (x.x == -CUDART_INF_F && M != x.x) L += x.y * 0.f;   // a warp without keys
+                if (x.x == -CUDART_INF_F && M != x.x) L += x.y * 0.f;   // 0, or NaN
                 else L += x.y * ex2_approx(x.x == -CUDART_INF_F ? 0.f : x.x - M);
             }
             Mr[i] = M;
@@ -557,8 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) {
-                const float2 y = *reinterpret_cast<const float2 *>(
-                    xchg + (w * kMaxRows + r) * kRowFloats + 2 * dd);
+                const float2 y = xchg[(w * kMaxRows + r) * 64 + (dd ^ ((r & 3) << 2))];
                 acc.x += y.x;
                 acc.y += y.y;
             }
@@ -580,58 +594,102 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Merges the partials of pairs that span several CTAs: one warp per (token, query head),
-// 4 dims per lane.
-__global__ void __launch_bounds__(256) paged_decode_combine_kernel(const Params p, int ctas) {
+// Merges the partials of pairs that span several CTAs.  Block (c, r) takes row r of the pair
+// that begins in attention CTA c and goes on in the next ones.  Every warp forms the
+// partials' weights (a lane per partial; there are at most kSMs), the four warps add up every
+// fourth partial, 4 dims per lane, and their sums meet in shared memory.  A warp's first
+// weight and partial are fetched along with the block's record, not after it.
+// (A warp per row and its partials in turn took 20 us for one pair that all CTAs share.)
+constexpr int kCombineWarps = 4;
+__global__ void __launch_bounds__(32 * kCombineWarps) paged_decode_combine_kernel(const Params p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int row = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int i = packed_row_seq(p.cu, p.nseq, row);
-    if (i >= p.nseq || h >= p.Hq) return;
-    const PackedSeq s = packed_seq(p.cu, p.kv_lens, i, p.bounds, nullptr);
-    if (row < s.row0 || row >= s.row0 + s.T) return;
-    const int n = count_units(s, p.window), g = h / p.G;
-    const int per = (p.ws_units[p.nseq] + ctas - 1) / ctas;
-    const int a = p.ws_units[i] + g * n;
-    const int c0 = a / per, c1 = (a + n - 1) / per;
-    if (c0 == c1) return;   // finished by its CTA
-    const int r = (row - s.row0) * p.G + h - g * p.G;
-    auto rec = [&](int c) { return (size_t)(2 * c + (c == c0 ? 1 : 0)) * kMaxRows + r; };
+    constexpr int W = kCombineWarps;
+    __shared__ float4 part[W][32];
+    const int w0 = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
+    // partial k: CTA c + k, its last pair for k = 0, its first for the others
+    auto rec = [&](int k) {
+        return (size_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kMaxRows + r;
+    };
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
-    float M = -CUDART_INF_F;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, ml[rec(c)].x);
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const float2 x = ml[rec(c)];
-        const float4 y = reinterpret_cast<const float4 *>(p.ws_o + rec(c) * kD)[lane];
-        // a span none of whose keys this row sees: m = -inf, l = 0 and O = 0
-        const float f = x.x == -CUDART_INF_F ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx(x.x - M);
-        L = fmaf(x.y, f, L);
-        acc.x = fmaf(y.x, f, acc.x);
-        acc.y = fmaf(y.y, f, acc.y);
-        acc.z = fmaf(y.z, f, acc.z);
-        acc.w = fmaf(y.w, f, acc.w);
+    auto out = [&](int k) { return reinterpret_cast<const float4 *>(p.ws_o + rec(k) * kD)[lane]; };
+    // (used only if the record says that these are there)
+    const int most = kSMs - blockIdx.x;   // partials there can be
+    float2 x0 = make_float2(0.f, 0.f);
+    float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane < most) x0 = ml[rec(lane)];
+    if (w0 < most) y0 = out(w0);
+    const Joint j = p.ws_joint[blockIdx.x];
+    if (r >= j.rows) return;   // also where nothing begins (rows = 0)
+    constexpr int kTurns = (kSMs + 31) / 32;
+    float2 x[kTurns];
+    float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        x[i] = make_float2(-CUDART_INF_F, 0.f);
+        if (32 * i + lane < j.parts) x[i] = i == 0 ? x0 : ml[rec(32 * i + lane)];
+        M = fmaxf(M, x[i].x);
     }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        if (32 * i >= j.parts) break;
+        // a partial none of whose keys this row sees: m = -inf, l = 0 and O = 0 (NaN scores
+        // alone also leave m at -inf, with l and O NaN)
+        const float f = x[i].x == -CUDART_INF_F ? (x[i].y == 0.f ? 0.f : 1.f) : ex2_approx(x[i].x - M);
+        L = fmaf(x[i].y, f, L);
+        float4 y[32 / W];   // all in flight together
+#pragma unroll
+        for (int n = 0; n < 32 / W; ++n) {
+            const int k = 32 * i + n * W + w0;
+            y[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < j.parts) y[n] = k == w0 ? y0 : out(k);
+        }
+#pragma unroll
+        for (int n = 0; n < 32 / W; ++n) {
+            const float fk = __shfl_sync(0xffffffffu, f, n * W + w0);
+            if (32 * i + n * W + w0 >= j.parts) continue;   // (fk may be a NaN's 1)
+            acc.x = fmaf(y[n].x, fk, acc.x);
+            acc.y = fmaf(y[n].y, fk, acc.y);
+            acc.z = fmaf(y[n].z, fk, acc.z);
+            acc.w = fmaf(y[n].w, fk, acc.w);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    part[w0][lane] = acc;
+    __syncthreads();
+    if (w0 > 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+        const float4 y = part[w][lane];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
+    }
+    const int t = r / p.G, h = j.g * p.G + r - t * p.G;
+    const long row = j.row0 + t;
     const float inv = 1.0f / L;
-    reinterpret_cast<uint2 *>(p.o + (long)row * p.o_stride + h * kD)[lane] =
+    reinterpret_cast<uint2 *>(p.o + row * p.o_stride + h * kD)[lane] =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (p.lse && lane == 0)
         p.lse[(long)h * p.bounds.total + row] = (M + __log2f(L)) * 0.69314718055994531f;
 }
 
-// One CTA per (sequence, KV head) and no combine: for short caches.
+// Short caches: whole pairs per CTA, one after the other, and no combine.
 bool whole_pairs(int max_kv) { return max_kv <= 8 * kUnit; }
 
 }  // namespace
 
 bool paged_decode_fits(int max_q, int G) { return static_cast<long>(max_q) * G <= kMaxRows; }
 
-size_t paged_decode_workspace_bytes(int nseq, int max_kv) {
+size_t paged_decode_workspace_bytes(int max_kv) {
     if (whole_pairs(max_kv)) return 0;
     const size_t rec = (size_t)2 * kSMs * kMaxRows;
-    return rec * (kD + 2) * sizeof(float) + ((size_t)nseq + 1) * sizeof(int);
+    return rec * (kD + 2) * sizeof(float) + kSMs * sizeof(Joint);
 }
 
 int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
@@ -664,26 +722,28 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
         const size_t rec = (size_t)2 * kSMs * kMaxRows;
         p.ws_o = static_cast<float *>(ws);
         p.ws_ml = p.ws_o + rec * kD;
-        p.ws_units = reinterpret_cast<int *>(p.ws_ml + rec * 2);
+        p.ws_joint = reinterpret_cast<Joint *>(p.ws_ml + rec * 2);
     }
     const long slabs = (long)c.num_pages * c.Hkv, page = c.page_size;
     const int box = c.page_size < kUnit ? c.page_size : kUnit;
     CUtensorMap mk, mv;
-    if (!make_rows_map(&mk, c.k, page, kD, slabs, page * kD, box, 1) ||
-        !make_rows_map(&mv, c.v, page, kD, slabs, page * kD, box, 1))
+    if (!make_page_map(&mk, c.k, page, slabs, box) || !make_page_map(&mv, c.v, page, slabs, box))
         return GQA_ERR_CUDA;
-    const long grid = p.whole ? (long)a.nseq * a.Hkv : kSMs;
-    auto kern = static_cast<long>(a.max_q) * p.G <= 8 ? paged_decode_kernel<8>
-                                                      : paged_decode_kernel<16>;
+    const long pairs = (long)a.nseq * a.Hkv;
+    const long grid = p.whole && pairs < kSMs ? pairs : kSMs;
+    const bool eight = static_cast<long>(a.max_q) * p.G <= 8;
+    auto kern = eight ? paged_decode_kernel<8> : paged_decode_kernel<16>;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes) != cudaSuccess)
         return GQA_ERR_CUDA;
     if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, mk, mv,
                    p) != cudaSuccess)
         return GQA_ERR_CUDA;
-    if (!p.whole &&
-        launch_pdl(paged_decode_combine_kernel, dim3(a.total, (a.Hq + 7) / 8), dim3(256), 0, s, p,
-                   kSMs) != cudaSuccess)
-        return GQA_ERR_CUDA;
+    if (!p.whole) {
+        const dim3 grid(kSMs, static_cast<unsigned>(a.max_q * p.G));
+        if (launch_pdl(paged_decode_combine_kernel, grid, dim3(32 * kCombineWarps), 0, s, p) !=
+            cudaSuccess)
+            return GQA_ERR_CUDA;
+    }
     return GQA_OK;
 }
 
