@@ -36,13 +36,13 @@
 // issued once PV_i(j) has completed.  O is rescaled only when a row's maximum grows by more
 // than 2^8 (exact: O and the sum share one reference maximum).
 //
-// The V guard.  A hidden key has weight 0, but 0 * NaN is NaN, so a value that no row may see
-// must not reach the product as NaN or infinity: rows past a sequence's end belong to another
-// sequence or to no one.  In the tiles that straddle an edge of the mask, warp 3 zeroes the
-// rows that no row of the item sees, and in those that only some rows see it replaces
-// non-finite elements by 0 and marks the key; the epilogue then adds a marked key's
-// non-finite elements to the rows that do see it.  Without such values the cost is reading
-// the edge rows of two tiles per item, off the critical path.
+// The V guard.  A hidden key has weight 0, but 0 * NaN is NaN, so a value that a row may not
+// see must not reach its product as NaN or infinity: rows past a sequence's end belong to
+// another sequence or to no one.  In the tiles that straddle an edge of the mask, warp 3 looks
+// at the rows that some row of the item does not see, replaces non-finite elements by 0 and
+// marks the keys that others do see; the epilogue adds a marked key's non-finite elements to
+// the rows that see it.  The softmax warps hand P over only when the guard is done with the
+// tile, so the MMA thread, which has no time to spare, knows nothing of it.
 //
 // Shared memory: Q 64 KB, ring 4 x 32 KB, O staging 2 x 16 KB (one half of the columns of
 // each tile at a time).
@@ -50,6 +50,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "internal.h"
 #include "packed.cuh"
@@ -101,7 +103,7 @@ struct Bars {
     uint64_t item_full[kItemSlots], item_free[kItemSlots];
     uint64_t q_full, q_free;
     uint64_t full[kSlots], empty[kSlots];         // K/V ring
-    uint64_t guard_go[2], guard[2];               // a guarded V tile is there / is clean (alternate)
+    uint64_t guard_go[2], guard[2];               // a guarded V tile is on its way / clean (alternate)
     uint64_t s_full[2], p_full[2], o_done[2];     // per query tile
     uint64_t o_final[2];                          // an item's last PV product of the tile
     uint64_t o_free[2];                           // the epilogue has read O out of TMEM
@@ -328,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int u = 0;        // ring loads issued
             int nq = 0;       // items whose Q tiles have been issued
             int claims = 0;   // responses asked for
+            int gc = 0;       // guarded V tiles issued
             Walk walk;
             auto fail = [&](int barrier, int at) {
                 ok = false;
@@ -446,6 +449,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                     ++u;
+                    if ((l & 1) && e.guarded(n0)) {
+                        if (lane == 0) mbar_arrive(&bars->guard_go[gc & 1]);
+                        ++gc;
+                    }
                     if constexpr (PAGED)
                         if (l & 1) slab = slab_next;
                     // Q after the item's first K and V: by then the previous item's last
@@ -474,7 +481,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t q0 = smem_u32(smem + kSmemQ);
                 bool ok = true;
                 int u = 0;                 // ring slots consumed
-                int gc = 0;                // guarded V tiles consumed
                 int cpv[2] = {0, 0};       // PV products issued, per query tile (all items)
                 int nepi[2] = {0, 0};      // items finished, per query tile
                 auto fail = [&](int barrier, int at) {
@@ -508,13 +514,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 sdesc_sw128(va + kk * 16 * 128, kBoxBytes, 1024), idesc_o,
                                 (acc || kk > 0) ? 1u : 0u);
                     umma_commit(&bars->o_done[i]);
-                    ++cpv[i];
-                };
-                // waits until PV product number cpv[i] - 1 of tile i has completed
-                auto wait_last_pv = [&](int i, int where) {
-                    if (cpv[i] > 0 && !mbar_wait(&bars->o_done[i], (cpv[i] - 1) & 1))
-                        fail(where, cpv[i]);
-                    tc_fence_after();
                 };
                 for (int k = 0;; ++k) {
                     ItemRec it;
@@ -524,72 +523,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (it.n_tiles < 0) break;
                     mbar_arrive(&bars->item_free[k & (kItemSlots - 1)]);
-                    const int ntile = it.ntok > p.Mt ? 2 : 1, n = it.n_tiles;
-                    const Edges e(it, p.window);
+                    const bool two = it.ntok > p.Mt;
+                    const int n = it.n_tiles;
                     int kst = 0, vst = 0;
                     if (!mbar_wait(&bars->q_full, k & 1)) {
                         fail(0, k);
                         break;
                     }
                     take(kst);
-                    for (int i = 0; i < ntile && ok; ++i) {
-                        // S_i(0) overwrites the columns the previous item's last P_i sits in
-                        wait_last_pv(i, 2);
-                        if (ok) issue_s(i, kst);
-                    }
+                    // S_i(0) overwrites the columns the previous item's last P_i sits in
+                    if (ok && cpv[0] > 0 && !mbar_wait(&bars->o_done[0], (cpv[0] - 1) & 1))
+                        fail(2, cpv[0]);
                     if (!ok) break;
+                    tc_fence_after();
+                    issue_s(0, kst);
+                    if (two) {
+                        if (cpv[1] > 0 && !mbar_wait(&bars->o_done[1], (cpv[1] - 1) & 1)) {
+                            fail(2, cpv[1]);
+                            break;
+                        }
+                        tc_fence_after();
+                        issue_s(1, kst);
+                    }
                     if (n == 1) umma_commit(&bars->q_free);
                     umma_commit(&bars->empty[kst]);
                     int kprev = kst;   // K slot of the last score products issued
+                    // one query tile's turn at key tile j (the index is a constant, so the
+                    // counters stay in registers)
+                    auto turn = [&](auto I, int j) {
+                        constexpr int i = decltype(I)::value;
+                        if (!mbar_wait(&bars->p_full[i], cpv[i] & 1)) return fail(3, cpv[i]);
+                        // the first PV of an item overwrites O_i: the previous item's
+                        // epilogue must have read it out
+                        if (j == 0 && nepi[i] > 0 &&
+                            !mbar_wait(&bars->o_free[i], (nepi[i] - 1) & 1))
+                            return fail(4, nepi[i]);
+                        tc_fence_after();
+                        issue_pv(i, vst, j > 0);
+                        ++cpv[i];
+                        if (j + 1 < n) {
+                            if (i == 0) take(kst);
+                            if (!ok) return;
+                            // S_i(j+1) overwrites the columns P_i(j) sits in
+                            if (!mbar_wait(&bars->o_done[i], (cpv[i] - 1) & 1)) return fail(5, cpv[i]);
+                            tc_fence_after();
+                            // PV_i(j) has completed, and with it every earlier product:
+                            // K(j) is free once PV_0(j) is, V(j) once the last tile's is
+                            if (i == 0 && j > 0) mbar_arrive(&bars->empty[kprev]);
+                            if (i == 1 || !two) mbar_arrive(&bars->empty[vst]);
+                            issue_s(i, kst);
+                            if (j + 2 == n && (i == 1 || !two)) umma_commit(&bars->q_free);
+                        } else {
+                            umma_commit(&bars->o_final[i]);
+                            // the item's last key tile: K and V go free when its products do
+                            if (i == 0 && j > 0) umma_commit(&bars->empty[kprev]);
+                            if (i == 1 || !two) umma_commit(&bars->empty[vst]);
+                        }
+                    };
                     for (int j = 0; j < n && ok; ++j) {
                         take(vst);
                         if (!ok) break;
-                        // the guard works while the softmax does
-                        const bool guarded = e.guarded((it.kt_first + j) * kBN);
-                        if (guarded) mbar_arrive(&bars->guard_go[gc & 1]);
-                        for (int i = 0; i < ntile && ok; ++i) {
-                            if (!mbar_wait(&bars->p_full[i], cpv[i] & 1)) {
-                                fail(3, cpv[i]);
-                                break;
-                            }
-                            // the first PV of an item overwrites O_i: the previous item's
-                            // epilogue must have read it out
-                            if (j == 0 && nepi[i] > 0 &&
-                                !mbar_wait(&bars->o_free[i], (nepi[i] - 1) & 1)) {
-                                fail(4, nepi[i]);
-                                break;
-                            }
-                            if (guarded && i == 0) {
-                                if (!mbar_wait(&bars->guard[gc & 1], (gc >> 1) & 1)) {
-                                    fail(7, gc);
-                                    break;
-                                }
-                                ++gc;
-                            }
-                            tc_fence_after();
-                            issue_pv(i, vst, j > 0);
-                            if (j == n - 1) umma_commit(&bars->o_final[i]);
-                            if (j + 1 < n) {
-                                if (i == 0) take(kst);
-                                if (!ok) break;
-                                // S_i(j+1) overwrites the columns P_i(j) sits in
-                                wait_last_pv(i, 5);
-                                // PV_i(j) has completed, and with it every earlier product:
-                                // K(j) is free once PV_0(j) is, V(j) once the last tile's is
-                                if (i == 0 && j > 0) mbar_arrive(&bars->empty[kprev]);
-                                if (i == ntile - 1) mbar_arrive(&bars->empty[vst]);
-                                if (ok) issue_s(i, kst);
-                                if (j + 2 == n && i == ntile - 1) umma_commit(&bars->q_free);
-                            } else {
-                                // the item's last key tile: K and V go free when its products do
-                                if (i == 0 && j > 0) umma_commit(&bars->empty[kprev]);
-                                if (i == ntile - 1) umma_commit(&bars->empty[vst]);
-                            }
-                        }
+                        turn(std::integral_constant<int, 0>{}, j);
+                        if (two && ok) turn(std::integral_constant<int, 1>{}, j);
                         kprev = kst;
                     }
                     if (!ok) break;
-                    for (int i = 0; i < ntile; ++i) ++nepi[i];
+                    ++nepi[0];
+                    if (two) ++nepi[1];
                 }
                 if (!ok) set_status(p.status, GQA_ERR_DEVICE_TIMEOUT);
                 // every tcgen05 operation issued above completes before TMEM is released
@@ -659,9 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < it.n_tiles; ++j) {
                     const int n0 = (it.kt_first + j) * kBN;
                     if (!e.guarded(n0)) continue;
-                    // the MMA thread has seen this V tile land and waits for the guard, so
-                    // the slot's phase cannot move on (waiting on it alone could take an
-                    // older phase of the same parity for this one)
+                    // The producer has armed the slot for this tile, and its phase cannot
+                    // move on before the guard is done (waiting on the slot alone could take
+                    // an older phase of the same parity for this one).
                     const int uu = u + 2 * j + 1, st = uu % kSlots;
                     if (!warp_wait(&bars->guard_go[gc & 1], (gc >> 1) & 1) ||
                         !warp_wait(&bars->full[st], (uu / kSlots) & 1)) {
@@ -671,48 +671,61 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t *tile = smem + kSmemRing + st * kTileBytes;
                     // rows [a, b) of the tile need a look: below the window's edge for some
-                    // row, or past the diagonal for some row
-                    auto look = [&](int a, int b) {
-                        // eight rows at a time, 4 lanes to a row of 16 16-byte chunks
-                        for (int r = a + (lane >> 2); r < b; r += 8) {
+                    // row, or past the diagonal for some row.  A lane holds one 16-byte piece
+                    // of a row, two rows to a load (which piece is which does not matter).
+                    const int pc = lane & 15;
+                    uint8_t *col = tile + (pc >> 3) * kBoxBytes + (pc & 7) * 16;
+                    // 0 * x stays 0 unless x is infinite or NaN: one packed multiply-add per
+                    // two elements, since this warp's instructions come off those of the
+                    // softmax warps beside it
+                    auto clean = [&](int a, int b) {
+                        uint32_t z = 0;
+                        for (int r0 = a + (lane >> 4); r0 < b; r0 += 16) {
+                            uint4 x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                x[i] = make_uint4(0, 0, 0, 0);
+                                if (r0 + 2 * i < b)
+                                    x[i] = *reinterpret_cast<const uint4 *>(col + (r0 + 2 * i) * 128);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                z = hfma2_bf16(x[i].x, 0u, z);
+                                z = hfma2_bf16(x[i].y, 0u, z);
+                                z = hfma2_bf16(x[i].z, 0u, z);
+                                z = hfma2_bf16(x[i].w, 0u, z);
+                            }
+                        }
+                        return (z & 0x7fff7fffu) == 0;   // neither half is NaN
+                    };
+                    bool touched = false;
+                    auto strip = [&](int a, int b) {
+                        for (int r = a + (lane >> 4); r < b; r += 2) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(col + r * 128);
+                            if (!(nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) ||
+                                  nonfinite2(x.w)))
+                                continue;
+                            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                if ((w[q] & 0x7f80u) == 0x7f80u) w[q] &= 0xffff0000u;
+                                if ((w[q] & 0x7f800000u) == 0x7f800000u) w[q] &= 0xffffu;
+                            }
+                            *reinterpret_cast<uint4 *>(col + r * 128) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                            touched = true;
                             const int key = n0 + r;
-                            const bool gone = key < e.lo || key > e.hi;
-                            bool marked = false;
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const int cc = (lane & 3) + 4 * c;   // order does not matter
-                                uint4 *at = reinterpret_cast<uint4 *>(tile + (cc >> 3) * kBoxBytes +
-                                                                      r * 128 + (cc & 7) * 16);
-                                if (gone) {
-                                    *at = make_uint4(0, 0, 0, 0);
-                                    continue;
-                                }
-                                const uint4 x = *at;
-                                if (!(nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) ||
-                                      nonfinite2(x.w)))
-                                    continue;
-                                marked = true;
-                                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    if ((w[q] & 0x7f80u) == 0x7f80u) w[q] &= 0xffff0000u;
-                                    if ((w[q] & 0x7f800000u) == 0x7f800000u) w[q] &= 0xffffu;
-                                }
-                                *at = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                            if (marked) {
-                                const int b0 = key > e.hi_all ? key - e.hi_all - 1
-                                                              : 256 + key - e.lo;
-                                atomicOr(&slot.bad[b0 >> 5], 1u << (b0 & 31));
-                                atomicOr(&slot.any_bad, 1u);
-                            }
+                            if (key < e.lo || key > e.hi) continue;
+                            const int b0 = key > e.hi_all ? key - e.hi_all - 1 : 256 + key - e.lo;
+                            atomicOr(&slot.bad[b0 >> 5], 1u << (b0 & 31));
+                            atomicOr(&slot.any_bad, 1u);
                         }
                     };
                     const int below = min(kBN, max(0, e.lo_all - n0));
                     const int above = min(kBN, max(below, e.hi_all + 1 - n0));
-                    look(0, below);
-                    look(above, kBN);
-                    fence_proxy_async_smem();
+                    if (!clean(0, below)) strip(0, below);
+                    if (!clean(above, kBN)) strip(above, kBN);
+                    if (touched) fence_proxy_async_smem();
                     mbar_arrive(&bars->guard[gc & 1]);
                     ++gc;
                 }
@@ -736,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pvb = 0;   // PV products of the previous items
         int ne = 0;    // items finished
         int ns = 0;    // halves handed to the store warp
+        int gc = 0;    // guarded V tiles (all items)
         bool ok = true;
         auto fail = [&](int barrier, int at) {
             ok = false;
@@ -743,6 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         for (int k = 0; ok; ++k) {
             int n_tiles, n0, qpos, ntok;
+            int g_lo, g_hi;   // V tiles that begin below g_lo or above g_hi are guarded
             {
                 ItemRec it;
                 const bool got = read_item(bars, k, it);
@@ -756,12 +771,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 n0 = it.kt_first * kBN;
                 // rows behind the last token compute what the last token's would
                 qpos = it.qpos0 + wg * p.Mt + min(rtok, min(ntok, p.Mt) - 1);
+                const Edges e(it, p.window);
+                g_lo = e.lo_all;
+                g_hi = e.hi_all - kBN + 1;
             }
             auto free_item = [&]() {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->item_free[k & (kItemSlots - 1)]);
             };
             if (ntok <= 0) {
+                for (int j = 0; j < n_tiles; ++j, n0 += kBN) gc += n0 < g_lo || n0 > g_hi;
                 free_item();
                 continue;
             }
@@ -774,8 +793,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 ++cs;
-                if (!warp_on) {   // no row of this warp is stored: its P may be anything
+                // P is handed over only when the values that it meets are clean
+                const bool guarded = n0 < g_lo || n0 > g_hi;
+                auto hand_over = [&]() {
+                    if (guarded) {
+                        if (!warp_wait(&bars->guard[gc & 1], (gc >> 1) & 1)) fail(5, gc);
+                        ++gc;
+                    }
                     mbar_arrive(&bars->p_full[wg]);
+                };
+                if (!warp_on) {   // no row of this warp is stored: its P may be anything
+                    hand_over();
+                    if (!ok) break;
                     continue;
                 }
                 tc_fence_after();
@@ -889,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&bars->p_full[wg]);
+                hand_over();
                 if (!ok) break;
             }
             if (!ok) break;

@@ -555,6 +555,13 @@ __device__ __forceinline__ float2 ex2_fma2(float2 x) {
                        __uint_as_float(__float_as_uint(pw.y) + (__float_as_uint(t.y) << 23)));
 }
 
+// Packed bf16x2 a * b + c.
+__device__ __forceinline__ uint32_t hfma2_bf16(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
