@@ -155,13 +155,11 @@ size_t packed_prefill_workspace_bytes(int total, int max_kv, int Hq, int Hkv);
 bool paged_decode_fits(int max_q, int G);
 int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int max_kv);
-// bf16 [n2, n1, 128] with strides s1, s2 in elements, boxes of b2 x b1 rows of 64 elements,
-// 128-byte swizzle; false if the driver refuses it (packed_attn.cu)
-bool make_rows_map(CUtensorMap *map, const void *base, long n1, long s1, long n2, long s2, int b1,
-                   int b2);
-// the pages of a cache, bf16 [slabs, page, 128]: boxes of `rows` rows, all 128 elements, which
-// land as the rows' elements 0-63, then 64-127, each 128-byte swizzled
-bool make_page_map(CUtensorMap *map, const void *base, long page, long slabs, int rows);
+// A TMA map of bf16 elements: `rank` dims and box extents, innermost first, the strides of
+// dims 1 .. rank - 1 in bytes, 128-byte swizzle; false if the driver refuses it
+// (packed_attn.cu)
+bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                   const uint64_t *strides, const uint32_t *box);
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
 size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv, int d);
 

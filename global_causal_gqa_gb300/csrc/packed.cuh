@@ -62,4 +62,32 @@ __device__ __forceinline__ int packed_row_seq(const int32_t *cu, int nseq, int r
     return n;
 }
 
+// A producer warp's walk over the page-table entries of one sequence, in order: the lanes
+// hold 32 entries and the 32 after them, so an entry has been on its way for at least 32
+// pages' worth of loads when it is needed.
+struct PageWalk {
+    const int32_t *row;   // the sequence's entries
+    int end;              // entries from here on are not needed (and not read)
+    int base, cur, next;
+
+    __device__ __forceinline__ int fetch(int i) const { return i < end ? __ldg(row + i) : -1; }
+    __device__ __forceinline__ PageWalk(const int32_t *r, int first, int e) : row(r), end(e) {
+        const int lane = threadIdx.x & 31;
+        base = first & ~31;
+        cur = fetch(base + lane);
+        next = fetch(base + 32 + lane);
+    }
+    // The entry of page `first` + i for lane i < n (n a power of two up to 32 that divides
+    // `first`; warp-collective); `first` does not decrease.
+    __device__ __forceinline__ int get(int first, int n) {
+        const int lane = threadIdx.x & 31;
+        while (first >= base + 32) {
+            base += 32;
+            cur = next;
+            next = fetch(base + 32 + lane);
+        }
+        return __shfl_sync(0xffffffffu, cur, first - base + (lane & (n - 1)));
+    }
+};
+
 }  // namespace gqa

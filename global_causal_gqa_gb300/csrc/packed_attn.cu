@@ -29,29 +29,20 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-bool make_rows_map(CUtensorMap *map, const void *base, long n1, long s1, long n2, long s2, int b1,
-                   int b2) {
+bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                   const uint64_t *strides, const uint32_t *box) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)128, (cuuint64_t)n1, (cuuint64_t)n2};
-    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
-              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_page_map(CUtensorMap *map, const void *base, long page, long slabs, int rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[4] = {64, (cuuint64_t)page, 2, (cuuint64_t)slabs};
-    const cuuint64_t strides[3] = {256, 128, (cuuint64_t)page * 256};
-    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 2, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides,
-              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], one[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        one[i] = 1;
+        if (i + 1 < rank) s[i] = strides[i];
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, s, b, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

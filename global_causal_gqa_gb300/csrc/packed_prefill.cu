@@ -26,7 +26,7 @@
 // Within a sequence the blocks with the most keys come first.
 //
 // Warp roles (12 warps; 96 registers for warps 0-3, 200 for the softmax warps):
-//   warp 0      work claiming and TMA loads: Q of the item, K and V through a 4-slot ring.
+//   warp 0      work claiming and TMA loads: Q of the item, K and V through a 5-slot ring.
 //   warp 1      tensor-memory owner and the single MMA-issuing thread.
 //   warp 2      TMA stores of O.
 //   warp 3      the V guard (below).
@@ -44,8 +44,9 @@
 // the rows that see it.  The softmax warps hand P over only when the guard is done with the
 // tile, so the MMA thread, which has no time to spare, knows nothing of it.
 //
-// Shared memory: Q 64 KB, ring 4 x 32 KB, O staging 2 x 16 KB (one half of the columns of
-// each tile at a time).
+// Shared memory: Q 64 KB, ring 5 x 32 KB.  O leaves through the ring as well: after an item's
+// last V tile its O tiles take a slot each, so that K and V have all five slots inside an
+// item and three while O leaves.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -62,13 +63,21 @@ namespace {
 constexpr int kD = 128;
 constexpr int kBM = 128;
 constexpr int kBN = 128;
-constexpr int kSlots = 4;                     // K/V ring depth
+constexpr int kSlots = 5;                     // ring: K and V tiles, O on its way out
 constexpr int kBoxBytes = 128 * 128;          // 128 rows x 64 bf16 (one 128-byte swizzle span)
 constexpr int kTileBytes = 2 * kBoxBytes;     // 128 rows x 128 bf16
+// Where a key tile's rows lie, as its TMA boxes leave them: 8-row groups and, within a group's
+// reach, the second half of the head dimension.  Packed: one box, all rows of a half, then
+// the other.  Paged: a box per page, {64 dims, 8 rows, 2 halves, page / 8 groups}, so that
+// the groups of successive pages lie at one distance (which a matrix descriptor needs).
+template <bool PAGED>
+struct KeyTile {
+    static constexpr int kGroup = PAGED ? 2048 : 1024, kHalf = PAGED ? 1024 : kBoxBytes;
+    static __device__ __forceinline__ int row(int r) { return (r >> 3) * kGroup + (r & 7) * 128; }
+};
 constexpr int kSmemQ = 0;
 constexpr int kSmemRing = 2 * kTileBytes;
-constexpr int kSmemStage = kSmemRing + kSlots * kTileBytes;
-constexpr int kSmemBar = kSmemStage + 2 * kBoxBytes;
+constexpr int kSmemBar = kSmemRing + kSlots * kTileBytes;
 constexpr int kSmemBytes = kSmemBar + 1024 + 1024;  // + barriers + alignment slack
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
@@ -88,6 +97,8 @@ struct ItemRec {
     int seq;
     int kv_row0;    // packed prompts: row of the sequence's key 0
     int split;      // span of the keys, -1: all of them (the result is final)
+    int ring;       // ring position of its first load; its O tiles take those after the last
+    __device__ int o_slot(int i) const { return (ring + 2 * n_tiles + i) % kSlots; }
 };
 
 struct Slot {
@@ -103,11 +114,14 @@ struct Bars {
     uint64_t item_full[kItemSlots], item_free[kItemSlots];
     uint64_t q_full, q_free;
     uint64_t full[kSlots], empty[kSlots];         // K/V ring
-    uint64_t guard_go[2], guard[2];               // a guarded V tile is on its way / clean (alternate)
+    // A guarded V tile is on its way / clean, in turn: the ring holds three V tiles at most.
+    uint64_t guard_go[4], guard[4];
     uint64_t s_full[2], p_full[2], o_done[2];     // per query tile
-    uint64_t o_final[2];                          // an item's last PV product of the tile
     uint64_t o_free[2];                           // the epilogue has read O out of TMEM
-    uint64_t staged[2], stage_free[2];            // O halves in shared memory
+    // A ring slot is there for O / holds it, [query tile][alternate]: the ring slot of an
+    // item's O is freed before that of the item after next is reached, so neither can be two
+    // phases ahead of its waiter.
+    uint64_t stage_go[2][2], staged[2][2];
     uint64_t mma_done;
     uint32_t tmem_base;
 };
@@ -293,15 +307,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars->guard_go[i], 1);
-            mbar_init(&bars->guard[i], 32);
+            for (int a = 0; a < 4; a += 2) {
+                mbar_init(&bars->guard_go[i + a], 1);
+                mbar_init(&bars->guard[i + a], 32);
+            }
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->p_full[i], 128);
             mbar_init(&bars->o_done[i], 1);
-            mbar_init(&bars->o_final[i], 1);
             mbar_init(&bars->o_free[i], 128);
-            mbar_init(&bars->staged[i], 128);
-            mbar_init(&bars->stage_free[i], 1);
+            for (int a = 0; a < 2; ++a) {
+                mbar_init(&bars->stage_go[i][a], 1);
+                mbar_init(&bars->staged[i][a], 128);
+            }
         }
         mbar_init(&bars->mma_done, 1);
         fence_mbar_init();
@@ -331,6 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int nq = 0;       // items whose Q tiles have been issued
             int claims = 0;   // responses asked for
             int gc = 0;       // guarded V tiles issued
+            int ring_next = 0;   // ring position of the next item to be published
+            int outs[2] = {0, 0};   // ring slots handed to O, per query tile
             Walk walk;
             auto fail = [&](int barrier, int at) {
                 ok = false;
@@ -367,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 it.n_tiles = -1;
             };
+            // O tiles of an item that go through the ring (partials go straight out)
+            auto n_out = [&](const ItemRec &it) { return it.split >= 0 ? 0 : it.ntok > p.Mt ? 2 : 1; };
             auto publish = [&](int k, const ItemRec &it) {
                 Slot &s = bars->slot[k & (kItemSlots - 1)];
                 if (k >= kItemSlots &&
@@ -377,10 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane < 16) s.bad[lane] = 0;
                 if (lane == 0) {
                     s.it = it;
+                    s.it.ring = ring_next;
                     s.any_bad = 0;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->item_full[k & (kItemSlots - 1)]);
+                ring_next += 2 * it.n_tiles + n_out(it);
             };
             auto load_q = [&](int k, const ItemRec &it) {
                 if (k >= 1 && !warp_wait(&bars->q_free, (k - 1) & 1)) {
@@ -398,36 +421,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 nq = k + 1;
             };
-            ItemRec it;
+            // pages of a key tile: lane i holds the tile's i-th one
+            const int npg = PAGED ? kBN / p.page_size : 1;
+            auto walk_pages = [&](const ItemRec &it) {
+                const int hi = it.qpos0 + it.ntok - 1;
+                return PAGED && it.n_tiles > 0
+                           ? PageWalk(p.pages + (long)it.seq * p.max_pages, it.kt_first * npg,
+                                      hi / p.page_size + 1)
+                           : PageWalk(nullptr, 0, 0);
+            };
+            ItemRec it{}, next{};
             settle(blockIdx.x, it);
-            for (int k = 0; ok; ++k) {
-                publish(k, it);
-                if (!ok || it.n_tiles < 0) break;
+            if (ok) publish(0, it);
+            PageWalk pages = walk_pages(it), next_pages = pages;
+            if (ok && it.n_tiles > 0) load_q(0, it);
+            for (int k = 0; ok && it.n_tiles > 0; ++k, it = next, pages = next_pages) {
                 claim();   // one item ahead
                 const Edges e(it, p.window);
-                // pages of a key tile: lane i holds the slab of the tile's i-th page, -1 for
-                // one that no row sees or that is not in the pool (its box is zero fill)
-                const int npg = PAGED ? kBN / p.page_size : 1;
-                auto slab_of = [&](int n0) {
-                    int slab = -1;
-                    if (lane < npg) {
+                int slab = 0;
+                for (int l = 0; l < 2 * it.n_tiles && ok; ++l) {
+                    const int n0 = (it.kt_first + (l >> 1)) * kBN;
+                    if (PAGED && !(l & 1)) {
+                        const int pg = pages.get(n0 / p.page_size, npg);
                         const int key0 = n0 + lane * p.page_size;
-                        if (key0 <= e.hi && key0 + p.page_size > e.lo) {
-                            const int pg = __ldg(p.pages + (long)it.seq * p.max_pages +
-                                                 key0 / p.page_size);
+                        slab = -1;   // no row sees it, or not in the pool: zero fill
+                        if (lane < npg && key0 <= e.hi && key0 + p.page_size > e.lo) {
                             if (pg >= 0 && pg < p.num_pages) slab = pg * p.Hkv + it.g;
                             else set_status(p.status, GQA_ERR_INVALID_ARG);
                         }
                     }
-                    return slab;
-                };
-                int slab = 0, slab_next = 0;
-                if constexpr (PAGED) slab = slab_of(it.kt_first * kBN);
-                if (k == 0) load_q(k, it);
-                for (int l = 0; l < 2 * it.n_tiles && ok; ++l) {
-                    const int n0 = (it.kt_first + (l >> 1)) * kBN;
-                    if constexpr (PAGED)
-                        if (!(l & 1) && l + 2 < 2 * it.n_tiles) slab_next = slab_of(n0 + kBN);
                     const int st = u % kSlots;
                     if (u >= kSlots && !warp_wait(&bars->empty[st], (u / kSlots - 1) & 1)) {
                         fail(1, u);
@@ -438,31 +460,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], kTileBytes);
                     __syncwarp();
                     if constexpr (PAGED) {
-                        if (lane < npg) {
-                            uint8_t *d = dst + lane * p.page_size * 128;
-                            tma_load_3d(d, map, &bars->full[st], 0, 0, slab);
-                            tma_load_3d(d + kBoxBytes, map, &bars->full[st], 64, 0, slab);
-                        }
-                    } else if (lane < 2) {
-                        tma_load_3d(dst + lane * kBoxBytes, map, &bars->full[st], 64 * lane, it.g,
-                                    it.kv_row0 + n0);
+                        if (lane < npg)
+                            tma_load_5d(dst + lane * p.page_size * kD * 2, map, &bars->full[st], 0,
+                                        0, 0, 0, slab);
+                    } else if (lane == 0) {
+                        tma_load_4d(dst, map, &bars->full[st], 0, it.kv_row0 + n0, 0, it.g);
                     }
                     __syncwarp();
                     ++u;
                     if ((l & 1) && e.guarded(n0)) {
-                        if (lane == 0) mbar_arrive(&bars->guard_go[gc & 1]);
+                        if (lane == 0) mbar_arrive(&bars->guard_go[gc & 3]);
                         ++gc;
                     }
-                    if constexpr (PAGED)
-                        if (l & 1) slab = slab_next;
-                    // Q after the item's first K and V: by then the previous item's last
-                    // score products, which still read the buffer, are near
-                    if (l == 1 && k > 0) load_q(k, it);
+                    // Q after the item's first K, whose slot was free earlier: Q's buffer is
+                    // once the previous item's last score products are done
+                    if (l == 0 && k > 0) load_q(k, it);
+                    // the next item, well before its first load
+                    if (l == 1 && ok) {
+                        const int idx = claimed();
+                        if (ok) settle(idx, next);
+                        if (ok) publish(k + 1, next);
+                        if (ok) next_pages = walk_pages(next);
+                    }
                 }
-                if (!ok) break;
-                const int next = claimed();
-                if (!ok) break;
-                settle(next, it);
+                // ring slots for the item's O tiles
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i >= n_out(it) || !ok) break;
+                    const int st = u % kSlots;
+                    if (u >= kSlots && !warp_wait(&bars->empty[st], (u / kSlots - 1) & 1)) {
+                        fail(4, u);
+                        break;
+                    }
+                    // no load: the phase completes with this arrival alone
+                    if (lane == 0) {
+                        mbar_arrive(&bars->full[st]);
+                        mbar_arrive(&bars->stage_go[i][outs[i] & 1]);
+                    }
+                    __syncwarp();
+                    ++outs[i];
+                    ++u;
+                }
             }
             if (!ok) {
                 // never leave the CTA with copies in flight
@@ -496,23 +534,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++u;
                     tc_fence_after();
                 };
+                // Descriptors differ in their address field alone (16-byte units, low word).
+                using T = KeyTile<PAGED>;
+                const uint64_t qd0 = sdesc_sw128(q0, 16, 1024);
+                const uint64_t kd0 = sdesc_sw128(ring0, 16, T::kGroup);
+                const uint64_t vd0 = sdesc_sw128(ring0, T::kHalf, T::kGroup);
                 auto issue_s = [&](int i, int st) {
-                    const uint32_t ka = ring0 + st * kTileBytes, qa = q0 + i * kTileBytes;
+                    const uint64_t qd = qd0 + i * (kTileBytes >> 4), kd = kd0 + st * (kTileBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
-                        umma_ss(tmem + i * 128, sdesc_sw128(qa + off, 16, 1024),
-                                sdesc_sw128(ka + off, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
-                    }
+                    for (int kk = 0; kk < kD / 16; ++kk)
+                        umma_ss(tmem + i * 128, qd + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4),
+                                kd + (((kk >> 2) * T::kHalf + (kk & 3) * 32) >> 4), idesc_s,
+                                kk > 0 ? 1u : 0u);
                     umma_commit(&bars->s_full[i]);
                 };
                 auto issue_pv = [&](int i, int st, bool acc) {
-                    const uint32_t va = ring0 + st * kTileBytes;
+                    const uint64_t vd = vd0 + st * (kTileBytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk)
                         umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8,
-                                sdesc_sw128(va + kk * 16 * 128, kBoxBytes, 1024), idesc_o,
-                                (acc || kk > 0) ? 1u : 0u);
+                                vd + ((kk * 2 * T::kGroup) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
                     umma_commit(&bars->o_done[i]);
                 };
                 for (int k = 0;; ++k) {
@@ -525,65 +566,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bars->item_free[k & (kItemSlots - 1)]);
                     const bool two = it.ntok > p.Mt;
                     const int n = it.n_tiles;
-                    int kst = 0, vst = 0;
+                    u = it.ring;
+                    int kst = 0, vst = 0, kprev = 0;
                     if (!mbar_wait(&bars->q_full, k & 1)) {
                         fail(0, k);
                         break;
                     }
-                    take(kst);
-                    // S_i(0) overwrites the columns the previous item's last P_i sits in
-                    if (ok && cpv[0] > 0 && !mbar_wait(&bars->o_done[0], (cpv[0] - 1) & 1))
-                        fail(2, cpv[0]);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_s(0, kst);
-                    if (two) {
-                        if (cpv[1] > 0 && !mbar_wait(&bars->o_done[1], (cpv[1] - 1) & 1)) {
-                            fail(2, cpv[1]);
-                            break;
-                        }
-                        tc_fence_after();
-                        issue_s(1, kst);
-                    }
-                    if (n == 1) umma_commit(&bars->q_free);
-                    umma_commit(&bars->empty[kst]);
-                    int kprev = kst;   // K slot of the last score products issued
-                    // one query tile's turn at key tile j (the index is a constant, so the
-                    // counters stay in registers)
+                    // one query tile's turn: PV_i(j), then S_i(j + 1); j = -1 is the item's
+                    // start.  (The index is a constant, so the counters stay in registers;
+                    // every product is issued from one place, so that an item's first and
+                    // last tiles run code that is at hand.)
                     auto turn = [&](auto I, int j) {
                         constexpr int i = decltype(I)::value;
-                        if (!mbar_wait(&bars->p_full[i], cpv[i] & 1)) return fail(3, cpv[i]);
-                        // the first PV of an item overwrites O_i: the previous item's
-                        // epilogue must have read it out
-                        if (j == 0 && nepi[i] > 0 &&
-                            !mbar_wait(&bars->o_free[i], (nepi[i] - 1) & 1))
-                            return fail(4, nepi[i]);
-                        tc_fence_after();
-                        issue_pv(i, vst, j > 0);
-                        ++cpv[i];
+                        const bool last = i == 1 || !two;   // of the key tile's turns
+                        if (j >= 0) {
+                            if (!mbar_wait(&bars->p_full[i], cpv[i] & 1)) return fail(3, cpv[i]);
+                            // the first PV of an item overwrites O_i: the previous item's
+                            // epilogue must have read it out
+                            if (j == 0 && nepi[i] > 0 &&
+                                !mbar_wait(&bars->o_free[i], (nepi[i] - 1) & 1))
+                                return fail(4, nepi[i]);
+                            tc_fence_after();
+                            issue_pv(i, vst, j > 0);
+                            ++cpv[i];
+                        }
                         if (j + 1 < n) {
                             if (i == 0) take(kst);
                             if (!ok) return;
-                            // S_i(j+1) overwrites the columns P_i(j) sits in
-                            if (!mbar_wait(&bars->o_done[i], (cpv[i] - 1) & 1)) return fail(5, cpv[i]);
+                            // S_i(j+1) overwrites the columns P_i(j) sits in (of the previous
+                            // item, its last P_i)
+                            if (cpv[i] > 0 && !mbar_wait(&bars->o_done[i], (cpv[i] - 1) & 1))
+                                return fail(5, cpv[i]);
                             tc_fence_after();
                             // PV_i(j) has completed, and with it every earlier product:
                             // K(j) is free once PV_0(j) is, V(j) once the last tile's is
-                            if (i == 0 && j > 0) mbar_arrive(&bars->empty[kprev]);
-                            if (i == 1 || !two) mbar_arrive(&bars->empty[vst]);
+                            if (i == 0 && j >= 0) mbar_arrive(&bars->empty[kprev]);
+                            if (last && j >= 0) mbar_arrive(&bars->empty[vst]);
                             issue_s(i, kst);
-                            if (j + 2 == n && (i == 1 || !two)) umma_commit(&bars->q_free);
-                        } else {
-                            umma_commit(&bars->o_final[i]);
-                            // the item's last key tile: K and V go free when its products do
-                            if (i == 0 && j > 0) umma_commit(&bars->empty[kprev]);
-                            if (i == 1 || !two) umma_commit(&bars->empty[vst]);
+                            if (last && j + 2 == n) {
+                                // the item's last score products: Q and this K go free when
+                                // they are done
+                                umma_commit(&bars->q_free);
+                                umma_commit(&bars->empty[kst]);
+                            }
+                        } else if (last) {
+                            umma_commit(&bars->empty[vst]);
                         }
                     };
-                    for (int j = 0; j < n && ok; ++j) {
-                        take(vst);
-                        if (!ok) break;
-                        turn(std::integral_constant<int, 0>{}, j);
+                    for (int j = -1; j < n && ok; ++j) {
+                        if (j >= 0) take(vst);
+                        if (ok) turn(std::integral_constant<int, 0>{}, j);
                         if (two && ok) turn(std::integral_constant<int, 1>{}, j);
                         kprev = kst;
                     }
@@ -599,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp == 2) {
             // ================= O stores =================
-            int done[2] = {0, 0};   // halves stored, per tile
+            int done[2] = {0, 0};   // O tiles stored, per query tile
             for (int k = 0;; ++k) {
                 ItemRec it;
                 const bool got = read_item(bars, k, it);
@@ -610,21 +642,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (it.n_tiles < 0) break;
                 if (lane == 0) mbar_arrive(&bars->item_free[k & (kItemSlots - 1)]);
-                // whole tiles only: the epilogue stores ragged ones and partials itself
-                int left[2];
-                left[0] = it.split < 0 && it.ntok >= p.Mt ? 2 : 0;
-                left[1] = it.split < 0 && it.ntok >= 2 * p.Mt ? 2 : 0;
+                int left[2];   // partials are stored by the epilogue itself
+                left[0] = it.split < 0 ? 1 : 0;
+                left[1] = it.split < 0 && it.ntok > p.Mt ? 1 : 0;
                 if (lane == 0) {
                     const uint64_t t0 = globaltimer_ns();
                     while (left[0] + left[1] > 0) {
                         for (int i = 0; i < 2; ++i) {
-                            if (left[i] == 0 || !mbar_try_wait(&bars->staged[i], done[i] & 1))
+                            if (left[i] == 0 ||
+                                !mbar_try_wait(&bars->staged[i][done[i] & 1], (done[i] >> 1) & 1))
                                 continue;
-                            tma_store_3d(&tmO, smem + kSmemStage + i * kBoxBytes,
-                                         64 * (2 - left[i]), it.g * p.G, it.row0 + i * p.Mt);
-                            bulk_commit_group();
-                            bulk_wait_read_all();
-                            mbar_arrive(&bars->stage_free[i]);
+                            // (a ragged tile has been stored row by row by the epilogue)
+                            const int st = it.o_slot(i);
+                            if (it.ntok >= (i + 1) * p.Mt) {
+                                for (int h = 0; h < 2; ++h)
+                                    tma_store_3d(&tmO, smem + kSmemRing + st * kTileBytes + h * kBoxBytes,
+                                                 64 * h, it.g * p.G, it.row0 + i * p.Mt);
+                                bulk_commit_group();
+                                bulk_wait_read_all();
+                            }
+                            mbar_arrive(&bars->empty[st]);
                             ++done[i];
                             --left[i];
                         }
@@ -643,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else {
             // ================= V guard =================
-            int u = 0, gc = 0;
+            int gc = 0;
             for (int k = 0;; ++k) {
                 ItemRec it;
                 const bool got = read_item(bars, k, it);
@@ -662,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // The producer has armed the slot for this tile, and its phase cannot
                     // move on before the guard is done (waiting on the slot alone could take
                     // an older phase of the same parity for this one).
-                    const int uu = u + 2 * j + 1, st = uu % kSlots;
-                    if (!warp_wait(&bars->guard_go[gc & 1], (gc >> 1) & 1) ||
+                    const int uu = it.ring + 2 * j + 1, st = uu % kSlots;
+                    if (!warp_wait(&bars->guard_go[gc & 3], (gc >> 2) & 1) ||
                         !warp_wait(&bars->full[st], (uu / kSlots) & 1)) {
                         set_timeout(p.status, kDiagPacked, kRoleAux, 1, gc);
                         ok = false;
@@ -674,7 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // row, or past the diagonal for some row.  A lane holds one 16-byte piece
                     // of a row, two rows to a load (which piece is which does not matter).
                     const int pc = lane & 15;
-                    uint8_t *col = tile + (pc >> 3) * kBoxBytes + (pc & 7) * 16;
+                    using V = KeyTile<PAGED>;
+                    uint8_t *col = tile + (pc >> 3) * V::kHalf + (pc & 7) * 16;
                     // 0 * x stays 0 unless x is infinite or NaN: one packed multiply-add per
                     // two elements, since this warp's instructions come off those of the
                     // softmax warps beside it
@@ -686,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 8; ++i) {
                                 x[i] = make_uint4(0, 0, 0, 0);
                                 if (r0 + 2 * i < b)
-                                    x[i] = *reinterpret_cast<const uint4 *>(col + (r0 + 2 * i) * 128);
+                                    x[i] = *reinterpret_cast<const uint4 *>(col + V::row(r0 + 2 * i));
                             }
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
@@ -701,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bool touched = false;
                     auto strip = [&](int a, int b) {
                         for (int r = a + (lane >> 4); r < b; r += 2) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(col + r * 128);
+                            const uint4 x = *reinterpret_cast<const uint4 *>(col + V::row(r));
                             if (!(nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) ||
                                   nonfinite2(x.w)))
                                 continue;
@@ -711,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if ((w[q] & 0x7f80u) == 0x7f80u) w[q] &= 0xffff0000u;
                                 if ((w[q] & 0x7f800000u) == 0x7f800000u) w[q] &= 0xffffu;
                             }
-                            *reinterpret_cast<uint4 *>(col + r * 128) =
+                            *reinterpret_cast<uint4 *>(col + V::row(r)) =
                                 make_uint4(w[0], w[1], w[2], w[3]);
                             touched = true;
                             const int key = n0 + r;
@@ -726,10 +764,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!clean(0, below)) strip(0, below);
                     if (!clean(above, kBN)) strip(above, kBN);
                     if (touched) fence_proxy_async_smem();
-                    mbar_arrive(&bars->guard[gc & 1]);
+                    mbar_arrive(&bars->guard[gc & 3]);
                     ++gc;
                 }
-                u += 2 * it.n_tiles;
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->item_free[k & (kItemSlots - 1)]);
@@ -744,11 +781,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + wg * 128;
         const uint32_t tO = tmem + lane_off + 256 + wg * 128;
-        uint8_t *stage = smem + kSmemStage + wg * kBoxBytes;
         int cs = 0;    // score tiles consumed (all items)
         int pvb = 0;   // PV products of the previous items
-        int ne = 0;    // items finished
-        int ns = 0;    // halves handed to the store warp
+        int ns = 0;    // O tiles handed to the store warp
         int gc = 0;    // guarded V tiles (all items)
         bool ok = true;
         auto fail = [&](int barrier, int at) {
@@ -797,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool guarded = n0 < g_lo || n0 > g_hi;
                 auto hand_over = [&]() {
                     if (guarded) {
-                        if (!warp_wait(&bars->guard[gc & 1], (gc >> 1) & 1)) fail(5, gc);
+                        if (!warp_wait(&bars->guard[gc & 3], (gc >> 2) & 1)) fail(5, gc);
                         ++gc;
                     }
                     mbar_arrive(&bars->p_full[wg]);
@@ -924,11 +959,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             pvb += n_tiles;
             // ---- epilogue: O out of TMEM first (frees it for the next item)
-            if (!warp_wait(&bars->o_final[wg], ne & 1)) {
-                fail(2, ne);
+            if (!warp_wait(&bars->o_done[wg], (pvb - 1) & 1)) {
+                fail(2, pvb);
                 break;
             }
-            ++ne;
             tc_fence_after();
             float x[128];
 #pragma unroll
@@ -977,40 +1011,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 const float inv_l = l > 0.f || l != l ? 1.0f / l : 0.f;
                 const bool whole = ntok >= p.Mt;   // the tile's tokens are all there
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // the staging half's last store has read it
-                    if (ns > 0 && !warp_wait(&bars->stage_free[wg], (ns - 1) & 1)) {
-                        fail(3, ns);
-                        break;
-                    }
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float *y = x + 64 * h + 8 * c;
-                        *reinterpret_cast<uint4 *>(stage + r * 128 +
-                                                   ((whole ? c ^ (r & 7) : c) << 4)) =
-                            make_uint4(pack_bf16x2(y[0] * inv_l, y[1] * inv_l),
-                                       pack_bf16x2(y[2] * inv_l, y[3] * inv_l),
-                                       pack_bf16x2(y[4] * inv_l, y[5] * inv_l),
-                                       pack_bf16x2(y[6] * inv_l, y[7] * inv_l));
-                    }
-                    if (valid && slot.any_bad)
-                        marked([&](const __nv_bfloat16 *v) {
-                            add_marked(stage, r, whole, v + 64 * h);
-                        });
-                    fence_proxy_async_smem();
-                    if (whole) {
-                        mbar_arrive(&bars->staged[wg]);
-                        ++ns;
-                    } else if (valid) {
-                        // a ragged tile: each row's 128 bytes by themselves
-                        bulk_store(p.o + (size_t)row * p.o_stride + head * kD + 64 * h,
-                                   stage + r * 128, 128);
-                        bulk_commit_group();
-                        bulk_wait_read_all();
-                    }
+                // through a ring slot, as two halves of the columns like a Q tile
+                if (!warp_wait(&bars->stage_go[wg][ns & 1], (ns >> 1) & 1)) {
+                    fail(3, ns);
+                    break;
                 }
-                if (!ok) break;
+                uint8_t *stage = smem + kSmemRing + it.o_slot(wg) * kTileBytes;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float *y = x + 8 * c;
+                    *reinterpret_cast<uint4 *>(stage + (c >> 3) * kBoxBytes + r * 128 +
+                                               ((whole ? (c & 7) ^ (r & 7) : c & 7) << 4)) =
+                        make_uint4(pack_bf16x2(y[0] * inv_l, y[1] * inv_l),
+                                   pack_bf16x2(y[2] * inv_l, y[3] * inv_l),
+                                   pack_bf16x2(y[4] * inv_l, y[5] * inv_l),
+                                   pack_bf16x2(y[6] * inv_l, y[7] * inv_l));
+                }
+                if (valid && slot.any_bad)
+                    marked([&](const __nv_bfloat16 *v) {
+                        for (int h = 0; h < 2; ++h)
+                            add_marked(stage + h * kBoxBytes, r, whole, v + 64 * h);
+                    });
+                fence_proxy_async_smem();
+                if (!whole && valid) {
+                    // a ragged tile: each row's halves by themselves
+                    __nv_bfloat16 *dst = p.o + (size_t)row * p.o_stride + head * kD;
+                    for (int h = 0; h < 2; ++h)
+                        bulk_store(dst + 64 * h, stage + h * kBoxBytes + r * 128, 128);
+                    bulk_commit_group();
+                    bulk_wait_read_all();
+                }
+                mbar_arrive(&bars->staged[wg][ns & 1]);
+                ++ns;
                 if (valid && p.lse)
                     p.lse[(size_t)head * p.bounds.total + row] =
                         (m + __log2f(l)) * 0.69314718055994531f;
@@ -1115,9 +1147,15 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
     const int ntok = 2 * p.Mt;
     int spans = 1;
     CUtensorMap mq, mk, mv, mo;
-    if (!make_rows_map(&mq, a.q, a.Hq, kD, a.total, a.q_stride, p.G, p.Mt) ||
-        !make_rows_map(&mo, a.o, a.Hq, kD, a.total, a.o_stride, p.G, p.Mt))
-        return GQA_ERR_CUDA;
+    {
+        // {128 dims, query heads, tokens}: half the dims of G heads of Mt tokens per box
+        const uint64_t dims[3] = {kD, (uint64_t)a.Hq, (uint64_t)a.total};
+        const uint64_t qs[2] = {kD * 2, (uint64_t)a.q_stride * 2};
+        const uint64_t os[2] = {kD * 2, (uint64_t)a.o_stride * 2};
+        const uint32_t box[3] = {64, (uint32_t)p.G, (uint32_t)p.Mt};
+        if (!make_bf16_map(&mq, a.q, 3, dims, qs, box) || !make_bf16_map(&mo, a.o, 3, dims, os, box))
+            return GQA_ERR_CUDA;
+    }
     if (paged) {
         const gqa_paged_kv &c = *a.cache;
         p.kv_lens = c.kv_lens;
@@ -1134,13 +1172,22 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
             p.ws_o = static_cast<float *>(ws);
             p.ws_ml = p.ws_o + (size_t)spans * a.total * a.Hq * kD;
         }
-        const long slabs = (long)c.num_pages * c.Hkv, page = c.page_size;
-        if (!make_rows_map(&mk, c.k, page, kD, slabs, page * kD, c.page_size, 1) ||
-            !make_rows_map(&mv, c.v, page, kD, slabs, page * kD, c.page_size, 1))
+        // {64 dims, 8 rows, 2 halves, groups of 8 rows, (page, KV head)}, a page per box
+        const uint64_t page = c.page_size;
+        const uint64_t dims[5] = {64, 8, 2, page / 8, (uint64_t)c.num_pages * c.Hkv};
+        const uint64_t strides[4] = {256, 128, 2048, page * 256};
+        const uint32_t box[5] = {64, 8, 2, (uint32_t)(page / 8), 1};
+        if (!make_bf16_map(&mk, c.k, 5, dims, strides, box) ||
+            !make_bf16_map(&mv, c.v, 5, dims, strides, box))
             return GQA_ERR_CUDA;
-    } else if (!make_rows_map(&mk, a.k, a.Hkv, kD, a.total, a.k_stride, 1, kBN) ||
-               !make_rows_map(&mv, a.v, a.Hkv, kD, a.total, a.v_stride, 1, kBN)) {
-        return GQA_ERR_CUDA;
+    } else {
+        // {64 dims, rows, 2 halves, KV heads}, 128 rows per box
+        const uint64_t dims[4] = {64, (uint64_t)a.total, 2, (uint64_t)a.Hkv};
+        const uint64_t ks[3] = {(uint64_t)a.k_stride * 2, 128, 256};
+        const uint64_t vs[3] = {(uint64_t)a.v_stride * 2, 128, 256};
+        const uint32_t box[4] = {64, kBN, 2, 1};
+        if (!make_bf16_map(&mk, a.k, 4, dims, ks, box) || !make_bf16_map(&mv, a.v, 4, dims, vs, box))
+            return GQA_ERR_CUDA;
     }
     auto kern = paged ? packed_prefill_kernel<true> : packed_prefill_kernel<false>;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes) != cudaSuccess)

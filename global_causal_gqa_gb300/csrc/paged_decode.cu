@@ -272,24 +272,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             const int lo = p.window > 0 ? max(0, sg.S - sg.T - p.window + 1) : 0;
-            // the slab of this lane's box of a stage; -1 for one that no row sees or that is
-            // not in the pool (its box is zero fill).  The next stage's entries are fetched
-            // one stage ahead.
-            auto slab_of = [&](int unit) {
-                int slab = -1;
-                if (lane < boxes) {
-                    const int key0 = unit * kUnit + lane * box;
-                    if (key0 < sg.S && key0 + box > lo) {
-                        const int pg = __ldg(p.pages + (long)sg.seq * p.max_pages + key0 / p.page_size);
-                        if (pg >= 0 && pg < p.num_pages) slab = pg * p.Hkv + sg.g;
-                        else set_status(p.status, GQA_ERR_INVALID_ARG);
-                    }
-                }
-                return slab;
-            };
-            int slab = slab_of(sg.unit0);
+            PageWalk pages(p.pages + (long)sg.seq * p.max_pages, sg.unit0 * kUnit / p.page_size,
+                           (sg.S - 1) / p.page_size + 1);
             for (int j = 0; j < sg.stages; ++j, ++u) {
-                const int next = j + 1 < sg.stages ? slab_of(sg.unit0 + j + 1) : -1;
+                // the slab of this lane's box; -1 for one that no row sees or that is not in
+                // the pool (its box is zero fill)
+                const int unit_key = (sg.unit0 + j) * kUnit;
+                const int pg = pages.get(unit_key / p.page_size, boxes);
+                const int key0 = unit_key + lane * box;
+                int slab = -1;
+                if (lane < boxes && key0 < sg.S && key0 + box > lo) {
+                    if (pg >= 0 && pg < p.num_pages) slab = pg * p.Hkv + sg.g;
+                    else set_status(p.status, GQA_ERR_INVALID_ARG);
+                }
                 const int st = u % kStages;
                 if (u >= kStages && !warp_wait(&bars->empty[st], (u / kStages - 1) & 1)) {
                     set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 1, u);
@@ -300,12 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane < boxes) {
                     uint8_t *dst = smem + st * kStageBytes + lane * box * kD * 2;
-                    const int row = p.page_size > kUnit ? ((sg.unit0 + j) * kUnit) % p.page_size : 0;
+                    const int row = p.page_size > kUnit ? unit_key % p.page_size : 0;
                     tma_load_4d(dst, &tmK, &bars->full[st], 0, row, 0, slab);
                     tma_load_4d(dst + kTileBytes, &tmV, &bars->full[st], 0, row, 0, slab);
                 }
                 __syncwarp();
-                slab = next;
             }
             if (!ok) break;
         }
@@ -724,10 +718,14 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
         p.ws_ml = p.ws_o + rec * kD;
         p.ws_joint = reinterpret_cast<Joint *>(p.ws_ml + rec * 2);
     }
-    const long slabs = (long)c.num_pages * c.Hkv, page = c.page_size;
-    const int box = c.page_size < kUnit ? c.page_size : kUnit;
+    // {64 dims, rows, 2 halves, (page, KV head)}: a page, or 64 rows of it, per box
+    const uint64_t page = c.page_size;
+    const uint64_t dims[4] = {64, page, 2, (uint64_t)c.num_pages * c.Hkv};
+    const uint64_t strides[3] = {256, 128, page * 256};
+    const uint32_t box[4] = {64, (uint32_t)(page < kUnit ? page : kUnit), 2, 1};
     CUtensorMap mk, mv;
-    if (!make_page_map(&mk, c.k, page, slabs, box) || !make_page_map(&mv, c.v, page, slabs, box))
+    if (!make_bf16_map(&mk, c.k, 4, dims, strides, box) ||
+        !make_bf16_map(&mv, c.v, 4, dims, strides, box))
         return GQA_ERR_CUDA;
     const long pairs = (long)a.nseq * a.Hkv;
     const long grid = p.whole && pairs < kSMs ? pairs : kSMs;
