@@ -158,9 +158,18 @@ __host__ __device__ __forceinline__ int n_spans(int tiles, int split_tiles) {
     return split_tiles > 0 ? (tiles + split_tiles - 1) / split_tiles : 1;
 }
 
+// Waits with their polling loop and their error record out of line: a dozen roles wait at
+// some thirty places, and inlined the loops and records were most of the kernel's code, which
+// then no longer stayed in the instruction cache between an item's parts.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
+    return mbar_wait(bar, parity);
+}
+__device__ __noinline__ void expired(int *status, int role, int barrier, int at) {
+    set_timeout(status, kDiagPacked, role, barrier, at);
+}
 // A bounded wait whose outcome every lane of the warp agrees on.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    return __all_sync(0xffffffffu, wait(bar, parity));
 }
 
 enum Role { kRoleProducer = 0, kRoleMma = 1, kRoleSoftmax = 2, kRoleAux = 3 };
@@ -173,7 +182,7 @@ struct Walk {
     int count = 0, incl = 0;    // its items, and the inclusive sum over the lanes
 };
 
-__device__ __forceinline__ void walk_to(const Params &p, Walk &w, int base) {
+__device__ __noinline__ void walk_to(const Params &p, Walk &w, int base) {
     const int lane = threadIdx.x & 31;
     w.before += w.here;
     w.base = base;
@@ -198,7 +207,7 @@ __device__ __forceinline__ void walk_to(const Params &p, Walk &w, int base) {
 
 // Item `idx` (not below the last one asked for): 1 and the item, 0 if that number has no
 // work (a span past the block's keys), -1 past the last item.  Warp-collective.
-__device__ int find_item(const Params &p, Walk &w, int idx, ItemRec &it) {
+__device__ __noinline__ int find_item(const Params &p, Walk &w, int idx, ItemRec &it) {
     while (w.base < 0 || idx >= w.before + w.here) {
         if (w.base + 32 >= p.nseq) return -1;
         walk_to(p, w, w.base + 32);
@@ -234,7 +243,7 @@ __device__ int find_item(const Params &p, Walk &w, int idx, ItemRec &it) {
 
 // Item k as a reader role sees it (false: the wait expired).
 __device__ __forceinline__ bool read_item(Bars *bars, int k, ItemRec &it) {
-    if (!mbar_wait(&bars->item_full[k & (kItemSlots - 1)], (k / kItemSlots) & 1)) return false;
+    if (!wait(&bars->item_full[k & (kItemSlots - 1)], (k / kItemSlots) & 1)) return false;
     it = bars->slot[k & (kItemSlots - 1)].it;
     return true;
 }
@@ -353,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Walk walk;
             auto fail = [&](int barrier, int at) {
                 ok = false;
-                set_timeout(p.status, kDiagPacked, kRoleProducer, barrier, at);
+                expired(p.status, kRoleProducer, barrier, at);
             };
             auto claim = [&]() {
                 if (lane == 0) {
@@ -505,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) {
                 // never leave the CTA with copies in flight
                 for (int w = max(0, u - kSlots); w < u; ++w)
-                    mbar_wait(&bars->full[w % kSlots], (w / kSlots) & 1);
-                if (nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1);
-                if (claims > 0) mbar_wait(&bars->clc_full, (claims - 1) & 1);
+                    wait(&bars->full[w % kSlots], (w / kSlots) & 1);
+                if (nq > 0) wait(&bars->q_full, (nq - 1) & 1);
+                if (claims > 0) wait(&bars->clc_full, (claims - 1) & 1);
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -519,15 +528,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t q0 = smem_u32(smem + kSmemQ);
                 bool ok = true;
                 int u = 0;                 // ring slots consumed
-                int cpv[2] = {0, 0};       // PV products issued, per query tile (all items)
-                int nepi[2] = {0, 0};      // items finished, per query tile
                 auto fail = [&](int barrier, int at) {
                     ok = false;
-                    set_timeout(p.status, kDiagPacked, kRoleMma, barrier, at);
+                    expired(p.status, kRoleMma, barrier, at);
                 };
                 auto take = [&](int &st) {
                     st = u % kSlots;
-                    if (!mbar_wait(&bars->full[st], (u / kSlots) & 1)) {
+                    if (!wait(&bars->full[st], (u / kSlots) & 1)) {
                         fail(1, u);
                         return;
                     }
@@ -556,6 +563,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 vd + ((kk * 2 * T::kGroup) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
                     umma_commit(&bars->o_done[i]);
                 };
+                // an item's last score products: Q and their K go free when they are done
+                auto s_done = [&](int st) {
+                    umma_commit(&bars->q_free);
+                    umma_commit(&bars->empty[st]);
+                };
+                int cpv[2] = {0, 0};       // PV products issued, per query tile (all items)
+                int nepi[2] = {0, 0};      // items finished, per query tile
                 for (int k = 0;; ++k) {
                     ItemRec it;
                     if (!read_item(bars, k, it)) {
@@ -568,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int n = it.n_tiles;
                     u = it.ring;
                     int kst = 0, vst = 0, kprev = 0;
-                    if (!mbar_wait(&bars->q_full, k & 1)) {
+                    if (!wait(&bars->q_full, k & 1)) {
                         fail(0, k);
                         break;
                     }
@@ -580,11 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         constexpr int i = decltype(I)::value;
                         const bool last = i == 1 || !two;   // of the key tile's turns
                         if (j >= 0) {
-                            if (!mbar_wait(&bars->p_full[i], cpv[i] & 1)) return fail(3, cpv[i]);
+                            if (!wait(&bars->p_full[i], cpv[i] & 1)) return fail(3, cpv[i]);
                             // the first PV of an item overwrites O_i: the previous item's
                             // epilogue must have read it out
                             if (j == 0 && nepi[i] > 0 &&
-                                !mbar_wait(&bars->o_free[i], (nepi[i] - 1) & 1))
+                                !wait(&bars->o_free[i], (nepi[i] - 1) & 1))
                                 return fail(4, nepi[i]);
                             tc_fence_after();
                             issue_pv(i, vst, j > 0);
@@ -595,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!ok) return;
                             // S_i(j+1) overwrites the columns P_i(j) sits in (of the previous
                             // item, its last P_i)
-                            if (cpv[i] > 0 && !mbar_wait(&bars->o_done[i], (cpv[i] - 1) & 1))
+                            if (cpv[i] > 0 && !wait(&bars->o_done[i], (cpv[i] - 1) & 1))
                                 return fail(5, cpv[i]);
                             tc_fence_after();
                             // PV_i(j) has completed, and with it every earlier product:
@@ -603,12 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (i == 0 && j >= 0) mbar_arrive(&bars->empty[kprev]);
                             if (last && j >= 0) mbar_arrive(&bars->empty[vst]);
                             issue_s(i, kst);
-                            if (last && j + 2 == n) {
-                                // the item's last score products: Q and this K go free when
-                                // they are done
-                                umma_commit(&bars->q_free);
-                                umma_commit(&bars->empty[kst]);
-                            }
+                            if (last && j + 2 == n) s_done(kst);
                         } else if (last) {
                             umma_commit(&bars->empty[vst]);
                         }
@@ -626,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) set_status(p.status, GQA_ERR_DEVICE_TIMEOUT);
                 // every tcgen05 operation issued above completes before TMEM is released
                 umma_commit(&bars->mma_done);
-                mbar_wait(&bars->mma_done, 0);
+                wait(&bars->mma_done, 0);
             }
             __syncwarp();
         } else if (warp == 2) {
@@ -636,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ItemRec it;
                 const bool got = read_item(bars, k, it);
                 if (!__all_sync(0xffffffffu, got)) {
-                    set_timeout(p.status, kDiagPacked, kRoleAux, 6, k);
+                    expired(p.status, kRoleAux, 6, k);
                     break;
                 }
                 __syncwarp();
@@ -668,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // a whole item may pass before its epilogue: the limit is generous,
                         // but it is one
                         if (globaltimer_ns() - t0 > 2 * GQA_WAIT_LIMIT_NS) {
-                            set_timeout(p.status, kDiagPacked, kRoleAux, 0, k);
+                            expired(p.status, kRoleAux, 0, k);
                             break;
                         }
                     }
@@ -685,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ItemRec it;
                 const bool got = read_item(bars, k, it);
                 if (!__all_sync(0xffffffffu, got)) {
-                    set_timeout(p.status, kDiagPacked, kRoleAux, 5, k);
+                    expired(p.status, kRoleAux, 5, k);
                     break;
                 }
                 __syncwarp();
@@ -702,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int uu = it.ring + 2 * j + 1, st = uu % kSlots;
                     if (!warp_wait(&bars->guard_go[gc & 3], (gc >> 2) & 1) ||
                         !warp_wait(&bars->full[st], (uu / kSlots) & 1)) {
-                        set_timeout(p.status, kDiagPacked, kRoleAux, 1, gc);
+                        expired(p.status, kRoleAux, 1, gc);
                         ok = false;
                         break;
                     }
@@ -788,10 +797,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         auto fail = [&](int barrier, int at) {
             ok = false;
-            set_timeout(p.status, kDiagPacked, kRoleSoftmax, barrier, at);
+            expired(p.status, kRoleSoftmax, barrier, at);
         };
         for (int k = 0; ok; ++k) {
             int n_tiles, n0, qpos, ntok;
+            bool span;
             int g_lo, g_hi;   // V tiles that begin below g_lo or above g_hi are guarded
             {
                 ItemRec it;
@@ -804,6 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n_tiles < 0) break;
                 ntok = it.ntok - wg * p.Mt;    // tokens of this tile
                 n0 = it.kt_first * kBN;
+                span = it.split >= 0;
                 // rows behind the last token compute what the last token's would
                 qpos = it.qpos0 + wg * p.Mt + min(rtok, min(ntok, p.Mt) - 1);
                 const Edges e(it, p.window);
@@ -959,8 +970,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             pvb += n_tiles;
             // ---- epilogue: O out of TMEM first (frees it for the next item)
+            // (and, unless the item is a span, the ring slot that it leaves through)
             if (!warp_wait(&bars->o_done[wg], (pvb - 1) & 1)) {
                 fail(2, pvb);
+                break;
+            }
+            if (!span && !warp_wait(&bars->stage_go[wg][ns & 1], (ns >> 1) & 1)) {
+                fail(3, ns);
                 break;
             }
             tc_fence_after();
@@ -1012,10 +1028,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float inv_l = l > 0.f || l != l ? 1.0f / l : 0.f;
                 const bool whole = ntok >= p.Mt;   // the tile's tokens are all there
                 // through a ring slot, as two halves of the columns like a Q tile
-                if (!warp_wait(&bars->stage_go[wg][ns & 1], (ns >> 1) & 1)) {
-                    fail(3, ns);
-                    break;
-                }
                 uint8_t *stage = smem + kSmemRing + it.o_slot(wg) * kTileBytes;
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
