@@ -182,7 +182,7 @@ struct Walk {
     int count = 0, incl = 0;    // its items, and the inclusive sum over the lanes
 };
 
-__device__ __noinline__ void walk_to(const Params &p, Walk &w, int base) {
+__device__ __forceinline__ void walk_to(const Params &p, Walk &w, int base) {
     const int lane = threadIdx.x & 31;
     w.before += w.here;
     w.base = base;
@@ -207,7 +207,7 @@ __device__ __noinline__ void walk_to(const Params &p, Walk &w, int base) {
 
 // Item `idx` (not below the last one asked for): 1 and the item, 0 if that number has no
 // work (a span past the block's keys), -1 past the last item.  Warp-collective.
-__device__ __noinline__ int find_item(const Params &p, Walk &w, int idx, ItemRec &it) {
+__device__ __forceinline__ int find_item(const Params &p, Walk &w, int idx, ItemRec &it) {
     while (w.base < 0 || idx >= w.before + w.here) {
         if (w.base + 32 >= p.nseq) return -1;
         walk_to(p, w, w.base + 32);
@@ -265,19 +265,6 @@ __device__ __forceinline__ bool nonfinite2(uint32_t w) {   // of the two bf16 in
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// Adds the non-finite ones of 64 value elements to a row's staged half (bf16), row r at
-// `stage` + 128 r, 16-byte chunks swizzled or not.
-__device__ __noinline__ void add_marked(uint8_t *stage, int r, bool swizzled,
-                                        const __nv_bfloat16 *v) {
-    for (int c = 0; c < 64; ++c) {
-        const float x = __bfloat162float(v[c]);
-        if (isfinite(x)) continue;
-        const int chunk = swizzled ? (c >> 3) ^ (r & 7) : c >> 3;
-        __nv_bfloat16 *e = reinterpret_cast<__nv_bfloat16 *>(stage + r * 128 + chunk * 16) + (c & 7);
-        *e = __float2bfloat16_rn(__bfloat162float(*e) + x);
-    }
-}
-
 template <bool PAGED>
 __device__ __forceinline__ const __nv_bfloat16 *value_row(const Params &p, const ItemRec &it,
                                                           int key) {
@@ -287,6 +274,31 @@ __device__ __forceinline__ const __nv_bfloat16 *value_row(const Params &p, const
         // a marked key came from a page inside the pool (anything else is read as zeros)
         const int page = p.pages[(long)it.seq * p.max_pages + key / p.page_size];
         return p.v + (((long)page * p.Hkv + it.g) * p.page_size + key % p.page_size) * kD;
+    }
+}
+
+// Adds the non-finite values of the item's marked keys to a finished row at position qpos:
+// the fp32 partial at `dst` (r < 0), or row r of the bf16 tile staged there.
+template <bool PAGED>
+__device__ __noinline__ void add_marked(const Params &p, const Slot &slot, const ItemRec &it, int qpos,
+                                        uint8_t *dst, int r) {
+    for (int b = 0; b < 512; ++b) {
+        if (!(slot.bad[b >> 5] >> (b & 31) & 1)) continue;
+        const int key = b < 256 ? it.qpos0 + 1 + b : max(0, it.qpos0 - p.window + 1) + b - 256;
+        if (key > qpos || (p.window > 0 && qpos - key >= p.window)) continue;
+        const __nv_bfloat16 *v = value_row<PAGED>(p, it, key);
+        for (int c = 0; c < kD; ++c) {
+            const float x = __bfloat162float(v[c]);
+            if (isfinite(x)) continue;
+            if (r < 0) {
+                reinterpret_cast<float *>(dst)[c] += x;
+            } else {
+                const int piece = (c >> 3 & 7) ^ (r & 7);
+                __nv_bfloat16 *e = reinterpret_cast<__nv_bfloat16 *>(
+                                       dst + (c >> 6) * kBoxBytes + r * 128 + piece * 16) + (c & 7);
+                *e = __float2bfloat16_rn(__bfloat162float(*e) + x);
+            }
+        }
     }
 }
 
@@ -432,23 +444,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // pages of a key tile: lane i holds the tile's i-th one
             const int npg = PAGED ? kBN / p.page_size : 1;
-            auto walk_pages = [&](const ItemRec &it) {
-                const int hi = it.qpos0 + it.ntok - 1;
-                return PAGED && it.n_tiles > 0
-                           ? PageWalk(p.pages + (long)it.seq * p.max_pages, it.kt_first * npg,
-                                      hi / p.page_size + 1)
-                           : PageWalk(nullptr, 0, 0);
-            };
+            // Items in turn; k = -1 only finds the first one.  (One copy of everything: code
+            // that an item's ends alone ran would have to be fetched again every time.)
             ItemRec it{}, next{};
-            settle(blockIdx.x, it);
-            if (ok) publish(0, it);
-            PageWalk pages = walk_pages(it), next_pages = pages;
-            if (ok && it.n_tiles > 0) load_q(0, it);
-            for (int k = 0; ok && it.n_tiles > 0; ++k, it = next, pages = next_pages) {
-                claim();   // one item ahead
+            PageWalk pages(nullptr, 0, 0);
+            for (int k = -1; ok; ++k) {
+                if (k >= 0) claim();   // one item ahead
                 const Edges e(it, p.window);
                 int slab = 0;
-                for (int l = 0; l < 2 * it.n_tiles && ok; ++l) {
+                for (int l = k < 0 ? 2 : 0; ok; ++l) {
+                    if (l == 2) {   // the next item, well before its first load
+                        const int idx = k < 0 ? static_cast<int>(blockIdx.x) : claimed();
+                        if (!ok) break;
+                        settle(idx, next);
+                        if (ok) publish(k + 1, next);
+                    }
+                    if (!ok || l >= 2 * it.n_tiles) break;
                     const int n0 = (it.kt_first + (l >> 1)) * kBN;
                     if (PAGED && !(l & 1)) {
                         const int pg = pages.get(n0 / p.page_size, npg);
@@ -483,19 +494,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // Q after the item's first K, whose slot was free earlier: Q's buffer is
                     // once the previous item's last score products are done
-                    if (l == 0 && k > 0) load_q(k, it);
-                    // the next item, well before its first load
-                    if (l == 1 && ok) {
-                        const int idx = claimed();
-                        if (ok) settle(idx, next);
-                        if (ok) publish(k + 1, next);
-                        if (ok) next_pages = walk_pages(next);
-                    }
+                    if (l == 0) load_q(k, it);
                 }
                 // ring slots for the item's O tiles
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (i >= n_out(it) || !ok) break;
+                    if (k < 0 || i >= n_out(it) || !ok) break;
                     const int st = u % kSlots;
                     if (u >= kSlots && !warp_wait(&bars->empty[st], (u / kSlots - 1) & 1)) {
                         fail(4, u);
@@ -510,6 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++outs[i];
                     ++u;
                 }
+                if (!ok || next.n_tiles < 0) break;
+                it = next;
+                if constexpr (PAGED)
+                    pages = PageWalk(p.pages + (long)it.seq * p.max_pages, it.kt_first * npg,
+                                     (it.qpos0 + it.ntok - 1) / p.page_size + 1);
             }
             if (!ok) {
                 // never leave the CTA with copies in flight
@@ -770,8 +779,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     const int below = min(kBN, max(0, e.lo_all - n0));
                     const int above = min(kBN, max(below, e.hi_all + 1 - n0));
-                    if (!clean(0, below)) strip(0, below);
-                    if (!clean(above, kBN)) strip(above, kBN);
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) {
+                        const int a = part ? above : 0, b = part ? kBN : below;
+                        if (!clean(a, b)) strip(a, b);
+                    }
                     if (touched) fence_proxy_async_smem();
                     mbar_arrive(&bars->guard[gc & 3]);
                     ++gc;
@@ -870,19 +882,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool vis = c_lo <= 32 * c && 32 * c + 32 <= c_hi;
                         const bool hid = c_hi <= 32 * c || 32 * c + 32 <= c_lo || c_hi <= c_lo;
                         if (__all_sync(0xffffffffu, vis)) continue;
+                        if (__all_sync(0xffffffffu, hid)) dead |= 1u << c;
                         uint32_t rr[32];
-                        if (__all_sync(0xffffffffu, hid)) {
-                            dead |= 1u << c;
+                        tmem_ld32(tS + 32 * c, rr);
+                        tmem_wait_ld();
+                        const int lo = c_lo - 32 * c, hi = c_hi - 32 * c;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(-CUDART_INF_F);
-                        } else {
-                            tmem_ld32(tS + 32 * c, rr);
-                            tmem_wait_ld();
-                            const int lo = c_lo - 32 * c, hi = c_hi - 32 * c;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (i < lo || i >= hi) rr[i] = __float_as_uint(-CUDART_INF_F);
-                        }
+                        for (int i = 0; i < 32; ++i)
+                            if (i < lo || i >= hi) rr[i] = __float_as_uint(-CUDART_INF_F);
                         tmem_st32(tS + 32 * c, rr);
                     }
                     tmem_wait_st();
@@ -994,19 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Slot &slot = bars->slot[k & (kItemSlots - 1)];
             const ItemRec it = slot.it;
             const int row = it.row0 + wg * p.Mt + rtok, head = it.g * p.G + rhead;
-            // the marked keys that this row sees, one by one: `fn(value row)`
-            auto marked = [&](auto &&fn) {
-                for (int w = 0; w < 16; ++w) {
-                    for (uint32_t b = slot.bad[w]; b; b &= b - 1) {
-                        const int at = 32 * w + __ffs(b) - 1;
-                        const int key = at < 256 ? it.qpos0 + 1 + at
-                                                 : max(0, it.qpos0 - p.window + 1) + at - 256;
-                        if (key <= qpos && (p.window <= 0 || qpos - key < p.window))
-                            fn(value_row<PAGED>(p, it, key));
-                    }
-                }
-            };
-            if (it.split >= 0) {
+            if (PAGED && it.split >= 0) {
                 // a span of the keys: the unnormalised row with its maximum (log2) and sum
                 if (valid) {
                     const size_t rec = (size_t)it.split * p.bounds.total * p.Hq + (size_t)row * p.Hq + head;
@@ -1017,12 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p.ws_ml[2 * rec] = m;
                     p.ws_ml[2 * rec + 1] = l;
                     if (slot.any_bad)
-                        marked([&](const __nv_bfloat16 *v) {
-                            for (int c = 0; c < kD; ++c) {
-                                const float y = __bfloat162float(v[c]);
-                                if (!isfinite(y)) p.ws_o[rec * kD + c] += y;
-                            }
-                        });
+                        add_marked<PAGED>(p, slot, it, qpos, reinterpret_cast<uint8_t *>(dst), -1);
                 }
             } else {
                 const float inv_l = l > 0.f || l != l ? 1.0f / l : 0.f;
@@ -1033,25 +1023,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 16; ++c) {
                     const float *y = x + 8 * c;
                     *reinterpret_cast<uint4 *>(stage + (c >> 3) * kBoxBytes + r * 128 +
-                                               ((whole ? (c & 7) ^ (r & 7) : c & 7) << 4)) =
+                                               (((c & 7) ^ (r & 7)) << 4)) =
                         make_uint4(pack_bf16x2(y[0] * inv_l, y[1] * inv_l),
                                    pack_bf16x2(y[2] * inv_l, y[3] * inv_l),
                                    pack_bf16x2(y[4] * inv_l, y[5] * inv_l),
                                    pack_bf16x2(y[6] * inv_l, y[7] * inv_l));
                 }
-                if (valid && slot.any_bad)
-                    marked([&](const __nv_bfloat16 *v) {
-                        for (int h = 0; h < 2; ++h)
-                            add_marked(stage + h * kBoxBytes, r, whole, v + 64 * h);
-                    });
-                fence_proxy_async_smem();
-                if (!whole && valid) {
-                    // a ragged tile: each row's halves by themselves
-                    __nv_bfloat16 *dst = p.o + (size_t)row * p.o_stride + head * kD;
-                    for (int h = 0; h < 2; ++h)
-                        bulk_store(dst + 64 * h, stage + h * kBoxBytes + r * 128, 128);
-                    bulk_commit_group();
-                    bulk_wait_read_all();
+                if (valid && slot.any_bad) add_marked<PAGED>(p, slot, it, qpos, stage, r);
+                if (whole) {
+                    fence_proxy_async_smem();   // the store warp's TMA reads it
+                } else {
+                    // a ragged tile: the warp writes the rows that are there, two at a time
+                    __syncwarp();
+                    const int r0 = (warp & 3) * 32, c = lane & 15;
+                    const int rows = min(32, min(ntok, p.Mt) * p.G - r0);
+#pragma unroll 4
+                    for (int i = lane >> 4; i < rows; i += 2) {
+                        const int rr = r0 + i, t = rr / p.G;
+                        const uint4 y = *reinterpret_cast<const uint4 *>(
+                            stage + (c >> 3) * kBoxBytes + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
+                        *reinterpret_cast<uint4 *>(
+                            p.o + (size_t)(it.row0 + wg * p.Mt + t) * p.o_stride +
+                            (it.g * p.G + rr - t * p.G) * kD + 8 * c) = y;
+                    }
                 }
                 mbar_arrive(&bars->staged[wg][ns & 1]);
                 ++ns;
@@ -1061,7 +1055,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             free_item();
         }
-        bulk_wait_all();   // the stores complete before the CTA exits
         if (!ok) set_status(p.status, GQA_ERR_DEVICE_TIMEOUT);
     }
 
