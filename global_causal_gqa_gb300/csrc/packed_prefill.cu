@@ -868,86 +868,110 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const bool full = (n0 + kBN - 1 <= qpos) &&
                                   (p.window <= 0 || n0 >= qpos - p.window + 1);
-                // Masking, decided per warp and 32-column chunk, applied in tensor memory
-                // before the row is loaded: a chunk visible in all 32 rows of the warp is
-                // left alone; one hidden in all of them gets -inf and is skipped below (P = 0,
-                // no exponentials); a mixed one is masked element by element.
-                uint32_t dead = 0;   // chunks hidden in every row of the warp
-                if (!__all_sync(0xffffffffu, full)) {
-                    // visible columns of this row in the tile: [c_lo, c_hi)
-                    const int c_hi = min(kBN, qpos - n0 + 1);
-                    const int c_lo = p.window > 0 ? max(0, qpos - p.window + 1 - n0) : 0;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        const bool vis = c_lo <= 32 * c && 32 * c + 32 <= c_hi;
-                        const bool hid = c_hi <= 32 * c || 32 * c + 32 <= c_lo || c_hi <= c_lo;
-                        if (__all_sync(0xffffffffu, vis)) continue;
-                        if (__all_sync(0xffffffffu, hid)) dead |= 1u << c;
-                        uint32_t rr[32];
-                        tmem_ld32(tS + 32 * c, rr);
-                        tmem_wait_ld();
-                        const int lo = c_lo - 32 * c, hi = c_hi - 32 * c;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < lo || i >= hi) rr[i] = __float_as_uint(-CUDART_INF_F);
-                        tmem_st32(tS + 32 * c, rr);
+                // A tile visible in all 32 rows of the warp is taken whole, in registers.  One
+                // at an edge of the mask goes in 32-column chunks, in loops that are not
+                // unrolled: a chunk hidden in all rows is left out (P = 0), one hidden in
+                // part is masked and written back before the second pass reads it.
+                const bool whole_tile = __all_sync(0xffffffffu, full);
+                float f = 1.0f, nmref = 0.f;
+                bool need_o = false;
+                // takes the tile's raw row maximum into account
+                auto update = [&](float mraw) {
+                    const float m_new = fmaxf(m, mraw * p.scale_log2);   // scale > 0
+                    if (m_new > m + kRescaleThreshold) {   // false while both -inf
+                        need_o = j > 0 && m != -CUDART_INF_F;
+                        f = ex2_approx(m - m_new);         // 0 when m was -inf
+                        l *= f;
+                        m = m_new;
                     }
-                    tmem_wait_st();
-                }
-                // the whole S row in registers: four loads in flight, one wait
-                float x[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t rr[32];
-                    tmem_ld32(tS + 32 * c, rr);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[32 * c + i] = __uint_as_float(rr[i]);
-                }
-                tmem_wait_ld();
-                // row maximum of the raw scores: 3-input max, 8 independent chains of 16
-                float mx8[8];
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    mx8[kk] = fmax3(x[kk], x[kk + 8], x[kk + 16]);
-#pragma unroll
-                    for (int tt = 3; tt < 15; tt += 2)
-                        mx8[kk] = fmax3(mx8[kk], x[kk + 8 * tt], x[kk + 8 * tt + 8]);
-                    mx8[kk] = fmaxf(mx8[kk], x[kk + 120]);
-                }
-                const float mraw = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                                         fmaxf(mx8[6], mx8[7]));
-                const float mx = mraw * p.scale_log2;   // scale > 0: max commutes with it
-                const float m_new = fmaxf(m, mx);
-                const bool grow = m_new > m + kRescaleThreshold;  // false while both -inf
-                const bool need_o = grow && j > 0 && m != -CUDART_INF_F;
-                const float f = grow ? ex2_approx(m - m_new) : 1.0f;  // 0 when m was -inf
-                if (grow) {
-                    l *= f;
-                    m = m_new;
-                }
-                const float nmref = (m == -CUDART_INF_F) ? 0.f : -m;
+                    nmref = m == -CUDART_INF_F ? 0.f : -m;
+                };
                 // P = 2^(s * scale * log2e - m) as bf16 over the first 64 columns of the S
                 // tile, 16 columns at a time (each piece lands on columns already read); the
                 // row sum takes the unrounded weights
                 float2 ls[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-                    if (dead & (1u << c)) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
-                        tmem_st16(tS + 16 * c, pk);
-                        continue;
-                    }
+                auto weights = [&](auto &&score, uint32_t (&pk)[16]) {   // of 32 columns
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float2 a = ffma2(make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]),
+                        const float2 a = ffma2(make_float2(score(2 * i), score(2 * i + 1)),
                                                p.scale_log2, nmref);
                         const float e0 = ex2_approx(a.x), e1 = ex2_approx(a.y);
                         ls[i & 3] = fadd2(ls[i & 3], make_float2(e0, e1));
                         pk[i] = pack_bf16x2(e0, e1);
                     }
-                    tmem_st16(tS + 16 * c, pk);
+                };
+                if (whole_tile) {
+                    float x[128];
+                    // four loads in flight, one wait
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t rr[32];
+                        tmem_ld32(tS + 32 * c, rr);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[32 * c + i] = __uint_as_float(rr[i]);
+                    }
+                    tmem_wait_ld();
+                    // row maximum of the raw scores: 3-input max, 8 independent chains of 16
+                    float mx8[8];
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        mx8[kk] = fmax3(x[kk], x[kk + 8], x[kk + 16]);
+#pragma unroll
+                        for (int tt = 3; tt < 15; tt += 2)
+                            mx8[kk] = fmax3(mx8[kk], x[kk + 8 * tt], x[kk + 8 * tt + 8]);
+                        mx8[kk] = fmaxf(mx8[kk], x[kk + 120]);
+                    }
+                    update(fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                                 fmaxf(mx8[6], mx8[7])));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
+                        weights([&](int i) { return x[32 * c + i]; }, pk);
+                        tmem_st16(tS + 16 * c, pk);
+                    }
+                } else {
+                    uint32_t live = 0;   // chunks that some row of the warp sees
+                    // visible columns of this row in the tile: [c_lo, c_hi)
+                    const int c_hi = min(kBN, qpos - n0 + 1);
+                    const int c_lo = p.window > 0 ? max(0, qpos - p.window + 1 - n0) : 0;
+                    float mraw = -CUDART_INF_F;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const int lo = c_lo - 32 * c, hi = c_hi - 32 * c;
+                        if (!__any_sync(0xffffffffu, lo < 32 && hi > 0 && lo < hi)) continue;
+                        live |= 1u << c;
+                        uint32_t rr[32];
+                        tmem_ld32(tS + 32 * c, rr);
+                        tmem_wait_ld();
+                        if (!__all_sync(0xffffffffu, lo <= 0 && hi >= 32)) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < lo || i >= hi) rr[i] = __float_as_uint(-CUDART_INF_F);
+                            tmem_st32(tS + 32 * c, rr);
+                        }
+                        float m4[4] = {mraw, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            m4[i / 2 & 3] = fmax3(m4[i / 2 & 3], __uint_as_float(rr[i]),
+                                                  __uint_as_float(rr[i + 1]));
+                        mraw = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+                    }
+                    tmem_wait_st();
+                    update(mraw);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
+                        if (live >> c & 1) {
+                            uint32_t rr[32];
+                            tmem_ld32(tS + 32 * c, rr);
+                            tmem_wait_ld();
+                            weights([&](int i) { return __uint_as_float(rr[i]); }, pk);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                        }
+                        tmem_st16(tS + 16 * c, pk);
+                    }
                 }
                 l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) +
                      ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
