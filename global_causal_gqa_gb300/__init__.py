@@ -119,14 +119,16 @@ def _ptr(x) -> Optional[int]:
     if isinstance(x, int):
         return x or None
     if isinstance(x, np.ndarray):
-        return x.ctypes.data
+        return x.__array_interface__["data"][0]   # a third of the time of x.ctypes.data
     return x.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        # the current stream's handle without a Stream object around it: 0.3 us instead of 3,
+        # a quarter of a small call's time on the host
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None

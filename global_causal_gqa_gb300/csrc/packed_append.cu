@@ -13,7 +13,8 @@
 // elements pair up under RoPE, so the norm is a shuffle reduction and the rotation stays in
 // the thread.  The threads of a token walk its vectors, q heads, k heads, v heads, in memory
 // order (one row of the fused projection is contiguous); a thread keeps its chunk index, so
-// the table row is read once per token and the gains once per block.
+// the table row is read once per token.  Four blocks per SM (64 registers) hide the loads'
+// latency better than more of them in flight per thread (96 registers: 162 us instead of 118).
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -24,6 +25,7 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendTokens = 8;   // most tokens of one block: one per warp to look up
+constexpr int kDeepTokens = 4;     // tokens of a block of a batch that fills the GPU
 
 struct AppendParams {
     const uint4 *q, *k, *v;
@@ -41,7 +43,7 @@ struct AppendParams {
 // D: head dim.  `per` threads (a multiple of the D / 16 lanes of a vector) serve one token at
 // a time, the block's kAppendThreads / per groups take its `tokens` tokens in turn.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 4)
     packed_rope_append_kernel(const AppendParams p, int tokens, int per) {
     constexpr int L = D / 16;    // lanes of a vector; also the distance of a pair's chunks
     constexpr int C = D / 8;     // 16-byte chunks of a vector
@@ -83,94 +85,99 @@ __global__ void __launch_bounds__(kAppendThreads)
     const int group = threadIdx.x / per, groups = kAppendThreads / per;
     const int tid = threadIdx.x - group * per;
     const int c = tid % L, u0 = tid / L, step = per / L;
-    const int heads = p.Hq + p.Hkv + (p.v_pool ? p.Hkv : 0);
+    // The vector's elements in pairs of neighbours: x[i] = 8c + 2i, + 1, y[i] those d/2 on.
+    struct Vec {
+        float2 x[4], y[4];
+    };
+    auto unpack = [](const uint4 &a, const uint4 &b) {
+        Vec v;
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v.x[i] = make_float2(bf16lo(aw[i]), bf16hi(aw[i]));
+            v.y[i] = make_float2(bf16lo(bw[i]), bf16hi(bw[i]));
+        }
+        return v;
+    };
+    // gamma / sqrt(mean(x^2) + eps) over the vector's L lanes (every lane of the warp shuffles)
+    auto normalise = [&](Vec &v, const float4 *gamma, bool on) {
+        float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s2 = ffma2v(v.x[i], v.x[i], ffma2v(v.y[i], v.y[i], s2));
+        float ss = s2.x + s2.y;
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (!on) return;
+        const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 ga = __ldg(gamma + 2 * c + i), gb = __ldg(gamma + 2 * (c + L) + i);
+            v.x[2 * i] = fmul2(v.x[2 * i], make_float2(r * ga.x, r * ga.y));
+            v.x[2 * i + 1] = fmul2(v.x[2 * i + 1], make_float2(r * ga.z, r * ga.w));
+            v.y[2 * i] = fmul2(v.y[2 * i], make_float2(r * gb.x, r * gb.y));
+            v.y[2 * i + 1] = fmul2(v.y[2 * i + 1], make_float2(r * gb.z, r * gb.w));
+        }
+    };
     for (int t = group; t < tokens; t += groups) {
         const int pos = s_pos[t], page = s_page[t];
         if (pos < 0) continue;   // the same for the whole group, which is whole vectors
         const long row = row_base + t;
-        float cs[16];            // (cos, sin) of pairs 8c .. 8c + 7
+        float2 co[4], si[4];     // cos and sin of pairs 8c + 2i, + 1
         const float4 *tr = p.table + (long)pos * (D / 4) + 4 * c;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 x = __ldg(tr + i);
-            cs[4 * i] = x.x;
-            cs[4 * i + 1] = x.y;
-            cs[4 * i + 2] = x.z;
-            cs[4 * i + 3] = x.w;
+            const float4 w = __ldg(tr + i);
+            co[i] = make_float2(w.x, w.z);
+            si[i] = make_float2(w.y, w.w);
         }
-        const long slot = p.page_size ? pos % p.page_size : 0;
-        // every lane of a warp makes the same number of turns (the norm shuffles): heads
-        // past the last are computed on the last one and not stored
-        for (int ub = 0; ub < heads; ub += step) {
-            const int uu = ub + u0, u = min(uu, heads - 1);
-            const bool isq = u < p.Hq, isk = !isq && u < p.Hq + p.Hkv;
-            const int g = isq ? u : isk ? u - p.Hq : u - p.Hq - p.Hkv;
-            const uint4 *src = (isq ? p.q + row * p.q_stride
-                                    : isk ? p.k + row * p.k_stride : p.v + row * p.v_stride) +
-                               (long)g * C;
-            uint4 a = __ldg(src + c), b = __ldg(src + c + L);
-            const float4 *gam = isq ? p.q_gamma : isk ? p.k_gamma : nullptr;
-            float x[8], y[8];
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        auto rotate = [&](const Vec &v, uint4 &a, uint4 &b) {
+            uint32_t ao[4], bo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[2 * i] = bf16lo(aw[i]);
-                x[2 * i + 1] = bf16hi(aw[i]);
-                y[2 * i] = bf16lo(bw[i]);
-                y[2 * i + 1] = bf16hi(bw[i]);
+                const float2 ra = fsub2(fmul2(v.x[i], co[i]), fmul2(v.y[i], si[i]));
+                const float2 rb = ffma2v(v.x[i], si[i], fmul2(v.y[i], co[i]));
+                ao[i] = pack_bf16x2(ra.x, ra.y);
+                bo[i] = pack_bf16x2(rb.x, rb.y);
             }
-            if (p.q_gamma || p.k_gamma) {
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
-#pragma unroll
-                for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                if (gam) {
-                    const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 ga = __ldg(gam + 2 * c + i), gb = __ldg(gam + 2 * (c + L) + i);
-                        x[4 * i] *= r * ga.x;
-                        x[4 * i + 1] *= r * ga.y;
-                        x[4 * i + 2] *= r * ga.z;
-                        x[4 * i + 3] *= r * ga.w;
-                        y[4 * i] *= r * gb.x;
-                        y[4 * i + 1] *= r * gb.y;
-                        y[4 * i + 2] *= r * gb.z;
-                        y[4 * i + 3] *= r * gb.w;
-                    }
-                }
+            a = make_uint4(ao[0], ao[1], ao[2], ao[3]);
+            b = make_uint4(bo[0], bo[1], bo[2], bo[3]);
+        };
+        // Queries, then keys and values.  Every lane of a warp makes the same number of turns
+        // (the norm shuffles), past the last vector on the last one, without storing.
+        const uint4 *src = p.q + row * p.q_stride + c;
+        uint4 *dst = p.q_out + row * p.Hq * C + c;
+        for (int ub = 0; ub < p.Hq; ub += step) {
+            const int u = min(ub + u0, p.Hq - 1);
+            uint4 a = __ldg(src + (long)u * C), b = __ldg(src + (long)u * C + L);
+            Vec v = unpack(a, b);
+            if (p.q_gamma) normalise(v, p.q_gamma, true);
+            rotate(v, a, b);
+            if (ub + u0 < p.Hq) {
+                dst[(long)u * C] = a;
+                dst[(long)u * C + L] = b;
             }
-            if (isq || isk) {
-                uint32_t ao[4], bo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float c0 = cs[4 * i], s0 = cs[4 * i + 1];
-                    const float c1 = cs[4 * i + 2], s1 = cs[4 * i + 3];
-                    const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-                    ao[i] = pack_bf16x2(fmaf(x0, c0, -y0 * s0), fmaf(x1, c1, -y1 * s1));
-                    bo[i] = pack_bf16x2(fmaf(x0, s0, y0 * c0), fmaf(x1, s1, y1 * c1));
-                }
-                a = make_uint4(ao[0], ao[1], ao[2], ao[3]);
-                b = make_uint4(bo[0], bo[1], bo[2], bo[3]);
+        }
+        const int heads = p.v_pool ? 2 * p.Hkv : p.Hkv;
+        const long slot = p.page_size ? ((long)page * p.Hkv * p.page_size + pos % p.page_size) : 0;
+        for (int ub = 0; ub < heads; ub += step) {
+            const int u = min(ub + u0, heads - 1);
+            const bool isk = u < p.Hkv;
+            const int g = isk ? u : u - p.Hkv;
+            const uint4 *s = (isk ? p.k + row * p.k_stride : p.v + row * p.v_stride) + (long)g * C + c;
+            uint4 a = __ldg(s), b = __ldg(s + L);
+            Vec v = unpack(a, b);
+            if (p.k_gamma) normalise(v, p.k_gamma, isk);
+            if (isk) rotate(v, a, b);
+            if (ub + u0 >= heads) continue;
+            if (page >= 0 && p.k_pool) {
+                uint4 *d = (isk ? p.k_pool : p.v_pool) + (slot + (long)g * p.page_size) * C + c;
+                d[0] = a;
+                d[L] = b;
             }
-            if (uu >= heads) continue;   // after this turn's shuffles
-            uint4 *dst = nullptr;
-            if (isq) {
-                dst = p.q_out + (row * p.Hq + g) * C;
-            } else {
-                if (page >= 0)
-                    dst = (isk ? p.k_pool : p.v_pool) +
-                          (((long)page * p.Hkv + g) * p.page_size + slot) * C;
-                if (isk && p.k_out) {
-                    uint4 *ko = p.k_out + (row * p.Hkv + g) * C;
-                    ko[c] = a;
-                    ko[c + L] = b;
-                }
-            }
-            if (dst) {
-                dst[c] = a;
-                dst[c + L] = b;
+            if (isk && p.k_out) {
+                uint4 *d = p.k_out + (row * p.Hkv + g) * C + c;
+                d[0] = a;
+                d[L] = b;
             }
         }
     }
@@ -215,15 +222,16 @@ cudaError_t launch_packed_rope_append(const void *q, int64_t q_stride, const voi
         p.v_pool = static_cast<uint4 *>(cache->v);
         p.bounds.cap = (long)cache->max_pages * cache->page_size;
     }
-    // threads per token: the power of two that covers its vectors' lanes, within a block (and
-    // at least a warp, whose lanes shuffle together)
+    // Threads per token: a power of two, at least a warp (whose lanes shuffle together), that
+    // covers the token's lanes; for a batch that fills the GPU half a block at most and four
+    // tokens per block (64 + 8 + 8 heads of 128 are 640 lanes, 5 turns of 128: 118 us for 15424
+    // tokens, 133 with 3 turns of 256, 125 with eight tokens per block; 4.8 TB/s).
+    const bool deep = total > 8 * 152;
     const int lanes = (Hq + 2 * Hkv) * (d / 16);
     int per = 32;
-    while (per < lanes && per < kAppendThreads) per <<= 1;
-    // one token per group of threads; more per block only when the grid is deep without
+    while (per < lanes && per < (deep ? kAppendThreads / 2 : kAppendThreads)) per <<= 1;
     int tokens = kAppendThreads / per;
-    while (tokens < kAppendTokens && (long)total > 8L * 152 * tokens) tokens <<= 1;
-    if (tokens > kAppendTokens) tokens = kAppendTokens;
+    if (deep && tokens < kDeepTokens) tokens = kDeepTokens;
     auto kern = d == 64    ? packed_rope_append_kernel<64>
                 : d == 128 ? packed_rope_append_kernel<128>
                 : d == 256 ? packed_rope_append_kernel<256>
