@@ -137,6 +137,10 @@ __device__ __forceinline__ bool strip_nonfinite(uint32_t &w) {
     return lo || hi;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 enum Role { kRoleProducer = 0, kRoleConsumer = 2 };
 
 // ROWS: 8 or 16 rows of the MMA in use (8: the upper half is zero and costs no exponentials).
@@ -267,6 +271,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars->seg_full[slot]);
             }
             __syncwarp();
+            // its queries on their way to L2: two 128-byte lines a row
+            if (sg.stages > 0 && lane < 2 * sg.T * p.G) {
+                const int r = lane >> 1, t = r / p.G;
+                prefetch_l2(p.q + (long)(sg.row0 + t) * p.q_stride +
+                            (sg.g * p.G + r - t * p.G) * kD + 64 * (lane & 1));
+            }
             if (sg.stages < 0) {
                 if (!p.whole && lane == 0) p.ws_joint[blockIdx.x] = joint;
                 break;
@@ -323,6 +333,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rows16 = part / box * 2 * half + part % box * 128;
     const uint32_t k_row = rows16 + (((mat >> 1) << 3) + l7) * 128;
     const uint32_t v_row = kTileBytes + rows16 + (((mat & 1) << 3) + l7) * 128;
+    // swizzled place of chunk 2i (+ 1 for the odd matrices) of a half, i = 0..3
+    uint32_t k_off[4], v_off[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        k_off[i] = k_row + (((2 * i + (mat & 1)) ^ l7) << 4);
+        v_off[i] = v_row + (((2 * i + (mat >> 1)) ^ l7) << 4);
+    }
     int meets = 0;
     auto meet = [&]() {
         __syncwarp();
@@ -389,8 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
                     uint32_t b[4];
-                    const int c = 2 * ks + (mat & 1);
-                    ldsm4(b, base + (c >> 3) * half + k_row + (((c & 7) ^ l7) << 4));
+                    ldsm4(b, (ks < 4 ? base : base + half) + k_off[ks & 3]);
                     const uint32_t a0 = qa[ks][0], a1 = HR > 1 ? qa[ks][1] : 0u;
                     const uint32_t a2 = qa[ks][HR], a3 = HR > 1 ? qa[ks][HR + 1] : 0u;
                     mma16816(ks & 1 ? t0 : s0, a0, a1, a2, a3, b[0], b[1]);
@@ -470,8 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int nn = 0; nn < 8; ++nn) {
                     uint32_t b[4];
-                    const int c = 2 * nn + (mat >> 1);
-                    ldsm4_trans(b, base + (c >> 3) * half + v_row + (((c & 7) ^ l7) << 4));
+                    ldsm4_trans(b, (nn < 4 ? base : base + half) + v_off[nn & 3]);
                     if (edge) {
                         b[0] &= seen0;
                         b[1] &= seen1;
