@@ -1,4 +1,6 @@
-"""Decode step over every attention layer of a hybrid local/global decoder.
+"""Attention steps over every layer of a hybrid local/global decoder.
+
+Decode over linear and ring caches (`LayerStack`):
 
 "PLaMo 3アーキテクチャ徹底解析" §2.3 and §4.4: in a decode step each layer appends the new
 token's K and V to its cache and attends over it; local layers keep a ring of the newest
@@ -7,6 +9,10 @@ global).  `LayerStack` drives that step through the C ABI: per layer one gqa_kv_
 and one gqa_attn_decode on a stream, with every layer's descriptor array in one device
 buffer so that a whole step can be replayed from the same cache state (one copy restores
 every layer's counts).  The step can be captured once in a CUDA graph and replayed.
+
+Steps over paged caches (`PagedStack`): a packed batch of prompts, chunks, drafts and decode
+tokens goes through each layer's QK norm + RoPE + append and its attention, local layers with
+their window, over page tables that all layers share.
 
 Argument marshalling and launch order only: every step of the computation runs in the
 library's kernels.  The caller owns the caches, query and new-token tensors, outputs and
@@ -19,8 +25,9 @@ from typing import List, Sequence
 
 import numpy as np
 
-from . import (KV_DESC_DTYPE, gqa_attn_decode, gqa_decode_workspace_bytes, gqa_kv_append,
-               make_kv_descs)
+from . import (KV_DESC_DTYPE, gqa_attn_decode, gqa_attn_paged, gqa_attn_paged_workspace_bytes,
+               gqa_decode_workspace_bytes, gqa_kv_append, gqa_packed_rope_append, make_kv_descs,
+               make_paged_kv)
 
 
 @dataclass
@@ -95,3 +102,67 @@ class LayerStack:
     def counts(self, layer: int) -> np.ndarray:
         a = self.descs[layer].cpu().numpy().view(KV_DESC_DTYPE)
         return a["count"].astype(np.int64)
+
+
+@dataclass
+class PagedLayer:
+    """One attention layer's caller-owned device tensors for a packed batch of `total` tokens."""
+    k_pool: object         # [num_pages, Hkv, page_size, d] bf16, keys after RoPE
+    v_pool: object         # the same shape
+    qkv: object            # [total, (Hq + 2 Hkv) d] bf16, rows of the fused projection
+    o: object              # [total, Hq, d] bf16, the attention output
+    q_gamma: object        # [d] float32 gains of the Q/K RMSNorm, or None
+    k_gamma: object
+    table: object          # RoPE table of the layer type, table_len positions
+    table_len: int
+    window: int            # 0: global layer
+
+
+class PagedStack:
+    """A serving step over paged caches: per layer one gqa_packed_rope_append and one
+    gqa_attn_paged.  cu_seqlens (int32 [nseq + 1]), kv_lens (int32 [nseq], counted with the new
+    tokens) and page_table (int32 [nseq, max_pages], used by every layer with its own pools)
+    are device tensors read when the kernels run: a captured step follows what the caller
+    writes to them between replays, up to max_q new tokens and max_kv tokens of a sequence."""
+
+    def __init__(self, layers: List[PagedLayer], cu_seqlens, kv_lens, page_table, max_q: int,
+                 max_kv: int, Hq: int, Hkv: int, d: int, scale: float, eps: float = 1e-6):
+        import torch
+        self.layers, self.cu_seqlens, self.kv_lens = layers, cu_seqlens, kv_lens
+        self.page_table = page_table
+        self.max_q, self.max_kv, self.Hq, self.Hkv, self.d = max_q, max_kv, Hq, Hkv, d
+        self.scale, self.eps = scale, eps
+        self.nseq, self.total = page_table.shape[0], layers[0].qkv.shape[0]
+        self.caches = [make_paged_kv(L.k_pool, L.v_pool, page_table, kv_lens) for L in layers]
+        dev = layers[0].qkv.device
+        self.wsb = gqa_attn_paged_workspace_bytes(self.nseq, self.total, max_q, max_kv, Hq, Hkv, d)
+        self.ws = torch.empty(max(self.wsb, 16), dtype=torch.uint8, device=dev)
+        self.q = torch.empty(self.total, Hq, d, dtype=torch.bfloat16, device=dev)
+        self.graph = None
+
+    def step(self, stream=None):
+        """One step: every layer appends its new tokens' keys and values, then attends."""
+        Hq, Hkv, d = self.Hq, self.Hkv, self.d
+        row = (Hq + 2 * Hkv) * d
+        for L, cache in zip(self.layers, self.caches):
+            q, k, v = L.qkv.split([Hq * d, Hkv * d, Hkv * d], 1)
+            gqa_packed_rope_append(q, row, k, row, v, row, self.cu_seqlens, self.nseq, self.total,
+                                   Hq, Hkv, d, L.q_gamma, L.k_gamma, self.eps, L.table,
+                                   L.table_len, self.q, None, cache, stream)
+            gqa_attn_paged(self.q, Hq * d, cache, self.cu_seqlens, self.nseq, self.total,
+                           self.max_q, self.max_kv, Hq, L.window, self.scale, L.o, Hq * d, None,
+                           self.ws, self.wsb, stream)
+
+    def capture(self):
+        """Captures `step` in a CUDA graph on a side stream (run `step` once before: the first
+        call of a kernel loads it)."""
+        import torch
+        graph = torch.cuda.CUDAGraph()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            with torch.cuda.graph(graph, stream=side):
+                self.step()
+        torch.cuda.current_stream().wait_stream(side)
+        self.graph = graph
+        return graph
