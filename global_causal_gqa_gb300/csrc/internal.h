@@ -150,7 +150,7 @@ struct PackedAttn {
 };
 // the tensor-core kernel for prompts and chunks (packed_prefill.cu); returns a gqa_status
 int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
-size_t packed_prefill_workspace_bytes(int total, int max_kv, int Hq, int Hkv);
+size_t packed_prefill_workspace_bytes(int nseq, int total, int max_kv, int Hq, int Hkv);
 // the streaming kernel for a few rows per sequence (paged_decode.cu)
 bool paged_decode_fits(int max_q, int G);
 int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s);

@@ -62,6 +62,11 @@ __device__ __forceinline__ int packed_row_seq(const int32_t *cu, int nseq, int r
     return n;
 }
 
+// Starts a load of *p into L1 without waiting for it.
+__device__ __forceinline__ void touch(const int32_t *p) {
+    asm volatile("{\n\t.reg .b32 t;\n\tld.global.nc.b32 t, [%0];\n\t}" ::"l"(p));
+}
+
 // A producer warp's walk over the page-table entries of one sequence, in order: the lanes
 // hold 32 entries and the 32 after them, so an entry has been on its way for at least 32
 // pages' worth of loads when it is needed.

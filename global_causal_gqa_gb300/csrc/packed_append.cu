@@ -48,7 +48,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
     constexpr int L = D / 16;    // lanes of a vector; also the distance of a pair's chunks
     constexpr int C = D / 8;     // 16-byte chunks of a vector
     griddep_wait();
-    griddep_launch_dependents();
+    // The next kernel's blocks may come at once where this grid is all resident; a deeper grid
+    // keeps the SMs to itself (prompts of 6000 tokens, append + attention: 252 against 272 us).
+    if (gridDim.x <= 4 * 152) griddep_launch_dependents();
     __shared__ int s_pos[kAppendTokens];     // position; -1: nothing to do for this token
     __shared__ int s_page[kAppendTokens];    // page; -1: outside the pool
     const int row_base = blockIdx.x * tokens;

@@ -47,10 +47,10 @@ bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t paged_workspace_bytes(int, int total, int max_q, int max_kv, int Hq, int Hkv, int) {
+size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv, int) {
     return paged_decode_fits(max_q, Hq / Hkv)
                ? paged_decode_workspace_bytes(max_kv)
-               : packed_prefill_workspace_bytes(total, max_kv, Hq, Hkv);
+               : packed_prefill_workspace_bytes(nseq, total, max_kv, Hq, Hkv);
 }
 
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {

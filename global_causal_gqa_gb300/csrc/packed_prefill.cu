@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ CUtensorMap tmO, const Params p) {
+    griddep_wait();
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte alignment for the 128-byte swizzle atoms
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -315,6 +316,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars *bars = reinterpret_cast<Bars *>(smem + kSmemBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // the first sequences' offsets and lengths into L1 while the barriers and tensor memory are
+    // set up (the producer's walk reads them first)
+    if (warp == 2) {
+        if (lane <= p.nseq) touch(p.cu + lane);
+        if (PAGED && lane < p.nseq) touch(p.kv_lens + lane);
+        if (lane == 0) {
+            tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+            tma_prefetch_desc(&tmO);
+        }
+    }
     if (threadIdx.x == 0) {
         mbar_init(&bars->clc_full, 1);
         for (int i = 0; i < kItemSlots; ++i) {
@@ -358,12 +371,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         reg_dealloc<96>();
         if (warp == 0) {
             // ================= work claiming, TMA loads =================
-            if (lane == 0) {
-                tma_prefetch_desc(&tmQ);
-                tma_prefetch_desc(&tmK);
-                tma_prefetch_desc(&tmV);
-                tma_prefetch_desc(&tmO);
-            }
             bool ok = true;
             int u = 0;        // ring loads issued
             int nq = 0;       // items whose Q tiles have been issued
@@ -1082,6 +1089,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) set_status(p.status, GQA_ERR_DEVICE_TIMEOUT);
     }
 
+    // only now: a CTA of the next kernel that came earlier would sit on an SM that this grid's
+    // unclaimed CTAs need (162 us for the 16 prompts in a row became 176)
+    griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -1090,11 +1100,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Merges the spans of split items: one warp per (token, query head), 4 dims per lane.
-__global__ void packed_combine_kernel(const Params p) {
-    const int row = blockIdx.x, lane = threadIdx.x & 31;
+// Merges the spans of split items: one warp per (token, query head), the spans' maxima and
+// sums in the lanes, 4 dims of the output per lane.
+constexpr int kMostSpans = 64;
+constexpr int kCombineWarps = 8;
+__global__ void __launch_bounds__(32 * kCombineWarps) packed_combine_kernel(const Params p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int row = blockIdx.x, h = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
     const int i = packed_row_seq(p.cu, p.nseq, row);
-    if (i >= p.nseq) return;
+    if (i >= p.nseq || h >= p.Hq) return;
     const PackedSeq s = packed_seq(p.cu, p.kv_lens, i, p.bounds, nullptr);
     if (row < s.row0 || row >= s.row0 + s.T) return;
     // the block of tokens that the row was computed in
@@ -1102,56 +1118,90 @@ __global__ void packed_combine_kernel(const Params p) {
     const int q_lo = s.S - s.T + t0, q_hi = q_lo + min(ntok, s.T - t0) - 1;
     const int spans = n_spans(q_hi / kBN - first_tile(q_lo, p.window) + 1, p.split_tiles);
     if (spans <= 1) return;   // written by the attention kernel itself
-    const size_t step = (size_t)p.bounds.total * p.Hq;
-    for (int h = threadIdx.x >> 5; h < p.Hq; h += blockDim.x >> 5) {
-        const size_t rec = (size_t)row * p.Hq + h;
-        float M = -CUDART_INF_F;
-        for (int k = 0; k < spans; ++k) M = fmaxf(M, p.ws_ml[2 * (rec + k * step)]);
-        float L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < spans; ++k) {
-            const size_t at = rec + k * step;
-            const float m = p.ws_ml[2 * at];
-            if (m == -CUDART_INF_F && p.ws_ml[2 * at + 1] == 0.f) continue;   // a span with no visible key
-            const float f = ex2_approx(m - M);
-            const float4 o = reinterpret_cast<const float4 *>(p.ws_o + at * kD)[lane];
-            L = fmaf(p.ws_ml[2 * at + 1], f, L);
-            acc.x = fmaf(o.x, f, acc.x);
-            acc.y = fmaf(o.y, f, acc.y);
-            acc.z = fmaf(o.z, f, acc.z);
-            acc.w = fmaf(o.w, f, acc.w);
-        }
-        const float r = 1.0f / L;
-        reinterpret_cast<uint2 *>(p.o + (size_t)row * p.o_stride + h * kD)[lane] =
-            make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
-        if (p.lse && lane == 0)
-            p.lse[(size_t)h * p.bounds.total + row] = (M + __log2f(L)) * 0.69314718055994531f;
+    const size_t step = (size_t)p.bounds.total * p.Hq, rec = (size_t)row * p.Hq + h;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
+    float2 x[kMostSpans / 32];
+    float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+    for (int t = 0; t < kMostSpans / 32; ++t) {
+        x[t] = make_float2(-CUDART_INF_F, 0.f);
+        if (32 * t + lane < spans) x[t] = ml[rec + (32 * t + lane) * step];
+        M = fmaxf(M, x[t].x);
     }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int t = 0; t < kMostSpans / 32; ++t) {
+        // a span with no key that the row sees: m = -inf, l = 0 and O = 0 (NaN scores alone
+        // also leave m at -inf, with l and O NaN)
+        const float f = x[t].x == -CUDART_INF_F ? (x[t].y == 0.f ? 0.f : 1.f) : ex2_approx(x[t].x - M);
+        L = fmaf(x[t].y, f, L);
+        const int n = min(32, spans - 32 * t);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float4 o = reinterpret_cast<const float4 *>(p.ws_o + (rec + (32 * t + k) * step) * kD)[lane];
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            acc.x = fmaf(o.x, fk, acc.x);
+            acc.y = fmaf(o.y, fk, acc.y);
+            acc.z = fmaf(o.z, fk, acc.z);
+            acc.w = fmaf(o.w, fk, acc.w);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    const float r = 1.0f / L;
+    reinterpret_cast<uint2 *>(p.o + (size_t)row * p.o_stride + h * kD)[lane] =
+        make_uint2(pack_bf16x2(acc.x * r, acc.y * r), pack_bf16x2(acc.z * r, acc.w * r));
+    if (p.lse && lane == 0)
+        p.lse[(size_t)h * p.bounds.total + row] = (M + __log2f(L)) * 0.69314718055994531f;
 }
 
 // How many key tiles a span of a split item has (0: items stay whole), and the most spans.
-// Items stay whole when there are enough of them for every SM; otherwise each is split so
-// that the grid has about two per SM, but no span is shorter than 4 tiles (512 keys).
+// The number of spans n that an estimate likes best: rounds of items over the SMs, each of
+// tiles / n key tiles at kTileUs and a fixed part, and for n > 1 the partials' bytes out and in
+// and the combine kernel.  (Measured, 64 heads on 8: a chunk of 512 tokens over 8192 keys, 128
+// items of 64 tiles: whole TODO us, 3 spans 155 us.)
 struct SpanRule {
     int split_tiles, spans;
-    int most;   // spans of this shape with any window: a window only lowers it
 };
-SpanRule span_rule(int total, int max_kv, int Hkv, int G, int window) {
-    const int ntok = 2 * (kBM / G);
-    const long items = (long)((total + ntok - 1) / ntok) * Hkv;
+constexpr double kTileUs = 1.8, kItemUs = 5.0, kPartialUs = 8.0, kCombineUs = 4.0, kBytesPerUs = 5e6;
+int best_spans(int nseq, int total, int tiles, int Hq, int Hkv, int most) {
+    const int ntok = 2 * (kBM / (Hq / Hkv));
+    // every sequence ends in half a block on average
+    const long blocks = nseq > 1 ? total / ntok + (nseq < total ? nseq : total) / 2 + 1
+                                 : (total + ntok - 1) / ntok;
+    const long items = blocks * Hkv;
+    int best = 1;
+    double least = 0;
+    for (int n = 1; n <= most && (n == 1 || tiles / n >= 4); ++n) {
+        const double rounds = (items * n + kSMs - 1) / kSMs;
+        double us = rounds * (kTileUs * ((tiles + n - 1) / n) + (n > 1 ? kPartialUs : kItemUs));
+        if (n > 1) us += kCombineUs + 2.0 * n * total * Hq * (kD + 2) * sizeof(float) / kBytesPerUs;
+        if (n == 1 || us < least) {
+            best = n;
+            least = us;
+        }
+    }
+    return best;
+}
+// `window` only ever lowers the number of spans: the workspace is sized without it.
+SpanRule span_rule(int nseq, int total, int max_kv, int Hq, int Hkv, int window) {
+    const int ntok = 2 * (kBM / (Hq / Hkv));
+    int n = best_spans(nseq, total, most_tiles(max_kv, ntok, 0), Hq, Hkv, kMostSpans);
     const int tiles = most_tiles(max_kv, ntok, window);
-    long want = (2 * kSMs + items - 1) / items;
-    if (want > tiles / 4) want = tiles / 4;
-    if (want <= 1) return {0, 1, 1};
-    const int per = static_cast<int>((tiles + want - 1) / want);
-    return {per, n_spans(tiles, per), static_cast<int>(want)};
+    if (window > 0) n = best_spans(nseq, total, tiles, Hq, Hkv, n);
+    if (n <= 1) return {0, 1};
+    const int per = (tiles + n - 1) / n;
+    return {per, n_spans(tiles, per)};
 }
 
 }  // namespace
 
-size_t packed_prefill_workspace_bytes(int total, int max_kv, int Hq, int Hkv) {
-    const SpanRule r = span_rule(total, max_kv, Hkv, Hq / Hkv, 0);
-    return r.most <= 1 ? 0 : (size_t)r.most * total * Hq * (kD + 2) * sizeof(float);
+size_t packed_prefill_workspace_bytes(int nseq, int total, int max_kv, int Hq, int Hkv) {
+    const int tiles = most_tiles(max_kv, 2 * (kBM / (Hq / Hkv)), 0);
+    const int n = best_spans(nseq, total, tiles, Hq, Hkv, kMostSpans);
+    return n <= 1 ? 0 : (size_t)n * total * Hq * (kD + 2) * sizeof(float);
 }
 
 int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
@@ -1193,7 +1243,7 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
         p.page_size = c.page_size;
         p.max_pages = c.max_pages;
         p.bounds.cap = (long)c.max_pages * c.page_size;
-        const SpanRule r = span_rule(a.total, a.max_kv, a.Hkv, p.G, a.window);
+        const SpanRule r = span_rule(a.nseq, a.total, a.max_kv, a.Hq, a.Hkv, a.window);
         p.split_tiles = r.split_tiles;
         spans = r.spans;
         if (spans > 1) {
@@ -1225,12 +1275,14 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
     const long blocks = (long)a.total / ntok + (a.nseq < a.total ? a.nseq : a.total);
     const long grid = blocks * a.Hkv * spans;
     if (grid > 0x7fffffffL) return GQA_ERR_UNSUPPORTED;
-    kern<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, s>>>(mq, mk, mv, mo, p);
-    if (cudaPeekAtLastError() != cudaSuccess) return GQA_ERR_CUDA;
-    if (spans > 1) {
-        packed_combine_kernel<<<a.total, 256, 0, s>>>(p);
-        if (cudaPeekAtLastError() != cudaSuccess) return GQA_ERR_CUDA;
-    }
+    if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, mq, mk,
+                   mv, mo, p) != cudaSuccess)
+        return GQA_ERR_CUDA;
+    if (spans > 1 &&
+        launch_pdl(packed_combine_kernel,
+                   dim3(a.total, (a.Hq + kCombineWarps - 1) / kCombineWarps),
+                   dim3(32 * kCombineWarps), 0, s, p) != cudaSuccess)
+        return GQA_ERR_CUDA;
     return GQA_OK;
 }
 
