@@ -1158,25 +1158,35 @@ __global__ void __launch_bounds__(32 * kCombineWarps) packed_combine_kernel(cons
 }
 
 // How many key tiles a span of a split item has (0: items stay whole), and the most spans.
-// The number of spans n that an estimate likes best: rounds of items over the SMs, each of
-// tiles / n key tiles at kTileUs and a fixed part, and for n > 1 the partials' bytes out and in
-// and the combine kernel.  (Measured, 64 heads on 8: a chunk of 512 tokens over 8192 keys, 128
-// items of 64 tiles: whole TODO us, 3 spans 155 us.)
+// The number of spans n is the one that an estimate of the time likes best.  An item of
+// tiles / n key tiles takes kTileUs each and a fixed part, more where it writes a partial.
+// One sequence: all items are about as long, and go in rounds over the SMs.  Several: items
+// are shorter than the host's bound on the keys (kMean of it, taken together) and the longest
+// may come last.  Partials cost their bytes and the combine kernel.
+// (Measured, 64 heads on 8: 512 tokens over 8192 keys 116 us whole, 137 / 151 / 173 in 2 / 4 / 8
+// spans; 128 over 32000: 227 / 124 / 136 us in 2 / 4 / 8; 12 chunks of 1-300 over 1000-12000:
+// 272 whole, 203 / 169 / 186.)
 struct SpanRule {
     int split_tiles, spans;
 };
-constexpr double kTileUs = 1.8, kItemUs = 5.0, kPartialUs = 8.0, kCombineUs = 4.0, kBytesPerUs = 5e6;
+constexpr double kTileUs = 1.75, kItemUs = 5.0, kPartialUs = 8.0, kCombineUs = 4.0, kBytesPerUs = 1e7;
+constexpr double kMean = 0.6;
 int best_spans(int nseq, int total, int tiles, int Hq, int Hkv, int most) {
     const int ntok = 2 * (kBM / (Hq / Hkv));
     // every sequence ends in half a block on average
     const long blocks = nseq > 1 ? total / ntok + (nseq < total ? nseq : total) / 2 + 1
                                  : (total + ntok - 1) / ntok;
-    const long items = blocks * Hkv;
+    const double items = static_cast<double>(blocks) * Hkv;
     int best = 1;
     double least = 0;
     for (int n = 1; n <= most && (n == 1 || tiles / n >= 4); ++n) {
-        const double rounds = (items * n + kSMs - 1) / kSMs;
-        double us = rounds * (kTileUs * ((tiles + n - 1) / n) + (n > 1 ? kPartialUs : kItemUs));
+        const double fixed = n > 1 ? kPartialUs : kItemUs;
+        const double longest = kTileUs * ((tiles + n - 1) / n) + fixed;
+        double us = longest;
+        if (nseq == 1)
+            us *= static_cast<long>((items * n + kSMs - 1) / kSMs);
+        else if (items * n > kSMs)
+            us += items * (kMean * kTileUs * tiles + n * fixed) / kSMs;
         if (n > 1) us += kCombineUs + 2.0 * n * total * Hq * (kD + 2) * sizeof(float) / kBytesPerUs;
         if (n == 1 || us < least) {
             best = n;
