@@ -179,6 +179,7 @@ struct Walk {
     int base = -32;        // first sequence of the block in the lanes
     int before = 0, here = 0;   // items before the block, in the block
     PackedSeq s{0, 0, 0};  // this lane's sequence
+    int blocks = 0, spans = 1;  // its blocks of tokens, and spans of each
     int count = 0, incl = 0;    // its items, and the inclusive sum over the lanes
 };
 
@@ -192,8 +193,9 @@ __device__ __forceinline__ void walk_to(const Params &p, Walk &w, int base) {
         w.s = packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status);
         if (w.s.T > 0) {
             const int ntok = 2 * p.Mt;
-            w.count = (w.s.T + ntok - 1) / ntok * p.Hkv *
-                      n_spans(most_tiles(w.s.S, ntok, p.window), p.split_tiles);
+            w.blocks = (w.s.T + ntok - 1) / ntok;
+            w.spans = n_spans(most_tiles(w.s.S, ntok, p.window), p.split_tiles);
+            w.count = w.blocks * p.Hkv * w.spans;
         }
     }
     w.incl = w.count;
@@ -218,12 +220,16 @@ __device__ __forceinline__ int find_item(const Params &p, Walk &w, int idx, Item
     const int T = __shfl_sync(0xffffffffu, w.s.T, lane_s);
     const int S = __shfl_sync(0xffffffffu, w.s.S, lane_s);
     int r = rel - __shfl_sync(0xffffffffu, w.incl - w.count, lane_s);
-    const int ntok = 2 * p.Mt, blocks = (T + ntok - 1) / ntok;
-    const int spans = n_spans(most_tiles(S, ntok, p.window), p.split_tiles);
-    const int split = r % spans;
-    r /= spans;
-    it.g = r % p.Hkv;
-    const int t0 = (blocks - 1 - r / p.Hkv) * ntok;
+    const int ntok = 2 * p.Mt, blocks = __shfl_sync(0xffffffffu, w.blocks, lane_s);
+    const int spans = __shfl_sync(0xffffffffu, w.spans, lane_s);
+    int split = 0;
+    if (spans > 1) {
+        split = r % spans;
+        r /= spans;
+    }
+    const int back = r / p.Hkv;   // blocks from the last one
+    it.g = r - back * p.Hkv;
+    const int t0 = (blocks - 1 - back) * ntok;
     it.seq = w.base + lane_s;
     it.row0 = row0 + t0;
     it.ntok = min(ntok, T - t0);
@@ -1068,14 +1074,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     const int r0 = (warp & 3) * 32, c = lane & 15;
                     const int rows = min(32, min(ntok, p.Mt) * p.G - r0);
+                    const long mine = (long)row * p.o_stride + head * kD;   // this thread's row
 #pragma unroll 4
-                    for (int i = lane >> 4; i < rows; i += 2) {
-                        const int rr = r0 + i, t = rr / p.G;
+                    for (int i = 0; i < rows; i += 2) {
+                        const int ii = i + (lane >> 4), rr = r0 + ii;
+                        const long at = __shfl_sync(0xffffffffu, mine, ii);
+                        if (ii >= rows) continue;
                         const uint4 y = *reinterpret_cast<const uint4 *>(
                             stage + (c >> 3) * kBoxBytes + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
-                        *reinterpret_cast<uint4 *>(
-                            p.o + (size_t)(it.row0 + wg * p.Mt + t) * p.o_stride +
-                            (it.g * p.G + rr - t * p.G) * kD + 8 * c) = y;
+                        *reinterpret_cast<uint4 *>(p.o + at + 8 * c) = y;
                     }
                 }
                 mbar_arrive(&bars->staged[wg][ns & 1]);
