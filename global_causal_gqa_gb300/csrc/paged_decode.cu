@@ -54,7 +54,7 @@ constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kMaxRows = 16;
 constexpr int kSmemXchg = kStages * kStageBytes;
 constexpr int kSmemBar = kSmemXchg + kConsumers * kMaxRows * kD * 4;
-constexpr int kSmemBytes = kSmemBar + 1024 + 1024;
+constexpr int kSmemBytes = kSmemBar + 1536 + 1024;
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
 constexpr int kSegSlots = 4;
 constexpr int kSMs = 152;
@@ -75,11 +75,11 @@ struct Bars {
     uint64_t full[kStages], empty[kStages];
     uint64_t seg_full[kSegSlots], seg_free[kSegSlots];
     uint64_t merge;                // the consumer warps meet (a barrier with a bounded wait)
-    float2 ml[kConsumers][kMaxRows];
+    float2 ml[2][kConsumers][kMaxRows];   // of the last two pairs
     int scan[kThreads / 32];
     int start_seq, start_unit;
 };
-static_assert(sizeof(Bars) <= 1024, "barrier block");
+static_assert(sizeof(Bars) <= 1536, "barrier block");
 
 struct Params {
     const __nv_bfloat16 *q;
@@ -92,9 +92,15 @@ struct Params {
     long q_stride, o_stride;
     PackedBounds bounds;
     int nseq, Hq, Hkv, G, window, num_pages, page_size, max_pages;
+    uint32_t inv_g;                // 2^16 / G, rounded up
     int whole;                     // 1: CTAs take whole pairs, every gridDim.x-th one
     float scale_log2;
 };
+
+// r / G for a row r <= kMaxRows of a pair (the error, r / 2^16 at most, is below 1 / G).
+__device__ __forceinline__ int token_of(const Params &p, int r) {
+    return static_cast<int>(r * p.inv_g >> 16);
+}
 
 // Units of one (sequence, KV head): [first, first + count) of 64 keys each.
 __device__ __forceinline__ int first_unit(const PackedSeq &s, int window) {
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             // its queries on their way to L2: two 128-byte lines a row
             if (sg.stages > 0 && lane < 2 * sg.T * p.G) {
-                const int r = lane >> 1, t = r / p.G;
+                const int r = lane >> 1, t = token_of(p, r);
                 prefetch_l2(p.q + (long)(sg.row0 + t) * p.q_stride +
                             (sg.g * p.G + r - t * p.G) * kD + 64 * (lane & 1));
             }
@@ -348,26 +354,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 2, meets);
         return false;
     };
-    int u = 0;
-    for (int k = 0;; ++k) {
+    // Segment k and this thread's part of its queries, rows gq and gq + 8 (rows past the last
+    // one are zero).
+    Segment sg;
+    uint32_t qa[8][2 * HR];
+    auto next_segment = [&](int k) {
         const int slot = k & (kSegSlots - 1);
         if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
             set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 0, k);
-            return;
+            return false;
         }
-        const Segment sg = bars->seg[slot];
+        sg = bars->seg[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->seg_free[slot]);
-        if (sg.stages < 0) return;
-        const int rows = sg.T * p.G;              // <= ROWS (the host's rule on max_q)
-        // this thread's rows gq, gq + 8: their query and position (rows past the last one
-        // are zero queries at the last position)
-        uint32_t qa[8][2 * HR];
-        int qpos[HR];
+        const int rows = sg.stages < 0 ? 0 : sg.T * p.G;   // <= ROWS (the host's rule on max_q)
 #pragma unroll
         for (int h = 0; h < HR; ++h) {
-            const int r = gq + 8 * h, t = min(r, rows - 1) / p.G;
-            qpos[h] = sg.S - sg.T + t;
+            const int r = gq + 8 * h, t = token_of(p, r);
             const __nv_bfloat16 *qr = p.q + (long)(sg.row0 + t) * p.q_stride +
                                       (sg.g * p.G + (r - t * p.G)) * kD + 2 * tq;
 #pragma unroll
@@ -379,6 +382,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        return true;
+    };
+    if (!next_segment(0)) return;
+    int u = 0;
+    for (int k = 0; sg.stages >= 0; ++k) {
+        const int rows = sg.T * p.G;
+        int qpos[HR];   // rows past the last one: the last position
+#pragma unroll
+        for (int h = 0; h < HR; ++h)
+            qpos[h] = sg.S - sg.T + min(token_of(p, gq + 8 * h), sg.T - 1);
         const int q_first = sg.S - sg.T;          // hi_all: keys beyond are hidden from some
         const int lo = p.window > 0 ? max(0, q_first - p.window + 1) : 0;
         const int lo_all = p.window > 0 ? max(0, sg.S - p.window) : 0;
@@ -528,76 +541,68 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->empty[st]);
         }
-        // ---- the pair's (or span's) result: merge the four warps
+        // ---- the pair's (or span's) result.  The next one's queries are on their way
+        // meanwhile.
+        const int row0 = sg.row0, head0 = sg.g * p.G, out = sg.slot;
+        if (!next_segment(k + 1)) return;
+        // The warps' shares meet in shared memory, each relative to its own maximum: [warp]
+        // [row][64 pairs of dims], a row's pairs permuted so that the 16 lanes of a half warp
+        // (4 rows x 4 pairs) meet 16 different places.  Up to 8 rows there is room for two
+        // pairs' shares, and one meeting per pair keeps writers off the readers.
+        constexpr bool kTwo = ROWS <= kMaxRows / 2;
+        if (!kTwo && k > 0 && !meet()) return;
+        float2 *share = xchg + (kTwo ? (k & 1) * kConsumers * ROWS * 64 : 0);
+        float2(*ml)[kMaxRows] = bars->ml[k & 1];
 #pragma unroll
         for (int h = 0; h < HR; ++h) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (tq == 0) bars->ml[warp][gq + 8 * h] = make_float2(m[h], l[h]);
+            const int r = gq + 8 * h;
+            if (tq == 0) ml[warp][r] = make_float2(m[h], l[h]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                share[(warp * ROWS + r) * 64 + ((4 * i + tq) ^ ((r & 3) << 2))] =
+                    make_float2(o[i][2 * h], o[i][2 * h + 1]);
         }
         if (!meet()) return;
-        // the exchange: [4][16 rows][64 pairs of dims], a row's pairs permuted so that the 16
-        // lanes of a half warp (4 rows x 4 pairs) meet 16 different places
-        auto place = [&](int i, int h) {
-            return xchg + (warp * kMaxRows + gq + 8 * h) * 64 + ((4 * i + tq) ^ ((gq & 3) << 2));
-        };
-#pragma unroll
-        for (int h = 0; h < HR; ++h) {
-            float M = -CUDART_INF_F;
-#pragma unroll
-            for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, bars->ml[w][gq + 8 * h].x);
-            // this warp's outputs, relative to M (0 where it saw no key and another one did)
-            const float f = m[h] == -CUDART_INF_F && M != m[h]
-                                ? 0.f
-                                : ex2_approx(mr[h] - (M == -CUDART_INF_F ? 0.f : M));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                *place(i, h) = make_float2(o[i][2 * h] * f, o[i][2 * h + 1] * f);
-            }
-        }
-        // every thread: dims 2 dd, + 1 of every other row
-        const int dd = threadIdx.x & 63;
-        float Mr[ROWS / 2], Lr[ROWS / 2];
-#pragma unroll
-        for (int i = 0; i < ROWS / 2; ++i) {
-            const int r = (threadIdx.x >> 6) + 2 * i;
+        // a warp adds up every fourth row, 4 dims per lane
+        for (int r = warp; r < rows; r += kConsumers) {
+            float2 x[kConsumers];
+            float4 y[kConsumers];
             float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, bars->ml[w][r].x);
+            for (int w = 0; w < kConsumers; ++w) {
+                x[w] = ml[w][r];
+                y[w] = *reinterpret_cast<const float4 *>(share + (w * ROWS + r) * 64 +
+                                                         ((2 * lane) ^ ((r & 3) << 2)));
+                M = fmaxf(M, x[w].x);
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) {
-                const float2 x = bars->ml[w][r];
-                if (x.x == -CUDART_INF_F && M != x.x) L += x.y * 0.f;   // 0, or NaN
-                else L += x.y * ex2_approx(x.x == -CUDART_INF_F ? 0.f : x.x - M);
+                // a share none of whose keys this row sees: m = -inf, l = 0 and O = 0 (NaN
+                // scores alone also leave m at -inf, with l and O NaN)
+                const float f = x[w].x == -CUDART_INF_F ? (x[w].y == 0.f ? 0.f : 1.f)
+                                                        : ex2_approx(x[w].x - M);
+                L = fmaf(x[w].y, f, L);
+                acc.x = fmaf(y[w].x, f, acc.x);
+                acc.y = fmaf(y[w].y, f, acc.y);
+                acc.z = fmaf(y[w].z, f, acc.z);
+                acc.w = fmaf(y[w].w, f, acc.w);
             }
-            Mr[i] = M;
-            Lr[i] = L;
-        }
-        if (!meet()) return;
-#pragma unroll
-        for (int i = 0; i < ROWS / 2; ++i) {
-            const int r = (threadIdx.x >> 6) + 2 * i;
-            if (r >= rows) continue;
-            float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kConsumers; ++w) {
-                const float2 y = xchg[(w * kMaxRows + r) * 64 + (dd ^ ((r & 3) << 2))];
-                acc.x += y.x;
-                acc.y += y.y;
-            }
-            if (sg.slot >= 0) {
-                const size_t rec = (size_t)sg.slot * kMaxRows + r;
-                reinterpret_cast<float2 *>(p.ws_o + rec * kD)[dd] = acc;
-                if (dd == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(Mr[i], Lr[i]);
+            if (out >= 0) {
+                const size_t rec = (size_t)out * kMaxRows + r;
+                reinterpret_cast<float4 *>(p.ws_o + rec * kD)[lane] = acc;
+                if (lane == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(M, L);
             } else {
-                const int t = r / p.G, head = sg.g * p.G + r - t * p.G;
-                const long row = sg.row0 + t;
-                const float inv = 1.0f / Lr[i];
-                reinterpret_cast<uint32_t *>(p.o + row * p.o_stride + head * kD)[dd] =
-                    pack_bf16x2(acc.x * inv, acc.y * inv);
-                if (p.lse && dd == 0)
+                const int t = token_of(p, r), head = head0 + r - t * p.G;
+                const long row = row0 + t;
+                const float inv = 1.0f / L;
+                reinterpret_cast<uint2 *>(p.o + row * p.o_stride + head * kD)[lane] = make_uint2(
+                    pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                if (p.lse && lane == 0)
                     p.lse[(long)head * p.bounds.total + row] =
-                        (Mr[i] + __log2f(Lr[i])) * 0.69314718055994531f;
+                        (M + __log2f(L)) * 0.69314718055994531f;
             }
         }
     }
@@ -679,7 +684,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_decode_combine_kerne
         acc.z += y.z;
         acc.w += y.w;
     }
-    const int t = r / p.G, h = j.g * p.G + r - t * p.G;
+    const int t = token_of(p, r), h = j.g * p.G + r - t * p.G;
     const long row = j.row0 + t;
     const float inv = 1.0f / L;
     reinterpret_cast<uint2 *>(p.o + row * p.o_stride + h * kD)[lane] =
@@ -718,6 +723,7 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;
     p.G = a.Hq / a.Hkv;
+    p.inv_g = (65536 + p.G - 1) / p.G;
     p.window = a.window;
     p.num_pages = c.num_pages;
     p.page_size = c.page_size;
