@@ -75,6 +75,7 @@ struct PageWalk {
     int end;              // entries from here on are not needed (and not read)
     int base, cur, next;
 
+    PageWalk() = default;
     __device__ __forceinline__ int fetch(int i) const { return i < end ? __ldg(row + i) : -1; }
     __device__ __forceinline__ PageWalk(const int32_t *r, int first, int e) : row(r), end(e) {
         const int lane = threadIdx.x & 31;

@@ -91,7 +91,7 @@ struct Params {
     int *status;
     long q_stride, o_stride;
     PackedBounds bounds;
-    int nseq, Hq, Hkv, G, window, num_pages, page_size, max_pages;
+    int nseq, Hq, Hkv, G, window, num_pages, page_size, page_shift, max_pages;
     uint32_t inv_g;                // 2^16 / G, rounded up
     int whole;                     // 1: CTAs take whole pairs, every gridDim.x-th one
     float scale_log2;
@@ -228,73 +228,114 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bool ok = true;
         int u = 0;   // stages issued
-        int seq = bars->start_seq, off = bars->start_unit;   // off: units into the sequence
-        int pair = blockIdx.x;                               // (whole pairs)
         Joint joint{0, 0, 0, 0};
         // boxes of a stage: one per page, or per 64 keys of a longer page
         const int box = min(p.page_size, kUnit), boxes = kUnit / box;
-        for (int k = 0;; ++k) {
+        // The run as a list of items, 32 of them in the lanes at a time: sequences from the
+        // run's first one, with all their KV heads, or the CTA's whole pairs.
+        const int items = !p.whole ? p.nseq
+                                   : (p.nseq * p.Hkv - static_cast<int>(blockIdx.x) +
+                                      static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+        const int heads = p.whole ? 1 : p.Hkv;
+        int base = 0, at = 0;      // the lanes' first item; the next one among them
+        PackedSeq s{0, 0, 0};      // of this lane's item, as are the next three
+        int s_seq = 0, s_head = 0, s_units = 0;
+        auto load_items = [&](int first) {
+            base = first;
+            at = 0;
+            s_units = 0;
+            const int i = base + lane;
+            if (i < items) {
+                const int pair = p.whole ? static_cast<int>(blockIdx.x + i * gridDim.x) : 0;
+                s_seq = p.whole ? pair / p.Hkv : i;
+                s_head = p.whole ? pair - s_seq * p.Hkv : 0;
+                s = packed_seq(p.cu, p.kv_lens, s_seq, p.bounds, p.whole ? p.status : nullptr);
+                s_units = count_units(s, p.window);
+            }
+        };
+        int head = 0, in = 0;      // the next pair's head within its item, units into it
+        if (p.whole) {
+            run = 0x7fffffff;
+            load_items(0);
+        } else if (run > 0) {
+            load_items(bars->start_seq);
+            const int n = __shfl_sync(0xffffffffu, s_units, 0);
+            head = bars->start_unit / n;
+            in = bars->start_unit - head * n;
+        }
+        auto next_segment = [&]() {
             Segment sg;
             sg.stages = -1;
-            while (p.whole ? pair < p.nseq * p.Hkv : run > 0) {
-                if (p.whole) seq = pair / p.Hkv;
-                const PackedSeq s = packed_seq(p.cu, p.kv_lens, seq, p.bounds,
-                                               p.whole && lane == 0 ? p.status : nullptr);
-                const int n = count_units(s, p.window);
-                if (p.whole) {
-                    off = n * (pair - seq * p.Hkv);
-                    run = n;
-                    pair += gridDim.x;
-                    if (n == 0) continue;
-                } else if (off >= n * p.Hkv) {
-                    ++seq;   // run > 0: a later sequence has units
-                    off = 0;
-                    continue;
-                }
-                sg.row0 = s.row0;
-                sg.T = s.T;
-                sg.S = s.S;
-                sg.seq = seq;
-                sg.g = off / n;
-                const int in = off - sg.g * n;
-                sg.unit0 = first_unit(s, p.window) + in;
-                sg.stages = min(run, n - in);
-                sg.slot = sg.stages == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (in == 0 ? 1 : 0);
-                off += sg.stages;
-                run -= sg.stages;
-                if (in == 0 && sg.stages < n)   // the rest of the pair's units, per CTA
-                    joint = {s.row0, sg.g, s.T * p.G, 1 + (n - sg.stages + per - 1) / per};
-                break;
+            uint32_t with = 0;     // items with work, from the next one on
+            while (run > 0) {
+                with = at < 32 ? __ballot_sync(0xffffffffu, s_units > 0) >> at << at : 0u;
+                if (with || base + 32 >= items) break;
+                load_items(base + 32);
             }
+            if (!with) return sg;
+            const int l = __ffs(with) - 1;
+            at = l;
+            const int n = __shfl_sync(0xffffffffu, s_units, l);
+            sg.row0 = __shfl_sync(0xffffffffu, s.row0, l);
+            sg.T = __shfl_sync(0xffffffffu, s.T, l);
+            sg.S = __shfl_sync(0xffffffffu, s.S, l);
+            sg.seq = __shfl_sync(0xffffffffu, s_seq, l);
+            sg.g = __shfl_sync(0xffffffffu, s_head, l) + head;
+            sg.unit0 = (p.window > 0 ? max(0, sg.S - sg.T - p.window + 1) / kUnit : 0) + in;
+            sg.stages = min(run, n - in);
+            sg.slot = sg.stages == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (in == 0 ? 1 : 0);
+            if (in == 0 && sg.stages < n)   // the rest of the pair's units, per CTA
+                joint = {sg.row0, sg.g, sg.T * p.G, 1 + (n - sg.stages + per - 1) / per};
+            if (!p.whole) run -= sg.stages;
+            in += sg.stages;
+            if (in == n) {
+                in = 0;
+                if (++head == heads) {
+                    head = 0;
+                    ++at;
+                }
+            }
+            return sg;
+        };
+        // The segment after the last one: its record out, its page entries on their way.
+        Segment ahead;
+        PageWalk walk_ahead;
+        int k = 0;
+        auto advance = [&]() {
+            ahead = next_segment();
             const int slot = k & (kSegSlots - 1);
             if (k >= kSegSlots && !warp_wait(&bars->seg_free[slot], (k / kSegSlots - 1) & 1)) {
                 set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 0, k);
                 ok = false;
-                break;
+                return;
             }
             if (lane == 0) {
-                bars->seg[slot] = sg;
+                bars->seg[slot] = ahead;
                 mbar_arrive(&bars->seg_full[slot]);
             }
             __syncwarp();
+            ++k;
+            if (ahead.stages < 0) return;
+            walk_ahead = PageWalk(p.pages + (long)ahead.seq * p.max_pages,
+                                  ahead.unit0 * kUnit >> p.page_shift,
+                                  (ahead.S - 1 >> p.page_shift) + 1);
             // its queries on their way to L2: two 128-byte lines a row
-            if (sg.stages > 0 && lane < 2 * sg.T * p.G) {
+            if (lane < 2 * ahead.T * p.G) {
                 const int r = lane >> 1, t = token_of(p, r);
-                prefetch_l2(p.q + (long)(sg.row0 + t) * p.q_stride +
-                            (sg.g * p.G + r - t * p.G) * kD + 64 * (lane & 1));
+                prefetch_l2(p.q + (long)(ahead.row0 + t) * p.q_stride +
+                            (ahead.g * p.G + r - t * p.G) * kD + 64 * (lane & 1));
             }
-            if (sg.stages < 0) {
-                if (!p.whole && lane == 0) p.ws_joint[blockIdx.x] = joint;
-                break;
-            }
+        };
+        advance();
+        Segment sg = ahead;
+        PageWalk walk = walk_ahead;
+        auto load = [&]() {
             const int lo = p.window > 0 ? max(0, sg.S - sg.T - p.window + 1) : 0;
-            PageWalk pages(p.pages + (long)sg.seq * p.max_pages, sg.unit0 * kUnit / p.page_size,
-                           (sg.S - 1) / p.page_size + 1);
             for (int j = 0; j < sg.stages; ++j, ++u) {
                 // the slab of this lane's box; -1 for one that no row sees or that is not in
                 // the pool (its box is zero fill)
                 const int unit_key = (sg.unit0 + j) * kUnit;
-                const int pg = pages.get(unit_key / p.page_size, boxes);
+                const int pg = walk.get(unit_key >> p.page_shift, boxes);
                 const int key0 = unit_key + lane * box;
                 int slab = -1;
                 if (lane < boxes && key0 < sg.S && key0 + box > lo) {
@@ -305,20 +346,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (u >= kStages && !warp_wait(&bars->empty[st], (u / kStages - 1) & 1)) {
                     set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 1, u);
                     ok = false;
-                    break;
+                    return;
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], kStageBytes);
                 __syncwarp();
                 if (lane < boxes) {
                     uint8_t *dst = smem + st * kStageBytes + lane * box * kD * 2;
-                    const int row = p.page_size > kUnit ? unit_key % p.page_size : 0;
+                    const int row = unit_key & (p.page_size - 1);
                     tma_load_4d(dst, &tmK, &bars->full[st], 0, row, 0, slab);
                     tma_load_4d(dst + kTileBytes, &tmV, &bars->full[st], 0, row, 0, slab);
                 }
                 __syncwarp();
             }
-            if (!ok) break;
+        };
+        // A segment is looked up ahead of the loads of the one before it, the second one after
+        // the first one's, which wait for nothing that they can do without.
+#pragma unroll 1
+        for (int turn = 0; ok && ahead.stages >= 0; ++turn) {
+            sg = ahead;
+            walk = walk_ahead;
+#pragma unroll 1
+            for (int part = 0; part < 2 && ok; ++part) {
+                if ((part == 0) == (turn == 0)) load();
+                else advance();
+            }
         }
+        if (ok && !p.whole && lane == 0) p.ws_joint[blockIdx.x] = joint;
         if (!ok)   // never leave the CTA with copies in flight
             for (int w = max(0, u - kStages); w < u; ++w)
                 mbar_wait(&bars->full[w % kStages], (w / kStages) & 1);
@@ -727,6 +780,7 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
     p.window = a.window;
     p.num_pages = c.num_pages;
     p.page_size = c.page_size;
+    p.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
     p.max_pages = c.max_pages;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.whole = whole_pairs(a.max_kv);
