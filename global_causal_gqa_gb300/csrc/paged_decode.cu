@@ -143,6 +143,13 @@ __device__ __forceinline__ bool strip_nonfinite(uint32_t &w) {
     return lo || hi;
 }
 
+// The transpose of an 8 x 8 matrix of 16-bit values, a row in four lanes.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
@@ -382,22 +389,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int gq = lane >> 2, tq = lane & 3;
     constexpr int HR = ROWS / 8;                  // row halves in use
     const uint32_t ring = smem_u32(smem);
-    float2 *xchg = reinterpret_cast<float2 *>(smem + kSmemXchg);
-    // ldmatrix rows: K: matrices (keys 0-7 | 8-15) x (chunk 2ks | 2ks + 1); V transposed:
-    // (dim chunk 2nn | 2nn + 1) x (keys 0-7 | 8-15)
+    float *xchg = reinterpret_cast<float *>(smem + kSmemXchg);
+    // ldmatrix rows, both operands A: K: matrices (chunk 2ks | 2ks + 1) x (keys 0-7 | 8-15);
+    // V transposed: (keys 0-7 | 8-15) x (dim chunk 2nn | 2nn + 1)
     const int mat = lane >> 3, l7 = lane & 7;
     const int box = min(p.page_size, kUnit);
     const uint32_t half = box * 128;          // a box: its rows' dims 0-63, then 64-127
     const int part = 16 * warp;               // first of this warp's keys in a stage
     const uint32_t rows16 = part / box * 2 * half + part % box * 128;
-    const uint32_t k_row = rows16 + (((mat >> 1) << 3) + l7) * 128;
-    const uint32_t v_row = kTileBytes + rows16 + (((mat & 1) << 3) + l7) * 128;
-    // swizzled place of chunk 2i (+ 1 for the odd matrices) of a half, i = 0..3
+    const uint32_t k_row = rows16 + (((mat & 1) << 3) + l7) * 128;
+    const uint32_t v_row = kTileBytes + rows16 + (((mat >> 1) << 3) + l7) * 128;
+    // swizzled place of chunk 2i (or 2i + 1) of a half, i = 0..3
     uint32_t k_off[4], v_off[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        k_off[i] = k_row + (((2 * i + (mat & 1)) ^ l7) << 4);
-        v_off[i] = v_row + (((2 * i + (mat >> 1)) ^ l7) << 4);
+        k_off[i] = k_row + (((2 * i + (mat >> 1)) ^ l7) << 4);
+        v_off[i] = v_row + (((2 * i + (mat & 1)) ^ l7) << 4);
     }
     int meets = 0;
     auto meet = [&]() {
@@ -410,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Segment k and this thread's part of its queries, rows gq and gq + 8 (rows past the last
     // one are zero).
     Segment sg;
-    uint32_t qa[8][2 * HR];
+    uint32_t qb[8][2 * HR];
     auto next_segment = [&](int k) {
         const int slot = k & (kSegSlots - 1);
         if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
@@ -428,10 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       (sg.g * p.G + (r - t * p.G)) * kD + 2 * tq;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
-                qa[ks][h] = qa[ks][HR + h] = 0u;
+                qb[ks][h] = qb[ks][HR + h] = 0u;
                 if (r < rows) {
-                    qa[ks][h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks));
-                    qa[ks][HR + h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks + 8));
+                    qb[ks][h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks));
+                    qb[ks][HR + h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks + 8));
                 }
             }
         }
@@ -441,22 +448,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     int u = 0;
     for (int k = 0; sg.stages >= 0; ++k) {
         const int rows = sg.T * p.G;
-        int qpos[HR];   // rows past the last one: the last position
+        // this thread's columns of the products: rows 8h + 2tq, + 1 (positions of rows past the
+        // last one: the last)
+        int qpos[HR][2];
 #pragma unroll
         for (int h = 0; h < HR; ++h)
-            qpos[h] = sg.S - sg.T + min(token_of(p, gq + 8 * h), sg.T - 1);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                qpos[h][c] = sg.S - sg.T + min(token_of(p, 8 * h + 2 * tq + c), sg.T - 1);
         const int q_first = sg.S - sg.T;          // hi_all: keys beyond are hidden from some
         const int lo = p.window > 0 ? max(0, q_first - p.window + 1) : 0;
         const int lo_all = p.window > 0 ? max(0, sg.S - p.window) : 0;
-        float o[16][4];
+        // o[i][h]: dims 16 i + gq (+ 8 for the second pair) of those rows
+        float o[8][HR][4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float m[HR], mr[HR], l[HR];               // mr: m, or 0 while m is -inf
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int h = 0; h < HR; ++h) {
-            m[h] = -CUDART_INF_F;
-            mr[h] = l[h] = 0.f;
-        }
+            for (int h = 0; h < HR; ++h) o[i][h][0] = o[i][h][1] = o[i][h][2] = o[i][h][3] = 0.f;
+        float m[HR][2], mr[HR][2], l[HR][2];      // mr: m, or 0 while m is -inf
+#pragma unroll
+        for (int h = 0; h < HR; ++h)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                m[h][c] = -CUDART_INF_F;
+                mr[h][c] = l[h][c] = 0.f;
+            }
         for (int j = 0; j < sg.stages; ++j, ++u) {
             const int st = u % kStages;
             if (!warp_wait(&bars->full[st], (u / kStages) & 1)) {
@@ -466,81 +482,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int kb = (sg.unit0 + j) * kUnit + part;   // this warp's 16 keys
             if (kb < sg.S && kb + 15 >= lo) {
                 const uint32_t base = ring + st * kStageBytes;
-                // ---- scores: rows x 16 keys, two chains per 8 keys
-                float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-                float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
+                // ---- scores: 16 keys x rows, in chains of four products
+                constexpr int kChains = 2;
+                float x[HR][4], xs[kChains][HR][4];
+#pragma unroll
+                for (int h = 0; h < HR; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int c = 0; c < kChains; ++c) xs[c][h][e] = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
-                    uint32_t b[4];
-                    ldsm4(b, (ks < 4 ? base : base + half) + k_off[ks & 3]);
-                    const uint32_t a0 = qa[ks][0], a1 = HR > 1 ? qa[ks][1] : 0u;
-                    const uint32_t a2 = qa[ks][HR], a3 = HR > 1 ? qa[ks][HR + 1] : 0u;
-                    mma16816(ks & 1 ? t0 : s0, a0, a1, a2, a3, b[0], b[1]);
-                    mma16816(ks & 1 ? t1 : s1, a0, a1, a2, a3, b[2], b[3]);
-                }
-                // x[h]: row gq + 8h, keys kb + 2tq, + 1, kb + 8 + 2tq, + 1
-                float x[HR][4];
+                    uint32_t a[4];
+                    ldsm4(a, (ks < 4 ? base : base + half) + k_off[ks & 3]);
 #pragma unroll
-                for (int h = 0; h < HR; ++h) {
-                    x[h][0] = s0[2 * h] + t0[2 * h];
-                    x[h][1] = s0[2 * h + 1] + t0[2 * h + 1];
-                    x[h][2] = s1[2 * h] + t1[2 * h];
-                    x[h][3] = s1[2 * h + 1] + t1[2 * h + 1];
+                    for (int h = 0; h < HR; ++h)
+                        mma16816(xs[ks % kChains][h], a[0], a[1], a[2], a[3], qb[ks][h], qb[ks][HR + h]);
                 }
+                // x[h]: keys kb + gq (rows 8h + 2tq, + 1), kb + gq + 8 (the same rows)
+#pragma unroll
+                for (int h = 0; h < HR; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[h][e] = xs[0][h][e] + xs[1][h][e];
                 const bool edge = kb + 15 > q_first || kb < lo_all;   // of the mask
                 if (edge) {
 #pragma unroll
                     for (int h = 0; h < HR; ++h)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int key = kb + 2 * tq + (e & 1) + 8 * (e >> 1);
-                            if (key > qpos[h] || (p.window > 0 && qpos[h] - key >= p.window))
+                            const int key = kb + gq + 8 * (e >> 1), at = qpos[h][e & 1];
+                            if (key > at || (p.window > 0 && at - key >= p.window))
                                 x[h][e] = -CUDART_INF_F;
                         }
                 }
                 // ---- online softmax: the maximum moves only when a score exceeds it by 2^8
                 bool grow = false;
 #pragma unroll
-                for (int h = 0; h < HR; ++h) {
-                    const float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
-                    grow |= mx * p.scale_log2 > m[h] + kRescaleThreshold;
-                }
+                for (int h = 0; h < HR; ++h)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        grow |= fmaxf(x[h][c], x[h][2 + c]) * p.scale_log2 >
+                                m[h][c] + kRescaleThreshold;
                 if (__any_sync(0xffffffffu, grow)) {
-                    float f[HR];
 #pragma unroll
-                    for (int h = 0; h < HR; ++h) {
-                        float mx = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        const float mn = fmaxf(m[h], mx * p.scale_log2);
-                        f[h] = m[h] == -CUDART_INF_F ? 0.f : ex2_approx(m[h] - mn);
-                        m[h] = mn;
-                        mr[h] = mn == -CUDART_INF_F ? 0.f : mn;
-                        l[h] *= f[h];
-                    }
+                    for (int h = 0; h < HR; ++h)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
+                        for (int c = 0; c < 2; ++c) {
+                            float mx = fmaxf(x[h][c], x[h][2 + c]);
 #pragma unroll
-                        for (int h = 0; h < HR; ++h) {
-                            o[i][2 * h] *= f[h];
-                            o[i][2 * h + 1] *= f[h];
+                            for (int d = 4; d < 32; d <<= 1)
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                            const float mn = fmaxf(m[h][c], mx * p.scale_log2);
+                            const float f =
+                                m[h][c] == -CUDART_INF_F ? 0.f : ex2_approx(m[h][c] - mn);
+                            m[h][c] = mn;
+                            mr[h][c] = mn == -CUDART_INF_F ? 0.f : mn;
+                            l[h][c] *= f;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                o[i][h][c] *= f;
+                                o[i][h][2 + c] *= f;
+                            }
                         }
                 }
-                // P as the A operand: rows gq (+ 8), keys 2tq, + 1 and 8 + 2tq, + 1; the sum
-                // takes the unrounded weights
-                uint32_t pa[4] = {0u, 0u, 0u, 0u};
+                // P as the B operand: row gq of half h, keys 2tq, + 1 and 8 + 2tq, + 1; the
+                // sum takes the unrounded weights
+                uint32_t pb[HR][2];
 #pragma unroll
                 for (int h = 0; h < HR; ++h) {
-                    const float e0 = ex2_approx(fmaf(x[h][0], p.scale_log2, -mr[h]));
-                    const float e1 = ex2_approx(fmaf(x[h][1], p.scale_log2, -mr[h]));
-                    const float e2 = ex2_approx(fmaf(x[h][2], p.scale_log2, -mr[h]));
-                    const float e3 = ex2_approx(fmaf(x[h][3], p.scale_log2, -mr[h]));
-                    l[h] += (e0 + e1) + (e2 + e3);
-                    pa[h] = pack_bf16x2(e0, e1);
-                    pa[2 + h] = pack_bf16x2(e2, e3);
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = ex2_approx(fmaf(x[h][e], p.scale_log2, -mr[h][e & 1]));
+                    l[h][0] += w[0] + w[2];
+                    l[h][1] += w[1] + w[3];
+                    pb[h][0] = transpose8x8(pack_bf16x2(w[0], w[1]));
+                    pb[h][1] = transpose8x8(pack_bf16x2(w[2], w[3]));
                 }
-                // ---- O += P V
-                // masks of the B fragment's keys 2tq, + 1 (and + 8): those that some row sees
+                // ---- O += V^T P
+                // masks of the A fragment's keys 2tq, + 1 (and + 8): those that some row sees
                 uint32_t seen0 = 0xffffffffu, seen1 = 0xffffffffu;
                 if (edge) {
                     const int ka = kb + 2 * tq;
@@ -551,43 +571,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool stripped = false;
 #pragma unroll
                 for (int nn = 0; nn < 8; ++nn) {
-                    uint32_t b[4];
-                    ldsm4_trans(b, (nn < 4 ? base : base + half) + v_off[nn & 3]);
+                    uint32_t a[4];
+                    ldsm4_trans(a, (nn < 4 ? base : base + half) + v_off[nn & 3]);
                     if (edge) {
-                        b[0] &= seen0;
-                        b[1] &= seen1;
-                        b[2] &= seen0;
-                        b[3] &= seen1;
+                        a[0] &= seen0;
+                        a[1] &= seen0;
+                        a[2] &= seen1;
+                        a[3] &= seen1;
                         if (sg.T > 1) {   // some of the block's keys are hidden from some rows
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) stripped |= strip_nonfinite(b[i]);
+                            for (int i = 0; i < 4; ++i) stripped |= strip_nonfinite(a[i]);
                         }
                     }
-                    mma16816(o[2 * nn], pa[0], pa[1], pa[2], pa[3], b[0], b[1]);
-                    mma16816(o[2 * nn + 1], pa[0], pa[1], pa[2], pa[3], b[2], b[3]);
+#pragma unroll
+                    for (int h = 0; h < HR; ++h)
+                        mma16816(o[nn][h], a[0], a[1], a[2], a[3], pb[h][0], pb[h][1]);
                 }
                 if (__any_sync(0xffffffffu, stripped)) {
-                    // add what was taken out to the rows that see it: this thread's elements
-                    // are rows gq (+ 8), dims 8 i + 2 tq, + 1
+                    // add what was taken out to the rows that see it
                     for (int kk = 0; kk < 16; ++kk) {
                         const int key = kb + kk;
                         if (key < lo || key >= sg.S) continue;
                         const uint8_t *vr = smem + st * kStageBytes + kTileBytes + rows16 +
-                                            kk * 128 + 4 * tq;
+                                            kk * 128 + 2 * gq;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                                vr + (i >> 3) * half + (((i & 7) ^ (kk & 7)) << 4));
+                        for (int i = 0; i < 8; ++i)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float y = e ? bf16hi(w) : bf16lo(w);
+                                const uint32_t w = *reinterpret_cast<const uint16_t *>(
+                                    vr + (i >> 2) * half + (((2 * (i & 3) + e) ^ (kk & 7)) << 4));
+                                const float y = bf16lo(w);
                                 if (isfinite(y)) continue;
 #pragma unroll
                                 for (int h = 0; h < HR; ++h)
-                                    if (key <= qpos[h] && (p.window <= 0 || qpos[h] - key < p.window))
-                                        o[i][2 * h + e] += y;
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c)
+                                        if (key <= qpos[h][c] &&
+                                            (p.window <= 0 || qpos[h][c] - key < p.window))
+                                            o[i][h][2 * e + c] += y;
                             }
-                        }
                     }
                 }
             }
@@ -599,24 +621,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row0 = sg.row0, head0 = sg.g * p.G, out = sg.slot;
         if (!next_segment(k + 1)) return;
         // The warps' shares meet in shared memory, each relative to its own maximum: [warp]
-        // [row][64 pairs of dims], a row's pairs permuted so that the 16 lanes of a half warp
-        // (4 rows x 4 pairs) meet 16 different places.  Up to 8 rows there is room for two
-        // pairs' shares, and one meeting per pair keeps writers off the readers.
+        // [row][128 dims], a row's dims permuted so that the lanes (4 rows x 8 dims) meet 32
+        // different banks.  Up to 8 rows there is room for two pairs' shares, and one meeting
+        // per pair keeps writers off the readers.
         constexpr bool kTwo = ROWS <= kMaxRows / 2;
         if (!kTwo && k > 0 && !meet()) return;
-        float2 *share = xchg + (kTwo ? (k & 1) * kConsumers * ROWS * 64 : 0);
+        float *share = xchg + (kTwo ? (k & 1) * kConsumers * ROWS * kD : 0);
         float2(*ml)[kMaxRows] = bars->ml[k & 1];
 #pragma unroll
-        for (int h = 0; h < HR; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            const int r = gq + 8 * h;
-            if (tq == 0) ml[warp][r] = make_float2(m[h], l[h]);
+        for (int h = 0; h < HR; ++h)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                share[(warp * ROWS + r) * 64 + ((4 * i + tq) ^ ((r & 3) << 2))] =
-                    make_float2(o[i][2 * h], o[i][2 * h + 1]);
-        }
+            for (int c = 0; c < 2; ++c) {
+                const int r = 8 * h + 2 * tq + c;
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[h][c] += __shfl_xor_sync(0xffffffffu, l[h][c], d);
+                if (gq == 0) ml[warp][r] = make_float2(m[h][c], l[h][c]);
+                float *mine = share + (warp * ROWS + r) * kD;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    mine[(16 * i + gq) ^ (tq << 3)] = o[i][h][c];
+                    mine[(16 * i + 8 + gq) ^ (tq << 3)] = o[i][h][2 + c];
+                }
+            }
         if (!meet()) return;
         // a warp adds up every fourth row, 4 dims per lane
         for (int r = warp; r < rows; r += kConsumers) {
@@ -626,8 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) {
                 x[w] = ml[w][r];
-                y[w] = *reinterpret_cast<const float4 *>(share + (w * ROWS + r) * 64 +
-                                                         ((2 * lane) ^ ((r & 3) << 2)));
+                y[w] = *reinterpret_cast<const float4 *>(share + (w * ROWS + r) * kD +
+                                                         ((4 * lane) ^ ((r >> 1 & 3) << 3)));
                 M = fmaxf(M, x[w].x);
             }
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
