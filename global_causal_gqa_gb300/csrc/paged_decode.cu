@@ -49,8 +49,11 @@ constexpr int kUnit = 64;                       // keys of a stage
 constexpr int kStages = 6;
 constexpr int kTileBytes = kUnit * kD * 2;      // K or V of a stage
 constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kConsumers = 4;                   // warps, 16 keys of a stage each
-constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kConsumers = 4;                   // warps of a group, 16 keys of a stage each
+// groups of consumers, which take the pairs in turn (16 rows: 204 registers allow one)
+constexpr int n_groups(int rows) { return rows <= 8 ? 2 : 1; }
+constexpr int n_threads(int rows) { return 32 * (n_groups(rows) * kConsumers + 1); }
+constexpr int kMaxGroups = 2;
 constexpr int kMaxRows = 16;
 constexpr int kSmemXchg = kStages * kStageBytes;
 constexpr int kSmemBar = kSmemXchg + kConsumers * kMaxRows * kD * 4;
@@ -62,6 +65,7 @@ constexpr int kSMs = 152;
 // A run of stages of one (sequence, KV head).  stages < 0: no more.
 struct Segment {
     int row0, T, S, seq, g, unit0, stages;
+    int u0;     // stages of the CTA's run before it
     int slot;   // -1: all of the pair's keys; else the partial's place
 };
 
@@ -72,11 +76,12 @@ struct Joint {
 
 struct Bars {
     Segment seg[kSegSlots];
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kMaxGroups][kStages];   // a stage's load, for the group that takes it
+    uint64_t empty[kStages];
     uint64_t seg_full[kSegSlots], seg_free[kSegSlots];
-    uint64_t merge;                // the consumer warps meet (a barrier with a bounded wait)
-    float2 ml[2][kConsumers][kMaxRows];   // of the last two pairs
-    int scan[kThreads / 32];
+    uint64_t merge[kMaxGroups];    // a group's warps meet (a barrier with a bounded wait)
+    float2 ml[kMaxGroups][kConsumers][kMaxRows];
+    int scan[n_threads(1) / 32];
     int start_seq, start_unit;
 };
 static_assert(sizeof(Bars) <= 1536, "barrier block");
@@ -158,7 +163,7 @@ enum Role { kRoleProducer = 0, kRoleConsumer = 2 };
 
 // ROWS: 8 or 16 rows of the MMA in use (8: the upper half is zero and costs no exponentials).
 template <int ROWS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(n_threads(ROWS), 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const Params p) {
     griddep_wait();
@@ -168,17 +173,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     Bars *bars = reinterpret_cast<Bars *>(smem + kSmemBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kGroups = n_groups(ROWS), kThreads = n_threads(ROWS);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bars->full[i], 1);
+            for (int g = 0; g < kGroups; ++g) mbar_init(&bars->full[g][i], kUnit / min(p.page_size, kUnit));
             mbar_init(&bars->empty[i], kConsumers);
         }
         for (int i = 0; i < kSegSlots; ++i) {
             mbar_init(&bars->seg_full[i], 1);
             mbar_init(&bars->seg_free[i], kConsumers);
         }
-        mbar_init(&bars->merge, kConsumers);
+        for (int g = 0; g < kGroups; ++g) mbar_init(&bars->merge[g], kConsumers);
         fence_mbar_init();
     }
     // ---- this CTA's run of units
@@ -227,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
     }
 
-    if (warp == kConsumers) {
+    if (warp == kGroups * kConsumers) {
         // ================= producer =================
         if (lane == 0) {
             tma_prefetch_desc(&tmK);
@@ -235,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bool ok = true;
         int u = 0;   // stages issued
+        uint32_t owner = 0, phases = 0;   // a place's last group; bits 8 group + place: full's
         Joint joint{0, 0, 0, 0};
         // boxes of a stage: one per page, or per 64 keys of a longer page
         const int box = min(p.page_size, kUnit), boxes = kUnit / box;
@@ -260,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s_units = count_units(s, p.window);
             }
         };
+        int listed = 0;            // stages of the segments so far
         int head = 0, in = 0;      // the next pair's head within its item, units into it
         if (p.whole) {
             run = 0x7fffffff;
@@ -290,6 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             sg.g = __shfl_sync(0xffffffffu, s_head, l) + head;
             sg.unit0 = (p.window > 0 ? max(0, sg.S - sg.T - p.window + 1) / kUnit : 0) + in;
             sg.stages = min(run, n - in);
+            sg.u0 = listed;
+            listed += sg.stages;
             sg.slot = sg.stages == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (in == 0 ? 1 : 0);
             if (in == 0 && sg.stages < n)   // the rest of the pair's units, per CTA
                 joint = {sg.row0, sg.g, sg.T * p.G, 1 + (n - sg.stages + per - 1) / per};
@@ -304,24 +314,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return sg;
         };
-        // The segment after the last one: its record out, its page entries on their way.
+        // The segment after the last one: its record out, its page entries on their way.  The
+        // end is a record for each group.
         Segment ahead;
         PageWalk walk_ahead;
         int k = 0;
         auto advance = [&]() {
             ahead = next_segment();
-            const int slot = k & (kSegSlots - 1);
-            if (k >= kSegSlots && !warp_wait(&bars->seg_free[slot], (k / kSegSlots - 1) & 1)) {
-                set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 0, k);
-                ok = false;
-                return;
+            const int records = ahead.stages < 0 ? kGroups : 1;
+            for (int i = 0; i < records; ++i, ++k) {
+                const int slot = k & (kSegSlots - 1);
+                if (k >= kSegSlots && !warp_wait(&bars->seg_free[slot], (k / kSegSlots - 1) & 1)) {
+                    set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 0, k);
+                    ok = false;
+                    return;
+                }
+                if (lane == 0) {
+                    bars->seg[slot] = ahead;
+                    mbar_arrive(&bars->seg_full[slot]);
+                }
+                __syncwarp();
             }
-            if (lane == 0) {
-                bars->seg[slot] = ahead;
-                mbar_arrive(&bars->seg_full[slot]);
-            }
-            __syncwarp();
-            ++k;
             if (ahead.stages < 0) return;
             walk_ahead = PageWalk(p.pages + (long)ahead.seq * p.max_pages,
                                   ahead.unit0 * kUnit >> p.page_shift,
@@ -336,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         advance();
         Segment sg = ahead;
         PageWalk walk = walk_ahead;
-        auto load = [&]() {
+        auto load = [&](int group) {
             const int lo = p.window > 0 ? max(0, sg.S - sg.T - p.window + 1) : 0;
             for (int j = 0; j < sg.stages; ++j, ++u) {
                 // the slab of this lane's box; -1 for one that no row sees or that is not in
@@ -350,20 +363,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else set_status(p.status, GQA_ERR_INVALID_ARG);
                 }
                 const int st = u % kStages;
-                if (u >= kStages && !warp_wait(&bars->empty[st], (u / kStages - 1) & 1)) {
+                uint64_t *full = &bars->full[group][st];
+                uint8_t *dst = smem + st * kStageBytes + lane * box * kD * 2;
+                const int row = unit_key & (p.page_size - 1);
+                // every lane with a box waits, announces its bytes and loads for itself
+                const bool free = u < kStages || mbar_wait(&bars->empty[st], (u / kStages - 1) & 1);
+                if (free && lane < boxes) {
+                    mbar_arrive_expect_tx(full, 2 * box * kD * 2);
+                    tma_load_4d(dst, &tmK, full, 0, row, 0, slab);
+                    tma_load_4d(dst + kTileBytes, &tmV, full, 0, row, 0, slab);
+                }
+                if (!__all_sync(0xffffffffu, free)) {
                     set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 1, u);
                     ok = false;
                     return;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], kStageBytes);
-                __syncwarp();
-                if (lane < boxes) {
-                    uint8_t *dst = smem + st * kStageBytes + lane * box * kD * 2;
-                    const int row = unit_key & (p.page_size - 1);
-                    tma_load_4d(dst, &tmK, &bars->full[st], 0, row, 0, slab);
-                    tma_load_4d(dst + kTileBytes, &tmV, &bars->full[st], 0, row, 0, slab);
-                }
-                __syncwarp();
+                owner = (owner & ~(1u << st)) | group << st;
+                phases ^= 1u << (8 * group + st);
             }
         };
         // A segment is looked up ahead of the loads of the one before it, the second one after
@@ -374,14 +390,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             walk = walk_ahead;
 #pragma unroll 1
             for (int part = 0; part < 2 && ok; ++part) {
-                if ((part == 0) == (turn == 0)) load();
+                if ((part == 0) == (turn == 0)) load(turn % kGroups);
                 else advance();
             }
         }
         if (ok && !p.whole && lane == 0) p.ws_joint[blockIdx.x] = joint;
         if (!ok)   // never leave the CTA with copies in flight
-            for (int w = max(0, u - kStages); w < u; ++w)
-                mbar_wait(&bars->full[w % kStages], (w / kStages) & 1);
+            for (int st = 0; st < min(u, kStages); ++st) {
+                const int group = owner >> st & 1;
+                mbar_wait(&bars->full[group][st], (phases >> (8 * group + st) & 1) ^ 1);
+            }
         return;
     }
 
@@ -389,13 +407,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int gq = lane >> 2, tq = lane & 3;
     constexpr int HR = ROWS / 8;                  // row halves in use
     const uint32_t ring = smem_u32(smem);
-    float *xchg = reinterpret_cast<float *>(smem + kSmemXchg);
+    const int group = warp / kConsumers, cw = warp % kConsumers;
+    float *xchg = reinterpret_cast<float *>(smem + kSmemXchg) + group * kConsumers * ROWS * kD;
+    float2(*ml)[kMaxRows] = bars->ml[group];
     // ldmatrix rows, both operands A: K: matrices (chunk 2ks | 2ks + 1) x (keys 0-7 | 8-15);
     // V transposed: (keys 0-7 | 8-15) x (dim chunk 2nn | 2nn + 1)
     const int mat = lane >> 3, l7 = lane & 7;
     const int box = min(p.page_size, kUnit);
     const uint32_t half = box * 128;          // a box: its rows' dims 0-63, then 64-127
-    const int part = 16 * warp;               // first of this warp's keys in a stage
+    const int part = 16 * cw;                 // first of this warp's keys in a stage
     const uint32_t rows16 = part / box * 2 * half + part % box * 128;
     const uint32_t k_row = rows16 + (((mat & 1) << 3) + l7) * 128;
     const uint32_t v_row = kTileBytes + rows16 + (((mat >> 1) << 3) + l7) * 128;
@@ -409,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int meets = 0;
     auto meet = [&]() {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->merge);
-        if (warp_wait(&bars->merge, meets++ & 1)) return true;
+        if (lane == 0) mbar_arrive(&bars->merge[group]);
+        if (warp_wait(&bars->merge[group], meets++ & 1)) return true;
         set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 2, meets);
         return false;
     };
@@ -444,9 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
     };
-    if (!next_segment(0)) return;
-    int u = 0;
-    for (int k = 0; sg.stages >= 0; ++k) {
+    if (!next_segment(group)) return;
+    uint32_t phases = 0;   // of the group's full barriers, a bit each
+    for (int k = group; sg.stages >= 0; k += kGroups) {
         const int rows = sg.T * p.G;
         // this thread's columns of the products: rows 8h + 2tq, + 1 (positions of rows past the
         // last one: the last)
@@ -473,12 +493,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m[h][c] = -CUDART_INF_F;
                 mr[h][c] = l[h][c] = 0.f;
             }
-        for (int j = 0; j < sg.stages; ++j, ++u) {
+        for (int j = 0, u = sg.u0; j < sg.stages; ++j, ++u) {
             const int st = u % kStages;
-            if (!warp_wait(&bars->full[st], (u / kStages) & 1)) {
+            if (!warp_wait(&bars->full[group][st], phases >> st & 1)) {
                 set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 1, u);
                 return;
             }
+            phases ^= 1u << st;
             const int kb = (sg.unit0 + j) * kUnit + part;   // this warp's 16 keys
             if (kb < sg.S && kb + 15 >= lo) {
                 const uint32_t base = ring + st * kStageBytes;
@@ -619,15 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- the pair's (or span's) result.  The next one's queries are on their way
         // meanwhile.
         const int row0 = sg.row0, head0 = sg.g * p.G, out = sg.slot;
-        if (!next_segment(k + 1)) return;
+        if (!next_segment(k + kGroups)) return;
         // The warps' shares meet in shared memory, each relative to its own maximum: [warp]
         // [row][128 dims], a row's dims permuted so that the lanes (4 rows x 8 dims) meet 32
-        // different banks.  Up to 8 rows there is room for two pairs' shares, and one meeting
-        // per pair keeps writers off the readers.
-        constexpr bool kTwo = ROWS <= kMaxRows / 2;
-        if (!kTwo && k > 0 && !meet()) return;
-        float *share = xchg + (kTwo ? (k & 1) * kConsumers * ROWS * kD : 0);
-        float2(*ml)[kMaxRows] = bars->ml[k & 1];
+        // different banks.
+        if (meets > 0 && !meet()) return;   // the last pair's have been read
 #pragma unroll
         for (int h = 0; h < HR; ++h)
 #pragma unroll
@@ -635,8 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r = 8 * h + 2 * tq + c;
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[h][c] += __shfl_xor_sync(0xffffffffu, l[h][c], d);
-                if (gq == 0) ml[warp][r] = make_float2(m[h][c], l[h][c]);
-                float *mine = share + (warp * ROWS + r) * kD;
+                if (gq == 0) ml[cw][r] = make_float2(m[h][c], l[h][c]);
+                float *mine = xchg + (cw * ROWS + r) * kD;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     mine[(16 * i + gq) ^ (tq << 3)] = o[i][h][c];
@@ -645,14 +662,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         if (!meet()) return;
         // a warp adds up every fourth row, 4 dims per lane
-        for (int r = warp; r < rows; r += kConsumers) {
+        for (int r = cw; r < rows; r += kConsumers) {
             float2 x[kConsumers];
             float4 y[kConsumers];
             float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
             for (int w = 0; w < kConsumers; ++w) {
                 x[w] = ml[w][r];
-                y[w] = *reinterpret_cast<const float4 *>(share + (w * ROWS + r) * kD +
+                y[w] = *reinterpret_cast<const float4 *>(xchg + (w * ROWS + r) * kD +
                                                          ((4 * lane) ^ ((r >> 1 & 3) << 3)));
                 M = fmaxf(M, x[w].x);
             }
@@ -834,7 +851,7 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
     auto kern = eight ? paged_decode_kernel<8> : paged_decode_kernel<16>;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes) != cudaSuccess)
         return GQA_ERR_CUDA;
-    if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, mk, mv,
+    if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(n_threads(eight ? 8 : 16)), kSmemBytes, s, mk, mv,
                    p) != cudaSuccess)
         return GQA_ERR_CUDA;
     if (!p.whole) {
