@@ -154,7 +154,7 @@ size_t packed_prefill_workspace_bytes(int nseq, int total, int max_kv, int Hq, i
 // the streaming kernel for a few rows per sequence (paged_decode.cu)
 bool paged_decode_fits(int max_q, int G);
 int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
-size_t paged_decode_workspace_bytes(int max_kv);
+size_t paged_decode_workspace_bytes(int nseq, int max_kv, int Hkv);
 // A TMA map of bf16 elements: `rank` dims and box extents, innermost first, the strides of
 // dims 1 .. rank - 1 in bytes, 128-byte swizzle; false if the driver refuses it
 // (packed_attn.cu)

@@ -50,17 +50,16 @@ constexpr int kStages = 6;
 constexpr int kTileBytes = kUnit * kD * 2;      // K or V of a stage
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kConsumers = 4;                   // warps of a group, 16 keys of a stage each
-// groups of consumers, which take the pairs in turn (16 rows: 204 registers allow one)
-constexpr int n_groups(int rows) { return rows <= 8 ? 2 : 1; }
-constexpr int n_threads(int rows) { return 32 * (n_groups(rows) * kConsumers + 1); }
-constexpr int kMaxGroups = 2;
+constexpr int kGroups = 2;                      // groups of consumers, which take the pairs in turn
+constexpr int kThreads = 32 * (kGroups * kConsumers + 1);
 constexpr int kMaxRows = 16;
 constexpr int kSmemXchg = kStages * kStageBytes;
-constexpr int kSmemBar = kSmemXchg + kConsumers * kMaxRows * kD * 4;
+constexpr int kSmemBar = kSmemXchg + kGroups * kConsumers * 8 * kD * 4;
 constexpr int kSmemBytes = kSmemBar + 1536 + 1024;
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
 constexpr int kSegSlots = 4;
 constexpr int kSMs = 152;
+constexpr int kMinRun = 128;                    // units per SM from which chunks come in levels
 
 // A run of stages of one (sequence, KV head).  stages < 0: no more.
 struct Segment {
@@ -69,20 +68,21 @@ struct Segment {
     int slot;   // -1: all of the pair's keys; else the partial's place
 };
 
-// A pair whose keys begin in one CTA and go on in the next ones.  rows = 0: none.
+// A pair whose keys begin in one chunk and go on in the next ones.  rows = 0: none.
 struct Joint {
     int row0, g, rows, parts;
 };
 
 struct Bars {
     Segment seg[kSegSlots];
-    uint64_t full[kMaxGroups][kStages];   // a stage's load, for the group that takes it
+    uint64_t full[kGroups][kStages];   // a stage's load, for the group that takes it
     uint64_t empty[kStages];
     uint64_t seg_full[kSegSlots], seg_free[kSegSlots];
-    uint64_t merge[kMaxGroups];    // a group's warps meet (a barrier with a bounded wait)
-    float2 ml[kMaxGroups][kConsumers][kMaxRows];
-    int scan[n_threads(1) / 32];
-    int start_seq, start_unit;
+    uint64_t merge[kGroups];    // a group's warps meet (a barrier with a bounded wait)
+    float2 ml[kGroups][kConsumers][8];
+    uint4 clc_resp;
+    uint64_t clc_full;
+    int scan[kThreads / 32];   // units of each warp's sequences
 };
 static_assert(sizeof(Bars) <= 1536, "barrier block");
 
@@ -91,7 +91,8 @@ struct Params {
     __nv_bfloat16 *o;
     float *lse;
     float *ws_o, *ws_ml;
-    Joint *ws_joint;               // one per CTA
+    Joint *ws_joint;               // one per chunk
+    int chunks;
     const int32_t *cu, *kv_lens, *pages;
     int *status;
     long q_stride, o_stride;
@@ -114,6 +115,50 @@ __device__ __forceinline__ int first_unit(const PackedSeq &s, int window) {
 __device__ __forceinline__ int count_units(const PackedSeq &s, int window) {
     return s.T > 0 ? (s.S + kUnit - 1) / kUnit - first_unit(s, window) : 0;
 }
+
+// The cut of all units into chunks, one level of kSMs equal chunks after the other.
+constexpr int kLevels = 4;
+struct Cut {
+    int all, size[kLevels];
+    __device__ Cut(int units, int chunks) : all(units) {
+        const int run = all / kSMs;
+        int rest = 0;
+        size[0] = 0;
+#pragma unroll
+        for (int l = 1; l < kLevels; ++l) {
+            size[l] = chunks > kSMs && run >= kMinRun ? run >> (l + 2) : 0;
+            rest += size[l];
+        }
+        size[0] = (all - kSMs * rest + kSMs - 1) / kSMs;
+    }
+    __device__ void get(int c, int &begin, int &n) const {
+        begin = 0;
+        n = 0;
+#pragma unroll
+        for (int l = 0; l < kLevels; ++l) {
+            const int i = c - l * kSMs;
+            if (i >= kSMs) begin += kSMs * size[l];
+            else if (i >= 0) {
+                begin += i * size[l];
+                n = max(0, min(size[l], all - begin));
+            }
+        }
+    }
+    __device__ int chunk_of(int unit) const {
+        int c = 0;
+#pragma unroll
+        for (int l = 0; l < kLevels; ++l) {
+            if (unit < 0) continue;
+            if (l + 1 == kLevels || unit < kSMs * size[l]) {
+                c = l * kSMs + (size[l] > 0 ? unit / size[l] : 0);
+                unit = -1;
+            } else {
+                unit -= kSMs * size[l];
+            }
+        }
+        return c;
+    }
+};
 
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -163,7 +208,7 @@ enum Role { kRoleProducer = 0, kRoleConsumer = 2 };
 
 // ROWS: 8 or 16 rows of the MMA in use (8: the upper half is zero and costs no exponentials).
 template <int ROWS>
-__global__ void __launch_bounds__(n_threads(ROWS), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const Params p) {
     griddep_wait();
@@ -173,7 +218,6 @@ __global__ void __launch_bounds__(n_threads(ROWS), 1)
     uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     Bars *bars = reinterpret_cast<Bars *>(smem + kSmemBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kGroups = n_groups(ROWS), kThreads = n_threads(ROWS);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -185,53 +229,22 @@ __global__ void __launch_bounds__(n_threads(ROWS), 1)
             mbar_init(&bars->seg_free[i], kConsumers);
         }
         for (int g = 0; g < kGroups; ++g) mbar_init(&bars->merge[g], kConsumers);
+        mbar_init(&bars->clc_full, 1);
         fence_mbar_init();
     }
-    // ---- this CTA's run of units
-    int run = 0, per = 0;          // units of the run; of every CTA's run
-    if (p.whole) {
-        __syncthreads();
-    } else {
-        const int m = (p.nseq + kThreads - 1) / kThreads;   // sequences per thread
+    // ---- the batch's units: each warp's sequences, in order
+    const int m = (p.nseq + kThreads - 1) / kThreads;   // sequences per thread
+    if (!p.whole) {
         const int s0 = threadIdx.x * m;
         int mine = 0;
         for (int i = s0; i < s0 + m && i < p.nseq; ++i)
             mine += p.Hkv * count_units(packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status),
                                         p.window);
-        int incl = mine;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += x;
-        }
-        if (lane == 31) bars->scan[warp] = incl;
-        if (threadIdx.x == 0) bars->start_seq = -1;
-        __syncthreads();
-        int all = 0, before = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += bars->scan[w];
-            all += bars->scan[w];
-        }
-        before += incl - mine;
-        per = (all + gridDim.x - 1) / gridDim.x;
-        const int u0 = blockIdx.x * per;
-        run = max(0, min(per, all - u0));
-        if (run > 0 && before <= u0 && u0 < before + mine) {
-            int at = before;
-            for (int i = s0; i < p.nseq; ++i) {
-                const int n = p.Hkv * count_units(
-                                          packed_seq(p.cu, p.kv_lens, i, p.bounds, nullptr), p.window);
-                if (u0 < at + n) {
-                    bars->start_seq = i;
-                    bars->start_unit = u0 - at;
-                    break;
-                }
-                at += n;
-            }
-        }
-        __syncthreads();
+        for (int d = 1; d < 32; d <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+        if (lane == 0) bars->scan[warp] = mine;
     }
+    __syncthreads();
 
     if (warp == kGroups * kConsumers) {
         // ================= producer =================
@@ -242,11 +255,10 @@ __global__ void __launch_bounds__(n_threads(ROWS), 1)
         bool ok = true;
         int u = 0;   // stages issued
         uint32_t owner = 0, phases = 0;   // a place's last group; bits 8 group + place: full's
-        Joint joint{0, 0, 0, 0};
         // boxes of a stage: one per page, or per 64 keys of a longer page
         const int box = min(p.page_size, kUnit), boxes = kUnit / box;
-        // The run as a list of items, 32 of them in the lanes at a time: sequences from the
-        // run's first one, with all their KV heads, or the CTA's whole pairs.
+        // The batch as a list of items, 32 of them in the lanes at a time: sequences with all
+        // their KV heads, or the CTA's whole pairs.
         const int items = !p.whole ? p.nseq
                                    : (p.nseq * p.Hkv - static_cast<int>(blockIdx.x) +
                                       static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
@@ -269,15 +281,66 @@ __global__ void __launch_bounds__(n_threads(ROWS), 1)
         };
         int listed = 0;            // stages of the segments so far
         int head = 0, in = 0;      // the next pair's head within its item, units into it
-        if (p.whole) {
-            run = 0x7fffffff;
-            load_items(0);
-        } else if (run > 0) {
-            load_items(bars->start_seq);
-            const int n = __shfl_sync(0xffffffffu, s_units, 0);
-            head = bars->start_unit / n;
-            in = bars->start_unit - head * n;
-        }
+        // The chunk at hand: its units left, the number of the next one, and the pair that goes
+        // on behind it.
+        int run = 0x7fffffff, chunk = blockIdx.x, pos = 0, all = 0;
+        Joint joint{0, 0, 0, 0};
+        if (!p.whole)
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) all += bars->scan[w];
+        const Cut cut(all, p.chunks);
+        auto start_chunk = [&]() {
+            cut.get(chunk, pos, run);
+            joint = {0, 0, 0, 0};
+            if (run == 0) return;
+            // the warp's sequences that hold unit `pos`, and then the one
+            int w = 0, before = 0;
+            while (w < kThreads / 32 - 1 && pos >= before + bars->scan[w]) before += bars->scan[w++];
+            int first = 32 * m * w, incl;
+            while (true) {
+                load_items(first);
+                incl = s_units * heads;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, incl, d);
+                    if (lane >= d) incl += x;
+                }
+                const int here = __shfl_sync(0xffffffffu, incl, 31);
+                if (pos < before + here || first + 32 >= items) break;
+                before += here;
+                first += 32;
+            }
+            const uint32_t behind = __ballot_sync(0xffffffffu, before + incl > pos);
+            at = behind ? __ffs(behind) - 1 : 31;
+            const int n = max(1, __shfl_sync(0xffffffffu, s_units, at));
+            const int rel = pos - before - (__shfl_sync(0xffffffffu, incl, at) - n * heads);
+            head = rel / n;
+            in = rel - head * n;
+        };
+        int claims = 0;
+        // Claims chunks until one has work; run = 0: there is none.
+        auto next_chunk = [&]() {
+            while (run == 0) {
+                if (lane == 0) p.ws_joint[chunk] = joint;
+                if (p.chunks == kSMs) return;   // a chunk per CTA
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars->clc_full, 16);
+                    clc_try_cancel(&bars->clc_resp, &bars->clc_full);
+                }
+                if (!warp_wait(&bars->clc_full, claims++ & 1)) {
+                    set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 3, claims);
+                    ok = false;
+                    return;
+                }
+                chunk = clc_decode(&bars->clc_resp);
+                fence_proxy_async_smem();   // read before the next response overwrites it
+                __syncwarp();
+                if (chunk < 0) return;
+                start_chunk();
+            }
+        };
+        if (p.whole) load_items(0);
+        else start_chunk();
         auto next_segment = [&]() {
             Segment sg;
             sg.stages = -1;
@@ -300,10 +363,13 @@ __global__ void __launch_bounds__(n_threads(ROWS), 1)
             sg.stages = min(run, n - in);
             sg.u0 = listed;
             listed += sg.stages;
-            sg.slot = sg.stages == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (in == 0 ? 1 : 0);
-            if (in == 0 && sg.stages < n)   // the rest of the pair's units, per CTA
-                joint = {sg.row0, sg.g, sg.T * p.G, 1 + (n - sg.stages + per - 1) / per};
-            if (!p.whole) run -= sg.stages;
+            sg.slot = sg.stages == n ? -1 : 2 * chunk + (in == 0 ? 1 : 0);
+            if (in == 0 && sg.stages < n)
+                joint = {sg.row0, sg.g, sg.T * p.G, cut.chunk_of(pos + n - 1) - chunk + 1};
+            if (!p.whole) {
+                run -= sg.stages;
+                pos += sg.stages;
+            }
             in += sg.stages;
             if (in == n) {
                 in = 0;
@@ -320,6 +386,8 @@ __global__ void __launch_bounds__(n_threads(ROWS), 1)
         PageWalk walk_ahead;
         int k = 0;
         auto advance = [&]() {
+            if (run == 0) next_chunk();
+            if (!ok) return;
             ahead = next_segment();
             const int records = ahead.stages < 0 ? kGroups : 1;
             for (int i = 0; i < records; ++i, ++k) {
@@ -382,24 +450,27 @@ __global__ void __launch_bounds__(n_threads(ROWS), 1)
                 phases ^= 1u << (8 * group + st);
             }
         };
-        // A segment is looked up ahead of the loads of the one before it, the second one after
-        // the first one's, which wait for nothing that they can do without.
+        // A segment is looked up ahead of the loads of the one before it; not the second one,
+        // as the first one's loads wait for nothing that they can do without, and not a chunk's
+        // first one, as chunks are claimed when they can be loaded.
 #pragma unroll 1
         for (int turn = 0; ok && ahead.stages >= 0; ++turn) {
             sg = ahead;
             walk = walk_ahead;
+            const int late = turn == 0 || run == 0 ? 1 : 0;
 #pragma unroll 1
             for (int part = 0; part < 2 && ok; ++part) {
-                if ((part == 0) == (turn == 0)) load(turn % kGroups);
-                else advance();
+                if (part == late) advance();
+                else load(turn % kGroups);
             }
         }
-        if (ok && !p.whole && lane == 0) p.ws_joint[blockIdx.x] = joint;
-        if (!ok)   // never leave the CTA with copies in flight
+        if (!ok) {   // never leave the CTA with copies in flight
             for (int st = 0; st < min(u, kStages); ++st) {
                 const int group = owner >> st & 1;
                 mbar_wait(&bars->full[group][st], (phases >> (8 * group + st) & 1) ^ 1);
             }
+            if (claims > 0) mbar_wait(&bars->clc_full, (claims - 1) & 1);
+        }
         return;
     }
 
@@ -408,8 +479,8 @@ __global__ void __launch_bounds__(n_threads(ROWS), 1)
     constexpr int HR = ROWS / 8;                  // row halves in use
     const uint32_t ring = smem_u32(smem);
     const int group = warp / kConsumers, cw = warp % kConsumers;
-    float *xchg = reinterpret_cast<float *>(smem + kSmemXchg) + group * kConsumers * ROWS * kD;
-    float2(*ml)[kMaxRows] = bars->ml[group];
+    float *xchg = reinterpret_cast<float *>(smem + kSmemXchg) + group * kConsumers * 8 * kD;
+    float2(*ml)[8] = bars->ml[group];
     // ldmatrix rows, both operands A: K: matrices (chunk 2ks | 2ks + 1) x (keys 0-7 | 8-15);
     // V transposed: (keys 0-7 | 8-15) x (dim chunk 2nn | 2nn + 1)
     const int mat = lane >> 3, l7 = lane & 7;
@@ -641,145 +712,135 @@ __global__ void __launch_bounds__(n_threads(ROWS), 1)
         // meanwhile.
         const int row0 = sg.row0, head0 = sg.g * p.G, out = sg.slot;
         if (!next_segment(k + kGroups)) return;
-        // The warps' shares meet in shared memory, each relative to its own maximum: [warp]
-        // [row][128 dims], a row's dims permuted so that the lanes (4 rows x 8 dims) meet 32
-        // different banks.
-        if (meets > 0 && !meet()) return;   // the last pair's have been read
+        // The warps' shares meet in shared memory, 8 rows at a time, each relative to its own
+        // maximum: [warp][row][128 dims], a row's dims permuted so that the lanes (4 rows x 8
+        // dims) meet 32 different banks.
 #pragma unroll
-        for (int h = 0; h < HR; ++h)
+        for (int h = 0; h < HR; ++h) {
+            if (meets > 0 && !meet()) return;   // the last ones have been read
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int r = 8 * h + 2 * tq + c;
+                const int r = 2 * tq + c;
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[h][c] += __shfl_xor_sync(0xffffffffu, l[h][c], d);
                 if (gq == 0) ml[cw][r] = make_float2(m[h][c], l[h][c]);
-                float *mine = xchg + (cw * ROWS + r) * kD;
+                float *mine = xchg + (cw * 8 + r) * kD;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     mine[(16 * i + gq) ^ (tq << 3)] = o[i][h][c];
                     mine[(16 * i + 8 + gq) ^ (tq << 3)] = o[i][h][2 + c];
                 }
             }
-        if (!meet()) return;
-        // a warp adds up every fourth row, 4 dims per lane
-        for (int r = cw; r < rows; r += kConsumers) {
-            float2 x[kConsumers];
-            float4 y[kConsumers];
-            float M = -CUDART_INF_F, L = 0.f;
+            if (!meet()) return;
+            // a warp adds up every fourth row, 4 dims per lane
+            for (int rr = cw; rr < min(8, rows - 8 * h); rr += kConsumers) {
+                const int r = 8 * h + rr;
+                float2 x[kConsumers];
+                float4 y[kConsumers];
+                float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kConsumers; ++w) {
-                x[w] = ml[w][r];
-                y[w] = *reinterpret_cast<const float4 *>(xchg + (w * ROWS + r) * kD +
-                                                         ((4 * lane) ^ ((r >> 1 & 3) << 3)));
-                M = fmaxf(M, x[w].x);
-            }
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = 0; w < kConsumers; ++w) {
+                    x[w] = ml[w][rr];
+                    y[w] = *reinterpret_cast<const float4 *>(xchg + (w * 8 + rr) * kD +
+                                                             ((4 * lane) ^ ((rr >> 1 & 3) << 3)));
+                    M = fmaxf(M, x[w].x);
+                }
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kConsumers; ++w) {
-                // a share none of whose keys this row sees: m = -inf, l = 0 and O = 0 (NaN
-                // scores alone also leave m at -inf, with l and O NaN)
-                const float f = x[w].x == -CUDART_INF_F ? (x[w].y == 0.f ? 0.f : 1.f)
-                                                        : ex2_approx(x[w].x - M);
-                L = fmaf(x[w].y, f, L);
-                acc.x = fmaf(y[w].x, f, acc.x);
-                acc.y = fmaf(y[w].y, f, acc.y);
-                acc.z = fmaf(y[w].z, f, acc.z);
-                acc.w = fmaf(y[w].w, f, acc.w);
-            }
-            if (out >= 0) {
-                const size_t rec = (size_t)out * kMaxRows + r;
-                reinterpret_cast<float4 *>(p.ws_o + rec * kD)[lane] = acc;
-                if (lane == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(M, L);
-            } else {
-                const int t = token_of(p, r), head = head0 + r - t * p.G;
-                const long row = row0 + t;
-                const float inv = 1.0f / L;
-                reinterpret_cast<uint2 *>(p.o + row * p.o_stride + head * kD)[lane] = make_uint2(
-                    pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                if (p.lse && lane == 0)
-                    p.lse[(long)head * p.bounds.total + row] =
-                        (M + __log2f(L)) * 0.69314718055994531f;
+                for (int w = 0; w < kConsumers; ++w) {
+                    // a share none of whose keys this row sees: m = -inf, l = 0 and O = 0 (NaN
+                    // scores alone also leave m at -inf, with l and O NaN)
+                    const float f = x[w].x == -CUDART_INF_F ? (x[w].y == 0.f ? 0.f : 1.f)
+                                                            : ex2_approx(x[w].x - M);
+                    L = fmaf(x[w].y, f, L);
+                    acc.x = fmaf(y[w].x, f, acc.x);
+                    acc.y = fmaf(y[w].y, f, acc.y);
+                    acc.z = fmaf(y[w].z, f, acc.z);
+                    acc.w = fmaf(y[w].w, f, acc.w);
+                }
+                if (out >= 0) {
+                    const size_t rec = (size_t)out * kMaxRows + r;
+                    reinterpret_cast<float4 *>(p.ws_o + rec * kD)[lane] = acc;
+                    if (lane == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(M, L);
+                } else {
+                    const int t = token_of(p, r), head = head0 + r - t * p.G;
+                    const long row = row0 + t;
+                    const float inv = 1.0f / L;
+                    reinterpret_cast<uint2 *>(p.o + row * p.o_stride + head * kD)[lane] = make_uint2(
+                        pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                    if (p.lse && lane == 0)
+                        p.lse[(long)head * p.bounds.total + row] =
+                            (M + __log2f(L)) * 0.69314718055994531f;
+                }
             }
         }
     }
 }
 
-// Merges the partials of pairs that span several CTAs.  Block (c, r) takes row r of the pair
-// that begins in attention CTA c and goes on in the next ones.  Every warp forms the
-// partials' weights (a lane per partial; there are at most kSMs), the four warps add up every
-// fourth partial, 4 dims per lane, and their sums meet in shared memory.  A warp's first
-// weight and partial are fetched along with the block's record, not after it.
-// (A warp per row and its partials in turn took 20 us for one pair that all CTAs share.)
-constexpr int kCombineWarps = 4;
-__global__ void __launch_bounds__(32 * kCombineWarps) paged_decode_combine_kernel(const Params p) {
+// Merges the partials of pairs that span several chunks.  Block c takes the pair that begins in
+// chunk c and goes on in the next ones, blockIdx.y a few of its rows, W warps to a row.  Every
+// warp forms the partials' weights, a lane per partial, and adds up every W-th partial, 4 dims
+// per lane; the W sums meet in shared memory.  A warp's first weights are fetched along with
+// the block's record, not after it.
+// (One pair that all SMs share: 20 us with a warp per row; W = 4 where there are few pairs.)
+constexpr int kCombineWarps = 8;
+__global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_kernel(const Params p, int W) {
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int W = kCombineWarps;
-    __shared__ float4 part[W][32];
-    const int w0 = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.y;
-    // partial k: CTA c + k, its last pair for k = 0, its first for the others
-    auto rec = [&](int k) {
-        return (size_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * kMaxRows + r;
-    };
+    __shared__ float4 part[kCombineWarps][32];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = w % W, c = blockIdx.x;
+    const int r = blockIdx.y * (kCombineWarps / W) + w / W;
+    // partial k: chunk c + k, its last pair for k = 0, its first for the others
+    auto rec = [&](int k) { return (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * kMaxRows + r; };
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
-    auto out = [&](int k) { return reinterpret_cast<const float4 *>(p.ws_o + rec(k) * kD)[lane]; };
-    // (used only if the record says that these are there)
-    const int most = kSMs - blockIdx.x;   // partials there can be
-    float2 x0 = make_float2(0.f, 0.f);
-    float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (lane < most) x0 = ml[rec(lane)];
-    if (w0 < most) y0 = out(w0);
-    const Joint j = p.ws_joint[blockIdx.x];
-    if (r >= j.rows) return;   // also where nothing begins (rows = 0)
-    constexpr int kTurns = (kSMs + 31) / 32;
-    float2 x[kTurns];
-    float M = -CUDART_INF_F, L = 0.f;
-#pragma unroll
-    for (int i = 0; i < kTurns; ++i) {
-        x[i] = make_float2(-CUDART_INF_F, 0.f);
-        if (32 * i + lane < j.parts) x[i] = i == 0 ? x0 : ml[rec(32 * i + lane)];
-        M = fmaxf(M, x[i].x);
-    }
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float2 x = make_float2(-CUDART_INF_F, 0.f);
+    if (r < kMaxRows && c + lane < p.chunks) x = ml[rec(lane)];   // used if the record says so
+    const Joint j = p.ws_joint[c];
+    // (a chunk that an expired wait left out has no record: what its place holds is checked)
+    const bool on = r < j.rows && j.rows <= kMaxRows && j.parts >= 2 && j.parts <= p.chunks - c &&
+                    j.g >= 0 && j.g < p.Hkv && j.row0 >= 0 &&
+                    j.row0 < p.bounds.total - token_of(p, j.rows - 1);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -CUDART_INF_F, L = 0.f;
+    if (on) {
+        if (lane >= j.parts) x = make_float2(-CUDART_INF_F, 0.f);
+        M = x.x;
+        for (int i = 32 + lane; i < j.parts; i += 32) M = fmaxf(M, ml[rec(i)].x);
 #pragma unroll
-    for (int i = 0; i < kTurns; ++i) {
-        if (32 * i >= j.parts) break;
-        // a partial none of whose keys this row sees: m = -inf, l = 0 and O = 0 (NaN scores
-        // alone also leave m at -inf, with l and O NaN)
-        const float f = x[i].x == -CUDART_INF_F ? (x[i].y == 0.f ? 0.f : 1.f) : ex2_approx(x[i].x - M);
-        L = fmaf(x[i].y, f, L);
-        float4 y[32 / W];   // all in flight together
-#pragma unroll
-        for (int n = 0; n < 32 / W; ++n) {
-            const int k = 32 * i + n * W + w0;
-            y[n] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k < j.parts) y[n] = k == w0 ? y0 : out(k);
+        for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        for (int i = 0; i < j.parts; i += 32) {
+            if (i > 0) x = i + lane < j.parts ? ml[rec(i + lane)] : make_float2(-CUDART_INF_F, 0.f);
+            // a partial none of whose keys this row sees: m = -inf, l = 0 and O = 0 (NaN scores
+            // alone also leave m at -inf, with l and O NaN)
+            const float f = x.x == -CUDART_INF_F ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx(x.x - M);
+            L = fmaf(x.y, f, L);
+            const int n = min(32, j.parts - i);
+#pragma unroll 4
+            for (int q = sub; q < n; q += W) {
+                const float4 y = reinterpret_cast<const float4 *>(p.ws_o + rec(i + q) * kD)[lane];
+                const float fk = __shfl_sync(0xffffffffu, f, q);
+                acc.x = fmaf(y.x, fk, acc.x);
+                acc.y = fmaf(y.y, fk, acc.y);
+                acc.z = fmaf(y.z, fk, acc.z);
+                acc.w = fmaf(y.w, fk, acc.w);
+            }
         }
 #pragma unroll
-        for (int n = 0; n < 32 / W; ++n) {
-            const float fk = __shfl_sync(0xffffffffu, f, n * W + w0);
-            if (32 * i + n * W + w0 >= j.parts) continue;   // (fk may be a NaN's 1)
-            acc.x = fmaf(y[n].x, fk, acc.x);
-            acc.y = fmaf(y[n].y, fk, acc.y);
-            acc.z = fmaf(y[n].z, fk, acc.z);
-            acc.w = fmaf(y[n].w, fk, acc.w);
+        for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    }
+    if (W > 1) {
+        part[w][lane] = acc;
+        __syncthreads();
+        if (sub > 0) return;
+        for (int i = 1; i < W; ++i) {
+            const float4 y = part[w + i][lane];
+            acc.x += y.x;
+            acc.y += y.y;
+            acc.z += y.z;
+            acc.w += y.w;
         }
     }
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-    part[w0][lane] = acc;
-    __syncthreads();
-    if (w0 > 0) return;
-#pragma unroll
-    for (int w = 1; w < W; ++w) {
-        const float4 y = part[w][lane];
-        acc.x += y.x;
-        acc.y += y.y;
-        acc.z += y.z;
-        acc.w += y.w;
-    }
+    if (!on) return;
     const int t = token_of(p, r), h = j.g * p.G + r - t * p.G;
     const long row = j.row0 + t;
     const float inv = 1.0f / L;
@@ -796,10 +857,24 @@ bool whole_pairs(int max_kv) { return max_kv <= 8 * kUnit; }
 
 bool paged_decode_fits(int max_q, int G) { return static_cast<long>(max_q) * G <= kMaxRows; }
 
-size_t paged_decode_workspace_bytes(int max_kv) {
+namespace {
+// Chunks of a batch that is not run by whole pairs.  Equal runs are not equal times (the
+// slowest SMs take a tenth longer), so the batch is cut into levels of smaller and smaller
+// chunks; not where it is small, or has so few pairs that one would have hundreds of partials.
+int n_chunks(int nseq, int max_kv, int Hkv, int max_q, int window) {
+    const long pairs = (long)nseq * Hkv, all = (max_kv + kUnit - 1) / kUnit;
+    // a span of window + max_q - 1 keys touches at most this many units
+    const long most = window > 0 ? ((long)window + max_q - 2) / kUnit + 2 : all;
+    return pairs >= kSMs / 4 && pairs * (most < all ? most : all) >= (long)kMinRun * kSMs
+               ? kLevels * kSMs
+               : kSMs;
+}
+}  // namespace
+
+size_t paged_decode_workspace_bytes(int nseq, int max_kv, int Hkv) {
     if (whole_pairs(max_kv)) return 0;
-    const size_t rec = (size_t)2 * kSMs * kMaxRows;
-    return rec * (kD + 2) * sizeof(float) + kSMs * sizeof(Joint);
+    const size_t chunks = n_chunks(nseq, max_kv, Hkv, 1, 0);
+    return 2 * chunks * kMaxRows * (kD + 2) * sizeof(float) + chunks * sizeof(Joint);
 }
 
 int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
@@ -831,7 +906,8 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
     if ((long)a.nseq * a.Hkv * ((a.max_kv + kUnit - 1) / kUnit) > 0x7fffffffL - kSMs)
         return GQA_ERR_UNSUPPORTED;
     if (!p.whole) {
-        const size_t rec = (size_t)2 * kSMs * kMaxRows;
+        p.chunks = n_chunks(a.nseq, a.max_kv, a.Hkv, a.max_q, a.window);
+        const size_t rec = (size_t)2 * p.chunks * kMaxRows;
         p.ws_o = static_cast<float *>(ws);
         p.ws_ml = p.ws_o + rec * kD;
         p.ws_joint = reinterpret_cast<Joint *>(p.ws_ml + rec * 2);
@@ -846,17 +922,18 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
         !make_bf16_map(&mv, c.v, 4, dims, strides, box))
         return GQA_ERR_CUDA;
     const long pairs = (long)a.nseq * a.Hkv;
-    const long grid = p.whole && pairs < kSMs ? pairs : kSMs;
+    const long grid = !p.whole ? p.chunks : pairs < kSMs ? pairs : kSMs;
     const bool eight = static_cast<long>(a.max_q) * p.G <= 8;
     auto kern = eight ? paged_decode_kernel<8> : paged_decode_kernel<16>;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes) != cudaSuccess)
         return GQA_ERR_CUDA;
-    if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(n_threads(eight ? 8 : 16)), kSmemBytes, s, mk, mv,
+    if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, mk, mv,
                    p) != cudaSuccess)
         return GQA_ERR_CUDA;
     if (!p.whole) {
-        const dim3 grid(kSMs, static_cast<unsigned>(a.max_q * p.G));
-        if (launch_pdl(paged_decode_combine_kernel, grid, dim3(32 * kCombineWarps), 0, s, p) !=
+        const int W = p.chunks > kSMs ? 1 : 4, rows = kCombineWarps / W;
+        const dim3 grid(p.chunks, (a.max_q * p.G + rows - 1) / rows);
+        if (launch_pdl(paged_decode_combine_kernel, grid, dim3(32 * kCombineWarps), 0, s, p, W) !=
             cudaSuccess)
             return GQA_ERR_CUDA;
     }
