@@ -49,17 +49,20 @@ __device__ __forceinline__ PackedSeq packed_seq(const int32_t *cu, const int32_t
 }
 
 // The sequence whose rows include packed row `row` (warp-collective: every lane gets it):
-// the number of entries cu[1 .. nseq] that are <= row.  The caller checks the row against
+// the number of entries cu[1 .. nseq] that are <= row, found by 32 probes at a time (two
+// loads one after the other for up to 1024 sequences).  The caller checks the row against
 // that sequence's bounds, which also rejects rows behind the last sequence (the result is
 // then nseq) and offsets that are not sorted.
 __device__ __forceinline__ int packed_row_seq(const int32_t *cu, int nseq, int row) {
     const int lane = threadIdx.x & 31;
-    int n = 0;
-    for (int base = 1; base <= nseq; base += 32) {
-        const int i = base + lane;
-        n += __popc(__ballot_sync(0xffffffffu, i <= nseq && __ldg(cu + i) <= row));
+    int n = 0, len = nseq;   // entries known to be <= row; those after them in question
+    while (len > 32) {
+        const int step = (len + 31) / 32, i = step * (lane + 1);
+        const int k = __popc(__ballot_sync(0xffffffffu, i <= len && __ldg(cu + n + i) <= row));
+        n += k * step;
+        len = min(step - 1, len - k * step);
     }
-    return n;
+    return n + __popc(__ballot_sync(0xffffffffu, lane < len && __ldg(cu + n + 1 + lane) <= row));
 }
 
 // Starts a load of *p into L1 without waiting for it.
