@@ -412,6 +412,9 @@ static bool stride_ok(int64_t stride, int heads, int d) {
     return stride >= static_cast<int64_t>(heads) * d && (stride & 7) == 0;
 }
 
+// Tokens of one sequence: its positions and the tiles around them stay within 32 bits.
+static constexpr int kMostKeys = 1 << 30;
+
 static gqa_status check_paged(const gqa_paged_kv *c) {
     if (!c->k || !c->v || !c->page_table || !c->kv_lens || c->num_pages <= 0 || c->Hkv <= 0 ||
         c->max_pages <= 0 || c->reserved != 0)
@@ -472,7 +475,7 @@ gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64
     if (!q || !k || !v || !o || !cu_seqlens || nseq <= 0 || total <= 0 || Hq <= 0 || Hkv <= 0 ||
         (Hq % Hkv) != 0 || !(scale > 0.f) || !std::isfinite(scale))
         return GQA_ERR_INVALID_ARG;
-    if (d != 128 || Hq / Hkv > 64) return GQA_ERR_UNSUPPORTED;
+    if (d != 128 || Hq / Hkv > 64 || total > kMostKeys) return GQA_ERR_UNSUPPORTED;
     if (!stride_ok(q_stride, Hq, d) || !stride_ok(k_stride, Hkv, d) ||
         !stride_ok(v_stride, Hkv, d) || !stride_ok(o_stride, Hq, d) || o == q || o == k || o == v)
         return GQA_ERR_INVALID_ARG;
@@ -492,7 +495,7 @@ gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64
 size_t gqa_attn_paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
                                       int Hkv, int d) {
     if (nseq <= 0 || total <= 0 || max_q <= 0 || max_kv <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 ||
-        (Hq % Hkv) != 0)
+        (Hq % Hkv) != 0 || max_kv > kMostKeys)
         return 0;
     return gqa::paged_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv, d);
 }
@@ -509,7 +512,7 @@ gqa_status gqa_attn_paged(const void *q, int64_t q_stride, const gqa_paged_kv *c
     if (bad != GQA_OK) return bad;
     const int Hkv = cache->Hkv, d = cache->d;
     if ((Hq % Hkv) != 0) return GQA_ERR_INVALID_ARG;
-    if (d != 128 || Hq / Hkv > 64) return GQA_ERR_UNSUPPORTED;
+    if (d != 128 || Hq / Hkv > 64 || max_kv > kMostKeys) return GQA_ERR_UNSUPPORTED;
     if (!stride_ok(q_stride, Hq, d) || !stride_ok(o_stride, Hq, d) || o == q)
         return GQA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(o) ||

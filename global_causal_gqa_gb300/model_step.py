@@ -133,6 +133,22 @@ class PagedStack:
         self.max_q, self.max_kv, self.Hq, self.Hkv, self.d = max_q, max_kv, Hq, Hkv, d
         self.scale, self.eps = scale, eps
         self.nseq, self.total = page_table.shape[0], layers[0].qkv.shape[0]
+        if cu_seqlens.shape != (self.nseq + 1,) or cu_seqlens.dtype != torch.int32:
+            raise ValueError("PagedStack: cu_seqlens is int32 [nseq + 1]")
+        for i, L in enumerate(layers):
+            for t, name, shape in ((L.qkv, "qkv", (self.total, (Hq + 2 * Hkv) * d)),
+                                   (L.o, "o", (self.total, Hq, d))):
+                if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
+                    raise ValueError(f"PagedStack: layer {i}: {name} is contiguous bfloat16 "
+                                     f"{list(shape)}")
+            if L.k_pool.shape[1] != Hkv or L.k_pool.shape[3] != d:
+                raise ValueError(f"PagedStack: layer {i}: pools of {Hkv} KV heads of {d}")
+            for t, name, n in ((L.q_gamma, "q_gamma", d), (L.k_gamma, "k_gamma", d),
+                               (L.table, "table", L.table_len * d)):
+                if t is not None and (t.numel() < n or t.dtype != torch.float32 or
+                                      not t.is_contiguous()):
+                    raise ValueError(f"PagedStack: layer {i}: {name} is contiguous float32, "
+                                     f"{n} values")
         self.caches = [make_paged_kv(L.k_pool, L.v_pool, page_table, kv_lens) for L in layers]
         dev = layers[0].qkv.device
         self.wsb = gqa_attn_paged_workspace_bytes(self.nseq, self.total, max_q, max_kv, Hq, Hkv, d)
