@@ -274,6 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i < items) {
                 const int pair = p.whole ? static_cast<int>(blockIdx.x + i * gridDim.x) : 0;
                 s_seq = p.whole ? pair / p.Hkv : i;
+                // its first page entries, not after its lengths but with them
+                if (p.whole) touch(p.pages + (long)s_seq * p.max_pages);
                 s_head = p.whole ? pair - s_seq * p.Hkv : 0;
                 s = packed_seq(p.cu, p.kv_lens, s_seq, p.bounds, p.whole ? p.status : nullptr);
                 s_units = count_units(s, p.window);
