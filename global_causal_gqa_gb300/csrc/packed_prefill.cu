@@ -1186,9 +1186,9 @@ constexpr double kTileUs = 1.75, kItemUs = 5.0, kPartialUs = 8.0, kCombineUs = 4
 constexpr double kMean = 0.6;
 int best_spans(int nseq, int total, int tiles, int Hq, int Hkv, int most) {
     const int ntok = 2 * (kBM / (Hq / Hkv));
-    // every sequence ends in half a block on average
-    const long blocks = nseq > 1 ? total / ntok + (nseq < total ? nseq : total) / 2 + 1
-                                 : (total + ntok - 1) / ntok;
+    // every sequence has a block at least, and ends in half a block on average
+    const long some = nseq < total ? nseq : total, on_average = total / ntok + some / 2 + 1;
+    const long blocks = nseq == 1 ? (total + ntok - 1) / ntok : on_average > some ? on_average : some;
     const double items = static_cast<double>(blocks) * Hkv;
     int best = 1;
     double least = 0;
