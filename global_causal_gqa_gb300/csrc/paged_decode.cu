@@ -9,26 +9,35 @@
 // keep HBM busy.
 //
 // Work split.  The unit is 64 keys of one (sequence, KV head).  All units of the batch, in
-// the order (sequence, KV head, keys), are cut into one equal run per SM, whatever the
-// lengths, so every SM streams the same number of bytes.  A pair of (sequence, KV head) that
-// lies within one CTA's run is finished there; one that spans several leaves a partial (m, l,
-// O) per CTA, at most two per CTA (its first and its last pair), and the combine kernel
-// merges them.  Calls whose keys are few per pair take one CTA per pair and no second kernel.
-// The lengths are read on the device: every CTA sums the units of all sequences (a thread per
-// sequence) and finds its own start.
+// the order (sequence, KV head, keys), are cut into chunks whatever the lengths.  A pair of
+// (sequence, KV head) that lies within one chunk is finished there; one that spans several
+// leaves a partial (m, l, O) per chunk, at most two per chunk (its first and its last pair), and
+// the combine kernel merges them.  A small batch has one chunk per SM.  Equal chunks are not
+// equal times, though: over 32 caches of 8k-64k tokens the median SM was done at 703 us, the
+// slowest at 791.  So a long batch has four levels of 152 chunks, of about 25/32, 1/8, 1/16 and
+// 1/32 of an SM's share, which the CTAs claim in this order as they come free: 757 instead of
+// 785 us (762 with three levels, 761 with five; below 128 units per SM the chunks' ends cost what
+// the levels give: 88 for 89.5 us at 111 units, 68 for 67 at 70).  The cut is a function of the
+// lengths alone, and so are the results.  Calls whose keys are few per pair take one CTA per
+// pair and no second kernel.  The lengths are read on the device: every CTA sums the units of all
+// sequences (a thread per sequence), and a chunk's start is found from those sums.
 //
 // A producer warp streams K and V by TMA into a ring of 6 stages of 64 keys (192 KB in
-// flight per SM) and runs ahead over the ends of pairs.  A box is one page with both halves of
-// the head dimension (their rows 128-byte swizzled): for 64 windows of 2048 keys in pages of
-// 16, 98 us; with a box per half 121 us.  Four consumer warps take 16 keys of each stage
-// (eight, four to a stage in turn, were no faster; with nothing computed at all that batch
-// took 91 us).  S = Q K^T and O += P V are m16n8k16 bf16 MMAs with the rows as M, so that P
-// leaves the score product in the layout of an A operand; accumulators and softmax statistics
-// are fp32, P is rounded to bf16 for its product, and the row maximum moves only when a score
-// exceeds it by 2^8 (exact: sum and O share the reference).  At the end of a pair the warps
-// merge through shared memory.
+// flight per SM) and runs ahead over the ends of pairs; it looks pairs up 32 sequences at a time
+// and a pair ahead of its loads (1024 caches of 100 tokens: 130 -> 119 us).  A box is one page
+// with both halves of the head dimension (their rows 128-byte swizzled): for 64 windows of 2048
+// keys in pages of 16, 98 us; with a box per half 121 us.  Two groups of four consumer warps take
+// the pairs in turn, so that one group's ends (queries in, merge, outputs) pass while the other
+// streams (the 1024 short caches: 115 -> 100 us, of which 79 are their whole pages at HBM's rate;
+// long pairs do not care).  Each warp takes 16 keys of each stage.  S^T = K Q^T and O^T += V^T P^T
+// are m16n8k16 bf16 MMAs with the keys, and then the dims, as M and 8 rows as N: half the
+// products that the rows as M would take for up to 8 rows.  P leaves the score product
+// transposed, 8 x 8 values at a time, as a B operand.  Accumulators and softmax statistics are
+// fp32, P is rounded to bf16 for its product, and the row maximum moves only when a score exceeds
+// it by 2^8 (exact: sum and O share the reference).  At the end of a pair a group's warps merge
+// through shared memory.
 //
-// Measured (GB300): 32 caches of 8k-64k tokens, 8 KV heads, 64-token pages: 785 us, 6.9 TB/s.
+// Measured (GB300): 32 caches of 8k-64k tokens, 8 KV heads, 64-token pages: 753 us, 7.2 TB/s.
 //
 // Hidden keys have weight 0, but 0 * NaN is NaN: in blocks that straddle an edge of the mask
 // the values of keys that no row sees are zeroed on their way into the product, and
