@@ -114,3 +114,28 @@ def test_append_many_sequences(n):
     want_v = torch.full_like(vp, -3.0)
     want_v[table[seq, pos // 16].long(), 0, pos % 16] = v[r]
     assert torch.equal(vp, want_v)
+
+
+def test_captured_levels_follow_the_lengths():
+    """One captured call over lengths that fill the levels, then some that do not, none, and the
+    first ones again."""
+    p = Paged([1] * 8, LONG, 16, 8, 64, 761, max_kv=60000)
+    p.run()
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            p.run(stream=side)
+    torch.cuda.synchronize()
+    full = (p.s, p.k, p.v)
+    for cut in (1, 40, 1, 3000, 7, 1):
+        p.s = [max(1, n // cut) for n in full[0]]
+        p.k, p.v = [x[:n] for x, n in zip(full[1], p.s)], [x[:n] for x, n in zip(full[2], p.s)]
+        p.s_d.copy_(pu.i32(p.s))
+        p.o.fill_(-7.0)
+        p.L.fill_(-7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert pu.status() == 0
+        p.check()
