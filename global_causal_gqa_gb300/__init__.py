@@ -60,6 +60,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """The loaded libgqa_attn.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -123,12 +125,20 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_current = None   # torch's current device and the handle of a device's current stream
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        # the current stream's handle without a Stream object around it: 0.3 us instead of 3,
-        # a quarter of a small call's time on the host
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+        global _current
+        if _current is None:
+            import torch
+            torch.cuda.current_device()   # initialises CUDA
+            _current = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        # the handle without a Stream object around it: 0.2 us instead of 3, half of a small
+        # call's time on the host
+        device, raw_stream = _current
+        return raw_stream(device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
