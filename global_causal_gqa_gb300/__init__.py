@@ -120,9 +120,12 @@ def _ptr(x) -> Optional[int]:
         return None
     if isinstance(x, int):
         return x or None
-    if isinstance(x, np.ndarray):
-        return getattr(x, "address", None) or x.ctypes.data
-    return x.data_ptr()
+    try:
+        return x.data_ptr()   # nearly every argument is a tensor
+    except AttributeError:
+        if isinstance(x, np.ndarray):
+            return x.ctypes.data
+        raise
 
 
 _current = None   # torch's current device and the handle of a device's current stream
@@ -323,8 +326,11 @@ assert PAGED_KV_DTYPE.itemsize == 56
 
 class PagedKV(np.ndarray):
     """A host gqa_paged_kv that knows its address (numpy takes 10 us to tell it of a record
-    array, as long as all else of a small call)."""
+    array, longer than all else of a small call)."""
     address: Optional[int] = None
+
+    def data_ptr(self) -> int:
+        return self.address or self.ctypes.data
 
 
 def make_paged_kv(k_pool, v_pool, page_table, kv_lens) -> np.ndarray:
