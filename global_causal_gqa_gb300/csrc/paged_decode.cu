@@ -91,7 +91,7 @@ struct Bars {
     float2 ml[kGroups][kConsumers][8];
     uint4 clc_resp;
     uint64_t clc_full;
-    int scan[kThreads / 32];   // units of each warp's sequences
+    int scan[kThreads / 32], most[kThreads / 32];   // units of each warp's sequences; of a pair
 };
 static_assert(sizeof(Bars) <= 1536, "barrier block");
 
@@ -125,17 +125,19 @@ __device__ __forceinline__ int count_units(const PackedSeq &s, int window) {
     return s.T > 0 ? (s.S + kUnit - 1) / kUnit - first_unit(s, window) : 0;
 }
 
-// The cut of all units into chunks, one level of kSMs equal chunks after the other.
+// The cut of all units into chunks, one level of kSMs equal chunks after the other; one level
+// alone also where a pair has so much of the whole (`most` units) that hundreds of chunks would
+// share it.
 constexpr int kLevels = 4;
 struct Cut {
     int all, size[kLevels];
-    __device__ Cut(int units, int chunks) : all(units) {
+    __device__ Cut(int units, int most, int chunks) : all(units) {
         const int run = all / kSMs;
         int rest = 0;
         size[0] = 0;
 #pragma unroll
         for (int l = 1; l < kLevels; ++l) {
-            size[l] = chunks > kSMs && run >= kMinRun ? run >> (l + 2) : 0;
+            size[l] = chunks > kSMs && run >= kMinRun && most <= all / 4 ? run >> (l + 2) : 0;
             rest += size[l];
         }
         size[0] = (all - kSMs * rest + kSMs - 1) / kSMs;
@@ -215,7 +217,7 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
 
 enum Role { kRoleProducer = 0, kRoleConsumer = 2 };
 
-// ROWS: 8 or 16 rows of the MMA in use (8: the upper half is zero and costs no exponentials).
+// ROWS: the most rows of a pair, 8 or 16.
 template <int ROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
@@ -245,13 +247,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int m = (p.nseq + kThreads - 1) / kThreads;   // sequences per thread
     if (!p.whole) {
         const int s0 = threadIdx.x * m;
-        int mine = 0;
-        for (int i = s0; i < s0 + m && i < p.nseq; ++i)
-            mine += p.Hkv * count_units(packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status),
-                                        p.window);
+        int mine = 0, most = 0;
+        for (int i = s0; i < s0 + m && i < p.nseq; ++i) {
+            const int n = count_units(packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status), p.window);
+            mine += p.Hkv * n;
+            most = max(most, n);
+        }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-        if (lane == 0) bars->scan[warp] = mine;
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) {
+            bars->scan[warp] = mine;
+            bars->most[warp] = most;
+        }
     }
     __syncthreads();
 
@@ -294,12 +302,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         int head = 0, in = 0;      // the next pair's head within its item, units into it
         // The chunk at hand: its units left, the number of the next one, and the pair that goes
         // on behind it.
-        int run = 0x7fffffff, chunk = blockIdx.x, pos = 0, all = 0;
+        int run = 0x7fffffff, chunk = blockIdx.x, pos = 0, all = 0, most = 0;
         Joint joint{0, 0, 0, 0};
         if (!p.whole)
 #pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) all += bars->scan[w];
-        const Cut cut(all, p.chunks);
+            for (int w = 0; w < kThreads / 32; ++w) {
+                all += bars->scan[w];
+                most = max(most, bars->most[w]);
+            }
+        const Cut cut(all, most, p.chunks);
         auto start_chunk = [&]() {
             cut.get(chunk, pos, run);
             joint = {0, 0, 0, 0};
@@ -793,8 +804,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // warp forms the partials' weights, a lane per partial, and adds up every W-th partial, 4 dims
 // per lane; the W sums meet in shared memory.  A warp's first weights are fetched along with
 // the block's record, not after it.
-// (One pair that all SMs share: 20 us with a warp per row; W = 4 where there are few pairs.)
-constexpr int kCombineWarps = 8;
+// (One pair that all SMs share: 20 us with a warp per row; W = 4 where there are few pairs, else
+// 2.  A pair of 10^6 keys next to 37 short ones: 146 us with levels and a partial at a time, 120
+// with one level and four partials in flight per warp.)
+constexpr int kCombineWarps = 8, kFlight = 4;
 __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_kernel(const Params p, int W) {
     griddep_wait();
     griddep_launch_dependents();
@@ -826,14 +839,23 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_ke
             const float f = x.x == -CUDART_INF_F ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx(x.x - M);
             L = fmaf(x.y, f, L);
             const int n = min(32, j.parts - i);
-#pragma unroll 4
-            for (int q = sub; q < n; q += W) {
-                const float4 y = reinterpret_cast<const float4 *>(p.ws_o + rec(i + q) * kD)[lane];
-                const float fk = __shfl_sync(0xffffffffu, f, q);
-                acc.x = fmaf(y.x, fk, acc.x);
-                acc.y = fmaf(y.y, fk, acc.y);
-                acc.z = fmaf(y.z, fk, acc.z);
-                acc.w = fmaf(y.w, fk, acc.w);
+            for (int q0 = sub; q0 < n; q0 += kFlight * W) {
+                float4 y[kFlight];   // all in flight together
+#pragma unroll
+                for (int k = 0; k < kFlight; ++k) {
+                    const int q = q0 + k * W;
+                    y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (q < n) y[k] = reinterpret_cast<const float4 *>(p.ws_o + rec(i + q) * kD)[lane];
+                }
+#pragma unroll
+                for (int k = 0; k < kFlight; ++k) {
+                    const float fk = __shfl_sync(0xffffffffu, f, min(q0 + k * W, 31));
+                    if (q0 + k * W >= n) continue;   // (fk may be a NaN's 1)
+                    acc.x = fmaf(y[k].x, fk, acc.x);
+                    acc.y = fmaf(y[k].y, fk, acc.y);
+                    acc.z = fmaf(y[k].z, fk, acc.z);
+                    acc.w = fmaf(y[k].w, fk, acc.w);
+                }
             }
         }
 #pragma unroll
@@ -942,7 +964,7 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
                    p) != cudaSuccess)
         return GQA_ERR_CUDA;
     if (!p.whole) {
-        const int W = p.chunks > kSMs ? 1 : 4, rows = kCombineWarps / W;
+        const int W = pairs < kSMs / 4 ? 4 : 2, rows = kCombineWarps / W;
         const dim3 grid(p.chunks, (a.max_q * p.G + rows - 1) / rows);
         if (launch_pdl(paged_decode_combine_kernel, grid, dim3(32 * kCombineWarps), 0, s, p, W) !=
             cudaSuccess)

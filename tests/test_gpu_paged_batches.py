@@ -139,3 +139,19 @@ def test_captured_levels_follow_the_lengths():
         torch.cuda.synchronize()
         assert pu.status() == 0
         p.check()
+
+
+@pytest.mark.parametrize("place", [0, 39])
+def test_one_long_sequence_among_short_ones(place):
+    """Enough keys for levels, but nearly all of them of one pair: a chunk per SM."""
+    s = [1 + (17 * i) % 150 for i in range(40)]
+    s[place] = 1250000
+    assert -(-s[place] // 64) >= 152 * 128
+    p = Paged([1] * 40, s, 8, 1, 128, 771)
+    p.run()
+    assert pu.status() == 0
+    p.check()
+    o = p.o.clone()
+    p.ws.fill_(float("nan"))
+    p.run()
+    assert torch.equal(p.o, o)
