@@ -1116,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Merges the spans of split items: one warp per (token, query head), the spans' maxima and
 // sums in the lanes, 4 dims of the output per lane.
 constexpr int kMostSpans = 64;
-constexpr int kCombineWarps = 8;
+constexpr int kCombineWarps = 8, kFlight = 4;   // partials in flight per warp
 __global__ void __launch_bounds__(32 * kCombineWarps) packed_combine_kernel(const Params p) {
     griddep_wait();
     griddep_launch_dependents();
@@ -1151,14 +1151,23 @@ __global__ void __launch_bounds__(32 * kCombineWarps) packed_combine_kernel(cons
         const float f = x[t].x == -CUDART_INF_F ? (x[t].y == 0.f ? 0.f : 1.f) : ex2_approx(x[t].x - M);
         L = fmaf(x[t].y, f, L);
         const int n = min(32, spans - 32 * t);
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float4 o = reinterpret_cast<const float4 *>(p.ws_o + (rec + (32 * t + k) * step) * kD)[lane];
-            const float fk = __shfl_sync(0xffffffffu, f, k);
-            acc.x = fmaf(o.x, fk, acc.x);
-            acc.y = fmaf(o.y, fk, acc.y);
-            acc.z = fmaf(o.z, fk, acc.z);
-            acc.w = fmaf(o.w, fk, acc.w);
+        for (int k0 = 0; k0 < n; k0 += kFlight) {
+            float4 o[kFlight];   // all in flight together
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k < n)
+                    o[k] = reinterpret_cast<const float4 *>(p.ws_o + (rec + (32 * t + k0 + k) * step) * kD)[lane];
+            }
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, min(k0 + k, 31));
+                if (k0 + k >= n) continue;   // (fk may be a NaN's 1)
+                acc.x = fmaf(o[k].x, fk, acc.x);
+                acc.y = fmaf(o[k].y, fk, acc.y);
+                acc.z = fmaf(o[k].z, fk, acc.z);
+                acc.w = fmaf(o[k].w, fk, acc.w);
+            }
         }
     }
 #pragma unroll
