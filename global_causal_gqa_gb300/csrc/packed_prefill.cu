@@ -1073,9 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    pack_bf16x2(y[6] * inv_l, y[7] * inv_l));
                 }
                 if (valid && slot.any_bad) add_marked<PAGED>(p, slot, it, qpos, stage, r);
-                if (whole) {
-                    fence_proxy_async_smem();   // the store warp's TMA reads it
-                } else {
+                if (!whole) {
                     // a ragged tile: the warp writes the rows that are there, two at a time
                     __syncwarp();
                     const int r0 = (warp & 3) * 32, c = lane & 15;
@@ -1091,6 +1089,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4 *>(p.o + at + 8 * c) = y;
                     }
                 }
+                // A whole tile is read by the store warp's TMA next.  A ragged one is not, but the
+                // slot then takes a K or V tile by TMA, which a barrier alone does not order
+                // after this thread's stores.
+                fence_proxy_async_smem();
                 mbar_arrive(&bars->staged[wg][ns & 1]);
                 ++ns;
                 if (valid && p.lse)
