@@ -492,12 +492,20 @@ gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64
     return static_cast<gqa_status>(rc);
 }
 
+// The shape of a paged call: what gqa_attn_paged refuses has no workspace.
+static gqa_status check_paged_shape(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv,
+                                    int d) {
+    if (nseq <= 0 || total <= 0 || max_q <= 0 || max_kv < max_q || Hq <= 0 || Hkv <= 0 || d <= 0 ||
+        (Hq % Hkv) != 0)
+        return GQA_ERR_INVALID_ARG;
+    if (d != 128 || Hq / Hkv > 64 || max_kv > kMostKeys) return GQA_ERR_UNSUPPORTED;
+    return GQA_OK;
+}
+
 size_t gqa_attn_paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
                                       int Hkv, int d) {
-    if (nseq <= 0 || total <= 0 || max_q <= 0 || max_kv <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 ||
-        (Hq % Hkv) != 0 || max_kv > kMostKeys)
-        return 0;
-    return gqa::paged_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv, d);
+    if (check_paged_shape(nseq, total, max_q, max_kv, Hq, Hkv, d) != GQA_OK) return 0;
+    return gqa::paged_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv);
 }
 
 gqa_status gqa_attn_paged(const void *q, int64_t q_stride, const gqa_paged_kv *cache,
@@ -505,21 +513,19 @@ gqa_status gqa_attn_paged(const void *q, int64_t q_stride, const gqa_paged_kv *c
                           int Hq, int window, float scale, void *o, int64_t o_stride,
                           float *lse, void *workspace, size_t workspace_bytes,
                           gqa_stream_t stream) {
-    if (!q || !cache || !o || !cu_seqlens || nseq <= 0 || total <= 0 || max_q <= 0 ||
-        max_kv < max_q || Hq <= 0 || !(scale > 0.f) || !std::isfinite(scale))
+    if (!q || !cache || !o || !cu_seqlens || !(scale > 0.f) || !std::isfinite(scale))
         return GQA_ERR_INVALID_ARG;
-    const gqa_status bad = check_paged(cache);
+    gqa_status bad = check_paged(cache);
     if (bad != GQA_OK) return bad;
     const int Hkv = cache->Hkv, d = cache->d;
-    if ((Hq % Hkv) != 0) return GQA_ERR_INVALID_ARG;
-    if (d != 128 || Hq / Hkv > 64 || max_kv > kMostKeys) return GQA_ERR_UNSUPPORTED;
+    bad = check_paged_shape(nseq, total, max_q, max_kv, Hq, Hkv, d);
+    if (bad != GQA_OK) return bad;
     if (!stride_ok(q_stride, Hq, d) || !stride_ok(o_stride, Hq, d) || o == q)
         return GQA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(o) ||
         ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_seqlens)) & 3u))
         return GQA_ERR_ALIGNMENT;
-    const size_t need =
-        gqa_attn_paged_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv, d);
+    const size_t need = gqa::paged_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv);
     if (need) {
         if (!workspace || workspace_bytes < need) return GQA_ERR_WORKSPACE;
         if (!aligned16(workspace)) return GQA_ERR_ALIGNMENT;

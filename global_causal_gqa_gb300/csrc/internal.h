@@ -161,7 +161,7 @@ size_t paged_decode_workspace_bytes(int nseq, int max_kv, int Hkv);
 bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
                    const uint64_t *strides, const uint32_t *box);
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
-size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv, int d);
+size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv);
 
 // Bounded-wait self-test (watchdog.cu)
 cudaError_t launch_watchdog_selftest(int64_t limit_ns, int *status, cudaStream_t s);

@@ -47,7 +47,7 @@ bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv, int) {
+size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv) {
     return paged_decode_fits(max_q, Hq / Hkv)
                ? paged_decode_workspace_bytes(nseq, max_kv, Hkv)
                : packed_prefill_workspace_bytes(nseq, total, max_kv, Hq, Hkv);

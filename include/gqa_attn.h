@@ -378,7 +378,7 @@ gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64
  * after RoPE, o [total, Hq, d], lse as for gqa_attn_packed.  max_q and max_kv: upper bounds on
  * T and S over the batch; they and the shape choose the kernel and its split of the keys, and
  * size the workspace (gqa_attn_paged_workspace_bytes with the same arguments; 0 = none
- * needed).  Its contents need no initialisation; calls that may overlap need one each.  Every
+ * needed, or a shape that the call refuses).  Its contents need no initialisation; calls that may overlap need one each.  Every
  * result is the same on every run of the same call.  d = 128; Hq / Hkv an integer of at most
  * 64; max_q <= max_kv <= 2^30. */
 size_t gqa_attn_paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
