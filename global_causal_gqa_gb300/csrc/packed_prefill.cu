@@ -1058,7 +1058,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         add_marked<PAGED>(p, slot, it, qpos, reinterpret_cast<uint8_t *>(dst), -1);
                 }
             } else {
-                const float inv_l = l > 0.f || l != l ? 1.0f / l : 0.f;
+                // (l = 0: every visible score is -inf, and 0 * inf gives the NaN of the definition,
+                // as the merge of a split item's spans does)
+                const float inv_l = 1.0f / l;
                 const bool whole = ntok >= p.Mt;   // the tile's tokens are all there
                 // through a ring slot, as two halves of the columns like a Q tile
                 uint8_t *stage = smem + kSmemRing + it.o_slot(wg) * kTileBytes;

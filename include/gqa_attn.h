@@ -364,7 +364,7 @@ gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k
  * [total, Hkv, d], o [total, Hq, d] with token strides; o may not alias an input.  lse
  * [Hq, total] float32 natural-log sum of exp of the scaled scores, or NULL.  scale finite and
  * > 0.  A row never depends on keys or values that its mask hides, not even through NaN or
- * infinities in them.  d = 128; Hq / Hkv an integer of at most 64; total <= 2^30. */
+ * infinities in them.  A row whose visible scores are all -inf is NaN, its lse -inf.  d = 128; Hq / Hkv an integer of at most 64; total <= 2^30. */
 gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                            const void *v, int64_t v_stride, void *o, int64_t o_stride,
                            float *lse, const int32_t *cu_seqlens, int nseq, int total, int Hq,
