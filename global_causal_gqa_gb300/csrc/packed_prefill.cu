@@ -1309,7 +1309,9 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
         return GQA_ERR_CUDA;
     // an upper bound on the items: a sequence adds at most one block that is not full
     const long blocks = (long)a.total / ntok + (a.nseq < a.total ? a.nseq : a.total);
-    const long grid = blocks * a.Hkv * spans;
+    // and one number more: the CTA that gets it walks past the last sequence, so that all of them
+    // have been looked over (one that passes the rows has no item that would lead to it)
+    const long grid = blocks * a.Hkv * spans + 1;
     if (grid > 0x7fffffffL) return GQA_ERR_UNSUPPORTED;
     if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, mq, mk,
                    mv, mo, p) != cudaSuccess)

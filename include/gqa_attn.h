@@ -323,7 +323,9 @@ gqa_status gqa_attn_decode_static(const void *q, const gqa_kv_desc *descs, int n
  * A sequence whose numbers are inconsistent (offsets that decrease or pass `total`, T > S)
  * is skipped, its outputs left as they were, and the status word records
  * GQA_ERR_INVALID_ARG; one that exceeds a bound given by the host (max_q, max_kv, the pages
- * of its table row) is skipped and records GQA_ERR_CAPACITY.  A page-table entry outside the
+ * of its table row) is skipped and records GQA_ERR_CAPACITY.  Rows over which offsets decrease
+ * (from cu_seqlens[i+1] to cu_seqlens[i]) may be written for any sequence that claims them, or
+ * for none; the other sequences' rows are computed.  A page-table entry outside the
  * pool records GQA_ERR_INVALID_ARG: nothing is written there, and zeros are read instead. */
 typedef struct gqa_paged_kv {
     void *k;                    /* device [num_pages, Hkv, page_size, d] bf16, after RoPE */
