@@ -119,6 +119,14 @@ __device__ __forceinline__ void find_token(const AppendParams &p, int row, int i
     }
 }
 
+// Looks every sequence over, a thread each from the first blocks' last ones: numbers that
+// contradict one another are recorded even where no row falls to them.
+__device__ __forceinline__ void check_sequences(const AppendParams &p) {
+    for (long i = (long)blockIdx.x * blockDim.x + blockDim.x - 1 - threadIdx.x; i < p.nseq;
+         i += (long)gridDim.x * blockDim.x)
+        packed_seq(p.cu, p.kv_lens, static_cast<int>(i), p.bounds, p.status);
+}
+
 // D: head dim.  `per` threads (a multiple of the D / 16 lanes of a vector) serve one token at
 // a time, the block's kAppendThreads / per groups take its `tokens` tokens in turn.
 template <int D>
@@ -144,6 +152,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
             s_page[warp] = page;
         }
     }
+    check_sequences(p);
     __syncthreads();
 
     const int group = threadIdx.x / per, groups = kAppendThreads / per;
@@ -329,6 +338,7 @@ __global__ void __launch_bounds__(32 * kStreamPlaces, 2)
             __syncwarp();
         }
     }
+    check_sequences(p);
     bulk_wait_all();
 }
 
