@@ -343,9 +343,10 @@ def make_paged_kv(k_pool, v_pool, page_table, kv_lens) -> np.ndarray:
             raise ValueError(f"make_paged_kv: {n} must be contiguous")
     if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
         raise ValueError("make_paged_kv: k_pool and v_pool are [num_pages, Hkv, page_size, d]")
-    if k_pool.element_size() != 2 or v_pool.dtype != k_pool.dtype:
+    import torch
+    if k_pool.dtype != torch.bfloat16 or v_pool.dtype != torch.bfloat16:
         raise ValueError("make_paged_kv: the pools are bfloat16")
-    if page_table.dim() != 2 or page_table.element_size() != 4 or kv_lens.element_size() != 4 \
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or kv_lens.dtype != torch.int32 \
             or kv_lens.numel() != page_table.shape[0]:
         raise ValueError("make_paged_kv: page_table is int32 [nseq, max_pages], kv_lens int32 "
                          "[nseq]")
