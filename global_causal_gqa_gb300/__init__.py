@@ -341,6 +341,8 @@ def make_paged_kv(k_pool, v_pool, page_table, kv_lens) -> np.ndarray:
                  (kv_lens, "kv_lens")):
         if not t.is_contiguous():
             raise ValueError(f"make_paged_kv: {n} must be contiguous")
+    if len({t.device for t in (k_pool, v_pool, page_table, kv_lens)}) > 1:
+        raise ValueError("make_paged_kv: the tensors lie on one device")
     if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
         raise ValueError("make_paged_kv: k_pool and v_pool are [num_pages, Hkv, page_size, d]")
     import torch

@@ -133,9 +133,13 @@ class PagedStack:
         self.max_q, self.max_kv, self.Hq, self.Hkv, self.d = max_q, max_kv, Hq, Hkv, d
         self.scale, self.eps = scale, eps
         self.nseq, self.total = page_table.shape[0], layers[0].qkv.shape[0]
-        if cu_seqlens.shape != (self.nseq + 1,) or cu_seqlens.dtype != torch.int32:
-            raise ValueError("PagedStack: cu_seqlens is int32 [nseq + 1]")
+        if cu_seqlens.shape != (self.nseq + 1,) or cu_seqlens.dtype != torch.int32 or \
+                not cu_seqlens.is_contiguous():
+            raise ValueError("PagedStack: cu_seqlens is contiguous int32 [nseq + 1]")
         for i, L in enumerate(layers):
+            if any(t is not None and t.device != page_table.device for t in
+                   (cu_seqlens, L.k_pool, L.qkv, L.o, L.q_gamma, L.k_gamma, L.table)):
+                raise ValueError(f"PagedStack: layer {i}: the tensors lie on one device")
             for t, name, shape in ((L.qkv, "qkv", (self.total, (Hq + 2 * Hkv) * d)),
                                    (L.o, "o", (self.total, Hq, d))):
                 if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or not t.is_contiguous():
