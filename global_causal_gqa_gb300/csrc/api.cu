@@ -475,7 +475,9 @@ gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64
     if (!q || !k || !v || !o || !cu_seqlens || nseq <= 0 || total <= 0 || Hq <= 0 || Hkv <= 0 ||
         (Hq % Hkv) != 0 || !(scale > 0.f) || !std::isfinite(scale))
         return GQA_ERR_INVALID_ARG;
-    if (d != 128 || Hq / Hkv > 64 || total > kMostKeys) return GQA_ERR_UNSUPPORTED;
+    if (d != 128 || Hq / Hkv > 64 || total > kMostKeys ||
+        !gqa::packed_prefill_counts_fit(nseq, total, 0, Hq, Hkv))
+        return GQA_ERR_UNSUPPORTED;
     if (!stride_ok(q_stride, Hq, d) || !stride_ok(k_stride, Hkv, d) ||
         !stride_ok(v_stride, Hkv, d) || !stride_ok(o_stride, Hq, d) || o == q || o == k || o == v)
         return GQA_ERR_INVALID_ARG;
@@ -498,7 +500,9 @@ static gqa_status check_paged_shape(int nseq, int total, int max_q, int max_kv, 
     if (nseq <= 0 || total <= 0 || max_q <= 0 || max_kv < max_q || Hq <= 0 || Hkv <= 0 || d <= 0 ||
         (Hq % Hkv) != 0)
         return GQA_ERR_INVALID_ARG;
-    if (d != 128 || Hq / Hkv > 64 || max_kv > kMostKeys) return GQA_ERR_UNSUPPORTED;
+    if (d != 128 || Hq / Hkv > 64 || max_kv > kMostKeys || total > kMostKeys ||
+        !gqa::paged_counts_fit(nseq, total, max_q, max_kv, Hq, Hkv))
+        return GQA_ERR_UNSUPPORTED;
     return GQA_OK;
 }
 

@@ -151,10 +151,13 @@ struct PackedAttn {
 // the tensor-core kernel for prompts and chunks (packed_prefill.cu); returns a gqa_status
 int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
 size_t packed_prefill_workspace_bytes(int nseq, int total, int max_kv, int Hq, int Hkv);
+// whether the items fit 32 bits (max_kv = 0: packed prompts)
+bool packed_prefill_counts_fit(int nseq, int total, int max_kv, int Hq, int Hkv);
 // the streaming kernel for a few rows per sequence (paged_decode.cu)
 bool paged_decode_fits(int max_q, int G);
 int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
 size_t paged_decode_workspace_bytes(int nseq, int max_kv, int Hkv);
+bool paged_decode_counts_fit(int nseq, int max_kv, int Hkv);
 // A TMA map of bf16 elements: `rank` dims and box extents, innermost first, the strides of
 // dims 1 .. rank - 1 in bytes, 128-byte swizzle; false if the driver refuses it
 // (packed_attn.cu)
@@ -162,6 +165,8 @@ bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t 
                    const uint64_t *strides, const uint32_t *box);
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
 size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv);
+// whether the work of such a call can be counted in 32 bits, as its kernels do
+bool paged_counts_fit(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv);
 
 // Bounded-wait self-test (watchdog.cu)
 cudaError_t launch_watchdog_selftest(int64_t limit_ns, int *status, cudaStream_t s);

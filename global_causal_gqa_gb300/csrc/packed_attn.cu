@@ -53,6 +53,12 @@ size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
                : packed_prefill_workspace_bytes(nseq, total, max_kv, Hq, Hkv);
 }
 
+bool paged_counts_fit(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv) {
+    return paged_decode_fits(max_q, Hq / Hkv)
+               ? paged_decode_counts_fit(nseq, max_kv, Hkv)
+               : packed_prefill_counts_fit(nseq, total, max_kv, Hq, Hkv);
+}
+
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
     if (a.cache && paged_decode_fits(a.max_q, a.Hq / a.Hkv))
         return launch_paged_decode(a, ws, status, s);

@@ -1232,12 +1232,31 @@ SpanRule span_rule(int nseq, int total, int max_kv, int Hq, int Hkv, int window)
     return {per, n_spans(tiles, per)};
 }
 
+// The numbers of a grid: an upper bound on the items (a sequence adds at most one block that is
+// not full), and one more: the CTA that gets it walks past the last sequence, so that all of them
+// have been looked over (one that passes the rows has no item that would lead to it).  -1: more
+// than 32 bits hold.
+long n_numbers(int nseq, int total, int Hq, int Hkv, int spans) {
+    const int ntok = 2 * (kBM / (Hq / Hkv));
+    const long blocks = (long)total / ntok + (nseq < total ? nseq : total), most = 0x7ffffffeL;
+    if (blocks > most || blocks * Hkv > most || blocks * Hkv * spans > most) return -1;
+    return blocks * Hkv * spans + 1;
+}
+
 }  // namespace
 
 size_t packed_prefill_workspace_bytes(int nseq, int total, int max_kv, int Hq, int Hkv) {
     const int tiles = most_tiles(max_kv, 2 * (kBM / (Hq / Hkv)), 0);
     const int n = best_spans(nseq, total, tiles, Hq, Hkv, kMostSpans);
     return n <= 1 ? 0 : (size_t)n * total * Hq * (kD + 2) * sizeof(float);
+}
+
+bool packed_prefill_counts_fit(int nseq, int total, int max_kv, int Hq, int Hkv) {
+    // packed prompts have one span; else the rule is asked only where the most would not do, and
+    // without a window, which only lowers the number of spans
+    if (max_kv == 0) return n_numbers(nseq, total, Hq, Hkv, 1) > 0;
+    return n_numbers(nseq, total, Hq, Hkv, kMostSpans) > 0 ||
+           n_numbers(nseq, total, Hq, Hkv, span_rule(nseq, total, max_kv, Hq, Hkv, 0).spans) > 0;
 }
 
 int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
@@ -1259,7 +1278,6 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.q_box_bytes = 64 * 2 * p.G * p.Mt;
     p.bounds = {a.total, a.max_q, a.max_kv, 0x7fffffffL};
-    const int ntok = 2 * p.Mt;
     int spans = 1;
     CUtensorMap mq, mk, mv, mo;
     {
@@ -1307,12 +1325,8 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
     auto kern = paged ? packed_prefill_kernel<true> : packed_prefill_kernel<false>;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes) != cudaSuccess)
         return GQA_ERR_CUDA;
-    // an upper bound on the items: a sequence adds at most one block that is not full
-    const long blocks = (long)a.total / ntok + (a.nseq < a.total ? a.nseq : a.total);
-    // and one number more: the CTA that gets it walks past the last sequence, so that all of them
-    // have been looked over (one that passes the rows has no item that would lead to it)
-    const long grid = blocks * a.Hkv * spans + 1;
-    if (grid > 0x7fffffffL) return GQA_ERR_UNSUPPORTED;
+    // (the entry points have seen that it fits 32 bits)
+    const long grid = n_numbers(a.nseq, a.total, a.Hq, a.Hkv, spans);
     if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, mq, mk,
                    mv, mo, p) != cudaSuccess)
         return GQA_ERR_CUDA;

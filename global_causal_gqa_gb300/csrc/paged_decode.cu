@@ -910,6 +910,12 @@ size_t paged_decode_workspace_bytes(int nseq, int max_kv, int Hkv) {
     return 2 * chunks * kMaxRows * (kD + 2) * sizeof(float) + chunks * sizeof(Joint);
 }
 
+// Units are counted in 32 bits (the last level of chunks may pass the end by kSMs - 1).
+bool paged_decode_counts_fit(int nseq, int max_kv, int Hkv) {
+    const long pairs = (long)nseq * Hkv, most = 0x7fffffffL - kSMs;
+    return pairs <= most && pairs * ((max_kv + kUnit - 1) / kUnit) <= most;
+}
+
 int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
     const gqa_paged_kv &c = *a.cache;
     Params p{};
@@ -935,9 +941,6 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
     p.max_pages = c.max_pages;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.whole = whole_pairs(a.max_kv);
-    // units are counted in 32 bits
-    if ((long)a.nseq * a.Hkv * ((a.max_kv + kUnit - 1) / kUnit) > 0x7fffffffL - kSMs)
-        return GQA_ERR_UNSUPPORTED;
     if (!p.whole) {
         p.chunks = n_chunks(a.nseq, a.max_kv, a.Hkv, a.max_q, a.window);
         const size_t rec = (size_t)2 * p.chunks * kMaxRows;

@@ -380,9 +380,13 @@ gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64
  * after RoPE, o [total, Hq, d], lse as for gqa_attn_packed.  max_q and max_kv: upper bounds on
  * T and S over the batch; they and the shape choose the kernel and its split of the keys, and
  * size the workspace (gqa_attn_paged_workspace_bytes with the same arguments; 0 = none
- * needed, or a shape that the call refuses).  Its contents need no initialisation; calls that may overlap need one each.  Every
- * result is the same on every run of the same call.  d = 128; Hq / Hkv an integer of at most
- * 64; max_q <= max_kv <= 2^30. */
+ * needed, or a shape that the call refuses).  Its contents need no initialisation; calls that
+ * may overlap need one each.  Every result is the same on every run of the same call.  d = 128; G = Hq / Hkv an integer of at most
+ * 64; max_q <= max_kv <= 2^30, total <= 2^30.  The work of a call is counted in 32 bits: with
+ * max_q * G <= 16, nseq * Hkv * ceil(max_kv / 64) is at most 2^31 - 153; with more rows,
+ * (floor(total / (2 floor(128 / G))) + min(nseq, total)) * Hkv times the spans of the keys (up to
+ * 64; 1 for gqa_attn_packed) at most 2^31 - 2.  Bounds beyond these return
+ * GQA_ERR_UNSUPPORTED. */
 size_t gqa_attn_paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
                                       int Hkv, int d);
 gqa_status gqa_attn_paged(const void *q, int64_t q_stride, const gqa_paged_kv *cache,
