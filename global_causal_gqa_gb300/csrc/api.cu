@@ -442,7 +442,8 @@ gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k
         (with_q && Hq <= 0) || Hkv <= 0 || table_len <= 0 || !(eps >= 0.f) ||
         !std::isfinite(eps))
         return GQA_ERR_INVALID_ARG;
-    if (!rope_dim_ok(d)) return GQA_ERR_UNSUPPORTED;
+    // (the grid is counted in 32 bits)
+    if (!rope_dim_ok(d) || total > 0x7fffffff - 512) return GQA_ERR_UNSUPPORTED;
     if ((with_q && !stride_ok(q_stride, Hq, d)) || !stride_ok(k_stride, Hkv, d) ||
         (cache && !stride_ok(v_stride, Hkv, d)))
         return GQA_ERR_INVALID_ARG;

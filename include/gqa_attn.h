@@ -351,7 +351,7 @@ typedef struct gqa_paged_kv {
  * (Hq ignored).  cache NULL: no cache is written, v is not read and may be NULL, and every
  * sequence starts at position 0 (the prompts of gqa_attn_packed).  With a cache, Hkv and d
  * must be the cache's.  A position at or past table_len records GQA_ERR_RANGE and its token
- * is skipped.  d in {64, 128, 256, 512}.  One kernel.  Two sequences of one call must not
+ * is skipped.  d in {64, 128, 256, 512}; total <= 2^31 - 513.  One kernel.  Two sequences of one call must not
  * append to the same page. */
 gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k,
                                   int64_t k_stride, const void *v, int64_t v_stride,

@@ -56,3 +56,9 @@ def test_packed_prompts():
                                    128, 0, 1.0, stream=1, check=False)
     assert call(2 ** 28, 2 ** 28, 8) == -2
     assert call(M, 2 ** 30, 2 ** 24) == -2
+
+
+@pytest.mark.parametrize("total", [M - 511, M - 63, M])
+def test_append_rows(total):
+    assert gqa.gqa_packed_rope_append(None, 0, P, 64, None, 0, P, 2, total, 0, 1, 64, None, None, 0.0,
+                                      P, 64, None, 2 * P, None, stream=1, check=False) == -2
