@@ -99,6 +99,16 @@ struct Rotation {
     }
 };
 
+constexpr int kSite = kDiagCache << 24;   // of the debug build's checks
+// Whether a token's rows and its table row are where they may be (the debug build's check).
+__device__ __forceinline__ bool token_in_bounds(const AppendParams &p, long row, int pos) {
+    return GQA_IN_BOUNDS(row, p.bounds.total, p.status, kSite | 7) &&
+           GQA_IN_BOUNDS(pos, p.table_len, p.status, kSite | 8);
+}
+__device__ __forceinline__ bool slot_in_bounds(const AppendParams &p, long slot) {
+    return GQA_IN_BOUNDS(slot, (long)p.num_pages * p.Hkv * p.page_size, p.status, kSite | 9);
+}
+
 // What a token at `row` of sequence i meets: its position (-1: nothing to do for it) and its
 // page (-1: outside the pool).
 __device__ __forceinline__ void find_token(const AppendParams &p, int row, int i, int &pos, int &page) {
@@ -110,7 +120,7 @@ __device__ __forceinline__ void find_token(const AppendParams &p, int row, int i
     if (pos >= p.table_len) {
         set_status(p.status, GQA_ERR_RANGE);
         pos = -1;
-    } else if (p.pages) {
+    } else if (p.pages && GQA_IN_BOUNDS(pos / p.page_size, p.max_pages, p.status, kSite | 6)) {
         page = __ldg(p.pages + (long)i * p.max_pages + pos / p.page_size);
         if (page < 0 || page >= p.num_pages) {
             set_status(p.status, GQA_ERR_INVALID_ARG);
@@ -162,6 +172,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
         const int pos = s_pos[t], page = s_page[t];
         if (pos < 0) continue;   // the same for the whole group, which is whole vectors
         const long row = row_base + t;
+        if (!token_in_bounds(p, row, pos)) continue;
         Rotation rot;
         const float4 *tr = p.table + (long)pos * (D / 4) + 4 * c;
 #pragma unroll
@@ -200,7 +211,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
             if (p.k_gamma) normalise(v, p.k_gamma, isk);
             if (isk) rot.apply(v, a, b);
             if (ub + u0 >= heads) continue;
-            if (page >= 0 && p.k_pool) {
+            if (page >= 0 && p.k_pool && slot_in_bounds(p, slot + (long)g * p.page_size)) {
                 uint4 *d = (isk ? p.k_pool : p.v_pool) + (slot + (long)g * p.page_size) * C + c;
                 d[0] = a;
                 d[L] = b;
@@ -277,6 +288,7 @@ __global__ void __launch_bounds__(32 * kStreamPlaces, 2)
             const long row = r0 + token;
             const int tpos = __shfl_sync(0xffffffffu, pos, j);
             const int tpage = __shfl_sync(0xffffffffu, page, j);
+            if (!token_in_bounds(p, row, tpos)) continue;
             // vectors [v0, v1): q heads up to q1, k heads (from nq) up to k1, v heads (from nk)
             const int v0 = (unit - token * parts) * per, v1 = min(v0 + per, nv);
             const int q1 = max(v0, min(v1, nq)), k1 = max(q1, min(v1, nk));
@@ -331,6 +343,7 @@ __global__ void __launch_bounds__(32 * kStreamPlaces, 2)
                     const int g = i < nk ? i - nq : i - nk;
                     const long slot =
                         ((long)tpage * p.Hkv + g) * p.page_size + (tpos & (p.page_size - 1));
+                    if (!slot_in_bounds(p, slot)) continue;
                     bulk_store((i < nk ? p.k_pool : p.v_pool) + slot * C, place + (i - v0) * kVec, kVec);
                 }
             bulk_commit_group();

@@ -145,6 +145,7 @@ struct Params {
     int nseq, Hq, Hkv, G, Mt, window;    // Mt = 128 / G tokens per tile
     int num_pages, page_size, max_pages;
     int split_tiles;               // key tiles of a span; 0: items are not split
+    int spans;                     // most spans of an item
     int q_box_bytes;               // bytes of one Q box
     float scale_log2;
 };
@@ -179,6 +180,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
 }
 
 enum Role { kRoleProducer = 0, kRoleMma = 1, kRoleSoftmax = 2, kRoleAux = 3 };
+constexpr int kSite = kDiagPacked << 24;   // of the debug build's checks
 
 // The producer's walk over the sequences: one block of 32 in the lanes at a time.
 struct Walk {
@@ -281,10 +283,13 @@ template <bool PAGED>
 __device__ __forceinline__ const __nv_bfloat16 *value_row(const Params &p, const ItemRec &it,
                                                           int key) {
     if constexpr (!PAGED) {
+        if (!GQA_IN_BOUNDS(it.kv_row0 + key, p.bounds.total, p.status, kSite | 1)) return p.v;
         return p.v + (long)(it.kv_row0 + key) * p.v_stride + it.g * kD;
     } else {
         // a marked key came from a page inside the pool (anything else is read as zeros)
+        if (!GQA_IN_BOUNDS(key / p.page_size, p.max_pages, p.status, kSite | 2)) return p.v;
         const int page = p.pages[(long)it.seq * p.max_pages + key / p.page_size];
+        if (!GQA_IN_BOUNDS(page, p.num_pages, p.status, kSite | 1)) return p.v;
         return p.v + (((long)page * p.Hkv + it.g) * p.page_size + key % p.page_size) * kD;
     }
 }
@@ -535,9 +540,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok || next.n_tiles < 0) break;
                 it = next;
-                if constexpr (PAGED)
+                if constexpr (PAGED) {
+                    const int last = (it.qpos0 + it.ntok - 1) / p.page_size;
+                    // (out of bounds: no entry is read, every key is zero fill)
+                    const bool in = GQA_IN_BOUNDS(last, p.max_pages, p.status, kSite | 2);
                     pages = PageWalk(p.pages + (long)it.seq * p.max_pages, it.kt_first * npg,
-                                     (it.qpos0 + it.ntok - 1) / p.page_size + 1);
+                                     in ? last + 1 : 0);
+                }
             }
             if (!ok) {
                 // never leave the CTA with copies in flight
@@ -1046,7 +1055,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = it.row0 + wg * p.Mt + rtok, head = it.g * p.G + rhead;
             if (PAGED && it.split >= 0) {
                 // a span of the keys: the unnormalised row with its maximum (log2) and sum
-                if (valid) {
+                const bool in = GQA_IN_BOUNDS(it.split, p.spans, p.status, kSite | 3) &&
+                                GQA_IN_BOUNDS(valid ? row : 0, p.bounds.total, p.status, kSite | 4);
+                if (valid && in) {
                     const size_t rec = (size_t)it.split * p.bounds.total * p.Hq + (size_t)row * p.Hq + head;
                     float4 *dst = reinterpret_cast<float4 *>(p.ws_o + rec * kD);
 #pragma unroll
@@ -1085,7 +1096,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < rows; i += 2) {
                         const int ii = i + (lane >> 4), rr = r0 + ii;
                         const long at = __shfl_sync(0xffffffffu, mine, ii);
-                        if (ii >= rows) continue;
+                        if (ii >= rows || !GQA_IN_BOUNDS(at / p.o_stride, p.bounds.total, p.status, kSite | 4))
+                            continue;
                         const uint4 y = *reinterpret_cast<const uint4 *>(
                             stage + (c >> 3) * kBoxBytes + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
                         *reinterpret_cast<uint4 *>(p.o + at + 8 * c) = y;
@@ -1097,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 mbar_arrive(&bars->staged[wg][ns & 1]);
                 ++ns;
-                if (valid && p.lse)
+                if (valid && p.lse && GQA_IN_BOUNDS(row, p.bounds.total, p.status, kSite | 4))
                     p.lse[(size_t)head * p.bounds.total + row] =
                         (m + __log2f(l)) * 0.69314718055994531f;
             }
@@ -1142,7 +1154,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) packed_combine_kernel(cons
 #pragma unroll
     for (int t = 0; t < kMostSpans / 32; ++t) {
         x[t] = make_float2(-CUDART_INF_F, 0.f);
-        if (32 * t + lane < spans) x[t] = ml[rec + (32 * t + lane) * step];
+        if (32 * t + lane < spans && GQA_IN_BOUNDS(32 * t + lane, p.spans, p.status, kSite | 5))
+            x[t] = ml[rec + (32 * t + lane) * step];
         M = fmaxf(M, x[t].x);
     }
 #pragma unroll
@@ -1160,7 +1173,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) packed_combine_kernel(cons
 #pragma unroll
             for (int k = 0; k < kFlight; ++k) {
                 o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k0 + k < n)
+                if (k0 + k < n && GQA_IN_BOUNDS(32 * t + k0 + k, p.spans, p.status, kSite | 5))
                     o[k] = reinterpret_cast<const float4 *>(p.ws_o + (rec + (32 * t + k0 + k) * step) * kD)[lane];
             }
 #pragma unroll
@@ -1299,7 +1312,7 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
         p.bounds.cap = (long)c.max_pages * c.page_size;
         const SpanRule r = span_rule(a.nseq, a.total, a.max_kv, a.Hq, a.Hkv, a.window);
         p.split_tiles = r.split_tiles;
-        spans = r.spans;
+        p.spans = spans = r.spans;
         if (spans > 1) {
             // the outputs come first (16-byte aligned), then the maxima and sums
             p.ws_o = static_cast<float *>(ws);

@@ -216,6 +216,7 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
 }
 
 enum Role { kRoleProducer = 0, kRoleConsumer = 2 };
+constexpr int kSite = kDiagPagedDecode << 24;   // of the debug build's checks
 
 // ROWS: the most rows of a pair, 8 or 16.
 template <int ROWS>
@@ -343,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Claims chunks until one has work; run = 0: there is none.
         auto next_chunk = [&]() {
             while (run == 0) {
-                if (lane == 0) p.ws_joint[chunk] = joint;
+                if (lane == 0 && GQA_IN_BOUNDS(chunk, p.chunks, p.status, kSite | 1))
+                    p.ws_joint[chunk] = joint;
                 if (p.chunks == kSMs) return;   // a chunk per CTA
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bars->clc_full, 16);
@@ -426,6 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             if (ahead.stages < 0) return;
+            if (!GQA_IN_BOUNDS(ahead.S - 1 >> p.page_shift, p.max_pages, p.status, kSite | 2))
+                ahead.S = 0;   // no entry is read, every key is zero fill
             walk_ahead = PageWalk(p.pages + (long)ahead.seq * p.max_pages,
                                   ahead.unit0 * kUnit >> p.page_shift,
                                   (ahead.S - 1 >> p.page_shift) + 1);
@@ -549,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 qb[ks][h] = qb[ks][HR + h] = 0u;
-                if (r < rows) {
+                if (r < rows && GQA_IN_BOUNDS(sg.row0 + t, p.bounds.total, p.status, kSite | 3)) {
                     qb[ks][h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks));
                     qb[ks][HR + h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks + 8));
                 }
@@ -782,11 +786,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (out >= 0) {
                     const size_t rec = (size_t)out * kMaxRows + r;
+                    if (!GQA_IN_BOUNDS(rec, (long)2 * p.chunks * kMaxRows, p.status, kSite | 4)) continue;
                     reinterpret_cast<float4 *>(p.ws_o + rec * kD)[lane] = acc;
                     if (lane == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(M, L);
                 } else {
                     const int t = token_of(p, r), head = head0 + r - t * p.G;
                     const long row = row0 + t;
+                    if (!GQA_IN_BOUNDS(row, p.bounds.total, p.status, kSite | 5)) continue;
                     const float inv = 1.0f / L;
                     reinterpret_cast<uint2 *>(p.o + row * p.o_stride + head * kD)[lane] = make_uint2(
                         pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -818,7 +824,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_ke
     auto rec = [&](int k) { return (size_t)(2 * (c + k) + (k == 0 ? 1 : 0)) * kMaxRows + r; };
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml);
     float2 x = make_float2(-CUDART_INF_F, 0.f);
-    if (r < kMaxRows && c + lane < p.chunks) x = ml[rec(lane)];   // used if the record says so
+    const long n_rec = (long)2 * p.chunks * kMaxRows;
+    if (r < kMaxRows && c + lane < p.chunks && GQA_IN_BOUNDS(rec(lane), n_rec, p.status, kSite | 6))
+        x = ml[rec(lane)];   // used if the record says so
     const Joint j = p.ws_joint[c];
     // (a chunk that an expired wait left out has no record: what its place holds is checked)
     const bool on = r < j.rows && j.rows <= kMaxRows && j.parts >= 2 && j.parts <= p.chunks - c &&
@@ -829,11 +837,15 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_ke
     if (on) {
         if (lane >= j.parts) x = make_float2(-CUDART_INF_F, 0.f);
         M = x.x;
-        for (int i = 32 + lane; i < j.parts; i += 32) M = fmaxf(M, ml[rec(i)].x);
+        for (int i = 32 + lane; i < j.parts; i += 32)
+            if (GQA_IN_BOUNDS(rec(i), n_rec, p.status, kSite | 6)) M = fmaxf(M, ml[rec(i)].x);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
         for (int i = 0; i < j.parts; i += 32) {
-            if (i > 0) x = i + lane < j.parts ? ml[rec(i + lane)] : make_float2(-CUDART_INF_F, 0.f);
+            if (i > 0)
+                x = i + lane < j.parts && GQA_IN_BOUNDS(rec(i + lane), n_rec, p.status, kSite | 6)
+                        ? ml[rec(i + lane)]
+                        : make_float2(-CUDART_INF_F, 0.f);
             // a partial none of whose keys this row sees: m = -inf, l = 0 and O = 0 (NaN scores
             // alone also leave m at -inf, with l and O NaN)
             const float f = x.x == -CUDART_INF_F ? (x.y == 0.f ? 0.f : 1.f) : ex2_approx(x.x - M);
@@ -845,7 +857,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_ke
                 for (int k = 0; k < kFlight; ++k) {
                     const int q = q0 + k * W;
                     y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (q < n) y[k] = reinterpret_cast<const float4 *>(p.ws_o + rec(i + q) * kD)[lane];
+                    if (q < n && GQA_IN_BOUNDS(rec(i + q), n_rec, p.status, kSite | 6))
+                        y[k] = reinterpret_cast<const float4 *>(p.ws_o + rec(i + q) * kD)[lane];
                 }
 #pragma unroll
                 for (int k = 0; k < kFlight; ++k) {
@@ -876,6 +889,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_ke
     if (!on) return;
     const int t = token_of(p, r), h = j.g * p.G + r - t * p.G;
     const long row = j.row0 + t;
+    if (!GQA_IN_BOUNDS(row, p.bounds.total, p.status, kSite | 7)) return;
     const float inv = 1.0f / L;
     reinterpret_cast<uint2 *>(p.o + row * p.o_stride + h * kD)[lane] =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));

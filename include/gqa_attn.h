@@ -406,7 +406,8 @@ gqa_status gqa_get_device_status(gqa_stream_t stream);
  * (kernel << 24) | (role << 20) | (barrier << 16) | (tile index & 0xffff), kernel 1 =
  * prefill d=128, 2 = prefill d=256, 3 = decode, 4 = gqa_watchdog_selftest,
  * 5 = prefill d=512 (a pair of CTAs), 6 = cache append, chunk gather, RoPE pass, Q/K
- * normalisation, 7 = packed / paged prefill, 8 = paged decode.  A library compiled with -DGQA_DEBUG_BOUNDS checks the indices of the
+ * normalisation, packed append, 7 = packed / paged prefill, 8 = paged decode.  A library
+ * compiled with -DGQA_DEBUG_BOUNDS checks the indices of the
  * global accesses it derives from device-side data; the first failed check records
  * GQA_ERR_DEVICE_BOUNDS and, in diag[0], (kernel << 24) | (1 << 23) | site, and the access
  * is skipped.  For diagnosing device-side errors; gqa_get_device_status leaves the codes
