@@ -19,8 +19,9 @@ struct InvFreq {
 // kernel's tail.  The kernel must call griddep_wait() before it reads anything an earlier
 // kernel on the stream wrote (the decode step's append -> partial -> combine chain).
 // Not while the stream is being captured into a CUDA graph: a graph already launches
-// back to back, and with programmatic edges the 64-layer decode step ran 1% slower
-// (eagerly it runs 7% faster with them).
+// back to back, and with programmatic edges the 64-layer decode step over linear caches ran
+// 1% slower (eagerly it runs 7% faster with them; the packed and paged calls' chain was not
+// measured with such edges).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                        cudaStream_t s, Args... args) {

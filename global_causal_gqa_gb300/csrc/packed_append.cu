@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
 // The same for a batch that keeps every SM busy for long: a CTA streams its run of tokens
 // through shared memory.  A unit of work is a token, or one of `parts` runs of its vectors (q
 // heads, k heads, v heads, `per` of them each) where a whole token would take too much of it.
-// Each warp has a place of its own for the vectors and the table row and takes every 16th unit:
+// Each warp has a place of its own for the vectors and the table row and takes every 8th unit:
 // bulk copies in, norm and rotation in place, bulk copies out, q and k_out as they lie, keys and
 // values head by head to their page.  Runs are short where there are many, since equal runs are
 // not equal times (one run per SM for the 16384 tokens: 131 us); three blocks of 74 KB per SM

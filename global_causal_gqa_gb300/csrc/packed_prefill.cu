@@ -44,8 +44,8 @@
 // the rows that see it.  The softmax warps hand P over only when the guard is done with the
 // tile, so the MMA thread, which has no time to spare, knows nothing of it.
 //
-// Measured (GB300, 64 heads on 8): a prompt of 16384 tokens 3.05 ms, 1440 TFLOP/s; prompts of
-// 2500-8192 with a window of 2048 1.07 ms, 1300; 16 prompts of 33-2000 160 us.  A key tile's
+// Measured (GB300, 64 heads on 8): a prompt of 16384 tokens 3.11 ms, 1410 TFLOP/s; prompts of
+// 2500-8192 with a window of 2048 1.10 ms, 1245; 16 prompts of 33-2000 162 us.  A key tile's
 // four products take 2048 cycles of the tensor pipe, the period is about 3300: the chain of
 // one tile (score product, softmax, value product, and the next score product, which waits
 // for it because P lies in S's columns), each link with its hand-over.

@@ -37,7 +37,7 @@
 // it by 2^8 (exact: sum and O share the reference).  At the end of a pair a group's warps merge
 // through shared memory.
 //
-// Measured (GB300): 32 caches of 8k-64k tokens, 8 KV heads, 64-token pages: 740-753 us, 7.2 TB/s.
+// Measured (GB300): 32 caches of 8k-64k tokens, 8 KV heads, 64-token pages: 740-752 us, 7.2-7.3 TB/s.
 //
 // Hidden keys have weight 0, but 0 * NaN is NaN: in blocks that straddle an edge of the mask
 // the values of keys that no row sees are zeroed on their way into the product, and

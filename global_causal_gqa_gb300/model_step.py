@@ -123,7 +123,9 @@ class PagedStack:
     gqa_attn_paged.  cu_seqlens (int32 [nseq + 1]), kv_lens (int32 [nseq], counted with the new
     tokens) and page_table (int32 [nseq, max_pages], used by every layer with its own pools)
     are device tensors read when the kernels run: a captured step follows what the caller
-    writes to them between replays, up to max_q new tokens and max_kv tokens of a sequence."""
+    writes to them between replays, up to max_q new tokens and max_kv tokens of a sequence.
+    Chunks run fastest with a max_kv near the longest sequence.  A stack has one workspace and
+    one tensor of rotated queries: its steps, eager or replayed, must not overlap."""
 
     def __init__(self, layers: List[PagedLayer], cu_seqlens, kv_lens, page_table, max_q: int,
                  max_kv: int, Hq: int, Hkv: int, d: int, scale: float, eps: float = 1e-6):

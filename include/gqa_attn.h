@@ -31,7 +31,8 @@
  *     out of range) are recorded in the device status word and returned by the next
  *     gqa_get_device_status().  Device code never traps.
  *   - Stream order holds as for any kernel.  On a stream that is not being captured,
- *     gqa_kv_append and the decode calls launch with programmatic stream serialization
+ *     gqa_kv_append, the decode calls and the packed and paged calls launch with programmatic
+ *     stream serialization
  *     and let the next kernel begin launching early.  Each of their kernels waits for its
  *     predecessor before reading.  A caller's own kernel launched after them with that
  *     attribute must likewise execute griddepcontrol.wait (cudaGridDependencySynchronize)
@@ -350,7 +351,7 @@ typedef struct gqa_paged_kv {
  * may be q (k_out may be k) if that tensor's stride is dense.  q and q_out are NULL together
  * (Hq ignored).  cache NULL: no cache is written, v is not read and may be NULL, and every
  * sequence starts at position 0 (the prompts of gqa_attn_packed).  With a cache, Hkv and d
- * must be the cache's.  A position at or past table_len records GQA_ERR_RANGE and its token
+ * must be the cache's.  (The library's own attention over such a cache takes d = 128.)  A position at or past table_len records GQA_ERR_RANGE and its token
  * is skipped.  d in {64, 128, 256, 512}; total <= 2^31 - 513.  One kernel.  Two sequences of one call must not
  * append to the same page. */
 gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k,
@@ -378,8 +379,10 @@ gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64
  * to keys j <= S - T + t (window > 0: also with S - T + t - j < window; pages that lie wholly
  * below every window are not read and their table entries may be stale).  q [total, Hq, d]
  * after RoPE, o [total, Hq, d], lse as for gqa_attn_packed.  max_q and max_kv: upper bounds on
- * T and S over the batch; they and the shape choose the kernel and its split of the keys, and
- * size the workspace (gqa_attn_paged_workspace_bytes with the same arguments; 0 = none
+ * T and S over the batch (bounds far above them split the keys of chunks more coarsely, which
+ * costs time; a decode step is one kernel up to max_kv = 512, two beyond, and depends little on
+ * it otherwise); they and the shape choose the kernel and its
+ * split of the keys, and size the workspace (gqa_attn_paged_workspace_bytes with the same arguments; 0 = none
  * needed, or a shape that the call refuses).  Its contents need no initialisation; calls that
  * may overlap need one each.  Every result is the same on every run of the same call.  d = 128; G = Hq / Hkv an integer of at most
  * 64; max_q <= max_kv <= 2^30, total <= 2^30.  The work of a call is counted in 32 bits: with
