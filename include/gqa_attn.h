@@ -351,9 +351,10 @@ typedef struct gqa_paged_kv {
  * may be q (k_out may be k) if that tensor's stride is dense.  q and q_out are NULL together
  * (Hq ignored).  cache NULL: no cache is written, v is not read and may be NULL, and every
  * sequence starts at position 0 (the prompts of gqa_attn_packed).  With a cache, Hkv and d
- * must be the cache's.  (The library's own attention over such a cache takes d = 128.)  A position at or past table_len records GQA_ERR_RANGE and its token
- * is skipped.  d in {64, 128, 256, 512}; total <= 2^31 - 513.  One kernel.  Two sequences of one call must not
- * append to the same page. */
+ * must be the cache's.  (The library's own attention over such a cache takes d = 128.)  A
+ * position at or past table_len records GQA_ERR_RANGE and its token is skipped.  d in {64, 128,
+ * 256, 512}; total <= 2^31 - 513.  One kernel.  Two sequences of one call must not append to the
+ * same page. */
 gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k,
                                   int64_t k_stride, const void *v, int64_t v_stride,
                                   const int32_t *cu_seqlens, int nseq, int total, int Hq,
@@ -367,7 +368,8 @@ gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k
  * [total, Hkv, d], o [total, Hq, d] with token strides; o may not alias an input.  lse
  * [Hq, total] float32 natural-log sum of exp of the scaled scores, or NULL.  scale finite and
  * > 0.  A row never depends on keys or values that its mask hides, not even through NaN or
- * infinities in them.  A row whose visible scores are all -inf is NaN, its lse -inf.  d = 128; Hq / Hkv an integer of at most 64; total <= 2^30. */
+ * infinities in them.  A row whose visible scores are all -inf is NaN, its lse -inf.  d = 128;
+ * Hq / Hkv an integer of at most 64; total <= 2^30 (and see the limit on counts below). */
 gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                            const void *v, int64_t v_stride, void *o, int64_t o_stride,
                            float *lse, const int32_t *cu_seqlens, int nseq, int total, int Hq,
@@ -381,14 +383,14 @@ gqa_status gqa_attn_packed(const void *q, int64_t q_stride, const void *k, int64
  * after RoPE, o [total, Hq, d], lse as for gqa_attn_packed.  max_q and max_kv: upper bounds on
  * T and S over the batch (bounds far above them split the keys of chunks more coarsely, which
  * costs time; a decode step is one kernel up to max_kv = 512, two beyond, and depends little on
- * it otherwise); they and the shape choose the kernel and its
- * split of the keys, and size the workspace (gqa_attn_paged_workspace_bytes with the same arguments; 0 = none
- * needed, or a shape that the call refuses).  Its contents need no initialisation; calls that
- * may overlap need one each.  Every result is the same on every run of the same call.  d = 128; G = Hq / Hkv an integer of at most
- * 64; max_q <= max_kv <= 2^30, total <= 2^30.  The work of a call is counted in 32 bits: with
- * max_q * G <= 16, nseq * Hkv * ceil(max_kv / 64) is at most 2^31 - 153; with more rows,
- * (floor(total / (2 floor(128 / G))) + min(nseq, total)) * Hkv times the spans of the keys (up to
- * 64; 1 for gqa_attn_packed) at most 2^31 - 2.  Bounds beyond these return
+ * it otherwise); they and the shape choose the kernel and its split of the keys, and size the
+ * workspace (gqa_attn_paged_workspace_bytes with the same arguments; 0 = none needed, or a shape
+ * that the call refuses).  Its contents need no initialisation; calls that may overlap need one
+ * each.  Every result is the same on every run of the same call.  d = 128; G = Hq / Hkv an
+ * integer of at most 64; max_q <= max_kv <= 2^30, total <= 2^30.  The work of a call is counted
+ * in 32 bits: with max_q * G <= 16, nseq * Hkv * ceil(max_kv / 64) is at most 2^31 - 153; with
+ * more rows, (floor(total / (2 floor(128 / G))) + min(nseq, total)) * Hkv times the spans of the
+ * keys (up to 64; 1 for gqa_attn_packed) at most 2^31 - 2.  Bounds beyond these return
  * GQA_ERR_UNSUPPORTED. */
 size_t gqa_attn_paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
                                       int Hkv, int d);
