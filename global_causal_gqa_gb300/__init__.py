@@ -27,6 +27,8 @@ __all__ = [
     "gqa_qk_norm_rope", "gqa_qk_norm_append", "gqa_prefill_gather", "gqa_kv_append_chunk",
     "PAGED_KV_DTYPE", "make_paged_kv", "gqa_packed_rope_append", "gqa_attn_packed",
     "gqa_attn_paged_workspace_bytes", "gqa_attn_paged",
+    "PAGED_KV_Q8_DTYPE", "make_paged_kv_q8", "gqa_packed_rope_append_q8",
+    "gqa_attn_paged_q8_workspace_bytes", "gqa_attn_paged_q8", "gqa_paged_read_q8",
     "gqa_get_device_status", "gqa_get_device_diag", "gqa_watchdog_selftest",
     "gqa_status_string", "gqa_last_error_string", "gqa_device_check",
 ]
@@ -99,6 +101,11 @@ def lib() -> ctypes.CDLL:
                                 I),
             "gqa_attn_paged_workspace_bytes": ([I, I, I, I, I, I, I], Z),
             "gqa_attn_paged": ([P, L64, P, P, I, I, I, I, I, I, F, P, L64, P, P, Z, P], I),
+            "gqa_packed_rope_append_q8": ([P, L64, P, L64, P, L64, P, I, I, I, I, I, P, P, F, P,
+                                           I, P, P, P, P], I),
+            "gqa_attn_paged_q8_workspace_bytes": ([I, I, I, I, I, I, I], Z),
+            "gqa_attn_paged_q8": ([P, L64, P, P, I, I, I, I, I, I, F, P, L64, P, P, Z, P], I),
+            "gqa_paged_read_q8": ([P, P, I, I, P, L64, P, L64, P], I),
             "gqa_get_device_status": ([P], I),
             "gqa_get_device_diag": ([P, P, I], I),
             "gqa_watchdog_selftest": ([ctypes.c_int64, P], I),
@@ -392,6 +399,80 @@ def gqa_attn_paged(q, q_stride: int, cache, cu_seqlens, nseq: int, total: int, m
                               max_q, max_kv, Hq, window, scale, _ptr(o), o_stride, _ptr(lse),
                               _ptr(workspace), workspace_bytes, _stream(stream))
     return _check("gqa_attn_paged", st, check)
+
+
+# ---- the 8-bit paged cache ------------------------------------------------------------------
+
+# struct gqa_paged_kv_q8 { void *k, *v, *scales; const int32 *page_table, *kv_lens;
+#                          int32 num_pages, Hkv, page_size, d, max_pages, reserved; }
+PAGED_KV_Q8_DTYPE = np.dtype([("k", "<u8"), ("v", "<u8"), ("scales", "<u8"),
+                              ("page_table", "<u8"), ("kv_lens", "<u8"), ("num_pages", "<i4"),
+                              ("Hkv", "<i4"), ("page_size", "<i4"), ("d", "<i4"),
+                              ("max_pages", "<i4"), ("reserved", "<i4")])
+assert PAGED_KV_Q8_DTYPE.itemsize == 64
+
+
+def make_paged_kv_q8(k_pool, v_pool, scales, page_table, kv_lens) -> np.ndarray:
+    """The host struct gqa_paged_kv_q8 of an 8-bit paged cache: k_pool, v_pool [num_pages, Hkv,
+    page_size, d] float8_e4m3fn, scales [num_pages, Hkv, page_size, 2] float8_e8m0fnu (the key's,
+    then the value's power of two), page_table [nseq, max_pages] int32, kv_lens [nseq] int32, all
+    contiguous device tensors that the caller keeps alive; pass it as `cache` to the q8 calls."""
+    import torch
+    tensors = (k_pool, v_pool, scales, page_table, kv_lens)
+    for t, n in zip(tensors, ("k_pool", "v_pool", "scales", "page_table", "kv_lens")):
+        if not t.is_contiguous():
+            raise ValueError(f"make_paged_kv_q8: {n} must be contiguous")
+    if len({t.device for t in tensors}) > 1:
+        raise ValueError("make_paged_kv_q8: the tensors lie on one device")
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape:
+        raise ValueError("make_paged_kv_q8: k_pool and v_pool are [num_pages, Hkv, page_size, d]")
+    if k_pool.dtype != torch.float8_e4m3fn or v_pool.dtype != torch.float8_e4m3fn:
+        raise ValueError("make_paged_kv_q8: the pools are float8_e4m3fn")
+    if scales.dtype != torch.float8_e8m0fnu or tuple(scales.shape) != (*k_pool.shape[:3], 2):
+        raise ValueError("make_paged_kv_q8: scales is float8_e8m0fnu [num_pages, Hkv, page_size, "
+                         "2]")
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or kv_lens.dtype != torch.int32 \
+            or kv_lens.numel() != page_table.shape[0]:
+        raise ValueError("make_paged_kv_q8: page_table is int32 [nseq, max_pages], kv_lens int32 "
+                         "[nseq]")
+    num_pages, Hkv, page_size, d = k_pool.shape
+    a = np.zeros(1, dtype=PAGED_KV_Q8_DTYPE).view(PagedKV)
+    a.address = a.ctypes.data
+    a[0] = (_ptr(k_pool), _ptr(v_pool), _ptr(scales), _ptr(page_table), _ptr(kv_lens), num_pages,
+            Hkv, page_size, d, page_table.shape[1], 0)
+    return a
+
+
+def gqa_packed_rope_append_q8(q, q_stride: int, k, k_stride: int, v, v_stride: int, cu_seqlens,
+                              nseq: int, total: int, Hq: int, Hkv: int, d: int, q_gamma, k_gamma,
+                              eps: float, table, table_len: int, q_out, k_out, cache,
+                              stream=None, check: bool = True) -> int:
+    st = lib().gqa_packed_rope_append_q8(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                                         _ptr(cu_seqlens), nseq, total, Hq, Hkv, d, _ptr(q_gamma),
+                                         _ptr(k_gamma), eps, _ptr(table), table_len, _ptr(q_out),
+                                         _ptr(k_out), _ptr(cache), _stream(stream))
+    return _check("gqa_packed_rope_append_q8", st, check)
+
+
+def gqa_attn_paged_q8_workspace_bytes(nseq: int, total: int, max_q: int, max_kv: int, Hq: int,
+                                      Hkv: int, d: int) -> int:
+    return lib().gqa_attn_paged_q8_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv, d)
+
+
+def gqa_attn_paged_q8(q, q_stride: int, cache, cu_seqlens, nseq: int, total: int, max_q: int,
+                      max_kv: int, Hq: int, window: int, scale: float, o, o_stride: int, lse,
+                      workspace, workspace_bytes: int, stream=None, check: bool = True) -> int:
+    st = lib().gqa_attn_paged_q8(_ptr(q), q_stride, _ptr(cache), _ptr(cu_seqlens), nseq, total,
+                                 max_q, max_kv, Hq, window, scale, _ptr(o), o_stride, _ptr(lse),
+                                 _ptr(workspace), workspace_bytes, _stream(stream))
+    return _check("gqa_attn_paged_q8", st, check)
+
+
+def gqa_paged_read_q8(cache, cu_seqlens, nseq: int, total: int, k_out, k_stride: int, v_out,
+                      v_stride: int, stream=None, check: bool = True) -> int:
+    st = lib().gqa_paged_read_q8(_ptr(cache), _ptr(cu_seqlens), nseq, total, _ptr(k_out), k_stride,
+                                 _ptr(v_out), v_stride, _stream(stream))
+    return _check("gqa_paged_read_q8", st, check)
 
 
 # ---- status ---------------------------------------------------------------------------------

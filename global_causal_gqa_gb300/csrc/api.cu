@@ -430,42 +430,55 @@ static gqa_status check_paged(const gqa_paged_kv *c) {
     return GQA_OK;
 }
 
-gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k,
-                                  int64_t k_stride, const void *v, int64_t v_stride,
-                                  const int32_t *cu_seqlens, int nseq, int total, int Hq,
-                                  int Hkv, int d, const float *q_gamma, const float *k_gamma,
-                                  float eps, const float *table, int table_len, void *q_out,
-                                  void *k_out, const gqa_paged_kv *cache, gqa_stream_t stream) {
+// The arguments that both forms of the append share.
+static gqa_status check_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                               const void *v, int64_t v_stride, const int32_t *cu_seqlens,
+                               int nseq, int total, int Hq, int Hkv, int d, const float *q_gamma,
+                               const float *k_gamma, float eps, const float *table, int table_len,
+                               const void *q_out, const void *k_out, bool with_cache) {
     const bool with_q = q != nullptr;
     if (!k || !cu_seqlens || !table || with_q != (q_out != nullptr) ||
-        (!q_out && !k_out && !cache) || (cache && !v) || nseq <= 0 || total <= 0 ||
+        (!q_out && !k_out && !with_cache) || (with_cache && !v) || nseq <= 0 || total <= 0 ||
         (with_q && Hq <= 0) || Hkv <= 0 || table_len <= 0 || !(eps >= 0.f) ||
         !std::isfinite(eps))
         return GQA_ERR_INVALID_ARG;
     // (the grid is counted in 32 bits)
     if (!rope_dim_ok(d) || total > 0x7fffffff - 512) return GQA_ERR_UNSUPPORTED;
     if ((with_q && !stride_ok(q_stride, Hq, d)) || !stride_ok(k_stride, Hkv, d) ||
-        (cache && !stride_ok(v_stride, Hkv, d)))
+        (with_cache && !stride_ok(v_stride, Hkv, d)))
         return GQA_ERR_INVALID_ARG;
     // in place only where the rows lie as the dense output's
     if ((with_q && q_out == q && q_stride != static_cast<int64_t>(Hq) * d) ||
         (k_out && k_out == k && k_stride != static_cast<int64_t>(Hkv) * d))
         return GQA_ERR_INVALID_ARG;
     if ((with_q && (!aligned16(q) || !aligned16(q_out))) || !aligned16(k) ||
-        (cache && !aligned16(v)) || (k_out && !aligned16(k_out)) ||
+        (with_cache && !aligned16(v)) || (k_out && !aligned16(k_out)) ||
         (q_gamma && !aligned16(q_gamma)) || (k_gamma && !aligned16(k_gamma)) ||
         !aligned16(table) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
         return GQA_ERR_ALIGNMENT;
+    return GQA_OK;
+}
+
+gqa_status gqa_packed_rope_append(const void *q, int64_t q_stride, const void *k,
+                                  int64_t k_stride, const void *v, int64_t v_stride,
+                                  const int32_t *cu_seqlens, int nseq, int total, int Hq,
+                                  int Hkv, int d, const float *q_gamma, const float *k_gamma,
+                                  float eps, const float *table, int table_len, void *q_out,
+                                  void *k_out, const gqa_paged_kv *cache, gqa_stream_t stream) {
+    gqa_status bad = check_append(q, q_stride, k, k_stride, v, v_stride, cu_seqlens, nseq, total,
+                                  Hq, Hkv, d, q_gamma, k_gamma, eps, table, table_len, q_out,
+                                  k_out, cache != nullptr);
+    if (bad != GQA_OK) return bad;
     if (cache) {
-        const gqa_status bad = check_paged(cache);
+        bad = check_paged(cache);
         if (bad != GQA_OK) return bad;
         if (cache->Hkv != Hkv || cache->d != d) return GQA_ERR_INVALID_ARG;
     }
     int *st = status_ptr();
     if (!st) return GQA_ERR_CUDA;
     return from_cuda(gqa::launch_packed_rope_append(
-        q, q_stride, k, k_stride, v, v_stride, cu_seqlens, nseq, total, with_q ? Hq : 0, Hkv, d,
-        q_gamma, k_gamma, eps, table, table_len, q_out, k_out, cache, st,
+        q, q_stride, k, k_stride, v, v_stride, cu_seqlens, nseq, total, q ? Hq : 0, Hkv, d,
+        q_gamma, k_gamma, eps, table, table_len, q_out, k_out, cache, nullptr, st,
         reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -543,6 +556,114 @@ gqa_status gqa_attn_paged(const void *q, int64_t q_stride, const gqa_paged_kv *c
         gqa::launch_packed_attn(a, workspace, st, reinterpret_cast<cudaStream_t>(stream));
     if (rc == GQA_ERR_CUDA) t_last_cuda_error = cudaGetLastError();
     return static_cast<gqa_status>(rc);
+}
+
+// ---- the 8-bit paged cache ----------------------------------------------------------------
+// The struct without its scales, which the pools' descriptions share.
+static gqa_paged_kv pools_of(const gqa_paged_kv_q8 *c) {
+    return {c->k, c->v, c->page_table, c->kv_lens, c->num_pages, c->Hkv, c->page_size, c->d,
+            c->max_pages, c->reserved};
+}
+
+static gqa_status check_paged_q8(const gqa_paged_kv_q8 *c) {
+    const gqa_paged_kv pools = pools_of(c);
+    if (!c->scales) return GQA_ERR_INVALID_ARG;
+    const gqa_status bad = check_paged(&pools);
+    if (bad != GQA_OK) return bad;
+    return aligned16(c->scales) ? GQA_OK : GQA_ERR_ALIGNMENT;
+}
+
+gqa_status gqa_packed_rope_append_q8(const void *q, int64_t q_stride, const void *k,
+                                     int64_t k_stride, const void *v, int64_t v_stride,
+                                     const int32_t *cu_seqlens, int nseq, int total, int Hq,
+                                     int Hkv, int d, const float *q_gamma, const float *k_gamma,
+                                     float eps, const float *table, int table_len, void *q_out,
+                                     void *k_out, const gqa_paged_kv_q8 *cache,
+                                     gqa_stream_t stream) {
+    if (!cache) return GQA_ERR_INVALID_ARG;
+    gqa_status bad = check_append(q, q_stride, k, k_stride, v, v_stride, cu_seqlens, nseq, total,
+                                  Hq, Hkv, d, q_gamma, k_gamma, eps, table, table_len, q_out,
+                                  k_out, true);
+    if (bad != GQA_OK) return bad;
+    bad = check_paged_q8(cache);
+    if (bad != GQA_OK) return bad;
+    if (cache->Hkv != Hkv || cache->d != d) return GQA_ERR_INVALID_ARG;
+    int *st = status_ptr();
+    if (!st) return GQA_ERR_CUDA;
+    const gqa_paged_kv pools = pools_of(cache);
+    return from_cuda(gqa::launch_packed_rope_append(
+        q, q_stride, k, k_stride, v, v_stride, cu_seqlens, nseq, total, q ? Hq : 0, Hkv, d,
+        q_gamma, k_gamma, eps, table, table_len, q_out, k_out, &pools,
+        static_cast<uint8_t *>(cache->scales), st, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The shape of an 8-bit paged call: that of the bf16 call, and room for its keys.
+static gqa_status check_paged_q8_shape(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv,
+                                       int d) {
+    const gqa_status bad = check_paged_shape(nseq, total, max_q, max_kv, Hq, Hkv, d);
+    if (bad != GQA_OK) return bad;
+    return gqa::paged_q8_counts_fit(nseq, total, max_q, max_kv, Hq, Hkv) ? GQA_OK
+                                                                         : GQA_ERR_UNSUPPORTED;
+}
+
+size_t gqa_attn_paged_q8_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
+                                         int Hkv, int d) {
+    if (check_paged_q8_shape(nseq, total, max_q, max_kv, Hq, Hkv, d) != GQA_OK) return 0;
+    return gqa::paged_q8_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv);
+}
+
+gqa_status gqa_attn_paged_q8(const void *q, int64_t q_stride, const gqa_paged_kv_q8 *cache,
+                             const int32_t *cu_seqlens, int nseq, int total, int max_q, int max_kv,
+                             int Hq, int window, float scale, void *o, int64_t o_stride,
+                             float *lse, void *workspace, size_t workspace_bytes,
+                             gqa_stream_t stream) {
+    if (!q || !cache || !o || !cu_seqlens || !(scale > 0.f) || !std::isfinite(scale))
+        return GQA_ERR_INVALID_ARG;
+    gqa_status bad = check_paged_q8(cache);
+    if (bad != GQA_OK) return bad;
+    const int Hkv = cache->Hkv, d = cache->d;
+    bad = check_paged_q8_shape(nseq, total, max_q, max_kv, Hq, Hkv, d);
+    if (bad != GQA_OK) return bad;
+    if (!stride_ok(q_stride, Hq, d) || !stride_ok(o_stride, Hq, d) || o == q)
+        return GQA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) ||
+        ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(cu_seqlens)) & 3u))
+        return GQA_ERR_ALIGNMENT;
+    const size_t need = gqa::paged_q8_workspace_bytes(nseq, total, max_q, max_kv, Hq, Hkv);
+    if (need) {
+        if (!workspace || workspace_bytes < need) return GQA_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return GQA_ERR_ALIGNMENT;
+    }
+    int *st = status_ptr();
+    if (!st) return GQA_ERR_CUDA;
+    gqa::PackedAttn a{q, cache->k, cache->v, o, lse, q_stride, 0, 0, o_stride, cu_seqlens,
+                      nullptr, nseq, total, max_q, max_kv, Hq, Hkv, window, scale};
+    const int rc =
+        gqa::launch_paged_q8(a, *cache, workspace, st, reinterpret_cast<cudaStream_t>(stream));
+    if (rc == GQA_ERR_CUDA) t_last_cuda_error = cudaGetLastError();
+    return static_cast<gqa_status>(rc);
+}
+
+gqa_status gqa_paged_read_q8(const gqa_paged_kv_q8 *cache, const int32_t *cu_seqlens, int nseq,
+                             int total, void *k_out, int64_t k_stride, void *v_out,
+                             int64_t v_stride, gqa_stream_t stream) {
+    if (!cache || !cu_seqlens || (!k_out && !v_out) || nseq <= 0 || total <= 0)
+        return GQA_ERR_INVALID_ARG;
+    const gqa_status bad = check_paged_q8(cache);
+    if (bad != GQA_OK) return bad;
+    if (!rope_dim_ok(cache->d) || total > kMostKeys) return GQA_ERR_UNSUPPORTED;
+    if ((k_out && !stride_ok(k_stride, cache->Hkv, cache->d)) ||
+        (v_out && !stride_ok(v_stride, cache->Hkv, cache->d)) || k_out == v_out ||
+        k_out == cache->k || k_out == cache->v || v_out == cache->k || v_out == cache->v)
+        return GQA_ERR_INVALID_ARG;
+    if ((k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out)) ||
+        (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u))
+        return GQA_ERR_ALIGNMENT;
+    int *st = status_ptr();
+    if (!st) return GQA_ERR_CUDA;
+    return from_cuda(gqa::launch_paged_read_q8(*cache, cu_seqlens, nseq, total, k_out, k_stride,
+                                               v_out, v_stride, st,
+                                               reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gqa_status gqa_get_device_status(gqa_stream_t stream) {

@@ -134,8 +134,8 @@ cudaError_t launch_packed_rope_append(const void *q, int64_t q_stride, const voi
                                       const int32_t *cu, int nseq, int total, int Hq, int Hkv,
                                       int d, const float *q_gamma, const float *k_gamma,
                                       float eps, const float *table, int table_len, void *q_out,
-                                      void *k_out, const gqa_paged_kv *cache, int *status,
-                                      cudaStream_t s);
+                                      void *k_out, const gqa_paged_kv *cache, uint8_t *scales,
+                                      int *status, cudaStream_t s);
 
 // What the attention kernels take: token strides in elements; for a paged call k and v are
 // the pools and `cache` describes them (packed prompts: cache == nullptr).
@@ -148,6 +148,7 @@ struct PackedAttn {
     const gqa_paged_kv *cache;
     int nseq, total, max_q, max_kv, Hq, Hkv, window;
     float scale;
+    long cap = 0;   // keys that a table row holds; 0: as the cache says
 };
 // the tensor-core kernel for prompts and chunks (packed_prefill.cu); returns a gqa_status
 int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
@@ -168,6 +169,20 @@ int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t 
 size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv);
 // whether the work of such a call can be counted in 32 bits, as its kernels do
 bool paged_counts_fit(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv);
+
+// The 8-bit paged cache (paged_read.cu, paged_q8.cu): read back into packed rows; all keys that
+// a call sees, in bf16 pages of 128 in the workspace (`out` describes them); attention.
+cudaError_t launch_paged_read_q8(const gqa_paged_kv_q8 &c, const int32_t *cu, int nseq, int total,
+                                 void *k_out, int64_t k_stride, void *v_out, int64_t v_stride,
+                                 int *status, cudaStream_t s);
+cudaError_t launch_paged_expand_q8(const gqa_paged_kv_q8 &c, const PackedAttn &a, void *ws,
+                                   gqa_paged_kv *out, int *status, cudaStream_t s);
+size_t paged_expand_q8_bytes(int nseq, int max_kv, int Hkv);
+bool paged_expand_counts_fit(int nseq, int max_kv, int Hkv);
+int launch_paged_q8(const PackedAttn &a, const gqa_paged_kv_q8 &c, void *ws, int *status,
+                    cudaStream_t s);
+size_t paged_q8_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv);
+bool paged_q8_counts_fit(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv);
 
 // Bounded-wait self-test (watchdog.cu)
 cudaError_t launch_watchdog_selftest(int64_t limit_ns, int *status, cudaStream_t s);

@@ -22,6 +22,7 @@
 
 #include "internal.h"
 #include "packed.cuh"
+#include "q8.cuh"
 
 namespace gqa {
 namespace {
@@ -40,6 +41,7 @@ struct AppendParams {
     const float4 *table;
     float eps;
     uint4 *q_out, *k_out, *k_pool, *v_pool;
+    uint8_t *scales;                     // of an 8-bit cache
     int *status;
 };
 
@@ -66,6 +68,37 @@ struct Vec {
         for (int o = 1; o < D / 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         return rsqrtf(ss * (1.0f / D) + eps);   // off by 2^-22 at most
     }
+    // The lane's elements in an 8-bit page and, from the first lane, their power of two: the vector
+    // begins at row `slot` of the pools' vectors (every lane of the warp shuffles; `store`: this
+    // one writes).
+    template <int D>
+    __device__ __forceinline__ void store_q8(const AppendParams &p, bool key, long slot, int c,
+                                             bool store) const {
+        constexpr int L = D / 16;
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            most = amax_nan(most, amax_nan(amax_nan(x[i].x, x[i].y), amax_nan(y[i].x, y[i].y)));
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) most = amax_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+        if (!store) return;
+        const uint32_t byte = scale_byte(most);
+        const float f = inverse_scale(byte);
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 *z = h ? y : x;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                w[2 * h + i] = to_e4m3x2(z[2 * i].x * f, z[2 * i].y * f) |
+                               to_e4m3x2(z[2 * i + 1].x * f, z[2 * i + 1].y * f) << 16;
+        }
+        uint2 *d = reinterpret_cast<uint2 *>(key ? p.k_pool : p.v_pool) + slot * (D / 8) + c;
+        // (a vector that is not finite is stored as zeros: inf and NaN times f = 0 are not)
+        d[0] = byte == kScaleNan ? make_uint2(0, 0) : make_uint2(w[0], w[1]);
+        d[L] = byte == kScaleNan ? make_uint2(0, 0) : make_uint2(w[2], w[3]);
+        if (c == 0) p.scales[2 * slot + (key ? 0 : 1)] = static_cast<uint8_t>(byte);
+    }
     // times r and the gain's elements in the same places
     __device__ __forceinline__ void scale(float r, const float4 (&ga)[2], const float4 (&gb)[2]) {
 #pragma unroll
@@ -85,12 +118,14 @@ struct Rotation {
         co[i] = make_float2(w.x, w.z);
         si[i] = make_float2(w.y, w.w);
     }
-    __device__ __forceinline__ void apply(const Vec &v, uint4 &a, uint4 &b) const {
+    __device__ __forceinline__ void apply(Vec &v, uint4 &a, uint4 &b) const {
         uint32_t ao[4], bo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 ra = fsub2(fmul2(v.x[i], co[i]), fmul2(v.y[i], si[i]));
             const float2 rb = ffma2v(v.x[i], si[i], fmul2(v.y[i], co[i]));
+            v.x[i] = ra;
+            v.y[i] = rb;
             ao[i] = pack_bf16x2(ra.x, ra.y);
             bo[i] = pack_bf16x2(rb.x, rb.y);
         }
@@ -138,8 +173,9 @@ __device__ __forceinline__ void check_sequences(const AppendParams &p) {
 }
 
 // D: head dim.  `per` threads (a multiple of the D / 16 lanes of a vector) serve one token at
-// a time, the block's kAppendThreads / per groups take its `tokens` tokens in turn.
-template <int D>
+// a time, the block's kAppendThreads / per groups take its `tokens` tokens in turn.  Q8: the pools
+// are an 8-bit cache's.
+template <int D, bool Q8>
 __global__ void __launch_bounds__(kAppendThreads, 4)
     packed_rope_append_kernel(const AppendParams p, int tokens, int per) {
     constexpr int L = D / 16;    // lanes of a vector; also the distance of a pair's chunks
@@ -210,8 +246,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4)
             Vec v(a, b);
             if (p.k_gamma) normalise(v, p.k_gamma, isk);
             if (isk) rot.apply(v, a, b);
+            if constexpr (Q8)
+                v.template store_q8<D>(p, isk, slot + (long)g * p.page_size, c,
+                                       ub + u0 < heads && page >= 0 &&
+                                           slot_in_bounds(p, slot + (long)g * p.page_size));
             if (ub + u0 >= heads) continue;
-            if (page >= 0 && p.k_pool && slot_in_bounds(p, slot + (long)g * p.page_size)) {
+            if (!Q8 && page >= 0 && p.k_pool && slot_in_bounds(p, slot + (long)g * p.page_size)) {
                 uint4 *d = (isk ? p.k_pool : p.v_pool) + (slot + (long)g * p.page_size) * C + c;
                 d[0] = a;
                 d[L] = b;
@@ -238,7 +278,7 @@ constexpr int kPlaceBytes = 13824;
 constexpr int kStreamBytes = kStreamPlaces * kPlaceBytes;
 constexpr int kStreamSmem = kStreamBytes + kStreamPlaces * 8 + 128;
 
-template <int D>
+template <int D, bool Q8>
 __global__ void __launch_bounds__(32 * kStreamPlaces, 2)
     packed_append_stream_kernel(const AppendParams p, int parts, int per, int run) {
     constexpr int L = D / 16, V = 32 / L;    // lanes of a vector, vectors of a warp
@@ -313,7 +353,9 @@ __global__ void __launch_bounds__(32 * kStreamPlaces, 2)
             Rotation rot;
 #pragma unroll
             for (int i = 0; i < 4; ++i) rot.set(i, reinterpret_cast<const float4 *>(table)[4 * c + i]);
-            auto vectors = [&](auto W, uint8_t *at, int n, bool norm) {
+            // Vectors of kind W (0: q, 1: k, 2: v of an 8-bit cache), the first of them of head
+            // `head`: an 8-bit cache's go from here to their page.
+            auto vectors = [&](auto W, uint8_t *at, int n, bool norm, int head) {
                 constexpr int w = decltype(W)::value;
 #pragma unroll 1
                 for (int b = 0; b < n; b += V) {
@@ -321,24 +363,34 @@ __global__ void __launch_bounds__(32 * kStreamPlaces, 2)
                     uint4 *x = reinterpret_cast<uint4 *>(at + (size_t)min(i, n - 1) * kVec) + c;
                     uint4 a = x[0], d = x[L];
                     Vec v(a, d);
-                    if (norm) v.scale(v.template inverse_norm<D>(p.eps), gain[w][0], gain[w][1]);
-                    rot.apply(v, a, d);
+                    if constexpr (w < 2) {
+                        if (norm) v.scale(v.template inverse_norm<D>(p.eps), gain[w][0], gain[w][1]);
+                        rot.apply(v, a, d);
+                    }
+                    if constexpr (Q8 && w > 0) {
+                        const long slot = ((long)tpage * p.Hkv + head + i) * p.page_size +
+                                          (tpos & (p.page_size - 1));
+                        v.template store_q8<D>(p, w == 1, slot, c,
+                                               i < n && tpage >= 0 && slot_in_bounds(p, slot));
+                    }
                     __syncwarp();            // a clamped lane may have read the last vector
-                    if (i < n) {
+                    if (w < 2 && i < n) {
                         x[0] = a;
                         x[L] = d;
                     }
                 }
             };
-            vectors(std::integral_constant<int, 0>{}, place, q1 - v0, p.q_gamma != nullptr);
-            vectors(std::integral_constant<int, 1>{}, keys, k1 - q1, p.k_gamma != nullptr);
+            vectors(std::integral_constant<int, 0>{}, place, q1 - v0, p.q_gamma != nullptr, 0);
+            vectors(std::integral_constant<int, 1>{}, keys, k1 - q1, p.k_gamma != nullptr, q1 - nq);
+            if constexpr (Q8)
+                vectors(std::integral_constant<int, 2>{}, values, v1 - k1, false, k1 - nk);
             fence_proxy_async_smem();        // before the bulk copies read it
             __syncwarp();
             if (lane == 0 && q1 > v0)
                 bulk_store(p.q_out + (row * p.Hq + v0) * C, place, (q1 - v0) * kVec);
             if (lane == 1 && p.k_out && k1 > q1)
                 bulk_store(p.k_out + (row * p.Hkv + q1 - nq) * C, keys, (k1 - q1) * kVec);
-            if (p.k_pool && tpage >= 0)
+            if (!Q8 && p.k_pool && tpage >= 0)
                 for (int i = q1 + lane; i < v1; i += 32) {
                     const int g = i < nk ? i - nq : i - nk;
                     const long slot =
@@ -362,9 +414,10 @@ cudaError_t launch_packed_rope_append(const void *q, int64_t q_stride, const voi
                                       const int32_t *cu, int nseq, int total, int Hq, int Hkv,
                                       int d, const float *q_gamma, const float *k_gamma,
                                       float eps, const float *table, int table_len, void *q_out,
-                                      void *k_out, const gqa_paged_kv *cache, int *status,
-                                      cudaStream_t s) {
+                                      void *k_out, const gqa_paged_kv *cache, uint8_t *scales,
+                                      int *status, cudaStream_t s) {
     AppendParams p{};
+    p.scales = scales;
     p.q = static_cast<const uint4 *>(q);
     p.k = static_cast<const uint4 *>(k);
     p.v = static_cast<const uint4 *>(v);
@@ -395,10 +448,14 @@ cudaError_t launch_packed_rope_append(const void *q, int64_t q_stride, const voi
         p.bounds.cap = (long)cache->max_pages * cache->page_size;
     }
     if (total > kFewTokens) {
-        auto kern = d == 64    ? packed_append_stream_kernel<64>
-                    : d == 128 ? packed_append_stream_kernel<128>
-                    : d == 256 ? packed_append_stream_kernel<256>
-                               : packed_append_stream_kernel<512>;
+        auto kern = scales ? (d == 64    ? packed_append_stream_kernel<64, true>
+                              : d == 128 ? packed_append_stream_kernel<128, true>
+                              : d == 256 ? packed_append_stream_kernel<256, true>
+                                         : packed_append_stream_kernel<512, true>)
+                           : (d == 64    ? packed_append_stream_kernel<64, false>
+                              : d == 128 ? packed_append_stream_kernel<128, false>
+                              : d == 256 ? packed_append_stream_kernel<256, false>
+                                         : packed_append_stream_kernel<512, false>);
         const cudaError_t err = ensure_smem_attr(reinterpret_cast<const void *>(kern), kStreamSmem);
         if (err != cudaSuccess) return err;
         // runs of vectors that fit a place, as equal as can be
@@ -414,10 +471,14 @@ cudaError_t launch_packed_rope_append(const void *q, int64_t q_stride, const voi
     int per = 32;
     while (per < lanes && per < kAppendThreads) per <<= 1;
     const int tokens = kAppendThreads / per;
-    auto kern = d == 64    ? packed_rope_append_kernel<64>
-                : d == 128 ? packed_rope_append_kernel<128>
-                : d == 256 ? packed_rope_append_kernel<256>
-                           : packed_rope_append_kernel<512>;
+    auto kern = scales ? (d == 64    ? packed_rope_append_kernel<64, true>
+                          : d == 128 ? packed_rope_append_kernel<128, true>
+                          : d == 256 ? packed_rope_append_kernel<256, true>
+                                     : packed_rope_append_kernel<512, true>)
+                       : (d == 64    ? packed_rope_append_kernel<64, false>
+                          : d == 128 ? packed_rope_append_kernel<128, false>
+                          : d == 256 ? packed_rope_append_kernel<256, false>
+                                     : packed_rope_append_kernel<512, false>);
     return launch_pdl(kern, dim3((total + tokens - 1) / tokens), dim3(kAppendThreads), 0, s, p,
                       tokens, per);
 }

@@ -1309,7 +1309,7 @@ int launch_packed_prefill(const PackedAttn &a, void *ws, int *status, cudaStream
         p.num_pages = c.num_pages;
         p.page_size = c.page_size;
         p.max_pages = c.max_pages;
-        p.bounds.cap = (long)c.max_pages * c.page_size;
+        p.bounds.cap = a.cap ? a.cap : (long)c.max_pages * c.page_size;
         const SpanRule r = span_rule(a.nseq, a.total, a.max_kv, a.Hq, a.Hkv, a.window);
         p.split_tiles = r.split_tiles;
         p.spans = spans = r.spans;

@@ -942,7 +942,7 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
     p.status = status;
     p.q_stride = a.q_stride;
     p.o_stride = a.o_stride;
-    p.bounds = {a.total, a.max_q, a.max_kv, (long)c.max_pages * c.page_size};
+    p.bounds = {a.total, a.max_q, a.max_kv, a.cap ? a.cap : (long)c.max_pages * c.page_size};
     p.nseq = a.nseq;
     p.Hq = a.Hq;
     p.Hkv = a.Hkv;

@@ -25,9 +25,10 @@ from typing import List, Sequence
 
 import numpy as np
 
-from . import (KV_DESC_DTYPE, gqa_attn_decode, gqa_attn_paged, gqa_attn_paged_workspace_bytes,
-               gqa_decode_workspace_bytes, gqa_kv_append, gqa_packed_rope_append, make_kv_descs,
-               make_paged_kv)
+from . import (KV_DESC_DTYPE, gqa_attn_decode, gqa_attn_paged, gqa_attn_paged_q8,
+               gqa_attn_paged_q8_workspace_bytes, gqa_attn_paged_workspace_bytes,
+               gqa_decode_workspace_bytes, gqa_kv_append, gqa_packed_rope_append,
+               gqa_packed_rope_append_q8, make_kv_descs, make_paged_kv, make_paged_kv_q8)
 
 
 @dataclass
@@ -116,11 +117,13 @@ class PagedLayer:
     table: object          # RoPE table of the layer type, table_len positions
     table_len: int
     window: int            # 0: global layer
+    scales: object = None  # an 8-bit layer: float8_e8m0fnu [num_pages, Hkv, page_size, 2], and
+                           # pools of float8_e4m3fn
 
 
 class PagedStack:
     """A serving step over paged caches: per layer one gqa_packed_rope_append and one
-    gqa_attn_paged.  cu_seqlens (int32 [nseq + 1]), kv_lens (int32 [nseq], counted with the new
+    gqa_attn_paged, or, for a layer with `scales`, their 8-bit forms.  cu_seqlens (int32 [nseq + 1]), kv_lens (int32 [nseq], counted with the new
     tokens) and page_table (int32 [nseq, max_pages], used by every layer with its own pools)
     are device tensors read when the kernels run: a captured step follows what the caller
     writes to them between replays, up to max_q new tokens and max_kv tokens of a sequence.
@@ -140,7 +143,7 @@ class PagedStack:
             raise ValueError("PagedStack: cu_seqlens is contiguous int32 [nseq + 1]")
         for i, L in enumerate(layers):
             if any(t is not None and t.device != page_table.device for t in
-                   (cu_seqlens, L.k_pool, L.qkv, L.o, L.q_gamma, L.k_gamma, L.table)):
+                   (cu_seqlens, L.k_pool, L.qkv, L.o, L.q_gamma, L.k_gamma, L.table, L.scales)):
                 raise ValueError(f"PagedStack: layer {i}: the tensors lie on one device")
             for t, name, shape in ((L.qkv, "qkv", (self.total, (Hq + 2 * Hkv) * d)),
                                    (L.o, "o", (self.total, Hq, d))):
@@ -155,9 +158,13 @@ class PagedStack:
                                       not t.is_contiguous()):
                     raise ValueError(f"PagedStack: layer {i}: {name} is contiguous float32, "
                                      f"{n} values")
-        self.caches = [make_paged_kv(L.k_pool, L.v_pool, page_table, kv_lens) for L in layers]
+        self.caches = [make_paged_kv(L.k_pool, L.v_pool, page_table, kv_lens) if L.scales is None
+                       else make_paged_kv_q8(L.k_pool, L.v_pool, L.scales, page_table, kv_lens)
+                       for L in layers]
         dev = layers[0].qkv.device
-        self.wsb = gqa_attn_paged_workspace_bytes(self.nseq, self.total, max_q, max_kv, Hq, Hkv, d)
+        shape = self.nseq, self.total, max_q, max_kv, Hq, Hkv, d
+        self.wsb = max(gqa_attn_paged_workspace_bytes(*shape) if L.scales is None else
+                       gqa_attn_paged_q8_workspace_bytes(*shape) for L in layers)
         self.ws = torch.empty(max(self.wsb, 16), dtype=torch.uint8, device=dev)
         self.q = torch.empty(self.total, Hq, d, dtype=torch.bfloat16, device=dev)
         self.graph = None
@@ -168,12 +175,14 @@ class PagedStack:
         row = (Hq + 2 * Hkv) * d
         for L, cache in zip(self.layers, self.caches):
             q, k, v = L.qkv.split([Hq * d, Hkv * d, Hkv * d], 1)
-            gqa_packed_rope_append(q, row, k, row, v, row, self.cu_seqlens, self.nseq, self.total,
-                                   Hq, Hkv, d, L.q_gamma, L.k_gamma, self.eps, L.table,
-                                   L.table_len, self.q, None, cache, stream)
-            gqa_attn_paged(self.q, Hq * d, cache, self.cu_seqlens, self.nseq, self.total,
-                           self.max_q, self.max_kv, Hq, L.window, self.scale, L.o, Hq * d, None,
-                           self.ws, self.wsb, stream)
+            append, attend = (gqa_packed_rope_append, gqa_attn_paged) if L.scales is None else \
+                (gqa_packed_rope_append_q8, gqa_attn_paged_q8)
+            append(q, row, k, row, v, row, self.cu_seqlens, self.nseq, self.total, Hq, Hkv, d,
+                   L.q_gamma, L.k_gamma, self.eps, L.table, L.table_len, self.q, None, cache,
+                   stream)
+            attend(self.q, Hq * d, cache, self.cu_seqlens, self.nseq, self.total, self.max_q,
+                   self.max_kv, Hq, L.window, self.scale, L.o, Hq * d, None, self.ws, self.wsb,
+                   stream)
 
     def capture(self):
         """Captures `step` in a CUDA graph on a side stream (run `step` once before: the first

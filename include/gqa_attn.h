@@ -400,6 +400,66 @@ gqa_status gqa_attn_paged(const void *q, int64_t q_stride, const gqa_paged_kv *c
                           float *lse, void *workspace, size_t workspace_bytes,
                           gqa_stream_t stream);
 
+/* ---- The 8-bit paged cache -----------------------------------------------------------------
+ * The paged cache of the section above with keys and values in 8 bits, half the bytes of a decode
+ * step and of the memory.  A key or value vector x (one token, one KV head) is kept as d e4m3
+ * numbers y and one power of two:
+ *   e = the smallest integer in [-126, 119] with max |x| <= 448 * 2^e  (-126 for a zero vector),
+ *   y_i = x_i / 2^e rounded to the nearest e4m3 number, ties to even, at most 448 in magnitude,
+ * and the byte e + 127 (E8M0) in `scales`.  It reads back as y_i * 2^(byte - 127), off by at most
+ * 2^-4 of |x_i| and 2^(e-10) for elements below 2^(e-6).  A vector that holds an infinity or a NaN
+ * gets the byte 255 and reads back as NaN; its numbers are zeros.  Rows, pages, lengths, flagged
+ * contents and the meaning of a page-table entry are those of gqa_paged_kv. */
+typedef struct gqa_paged_kv_q8 {
+    void *k;                    /* device [num_pages, Hkv, page_size, d] e4m3, after RoPE */
+    void *v;                    /* device, the same shape */
+    void *scales;               /* device [num_pages, Hkv, page_size, 2]: the key's byte, then the
+                                   value's */
+    const int32_t *page_table;  /* device [nseq, max_pages] */
+    const int32_t *kv_lens;     /* device [nseq] */
+    int32_t num_pages;
+    int32_t Hkv;
+    int32_t page_size;          /* 16, 32, 64 or 128 */
+    int32_t d;
+    int32_t max_pages;          /* entries of a page_table row */
+    int32_t reserved;           /* 0 */
+} gqa_paged_kv_q8;
+
+/* As gqa_packed_rope_append (same arguments, checks and flags) into an 8-bit cache, which may not
+ * be NULL.  The rotated key and the value are rounded once, from fp32, to the cache's numbers;
+ * k_out, if given, receives the rotated key in bf16 (for gqa_attn_packed over the same prompts).
+ * One kernel. */
+gqa_status gqa_packed_rope_append_q8(const void *q, int64_t q_stride, const void *k,
+                                     int64_t k_stride, const void *v, int64_t v_stride,
+                                     const int32_t *cu_seqlens, int nseq, int total, int Hq,
+                                     int Hkv, int d, const float *q_gamma, const float *k_gamma,
+                                     float eps, const float *table, int table_len, void *q_out,
+                                     void *k_out, const gqa_paged_kv_q8 *cache,
+                                     gqa_stream_t stream);
+
+/* As gqa_attn_paged over an 8-bit cache: the same arguments, masks, limits, flags and NaN rules,
+ * applied to the numbers that the cache stands for.  gqa_attn_paged_q8_workspace_bytes sizes its
+ * own workspace (with the arguments of the call), which may include room for every key that the
+ * bounds allow in bf16: pass a max_kv near the longest sequence. */
+size_t gqa_attn_paged_q8_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
+                                         int Hkv, int d);
+gqa_status gqa_attn_paged_q8(const void *q, int64_t q_stride, const gqa_paged_kv_q8 *cache,
+                             const int32_t *cu_seqlens, int nseq, int total, int max_q, int max_kv,
+                             int Hq, int window, float scale, void *o, int64_t o_stride,
+                             float *lse, void *workspace, size_t workspace_bytes,
+                             gqa_stream_t stream);
+
+/* Reads an 8-bit cache back: sequence i owns rows cu_seqlens[i] .. cu_seqlens[i+1] - 1 of k_out
+ * and v_out [total, Hkv, d] bf16 (token strides as above; either may be NULL), which receive its
+ * tokens S - T .. S - 1, S = kv_lens[i], T its number of rows: all of them, or the newest; another
+ * kv_lens in the struct reads another range.  Each value is rounded once to bf16, exact unless it
+ * leaves bf16's range.  Rows of no sequence are not written; a page outside the pool is flagged and
+ * reads as zeros.  d in {64, 128, 256, 512}; total <= 2^30.  k_out and v_out may not overlap each
+ * other, or the pools. */
+gqa_status gqa_paged_read_q8(const gqa_paged_kv_q8 *cache, const int32_t *cu_seqlens, int nseq,
+                             int total, void *k_out, int64_t k_stride, void *v_out,
+                             int64_t v_stride, gqa_stream_t stream);
+
 /* ---- Status ----------------------------------------------------------------------------
  * Waits for `stream`, then returns and clears the current device's status word
  * (GQA_OK if no device-side error was recorded since the last call). */
