@@ -27,10 +27,8 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-}  // namespace
-
-bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
-                   const uint64_t *strides, const uint32_t *box) {
+bool make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, int rank,
+              const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t d[5], s[4];
@@ -41,15 +39,26 @@ bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t 
         one[i] = 1;
         if (i + 1 < rank) s[i] = strides[i];
     }
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, s, b, one,
+    return fn(map, type, rank, const_cast<void *>(base), d, s, b, one,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+bool make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                   const uint64_t *strides, const uint32_t *box) {
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides, box);
+}
+bool make_byte_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                   const uint64_t *strides, const uint32_t *box) {
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides, box);
+}
+
 size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv) {
     return paged_decode_fits(max_q, Hq / Hkv)
-               ? paged_decode_workspace_bytes(nseq, max_kv, Hkv)
+               ? paged_decode_workspace_bytes(nseq, max_kv, Hkv, false)
                : packed_prefill_workspace_bytes(nseq, total, max_kv, Hq, Hkv);
 }
 
@@ -61,7 +70,7 @@ bool paged_counts_fit(int nseq, int total, int max_q, int max_kv, int Hq, int Hk
 
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
     if (a.cache && paged_decode_fits(a.max_q, a.Hq / a.Hkv))
-        return launch_paged_decode(a, ws, status, s);
+        return launch_paged_decode(a, nullptr, ws, status, s);
     return launch_packed_prefill(a, ws, status, s);
 }
 

@@ -49,23 +49,35 @@
 
 #include "internal.h"
 #include "packed.cuh"
+#include "q8.cuh"
 
 namespace gqa {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kUnit = 64;                       // keys of a stage
-constexpr int kStages = 6;
-constexpr int kTileBytes = kUnit * kD * 2;      // K or V of a stage
+constexpr int kTileBytes = 16384;               // K or V of a stage
 constexpr int kStageBytes = 2 * kTileBytes;
-constexpr int kConsumers = 4;                   // warps of a group, 16 keys of a stage each
+constexpr int kMostStages = 6;
+constexpr int kConsumers = 4;                   // warps of a group, a quarter of a stage's keys each
 constexpr int kGroups = 2;                      // groups of consumers, which take the pairs in turn
 constexpr int kThreads = 32 * (kGroups * kConsumers + 1);
 constexpr int kMaxRows = 16;
-constexpr int kSmemXchg = kStages * kStageBytes;
-constexpr int kSmemBar = kSmemXchg + kGroups * kConsumers * 8 * kD * 4;
-constexpr int kSmemBytes = kSmemBar + 1536 + 1024;
+
+// What the two kinds of cache differ in: keys of a stage (a unit), stages of the ring, and shared
+// memory, in which an 8-bit cache's ring is followed by its stages' scale bytes.
+template <bool Q8>
+struct Ring {
+    static constexpr int kUnit = Q8 ? 128 : 64;
+    static constexpr int kStages = Q8 ? 5 : 6;
+    static constexpr int kScales = kStages * kStageBytes;
+    static constexpr int kXchg = kScales + (Q8 ? kStages * 2 * kUnit : 0);
+    static constexpr int kBar = kXchg + kGroups * kConsumers * 8 * kD * 4;
+    static constexpr int kBytes = kBar + 1536 + 1024;
+};
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
+// An 8-bit cache's weights go into their product as f16: up to 2^(9 + 6), and no less than 2^-24,
+// 2^-33 of the reference.
+constexpr float kGrow8 = 6.0f, kShift8 = 9.0f;
 constexpr int kSegSlots = 4;
 constexpr int kSMs = 152;
 constexpr int kMinRun = 128;                    // units per SM from which chunks come in levels
@@ -84,8 +96,8 @@ struct Joint {
 
 struct Bars {
     Segment seg[kSegSlots];
-    uint64_t full[kGroups][kStages];   // a stage's load, for the group that takes it
-    uint64_t empty[kStages];
+    uint64_t full[kGroups][kMostStages];   // a stage's load, for the group that takes it
+    uint64_t empty[kMostStages];
     uint64_t seg_full[kSegSlots], seg_free[kSegSlots];
     uint64_t merge[kGroups];    // a group's warps meet (a barrier with a bounded wait)
     float2 ml[kGroups][kConsumers][8];
@@ -103,6 +115,7 @@ struct Params {
     Joint *ws_joint;               // one per chunk
     int chunks;
     const int32_t *cu, *kv_lens, *pages;
+    const uint8_t *scales;         // of an 8-bit cache
     int *status;
     long q_stride, o_stride;
     PackedBounds bounds;
@@ -117,12 +130,14 @@ __device__ __forceinline__ int token_of(const Params &p, int r) {
     return static_cast<int>(r * p.inv_g >> 16);
 }
 
-// Units of one (sequence, KV head): [first, first + count) of 64 keys each.
+// Units of one (sequence, KV head): [first, first + count) of `unit` keys each.
+template <int unit>
 __device__ __forceinline__ int first_unit(const PackedSeq &s, int window) {
-    return window > 0 && s.S - s.T - window + 1 > 0 ? (s.S - s.T - window + 1) / kUnit : 0;
+    return window > 0 && s.S - s.T - window + 1 > 0 ? (s.S - s.T - window + 1) / unit : 0;
 }
+template <int unit>
 __device__ __forceinline__ int count_units(const PackedSeq &s, int window) {
-    return s.T > 0 ? (s.S + kUnit - 1) / kUnit - first_unit(s, window) : 0;
+    return s.T > 0 ? (s.S + unit - 1) / unit - first_unit<unit>(s, window) : 0;
 }
 
 // The cut of all units into chunks, one level of kSMs equal chunks after the other; one level
@@ -183,6 +198,36 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1,
+                                             uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 y = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&y);
+}
+// Two transposed 16 x 16 matrices of bytes, their rows at the addresses of lanes 0-15 and 16-31: of
+// each, the lane's columns lane / 4 and + 8, rows 4 (lane % 4) and the three after it.
+__device__ __forceinline__ void ldsm_b8_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// byte - 127, the exponent that a scale byte stands for; NaN for 255.
+__device__ __forceinline__ float exponent_of(uint32_t byte) {
+    return byte == kScaleNan ? CUDART_NAN_F : __uint_as_float(0x4b000000u | byte) - 8388735.0f;
+}
+// Clears the NaN among the four e4m3 in w; true if there was one.
+__device__ __forceinline__ bool strip_nan(uint32_t &w) {
+    const uint32_t nan = __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    w &= ~nan;
+    return nan != 0;
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -218,17 +263,19 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
 enum Role { kRoleProducer = 0, kRoleConsumer = 2 };
 constexpr int kSite = kDiagPagedDecode << 24;   // of the debug build's checks
 
-// ROWS: the most rows of a pair, 8 or 16.
-template <int ROWS>
+// ROWS: the most rows of a pair, 8 or 16.  Q8: an 8-bit cache.
+template <int ROWS, bool Q8>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const Params p) {
     griddep_wait();
     griddep_launch_dependents();
+    constexpr int kUnit = Ring<Q8>::kUnit, kStages = Ring<Q8>::kStages;
+    constexpr int kRow = Q8 ? kD : 2 * kD;   // bytes of a key or value
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-    Bars *bars = reinterpret_cast<Bars *>(smem + kSmemBar);
+    Bars *bars = reinterpret_cast<Bars *>(smem + Ring<Q8>::kBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -250,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s0 = threadIdx.x * m;
         int mine = 0, most = 0;
         for (int i = s0; i < s0 + m && i < p.nseq; ++i) {
-            const int n = count_units(packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status), p.window);
+            const int n = count_units<kUnit>(packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status), p.window);
             mine += p.Hkv * n;
             most = max(most, n);
         }
@@ -296,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (p.whole) touch(p.pages + (long)s_seq * p.max_pages);
                 s_head = p.whole ? pair - s_seq * p.Hkv : 0;
                 s = packed_seq(p.cu, p.kv_lens, s_seq, p.bounds, p.whole ? p.status : nullptr);
-                s_units = count_units(s, p.window);
+                s_units = count_units<kUnit>(s, p.window);
             }
         };
         int listed = 0;            // stages of the segments so far
@@ -458,14 +505,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const int st = u % kStages;
                 uint64_t *full = &bars->full[group][st];
-                uint8_t *dst = smem + st * kStageBytes + lane * box * kD * 2;
+                uint8_t *dst = smem + st * kStageBytes + lane * box * kRow;
                 const int row = unit_key & (p.page_size - 1);
                 // every lane with a box waits, announces its bytes and loads for itself
                 const bool free = u < kStages || mbar_wait(&bars->empty[st], (u / kStages - 1) & 1);
                 if (free && lane < boxes) {
-                    mbar_arrive_expect_tx(full, 2 * box * kD * 2);
-                    tma_load_4d(dst, &tmK, full, 0, row, 0, slab);
-                    tma_load_4d(dst + kTileBytes, &tmV, full, 0, row, 0, slab);
+                    if constexpr (Q8) {
+                        uint8_t *bytes = smem + Ring<Q8>::kScales + (st * kUnit + lane * box) * 2;
+                        if (slab < 0) {   // (zeros with any power of two)
+                            for (int i = 0; i < box / 8; ++i)
+                                reinterpret_cast<uint4 *>(bytes)[i] =
+                                    make_uint4(0x01010101, 0x01010101, 0x01010101, 0x01010101);
+                            fence_proxy_async_smem();
+                        }
+                        mbar_arrive_expect_tx(full, 2 * box * kRow + (slab < 0 ? 0 : 2 * box));
+                        tma_load_3d(dst, &tmK, full, 0, row, slab);
+                        tma_load_3d(dst + kTileBytes, &tmV, full, 0, row, slab);
+                        if (slab >= 0)
+                            bulk_copy_g2s(bytes, p.scales + ((long)slab * p.page_size + row) * 2,
+                                          2 * box, full);
+                    } else {
+                        mbar_arrive_expect_tx(full, 2 * box * kRow);
+                        tma_load_4d(dst, &tmK, full, 0, row, 0, slab);
+                        tma_load_4d(dst + kTileBytes, &tmV, full, 0, row, 0, slab);
+                    }
                 }
                 if (!__all_sync(0xffffffffu, free)) {
                     set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 1, u);
@@ -505,14 +568,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int HR = ROWS / 8;                  // row halves in use
     const uint32_t ring = smem_u32(smem);
     const int group = warp / kConsumers, cw = warp % kConsumers;
-    float *xchg = reinterpret_cast<float *>(smem + kSmemXchg) + group * kConsumers * 8 * kD;
+    float *xchg = reinterpret_cast<float *>(smem + Ring<Q8>::kXchg) + group * kConsumers * 8 * kD;
     float2(*ml)[8] = bars->ml[group];
     // ldmatrix rows, both operands A: K: matrices (chunk 2ks | 2ks + 1) x (keys 0-7 | 8-15);
     // V transposed: (keys 0-7 | 8-15) x (dim chunk 2nn | 2nn + 1)
     const int mat = lane >> 3, l7 = lane & 7;
     const int box = min(p.page_size, kUnit);
     const uint32_t half = box * 128;          // a box: its rows' dims 0-63, then 64-127
-    const int part = 16 * cw;                 // first of this warp's keys in a stage
+    const int part = kUnit / kConsumers * cw;   // first of this warp's keys in a stage
     const uint32_t rows16 = part / box * 2 * half + part % box * 128;
     const uint32_t k_row = rows16 + (((mat & 1) << 3) + l7) * 128;
     const uint32_t v_row = kTileBytes + rows16 + (((mat >> 1) << 3) + l7) * 128;
@@ -522,6 +585,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) {
         k_off[i] = k_row + (((2 * i + (mat >> 1)) ^ l7) << 4);
         v_off[i] = v_row + (((2 * i + (mat & 1)) ^ l7) << 4);
+    }
+    // An 8-bit cache's: rows of 128 bytes, 128-byte swizzled.  A block of 16 keys has the keys
+    // 0-7 and 8 + (0-7 ^ 4) as the rows 0-7 and 8-15 of the score product's A operand.  There
+    // each four numbers of a lane are two of the product's k-steps' pairs: the queries' dims are
+    // taken in the same order.  V's 16 x 16 matrices, transposed, bring a lane four rows, which
+    // are the keys of its pairs 2tq, + 1 and 8 + 2tq, + 1 in the value product: rows 4i .. 4i + 3
+    // are the score rows 2i, 2i + 1, 8 + 2i, 8 + 2i + 1.  (The ^ 4: eight rows of either operand
+    // lie in eight different swizzled columns.)
+    uint32_t k8 = 0, v8 = 0;
+    if constexpr (Q8) {
+        const int kk = mat & 1 ? 8 + (l7 ^ 4) : l7;
+        k8 = (part + kk) * kD + (((mat >> 1) ^ (kk & 7)) << 4);
+        const int rho = lane & 15, i = 2 * (rho >> 2) + (rho & 1);
+        const int vk = rho & 2 ? 8 + (i ^ 4) : i;
+        v8 = kTileBytes + (part + 16 * (lane >> 4) + vk) * kD + ((vk & 7) << 4);
     }
     int meets = 0;
     auto meet = [&]() {
@@ -535,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one are zero).
     Segment sg;
     uint32_t qb[8][2 * HR];
+    float sl_next[HR][2];   // an 8-bit cache's: the factor of a score of this thread's columns
     auto next_segment = [&](int k) {
         const int slot = k & (kSegSlots - 1);
         if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
@@ -549,14 +628,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int h = 0; h < HR; ++h) {
             const int r = gq + 8 * h, t = token_of(p, r);
             const __nv_bfloat16 *qr = p.q + (long)(sg.row0 + t) * p.q_stride +
-                                      (sg.g * p.G + (r - t * p.G)) * kD + 2 * tq;
+                                      (sg.g * p.G + (r - t * p.G)) * kD + (Q8 ? 4 : 2) * tq;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 qb[ks][h] = qb[ks][HR + h] = 0u;
                 if (r < rows && GQA_IN_BOUNDS(sg.row0 + t, p.bounds.total, p.status, kSite | 3)) {
-                    qb[ks][h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks));
-                    qb[ks][HR + h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks + 8));
+                    if constexpr (Q8) {
+                        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(qr + 16 * ks));
+                        qb[ks][h] = w.x;
+                        qb[ks][HR + h] = w.y;
+                    } else {
+                        qb[ks][h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks));
+                        qb[ks][HR + h] = __ldg(reinterpret_cast<const uint32_t *>(qr + 16 * ks + 8));
+                    }
                 }
+            }
+            if constexpr (Q8) {
+                // To f16, the row's largest element brought to [2^14, 2^15): what that leaves of
+                // a number below 2^-14 is a multiple of 2^-24, 2^-38 of the largest at most.
+                float most = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w = qb[ks][HR * i + h];
+                        most = amax_nan(most, amax_nan(bf16lo(w), bf16hi(w)));
+                    }
+                most = amax_nan(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = amax_nan(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                const uint32_t e = max(__float_as_uint(most) >> 23, 15u);
+                const float up = __uint_as_float((268 - e) << 23);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w = qb[ks][HR * i + h];
+                        const __half2 y = __floats2half2_rn(bf16lo(w) * up, bf16hi(w) * up);
+                        qb[ks][HR * i + h] = *reinterpret_cast<const uint32_t *>(&y);
+                    }
+                // the way back, from the lanes of rows 2tq, + 1
+                const float down = __uint_as_float((e - 14) << 23) * p.scale_log2;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    sl_next[h][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * tq + c));
             }
         }
         return true;
@@ -565,6 +679,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phases = 0;   // of the group's full barriers, a bit each
     for (int k = group; sg.stages >= 0; k += kGroups) {
         const int rows = sg.T * p.G;
+        float sl[HR][2];        // a score's factor, in log2 units
+#pragma unroll
+        for (int h = 0; h < HR; ++h)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) sl[h][c] = Q8 ? sl_next[h][c] : p.scale_log2;
         // this thread's columns of the products: rows 8h + 2tq, + 1 (positions of rows past the
         // last one: the last)
         int qpos[HR][2];
@@ -583,11 +702,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < HR; ++h) o[i][h][0] = o[i][h][1] = o[i][h][2] = o[i][h][3] = 0.f;
         float m[HR][2], mr[HR][2], l[HR][2];      // mr: m, or 0 while m is -inf
+        float mo[HR][2];        // an 8-bit cache's: O's reference, the weight of 1 of a value of 1
 #pragma unroll
         for (int h = 0; h < HR; ++h)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                m[h][c] = -CUDART_INF_F;
+                m[h][c] = mo[h][c] = -CUDART_INF_F;
                 mr[h][c] = l[h][c] = 0.f;
             }
         for (int j = 0, u = sg.u0; j < sg.stages; ++j, ++u) {
@@ -597,8 +717,204 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return;
             }
             phases ^= 1u << st;
-            const int kb = (sg.unit0 + j) * kUnit + part;   // this warp's 16 keys
-            if (kb < sg.S && kb + 15 >= lo) {
+            const int kb = (sg.unit0 + j) * kUnit + part;   // this warp's keys
+            if constexpr (Q8) {
+                if (kb < sg.S && kb + 31 >= lo) {
+                    const uint32_t base = ring + st * kStageBytes;
+                    const uint16_t *bytes = reinterpret_cast<const uint16_t *>(
+                                                smem + Ring<Q8>::kScales) + st * kUnit + part;
+                    // ---- scores: two blocks of 16 keys x rows
+                    float x[2][HR][4], xs[2][2][HR][4];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int h = 0; h < HR; ++h)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) xs[0][b][h][e] = xs[1][b][h][e] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            uint32_t w[4];
+                            ldsm4(w, ((base + k8) ^ (i << 5)) + b * 16 * kD);
+#pragma unroll
+                            for (int s = 0; s < 2; ++s) {
+                                const uint32_t a0 = e4m3x2_f16x2(w[2 * s]);
+                                const uint32_t a1 = e4m3x2_f16x2(w[2 * s + 1]);
+                                const uint32_t a2 = e4m3x2_f16x2(w[2 * s] >> 16);
+                                const uint32_t a3 = e4m3x2_f16x2(w[2 * s + 1] >> 16);
+#pragma unroll
+                                for (int h = 0; h < HR; ++h)
+                                    mma16816_f16(xs[s][b][h], a0, a1, a2, a3, qb[2 * i + s][h],
+                                                 qb[2 * i + s][HR + h]);
+                            }
+                        }
+                    // x[b][h]: keys kb + 16b + gq (rows 8h + 2tq, + 1) and + 8 + (gq ^ 4)
+                    float ev[2][2];   // the values' exponents
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const uint32_t w = bytes[16 * b + (f ? 8 + (gq ^ 4) : gq)];
+                            const float kf = scale_of(w & 255u);
+                            ev[b][f] = exponent_of(w >> 8);
+#pragma unroll
+                            for (int h = 0; h < HR; ++h)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    x[b][h][2 * f + c] =
+                                        (xs[0][b][h][2 * f + c] + xs[1][b][h][2 * f + c]) * kf;
+                        }
+                    const bool edge = kb + 31 > q_first || kb < lo_all;   // of the mask
+                    uint32_t hidden = 0;   // bits 4 (2b + h) + e
+                    if (edge) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int h = 0; h < HR; ++h)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int key = kb + 16 * b + (e >> 1 ? 8 + (gq ^ 4) : gq);
+                                    const int at = qpos[h][e & 1];
+                                    if (key > at || (p.window > 0 && at - key >= p.window)) {
+                                        x[b][h][e] = -CUDART_INF_F;
+                                        hidden |= 1u << (4 * (2 * b + h) + e);
+                                    }
+                                }
+                    }
+                    // ---- online softmax: the references move only when something exceeds them
+                    // by 2^6
+                    bool grow = false;
+                    float top[HR][2], topo[HR][2];
+#pragma unroll
+                    for (int h = 0; h < HR; ++h)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float t = -CUDART_INF_F, to = -CUDART_INF_F;
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                                for (int f = 0; f < 2; ++f) {
+                                    const float y = x[b][h][2 * f + c];
+                                    t = fmaxf(t, y);
+                                    to = fmaxf(to, fmaf(y, sl[h][c], ev[b][f]));
+                                }
+                            top[h][c] = t * sl[h][c];
+                            topo[h][c] = to;
+                            grow |= top[h][c] > m[h][c] + kGrow8 || to > mo[h][c] + kGrow8;
+                        }
+                    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                        for (int h = 0; h < HR; ++h)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float mx = top[h][c], mxo = topo[h][c];
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1) {
+                                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                                    mxo = fmaxf(mxo, __shfl_xor_sync(0xffffffffu, mxo, d));
+                                }
+                                const float mn = fmaxf(m[h][c], mx), mno = fmaxf(mo[h][c], mxo);
+                                const float f = m[h][c] == -CUDART_INF_F ? 0.f : ex2_approx(m[h][c] - mn);
+                                const float fo =
+                                    mo[h][c] == -CUDART_INF_F ? 1.f : ex2_approx(mo[h][c] - mno);
+                                m[h][c] = mn;
+                                mr[h][c] = mn == -CUDART_INF_F ? 0.f : mn;
+                                l[h][c] *= f;
+                                mo[h][c] = mno;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    o[i][h][c] *= fo;
+                                    o[i][h][2 + c] *= fo;
+                                }
+                            }
+                    }
+                    // P as the B operand: row gq of half h, the score rows 2tq, + 1 and 8 + 2tq,
+                    // + 1 of a block.  The sum takes the weights, O their products with the
+                    // values' powers of two, 2^9 where that is the reference.
+                    uint32_t pb[2][HR][2];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int h = 0; h < HR; ++h) {
+                            float w[4], wv[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int c = e & 1;
+                                const float ro = mo[h][c] == -CUDART_INF_F ? 0.f : mo[h][c] - kShift8;
+                                w[e] = ex2_approx(fmaf(x[b][h][e], sl[h][c], -mr[h][c]));
+                                wv[e] = ex2_approx(fmaf(x[b][h][e], sl[h][c], ev[b][e >> 1] - ro));
+                            }
+                            if (edge) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (hidden >> (4 * (2 * b + h) + e) & 1) wv[e] = 0.f;
+                            }
+                            l[h][0] += w[0] + w[2];
+                            l[h][1] += w[1] + w[3];
+                            pb[b][h][0] = transpose8x8(pack_f16x2(wv[0], wv[1]));
+                            pb[b][h][1] = transpose8x8(pack_f16x2(wv[2], wv[3]));
+                        }
+                    // ---- O += V^T P
+                    uint32_t seen[2] = {0xffffffffu, 0xffffffffu};   // keys that some row sees
+                    if (edge) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            seen[b] = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = 2 * tq + (i & 1);
+                                const int key = kb + 16 * b + (i & 2 ? 8 + (r ^ 4) : r);
+                                if (key >= lo && key < sg.S) seen[b] |= 0xffu << (8 * i);
+                            }
+                        }
+                    }
+                    bool stripped = false;
+#pragma unroll
+                    for (int nn = 0; nn < 8; ++nn) {
+                        uint32_t w[4];
+                        ldsm_b8_trans(w, (base + v8) ^ (nn << 4));
+                        if (edge) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                w[i] &= seen[i >> 1];
+                                if (sg.T > 1) stripped |= strip_nan(w[i]);
+                            }
+                        }
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const uint32_t a0 = e4m3x2_f16x2(w[2 * b]);
+                            const uint32_t a1 = e4m3x2_f16x2(w[2 * b + 1]);
+                            const uint32_t a2 = e4m3x2_f16x2(w[2 * b] >> 16);
+                            const uint32_t a3 = e4m3x2_f16x2(w[2 * b + 1] >> 16);
+#pragma unroll
+                            for (int h = 0; h < HR; ++h)
+                                mma16816_f16(o[nn][h], a0, a1, a2, a3, pb[b][h][0], pb[b][h][1]);
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, stripped)) {
+                        // the NaN that were taken out, for the rows that see them
+                        for (int kk = 0; kk < 32; ++kk) {
+                            const int key = kb + kk;
+                            if (key < lo || key >= sg.S) continue;
+                            const uint8_t *vr = smem + st * kStageBytes + kTileBytes + (part + kk) * kD + gq;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    if ((vr[((i ^ (kk & 7)) << 4) + 8 * e] & 0x7f) != 0x7f) continue;
+#pragma unroll
+                                    for (int h = 0; h < HR; ++h)
+#pragma unroll
+                                        for (int c = 0; c < 2; ++c)
+                                            if (key <= qpos[h][c] &&
+                                                (p.window <= 0 || qpos[h][c] - key < p.window))
+                                                o[i][h][2 * e + c] = CUDART_NAN_F;
+                                }
+                        }
+                    }
+                }
+            } else if (kb < sg.S && kb + 15 >= lo) {
                 const uint32_t base = ring + st * kStageBytes;
                 // ---- scores: 16 keys x rows, in chains of four products
                 constexpr int kChains = 2;
@@ -733,6 +1049,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->empty[st]);
+        }
+        if constexpr (Q8) {
+            // O relative to m: times 2^(mo - 9 - m), in two steps as that may be 2^-135
+#pragma unroll
+            for (int h = 0; h < HR; ++h)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (mo[h][c] == -CUDART_INF_F) continue;   // O is 0, or NaN
+                    float mg = m[h][c], mog = mo[h][c];
+                    const float f = ex2_approx(0.5f * (mog - kShift8 - mg));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[i][h][c] = o[i][h][c] * f * f;
+                        o[i][h][2 + c] = o[i][h][2 + c] * f * f;
+                    }
+                }
         }
         // ---- the pair's (or span's) result.  The next one's queries are on their way
         // meanwhile.
@@ -898,7 +1230,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_ke
 }
 
 // Short caches: whole pairs per CTA, one after the other, and no combine.
-bool whole_pairs(int max_kv) { return max_kv <= 8 * kUnit; }
+bool whole_pairs(int max_kv) { return max_kv <= 512; }
 
 }  // namespace
 
@@ -908,29 +1240,35 @@ namespace {
 // Chunks of a batch that is not run by whole pairs.  Equal runs are not equal times (the
 // slowest SMs take a tenth longer), so the batch is cut into levels of smaller and smaller
 // chunks; not where it is small, or has so few pairs that one would have hundreds of partials.
-int n_chunks(int nseq, int max_kv, int Hkv, int max_q, int window) {
-    const long pairs = (long)nseq * Hkv, all = (max_kv + kUnit - 1) / kUnit;
+int n_chunks(int nseq, int max_kv, int Hkv, int max_q, int window, int unit) {
+    const long pairs = (long)nseq * Hkv, all = (max_kv + unit - 1) / unit;
     // a span of window + max_q - 1 keys touches at most this many units
-    const long most = window > 0 ? ((long)window + max_q - 2) / kUnit + 2 : all;
+    const long most = window > 0 ? ((long)window + max_q - 2) / unit + 2 : all;
     return pairs >= kSMs / 4 && pairs * (most < all ? most : all) >= (long)kMinRun * kSMs
                ? kLevels * kSMs
                : kSMs;
 }
 }  // namespace
 
-size_t paged_decode_workspace_bytes(int nseq, int max_kv, int Hkv) {
+size_t paged_decode_workspace_bytes(int nseq, int max_kv, int Hkv, bool q8) {
     if (whole_pairs(max_kv)) return 0;
-    const size_t chunks = n_chunks(nseq, max_kv, Hkv, 1, 0);
+    const size_t chunks =
+        n_chunks(nseq, max_kv, Hkv, 1, 0, q8 ? Ring<true>::kUnit : Ring<false>::kUnit);
     return 2 * chunks * kMaxRows * (kD + 2) * sizeof(float) + chunks * sizeof(Joint);
 }
 
 // Units are counted in 32 bits (the last level of chunks may pass the end by kSMs - 1).
 bool paged_decode_counts_fit(int nseq, int max_kv, int Hkv) {
     const long pairs = (long)nseq * Hkv, most = 0x7fffffffL - kSMs;
-    return pairs <= most && pairs * ((max_kv + kUnit - 1) / kUnit) <= most;
+    constexpr int unit = Ring<false>::kUnit;   // the smaller one
+    return pairs <= most && pairs * ((max_kv + unit - 1) / unit) <= most;
 }
 
-int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
+namespace {
+template <bool Q8>
+int launch_decode_of(const PackedAttn &a, const void *scales, void *ws, int *status,
+                     cudaStream_t s) {
+    constexpr int kUnit = Ring<Q8>::kUnit, kSmemBytes = Ring<Q8>::kBytes;
     const gqa_paged_kv &c = *a.cache;
     Params p{};
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
@@ -939,6 +1277,7 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
     p.cu = a.cu;
     p.kv_lens = c.kv_lens;
     p.pages = c.page_table;
+    p.scales = static_cast<const uint8_t *>(scales);
     p.status = status;
     p.q_stride = a.q_stride;
     p.o_stride = a.o_stride;
@@ -956,25 +1295,33 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.whole = whole_pairs(a.max_kv);
     if (!p.whole) {
-        p.chunks = n_chunks(a.nseq, a.max_kv, a.Hkv, a.max_q, a.window);
+        p.chunks = n_chunks(a.nseq, a.max_kv, a.Hkv, a.max_q, a.window, kUnit);
         const size_t rec = (size_t)2 * p.chunks * kMaxRows;
         p.ws_o = static_cast<float *>(ws);
         p.ws_ml = p.ws_o + rec * kD;
         p.ws_joint = reinterpret_cast<Joint *>(p.ws_ml + rec * 2);
     }
-    // {64 dims, rows, 2 halves, (page, KV head)}: a page, or 64 rows of it, per box
-    const uint64_t page = c.page_size;
-    const uint64_t dims[4] = {64, page, 2, (uint64_t)c.num_pages * c.Hkv};
-    const uint64_t strides[3] = {256, 128, page * 256};
-    const uint32_t box[4] = {64, (uint32_t)(page < kUnit ? page : kUnit), 2, 1};
+    // a page, or a unit's rows of it, per box
+    const uint64_t page = c.page_size, slabs = (uint64_t)c.num_pages * c.Hkv;
+    const uint32_t rows = page < kUnit ? page : kUnit;
     CUtensorMap mk, mv;
-    if (!make_bf16_map(&mk, c.k, 4, dims, strides, box) ||
-        !make_bf16_map(&mv, c.v, 4, dims, strides, box))
-        return GQA_ERR_CUDA;
+    if constexpr (Q8) {   // {128 numbers, rows, (page, KV head)}
+        const uint64_t dims[3] = {kD, page, slabs}, strides[2] = {kD, page * kD};
+        const uint32_t box[3] = {kD, rows, 1};
+        if (!make_byte_map(&mk, c.k, 3, dims, strides, box) ||
+            !make_byte_map(&mv, c.v, 3, dims, strides, box))
+            return GQA_ERR_CUDA;
+    } else {              // {64 dims, rows, 2 halves, (page, KV head)}
+        const uint64_t dims[4] = {64, page, 2, slabs}, strides[3] = {256, 128, page * 256};
+        const uint32_t box[4] = {64, rows, 2, 1};
+        if (!make_bf16_map(&mk, c.k, 4, dims, strides, box) ||
+            !make_bf16_map(&mv, c.v, 4, dims, strides, box))
+            return GQA_ERR_CUDA;
+    }
     const long pairs = (long)a.nseq * a.Hkv;
     const long grid = !p.whole ? p.chunks : pairs < kSMs ? pairs : kSMs;
     const bool eight = static_cast<long>(a.max_q) * p.G <= 8;
-    auto kern = eight ? paged_decode_kernel<8> : paged_decode_kernel<16>;
+    auto kern = eight ? paged_decode_kernel<8, Q8> : paged_decode_kernel<16, Q8>;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), kSmemBytes) != cudaSuccess)
         return GQA_ERR_CUDA;
     if (launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmemBytes, s, mk, mv,
@@ -988,6 +1335,13 @@ int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t
             return GQA_ERR_CUDA;
     }
     return GQA_OK;
+}
+}  // namespace
+
+int launch_paged_decode(const PackedAttn &a, const void *scales, void *ws, int *status,
+                        cudaStream_t s) {
+    return scales ? launch_decode_of<true>(a, scales, ws, status, s)
+                  : launch_decode_of<false>(a, nullptr, ws, status, s);
 }
 
 }  // namespace gqa
