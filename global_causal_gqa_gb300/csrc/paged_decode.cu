@@ -62,6 +62,7 @@ constexpr int kConsumers = 4;                   // warps of a group, a quarter o
 constexpr int kGroups = 2;                      // groups of consumers, which take the pairs in turn
 constexpr int kThreads = 32 * (kGroups * kConsumers + 1);
 constexpr int kMaxRows = 16;
+constexpr int kScaleCopies = 16;                // lanes that copy an 8-bit stage's 256 scale bytes
 
 // What the two kinds of cache differ in: keys of a stage (a unit), stages of the ring, and shared
 // memory, in which an 8-bit cache's ring is followed by its stages' scale bytes.
@@ -116,6 +117,7 @@ struct Params {
     int chunks;
     const int32_t *cu, *kv_lens, *pages;
     const uint8_t *scales;         // of an 8-bit cache
+    int joint, v_first;            // an 8-bit cache's box has keys and values, these first
     int *status;
     long q_stride, o_stride;
     PackedBounds bounds;
@@ -260,6 +262,17 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
 
+// Copies 16 bytes to shared memory, or `bytes` of them and zeros, and arrives on the barrier when
+// they are there (an arrival of its own, which the barrier's count includes).
+__device__ __forceinline__ void copy_async16(void *dst, const void *src, uint32_t bytes,
+                                             uint64_t *bar) {
+    asm volatile(
+        "cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t"
+        "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%3];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 enum Role { kRoleProducer = 0, kRoleConsumer = 2 };
 constexpr int kSite = kDiagPagedDecode << 24;   // of the debug build's checks
 
@@ -277,17 +290,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
     Bars *bars = reinterpret_cast<Bars *>(smem + Ring<Q8>::kBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // The groups take a pair's stages in turn, or the pairs.
+    const bool both = Q8 && !p.whole;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            for (int g = 0; g < kGroups; ++g) mbar_init(&bars->full[g][i], kUnit / min(p.page_size, kUnit));
+            for (int g = 0; g < kGroups; ++g)
+                mbar_init(&bars->full[g][i],
+                          kUnit / min(p.page_size, kUnit) + (Q8 ? kScaleCopies : 0));
             mbar_init(&bars->empty[i], kConsumers);
         }
         for (int i = 0; i < kSegSlots; ++i) {
             mbar_init(&bars->seg_full[i], 1);
-            mbar_init(&bars->seg_free[i], kConsumers);
+            mbar_init(&bars->seg_free[i], both ? kGroups * kConsumers : kConsumers);
         }
-        for (int g = 0; g < kGroups; ++g) mbar_init(&bars->merge[g], kConsumers);
+        for (int g = 0; g < kGroups; ++g)
+            mbar_init(&bars->merge[g], both ? kGroups * kConsumers : kConsumers);
         mbar_init(&bars->clc_full, 1);
         fence_mbar_init();
     }
@@ -460,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (run == 0) next_chunk();
             if (!ok) return;
             ahead = next_segment();
-            const int records = ahead.stages < 0 ? kGroups : 1;
+            const int records = ahead.stages < 0 && !both ? kGroups : 1;
             for (int i = 0; i < records; ++i, ++k) {
                 const int slot = k & (kSegSlots - 1);
                 if (k >= kSegSlots && !warp_wait(&bars->seg_free[slot], (k / kSegSlots - 1) & 1)) {
@@ -490,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         advance();
         Segment sg = ahead;
         PageWalk walk = walk_ahead;
-        auto load = [&](int group) {
+        auto load = [&](int turn) {
             const int lo = p.window > 0 ? max(0, sg.S - sg.T - p.window + 1) : 0;
             for (int j = 0; j < sg.stages; ++j, ++u) {
                 // the slab of this lane's box; -1 for one that no row sees or that is not in
@@ -503,32 +521,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (pg >= 0 && pg < p.num_pages) slab = pg * p.Hkv + sg.g;
                     else set_status(p.status, GQA_ERR_INVALID_ARG);
                 }
-                const int st = u % kStages;
+                const int st = u % kStages, group = (both ? j : turn) % kGroups;
                 uint64_t *full = &bars->full[group][st];
-                uint8_t *dst = smem + st * kStageBytes + lane * box * kRow;
+                uint8_t *dst = smem + st * kStageBytes + lane * box * kRow * (Q8 ? 2 : 1);
                 const int row = unit_key & (p.page_size - 1);
                 // every lane with a box waits, announces its bytes and loads for itself
                 const bool free = u < kStages || mbar_wait(&bars->empty[st], (u / kStages - 1) & 1);
                 if (free && lane < boxes) {
+                    mbar_arrive_expect_tx(full, 2 * box * kRow);
                     if constexpr (Q8) {
-                        uint8_t *bytes = smem + Ring<Q8>::kScales + (st * kUnit + lane * box) * 2;
-                        if (slab < 0) {   // (zeros with any power of two)
-                            for (int i = 0; i < box / 8; ++i)
-                                reinterpret_cast<uint4 *>(bytes)[i] =
-                                    make_uint4(0x01010101, 0x01010101, 0x01010101, 0x01010101);
-                            fence_proxy_async_smem();
-                        }
-                        mbar_arrive_expect_tx(full, 2 * box * kRow + (slab < 0 ? 0 : 2 * box));
-                        tma_load_3d(dst, &tmK, full, 0, row, slab);
-                        tma_load_3d(dst + kTileBytes, &tmV, full, 0, row, slab);
-                        if (slab >= 0)
-                            bulk_copy_g2s(bytes, p.scales + ((long)slab * p.page_size + row) * 2,
-                                          2 * box, full);
+                        tma_load_4d(dst, &tmK, full, 0, row, slab, 0);
+                        if (!p.joint) tma_load_4d(dst + box * kRow, &tmV, full, 0, row, slab, 0);
                     } else {
-                        mbar_arrive_expect_tx(full, 2 * box * kRow);
                         tma_load_4d(dst, &tmK, full, 0, row, 0, slab);
                         tma_load_4d(dst + kTileBytes, &tmV, full, 0, row, 0, slab);
                     }
+                }
+                if constexpr (Q8) {
+                    // the bytes of 8 keys per lane (a third copy per page by TMA took longer than
+                    // the keys: windows of 2048 in pages of 16 @@)
+                    const int key = 8 * lane & (kUnit - 1), from = key / box;
+                    const int at = __shfl_sync(0xffffffffu, slab, from);
+                    if (free && lane < kScaleCopies)
+                        copy_async16(smem + Ring<Q8>::kScales + (st * kUnit + key) * 2,
+                                     p.scales + ((long)max(at, 0) * p.page_size + row + key % box) * 2,
+                                     at >= 0 ? 16 : 0, full);
                 }
                 if (!__all_sync(0xffffffffu, free)) {
                     set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 1, u);
@@ -550,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int part = 0; part < 2 && ok; ++part) {
                 if (part == late) advance();
-                else load(turn % kGroups);
+                else load(turn);
             }
         }
         if (!ok) {   // never leave the CTA with copies in flight
@@ -593,19 +610,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     // are the keys of its pairs 2tq, + 1 and 8 + 2tq, + 1 in the value product: rows 4i .. 4i + 3
     // are the score rows 2i, 2i + 1, 8 + 2i, 8 + 2i + 1.  (The ^ 4: eight rows of either operand
     // lie in eight different swizzled columns.)
-    uint32_t k8 = 0, v8 = 0;
+    // A box of a stage has the keys of a page (or a unit's rows of it) and their values.
+    uint32_t k8[2] = {0, 0}, v8 = 0, block8[2] = {0, 0};
+    const uint32_t values8 = p.v_first ? 0 : box * kD, keys8 = box * kD - values8;
     if constexpr (Q8) {
         const int kk = mat & 1 ? 8 + (l7 ^ 4) : l7;
-        k8 = (part + kk) * kD + (((mat >> 1) ^ (kk & 7)) << 4);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            block8[b] = (part + 16 * b) / box * 2 * box * kD + (part + 16 * b) % box * kD;
+            k8[b] = block8[b] + keys8 + kk * kD + (((mat >> 1) ^ (kk & 7)) << 4);
+        }
         const int rho = lane & 15, i = 2 * (rho >> 2) + (rho & 1);
         const int vk = rho & 2 ? 8 + (i ^ 4) : i;
-        v8 = kTileBytes + (part + 16 * (lane >> 4) + vk) * kD + ((vk & 7) << 4);
+        v8 = block8[lane >> 4] + values8 + vk * kD + ((vk & 7) << 4);
     }
     int meets = 0;
     auto meet = [&]() {
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->merge[group]);
-        if (warp_wait(&bars->merge[group], meets++ & 1)) return true;
+        uint64_t *bar = &bars->merge[both ? 0 : group];
+        if (lane == 0) mbar_arrive(bar);
+        if (warp_wait(bar, meets++ & 1)) return true;
         set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 2, meets);
         return false;
     };
@@ -675,9 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
     };
-    if (!next_segment(group)) return;
+    const int first = both ? 0 : group, step = both ? 1 : kGroups;
+    if (!next_segment(first)) return;
     uint32_t phases = 0;   // of the group's full barriers, a bit each
-    for (int k = group; sg.stages >= 0; k += kGroups) {
+    for (int k = first; sg.stages >= 0; k += step) {
         const int rows = sg.T * p.G;
         float sl[HR][2];        // a score's factor, in log2 units
 #pragma unroll
@@ -710,7 +735,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m[h][c] = mo[h][c] = -CUDART_INF_F;
                 mr[h][c] = l[h][c] = 0.f;
             }
-        for (int j = 0, u = sg.u0; j < sg.stages; ++j, ++u) {
+        const int j0 = both ? group : 0, dj = both ? kGroups : 1;
+        for (int j = j0, u = sg.u0 + j0; j < sg.stages; j += dj, u += dj) {
             const int st = u % kStages;
             if (!warp_wait(&bars->full[group][st], phases >> st & 1)) {
                 set_timeout(p.status, kDiagPagedDecode, kRoleConsumer, 1, u);
@@ -736,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             uint32_t w[4];
-                            ldsm4(w, ((base + k8) ^ (i << 5)) + b * 16 * kD);
+                            ldsm4(w, (base + k8[b]) ^ (i << 5));
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
                                 const uint32_t a0 = e4m3x2_f16x2(w[2 * s]);
@@ -897,7 +923,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int kk = 0; kk < 32; ++kk) {
                             const int key = kb + kk;
                             if (key < lo || key >= sg.S) continue;
-                            const uint8_t *vr = smem + st * kStageBytes + kTileBytes + (part + kk) * kD + gq;
+                            const uint8_t *vr = smem + st * kStageBytes + block8[kk >> 4] + values8 +
+                                                (kk & 15) * kD + gq;
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -1069,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- the pair's (or span's) result.  The next one's queries are on their way
         // meanwhile.
         const int row0 = sg.row0, head0 = sg.g * p.G, out = sg.slot;
-        if (!next_segment(k + kGroups)) return;
+        if (!next_segment(k + step)) return;
         // The warps' shares meet in shared memory, 8 rows at a time, each relative to its own
         // maximum: [warp][row][128 dims], a row's dims permuted so that the lanes (4 rows x 8
         // dims) meet 32 different banks.
@@ -1090,31 +1117,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!meet()) return;
-            // a warp adds up every fourth row, 4 dims per lane
-            for (int rr = cw; rr < min(8, rows - 8 * h); rr += kConsumers) {
+            // a warp adds up every fourth row (every eighth of the groups' together), 4 dims per
+            // lane
+            const float2(*mls)[8] = both ? bars->ml[0] : ml;
+            const float *shares = both ? xchg - group * kConsumers * 8 * kD : xchg;
+            for (int rr = both ? warp : cw; rr < min(8, rows - 8 * h);
+                 rr += both ? kGroups * kConsumers : kConsumers) {
                 const int r = 8 * h + rr;
-                float2 x[kConsumers];
+                constexpr int kShares = Q8 ? kGroups * kConsumers : kConsumers;
+                float2 x[kShares];
                 float4 y[kConsumers];
                 float M = -CUDART_INF_F, L = 0.f;
-#pragma unroll
-                for (int w = 0; w < kConsumers; ++w) {
-                    x[w] = ml[w][rr];
-                    y[w] = *reinterpret_cast<const float4 *>(xchg + (w * 8 + rr) * kD +
+                auto share = [&](int w) {
+                    return *reinterpret_cast<const float4 *>(shares + (w * 8 + rr) * kD +
                                                              ((4 * lane) ^ ((rr >> 1 & 3) << 3)));
+                };
+#pragma unroll
+                for (int w = 0; w < kShares; ++w) {
+                    if (w >= kConsumers && !both) continue;
+                    x[w] = mls[w][rr];
+                    if (w < kConsumers) y[w] = share(w);
                     M = fmaxf(M, x[w].x);
                 }
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kConsumers; ++w) {
+                for (int w = 0; w < kShares; ++w) {
+                    if (w >= kConsumers && !both) continue;
+                    const float4 yw = w < kConsumers ? y[w % kConsumers] : share(w);
                     // a share none of whose keys this row sees: m = -inf, l = 0 and O = 0 (NaN
                     // scores alone also leave m at -inf, with l and O NaN)
                     const float f = x[w].x == -CUDART_INF_F ? (x[w].y == 0.f ? 0.f : 1.f)
                                                             : ex2_approx(x[w].x - M);
                     L = fmaf(x[w].y, f, L);
-                    acc.x = fmaf(y[w].x, f, acc.x);
-                    acc.y = fmaf(y[w].y, f, acc.y);
-                    acc.z = fmaf(y[w].z, f, acc.z);
-                    acc.w = fmaf(y[w].w, f, acc.w);
+                    acc.x = fmaf(yw.x, f, acc.x);
+                    acc.y = fmaf(yw.y, f, acc.y);
+                    acc.z = fmaf(yw.z, f, acc.z);
+                    acc.w = fmaf(yw.w, f, acc.w);
                 }
                 if (out >= 0) {
                     const size_t rec = (size_t)out * kMaxRows + r;
@@ -1305,11 +1343,18 @@ int launch_decode_of(const PackedAttn &a, const void *scales, void *ws, int *sta
     const uint64_t page = c.page_size, slabs = (uint64_t)c.num_pages * c.Hkv;
     const uint32_t rows = page < kUnit ? page : kUnit;
     CUtensorMap mk, mv;
-    if constexpr (Q8) {   // {128 numbers, rows, (page, KV head)}
-        const uint64_t dims[3] = {kD, page, slabs}, strides[2] = {kD, page * kD};
-        const uint32_t box[3] = {kD, rows, 1};
-        if (!make_byte_map(&mk, c.k, 3, dims, strides, box) ||
-            !make_byte_map(&mv, c.v, 3, dims, strides, box))
+    if constexpr (Q8) {
+        // {128 numbers, rows, (page, KV head), the two pools}: a map takes a stride from pool to
+        // pool below 2^40, and then a page's keys and values come as one copy; else as two
+        const uint64_t kp = reinterpret_cast<uint64_t>(c.k), vp = reinterpret_cast<uint64_t>(c.v);
+        const uint64_t apart = kp < vp ? vp - kp : kp - vp;
+        p.joint = apart < (1ull << 40);
+        p.v_first = p.joint && vp < kp;
+        const uint64_t dims[4] = {kD, page, slabs, p.joint ? 2u : 1u};
+        const uint64_t strides[3] = {kD, page * kD, p.joint ? apart : slabs * page * kD};
+        const uint32_t box[4] = {kD, rows, 1, p.joint ? 2u : 1u};
+        if (!make_byte_map(&mk, p.v_first ? c.v : c.k, 4, dims, strides, box) ||
+            !make_byte_map(&mv, c.v, 4, dims, strides, box))
             return GQA_ERR_CUDA;
     } else {              // {64 dims, rows, 2 halves, (page, KV head)}
         const uint64_t dims[4] = {64, page, 2, slabs}, strides[3] = {256, 128, page * 256};
