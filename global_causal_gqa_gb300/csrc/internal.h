@@ -157,10 +157,8 @@ size_t packed_prefill_workspace_bytes(int nseq, int total, int max_kv, int Hq, i
 bool packed_prefill_counts_fit(int nseq, int total, int max_kv, int Hq, int Hkv);
 // the streaming kernel for a few rows per sequence (paged_decode.cu)
 bool paged_decode_fits(int max_q, int G);
-// (`scales`: those of an 8-bit cache whose pools a.cache describes, else nullptr)
-int launch_paged_decode(const PackedAttn &a, const void *scales, void *ws, int *status,
-                        cudaStream_t s);
-size_t paged_decode_workspace_bytes(int nseq, int max_kv, int Hkv, bool q8);
+int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s);
+size_t paged_decode_workspace_bytes(int nseq, int max_kv, int Hkv);
 bool paged_decode_counts_fit(int nseq, int max_kv, int Hkv);
 // A TMA map of bf16 elements: `rank` dims and box extents, innermost first, the strides of
 // dims 1 .. rank - 1 in bytes, 128-byte swizzle; false if the driver refuses it

@@ -58,7 +58,7 @@ bool make_byte_map(CUtensorMap *map, const void *base, int rank, const uint64_t 
 
 size_t paged_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv) {
     return paged_decode_fits(max_q, Hq / Hkv)
-               ? paged_decode_workspace_bytes(nseq, max_kv, Hkv, false)
+               ? paged_decode_workspace_bytes(nseq, max_kv, Hkv)
                : packed_prefill_workspace_bytes(nseq, total, max_kv, Hq, Hkv);
 }
 
@@ -70,7 +70,7 @@ bool paged_counts_fit(int nseq, int total, int max_q, int max_kv, int Hq, int Hk
 
 int launch_packed_attn(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
     if (a.cache && paged_decode_fits(a.max_q, a.Hq / a.Hkv))
-        return launch_paged_decode(a, nullptr, ws, status, s);
+        return launch_paged_decode(a, ws, status, s);
     return launch_packed_prefill(a, ws, status, s);
 }
 

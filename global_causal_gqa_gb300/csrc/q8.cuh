@@ -57,6 +57,14 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
     return r;
 }
+// Two f16 numbers as e5m2, rounded to nearest, the first in the low byte.
+__device__ __forceinline__ uint32_t to_e5m2x2(__half2 x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;"
+        : "=h"(r)
+        : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+    return r;
+}
 // Four e4m3 numbers times f, as bf16.
 __device__ __forceinline__ uint2 e4m3x4_bf16(uint32_t w, float f) {
     const uint32_t a = e4m3x2_f16x2(w & 0xffffu), b = e4m3x2_f16x2(w >> 16);

@@ -44,10 +44,12 @@ def values(data, byte):
 
 def attention64(q, kd, kb, vd, vb, window, scale):
     """packed_utils.attention64 over a sequence's numbers and bytes [S, Hkv, ...].  Besides the
-    roundings named there (a weight to bf16; an f16 weight is finer) a kernel may bring q to f16
-    with a row's largest element between 2^14 and 2^15, which changes an element by at most 2^-25,
-    2^-39 of the largest; and a weight times its value's power of two to f16 with the row's largest
-    such product between 2^3 and 2^15, which loses at most 2^-25 of it, 2^-28 of the largest."""
+    roundings named there (a weight to bf16: 2^-8; as a sum of three e5m2 numbers of an f16 it is
+    off by 2^-9 + 2^-11) a kernel may bring q to two e4m3 numbers with the row's largest element
+    between 2^7 and 2^8, h + l / 16: exact above 2^-3; below, l / 16 is a multiple of 2^-13, an
+    element is off by 2^-14 at most, 2^-21 of the largest.  And a weight times its value's power of
+    two is such a sum with the row's largest product between 2^12 and 2^15, and loses at most 2^-17
+    of it, 2^-29 of the largest."""
     S = kd.shape[0]
     k, v = values(kd, kb), values(vd, vb)
     o, lse, bo, bl = pu.attention64(q, k, v, window, scale)
@@ -58,13 +60,13 @@ def attention64(q, kd, kb, vd, vb, window, scale):
     see = (j <= i) & ((i - j < window) if window > 0 else (j <= i))
     for h in range(Hq):
         g = h // G
-        r = scale * 2.0 ** -38 * q[:, h].double().abs().amax(1) * k[:, g].abs().sum(1).max()
+        r = scale * 2.0 ** -21 * q[:, h].double().abs().amax(1) * k[:, g].abs().sum(1).max()
         p = torch.exp(scale * (q[:, h].double() @ k[:, g].T) - lse[h][:, None])
         p = torch.where(see, p, 0.0)
         bl[h] += r
         bo[:, h] += 2 * r[:, None] * (p @ v[:, g].abs())
         most = (p * torch.where(see, power(vb[:, g]), 0.0)).amax(1)
-        bo[:, h] += 2.0 ** -28 * most[:, None] * (see.double() @ numbers(vd[:, g]).abs())
+        bo[:, h] += 2.0 ** -29 * most[:, None] * (see.double() @ numbers(vd[:, g]).abs())
     return o, lse, bo, bl
 
 
