@@ -28,8 +28,8 @@
 //
 // Warps: two groups of four (softmax, a quarter of a stage's keys each; the groups take the pairs
 // in turn, so that one's ends pass while the other streams, or with 17 to 32 rows 16 of them
-// each), the producer, one that issues the products, and one that brings the queries into operands
-// a pair ahead.
+// each), the producer, two that issue the products, and one that brings the queries into operands a
+// pair ahead.
 #include "paged_stream.cuh"
 #include "q8.cuh"
 
@@ -37,12 +37,11 @@ namespace gqa {
 using namespace stream;
 namespace {
 
-constexpr int kProducerWarp = 8, kProductWarp = 9, kQueryWarp = 10;
+constexpr int kProducerWarp = 8, kScoreWarp = 9, kValueWarp = 10, kQueryWarp = 11;
 constexpr int kScoreTiles = 2;       // of a group, in tensor memory
 // A pair's factors are read after its queries' tile is free again, and that of the pair after next
 // may be, too, as scores are formed ahead.
 constexpr int kFactorSlots = 8;
-constexpr int kAhead = 3;            // stages whose scores are formed ahead of their values' product
 constexpr float kGrow = 3.0f, kShift = 12.0f, kLargest = 32768.0f;   // log2 units; 2^(3 + 12)
 // Values below 2^-100 count as 2^-100 in mo, so that 2^(m - mo) stays within fp32.
 constexpr float kLeast = -100.0f;
@@ -50,7 +49,7 @@ constexpr float kLeast = -100.0f;
 struct Q8Bars : StreamBars {
     uint64_t q_full[2], q_free[2];
     uint64_t s_full[kGroups][kScoreTiles], s_free[kGroups][kScoreTiles];
-    uint64_t p_full[kGroups], pv_done[kGroups], meet[kGroups], drained;
+    uint64_t p_full[kGroups], pv_done[kGroups], meet[kGroups], drained[2];
     uint32_t tmem;
     int vote[kGroups][2];            // the last stage of either parity that moved the references
     int nan_any[kGroups][2];
@@ -81,6 +80,9 @@ struct Layout {
     static constexpr int kColumns = R == 8 ? 128 : 256;
     static_assert(kOutputs + kGroups * kOutputStride <= kColumns, "tensor memory");
 };
+
+// Bytes of a stage from 8 keys (or values) to the next 8.
+__device__ __forceinline__ uint32_t key_step(const Params &p) { return p.joint ? 2048 : 1024; }
 
 // (Out of line: the records of expired waits are never run in earnest.)
 __device__ __noinline__ void expired(int *status, int role, int barrier, int n) {
@@ -195,119 +197,120 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
     }
 }
 
-// ---- the thread that issues the products --------------------------------------------------------
-// The scores of a stage as soon as its keys, its queries and a score tile are there, up to kAhead
-// stages ahead of the values' products, which come first where their weights are there.
+// ---- the threads that issue the products, a warp each -------------------------------------------
+// (One thread for both took 1500 cycles per stage, as it tests barriers and issues 46 cycles per
+// product in turn: 32 caches of 8k-64k tokens 548 us.)
+//
+// Scores: as soon as a stage's keys, its pair's queries and a score tile of its group are there.
 template <int R, bool SPLIT>
-__device__ __forceinline__ void issue_products(const Params &p, Q8Bars *bars, uint8_t *smem,
-                                               uint32_t tmem) {
+__device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint8_t *smem,
+                                             uint32_t tmem) {
     using L = Layout<R, SPLIT>;
     constexpr int kStages = L::S::kStages;
-    const uint32_t sbo = p.joint ? 2048 : 1024;   // from 8 keys to the next 8
     const uint32_t ring = smem_u32(smem);
-    const uint64_t kd0 = sdesc_sw128(ring + (p.joint && p.v_first ? 1024 : 0), 16, sbo);
-    const uint64_t vd0 =
-        sdesc_sw128(ring + (!p.joint ? kTileBytes : p.v_first ? 0 : 1024), 16, sbo);
+    const uint64_t kd0 = sdesc_sw128(ring + (p.joint && p.v_first ? 1024 : 0), 16, key_step(p));
     const uint64_t qd0 = sdesc_sw128(ring + L::kQ, 16, 1024);
-    const uint64_t pd0 = sdesc_sw128(ring + L::kP, 16, 1024);
-    constexpr uint32_t idesc_s = idesc_f8_f32(128, L::kScoreCols, 0, 0);
-    constexpr uint32_t idesc_o = idesc_f8_f32(128, L::kValueCols, 1, 1);
-    int u = 0, v = 0;                  // stages whose scores, whose values' products are issued
-    int handed[kGroups] = {0, 0};      // values' products of each group
-    int scored[kGroups] = {0, 0};      // scores of each group
-    uint32_t turn = 0, fresh = 0;      // of stage i, bit i & 7: its group; a pair's first one
-    int k = 0, j = 0, stages = 0;      // the segment, the stage within it (stages = 0: none at hand)
-    bool done = false;
-    uint64_t idle = 0;
-    while (!(done && v == u)) {
-        bool moved = false;
-        if (v < u) {
-            const int g = turn >> (v & 7) & 1;
-            bool ready = mbar_test(&bars->p_full[SPLIT ? 0 : g], handed[SPLIT ? 0 : g] & 1);
-            if (SPLIT) ready = ready && mbar_test(&bars->p_full[1], handed[1] & 1);
-            if (ready) {
-                tc_fence_after();
-                const int st = v % kStages;
-                const uint64_t vd = vd0 + st * (kStageBytes >> 4);
+    constexpr uint32_t idesc = idesc_f8_f32(128, L::kScoreCols, 0, 0);
+    int n[2] = {0, 0};                 // scores of a group's stages
+    for (int k = 0, u = 0;; ++k) {
+        const int slot = k & (kSegSlots - 1), b = k & 1;
+        if (!mbar_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
+            expired(p.status, kRoleProducts, 0, k);
+            break;
+        }
+        const int stages = bars->seg[slot].stages;
+        mbar_arrive(&bars->seg_free[slot]);
+        if (stages < 0) break;
+        bool ok = mbar_wait(&bars->q_full[b], k >> 1 & 1);
+        const int g0 = SPLIT ? 0 : b;
+        int m = b && !SPLIT ? n[1] : n[0];
+        for (int j = 0; ok && j < stages; ++j, ++u, ++m) {
+            const int st = u % kStages, tile = m % kScoreTiles;
+            if (m >= kScoreTiles)
 #pragma unroll
-                for (int i = 0; i < L::kTiles; ++i) {
-                    const int gi = SPLIT ? i : g;
-                    const uint64_t pd = pd0 + gi * (L::kWeights >> 4);
+                for (int i = 0; i < L::kTiles; ++i)
+                    ok = ok && mbar_wait(&bars->s_free[g0 + i][tile], (m / kScoreTiles - 1) & 1);
+            ok = ok && mbar_wait(&bars->full[0][st], (u / kStages) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = kd0 + st * (kStageBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_f8_ss(tmem + L::kOutputs + gi * L::kOutputStride, vd + kk * (sbo >> 2),
-                                   pd + 2 * kk, idesc_o, kk > 0 || !(fresh >> (v & 7) & 1));
-                    umma_commit(&bars->pv_done[gi]);
-                    ++handed[gi];
-                }
-                umma_commit(&bars->empty[st]);
-                ++v;
-                moved = true;
+            for (int i = 0; i < L::kTiles; ++i) {
+                const uint64_t qd = qd0 + (b * L::kTiles + i) * (L::kQuery >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_f8_ss(tmem + ((g0 + i) * kScoreTiles + tile) * L::kScoreCols, kd + 2 * kk,
+                               qd + 2 * kk, idesc, kk > 0);
+                // (this thread's own arrival hands on what it has seen: the stage's scale bytes and
+                // the queries' factors)
+                mbar_arrive(&bars->s_full[g0 + i][tile]);
+                umma_commit(&bars->s_full[g0 + i][tile]);
             }
         }
-        if (!moved && !done && u - v < kAhead) {
-            if (stages == 0) {
-                const int slot = k & (kSegSlots - 1);
-                if (mbar_test(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
-                    stages = bars->seg[slot].stages;
-                    mbar_arrive(&bars->seg_free[slot]);
-                    done = stages < 0;
-                    j = 0;
-                    moved = true;
-                }
-            } else {
-                const int st = u % kStages, b = k & 1;
-                bool ready = (j > 0 || mbar_test(&bars->q_full[b], k >> 1 & 1)) &&
-                             mbar_test(&bars->full[0][st], (u / kStages) & 1);
-#pragma unroll
-                for (int i = 0; i < L::kTiles; ++i) {
-                    const int gi = SPLIT ? i : b, n = scored[gi];
-                    ready = ready && (n < kScoreTiles ||
-                                      mbar_test(&bars->s_free[gi][n % kScoreTiles],
-                                                (n / kScoreTiles - 1) & 1));
-                }
-                if (ready) {
-                    tc_fence_after();
-                    const uint64_t kd = kd0 + st * (kStageBytes >> 4);
-#pragma unroll
-                    for (int i = 0; i < L::kTiles; ++i) {
-                        const int gi = SPLIT ? i : b, tile = scored[gi]++ % kScoreTiles;
-                        const uint64_t qd = qd0 + (b * L::kTiles + i) * (L::kQuery >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_f8_ss(tmem + (gi * kScoreTiles + tile) * L::kScoreCols, kd + 2 * kk,
-                                       qd + 2 * kk, idesc_s, kk > 0);
-                        // (this thread's own arrival hands on what it has seen: the stage's scale
-                        // bytes and the queries' factors)
-                        mbar_arrive(&bars->s_full[gi][tile]);
-                        umma_commit(&bars->s_full[gi][tile]);
-                    }
-                    const uint32_t bit = 1u << (u & 7);
-                    turn = b ? turn | bit : turn & ~bit;
-                    fresh = j == 0 ? fresh | bit : fresh & ~bit;
-                    ++u;
-                    if (++j == stages) {
-                        umma_commit(&bars->q_free[b]);
-                        stages = 0;
-                        ++k;
-                    }
-                    moved = true;
-                }
-            }
+        if (!ok) {
+            expired(p.status, kRoleProducts, 1, u);
+            break;
         }
-        if (moved) {
-            idle = 0;
-        } else {
-            const uint64_t now = globaltimer_ns();
-            if (idle == 0) idle = now;
-            else if (now - idle > GQA_WAIT_LIMIT_NS) {
-                expired(p.status, kRoleProducts, v < u ? 0 : 1, u);
-                break;
-            }
-        }
+        umma_commit(&bars->q_free[b]);
+        if (b && !SPLIT) n[1] = m;
+        else n[0] = m;
     }
-    umma_commit(&bars->drained);       // nothing in flight when the tensor memory is freed
-    if (!mbar_wait(&bars->drained, 0)) expired(p.status, kRoleProducts, 2, u);
+    umma_commit(&bars->drained[0]);    // nothing in flight when the tensor memory is freed
+    if (!mbar_wait(&bars->drained[0], 0)) expired(p.status, kRoleProducts, 2, 0);
+}
+
+// Values: as soon as a stage's weights are there.
+template <int R, bool SPLIT>
+__device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint8_t *smem,
+                                             uint32_t tmem) {
+    using L = Layout<R, SPLIT>;
+    constexpr int kStages = L::S::kStages;
+    const uint32_t ring = smem_u32(smem), step = key_step(p);
+    const uint64_t vd0 = sdesc_sw128(ring + (!p.joint ? kTileBytes : p.v_first ? 0 : 1024), 16, step);
+    const uint64_t pd0 = sdesc_sw128(ring + L::kP, 16, 1024);
+    constexpr uint32_t idesc = idesc_f8_f32(128, L::kValueCols, 1, 1);
+    int n[2] = {0, 0};                 // a group's products
+    for (int k = 0, u = 0;; ++k) {
+        const int slot = k & (kSegSlots - 1);
+        if (!mbar_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
+            expired(p.status, kRoleProducts, 3, k);
+            break;
+        }
+        const int stages = bars->seg[slot].stages;
+        mbar_arrive(&bars->seg_free[slot]);
+        if (stages < 0) break;
+        const int g0 = SPLIT ? 0 : k & 1;
+        int m = g0 ? n[1] : n[0];
+        bool ok = true;
+        for (int j = 0; j < stages; ++j, ++u, ++m) {
+            // (both groups': group 0 takes hidden values' NaN out for both)
+#pragma unroll
+            for (int i = 0; i < L::kTiles; ++i)
+                ok = ok && mbar_wait(&bars->p_full[g0 + i], m & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const int st = u % kStages;
+            const uint64_t vd = vd0 + st * (kStageBytes >> 4);
+#pragma unroll
+            for (int i = 0; i < L::kTiles; ++i) {
+                const uint64_t pd = pd0 + (g0 + i) * (L::kWeights >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_f8_ss(tmem + L::kOutputs + (g0 + i) * L::kOutputStride,
+                               vd + kk * (step >> 2), pd + 2 * kk, idesc, kk > 0 || j > 0);
+                umma_commit(&bars->pv_done[g0 + i]);
+            }
+            umma_commit(&bars->empty[st]);
+        }
+        if (!ok) {
+            expired(p.status, kRoleProducts, 4, u);
+            break;
+        }
+        if (g0) n[1] = m;
+        else n[0] = m;
+    }
+    umma_commit(&bars->drained[1]);
+    if (!mbar_wait(&bars->drained[1], 0)) expired(p.status, kRoleProducts, 5, 0);
 }
 
 // ---- a softmax group's warp ---------------------------------------------------------------------
@@ -619,7 +622,7 @@ __global__ void __launch_bounds__(Q8Stream<SPLIT>::kThreads, 1)
         }
         for (int i = 0; i < kSegSlots; ++i) {
             mbar_init(&bars->seg_full[i], 1);
-            mbar_init(&bars->seg_free[i], S::kReaders * kConsumers + 2);
+            mbar_init(&bars->seg_free[i], S::kReaders * kConsumers + 3);
         }
         for (int g = 0; g < kGroups; ++g) {
             mbar_init(&bars->q_full[g], 1);
@@ -631,9 +634,9 @@ __global__ void __launch_bounds__(Q8Stream<SPLIT>::kThreads, 1)
             mbar_init(&bars->p_full[g], kConsumers);
             mbar_init(&bars->pv_done[g], 1);
             mbar_init(&bars->meet[g], kConsumers);
+            mbar_init(&bars->drained[g], 1);
             for (int i = 0; i < 2; ++i) bars->vote[g][i] = bars->nan_any[g][i] = 0;
         }
-        mbar_init(&bars->drained, 1);
         mbar_init(&bars->clc_full, 1);
         fence_mbar_init();
     }
@@ -643,7 +646,7 @@ __global__ void __launch_bounds__(Q8Stream<SPLIT>::kThreads, 1)
     for (int i = threadIdx.x; i < 2 * 2 * R; i += S::kThreads)
         reinterpret_cast<uint4 *>(smem + L::kNan)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
-    if (warp == kProductWarp) {
+    if (warp == kScoreWarp) {
         tmem_alloc(&bars->tmem, L::kColumns);
         tmem_relinquish();
     }
@@ -655,11 +658,12 @@ __global__ void __launch_bounds__(Q8Stream<SPLIT>::kThreads, 1)
     if (warp < kGroups * kConsumers) softmax<R, SPLIT>(p, bars, smem, tmem);
     else if (warp == kProducerWarp) produce<S>(tmK, tmV, p, bars, smem, smem + L::kScales);
     else if (warp == kQueryWarp) bring_queries<R, SPLIT>(p, bars, smem);
-    else if (lane == 0) issue_products<R, SPLIT>(p, bars, smem, tmem);
+    else if (warp == kScoreWarp && lane == 0) issue_scores<R, SPLIT>(p, bars, smem, tmem);
+    else if (warp == kValueWarp && lane == 0) issue_values<R, SPLIT>(p, bars, smem, tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == kProductWarp) {
+    if (warp == kScoreWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kColumns);
     }

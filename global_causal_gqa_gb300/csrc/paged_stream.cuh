@@ -35,7 +35,7 @@ struct Bf16Stream {
 template <bool SPLIT>
 struct Q8Stream {
     static constexpr bool kQ8 = true;
-    static constexpr int kUnit = 128, kThreads = 32 * (kGroups * kConsumers + 3),
+    static constexpr int kUnit = 128, kThreads = 32 * (kGroups * kConsumers + 4),
                          kReaders = SPLIT ? kGroups : 1;
     static constexpr int kStages = SPLIT ? 5 : 6;
 };
