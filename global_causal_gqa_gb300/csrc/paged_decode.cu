@@ -49,7 +49,8 @@ using namespace stream;
 namespace {
 
 constexpr int kThreads = Bf16Stream::kThreads, kUnit = Bf16Stream::kUnit;
-constexpr int kStages = Bf16Stream::kStages;
+constexpr int kStages = Bf16Stream::kStages, kSegSlots = Bf16Stream::kSegSlots;
+constexpr int kGroups = Bf16Stream::kTeams;   // of consumers, which take the pairs in turn
 constexpr int kMaxRows = 16;
 constexpr int kSmemXchg = kStages * kStageBytes;
 constexpr int kSmemBar = kSmemXchg + kGroups * kConsumers * 8 * kD * 4;
@@ -463,7 +464,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_ke
     // (a chunk that an expired wait left out has no record: what its place holds is checked)
     const bool on = r < j.rows && j.rows <= p.rec_rows && j.parts >= 2 && j.parts <= p.chunks - c &&
                     j.g >= 0 && j.g < p.Hkv && j.row0 >= 0 &&
-                    j.row0 < p.bounds.total - token_of(p, j.rows - 1);
+                    j.r0 >= 0 && j.r0 < p.blocks * kBlockRows &&
+                    j.row0 < p.bounds.total - token_of(p, j.r0 + j.rows - 1);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -CUDART_INF_F, L = 0.f;
     if (on) {
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_ke
         }
     }
     if (!on) return;
-    const int t = token_of(p, r), h = j.g * p.G + r - t * p.G;
+    const int t = token_of(p, j.r0 + r), h = j.g * p.G + j.r0 + r - t * p.G;
     const long row = j.row0 + t;
     if (!GQA_IN_BOUNDS(row, p.bounds.total, p.status, kSite | 7)) return;
     const float inv = 1.0f / L;
@@ -535,8 +537,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 6) paged_decode_combine_ke
 bool stream::whole_pairs(int max_kv) { return max_kv <= 512; }
 
 cudaError_t stream::launch_combine(const Params &p, int max_q, cudaStream_t s) {
-    const int W = (long)p.nseq * p.Hkv < kSMs / 4 ? 4 : 2, rows = kCombineWarps / W;
-    return launch_pdl(paged_decode_combine_kernel, dim3(p.chunks, (max_q * p.G + rows - 1) / rows),
+    const int W = (long)p.nseq * p.Hkv * p.blocks < kSMs / 4 ? 4 : 2, rows = kCombineWarps / W;
+    const long most = (long)max_q * p.G < p.rec_rows ? (long)max_q * p.G : p.rec_rows;
+    return launch_pdl(paged_decode_combine_kernel,
+                      dim3(p.chunks, static_cast<unsigned>((most + rows - 1) / rows)),
                       dim3(32 * kCombineWarps), 0, s, p, W);
 }
 
@@ -559,7 +563,8 @@ size_t stream::partials_bytes(int chunks, int rows) {
 }
 
 // What of the parameters depends on neither kernel.
-stream::Params stream::params_of(const PackedAttn &a, int unit, int rec_rows, void *ws, int *status) {
+stream::Params stream::params_of(const PackedAttn &a, int unit, int rec_rows, int blocks, void *ws,
+                                 int *status) {
     const gqa_paged_kv &c = *a.cache;
     Params p{};
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
@@ -584,9 +589,10 @@ stream::Params stream::params_of(const PackedAttn &a, int unit, int rec_rows, vo
     p.max_pages = c.max_pages;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.rec_rows = rec_rows;
+    p.blocks = blocks;
     p.whole = whole_pairs(a.max_kv);
     if (!p.whole) {
-        p.chunks = n_chunks(a.nseq, a.max_kv, a.Hkv, a.max_q, a.window, unit);
+        p.chunks = n_chunks(a.nseq, a.max_kv, a.Hkv * blocks, a.max_q, a.window, unit);
         const size_t rec = (size_t)2 * p.chunks * rec_rows;
         p.ws_o = static_cast<float *>(ws);
         p.ws_ml = p.ws_o + rec * kD;
@@ -608,7 +614,7 @@ bool paged_decode_counts_fit(int nseq, int max_kv, int Hkv) {
 
 int launch_paged_decode(const PackedAttn &a, void *ws, int *status, cudaStream_t s) {
     const gqa_paged_kv &c = *a.cache;
-    const Params p = params_of(a, kUnit, kMaxRows, ws, status);
+    const Params p = params_of(a, kUnit, kMaxRows, 1, ws, status);
     // {64 dims, rows, 2 halves, (page, KV head)}: a page, or 64 rows of it, per box
     const uint64_t page = c.page_size;
     const uint64_t dims[4] = {64, page, 2, (uint64_t)c.num_pages * c.Hkv};

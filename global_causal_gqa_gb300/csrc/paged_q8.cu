@@ -37,48 +37,55 @@ namespace gqa {
 using namespace stream;
 namespace {
 
-constexpr int kProducerWarp = 8, kScoreWarp = 9, kValueWarp = 10, kQueryWarp = 11;
-constexpr int kScoreTiles = 2;       // of a group, in tensor memory
-// A pair's factors are read after its queries' tile is free again, and that of the pair after next
-// may be, too, as scores are formed ahead.
-constexpr int kFactorSlots = 8;
+constexpr int kRows = 8;             // of a group
+constexpr int kScoreTiles = 2;       // of a team, in tensor memory
+constexpr int kScoreCols = 2 * kRows, kValueCols = 3 * kRows;   // columns of a group
 constexpr float kGrow = 3.0f, kShift = 12.0f, kLargest = 32768.0f;   // log2 units; 2^(3 + 12)
 // Values below 2^-100 count as 2^-100 in mo, so that 2^(m - mo) stays within fp32.
 constexpr float kLeast = -100.0f;
 
 struct Q8Bars : StreamBars {
-    uint64_t q_full[2], q_free[2];
-    uint64_t s_full[kGroups][kScoreTiles], s_free[kGroups][kScoreTiles];
-    uint64_t p_full[kGroups], pv_done[kGroups], meet[kGroups], drained[2];
+    uint64_t q_full[4], q_free[4];
+    uint64_t s_full[4][kScoreTiles], s_free[4][kScoreTiles];   // of a team
+    uint64_t p_full[4], pv_done[4];
+    uint64_t meet[4];                // of a group
+    uint64_t drained[2];
     uint32_t tmem;
-    int vote[kGroups][2];            // the last stage of either parity that moved the references
-    int nan_any[kGroups][2];
+    int vote[4][2];                  // the last stage of either parity that moved a group's references
+    int nan_any[4][2];
 };
 
-// Shared memory.  R: rows of a group.
-template <int R, bool SPLIT>
+// TEAM groups share a pair, kRows rows each; the teams take the pairs in turn.
+template <int TEAM>
 struct Layout {
-    using S = Q8Stream<SPLIT>;
-    static constexpr int kTiles = SPLIT ? 2 : 1;                  // of a pair: query and score tiles
-    static constexpr int kScoreCols = 2 * R, kValueCols = R == 8 ? 32 : 3 * R;
-    static constexpr int kQuery = kScoreCols * kD, kWeights = kValueCols * kD;   // bytes of a tile
+    using S = Q8Stream<TEAM>;
+    static constexpr int kTeams = S::kTeams, kGroups = S::kGroups, kTeamRows = TEAM * kRows;
+    static constexpr int kScoreWarp = S::kProducer + 1, kValueWarp = S::kProducer + 2,
+                         kQueryWarp = S::kProducer + 3;
+    // columns of a team's products (a multiple of 16)
+    static constexpr int kScoreN = TEAM * kScoreCols, kValueN = TEAM == 1 ? 32 : TEAM * kValueCols;
+    static constexpr int kQuerySlots = kTeams > 2 ? kTeams : 2;
+    // A pair's factors are read after its queries' tile is free again; the team's next two pairs'
+    // scores may be formed by then, and the queries of the one or two after them be there.
+    static constexpr int kFactorSlots = TEAM == 4 ? 8 : 4 * kTeams;
+    // tensor memory: score tiles, then outputs
+    static constexpr int kOutputs = kTeams * kScoreTiles * kScoreN, kColumns = 256;
+    static_assert(kOutputs + kTeams * kValueN <= kColumns, "tensor memory");
+    // shared memory
+    static constexpr int kQuery = kScoreN * kD, kWeights = kValueN * kD;   // bytes of a tile
     static constexpr int kQ = S::kStages * kStageBytes;
-    static constexpr int kP = kQ + 2 * kTiles * kQuery;
-    static constexpr int kScales = kP + kGroups * kWeights;       // two bytes per key of a stage
-    static constexpr int kRowFactors = kScales + S::kStages * 2 * S::kUnit;   // float4 [group][warp][R]
-    static constexpr int kChanges = kRowFactors + kGroups * kConsumers * R * 16;   // float2
-    static constexpr int kMost = kChanges + kGroups * kConsumers * R * 8;          // float2
-    static constexpr int kSums = kMost + kGroups * kConsumers * R * 8;   // float [group][R][warp]
-    static constexpr int kQueryScales = kSums + kGroups * R * kConsumers * 4;   // float [pair][rows]
-    static constexpr int kNan = kQueryScales + kFactorSlots * kTiles * R * 4;   // a bit per row and dim
-    static constexpr int kBars = kNan + 2 * 2 * R * 16;
+    static constexpr int kP = kQ + kQuerySlots * kQuery;
+    static constexpr int kScales = kP + kTeams * kWeights;        // two bytes per key of a stage
+    static constexpr int kRowFactors = kScales + S::kStages * 2 * S::kUnit;   // float4 [warp][row]
+    static constexpr int kChanges = kRowFactors + kGroups * kConsumers * kRows * 16;   // float2
+    static constexpr int kMost = kChanges + kGroups * kConsumers * kRows * 8;          // float2
+    static constexpr int kSums = kMost + kGroups * kConsumers * kRows * 8;   // float [group][row][warp]
+    static constexpr int kFactors = kSums + kGroups * kRows * kConsumers * 4;   // float [pair][row]
+    static constexpr int kNan = kFactors + kFactorSlots * kTeamRows * 4;   // a bit per row and dim
+    static constexpr int kBars = kNan + kTeams * 2 * kTeamRows * 16;
     static constexpr int kBytes = kBars + static_cast<int>(sizeof(Q8Bars)) + 1024;
     static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kQuery % 1024 == 0 && kWeights % 1024 == 0 &&
                   kBars % 16 == 0 && kBytes <= 232448, "shared memory");
-    static constexpr int kOutputs = kGroups * kScoreTiles * kScoreCols;   // first column of O
-    static constexpr int kOutputStride = R == 8 ? 32 : 64;
-    static constexpr int kColumns = R == 8 ? 128 : 256;
-    static_assert(kOutputs + kGroups * kOutputStride <= kColumns, "tensor memory");
 };
 
 // Bytes of a stage from 8 keys (or values) to the next 8.
@@ -89,39 +96,24 @@ __device__ __noinline__ void expired(int *status, int role, int barrier, int n) 
     set_timeout(status, kDiagPagedDecode, role, barrier, n);
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[N]) {
-    if constexpr (N == 8) tmem_ld8(at, r);
-    else if constexpr (N == 16) tmem_ld16(at, r);
-    else tmem_ld32(at, r);
-}
-template <int N>
-__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[N]) {
-    if constexpr (N == 8) tmem_st8(at, r);
-    else tmem_st16(at, r);
-}
-
-// a[i] of all lanes brought together by `op`, a row in each lane: with R rows R - 1 exchanges of
-// halves and then whole ones.  Returns the row's number; a[0] is its value.
-template <int R, class Op>
-__device__ __forceinline__ int gather_rows(float (&a)[R], Op op) {
+// The rows' a[i] of all lanes brought together by `op`, in 9 exchanges: of halves, then whole.
+// Returns the row whose value the lane has in a[0].
+template <class Op>
+__device__ __forceinline__ int gather_rows(float (&a)[kRows], Op op) {
     const int lane = threadIdx.x & 31;
-    int row = 0;
 #pragma unroll
-    for (int n = R / 2, d = 16; d > 0; n >>= 1, d >>= 1) {
-        const bool up = lane & d;
+    for (int n = kRows / 2, d = 16; d > 0; n >>= 1, d >>= 1) {
         if (n > 0) {
 #pragma unroll
             for (int i = 0; i < n; ++i) {
-                const float keep = up ? a[i + n] : a[i], give = up ? a[i] : a[i + n];
+                const float keep = lane & d ? a[i + n] : a[i], give = lane & d ? a[i] : a[i + n];
                 a[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, d));
             }
-            row += up ? n : 0;
         } else {
             a[0] = op(a[0], __shfl_xor_sync(0xffffffffu, a[0], d));
         }
     }
-    return row;
+    return lane >> 2;
 }
 
 // byte - 127, the exponent that a scale byte stands for; NaN for 255.
@@ -130,12 +122,13 @@ __device__ __forceinline__ float exponent_of(uint32_t byte) {
 }
 
 // ---- the queries' warp: rows of bf16 to tiles of h and l, with the factor of their scores ------
-template <int R, bool SPLIT>
+template <int TEAM>
 __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uint8_t *smem) {
-    using L = Layout<R, SPLIT>;
+    using L = Layout<TEAM>;
+    constexpr int kSegSlots = L::S::kSegSlots;
     const int lane = threadIdx.x & 31;
     for (int k = 0;; ++k) {
-        const int slot = k & (kSegSlots - 1), b = k & 1;
+        const int slot = k % kSegSlots, b = k % L::kQuerySlots;
         if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
             expired(p.status, kRoleQueries, 0, k);
             return;
@@ -144,29 +137,28 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->seg_free[slot]);
         if (sg.stages < 0) return;
-        if (k >= 2 && !warp_wait(&bars->q_free[b], ((k >> 1) - 1) & 1)) {
+        if (k >= L::kQuerySlots && !warp_wait(&bars->q_free[b], (k / L::kQuerySlots - 1) & 1)) {
             expired(p.status, kRoleQueries, 1, k);
             return;
         }
-        const int rows = sg.T * p.G;   // <= L::kTiles * R (the host's rule on max_q)
-        float *factors = reinterpret_cast<float *>(smem + L::kQueryScales) +
-                         k % kFactorSlots * L::kTiles * R;
+        const int rows = sg.T * p.G - sg.r0;
+        float *factors = reinterpret_cast<float *>(smem + L::kFactors) +
+                         k % L::kFactorSlots * L::kTeamRows;
+        uint8_t *tile = smem + L::kQ + b * L::kQuery;
 #pragma unroll 1
-        for (int r0 = 0; r0 < L::kTiles * R; r0 += 8) {
-            uint2 w[8];                // four dims of eight rows
+        for (int i0 = 0; i0 < L::kTeamRows; i0 += 4) {
+            uint2 w[4];                // four dims of four rows
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = r0 + i, t = token_of(p, r);
+            for (int i = 0; i < 4; ++i) {
+                const int r = sg.r0 + i0 + i, t = token_of(p, r);
                 w[i] = make_uint2(0, 0);
-                if (r < rows && GQA_IN_BOUNDS(sg.row0 + t, p.bounds.total, p.status, kSite | 8))
+                if (i0 + i < rows && GQA_IN_BOUNDS(sg.row0 + t, p.bounds.total, p.status, kSite | 8))
                     w[i] = __ldg(reinterpret_cast<const uint2 *>(
                         p.q + (long)(sg.row0 + t) * p.q_stride + (sg.g * p.G + r - t * p.G) * kD +
                         4 * lane));
             }
-            uint8_t *tile = smem + L::kQ + (b * L::kTiles + r0 / R) * L::kQuery;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int n = r0 % R + i;
+            for (int i = 0; i < 4; ++i) {
                 const float x[4] = {bf16lo(w[i].x), bf16hi(w[i].x), bf16lo(w[i].y), bf16hi(w[i].y)};
                 uint32_t most = 0;     // (magnitudes compare as their bits do, NaN above all)
 #pragma unroll
@@ -184,11 +176,14 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
                     l |= to_e4m3x2((x[2 * e] * up - z.x) * 16.f, (x[2 * e + 1] * up - z.y) * 16.f)
                          << (16 * e);
                 }
-                // a row with an infinity or NaN: NaN
-                uint8_t *at = tile + n * kD + ((lane >> 2 ^ (n & 7)) << 4) + 4 * (lane & 3);
+                // row n of its group: h in the tile's row 16 g + n, l in row 16 g + 8 + n; a row
+                // with an infinity or NaN: NaN
+                const int n = (i0 + i) % kRows;
+                uint8_t *at = tile + ((i0 + i) / kRows * kScoreCols + n) * kD + ((lane >> 2 ^ n) << 4) +
+                              4 * (lane & 3);
                 *reinterpret_cast<uint32_t *>(at) = ex == 255 ? 0x7f7f7f7fu : h;
-                *reinterpret_cast<uint32_t *>(at + R * kD) = l;
-                if (lane == 0) factors[r0 + i] = __uint_as_float((ex - 7) << 23) * p.scale_log2;
+                *reinterpret_cast<uint32_t *>(at + kRows * kD) = l;
+                if (lane == 0) factors[i0 + i] = __uint_as_float((ex - 7) << 23) * p.scale_log2;
             }
         }
         fence_proxy_async_smem();
@@ -201,19 +196,19 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
 // (One thread for both took 1500 cycles per stage, as it tests barriers and issues 46 cycles per
 // product in turn: 32 caches of 8k-64k tokens 548 us.)
 //
-// Scores: as soon as a stage's keys, its pair's queries and a score tile of its group are there.
-template <int R, bool SPLIT>
+// Scores: as soon as a stage's keys, its pair's queries and a score tile of its team are there.
+template <int TEAM>
 __device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint8_t *smem,
                                              uint32_t tmem) {
-    using L = Layout<R, SPLIT>;
-    constexpr int kStages = L::S::kStages;
+    using L = Layout<TEAM>;
+    constexpr int kStages = L::S::kStages, kSegSlots = L::S::kSegSlots;
     const uint32_t ring = smem_u32(smem);
     const uint64_t kd0 = sdesc_sw128(ring + (p.joint && p.v_first ? 1024 : 0), 16, key_step(p));
     const uint64_t qd0 = sdesc_sw128(ring + L::kQ, 16, 1024);
-    constexpr uint32_t idesc = idesc_f8_f32(128, L::kScoreCols, 0, 0);
-    int n[2] = {0, 0};                 // scores of a group's stages
+    constexpr uint32_t idesc = idesc_f8_f32(128, L::kScoreN, 0, 0);
+    uint32_t counts = 0;               // scores of each team's stages, mod 256
     for (int k = 0, u = 0;; ++k) {
-        const int slot = k & (kSegSlots - 1), b = k & 1;
+        const int slot = k % kSegSlots, b = k % L::kQuerySlots, team = k % L::kTeams;
         if (!mbar_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
             expired(p.status, kRoleProducts, 0, k);
             break;
@@ -221,57 +216,49 @@ __device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint
         const int stages = bars->seg[slot].stages;
         mbar_arrive(&bars->seg_free[slot]);
         if (stages < 0) break;
-        bool ok = mbar_wait(&bars->q_full[b], k >> 1 & 1);
-        const int g0 = SPLIT ? 0 : b;
-        int m = b && !SPLIT ? n[1] : n[0];
-        for (int j = 0; ok && j < stages; ++j, ++u, ++m) {
-            const int st = u % kStages, tile = m % kScoreTiles;
-            if (m >= kScoreTiles)
-#pragma unroll
-                for (int i = 0; i < L::kTiles; ++i)
-                    ok = ok && mbar_wait(&bars->s_free[g0 + i][tile], (m / kScoreTiles - 1) & 1);
-            ok = ok && mbar_wait(&bars->full[0][st], (u / kStages) & 1);
+        bool ok = mbar_wait(&bars->q_full[b], (k / L::kQuerySlots) & 1);
+        uint32_t n = counts >> (8 * team) & 255;
+        for (int j = 0; ok && j < stages; ++j, ++u, n = n + 1 & 255) {
+            const int st = u % kStages, tile = n % kScoreTiles;
+            // (a tile's first use waits for the phase before its first, which reads as done)
+            ok = mbar_wait(&bars->s_free[team][tile], (n / kScoreTiles + 1) & 1) &&
+                 mbar_wait(&bars->full[0][st], (u / kStages) & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t kd = kd0 + st * (kStageBytes >> 4);
+            const uint64_t kd = kd0 + st * (kStageBytes >> 4), qd = qd0 + b * (L::kQuery >> 4);
 #pragma unroll
-            for (int i = 0; i < L::kTiles; ++i) {
-                const uint64_t qd = qd0 + (b * L::kTiles + i) * (L::kQuery >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_f8_ss(tmem + ((g0 + i) * kScoreTiles + tile) * L::kScoreCols, kd + 2 * kk,
-                               qd + 2 * kk, idesc, kk > 0);
-                // (this thread's own arrival hands on what it has seen: the stage's scale bytes and
-                // the queries' factors)
-                mbar_arrive(&bars->s_full[g0 + i][tile]);
-                umma_commit(&bars->s_full[g0 + i][tile]);
-            }
+            for (int kk = 0; kk < 4; ++kk)
+                umma_f8_ss(tmem + (team * kScoreTiles + tile) * L::kScoreN, kd + 2 * kk, qd + 2 * kk,
+                           idesc, kk > 0);
+            // (this thread's own arrival hands on what it has seen: the stage's scale bytes and the
+            // queries' factors)
+            mbar_arrive(&bars->s_full[team][tile]);
+            umma_commit(&bars->s_full[team][tile]);
         }
         if (!ok) {
             expired(p.status, kRoleProducts, 1, u);
             break;
         }
         umma_commit(&bars->q_free[b]);
-        if (b && !SPLIT) n[1] = m;
-        else n[0] = m;
+        counts = (counts & ~(255u << (8 * team))) | n << (8 * team);
     }
     umma_commit(&bars->drained[0]);    // nothing in flight when the tensor memory is freed
     if (!mbar_wait(&bars->drained[0], 0)) expired(p.status, kRoleProducts, 2, 0);
 }
 
 // Values: as soon as a stage's weights are there.
-template <int R, bool SPLIT>
+template <int TEAM>
 __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint8_t *smem,
                                              uint32_t tmem) {
-    using L = Layout<R, SPLIT>;
-    constexpr int kStages = L::S::kStages;
+    using L = Layout<TEAM>;
+    constexpr int kStages = L::S::kStages, kSegSlots = L::S::kSegSlots;
     const uint32_t ring = smem_u32(smem), step = key_step(p);
     const uint64_t vd0 = sdesc_sw128(ring + (!p.joint ? kTileBytes : p.v_first ? 0 : 1024), 16, step);
     const uint64_t pd0 = sdesc_sw128(ring + L::kP, 16, 1024);
-    constexpr uint32_t idesc = idesc_f8_f32(128, L::kValueCols, 1, 1);
-    int n[2] = {0, 0};                 // a group's products
+    constexpr uint32_t idesc = idesc_f8_f32(128, L::kValueN, 1, 1);
+    uint32_t parity = 0;               // of each team's weights, a bit each
     for (int k = 0, u = 0;; ++k) {
-        const int slot = k & (kSegSlots - 1);
+        const int slot = k % kSegSlots, team = k % L::kTeams;
         if (!mbar_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
             expired(p.status, kRoleProducts, 3, k);
             break;
@@ -279,59 +266,48 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
         const int stages = bars->seg[slot].stages;
         mbar_arrive(&bars->seg_free[slot]);
         if (stages < 0) break;
-        const int g0 = SPLIT ? 0 : k & 1;
-        int m = g0 ? n[1] : n[0];
+        const uint64_t pd = pd0 + team * (L::kWeights >> 4);
         bool ok = true;
-        for (int j = 0; j < stages; ++j, ++u, ++m) {
-            // (both groups': group 0 takes hidden values' NaN out for both)
-#pragma unroll
-            for (int i = 0; i < L::kTiles; ++i)
-                ok = ok && mbar_wait(&bars->p_full[g0 + i], m & 1);
+        for (int j = 0; j < stages; ++j, ++u, parity ^= 1u << team) {
+            ok = mbar_wait(&bars->p_full[team], parity >> team & 1);
             if (!ok) break;
             tc_fence_after();
             const int st = u % kStages;
             const uint64_t vd = vd0 + st * (kStageBytes >> 4);
 #pragma unroll
-            for (int i = 0; i < L::kTiles; ++i) {
-                const uint64_t pd = pd0 + (g0 + i) * (L::kWeights >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_f8_ss(tmem + L::kOutputs + (g0 + i) * L::kOutputStride,
-                               vd + kk * (step >> 2), pd + 2 * kk, idesc, kk > 0 || j > 0);
-                umma_commit(&bars->pv_done[g0 + i]);
-            }
+            for (int kk = 0; kk < 4; ++kk)
+                umma_f8_ss(tmem + L::kOutputs + team * L::kValueN, vd + kk * (step >> 2), pd + 2 * kk,
+                           idesc, kk > 0 || j > 0);
+            umma_commit(&bars->pv_done[team]);
             umma_commit(&bars->empty[st]);
         }
         if (!ok) {
             expired(p.status, kRoleProducts, 4, u);
             break;
         }
-        if (g0) n[1] = m;
-        else n[0] = m;
     }
     umma_commit(&bars->drained[1]);
     if (!mbar_wait(&bars->drained[1], 0)) expired(p.status, kRoleProducts, 5, 0);
 }
 
 // ---- a softmax group's warp ---------------------------------------------------------------------
-template <int R, bool SPLIT>
+template <int TEAM>
 __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *smem, uint32_t tmem) {
-    using L = Layout<R, SPLIT>;
-    constexpr int kStages = L::S::kStages, kUnit = L::S::kUnit;
+    using L = Layout<TEAM>;
+    constexpr int kStages = L::S::kStages, kUnit = L::S::kUnit, kSegSlots = L::S::kSegSlots;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = warp / kConsumers, cw = warp % kConsumers, tile = SPLIT ? group : 0;
-    // (of its group's barriers alone a warp sees every phase: a parity two phases back reads as
-    // done, so tiles that the groups shared would be read too early)
-    int scored = 0;                    // score tiles read
+    const int group = warp / kConsumers, cw = warp % kConsumers, team = group / TEAM, member = group % TEAM;
     const int t = 32 * cw + lane;      // the thread's key of a stage, and its dim of the outputs
-    const uint32_t lanes = static_cast<uint32_t>(32 * cw) << 16;
-    const uint32_t outputs = tmem + lanes + L::kOutputs + group * L::kOutputStride;
-    float4 *rowf = reinterpret_cast<float4 *>(smem + L::kRowFactors) + warp * R;
-    float2 *change = reinterpret_cast<float2 *>(smem + L::kChanges) + warp * R;
-    float2 *most = reinterpret_cast<float2 *>(smem + L::kMost) + group * kConsumers * R;
-    float *sums = reinterpret_cast<float *>(smem + L::kSums) + group * R * kConsumers;
-    uint8_t *weights = smem + L::kP + group * L::kWeights;
-    const int first_row = SPLIT ? R * group : 0;
+    tmem += static_cast<uint32_t>(32 * cw) << 16;
+    const uint32_t outputs = tmem + L::kOutputs + team * L::kValueN + member * kValueCols;
+    float4 *rowf = reinterpret_cast<float4 *>(smem + L::kRowFactors) + warp * kRows;
+    float2 *change = reinterpret_cast<float2 *>(smem + L::kChanges) + warp * kRows;
+    float2 *most = reinterpret_cast<float2 *>(smem + L::kMost) + group * kConsumers * kRows;
+    float *sums = reinterpret_cast<float *>(smem + L::kSums) + group * kRows * kConsumers;
+    uint8_t *weights = smem + L::kP + team * L::kWeights + member * kValueCols * kD;
+    // (of its team's and group's barriers alone a warp sees every phase: a parity two phases back
+    // reads as done, so tiles that the teams shared would be read too early)
+    int scored = 0;                    // score tiles read
     int handed = 0, meets = 0;         // weights handed over; meetings of the group's warps
     auto meet = [&]() {
         __syncwarp();
@@ -339,171 +315,175 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         return warp_wait(&bars->meet[group], meets++ & 1);
     };
     auto products_done = [&]() {       // of all weights handed over
-        return handed == 0 || warp_wait(&bars->pv_done[group], (handed - 1) & 1);
+        return handed == 0 || warp_wait(&bars->pv_done[team], (handed - 1) & 1);
     };
     auto fail = [&](int barrier, int n) { expired(p.status, kRoleConsumer, barrier, n); };
 #pragma unroll 1
-    for (int k = SPLIT ? 0 : group, turn = 0;; k += SPLIT ? 1 : kGroups, turn ^= 1) {
-        const int slot = k & (kSegSlots - 1);
+    for (int k = team, turn = 0;; k += L::kTeams, turn ^= 1) {
+        const int slot = k % kSegSlots;
         if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) return fail(0, k);
         const Segment sg = bars->seg[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->seg_free[slot]);
         if (sg.stages < 0) return;
-        const int rows = max(0, min(R, sg.T * p.G - first_row));
+        const int first_row = sg.r0 + kRows * member;
+        const int rows = max(0, min(kRows, sg.T * p.G - first_row));   // none: no weights, O unread
         const int q_first = sg.S - sg.T;          // keys beyond are hidden from some
         const int lo = p.window > 0 ? max(0, q_first - p.window + 1) : 0;
         const int lo_all = p.window > 0 ? max(0, sg.S - p.window) : 0;
-        // NaN among the values' numbers: a bit per row and dim of this pair, and of the last one
-        uint32_t *nan = reinterpret_cast<uint32_t *>(smem + L::kNan);
-        auto nan_row = [&](int which, int r) {    // r: of the pair
-            return nan + ((SPLIT ? which : 2 * group + which) * L::kTiles * R + r) * 4;
+        // NaN among the values' numbers: a bit per row and dim of this pair (turn), and of the last
+        auto nan_row = [&](int which, int r) {    // r: of the team's rows
+            return reinterpret_cast<uint32_t *>(smem + L::kNan) +
+                   ((2 * team + which) * L::kTeamRows + r) * 4;
         };
         float m = -CUDART_INF_F, mo = -CUDART_INF_F;   // of row `lane`
-        float l[R];
+        float l[kRows];
 #pragma unroll
-        for (int r = 0; r < R; ++r) l[r] = 0.f;
+        for (int r = 0; r < kRows; ++r) l[r] = 0.f;
 #pragma unroll 1
         for (int j = 0, u = sg.u0; j < sg.stages; ++j, ++u) {
             const int st = u % kStages, si = scored % kScoreTiles;
-            if (!warp_wait(&bars->s_full[group][si], (scored / kScoreTiles) & 1)) return fail(1, u);
+            if (!warp_wait(&bars->s_full[team][si], (scored / kScoreTiles) & 1)) return fail(1, u);
             ++scored;
-            tc_fence_after();
-            float y[R];
-            uint32_t bytes;
-            {
-                uint32_t s[2 * R];
-                tmem_ld<2 * R>(tmem + lanes + (group * kScoreTiles + si) * L::kScoreCols, s);
-                bytes = reinterpret_cast<const uint16_t *>(smem + L::kScales)[st * kUnit + t];
-                const float kf = scale_of(bytes & 255u), kl = kf * 0.0625f;
+            const int kb = (sg.unit0 + j) * kUnit, key = kb + t;
+            const bool edge = kb + kUnit - 1 > q_first || kb < lo_all;   // of the mask
+            if (rows > 0) {
+                tc_fence_after();
+                float y[kRows];
+                uint32_t s[kScoreCols];
+                tmem_ld16(tmem + (team * kScoreTiles + si) * L::kScoreN + member * kScoreCols, s);
+                const uint32_t bytes =
+                    reinterpret_cast<const uint16_t *>(smem + L::kScales)[st * kUnit + t];
+                const float kf = scale_of(bytes & 255u), kl = kf * 0.0625f, vf = scale_of(bytes >> 8);
+                uint32_t hidden = 0;       // a bit per row
+                if (edge) {
+                    // a token's rows at a time
+                    int tok = token_of(p, first_row), r = 0;
+#pragma unroll 1
+                    do {
+                        const int at = q_first + min(tok, sg.T - 1), to = ++tok * p.G - first_row;
+                        if (key > at || (p.window > 0 && at - key >= p.window))
+                            hidden |= (1u << min(to, kRows)) - (1u << r);
+                        r = to;
+                    } while (r < kRows);
+                }
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->s_free[group][si]);
+                if (lane == 0) mbar_arrive(&bars->s_free[team][si]);
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    y[r] = fmaf(__uint_as_float(s[R + r]), kl, __uint_as_float(s[r]) * kf);
-            }
-            const float vf = scale_of(bytes >> 8);
-            const int kb = (sg.unit0 + j) * kUnit, key = kb + t;
-            const bool edge = kb + kUnit - 1 > q_first || kb < lo_all;   // of the mask
-            uint32_t hidden = 0;       // a bit per row
-            if (edge) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int at = q_first + min(token_of(p, first_row + r), sg.T - 1);
-                    if (key > at || (p.window > 0 && at - key >= p.window)) {
-                        hidden |= 1u << r;
-                        y[r] = -CUDART_INF_F;
-                    }
+                for (int r = 0; r < kRows; ++r) {
+                    y[r] = fmaf(__uint_as_float(s[kRows + r]), kl, __uint_as_float(s[r]) * kf);
+                    if (hidden >> r & 1) y[r] = -CUDART_INF_F;
                 }
-            }
-            // ---- weights w and products P, against new references where the old ones are passed
-            float w[R], pw[R];
-            bool update = j == 0;
+                // ---- weights w and products P, against new references where the old are passed
+                float w[kRows], pw[kRows];
+                bool update = j == 0;
 #pragma unroll 1
-            while (true) {
-                if (update) {
-                    const float ev = fmaxf(exponent_of(bytes >> 8), kLeast);
-                    const float *factors =
-                        reinterpret_cast<const float *>(smem + L::kQueryScales) +
-                        (k % kFactorSlots * L::kTiles + tile) * R;
-                    float a[R], b[R];
+                while (true) {
+                    if (update) {
+                        const float ev = fmaxf(exponent_of(bytes >> 8), kLeast);
+                        const float *factors = reinterpret_cast<const float *>(smem + L::kFactors) +
+                                               k % L::kFactorSlots * L::kTeamRows + member * kRows;
+                        float a[kRows], b[kRows];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        a[r] = y[r] * factors[r];
-                        b[r] = a[r] + ev;
-                    }
-                    auto larger = [](float c, float d) { return fmaxf(c, d); };
-                    const int row = gather_rows(a, larger);
-                    gather_rows(b, larger);
-                    if ((lane & (32 / R - 1)) == 0) most[cw * R + row] = make_float2(a[0], b[0]);
-                    if (!meet()) return fail(3, u);
-                    if (lane < R) {
-                        float mn = m, mno = mo;
+                        for (int r = 0; r < kRows; ++r) {
+                            a[r] = y[r] * factors[r];
+                            b[r] = a[r] + ev;
+                        }
+                        auto larger = [](float c, float d) { return fmaxf(c, d); };
+                        const int row = gather_rows(a, larger);
+                        gather_rows(b, larger);
+                        if ((lane & 3) == 0) most[cw * kRows + row] = make_float2(a[0], b[0]);
+                        if (!meet()) return fail(3, u);
+                        if (lane < kRows) {
+                            float mn = m, mno = mo;
 #pragma unroll
-                        for (int c = 0; c < kConsumers; ++c) {
-                            const float2 x = most[c * R + lane];
-                            mn = fmaxf(mn, x.x);
-                            mno = fmaxf(mno, x.y);
+                            for (int c = 0; c < kConsumers; ++c) {
+                                const float2 x = most[c * kRows + lane];
+                                mn = fmaxf(mn, x.x);
+                                mno = fmaxf(mno, x.y);
+                            }
+                            change[lane] =
+                                make_float2(m == -CUDART_INF_F ? 0.f : ex2_approx(m - mn),
+                                            mo == -CUDART_INF_F ? 1.f : ex2_approx(mo - mno));
+                            m = mn;
+                            mo = mno;
+                            rowf[lane] = make_float4(
+                                factors[lane], -fmaxf(mn, -3.0e38f),
+                                mn == -CUDART_INF_F ? 0.f : ex2_approx(mn - mno + kShift), 0.f);
+                            if (j == 0 && cw == 0 && bars->nan_any[group][turn ^ 1]) {
+                                // the last pair's bits have been read
+                                *reinterpret_cast<uint4 *>(nan_row(turn ^ 1, kRows * member + lane)) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
                         }
-                        change[lane] =
-                            make_float2(m == -CUDART_INF_F ? 0.f : ex2_approx(m - mn),
-                                        mo == -CUDART_INF_F ? 1.f : ex2_approx(mo - mno));
-                        m = mn;
-                        mo = mno;
-                        rowf[lane] =
-                            make_float4(factors[lane], -fmaxf(mn, -3.0e38f),
-                                        mn == -CUDART_INF_F ? 0.f : ex2_approx(mn - mno + kShift), 0.f);
-                        if (j == 0 && cw == 0) {  // the last pair's bits have been read
-                            uint32_t *z = nan_row(turn ^ 1, first_row + lane);
-                            z[0] = z[1] = z[2] = z[3] = 0;
-                            if (lane == 0) bars->nan_any[group][turn ^ 1] = 0;
-                        }
-                    }
-                    __syncwarp();
-                    if (j > 0) {
-                        if (!products_done()) return fail(4, u);
-                        tc_fence_after();
+                        __syncwarp();
+                        if (j == 0 && cw == 0 && lane == 0) bars->nan_any[group][turn ^ 1] = 0;
+                        if (j > 0) {
+                            if (!products_done()) return fail(4, u);
+                            tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 3; ++c) {
-                            uint32_t o[R];
-                            tmem_ld<R>(outputs + c * R, o);
-                            tmem_wait_ld();
+                            for (int c = 0; c < 3; ++c) {
+                                uint32_t o[kRows];
+                                tmem_ld8(outputs + c * kRows, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int r = 0; r < R; ++r)
-                                o[r] = __float_as_uint(__uint_as_float(o[r]) * change[r].y);
-                            tmem_st<R>(outputs + c * R, o);
+                                for (int r = 0; r < kRows; ++r)
+                                    o[r] = __float_as_uint(__uint_as_float(o[r]) * change[r].y);
+                                tmem_st8(outputs + c * kRows, o);
+                            }
+                            tmem_wait_st();
+                            tc_fence_before();
+#pragma unroll
+                            for (int r = 0; r < kRows; ++r) l[r] *= change[r].x;
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-#pragma unroll
-                        for (int r = 0; r < R; ++r) l[r] *= change[r].x;
                     }
+                    bool over = false;
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        const float4 f = rowf[r];
+                        const float x = fmaf(y[r], f.x, f.y);
+                        w[r] = ex2_approx(x);
+                        pw[r] = w[r] * f.z * vf;
+                        over |= x > kGrow || pw[r] > kLargest;
+                    }
+                    if (update) break;
+                    if (__any_sync(0xffffffffu, over) && lane == 0) bars->vote[group][u & 1] = u + 1;
+                    if (!meet()) return fail(5, u);
+                    if (*const_cast<volatile int *>(&bars->vote[group][u & 1]) != u + 1) break;
+                    update = true;
                 }
-                bool over = false;
+                // ---- P, a byte per column, row and key
+                if (!products_done()) return fail(4, u);    // the last ones have been read
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float4 f = rowf[r];
-                    const float x = fmaf(y[r], f.x, f.y);
-                    w[r] = ex2_approx(x);
-                    pw[r] = w[r] * f.z * vf;
-                    over |= x > kGrow || pw[r] > kLargest;
+                for (int r = 0; r < kRows; r += 2) {
+                    l[r] += w[r];
+                    l[r + 1] += w[r + 1];
+                    // (a hidden key's value may have a NaN for a power)
+                    const __half2 x = __floats2half2_rn(hidden >> r & 1 ? 0.f : pw[r],
+                                                        hidden >> r & 2 ? 0.f : pw[r + 1]);
+                    const uint32_t c = *reinterpret_cast<const uint32_t *>(&x) & 0xff00ff00u;
+                    const __half2 x1 = __hsub2(x, *reinterpret_cast<const __half2 *>(&c));
+                    const uint32_t d = *reinterpret_cast<const uint32_t *>(&x1) & 0xff00ff00u;
+                    const __half2 x2 = __hsub2(x1, *reinterpret_cast<const __half2 *>(&d));
+                    const uint32_t f = to_e5m2x2(x2);
+                    uint8_t *at = weights + r * kD + (t ^ (r << 4));
+                    uint8_t *at1 = weights + (r + 1) * kD + (t ^ (r + 1 << 4));
+                    at[0] = static_cast<uint8_t>(c >> 8);
+                    at1[0] = static_cast<uint8_t>(c >> 24);
+                    at[kRows * kD] = static_cast<uint8_t>(d >> 8);
+                    at1[kRows * kD] = static_cast<uint8_t>(d >> 24);
+                    at[2 * kRows * kD] = static_cast<uint8_t>(f);
+                    at1[2 * kRows * kD] = static_cast<uint8_t>(f >> 8);
                 }
-                if (update) break;
-                if (__any_sync(0xffffffffu, over) && lane == 0) bars->vote[group][u & 1] = u + 1;
-                if (!meet()) return fail(5, u);
-                if (*const_cast<volatile int *>(&bars->vote[group][u & 1]) != u + 1) break;
-                update = true;
-            }
-            if (edge) {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (hidden >> r & 1) pw[r] = 0.f;   // (its value's byte may be NaN)
-            }
-            // ---- P, a byte per column, row and key
-            if (!products_done()) return fail(4, u);    // the last ones have been read
-#pragma unroll
-            for (int r = 0; r < R; r += 2) {
-                l[r] += w[r];
-                l[r + 1] += w[r + 1];
-                const __half2 x = __floats2half2_rn(pw[r], pw[r + 1]);
-                const uint32_t c = *reinterpret_cast<const uint32_t *>(&x) & 0xff00ff00u;
-                const __half2 x1 = __hsub2(x, *reinterpret_cast<const __half2 *>(&c));
-                const uint32_t d = *reinterpret_cast<const uint32_t *>(&x1) & 0xff00ff00u;
-                const __half2 x2 = __hsub2(x1, *reinterpret_cast<const __half2 *>(&d));
-                const uint32_t f = to_e5m2x2(x2);
-                uint8_t *at = weights + r * kD + (t ^ ((r & 7) << 4));
-                uint8_t *at1 = weights + (r + 1) * kD + (t ^ ((r + 1 & 7) << 4));
-                at[0] = static_cast<uint8_t>(c >> 8);
-                at1[0] = static_cast<uint8_t>(c >> 24);
-                at[R * kD] = static_cast<uint8_t>(d >> 8);
-                at1[R * kD] = static_cast<uint8_t>(d >> 24);
-                at[2 * R * kD] = static_cast<uint8_t>(f);
-                at1[2 * R * kD] = static_cast<uint8_t>(f >> 8);
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->s_free[team][si]);
+                if (!products_done()) return fail(4, u);   // (sees every phase)
             }
             // ---- values that the mask hides: 0 * NaN is NaN
-            if (edge && (!SPLIT || group == 0)) {
+            if (edge && member == 0) {
                 uint8_t *vr = smem + st * kStageBytes +
                               (!p.joint ? kTileBytes + t * kD
                                         : (t >> 3) * 2048 + (p.v_first ? 0 : 1024) + (t & 7) * kD);
@@ -516,18 +496,19 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
 #pragma unroll 1
                     for (int i = 0; i < kD / 4; ++i) {
                         uint32_t *at = reinterpret_cast<uint32_t *>(vr) + i;
-                        const uint32_t x = *at;
-                        uint32_t bad = __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        const uint32_t x = *at, bad = __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
                         if (!bad) continue;
                         *at = x & ~bad;
                         const int dim = 16 * (i >> 2 ^ (t & 7)) + 4 * (i & 3);
+#pragma unroll 1
                         for (int e = 0; e < 4; ++e) {
                             if (!(bad >> (8 * e) & 1)) continue;
-                            for (int r = 0; r < min(sg.T * p.G, L::kTiles * R); ++r) {
-                                const int pos = q_first + token_of(p, r);
+#pragma unroll 1
+                            for (int r = 0; r < min(sg.T * p.G - sg.r0, L::kTeamRows); ++r) {
+                                const int pos = q_first + token_of(p, sg.r0 + r);
                                 if (key > pos || (p.window > 0 && pos - key >= p.window)) continue;
                                 atomicOr(nan_row(turn, r) + (dim + e) / 32, 1u << ((dim + e) & 31));
-                                bars->nan_any[SPLIT ? r / R : group][turn] = 1;
+                                bars->nan_any[team * TEAM + r / kRows][turn] = 1;
                             }
                         }
                     }
@@ -535,80 +516,74 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[group]);
+            if (lane == 0) mbar_arrive(&bars->p_full[team]);
             ++handed;
         }
+        if (rows == 0) continue;
         // ---- the pair's (or span's) result: this thread's dim of all rows
-        {
-            const int row = gather_rows(l, [](float a, float b) { return a + b; });
-            if ((lane & (32 / R - 1)) == 0) sums[row * kConsumers + cw] = l[0];
-            // O relative to m: times 2^(mo - 12 - m), in two steps as that may be 2^-138
-            if (lane < R)
-                change[lane].x =
-                    mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift - m));
-        }
+        const int row = gather_rows(l, [](float a, float b) { return a + b; });
+        if ((lane & 3) == 0) sums[row * kConsumers + cw] = l[0];
         if (!meet()) return fail(6, k);
-        if (!products_done()) return fail(4, k);
-        tc_fence_after();
-        float o[R];
-        {
-            uint32_t a[R], b[R], c[R];
-            tmem_ld<R>(outputs, a);
-            tmem_ld<R>(outputs + R, b);
-            tmem_ld<R>(outputs + 2 * R, c);
-            tmem_wait_ld();
-            tc_fence_before();
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                o[r] = __uint_as_float(a[r]) + (__uint_as_float(b[r]) + __uint_as_float(c[r]));
-        }
-        const bool nans = *const_cast<volatile int *>(&bars->nan_any[group][turn]) != 0;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (r >= rows) continue;
-            float x = o[r] * change[r].x * change[r].x;
-            if (nans && nan_row(turn, first_row + r)[t / 32] >> (t & 31) & 1) x = CUDART_NAN_F;
-            const int n = first_row + r;
-            if (sg.slot >= 0) {
-                const size_t rec = (size_t)sg.slot * p.rec_rows + n;
-                if (GQA_IN_BOUNDS(rec, (long)2 * p.chunks * p.rec_rows, p.status, kSite | 9))
-                    p.ws_o[rec * kD + t] = x;
-            } else {
-                const float4 s = *reinterpret_cast<const float4 *>(sums + r * kConsumers);
-                const int tok = token_of(p, n), head = sg.g * p.G + n - tok * p.G;
-                const long row = sg.row0 + tok;
-                if (GQA_IN_BOUNDS(row, p.bounds.total, p.status, kSite | 10))
-                    p.o[row * p.o_stride + head * kD + t] =
-                        __float2bfloat16_rn(x * (1.0f / ((s.x + s.y) + (s.z + s.w))));
-            }
-        }
-        if (cw == 0 && lane < rows) {
+        if (lane < kRows) {
+            // A row's factors and where it goes.  O relative to m: times 2^(mo - 12 - m), in two
+            // steps as that may be 2^-138.
             const float4 s = *reinterpret_cast<const float4 *>(sums + lane * kConsumers);
             const float sum = (s.x + s.y) + (s.z + s.w);
+            const float f = mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift - m));
             const int n = first_row + lane;
-            if (sg.slot >= 0) {
-                const size_t rec = (size_t)sg.slot * p.rec_rows + n;
-                if (GQA_IN_BOUNDS(rec, (long)2 * p.chunks * p.rec_rows, p.status, kSite | 11))
-                    reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(m, sum);
-            } else if (p.lse) {
+            uint64_t to = 0;
+            if (lane < rows && sg.slot >= 0) {
+                const size_t rec = (size_t)sg.slot * p.rec_rows + kRows * member + lane;
+                if (GQA_IN_BOUNDS(rec, (long)2 * p.chunks * p.rec_rows, p.status, kSite | 9)) {
+                    to = reinterpret_cast<uint64_t>(p.ws_o + rec * kD);
+                    if (cw == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(m, sum);
+                }
+            } else if (lane < rows) {
                 const int tok = token_of(p, n), head = sg.g * p.G + n - tok * p.G;
-                const long row = sg.row0 + tok;
-                if (GQA_IN_BOUNDS(row, p.bounds.total, p.status, kSite | 12))
-                    p.lse[(long)head * p.bounds.total + row] =
-                        (m + __log2f(sum)) * 0.69314718055994531f;
+                const long at = sg.row0 + tok;
+                if (GQA_IN_BOUNDS(at, p.bounds.total, p.status, kSite | 10)) {
+                    to = reinterpret_cast<uint64_t>(p.o + at * p.o_stride + head * kD);
+                    if (p.lse && cw == 0)
+                        p.lse[(long)head * p.bounds.total + at] =
+                            (m + __log2f(sum)) * 0.69314718055994531f;
+                }
             }
+            rowf[lane] = make_float4(f, sg.slot >= 0 ? 1.f : 1.0f / sum,
+                                     __uint_as_float(static_cast<uint32_t>(to)),
+                                     __uint_as_float(static_cast<uint32_t>(to >> 32)));
         }
+        if (!products_done()) return fail(4, k);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t a[kRows], b[kRows], c[kRows];
+        tmem_ld8(outputs, a);
+        tmem_ld8(outputs + kRows, b);
+        tmem_ld8(outputs + 2 * kRows, c);
+        tmem_wait_ld();
+        tc_fence_before();
+        const bool nans = *const_cast<volatile int *>(&bars->nan_any[group][turn]) != 0;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const float4 f = rowf[r];
+            const uint64_t to = static_cast<uint64_t>(__float_as_uint(f.w)) << 32 | __float_as_uint(f.z);
+            if (to == 0) continue;
+            float x = (__uint_as_float(a[r]) + (__uint_as_float(b[r]) + __uint_as_float(c[r]))) * f.x *
+                      f.x * f.y;
+            if (nans && nan_row(turn, kRows * member + r)[t / 32] >> (t & 31) & 1) x = CUDART_NAN_F;
+            if (sg.slot >= 0) reinterpret_cast<float *>(to)[t] = x;
+            else reinterpret_cast<__nv_bfloat16 *>(to)[t] = __float2bfloat16_rn(x);
+        }
+        __syncwarp();                  // before the next pair's factors
     }
 }
 
-// R: rows of a group.  SPLIT: both groups on each pair, R rows each.
-template <int R, bool SPLIT>
-__global__ void __launch_bounds__(Q8Stream<SPLIT>::kThreads, 1)
+template <int TEAM>
+__global__ void __launch_bounds__(Q8Stream<TEAM>::kThreads, 1)
     paged_q8_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const Params p) {
     griddep_wait();
     griddep_launch_dependents();
-    using L = Layout<R, SPLIT>;
+    using L = Layout<TEAM>;
     using S = typename L::S;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -620,33 +595,33 @@ __global__ void __launch_bounds__(Q8Stream<SPLIT>::kThreads, 1)
             mbar_init(&bars->full[0][i], S::kUnit / min(p.page_size, S::kUnit) + kScaleCopies);
             mbar_init(&bars->empty[i], 1);
         }
-        for (int i = 0; i < kSegSlots; ++i) {
+        for (int i = 0; i < S::kSegSlots; ++i) {
             mbar_init(&bars->seg_full[i], 1);
-            mbar_init(&bars->seg_free[i], S::kReaders * kConsumers + 3);
+            mbar_init(&bars->seg_free[i], TEAM * kConsumers + 3);
         }
-        for (int g = 0; g < kGroups; ++g) {
+        for (int g = 0; g < 4; ++g) {
             mbar_init(&bars->q_full[g], 1);
             mbar_init(&bars->q_free[g], 1);
             for (int i = 0; i < kScoreTiles; ++i) {
                 mbar_init(&bars->s_full[g][i], 2);
-                mbar_init(&bars->s_free[g][i], kConsumers);
+                mbar_init(&bars->s_free[g][i], TEAM * kConsumers);
             }
-            mbar_init(&bars->p_full[g], kConsumers);
+            mbar_init(&bars->p_full[g], TEAM * kConsumers);
             mbar_init(&bars->pv_done[g], 1);
             mbar_init(&bars->meet[g], kConsumers);
-            mbar_init(&bars->drained[g], 1);
             for (int i = 0; i < 2; ++i) bars->vote[g][i] = bars->nan_any[g][i] = 0;
         }
+        for (int i = 0; i < 2; ++i) mbar_init(&bars->drained[i], 1);
         mbar_init(&bars->clc_full, 1);
         fence_mbar_init();
     }
     // columns of P that no weight is written to, and the NaN bits
-    for (int i = threadIdx.x; i < kGroups * L::kWeights / 16; i += S::kThreads)
+    for (int i = threadIdx.x; i < L::kTeams * L::kWeights / 16; i += S::kThreads)
         reinterpret_cast<uint4 *>(smem + L::kP)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = threadIdx.x; i < 2 * 2 * R; i += S::kThreads)
+    for (int i = threadIdx.x; i < L::kTeams * 2 * L::kTeamRows; i += S::kThreads)
         reinterpret_cast<uint4 *>(smem + L::kNan)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
-    if (warp == kScoreWarp) {
+    if (warp == L::kScoreWarp) {
         tmem_alloc(&bars->tmem, L::kColumns);
         tmem_relinquish();
     }
@@ -655,29 +630,39 @@ __global__ void __launch_bounds__(Q8Stream<SPLIT>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
-    if (warp < kGroups * kConsumers) softmax<R, SPLIT>(p, bars, smem, tmem);
-    else if (warp == kProducerWarp) produce<S>(tmK, tmV, p, bars, smem, smem + L::kScales);
-    else if (warp == kQueryWarp) bring_queries<R, SPLIT>(p, bars, smem);
-    else if (warp == kScoreWarp && lane == 0) issue_scores<R, SPLIT>(p, bars, smem, tmem);
-    else if (warp == kValueWarp && lane == 0) issue_values<R, SPLIT>(p, bars, smem, tmem);
+    if (warp < S::kProducer) softmax<TEAM>(p, bars, smem, tmem);
+    else if (warp == S::kProducer) produce<S>(tmK, tmV, p, bars, smem, smem + L::kScales);
+    else if (warp == L::kQueryWarp) bring_queries<TEAM>(p, bars, smem);
+    else if (warp == L::kScoreWarp && lane == 0) issue_scores<TEAM>(p, bars, smem, tmem);
+    else if (warp == L::kValueWarp && lane == 0) issue_values<TEAM>(p, bars, smem, tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == kScoreWarp) {
+    if (warp == L::kScoreWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kColumns);
     }
 }
 
-constexpr int kStreamRows = 32;      // up to here the streaming kernel
-int rows_of(int max_q, int Hq, int Hkv) {
+// How the streaming kernel takes a call: groups of a team (0: the tile kernel does) and blocks of
+// rows per sequence.
+struct Plan {
+    int team, blocks;
+};
+constexpr int kMostBlocks = 2;
+Plan plan_of(int max_q, int Hq, int Hkv) {
     const long n = static_cast<long>(max_q) * (Hq / Hkv);
-    return n > kStreamRows ? 0 : n > 16 ? 32 : 16;   // of a partial; 0: the tile kernel
+    if (n <= kRows) return {1, 1};
+    if (n <= 2 * kRows) return {2, 1};
+    const long blocks = (n + kBlockRows - 1) / kBlockRows;
+    return blocks <= kMostBlocks ? Plan{4, static_cast<int>(blocks)} : Plan{0, 0};
 }
 
-int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, int rows, void *ws, int *status,
+template <int TEAM>
+int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, int blocks, void *ws, int *status,
                   cudaStream_t s) {
-    Params p = params_of(a, Q8Stream<false>::kUnit, rows, ws, status);
+    using L = Layout<TEAM>;
+    Params p = params_of(a, L::S::kUnit, L::kTeamRows, blocks, ws, status);
     p.scales = static_cast<const uint8_t *>(c.scales);
     // {128 numbers, 8 keys, the two pools, groups of 8 keys, (page, KV head)}: a map takes a stride
     // from pool to pool below 2^40, and then a page's keys and values come as one copy, 8 of either
@@ -695,18 +680,12 @@ int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, int rows, void 
     if (!make_byte_map(&mk, p.v_first ? c.v : c.k, 5, dims, strides, box) ||
         !make_byte_map(&mv, c.v, 5, dims, strides, box))
         return GQA_ERR_CUDA;
-    const long pairs = (long)a.nseq * a.Hkv;
+    const long pairs = (long)a.nseq * a.Hkv * blocks;
     const long grid = !p.whole ? p.chunks : pairs < kSMs ? pairs : kSMs;
-    const bool eight = static_cast<long>(a.max_q) * p.G <= 8;
-    auto kern = rows == 32 ? paged_q8_kernel<16, true>
-                : eight    ? paged_q8_kernel<8, false>
-                           : paged_q8_kernel<16, false>;
-    const int bytes = rows == 32 ? Layout<16, true>::kBytes
-                      : eight    ? Layout<8, false>::kBytes
-                                 : Layout<16, false>::kBytes;
-    if (ensure_smem_attr(reinterpret_cast<const void *>(kern), bytes) != cudaSuccess ||
-        launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(Q8Stream<false>::kThreads), bytes, s,
-                   mk, mv, p) != cudaSuccess)
+    auto kern = paged_q8_kernel<TEAM>;
+    if (ensure_smem_attr(reinterpret_cast<const void *>(kern), L::kBytes) != cudaSuccess ||
+        launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(L::S::kThreads), L::kBytes, s, mk, mv,
+                   p) != cudaSuccess)
         return GQA_ERR_CUDA;
     if (!p.whole && launch_combine(p, a.max_q, s) != cudaSuccess) return GQA_ERR_CUDA;
     return GQA_OK;
@@ -715,16 +694,21 @@ int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, int rows, void 
 }  // namespace
 
 bool paged_q8_counts_fit(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv) {
-    return rows_of(max_q, Hq, Hkv) ? paged_decode_counts_fit(nseq, max_kv, Hkv)
-                                   : paged_expand_counts_fit(nseq, max_kv, Hkv) &&
-                                         packed_prefill_counts_fit(nseq, total, max_kv, Hq, Hkv);
+    const Plan plan = plan_of(max_q, Hq, Hkv);
+    if (plan.team)
+        return (long)Hkv * plan.blocks <= 0x7fffffffL &&
+               paged_decode_counts_fit(nseq, max_kv, Hkv * plan.blocks);
+    return paged_expand_counts_fit(nseq, max_kv, Hkv) &&
+           packed_prefill_counts_fit(nseq, total, max_kv, Hq, Hkv);
 }
 
 size_t paged_q8_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv) {
-    if (const int rows = rows_of(max_q, Hq, Hkv))
-        return whole_pairs(max_kv) ? 0
-                                   : partials_bytes(n_chunks(nseq, max_kv, Hkv, 1, 0,
-                                                             Q8Stream<false>::kUnit), rows);
+    const Plan plan = plan_of(max_q, Hq, Hkv);
+    if (plan.team)
+        return whole_pairs(max_kv)
+                   ? 0
+                   : partials_bytes(n_chunks(nseq, max_kv, Hkv * plan.blocks, 1, 0, Q8Stream<1>::kUnit),
+                                    plan.team * kRows);
     return paged_expand_q8_bytes(nseq, max_kv, Hkv) +
            packed_prefill_workspace_bytes(nseq, total, max_kv, Hq, Hkv);
 }
@@ -735,8 +719,12 @@ int launch_paged_q8(const PackedAttn &a, const gqa_paged_kv_q8 &c, void *ws, int
                           c.max_pages, 0};
     PackedAttn b = a;
     b.cache = &pages;
-    if (const int rows = rows_of(a.max_q, a.Hq, a.Hkv))
-        return launch_stream(b, c, rows, ws, status, s);
+    const Plan plan = plan_of(a.max_q, a.Hq, a.Hkv);
+    switch (plan.team) {
+        case 1: return launch_stream<1>(b, c, plan.blocks, ws, status, s);
+        case 2: return launch_stream<2>(b, c, plan.blocks, ws, status, s);
+        case 4: return launch_stream<4>(b, c, plan.blocks, ws, status, s);
+    }
     if (launch_paged_expand_q8(c, a, ws, &pages, status, s) != cudaSuccess) return GQA_ERR_CUDA;
     b.k = pages.k;
     b.v = pages.v;

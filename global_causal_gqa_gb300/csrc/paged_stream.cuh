@@ -18,49 +18,49 @@ constexpr int kD = 128;
 constexpr int kTileBytes = 16384;               // K or V of a stage
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kMostStages = 6;
-constexpr int kConsumers = 4;                   // warps of a group
-constexpr int kGroups = 2;                      // groups of consumers
-constexpr int kSegSlots = 4;
+constexpr int kConsumers = 4;                   // warps of a group of consumers
 constexpr int kSMs = 152;
 constexpr int kMinRun = 128;                    // units per SM from which chunks come in levels
 constexpr int kScaleCopies = 16;                // lanes that copy an 8-bit stage's scale bytes
 
-// What the kernels differ in.  kUnit: keys of a stage.  kStages: of the ring.  kThreads: of a CTA.  kReaders: groups that
-// read a segment's record, 1 (they take the pairs in turn) or both.
+// What the kernels differ in.  kUnit: keys of a stage.  kStages: of the ring.  kTeams: groups of
+// consumers, or teams of groups, that take the pairs in turn.  kProducer: the producer's warp.
 struct Bf16Stream {
     static constexpr bool kQ8 = false;
-    static constexpr int kUnit = 64, kThreads = 32 * (kGroups * kConsumers + 1), kReaders = 1;
-    static constexpr int kStages = 6;
+    static constexpr int kUnit = 64, kStages = 6, kSegSlots = 4, kTeams = 2;
+    static constexpr int kProducer = kTeams * kConsumers, kThreads = 32 * (kProducer + 1);
 };
-template <bool SPLIT>
+template <int TEAM>   // groups of a team
 struct Q8Stream {
     static constexpr bool kQ8 = true;
-    static constexpr int kUnit = 128, kThreads = 32 * (kGroups * kConsumers + 4),
-                         kReaders = SPLIT ? kGroups : 1;
-    static constexpr int kStages = SPLIT ? 5 : 6;
+    static constexpr int kGroups = 4, kTeams = kGroups / TEAM;
+    static constexpr int kUnit = 128, kStages = TEAM == 4 ? 5 : 6, kSegSlots = 8;
+    static constexpr int kProducer = kGroups * kConsumers, kThreads = 32 * (kProducer + 4);
 };
+constexpr int kBlockRows = 32;                  // of a pair where sequences have more
 
 // A run of stages of one (sequence, KV head).  stages < 0: no more.
 struct Segment {
     int row0, T, S, seq, g, unit0, stages;
     int u0;     // stages of the CTA's run before it
     int slot;   // -1: all of the pair's keys; else the partial's place
+    int r0;     // first of the pair's rows (8-bit pages: rows go in blocks)
 };
 
 // A pair whose keys begin in one chunk and go on in the next ones.  rows = 0: none.
 struct Joint {
-    int row0, g, rows, parts;
+    int row0, g, rows, parts, r0;
 };
 
 // What the producer shares with the consumers.
 struct StreamBars {
-    Segment seg[kSegSlots];
-    uint64_t full[kGroups][kMostStages];   // a stage's load (of 8-bit pages: [0] alone)
+    Segment seg[8];
+    uint64_t full[2][kMostStages];     // a stage's load, for its team (of 8-bit pages: [0] alone)
     uint64_t empty[kMostStages];
-    uint64_t seg_full[kSegSlots], seg_free[kSegSlots];
-    uint4 clc_resp;
+    uint64_t seg_full[8], seg_free[8];
     uint64_t clc_full;
-    int scan[12], most[12];            // units of each warp's sequences; of a pair
+    uint4 clc_resp;
+    int scan[20], most[20];            // units of each warp's sequences; of a pair
 };
 
 struct Params {
@@ -79,6 +79,7 @@ struct Params {
     int nseq, Hq, Hkv, G, window, num_pages, page_size, page_shift, max_pages;
     uint32_t inv_g;                // 2^16 / G, rounded up
     int whole;                     // 1: CTAs take whole pairs, every gridDim.x-th one
+    int blocks;                    // of kBlockRows rows, a pair each, that a sequence has at most
     float scale_log2;
 };
 
@@ -87,12 +88,18 @@ struct Params {
 bool whole_pairs(int max_kv);
 int n_chunks(int nseq, int max_kv, int Hkv, int max_q, int window, int unit);
 size_t partials_bytes(int chunks, int rows);
-Params params_of(const PackedAttn &a, int unit, int rec_rows, void *ws, int *status);
+Params params_of(const PackedAttn &a, int unit, int rec_rows, int blocks, void *ws, int *status);
 cudaError_t launch_combine(const Params &p, int max_q, cudaStream_t s);
 
-// r / G for a row r <= 32 of a pair (the error, r / 2^16 at most, is below 1 / G).
+// r / G for a row r < 1024 of a pair (the error, r / 2^16 at most, is below 1 / G).
 __device__ __forceinline__ int token_of(const Params &p, int r) {
     return static_cast<int>(r * p.inv_g >> 16);
+}
+
+// Pairs of a sequence's KV head: one, or one per block of its rows.
+template <class S>
+__device__ __forceinline__ int blocks_of(const Params &p, int T) {
+    return S::kQ8 && p.blocks > 1 ? (T * p.G + kBlockRows - 1) / kBlockRows : 1;
 }
 
 // Units of one (sequence, KV head): [first, first + count) of `unit` keys each.
@@ -187,8 +194,9 @@ __device__ __forceinline__ void scan_units(const Params &p, StreamBars *bars) {
         const int s0 = threadIdx.x * m;
         int mine = 0, most = 0;
         for (int i = s0; i < s0 + m && i < p.nseq; ++i) {
-            const int n = count_units<S::kUnit>(packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status), p.window);
-            mine += p.Hkv * n;
+            const PackedSeq s = packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status);
+            const int n = count_units<S::kUnit>(s, p.window);
+            mine += p.Hkv * blocks_of<S>(p, s.T) * n;
             most = max(most, n);
         }
 #pragma unroll
@@ -207,6 +215,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
                                         const Params &p, StreamBars *bars, uint8_t *smem,
                                         uint8_t *scales) {
     constexpr int kUnit = S::kUnit, kThreads = S::kThreads, kStages = S::kStages;
+    constexpr int kSegSlots = S::kSegSlots, kTeams = S::kTeams;
     const int lane = threadIdx.x & 31, m = sequences_each<S>(p);
     if (lane == 0) {
         tma_prefetch_desc(&tmK);
@@ -220,9 +229,10 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
     // The batch as a list of items, 32 of them in the lanes at a time: sequences with all
     // their KV heads, or the CTA's whole pairs.
     const int items = !p.whole ? p.nseq
-                               : (p.nseq * p.Hkv - static_cast<int>(blockIdx.x) +
+                               : (p.nseq * p.Hkv * p.blocks - static_cast<int>(blockIdx.x) +
                                   static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-    const int heads = p.whole ? 1 : p.Hkv;
+    // Pairs of an item: one, or an 8-bit stream's heads times the sequence's blocks of rows.
+    int s_heads = p.whole ? 1 : p.Hkv;
     int base = 0, at = 0;      // the lanes' first item; the next one among them
     PackedSeq s{0, 0, 0};      // of this lane's item, as are the next three
     int s_seq = 0, s_head = 0, s_units = 0;
@@ -233,12 +243,16 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         const int i = base + lane;
         if (i < items) {
             const int pair = p.whole ? static_cast<int>(blockIdx.x + i * gridDim.x) : 0;
-            s_seq = p.whole ? pair / p.Hkv : i;
+            s_seq = p.whole ? pair / (p.Hkv * p.blocks) : i;
             // its first page entries, not after its lengths but with them
             if (p.whole) touch(p.pages + (long)s_seq * p.max_pages);
-            s_head = p.whole ? pair - s_seq * p.Hkv : 0;
+            s_head = p.whole ? pair - s_seq * p.Hkv * p.blocks : 0;
             s = packed_seq(p.cu, p.kv_lens, s_seq, p.bounds, p.whole ? p.status : nullptr);
             s_units = count_units<kUnit>(s, p.window);
+            if constexpr (S::kQ8) {
+                if (!p.whole) s_heads = p.Hkv * blocks_of<S>(p, s.T);
+                else if (s_head % p.blocks >= blocks_of<S>(p, s.T)) s_units = 0;
+            }
         }
     };
     int listed = 0;            // stages of the segments so far
@@ -246,7 +260,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
     // The chunk at hand: its units left, the number of the next one, and the pair that goes
     // on behind it.
     int run = 0x7fffffff, chunk = blockIdx.x, pos = 0, all = 0, most = 0;
-    Joint joint{0, 0, 0, 0};
+    Joint joint{0, 0, 0, 0, 0};
     if (!p.whole)
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
@@ -256,7 +270,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
     const Cut cut(all, most, p.chunks);
     auto start_chunk = [&]() {
         cut.get(chunk, pos, run);
-        joint = {0, 0, 0, 0};
+        joint = {0, 0, 0, 0, 0};
         if (run == 0) return;
         // the warp's sequences that hold unit `pos`, and then the one
         int w = 0, before = 0;
@@ -264,7 +278,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         int first = 32 * m * w, incl;
         while (true) {
             load_items(first);
-            incl = s_units * heads;
+            incl = s_units * s_heads;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, incl, d);
@@ -278,6 +292,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         const uint32_t behind = __ballot_sync(0xffffffffu, before + incl > pos);
         at = behind ? __ffs(behind) - 1 : 31;
         const int n = max(1, __shfl_sync(0xffffffffu, s_units, at));
+        const int heads = S::kQ8 ? __shfl_sync(0xffffffffu, s_heads, at) : s_heads;
         const int rel = pos - before - (__shfl_sync(0xffffffffu, incl, at) - n * heads);
         head = rel / n;
         in = rel - head * n;
@@ -325,13 +340,25 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         sg.S = __shfl_sync(0xffffffffu, s.S, l);
         sg.seq = __shfl_sync(0xffffffffu, s_seq, l);
         sg.g = __shfl_sync(0xffffffffu, s_head, l) + head;
+        sg.r0 = 0;
+        int heads = s_heads;
+        if constexpr (S::kQ8) {
+            heads = __shfl_sync(0xffffffffu, s_heads, l);
+            if (p.blocks > 1) {        // a head's blocks behind one another: they share its pages
+                const int blocks = p.whole ? p.blocks : blocks_of<S>(p, sg.T);
+                const int h = sg.g / blocks;
+                sg.r0 = kBlockRows * (sg.g - h * blocks);
+                sg.g = h;
+            }
+        }
         sg.unit0 = (p.window > 0 ? max(0, sg.S - sg.T - p.window + 1) / kUnit : 0) + in;
         sg.stages = min(run, n - in);
         sg.u0 = listed;
         listed += sg.stages;
         sg.slot = sg.stages == n ? -1 : 2 * chunk + (in == 0 ? 1 : 0);
         if (in == 0 && sg.stages < n)
-            joint = {sg.row0, sg.g, sg.T * p.G, cut.chunk_of(pos + n - 1) - chunk + 1};
+            joint = {sg.row0, sg.g, S::kQ8 ? min(kBlockRows, sg.T * p.G - sg.r0) : sg.T * p.G,
+                     cut.chunk_of(pos + n - 1) - chunk + 1, sg.r0};
         if (!p.whole) {
             run -= sg.stages;
             pos += sg.stages;
@@ -347,7 +374,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         return sg;
     };
     // The segment after the last one: its record out, its page entries on their way.  The
-    // end is a record for each group.
+    // end is a record for each team.
     Segment ahead;
     PageWalk walk_ahead;
     int k = 0;
@@ -355,7 +382,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         if (run == 0) next_chunk();
         if (!ok) return;
         ahead = next_segment();
-        const int records = ahead.stages < 0 && S::kReaders == 1 ? kGroups : 1;
+        const int records = ahead.stages < 0 ? kTeams : 1;
         for (int i = 0; i < records; ++i, ++k) {
             const int slot = k & (kSegSlots - 1);
             if (k >= kSegSlots && !warp_wait(&bars->seg_free[slot], (k / kSegSlots - 1) & 1)) {
@@ -399,7 +426,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
                 if (pg >= 0 && pg < p.num_pages) slab = pg * p.Hkv + sg.g;
                 else set_status(p.status, GQA_ERR_INVALID_ARG);
             }
-            const int st = u % kStages, group = S::kQ8 ? 0 : turn % kGroups;
+            const int st = u % kStages, group = S::kQ8 ? 0 : turn % kTeams;
             uint64_t *full = &bars->full[group][st];
             // (8-bit pages: a box has keys and values where one copy brings both)
             uint8_t *dst = smem + st * kStageBytes +
