@@ -49,25 +49,29 @@ struct Q8Bars : StreamBars {
     uint64_t s_full[4][kScoreTiles], s_free[4][kScoreTiles];   // of a team
     uint64_t p_full[4], pv_done[4];
     uint64_t meet[4];                // of a group
+    uint64_t gathered, taken;        // the teams' shares of a pair: written; read
     uint64_t drained[2];
+    float2 share[4][8];              // (m, l) of a group's rows
     uint32_t tmem;
     int vote[4][2];                  // the last stage of either parity that moved a group's references
     int nan_any[4][2];
 };
 
-// TEAM groups share a pair, kRows rows each; the teams take the pairs in turn.
-template <int TEAM>
+// TEAM groups share a pair, kRows rows each; the teams take the pairs in turn, or (SHARE) each pair's
+// stages.
+template <int TEAM, bool SHARE>
 struct Layout {
-    using S = Q8Stream<TEAM>;
+    using S = Q8Stream<TEAM, SHARE>;
     static constexpr int kTeams = S::kTeams, kGroups = S::kGroups, kTeamRows = TEAM * kRows;
     static constexpr int kScoreWarp = S::kProducer + 1, kValueWarp = S::kProducer + 2,
                          kQueryWarp = S::kProducer + 3;
     // columns of a team's products (a multiple of 16)
     static constexpr int kScoreN = TEAM * kScoreCols, kValueN = TEAM == 1 ? 32 : TEAM * kValueCols;
     static constexpr int kQuerySlots = kTeams > 2 ? kTeams : 2;
-    // A pair's factors are read after its queries' tile is free again; the team's next two pairs'
-    // scores may be formed by then, and the queries of the one or two after them be there.
-    static constexpr int kFactorSlots = TEAM == 4 ? 8 : 4 * kTeams;
+    // A pair's factors are read after its queries' tile is free again: the scores of as many stages
+    // as the teams have tiles may be formed by then, and the queries of the pairs after those,
+    // as many as have a tile, be there.
+    static constexpr int kFactorSlots = TEAM == 1 ? 16 : 8;
     // tensor memory: score tiles, then outputs
     static constexpr int kOutputs = kTeams * kScoreTiles * kScoreN, kColumns = 256;
     static_assert(kOutputs + kTeams * kValueN <= kColumns, "tensor memory");
@@ -82,7 +86,8 @@ struct Layout {
     static constexpr int kSums = kMost + kGroups * kConsumers * kRows * 8;   // float [group][row][warp]
     static constexpr int kFactors = kSums + kGroups * kRows * kConsumers * 4;   // float [pair][row]
     static constexpr int kNan = kFactors + kFactorSlots * kTeamRows * 4;   // a bit per row and dim
-    static constexpr int kBars = kNan + kTeams * 2 * kTeamRows * 16;
+    static constexpr int kShares = kNan + kTeams * 2 * kTeamRows * 16;   // float [group][row][dim]
+    static constexpr int kBars = kShares + (SHARE ? kGroups * kRows * kD * 4 : 0);
     static constexpr int kBytes = kBars + static_cast<int>(sizeof(Q8Bars)) + 1024;
     static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kQuery % 1024 == 0 && kWeights % 1024 == 0 &&
                   kBars % 16 == 0 && kBytes <= 232448, "shared memory");
@@ -122,9 +127,9 @@ __device__ __forceinline__ float exponent_of(uint32_t byte) {
 }
 
 // ---- the queries' warp: rows of bf16 to tiles of h and l, with the factor of their scores ------
-template <int TEAM>
+template <int TEAM, bool SHARE>
 __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uint8_t *smem) {
-    using L = Layout<TEAM>;
+    using L = Layout<TEAM, SHARE>;
     constexpr int kSegSlots = L::S::kSegSlots;
     const int lane = threadIdx.x & 31;
     for (int k = 0;; ++k) {
@@ -197,10 +202,10 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
 // product in turn: 32 caches of 8k-64k tokens 548 us.)
 //
 // Scores: as soon as a stage's keys, its pair's queries and a score tile of its team are there.
-template <int TEAM>
+template <int TEAM, bool SHARE>
 __device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint8_t *smem,
                                              uint32_t tmem) {
-    using L = Layout<TEAM>;
+    using L = Layout<TEAM, SHARE>;
     constexpr int kStages = L::S::kStages, kSegSlots = L::S::kSegSlots;
     const uint32_t ring = smem_u32(smem);
     const uint64_t kd0 = sdesc_sw128(ring + (p.joint && p.v_first ? 1024 : 0), 16, key_step(p));
@@ -208,7 +213,7 @@ __device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint
     constexpr uint32_t idesc = idesc_f8_f32(128, L::kScoreN, 0, 0);
     uint32_t counts = 0;               // scores of each team's stages, mod 256
     for (int k = 0, u = 0;; ++k) {
-        const int slot = k % kSegSlots, b = k % L::kQuerySlots, team = k % L::kTeams;
+        const int slot = k % kSegSlots, b = k % L::kQuerySlots;
         if (!mbar_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
             expired(p.status, kRoleProducts, 0, k);
             break;
@@ -217,9 +222,10 @@ __device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint
         mbar_arrive(&bars->seg_free[slot]);
         if (stages < 0) break;
         bool ok = mbar_wait(&bars->q_full[b], (k / L::kQuerySlots) & 1);
-        uint32_t n = counts >> (8 * team) & 255;
-        for (int j = 0; ok && j < stages; ++j, ++u, n = n + 1 & 255) {
-            const int st = u % kStages, tile = n % kScoreTiles;
+        for (int j = 0; ok && j < stages; ++j, ++u) {
+            const int team = (SHARE ? u : k) % L::kTeams, st = u % kStages;
+            const uint32_t n = counts >> (8 * team) & 255, tile = n % kScoreTiles;
+            counts = (counts & ~(255u << (8 * team))) | (n + 1 & 255) << (8 * team);
             // (a tile's first use waits for the phase before its first, which reads as done)
             ok = mbar_wait(&bars->s_free[team][tile], (n / kScoreTiles + 1) & 1) &&
                  mbar_wait(&bars->full[0][st], (u / kStages) & 1);
@@ -240,17 +246,16 @@ __device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint
             break;
         }
         umma_commit(&bars->q_free[b]);
-        counts = (counts & ~(255u << (8 * team))) | n << (8 * team);
     }
     umma_commit(&bars->drained[0]);    // nothing in flight when the tensor memory is freed
     if (!mbar_wait(&bars->drained[0], 0)) expired(p.status, kRoleProducts, 2, 0);
 }
 
 // Values: as soon as a stage's weights are there.
-template <int TEAM>
+template <int TEAM, bool SHARE>
 __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint8_t *smem,
                                              uint32_t tmem) {
-    using L = Layout<TEAM>;
+    using L = Layout<TEAM, SHARE>;
     constexpr int kStages = L::S::kStages, kSegSlots = L::S::kSegSlots;
     const uint32_t ring = smem_u32(smem), step = key_step(p);
     const uint64_t vd0 = sdesc_sw128(ring + (!p.joint ? kTileBytes : p.v_first ? 0 : 1024), 16, step);
@@ -258,7 +263,7 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
     constexpr uint32_t idesc = idesc_f8_f32(128, L::kValueN, 1, 1);
     uint32_t parity = 0;               // of each team's weights, a bit each
     for (int k = 0, u = 0;; ++k) {
-        const int slot = k % kSegSlots, team = k % L::kTeams;
+        const int slot = k % kSegSlots;
         if (!mbar_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
             expired(p.status, kRoleProducts, 3, k);
             break;
@@ -266,18 +271,20 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
         const int stages = bars->seg[slot].stages;
         mbar_arrive(&bars->seg_free[slot]);
         if (stages < 0) break;
-        const uint64_t pd = pd0 + team * (L::kWeights >> 4);
         bool ok = true;
-        for (int j = 0; j < stages; ++j, ++u, parity ^= 1u << team) {
+        for (int j = 0; j < stages; ++j, ++u) {
+            const int team = (SHARE ? u : k) % L::kTeams;
+            const uint64_t pd = pd0 + team * (L::kWeights >> 4);
             ok = mbar_wait(&bars->p_full[team], parity >> team & 1);
             if (!ok) break;
+            parity ^= 1u << team;
             tc_fence_after();
             const int st = u % kStages;
             const uint64_t vd = vd0 + st * (kStageBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
                 umma_f8_ss(tmem + L::kOutputs + team * L::kValueN, vd + kk * (step >> 2), pd + 2 * kk,
-                           idesc, kk > 0 || j > 0);
+                           idesc, kk > 0 || j >= (SHARE ? L::kTeams : 1));
             umma_commit(&bars->pv_done[team]);
             umma_commit(&bars->empty[st]);
         }
@@ -291,9 +298,9 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
 }
 
 // ---- a softmax group's warp ---------------------------------------------------------------------
-template <int TEAM>
+template <int TEAM, bool SHARE>
 __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *smem, uint32_t tmem) {
-    using L = Layout<TEAM>;
+    using L = Layout<TEAM, SHARE>;
     constexpr int kStages = L::S::kStages, kUnit = L::S::kUnit, kSegSlots = L::S::kSegSlots;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = warp / kConsumers, cw = warp % kConsumers, team = group / TEAM, member = group % TEAM;
@@ -319,7 +326,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
     };
     auto fail = [&](int barrier, int n) { expired(p.status, kRoleConsumer, barrier, n); };
 #pragma unroll 1
-    for (int k = team, turn = 0;; k += L::kTeams, turn ^= 1) {
+    for (int k = SHARE ? 0 : team, turn = 0;; k += SHARE ? 1 : L::kTeams, turn ^= 1) {
         const int slot = k % kSegSlots;
         if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) return fail(0, k);
         const Segment sg = bars->seg[slot];
@@ -337,11 +344,13 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                    ((2 * team + which) * L::kTeamRows + r) * 4;
         };
         float m = -CUDART_INF_F, mo = -CUDART_INF_F;   // of row `lane`
+        bool fresh = true;             // no stage of this pair yet
         float l[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) l[r] = 0.f;
 #pragma unroll 1
         for (int j = 0, u = sg.u0; j < sg.stages; ++j, ++u) {
+            if (SHARE && u % L::kTeams != team) continue;
             const int st = u % kStages, si = scored % kScoreTiles;
             if (!warp_wait(&bars->s_full[team][si], (scored / kScoreTiles) & 1)) return fail(1, u);
             ++scored;
@@ -378,7 +387,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                 }
                 // ---- weights w and products P, against new references where the old are passed
                 float w[kRows], pw[kRows];
-                bool update = j == 0;
+                bool update = fresh;
 #pragma unroll 1
                 while (true) {
                     if (update) {
@@ -412,15 +421,15 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                             rowf[lane] = make_float4(
                                 factors[lane], -fmaxf(mn, -3.0e38f),
                                 mn == -CUDART_INF_F ? 0.f : ex2_approx(mn - mno + kShift), 0.f);
-                            if (j == 0 && cw == 0 && bars->nan_any[group][turn ^ 1]) {
+                            if (!SHARE && fresh && cw == 0 && bars->nan_any[group][turn ^ 1]) {
                                 // the last pair's bits have been read
                                 *reinterpret_cast<uint4 *>(nan_row(turn ^ 1, kRows * member + lane)) =
                                     make_uint4(0, 0, 0, 0);
                             }
                         }
                         __syncwarp();
-                        if (j == 0 && cw == 0 && lane == 0) bars->nan_any[group][turn ^ 1] = 0;
-                        if (j > 0) {
+                        if (!SHARE && fresh && cw == 0 && lane == 0) bars->nan_any[group][turn ^ 1] = 0;
+                        if (!fresh) {
                             if (!products_done()) return fail(4, u);
                             tc_fence_after();
 #pragma unroll 1
@@ -518,6 +527,101 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->p_full[team]);
             ++handed;
+            fresh = false;
+        }
+        if constexpr (SHARE) {
+            float *shares = reinterpret_cast<float *>(smem + L::kShares);
+            bool nans = false;
+            if (rows > 0) {
+                // this team's share, O relative to m (times 2^(mo - 12 - m), in two steps as that
+                // may be 2^-138)
+                const int row = gather_rows(l, [](float a, float b) { return a + b; });
+                if ((lane & 3) == 0) sums[row * kConsumers + cw] = l[0];
+                if (!meet() || !products_done()) return fail(6, k);
+                if (k > 0 && !warp_wait(&bars->taken, k - 1 & 1)) return fail(7, k);
+                if (lane < kRows) {
+                    const float4 s = *reinterpret_cast<const float4 *>(sums + lane * kConsumers);
+                    change[lane].x = mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift - m));
+                    if (cw == 0) bars->share[group][lane] = make_float2(m, (s.x + s.y) + (s.z + s.w));
+                }
+                __syncwarp();
+                tc_fence_after();
+                uint32_t a[kRows], b[kRows], c[kRows];
+                tmem_ld8(outputs, a);
+                tmem_ld8(outputs + kRows, b);
+                tmem_ld8(outputs + 2 * kRows, c);
+                tmem_wait_ld();
+                tc_fence_before();
+                nans = *const_cast<volatile int *>(&bars->nan_any[group][turn]) != 0;
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const float f = change[r].x;
+                    float x = (__uint_as_float(a[r]) + (__uint_as_float(b[r]) + __uint_as_float(c[r]))) *
+                              f * f;
+                    if (nans && nan_row(turn, kRows * member + r)[t / 32] >> (t & 31) & 1)
+                        x = CUDART_NAN_F;
+                    shares[(group * kRows + r) * kD + t] = fresh ? 0.f : x;
+                }
+            } else if (k > 0 && !warp_wait(&bars->taken, k - 1 & 1)) {   // (sees every phase)
+                return fail(7, k);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->gathered);
+            if (!warp_wait(&bars->gathered, k & 1)) return fail(8, k);
+            if (nans && cw == 0) {     // the bits have been read
+                if (lane < kRows)
+                    *reinterpret_cast<uint4 *>(nan_row(turn, kRows * member + lane)) =
+                        make_uint4(0, 0, 0, 0);
+                if (lane == 0) bars->nan_any[group][turn] = 0;
+            }
+            // a warp adds up a row, 4 dims per lane
+            const int row0 = sg.r0 + warp;
+            if (warp < L::kTeamRows && row0 < sg.T * p.G) {
+                float2 x[L::kTeams];
+                float M = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < L::kTeams; ++i) {
+                    x[i] = bars->share[i * TEAM + warp / kRows][warp % kRows];
+                    M = fmaxf(M, x[i].x);
+                }
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < L::kTeams; ++i) {
+                    // a share none of whose keys this row sees: m = -inf, l = 0 and O = 0 (NaN
+                    // scores alone also leave m at -inf, with l and O NaN)
+                    const float f = x[i].x == -CUDART_INF_F ? (x[i].y == 0.f ? 0.f : 1.f)
+                                                            : ex2_approx(x[i].x - M);
+                    const float4 y = reinterpret_cast<const float4 *>(
+                        shares + ((i * TEAM + warp / kRows) * kRows + warp % kRows) * kD)[lane];
+                    sum = fmaf(x[i].y, f, sum);
+                    acc.x = fmaf(y.x, f, acc.x);
+                    acc.y = fmaf(y.y, f, acc.y);
+                    acc.z = fmaf(y.z, f, acc.z);
+                    acc.w = fmaf(y.w, f, acc.w);
+                }
+                if (sg.slot >= 0) {
+                    const size_t rec = (size_t)sg.slot * p.rec_rows + warp;
+                    if (GQA_IN_BOUNDS(rec, (long)2 * p.chunks * p.rec_rows, p.status, kSite | 9)) {
+                        reinterpret_cast<float4 *>(p.ws_o + rec * kD)[lane] = acc;
+                        if (lane == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(M, sum);
+                    }
+                } else {
+                    const int tok = token_of(p, row0), head = sg.g * p.G + row0 - tok * p.G;
+                    const long at = sg.row0 + tok;
+                    if (GQA_IN_BOUNDS(at, p.bounds.total, p.status, kSite | 10)) {
+                        const float inv = 1.0f / sum;
+                        reinterpret_cast<uint2 *>(p.o + at * p.o_stride + head * kD)[lane] =
+                            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                       pack_bf16x2(acc.z * inv, acc.w * inv));
+                        if (p.lse && lane == 0)
+                            p.lse[(long)head * p.bounds.total + at] =
+                                (M + __log2f(sum)) * 0.69314718055994531f;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->taken);
+            continue;
         }
         if (rows == 0) continue;
         // ---- the pair's (or span's) result: this thread's dim of all rows
@@ -577,13 +681,13 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
     }
 }
 
-template <int TEAM>
-__global__ void __launch_bounds__(Q8Stream<TEAM>::kThreads, 1)
+template <int TEAM, bool SHARE>
+__global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
     paged_q8_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const Params p) {
     griddep_wait();
     griddep_launch_dependents();
-    using L = Layout<TEAM>;
+    using L = Layout<TEAM, SHARE>;
     using S = typename L::S;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -597,7 +701,7 @@ __global__ void __launch_bounds__(Q8Stream<TEAM>::kThreads, 1)
         }
         for (int i = 0; i < S::kSegSlots; ++i) {
             mbar_init(&bars->seg_full[i], 1);
-            mbar_init(&bars->seg_free[i], TEAM * kConsumers + 3);
+            mbar_init(&bars->seg_free[i], (SHARE ? L::kGroups : TEAM) * kConsumers + 3);
         }
         for (int g = 0; g < 4; ++g) {
             mbar_init(&bars->q_full[g], 1);
@@ -612,6 +716,8 @@ __global__ void __launch_bounds__(Q8Stream<TEAM>::kThreads, 1)
             for (int i = 0; i < 2; ++i) bars->vote[g][i] = bars->nan_any[g][i] = 0;
         }
         for (int i = 0; i < 2; ++i) mbar_init(&bars->drained[i], 1);
+        mbar_init(&bars->gathered, L::kGroups * kConsumers);
+        mbar_init(&bars->taken, L::kGroups * kConsumers);
         mbar_init(&bars->clc_full, 1);
         fence_mbar_init();
     }
@@ -630,11 +736,11 @@ __global__ void __launch_bounds__(Q8Stream<TEAM>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
-    if (warp < S::kProducer) softmax<TEAM>(p, bars, smem, tmem);
+    if (warp < S::kProducer) softmax<TEAM, SHARE>(p, bars, smem, tmem);
     else if (warp == S::kProducer) produce<S>(tmK, tmV, p, bars, smem, smem + L::kScales);
-    else if (warp == L::kQueryWarp) bring_queries<TEAM>(p, bars, smem);
-    else if (warp == L::kScoreWarp && lane == 0) issue_scores<TEAM>(p, bars, smem, tmem);
-    else if (warp == L::kValueWarp && lane == 0) issue_values<TEAM>(p, bars, smem, tmem);
+    else if (warp == L::kQueryWarp) bring_queries<TEAM, SHARE>(p, bars, smem);
+    else if (warp == L::kScoreWarp && lane == 0) issue_scores<TEAM, SHARE>(p, bars, smem, tmem);
+    else if (warp == L::kValueWarp && lane == 0) issue_values<TEAM, SHARE>(p, bars, smem, tmem);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -658,10 +764,10 @@ Plan plan_of(int max_q, int Hq, int Hkv) {
     return blocks <= kMostBlocks ? Plan{4, static_cast<int>(blocks)} : Plan{0, 0};
 }
 
-template <int TEAM>
+template <int TEAM, bool SHARE>
 int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, int blocks, void *ws, int *status,
                   cudaStream_t s) {
-    using L = Layout<TEAM>;
+    using L = Layout<TEAM, SHARE>;
     Params p = params_of(a, L::S::kUnit, L::kTeamRows, blocks, ws, status);
     p.scales = static_cast<const uint8_t *>(c.scales);
     // {128 numbers, 8 keys, the two pools, groups of 8 keys, (page, KV head)}: a map takes a stride
@@ -682,7 +788,7 @@ int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, int blocks, voi
         return GQA_ERR_CUDA;
     const long pairs = (long)a.nseq * a.Hkv * blocks;
     const long grid = !p.whole ? p.chunks : pairs < kSMs ? pairs : kSMs;
-    auto kern = paged_q8_kernel<TEAM>;
+    auto kern = paged_q8_kernel<TEAM, SHARE>;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), L::kBytes) != cudaSuccess ||
         launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(L::S::kThreads), L::kBytes, s, mk, mv,
                    p) != cudaSuccess)
@@ -707,7 +813,7 @@ size_t paged_q8_workspace_bytes(int nseq, int total, int max_q, int max_kv, int 
     if (plan.team)
         return whole_pairs(max_kv)
                    ? 0
-                   : partials_bytes(n_chunks(nseq, max_kv, Hkv * plan.blocks, 1, 0, Q8Stream<1>::kUnit),
+                   : partials_bytes(n_chunks(nseq, max_kv, Hkv * plan.blocks, 1, 0, Q8Stream<1, false>::kUnit),
                                     plan.team * kRows);
     return paged_expand_q8_bytes(nseq, max_kv, Hkv) +
            packed_prefill_workspace_bytes(nseq, total, max_kv, Hq, Hkv);
@@ -721,9 +827,13 @@ int launch_paged_q8(const PackedAttn &a, const gqa_paged_kv_q8 &c, void *ws, int
     b.cache = &pages;
     const Plan plan = plan_of(a.max_q, a.Hq, a.Hkv);
     switch (plan.team) {
-        case 1: return launch_stream<1>(b, c, plan.blocks, ws, status, s);
-        case 2: return launch_stream<2>(b, c, plan.blocks, ws, status, s);
-        case 4: return launch_stream<4>(b, c, plan.blocks, ws, status, s);
+        case 1:
+            return whole_pairs(a.max_kv) ? launch_stream<1, false>(b, c, 1, ws, status, s)
+                                         : launch_stream<1, true>(b, c, 1, ws, status, s);
+        case 2:
+            return whole_pairs(a.max_kv) ? launch_stream<2, false>(b, c, 1, ws, status, s)
+                                         : launch_stream<2, true>(b, c, 1, ws, status, s);
+        case 4: return launch_stream<4, false>(b, c, plan.blocks, ws, status, s);
     }
     if (launch_paged_expand_q8(c, a, ws, &pages, status, s) != cudaSuccess) return GQA_ERR_CUDA;
     b.k = pages.k;

@@ -24,17 +24,18 @@ constexpr int kMinRun = 128;                    // units per SM from which chunk
 constexpr int kScaleCopies = 16;                // lanes that copy an 8-bit stage's scale bytes
 
 // What the kernels differ in.  kUnit: keys of a stage.  kStages: of the ring.  kTeams: groups of
-// consumers, or teams of groups, that take the pairs in turn.  kProducer: the producer's warp.
+// consumers, or teams of groups, that take the pairs in turn.  kEnds: records of the end.  kProducer:
+// the producer's warp.
 struct Bf16Stream {
     static constexpr bool kQ8 = false;
-    static constexpr int kUnit = 64, kStages = 6, kSegSlots = 4, kTeams = 2;
+    static constexpr int kUnit = 64, kStages = 6, kSegSlots = 4, kTeams = 2, kEnds = kTeams;
     static constexpr int kProducer = kTeams * kConsumers, kThreads = 32 * (kProducer + 1);
 };
-template <int TEAM>   // groups of a team
+template <int TEAM, bool SHARE>   // groups of a team; the teams take a pair's stages in turn
 struct Q8Stream {
     static constexpr bool kQ8 = true;
-    static constexpr int kGroups = 4, kTeams = kGroups / TEAM;
-    static constexpr int kUnit = 128, kStages = TEAM == 4 ? 5 : 6, kSegSlots = 8;
+    static constexpr int kGroups = 4, kTeams = kGroups / TEAM, kEnds = SHARE ? 1 : kTeams;
+    static constexpr int kUnit = 128, kStages = SHARE || TEAM == 4 ? 5 : 6, kSegSlots = 8;
     static constexpr int kProducer = kGroups * kConsumers, kThreads = 32 * (kProducer + 4);
 };
 constexpr int kBlockRows = 32;                  // of a pair where sequences have more
@@ -215,7 +216,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
                                         const Params &p, StreamBars *bars, uint8_t *smem,
                                         uint8_t *scales) {
     constexpr int kUnit = S::kUnit, kThreads = S::kThreads, kStages = S::kStages;
-    constexpr int kSegSlots = S::kSegSlots, kTeams = S::kTeams;
+    constexpr int kSegSlots = S::kSegSlots;
     const int lane = threadIdx.x & 31, m = sequences_each<S>(p);
     if (lane == 0) {
         tma_prefetch_desc(&tmK);
@@ -382,7 +383,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         if (run == 0) next_chunk();
         if (!ok) return;
         ahead = next_segment();
-        const int records = ahead.stages < 0 ? kTeams : 1;
+        const int records = ahead.stages < 0 ? S::kEnds : 1;
         for (int i = 0; i < records; ++i, ++k) {
             const int slot = k & (kSegSlots - 1);
             if (k >= kSegSlots && !warp_wait(&bars->seg_free[slot], (k / kSegSlots - 1) & 1)) {
@@ -426,7 +427,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
                 if (pg >= 0 && pg < p.num_pages) slab = pg * p.Hkv + sg.g;
                 else set_status(p.status, GQA_ERR_INVALID_ARG);
             }
-            const int st = u % kStages, group = S::kQ8 ? 0 : turn % kTeams;
+            const int st = u % kStages, group = S::kQ8 ? 0 : turn % S::kTeams;
             uint64_t *full = &bars->full[group][st];
             // (8-bit pages: a box has keys and values where one copy brings both)
             uint8_t *dst = smem + st * kStageBytes +
