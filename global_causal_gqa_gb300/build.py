@@ -29,7 +29,8 @@ LIB_DEBUG = os.path.join(PKG, "libgqa_attn_debug.so")
 SOURCES = ["api.cu", "rope.cu", "kv.cu", "decode.cu", "prefill.cu", "prefill_stream.cu",
            "prefill_wide.cu", "prefill_pair.cu", "qknorm.cu", "chunk.cu", "watchdog.cu",
            "packed_append.cu", "packed_prefill.cu", "paged_decode.cu",
-           "packed_attn.cu", "paged_read.cu", "paged_q8.cu"]
+           "packed_attn.cu", "paged_read.cu", "paged_q8.cu",
+           "paged_q8_few.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "packed.cuh", "q8.cuh",
            "paged_stream.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

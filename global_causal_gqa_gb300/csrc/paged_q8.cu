@@ -66,12 +66,12 @@ struct Layout {
     static constexpr int kScoreWarp = S::kProducer + 1, kValueWarp = S::kProducer + 2,
                          kQueryWarp = S::kProducer + 3;
     // columns of a team's products (a multiple of 16)
-    static constexpr int kScoreN = TEAM * kScoreCols, kValueN = TEAM == 1 ? 32 : TEAM * kValueCols;
-    static constexpr int kQuerySlots = kTeams > 2 ? kTeams : 2;
+    static constexpr int kScoreN = TEAM * kScoreCols, kValueN = TEAM * kValueCols;
+    static constexpr int kQuerySlots = 2;
     // A pair's factors are read after its queries' tile is free again: the scores of as many stages
     // as the teams have tiles may be formed by then, and the queries of the pairs after those,
     // as many as have a tile, be there.
-    static constexpr int kFactorSlots = TEAM == 1 ? 16 : 8;
+    static constexpr int kFactorSlots = 8;
     // tensor memory: score tiles, then outputs
     static constexpr int kOutputs = kTeams * kScoreTiles * kScoreN, kColumns = 256;
     static_assert(kOutputs + kTeams * kValueN <= kColumns, "tensor memory");
@@ -119,11 +119,6 @@ __device__ __forceinline__ int gather_rows(float (&a)[kRows], Op op) {
         }
     }
     return lane >> 2;
-}
-
-// byte - 127, the exponent that a scale byte stands for; NaN for 255.
-__device__ __forceinline__ float exponent_of(uint32_t byte) {
-    return byte == kScaleNan ? CUDART_NAN_F : __uint_as_float(0x4b000000u | byte) - 8388735.0f;
 }
 
 // ---- the queries' warp: rows of bf16 to tiles of h and l, with the factor of their scores ------
@@ -750,12 +745,12 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
     }
 }
 
-// How the streaming kernel takes a call: groups of a team (0: the tile kernel does) and blocks of
-// rows per sequence.
+// How a call is taken: groups of a team (1: by the kernel for up to 8 rows; 0: by the tile kernel)
+// and blocks of rows per sequence.
 struct Plan {
     int team, blocks;
 };
-constexpr int kMostBlocks = 2;
+constexpr int kMostBlocks = 2, kStreamUnit = 128;
 Plan plan_of(int max_q, int Hq, int Hkv) {
     const long n = static_cast<long>(max_q) * (Hq / Hkv);
     if (n <= kRows) return {1, 1};
@@ -764,16 +759,11 @@ Plan plan_of(int max_q, int Hq, int Hkv) {
     return blocks <= kMostBlocks ? Plan{4, static_cast<int>(blocks)} : Plan{0, 0};
 }
 
-template <int TEAM, bool SHARE>
-int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, int blocks, void *ws, int *status,
-                  cudaStream_t s) {
-    using L = Layout<TEAM, SHARE>;
-    Params p = params_of(a, L::S::kUnit, L::kTeamRows, blocks, ws, status);
-    p.scales = static_cast<const uint8_t *>(c.scales);
-    // {128 numbers, 8 keys, the two pools, groups of 8 keys, (page, KV head)}: a map takes a stride
-    // from pool to pool below 2^40, and then a page's keys and values come as one copy, 8 of either
-    // in turn (32 caches of 8k-64k tokens in pages of 16: 577 us with two copies, 458 with one);
-    // else as two.
+// The call's tensor maps, in p what they come to: {128 numbers, 8 keys, the two pools, groups of 8
+// keys, (page, KV head)}.  A map takes a stride from pool to pool below 2^40, and then a page's keys
+// and values come as one copy, 8 of either in turn (32 caches of 8k-64k tokens in pages of 16: 577 us
+// with two copies, 458 with one); else as two.
+bool make_maps(const gqa_paged_kv_q8 &c, Params &p, CUtensorMap *mk, CUtensorMap *mv) {
     const uint64_t kp = reinterpret_cast<uint64_t>(c.k), vp = reinterpret_cast<uint64_t>(c.v);
     const uint64_t apart = kp < vp ? vp - kp : kp - vp, page = c.page_size;
     p.joint = apart > 0 && apart < (1ull << 40);
@@ -782,19 +772,35 @@ int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, int blocks, voi
     const uint64_t dims[5] = {kD, 8, pools, page / 8, (uint64_t)c.num_pages * c.Hkv};
     const uint64_t strides[4] = {kD, p.joint ? apart : kD, 8 * kD, page * kD};
     const uint32_t box[5] = {kD, 8, pools, (uint32_t)page / 8, 1};
-    CUtensorMap mk, mv;
-    if (!make_byte_map(&mk, p.v_first ? c.v : c.k, 5, dims, strides, box) ||
-        !make_byte_map(&mv, c.v, 5, dims, strides, box))
-        return GQA_ERR_CUDA;
-    const long pairs = (long)a.nseq * a.Hkv * blocks;
-    const long grid = !p.whole ? p.chunks : pairs < kSMs ? pairs : kSMs;
+    return make_byte_map(mk, p.v_first ? c.v : c.k, 5, dims, strides, box) &&
+           make_byte_map(mv, c.v, 5, dims, strides, box);
+}
+
+template <int TEAM, bool SHARE>
+int launch(const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, long grid, cudaStream_t s) {
+    using L = Layout<TEAM, SHARE>;
     auto kern = paged_q8_kernel<TEAM, SHARE>;
     if (ensure_smem_attr(reinterpret_cast<const void *>(kern), L::kBytes) != cudaSuccess ||
         launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(L::S::kThreads), L::kBytes, s, mk, mv,
                    p) != cudaSuccess)
         return GQA_ERR_CUDA;
-    if (!p.whole && launch_combine(p, a.max_q, s) != cudaSuccess) return GQA_ERR_CUDA;
     return GQA_OK;
+}
+
+int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, const Plan &plan, void *ws,
+                  int *status, cudaStream_t s) {
+    Params p = params_of(a, kStreamUnit, plan.team * kRows, plan.blocks, ws, status);
+    p.scales = static_cast<const uint8_t *>(c.scales);
+    CUtensorMap mk, mv;
+    if (!make_maps(c, p, &mk, &mv)) return GQA_ERR_CUDA;
+    const long pairs = (long)a.nseq * a.Hkv * plan.blocks;
+    const long grid = !p.whole ? p.chunks : pairs < kSMs ? pairs : kSMs;
+    const int rc = plan.team == 1   ? launch_q8_few(mk, mv, p, grid, s)
+                   : plan.team == 4 ? launch<4, false>(mk, mv, p, grid, s)
+                   : p.whole        ? launch<2, false>(mk, mv, p, grid, s)
+                                    : launch<2, true>(mk, mv, p, grid, s);
+    if (rc == GQA_OK && !p.whole && launch_combine(p, a.max_q, s) != cudaSuccess) return GQA_ERR_CUDA;
+    return rc;
 }
 
 }  // namespace
@@ -813,7 +819,7 @@ size_t paged_q8_workspace_bytes(int nseq, int total, int max_q, int max_kv, int 
     if (plan.team)
         return whole_pairs(max_kv)
                    ? 0
-                   : partials_bytes(n_chunks(nseq, max_kv, Hkv * plan.blocks, 1, 0, Q8Stream<1, false>::kUnit),
+                   : partials_bytes(n_chunks(nseq, max_kv, Hkv * plan.blocks, 1, 0, kStreamUnit),
                                     plan.team * kRows);
     return paged_expand_q8_bytes(nseq, max_kv, Hkv) +
            packed_prefill_workspace_bytes(nseq, total, max_kv, Hq, Hkv);
@@ -826,15 +832,7 @@ int launch_paged_q8(const PackedAttn &a, const gqa_paged_kv_q8 &c, void *ws, int
     PackedAttn b = a;
     b.cache = &pages;
     const Plan plan = plan_of(a.max_q, a.Hq, a.Hkv);
-    switch (plan.team) {
-        case 1:
-            return whole_pairs(a.max_kv) ? launch_stream<1, false>(b, c, 1, ws, status, s)
-                                         : launch_stream<1, true>(b, c, 1, ws, status, s);
-        case 2:
-            return whole_pairs(a.max_kv) ? launch_stream<2, false>(b, c, 1, ws, status, s)
-                                         : launch_stream<2, true>(b, c, 1, ws, status, s);
-        case 4: return launch_stream<4, false>(b, c, plan.blocks, ws, status, s);
-    }
+    if (plan.team) return launch_stream(b, c, plan, ws, status, s);
     if (launch_paged_expand_q8(c, a, ws, &pages, status, s) != cudaSuccess) return GQA_ERR_CUDA;
     b.k = pages.k;
     b.v = pages.v;

@@ -25,11 +25,12 @@ constexpr int kScaleCopies = 16;                // lanes that copy an 8-bit stag
 
 // What the kernels differ in.  kUnit: keys of a stage.  kStages: of the ring.  kTeams: groups of
 // consumers, or teams of groups, that take the pairs in turn.  kEnds: records of the end.  kProducer:
-// the producer's warp.
+// the producer's warp.  full_of: which of its barriers a stage's load completes.
 struct Bf16Stream {
     static constexpr bool kQ8 = false;
     static constexpr int kUnit = 64, kStages = 6, kSegSlots = 4, kTeams = 2, kEnds = kTeams;
     static constexpr int kProducer = kTeams * kConsumers, kThreads = 32 * (kProducer + 1);
+    __device__ static int full_of(int turn, int) { return turn % kTeams; }
 };
 template <int TEAM, bool SHARE>   // groups of a team; the teams take a pair's stages in turn
 struct Q8Stream {
@@ -37,6 +38,7 @@ struct Q8Stream {
     static constexpr int kGroups = 4, kTeams = kGroups / TEAM, kEnds = SHARE ? 1 : kTeams;
     static constexpr int kUnit = 128, kStages = SHARE || TEAM == 4 ? 5 : 6, kSegSlots = 8;
     static constexpr int kProducer = kGroups * kConsumers, kThreads = 32 * (kProducer + 4);
+    __device__ static int full_of(int, int) { return 0; }
 };
 constexpr int kBlockRows = 32;                  // of a pair where sequences have more
 
@@ -56,7 +58,7 @@ struct Joint {
 // What the producer shares with the consumers.
 struct StreamBars {
     Segment seg[8];
-    uint64_t full[2][kMostStages];     // a stage's load, for its team (of 8-bit pages: [0] alone)
+    uint64_t full[2][kMostStages];     // a stage's load
     uint64_t empty[kMostStages];
     uint64_t seg_full[8], seg_free[8];
     uint64_t clc_full;
@@ -91,6 +93,9 @@ int n_chunks(int nseq, int max_kv, int Hkv, int max_q, int window, int unit);
 size_t partials_bytes(int chunks, int rows);
 Params params_of(const PackedAttn &a, int unit, int rec_rows, int blocks, void *ws, int *status);
 cudaError_t launch_combine(const Params &p, int max_q, cudaStream_t s);
+// The kernel for up to 8 rows over 8-bit pages (paged_q8_few.cu); returns a gqa_status.
+int launch_q8_few(const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, long grid,
+                  cudaStream_t s);
 
 // r / G for a row r < 1024 of a pair (the error, r / 2^16 at most, is below 1 / G).
 __device__ __forceinline__ int token_of(const Params &p, int r) {
@@ -176,6 +181,19 @@ __device__ __forceinline__ void copy_async16(void *dst, const void *src, uint32_
         "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%3];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// The transpose of an 8 x 8 matrix of 16-bit values, a row in four lanes.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 enum Role { kRoleProducer = 0, kRoleProducts = 1, kRoleConsumer = 2, kRoleQueries = 3 };
@@ -427,7 +445,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
                 if (pg >= 0 && pg < p.num_pages) slab = pg * p.Hkv + sg.g;
                 else set_status(p.status, GQA_ERR_INVALID_ARG);
             }
-            const int st = u % kStages, group = S::kQ8 ? 0 : turn % S::kTeams;
+            const int st = u % kStages, group = S::full_of(turn, j);
             uint64_t *full = &bars->full[group][st];
             // (8-bit pages: a box has keys and values where one copy brings both)
             uint8_t *dst = smem + st * kStageBytes +

@@ -40,6 +40,11 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
     return byte == 0 ? __uint_as_float(0x00400000u)
                      : __uint_as_float(byte == kScaleNan ? 0x7fffffffu : byte << 23);
 }
+// byte - 127, the exponent that a scale byte stands for; NaN for 255.
+__device__ __forceinline__ float exponent_of(uint32_t byte) {
+    return byte == kScaleNan ? __uint_as_float(0x7fffffffu)
+                             : __uint_as_float(0x4b000000u | byte) - 8388735.0f;
+}
 // 2^(127 - byte) for a byte that scale_byte gives to finite vectors; 0 for the others
 __device__ __forceinline__ float inverse_scale(uint32_t byte) {
     return byte == kScaleNan ? 0.f : __uint_as_float((254u - byte) << 23);
