@@ -30,9 +30,9 @@ SOURCES = ["api.cu", "rope.cu", "kv.cu", "decode.cu", "prefill.cu", "prefill_str
            "prefill_wide.cu", "prefill_pair.cu", "qknorm.cu", "chunk.cu", "watchdog.cu",
            "packed_append.cu", "packed_prefill.cu", "paged_decode.cu",
            "packed_attn.cu", "paged_read.cu", "paged_q8.cu",
-           "paged_q8_few.cu"]
+           "paged_q8_few.cu", "paged_q8_short.cu"]
 HEADERS = ["ptx.cuh", "internal.h", "packed.cuh", "q8.cuh",
-           "paged_stream.cuh"]
+           "paged_stream.cuh", "paged_q8_few.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
          "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr"]

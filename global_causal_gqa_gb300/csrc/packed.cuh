@@ -21,13 +21,11 @@ struct PackedBounds {
     long cap;
 };
 
-// Sequence i.  kv_lens == nullptr: packed prompts, S = T.  Numbers that contradict one
-// another or exceed a bound give T = 0 and are recorded in `status` (nullable).
-__device__ __forceinline__ PackedSeq packed_seq(const int32_t *cu, const int32_t *kv_lens, int i,
-                                                const PackedBounds &b, int *status) {
+// A sequence of rows r0 .. r1 - 1 and `keys` keys.  Numbers that contradict one another or exceed a
+// bound give T = 0 and are recorded in `status` (nullable).
+__device__ __forceinline__ PackedSeq check_seq(int r0, int r1, int keys, const PackedBounds &b,
+                                               int *status) {
     PackedSeq s;
-    const int r0 = __ldg(cu + i), r1 = __ldg(cu + i + 1);
-    const int keys = kv_lens ? __ldg(kv_lens + i) : r1 - r0;   // in flight with the offsets
     s.row0 = r0;
     s.T = r1 - r0;
     if (r0 < 0 || r1 < r0 || r1 > b.total) {
@@ -46,6 +44,14 @@ __device__ __forceinline__ PackedSeq packed_seq(const int32_t *cu, const int32_t
         }
     }
     return s;
+}
+
+// Sequence i.  kv_lens == nullptr: packed prompts, S = T.
+__device__ __forceinline__ PackedSeq packed_seq(const int32_t *cu, const int32_t *kv_lens, int i,
+                                                const PackedBounds &b, int *status) {
+    const int r0 = __ldg(cu + i), r1 = __ldg(cu + i + 1);
+    const int keys = kv_lens ? __ldg(kv_lens + i) : r1 - r0;   // in flight with the offsets
+    return check_seq(r0, r1, keys, b, status);
 }
 
 // The sequence whose rows include packed row `row` (warp-collective: every lane gets it):

@@ -760,10 +760,10 @@ Plan plan_of(int max_q, int Hq, int Hkv) {
 }
 
 // The call's tensor maps, in p what they come to: {128 numbers, 8 keys, the two pools, groups of 8
-// keys, (page, KV head)}.  A map takes a stride from pool to pool below 2^40, and then a page's keys
+// keys, (page, KV head)}, a box of `most` keys of a page at most.  A map takes a stride from pool to pool below 2^40, and then a page's keys
 // and values come as one copy, 8 of either in turn (32 caches of 8k-64k tokens in pages of 16: 577 us
 // with two copies, 458 with one); else as two.
-bool make_maps(const gqa_paged_kv_q8 &c, Params &p, CUtensorMap *mk, CUtensorMap *mv) {
+bool make_maps(const gqa_paged_kv_q8 &c, int most, Params &p, CUtensorMap *mk, CUtensorMap *mv) {
     const uint64_t kp = reinterpret_cast<uint64_t>(c.k), vp = reinterpret_cast<uint64_t>(c.v);
     const uint64_t apart = kp < vp ? vp - kp : kp - vp, page = c.page_size;
     p.joint = apart > 0 && apart < (1ull << 40);
@@ -771,7 +771,7 @@ bool make_maps(const gqa_paged_kv_q8 &c, Params &p, CUtensorMap *mk, CUtensorMap
     const uint32_t pools = p.joint ? 2 : 1;
     const uint64_t dims[5] = {kD, 8, pools, page / 8, (uint64_t)c.num_pages * c.Hkv};
     const uint64_t strides[4] = {kD, p.joint ? apart : kD, 8 * kD, page * kD};
-    const uint32_t box[5] = {kD, 8, pools, (uint32_t)page / 8, 1};
+    const uint32_t box[5] = {kD, 8, pools, static_cast<uint32_t>(c.page_size < most ? page : most) / 8, 1};
     return make_byte_map(mk, p.v_first ? c.v : c.k, 5, dims, strides, box) &&
            make_byte_map(mv, c.v, 5, dims, strides, box);
 }
@@ -792,8 +792,14 @@ int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, const Plan &pla
     Params p = params_of(a, kStreamUnit, plan.team * kRows, plan.blocks, ws, status);
     p.scales = static_cast<const uint8_t *>(c.scales);
     CUtensorMap mk, mv;
-    if (!make_maps(c, p, &mk, &mv)) return GQA_ERR_CUDA;
     const long pairs = (long)a.nseq * a.Hkv * plan.blocks;
+    // A warp per pair where there are many, or some of two steps at most (8 heads of 20-450 tokens:
+    // 304 pairs 24 us and 14 with a CTA per pair, 608 26 and 22, 1024 27 and 29, 2048 39 and 57; 608
+    // of 20-40 tokens 8 and 13).
+    const bool each = plan.team == 1 && p.whole &&
+                      pairs >= (a.max_kv <= 2 * kShortKeys ? 1 : 6) * static_cast<long>(kSMs);
+    if (!make_maps(c, each ? kShortKeys : kStreamUnit, p, &mk, &mv)) return GQA_ERR_CUDA;
+    if (each) return launch_q8_short(mk, mv, p, s);
     const long grid = !p.whole ? p.chunks : pairs < kSMs ? pairs : kSMs;
     const int rc = plan.team == 1   ? launch_q8_few(mk, mv, p, grid, s)
                    : plan.team == 4 ? launch<4, false>(mk, mv, p, grid, s)

@@ -96,6 +96,9 @@ cudaError_t launch_combine(const Params &p, int max_q, cudaStream_t s);
 // The kernel for up to 8 rows over 8-bit pages (paged_q8_few.cu); returns a gqa_status.
 int launch_q8_few(const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, long grid,
                   cudaStream_t s);
+// The one for many short caches among them (paged_q8_short.cu): boxes of kShortKeys keys at most.
+constexpr int kShortKeys = 32;
+int launch_q8_short(const CUtensorMap &mk, const CUtensorMap &mv, const Params &p, cudaStream_t s);
 
 // r / G for a row r < 1024 of a pair (the error, r / 2^16 at most, is below 1 / G).
 __device__ __forceinline__ int token_of(const Params &p, int r) {

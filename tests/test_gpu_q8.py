@@ -341,14 +341,16 @@ class PagedQ8:
     def out(self):
         return self.o[:, :self.Hq * D].reshape(self.total, self.Hq, D)
 
-    def check(self, window=0, scale=D ** -0.5, skip=()):
+    def check(self, window=0, scale=D ** -0.5, skip=(), only=None):
+        """only: the sequences that are looked at (None: all); those of `skip` have to be as they
+        were."""
         o = self.out()
         assert (self.o[:, self.Hq * D:] == -7).all()
         for rows in (slice(0, self.cu[0]), slice(self.cu[-1], self.total)):
             assert (o[rows] == -7).all() and (self.L[:, rows] == -7).all()
         for i, n in enumerate(self.t):
             a, b = self.cu[i], self.cu[i + 1]
-            if n == 0:
+            if n == 0 or (only is not None and i not in only):
                 continue
             if i in skip:
                 assert (o[a:b] == -7).all() and (self.L[:, a:b] == -7).all()
@@ -358,12 +360,12 @@ class PagedQ8:
             pu.check(self.L[:, a:b], rl, bl, f"lse of sequence {i} ({n} of {self.s[i]})")
 
 
-def _paged(t, s, Hq, Hkv, page, window, seed, scale=D ** -0.5, **kw):
+def _paged(t, s, Hq, Hkv, page, window, seed, scale=D ** -0.5, only=None, **kw):
     p = PagedQ8(t, s, Hq, Hkv, page, seed, **kw)
     p.run(window, scale)
     st = pu.status()
     assert st == 0, gqa.STATUS_NAMES.get(st, st)
-    p.check(window, scale)
+    p.check(window, scale, only=only)
     return p
 
 
