@@ -13,9 +13,8 @@
 namespace gqa {
 namespace {
 
-constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 8;       // packed rows of a block, one per warp to look up
-constexpr int kPageTokens = 32;      // keys of a block that fills pages
+constexpr int kReadThreads = 128;
+constexpr int kBatch = 4;            // units of a thread in flight
 constexpr int kSite = kDiagCache << 24;   // of the debug build's checks
 
 struct ReadParams {
@@ -41,87 +40,93 @@ __device__ __forceinline__ int page_of(const ReadParams &p, int i, int pos) {
     return -1;
 }
 
-// 8 numbers of a pool, times the power of two that `byte` stands for.
-__device__ __forceinline__ void read_chunk(const uint2 *pool, long at, uint32_t byte, uint4 *dst) {
-    const uint2 w = __ldcs(pool + at);
+// 8 numbers times the power of two that `byte` stands for, as bf16.
+__device__ __forceinline__ uint4 read_chunk(const uint2 &w, uint32_t byte) {
     const float f = scale_of(byte);
     const uint2 a = e4m3x4_bf16(w.x, f), b = e4m3x4_bf16(w.y, f);
-    *dst = make_uint4(a.x, a.y, b.x, b.y);
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ uint2 load_once(const uint2 *p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
 }
 
-// PAGES: into pages of 128 keys; else into packed rows.  D: head dim.
-template <int D, bool PAGES>
-__global__ void __launch_bounds__(kReadThreads) paged_read_kernel(const ReadParams p) {
+// The units u0, u0 + step, .. of a vector row of `per` units (heads of 8 numbers each), kBatch of
+// them with all their loads before the first store (the compiler may not move a load up past one).
+// slot: the vector of head 0, or -1: zeros.  kd, vd: the row's place, or nullptr; `apart`: chunks
+// from a head's vector to the next one's there.
+template <int D>
+__device__ __forceinline__ void read_row(const ReadParams &p, long slot, int u0, int step, uint4 *kd,
+                                         uint4 *vd, int apart) {
     constexpr int C = D / 8;
-    constexpr int kTokens = PAGES ? kPageTokens : kReadTokens;
+    const int per = p.Hkv * C;
+#pragma unroll 1
+    for (; u0 < per; u0 += kBatch * step) {
+        uint2 kw[kBatch], vw[kBatch];
+        uint32_t bytes[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int u = u0 + i * step, h = u / C;
+            kw[i] = vw[i] = make_uint2(0, 0);
+            bytes[i] = 0x7f7f;
+            const long at = slot + (long)h * p.page_size;
+            if (u >= per || slot < 0 ||
+                !GQA_IN_BOUNDS(at, (long)p.num_pages * p.Hkv * p.page_size, p.status, kSite | 11))
+                continue;
+            bytes[i] = __ldg(p.scales + at);
+            if (kd) kw[i] = load_once(p.k + at * C + u % C);
+            if (vd) vw[i] = load_once(p.v + at * C + u % C);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int u = u0 + i * step;
+            if (u >= per) continue;
+            const long to = (long)(u / C) * apart + u % C;
+            if (kd) kd[to] = read_chunk(kw[i], bytes[i] & 255u);
+            if (vd) vd[to] = read_chunk(vw[i], bytes[i] >> 8);
+        }
+    }
+}
+
+// Packed rows, a warp each.
+template <int D>
+__global__ void __launch_bounds__(kReadThreads) paged_read_kernel(const ReadParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    __shared__ long s_slot[kTokens];     // vector of head 0; -1: outside the pool
-    __shared__ int s_on[kTokens];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int blocks = PAGES ? p.out_pages * (128 / kTokens) : 1;   // of a sequence
-    const int seq = PAGES ? blockIdx.x / blocks : 0;
-    const int first = (PAGES ? blockIdx.x - seq * blocks : blockIdx.x) * kTokens;
-    if (PAGES) {
-        if (warp == 0) {
-            const PackedSeq s = packed_seq(p.cu, p.kv_lens, seq, p.bounds, p.status);
-            const int lo = p.window > 0 ? max(0, s.S - s.T - p.window + 1) : 0;
-            const int key = first + lane;
-            s_on[lane] = s.T > 0 && key >= lo && key < s.S;
-            if (s_on[lane]) {
-                const int page = page_of(p, seq, key);
-                s_slot[lane] = page < 0 ? -1 : (long)page * p.Hkv * p.page_size + key % p.page_size;
-            }
-            if (lane == 0 && first % 128 == 0)
-                p.out_table[(long)seq * p.out_pages + first / 128] = seq * p.out_pages + first / 128;
-        }
-    } else {
-        const int row = first + warp;
-        int i = 0;
-        if (row < p.bounds.total) i = packed_row_seq(p.cu, p.nseq, row);
-        if (lane == 0) {
-            s_on[warp] = 0;
-            if (row < p.bounds.total && i < p.nseq) {
-                const PackedSeq s = packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status);
-                if (row >= s.row0 && row < s.row0 + s.T) {
-                    const int pos = s.S - s.T + (row - s.row0), page = page_of(p, i, pos);
-                    s_on[warp] = 1;
-                    s_slot[warp] = page < 0 ? -1 : (long)page * p.Hkv * p.page_size + pos % p.page_size;
-                }
-            }
-        }
-        // every sequence is looked over, also those that no row falls to
-        for (long n = (long)blockIdx.x * blockDim.x + threadIdx.x; n < p.nseq;
-             n += (long)gridDim.x * blockDim.x)
-            packed_seq(p.cu, p.kv_lens, static_cast<int>(n), p.bounds, p.status);
-    }
-    __syncthreads();
-    const int per = p.Hkv * C;
-#pragma unroll 4
-    for (int u = threadIdx.x; u < kTokens * per; u += kReadThreads) {
-        const int t = u / per, r = u - t * per, h = r / C, c = r - h * C;
-        if (!s_on[t]) continue;
-        uint4 *kd, *vd;
-        if (PAGES) {
-            const int key = first + t;
-            const long at = ((((long)seq * p.out_pages + key / 128) * p.Hkv + h) * 128 + key % 128) * C + c;
-            kd = p.k_out + at;
-            vd = p.v_out + at;
-        } else {
-            kd = p.k_out ? p.k_out + (long)(first + t) * p.k_stride + r : nullptr;
-            vd = p.v_out ? p.v_out + (long)(first + t) * p.v_stride + r : nullptr;
-        }
-        const long slot = s_slot[t] < 0 ? -1 : s_slot[t] + (long)h * p.page_size;
-        if (slot < 0 || !GQA_IN_BOUNDS(slot, (long)p.num_pages * p.Hkv * p.page_size, p.status,
-                                       kSite | 11)) {
-            if (kd) *kd = make_uint4(0, 0, 0, 0);
-            if (vd) *vd = make_uint4(0, 0, 0, 0);
-            continue;
-        }
-        const uint32_t bytes = __ldg(p.scales + slot);
-        if (kd) read_chunk(p.k, slot * C + c, bytes & 255u, kd);
-        if (vd) read_chunk(p.v, slot * C + c, bytes >> 8, vd);
-    }
+    const int lane = threadIdx.x & 31;
+    // every sequence is looked over, also those that no row falls to
+    for (long n = (long)blockIdx.x * blockDim.x + threadIdx.x; n < p.nseq;
+         n += (long)gridDim.x * blockDim.x)
+        packed_seq(p.cu, p.kv_lens, static_cast<int>(n), p.bounds, p.status);
+    const int row = static_cast<int>(blockIdx.x) * (kReadThreads / 32) + (threadIdx.x >> 5);
+    if (row >= p.bounds.total) return;
+    const int i = packed_row_seq(p.cu, p.nseq, row);
+    if (i >= p.nseq) return;
+    const PackedSeq s = packed_seq(p.cu, p.kv_lens, i, p.bounds, lane == 0 ? p.status : nullptr);
+    if (row < s.row0 || row >= s.row0 + s.T) return;
+    const int pos = s.S - s.T + (row - s.row0), page = page_of(p, i, pos);
+    read_row<D>(p, page < 0 ? -1 : (long)page * p.Hkv * p.page_size + pos % p.page_size, lane, 32,
+                p.k_out ? p.k_out + row * p.k_stride : nullptr,
+                p.v_out ? p.v_out + row * p.v_stride : nullptr, D / 8);
+}
+
+// All keys that a call sees into pages of 128, a warp each.
+__global__ void __launch_bounds__(kReadThreads) paged_expand_kernel(const ReadParams p) {
+    constexpr int C = 128 / 8;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, keys = kReadThreads / 32, blocks = p.out_pages * (128 / keys);
+    const int seq = blockIdx.x / blocks, key0 = (blockIdx.x - seq * blocks) * keys;
+    const int key = key0 + (threadIdx.x >> 5), to = seq * p.out_pages + key / 128;
+    if (threadIdx.x == 0 && key % 128 == 0) p.out_table[to] = to;
+    const PackedSeq s = packed_seq(p.cu, p.kv_lens, seq, p.bounds, lane == 0 ? p.status : nullptr);
+    const int lo = p.window > 0 ? max(0, s.S - s.T - p.window + 1) : 0;
+    if (s.T == 0 || key < lo || key >= s.S) return;
+    const int page = page_of(p, seq, key);
+    const long at = (long)to * p.Hkv * 128 * C + key % 128 * C;
+    read_row<128>(p, page < 0 ? -1 : (long)page * p.Hkv * p.page_size + key % p.page_size, lane, 32,
+                  p.k_out + at, p.v_out + at, 128 * C);
 }
 
 ReadParams read_params(const gqa_paged_kv_q8 &c, const int32_t *cu, int nseq, int *status) {
@@ -152,18 +157,18 @@ cudaError_t launch_paged_read_q8(const gqa_paged_kv_q8 &c, const int32_t *cu, in
     p.v_out = static_cast<uint4 *>(v_out);
     p.k_stride = k_stride / 8;
     p.v_stride = v_stride / 8;
-    auto kern = c.d == 64    ? paged_read_kernel<64, false>
-                : c.d == 128 ? paged_read_kernel<128, false>
-                : c.d == 256 ? paged_read_kernel<256, false>
-                             : paged_read_kernel<512, false>;
-    return launch_pdl(kern, dim3((total + kReadTokens - 1) / kReadTokens), dim3(kReadThreads), 0, s,
-                      p);
+    auto kern = c.d == 64    ? paged_read_kernel<64>
+                : c.d == 128 ? paged_read_kernel<128>
+                : c.d == 256 ? paged_read_kernel<256>
+                             : paged_read_kernel<512>;
+    constexpr int rows = kReadThreads / 32;
+    return launch_pdl(kern, dim3((total + rows - 1) / rows), dim3(kReadThreads), 0, s, p);
 }
 
 // Pages, their table's numbers and the grid are counted in 32 bits.
 bool paged_expand_counts_fit(int nseq, int max_kv, int Hkv) {
     const long pages = (long)nseq * ((max_kv + 127) / 128);
-    return pages * (128 / kPageTokens) <= 0x7fffffffL && pages * Hkv <= 0x7fffffffL;
+    return pages * (128 / (kReadThreads / 32)) <= 0x7fffffffL && pages * Hkv <= 0x7fffffffL;
 }
 
 size_t paged_expand_q8_bytes(int nseq, int max_kv, int Hkv) {
@@ -183,9 +188,9 @@ cudaError_t launch_paged_expand_q8(const gqa_paged_kv_q8 &c, const PackedAttn &a
     p.out_table = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + 2 * bytes);
     *out = {p.k_out, p.v_out, p.out_table, c.kv_lens, static_cast<int32_t>(pages), c.Hkv, 128, 128,
             p.out_pages, 0};
-    return launch_pdl(paged_read_kernel<128, true>,
-                      dim3(static_cast<unsigned>(pages * (128 / kPageTokens))), dim3(kReadThreads),
-                      0, s, p);
+    return launch_pdl(paged_expand_kernel,
+                      dim3(static_cast<unsigned>(pages * (128 / (kReadThreads / 32)))),
+                      dim3(kReadThreads), 0, s, p);
 }
 
 }  // namespace gqa
