@@ -48,12 +48,10 @@ struct Q8Bars : StreamBars {
     uint64_t q_full[4], q_free[4];
     uint64_t s_full[4][kScoreTiles], s_free[4][kScoreTiles];   // of a team
     uint64_t p_full[4], pv_done[4];
-    uint64_t meet[4];                // of a group
     uint64_t gathered, taken;        // the teams' shares of a pair: written; read
     uint64_t drained[2];
     float2 share[4][8];              // (m, l) of a group's rows
     uint32_t tmem;
-    int vote[4][2];                  // the last stage of either parity that moved a group's references
     int nan_any[4][2];
 };
 
@@ -92,6 +90,18 @@ struct Layout {
     static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kQuery % 1024 == 0 && kWeights % 1024 == 0 &&
                   kBars % 16 == 0 && kBytes <= 232448, "shared memory");
 };
+
+// Whether a thread of the `threads` that meet at barrier `id` says so.
+__device__ __forceinline__ bool group_any(int id, int threads, bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(mine)), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
 
 // Bytes of a stage from 8 keys (or values) to the next 8.
 __device__ __forceinline__ uint32_t key_step(const Params &p) { return p.joint ? 2048 : 1024; }
@@ -310,12 +320,11 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
     // (of its team's and group's barriers alone a warp sees every phase: a parity two phases back
     // reads as done, so tiles that the teams shared would be read too early)
     int scored = 0;                    // score tiles read
-    int handed = 0, meets = 0;         // weights handed over; meetings of the group's warps
-    auto meet = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->meet[group]);
-        return warp_wait(&bars->meet[group], meets++ & 1);
-    };
+    int handed = 0;                    // weights handed over
+    // The group's warps meet: whether one of them says so.  A warp whose wait has expired goes on to
+    // the next meeting and says it there, so that all four leave together.
+    bool ok = true;
+    auto any = [&](bool mine) { return group_any(group + 1, 32 * kConsumers, mine); };
     auto products_done = [&]() {       // of all weights handed over
         return handed == 0 || warp_wait(&bars->pv_done[team], (handed - 1) & 1);
     };
@@ -323,7 +332,8 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
 #pragma unroll 1
     for (int k = SHARE ? 0 : team, turn = 0;; k += SHARE ? 1 : L::kTeams, turn ^= 1) {
         const int slot = k % kSegSlots;
-        if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) return fail(0, k);
+        if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) ok = false;
+        if (any(!ok)) return fail(0, k);
         const Segment sg = bars->seg[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->seg_free[slot]);
@@ -347,7 +357,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         for (int j = 0, u = sg.u0; j < sg.stages; ++j, ++u) {
             if (SHARE && u % L::kTeams != team) continue;
             const int st = u % kStages, si = scored % kScoreTiles;
-            if (!warp_wait(&bars->s_full[team][si], (scored / kScoreTiles) & 1)) return fail(1, u);
+            if (!warp_wait(&bars->s_full[team][si], (scored / kScoreTiles) & 1)) ok = false;
             ++scored;
             const int kb = (sg.unit0 + j) * kUnit, key = kb + t;
             const bool edge = kb + kUnit - 1 > q_first || kb < lo_all;   // of the mask
@@ -376,9 +386,12 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_free[team][si]);
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
+                for (int r = 0; r < kRows; ++r)
                     y[r] = fmaf(__uint_as_float(s[kRows + r]), kl, __uint_as_float(s[r]) * kf);
-                    if (hidden >> r & 1) y[r] = -CUDART_INF_F;
+                if (edge) {
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)
+                        if (hidden >> r & 1) y[r] = -CUDART_INF_F;
                 }
                 // ---- weights w and products P, against new references where the old are passed
                 float w[kRows], pw[kRows];
@@ -399,7 +412,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                         const int row = gather_rows(a, larger);
                         gather_rows(b, larger);
                         if ((lane & 3) == 0) most[cw * kRows + row] = make_float2(a[0], b[0]);
-                        if (!meet()) return fail(3, u);
+                        if (any(!ok)) return fail(1, u);
                         if (lane < kRows) {
                             float mn = m, mno = mo;
 #pragma unroll
@@ -425,7 +438,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                         __syncwarp();
                         if (!SHARE && fresh && cw == 0 && lane == 0) bars->nan_any[group][turn ^ 1] = 0;
                         if (!fresh) {
-                            if (!products_done()) return fail(4, u);
+                            if (!products_done()) ok = false;
                             tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < 3; ++c) {
@@ -443,30 +456,36 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                             for (int r = 0; r < kRows; ++r) l[r] *= change[r].x;
                         }
                     }
-                    bool over = false;
+                    float top = -CUDART_INF_F, largest = 0.f;
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) {
-                        const float4 f = rowf[r];
-                        const float x = fmaf(y[r], f.x, f.y);
-                        w[r] = ex2_approx(x);
-                        pw[r] = w[r] * f.z * vf;
-                        over |= x > kGrow || pw[r] > kLargest;
+                    for (int r = 0; r < kRows; r += 2) {
+                        float x[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float4 f = rowf[r + i];
+                            x[i] = fmaf(y[r + i], f.x, f.y);
+                            w[r + i] = ex2_approx(x[i]);
+                            pw[r + i] = w[r + i] * f.z * vf;
+                        }
+                        top = fmax3(top, x[0], x[1]);
+                        largest = fmax3(largest, pw[r], pw[r + 1]);
                     }
-                    if (update) break;
-                    if (__any_sync(0xffffffffu, over) && lane == 0) bars->vote[group][u & 1] = u + 1;
-                    if (!meet()) return fail(5, u);
-                    if (*const_cast<volatile int *>(&bars->vote[group][u & 1]) != u + 1) break;
+                    if (update || !any(top > kGrow || largest > kLargest || !ok)) break;
                     update = true;
                 }
                 // ---- P, a byte per column, row and key
-                if (!products_done()) return fail(4, u);    // the last ones have been read
+                if (!products_done()) ok = false;           // the last ones have been read
+                if (edge) {
+                    // (a hidden key's value may have a NaN for a power)
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)
+                        if (hidden >> r & 1) pw[r] = 0.f;
+                }
 #pragma unroll
                 for (int r = 0; r < kRows; r += 2) {
                     l[r] += w[r];
                     l[r + 1] += w[r + 1];
-                    // (a hidden key's value may have a NaN for a power)
-                    const __half2 x = __floats2half2_rn(hidden >> r & 1 ? 0.f : pw[r],
-                                                        hidden >> r & 2 ? 0.f : pw[r + 1]);
+                    const __half2 x = __floats2half2_rn(pw[r], pw[r + 1]);
                     const uint32_t c = *reinterpret_cast<const uint32_t *>(&x) & 0xff00ff00u;
                     const __half2 x1 = __hsub2(x, *reinterpret_cast<const __half2 *>(&c));
                     const uint32_t d = *reinterpret_cast<const uint32_t *>(&x1) & 0xff00ff00u;
@@ -484,7 +503,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
             } else {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_free[team][si]);
-                if (!products_done()) return fail(4, u);   // (sees every phase)
+                if (!products_done()) ok = false;          // (sees every phase)
             }
             // ---- values that the mask hides: 0 * NaN is NaN
             if (edge && member == 0) {
@@ -532,8 +551,9 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                 // may be 2^-138)
                 const int row = gather_rows(l, [](float a, float b) { return a + b; });
                 if ((lane & 3) == 0) sums[row * kConsumers + cw] = l[0];
-                if (!meet() || !products_done()) return fail(6, k);
-                if (k > 0 && !warp_wait(&bars->taken, k - 1 & 1)) return fail(7, k);
+                if (any(!ok)) return fail(2, k);
+                if (!products_done()) ok = false;
+                if (k > 0 && !warp_wait(&bars->taken, k - 1 & 1)) ok = false;
                 if (lane < kRows) {
                     const float4 s = *reinterpret_cast<const float4 *>(sums + lane * kConsumers);
                     change[lane].x = mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift - m));
@@ -558,11 +578,11 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                     shares[(group * kRows + r) * kD + t] = fresh ? 0.f : x;
                 }
             } else if (k > 0 && !warp_wait(&bars->taken, k - 1 & 1)) {   // (sees every phase)
-                return fail(7, k);
+                ok = false;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->gathered);
-            if (!warp_wait(&bars->gathered, k & 1)) return fail(8, k);
+            if (!warp_wait(&bars->gathered, k & 1)) ok = false;
             if (nans && cw == 0) {     // the bits have been read
                 if (lane < kRows)
                     *reinterpret_cast<uint4 *>(nan_row(turn, kRows * member + lane)) =
@@ -622,7 +642,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         // ---- the pair's (or span's) result: this thread's dim of all rows
         const int row = gather_rows(l, [](float a, float b) { return a + b; });
         if ((lane & 3) == 0) sums[row * kConsumers + cw] = l[0];
-        if (!meet()) return fail(6, k);
+        if (any(!ok)) return fail(2, k);
         if (lane < kRows) {
             // A row's factors and where it goes.  O relative to m: times 2^(mo - 12 - m), in two
             // steps as that may be 2^-138.
@@ -651,7 +671,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                                      __uint_as_float(static_cast<uint32_t>(to)),
                                      __uint_as_float(static_cast<uint32_t>(to >> 32)));
         }
-        if (!products_done()) return fail(4, k);
+        if (!products_done()) ok = false;
         __syncwarp();
         tc_fence_after();
         uint32_t a[kRows], b[kRows], c[kRows];
@@ -707,8 +727,7 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
             }
             mbar_init(&bars->p_full[g], TEAM * kConsumers);
             mbar_init(&bars->pv_done[g], 1);
-            mbar_init(&bars->meet[g], kConsumers);
-            for (int i = 0; i < 2; ++i) bars->vote[g][i] = bars->nan_any[g][i] = 0;
+            for (int i = 0; i < 2; ++i) bars->nan_any[g][i] = 0;
         }
         for (int i = 0; i < 2; ++i) mbar_init(&bars->drained[i], 1);
         mbar_init(&bars->gathered, L::kGroups * kConsumers);
