@@ -155,45 +155,48 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
         float *factors = reinterpret_cast<float *>(smem + L::kFactors) +
                          k % L::kFactorSlots * L::kTeamRows;
         uint8_t *tile = smem + L::kQ + b * L::kQuery;
+        // 16 rows at a time, two per load: half a warp has a row, 8 dims per lane
+        const int half = lane >> 4, c = lane & 15;
 #pragma unroll 1
-        for (int i0 = 0; i0 < L::kTeamRows; i0 += 4) {
-            uint2 w[4];                // four dims of four rows
+        for (int i0 = 0; i0 < L::kTeamRows; i0 += 16) {
+            uint4 w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = sg.r0 + i0 + i, t = token_of(p, r);
-                w[i] = make_uint2(0, 0);
-                if (i0 + i < rows && GQA_IN_BOUNDS(sg.row0 + t, p.bounds.total, p.status, kSite | 8))
-                    w[i] = __ldg(reinterpret_cast<const uint2 *>(
-                        p.q + (long)(sg.row0 + t) * p.q_stride + (sg.g * p.G + r - t * p.G) * kD +
-                        4 * lane));
+            for (int i = 0; i < 8; ++i) {
+                const int n = i0 + 2 * i + half, r = sg.r0 + n, t = token_of(p, r);
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (n < rows && GQA_IN_BOUNDS(sg.row0 + t, p.bounds.total, p.status, kSite | 8))
+                    w[i] = __ldg(reinterpret_cast<const uint4 *>(
+                        p.q + (long)(sg.row0 + t) * p.q_stride + (sg.g * p.G + r - t * p.G) * kD + 8 * c));
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x[4] = {bf16lo(w[i].x), bf16hi(w[i].x), bf16lo(w[i].y), bf16hi(w[i].y)};
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
                 uint32_t most = 0;     // (magnitudes compare as their bits do, NaN above all)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) most = max(most, __float_as_uint(x[e]) & 0x7fffffffu);
-                most = __reduce_max_sync(0xffffffffu, most);
+                for (int e = 0; e < 4; ++e)
+                    most = max(most, max(words[e] << 16 & 0x7fffffffu, words[e] & 0x7fff0000u));
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1)
+                    most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
                 const uint32_t ex = max(most >> 23, 8u);
                 const float up = __uint_as_float((261 - ex) << 23);   // 2^(7 - exponent)
-                const uint32_t h = to_e4m3x2(x[0] * up, x[1] * up) |
-                                   to_e4m3x2(x[2] * up, x[3] * up) << 16;
-                uint32_t l = 0;
+                uint32_t h[2] = {0, 0}, l[2] = {0, 0};
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t y = e4m3x2_f16x2(h >> (16 * e) & 0xffffu);
-                    const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-                    l |= to_e4m3x2((x[2 * e] * up - z.x) * 16.f, (x[2 * e + 1] * up - z.y) * 16.f)
-                         << (16 * e);
+                for (int e = 0; e < 4; ++e) {
+                    const float x0 = bf16lo(words[e]) * up, x1 = bf16hi(words[e]) * up;
+                    const uint32_t y = to_e4m3x2(x0, x1), back = e4m3x2_f16x2(y);
+                    const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                    h[e >> 1] |= y << (16 * (e & 1));
+                    l[e >> 1] |= to_e4m3x2((x0 - z.x) * 16.f, (x1 - z.y) * 16.f) << (16 * (e & 1));
                 }
                 // row n of its group: h in the tile's row 16 g + n, l in row 16 g + 8 + n; a row
                 // with an infinity or NaN: NaN
-                const int n = (i0 + i) % kRows;
-                uint8_t *at = tile + ((i0 + i) / kRows * kScoreCols + n) * kD + ((lane >> 2 ^ n) << 4) +
-                              4 * (lane & 3);
-                *reinterpret_cast<uint32_t *>(at) = ex == 255 ? 0x7f7f7f7fu : h;
-                *reinterpret_cast<uint32_t *>(at + kRows * kD) = l;
-                if (lane == 0) factors[i0 + i] = __uint_as_float((ex - 7) << 23) * p.scale_log2;
+                const int row = i0 + 2 * i + half, n = row % kRows;
+                uint8_t *at = tile + (row / kRows * kScoreCols + n) * kD + ((c >> 1 ^ n) << 4) + 8 * (c & 1);
+                *reinterpret_cast<uint2 *>(at) =
+                    ex == 255 ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : make_uint2(h[0], h[1]);
+                *reinterpret_cast<uint2 *>(at + kRows * kD) = make_uint2(l[0], l[1]);
+                if (c == 0) factors[row] = __uint_as_float((ex - 7) << 23) * p.scale_log2;
             }
         }
         fence_proxy_async_smem();
