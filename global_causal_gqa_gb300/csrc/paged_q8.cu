@@ -45,7 +45,7 @@ constexpr float kGrow = 3.0f, kShift = 12.0f, kLargest = 32768.0f;   // log2 uni
 constexpr float kLeast = -100.0f;
 
 struct Q8Bars : StreamBars {
-    uint64_t q_full[4], q_free[4];
+    uint64_t q_full[4], q_free[4], q_raw;
     uint64_t s_full[4][kScoreTiles], s_free[4][kScoreTiles];   // of a team
     uint64_t p_full[4], pv_done[4];
     uint64_t gathered, taken;        // the teams' shares of a pair: written; read
@@ -53,6 +53,11 @@ struct Q8Bars : StreamBars {
     float2 share[4][8];              // (m, l) of a group's rows
     uint32_t tmem;
     int nan_any[4][2];
+};
+
+// Where a row's result goes: its dims (of a partial in fp32, else in bf16), and its sum, or its lse.
+struct Place {
+    void *o, *sum;
 };
 
 // TEAM groups share a pair, kRows rows each; the teams take the pairs in turn, or (SHARE) each pair's
@@ -84,7 +89,9 @@ struct Layout {
     static constexpr int kSums = kMost + kGroups * kConsumers * kRows * 8;   // float [group][row][warp]
     static constexpr int kFactors = kSums + kGroups * kRows * kConsumers * 4;   // float [pair][row]
     static constexpr int kNan = kFactors + kFactorSlots * kTeamRows * 4;   // a bit per row and dim
-    static constexpr int kShares = kNan + kTeams * 2 * kTeamRows * 16;   // float [group][row][dim]
+    static constexpr int kRaw = kNan + kTeams * 2 * kTeamRows * 16;   // a pair's queries in bf16
+    static constexpr int kPlaces = kRaw + kTeamRows * kD * 2;         // Place [pair][row]
+    static constexpr int kShares = kPlaces + kFactorSlots * kTeamRows * 16;   // float [group][row][dim]
     static constexpr int kBars = kShares + (SHARE ? kGroups * kRows * kD * 4 : 0);
     static constexpr int kBytes = kBars + static_cast<int>(sizeof(Q8Bars)) + 1024;
     static_assert(kQ % 1024 == 0 && kP % 1024 == 0 && kQuery % 1024 == 0 && kWeights % 1024 == 0 &&
@@ -155,49 +162,72 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
         float *factors = reinterpret_cast<float *>(smem + L::kFactors) +
                          k % L::kFactorSlots * L::kTeamRows;
         uint8_t *tile = smem + L::kQ + b * L::kQuery;
-        // 16 rows at a time, two per load: half a warp has a row, 8 dims per lane
+        // The rows as they lie, a token's heads by one copy; meanwhile where their results go.
+        const int n_rows = min(rows, L::kTeamRows);
+        const int tok0 = token_of(p, sg.r0), toks = token_of(p, sg.r0 + n_rows - 1) - tok0 + 1;
+        if (lane == 0) mbar_arrive_expect_tx(&bars->q_raw, n_rows * kD * 2);
+        __syncwarp();
+        if (lane < toks) {
+            const int t = tok0 + lane, h0 = max(0, sg.r0 - t * p.G);
+            const int h1 = min(p.G, sg.r0 + n_rows - t * p.G);
+            long at = sg.row0 + t;
+            if (!GQA_IN_BOUNDS(at, p.bounds.total, p.status, kSite | 8)) at = 0;
+            bulk_copy_g2s(smem + L::kRaw + (t * p.G + h0 - sg.r0) * kD * 2,
+                          p.q + at * p.q_stride + (sg.g * p.G + h0) * kD, (h1 - h0) * kD * 2,
+                          &bars->q_raw);
+        }
+        if (lane < L::kTeamRows) {
+            Place to{nullptr, nullptr};
+            if (lane < n_rows && sg.slot >= 0) {
+                const size_t rec = (size_t)sg.slot * p.rec_rows + lane;
+                if (GQA_IN_BOUNDS(rec, (long)2 * p.chunks * p.rec_rows, p.status, kSite | 9))
+                    to = {p.ws_o + rec * kD, p.ws_ml + rec * 2};
+            } else if (lane < n_rows) {
+                const int r = sg.r0 + lane, tok = token_of(p, r), head = sg.g * p.G + r - tok * p.G;
+                const long at = sg.row0 + tok;
+                if (GQA_IN_BOUNDS(at, p.bounds.total, p.status, kSite | 10))
+                    to = {p.o + at * p.o_stride + head * kD,
+                          p.lse ? p.lse + (long)head * p.bounds.total + at : nullptr};
+            }
+            reinterpret_cast<Place *>(smem + L::kPlaces)[k % L::kFactorSlots * L::kTeamRows + lane] = to;
+        }
+        if (!warp_wait(&bars->q_raw, k & 1)) {
+            expired(p.status, kRoleQueries, 2, k);
+            return;
+        }
+        // two rows at a time: half a warp has a row, 8 dims per lane
         const int half = lane >> 4, c = lane & 15;
-#pragma unroll 1
-        for (int i0 = 0; i0 < L::kTeamRows; i0 += 16) {
-            uint4 w[8];
+#pragma unroll 2
+        for (int i0 = 0; i0 < L::kTeamRows; i0 += 2) {
+            const int row = i0 + half, n = row % kRows;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row < n_rows) w = *reinterpret_cast<const uint4 *>(smem + L::kRaw + row * kD * 2 + 16 * c);
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+            uint32_t most = 0;         // (magnitudes compare as their bits do, NaN above all)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int n = i0 + 2 * i + half, r = sg.r0 + n, t = token_of(p, r);
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (n < rows && GQA_IN_BOUNDS(sg.row0 + t, p.bounds.total, p.status, kSite | 8))
-                    w[i] = __ldg(reinterpret_cast<const uint4 *>(
-                        p.q + (long)(sg.row0 + t) * p.q_stride + (sg.g * p.G + r - t * p.G) * kD + 8 * c));
+            for (int e = 0; e < 4; ++e)
+                most = max(most, max(words[e] << 16 & 0x7fffffffu, words[e] & 0x7fff0000u));
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1)
+                most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+            const uint32_t ex = max(most >> 23, 8u);
+            const float up = __uint_as_float((261 - ex) << 23);   // 2^(7 - exponent)
+            uint32_t h[2] = {0, 0}, l[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = bf16lo(words[e]) * up, x1 = bf16hi(words[e]) * up;
+                const uint32_t y = to_e4m3x2(x0, x1), back = e4m3x2_f16x2(y);
+                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                h[e >> 1] |= y << (16 * (e & 1));
+                l[e >> 1] |= to_e4m3x2((x0 - z.x) * 16.f, (x1 - z.y) * 16.f) << (16 * (e & 1));
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                uint32_t most = 0;     // (magnitudes compare as their bits do, NaN above all)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    most = max(most, max(words[e] << 16 & 0x7fffffffu, words[e] & 0x7fff0000u));
-#pragma unroll
-                for (int d = 1; d < 16; d <<= 1)
-                    most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-                const uint32_t ex = max(most >> 23, 8u);
-                const float up = __uint_as_float((261 - ex) << 23);   // 2^(7 - exponent)
-                uint32_t h[2] = {0, 0}, l[2] = {0, 0};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x0 = bf16lo(words[e]) * up, x1 = bf16hi(words[e]) * up;
-                    const uint32_t y = to_e4m3x2(x0, x1), back = e4m3x2_f16x2(y);
-                    const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-                    h[e >> 1] |= y << (16 * (e & 1));
-                    l[e >> 1] |= to_e4m3x2((x0 - z.x) * 16.f, (x1 - z.y) * 16.f) << (16 * (e & 1));
-                }
-                // row n of its group: h in the tile's row 16 g + n, l in row 16 g + 8 + n; a row
-                // with an infinity or NaN: NaN
-                const int row = i0 + 2 * i + half, n = row % kRows;
-                uint8_t *at = tile + (row / kRows * kScoreCols + n) * kD + ((c >> 1 ^ n) << 4) + 8 * (c & 1);
-                *reinterpret_cast<uint2 *>(at) =
-                    ex == 255 ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : make_uint2(h[0], h[1]);
-                *reinterpret_cast<uint2 *>(at + kRows * kD) = make_uint2(l[0], l[1]);
-                if (c == 0) factors[row] = __uint_as_float((ex - 7) << 23) * p.scale_log2;
-            }
+            // row n of its group: h in the tile's row 16 g + n, l in row 16 g + 8 + n; a row with an
+            // infinity or NaN: NaN
+            uint8_t *at = tile + (row / kRows * kScoreCols + n) * kD + ((c >> 1 ^ n) << 4) + 8 * (c & 1);
+            *reinterpret_cast<uint2 *>(at) =
+                ex == 255 ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : make_uint2(h[0], h[1]);
+            *reinterpret_cast<uint2 *>(at + kRows * kD) = make_uint2(l[0], l[1]);
+            if (c == 0) factors[row] = __uint_as_float((ex - 7) << 23) * p.scale_log2;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -342,6 +372,8 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         if (lane == 0) mbar_arrive(&bars->seg_free[slot]);
         if (sg.stages < 0) return;
         const int first_row = sg.r0 + kRows * member;
+        const Place *places = reinterpret_cast<const Place *>(smem + L::kPlaces) +
+                              k % L::kFactorSlots * L::kTeamRows;
         const int rows = max(0, min(kRows, sg.T * p.G - first_row));   // none: no weights, O unread
         const int q_first = sg.S - sg.T;          // keys beyond are hidden from some
         const int lo = p.window > 0 ? max(0, q_first - p.window + 1) : 0;
@@ -593,8 +625,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                 if (lane == 0) bars->nan_any[group][turn] = 0;
             }
             // a warp adds up a row, 4 dims per lane
-            const int row0 = sg.r0 + warp;
-            if (warp < L::kTeamRows && row0 < sg.T * p.G) {
+            if (warp < L::kTeamRows && sg.r0 + warp < sg.T * p.G) {
                 float2 x[L::kTeams];
                 float M = -CUDART_INF_F, sum = 0.f;
 #pragma unroll
@@ -617,24 +648,16 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                     acc.z = fmaf(y.z, f, acc.z);
                     acc.w = fmaf(y.w, f, acc.w);
                 }
-                if (sg.slot >= 0) {
-                    const size_t rec = (size_t)sg.slot * p.rec_rows + warp;
-                    if (GQA_IN_BOUNDS(rec, (long)2 * p.chunks * p.rec_rows, p.status, kSite | 9)) {
-                        reinterpret_cast<float4 *>(p.ws_o + rec * kD)[lane] = acc;
-                        if (lane == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(M, sum);
-                    }
-                } else {
-                    const int tok = token_of(p, row0), head = sg.g * p.G + row0 - tok * p.G;
-                    const long at = sg.row0 + tok;
-                    if (GQA_IN_BOUNDS(at, p.bounds.total, p.status, kSite | 10)) {
-                        const float inv = 1.0f / sum;
-                        reinterpret_cast<uint2 *>(p.o + at * p.o_stride + head * kD)[lane] =
-                            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                                       pack_bf16x2(acc.z * inv, acc.w * inv));
-                        if (p.lse && lane == 0)
-                            p.lse[(long)head * p.bounds.total + at] =
-                                (M + __log2f(sum)) * 0.69314718055994531f;
-                    }
+                const Place to = places[warp];
+                if (to.o && sg.slot >= 0) {
+                    reinterpret_cast<float4 *>(to.o)[lane] = acc;
+                    if (lane == 0) *reinterpret_cast<float2 *>(to.sum) = make_float2(M, sum);
+                } else if (to.o) {
+                    const float inv = 1.0f / sum;
+                    reinterpret_cast<uint2 *>(to.o)[lane] = make_uint2(
+                        pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                    if (to.sum && lane == 0)
+                        *reinterpret_cast<float *>(to.sum) = (M + __log2f(sum)) * 0.69314718055994531f;
                 }
             }
             __syncwarp();
@@ -647,32 +670,17 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         if ((lane & 3) == 0) sums[row * kConsumers + cw] = l[0];
         if (any(!ok)) return fail(2, k);
         if (lane < kRows) {
-            // A row's factors and where it goes.  O relative to m: times 2^(mo - 12 - m), in two
-            // steps as that may be 2^-138.
+            // A row's factors.  O relative to m: times 2^(mo - 12 - m), in two steps as that may be
+            // 2^-138.
             const float4 s = *reinterpret_cast<const float4 *>(sums + lane * kConsumers);
             const float sum = (s.x + s.y) + (s.z + s.w);
-            const float f = mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift - m));
-            const int n = first_row + lane;
-            uint64_t to = 0;
-            if (lane < rows && sg.slot >= 0) {
-                const size_t rec = (size_t)sg.slot * p.rec_rows + kRows * member + lane;
-                if (GQA_IN_BOUNDS(rec, (long)2 * p.chunks * p.rec_rows, p.status, kSite | 9)) {
-                    to = reinterpret_cast<uint64_t>(p.ws_o + rec * kD);
-                    if (cw == 0) reinterpret_cast<float2 *>(p.ws_ml)[rec] = make_float2(m, sum);
-                }
-            } else if (lane < rows) {
-                const int tok = token_of(p, n), head = sg.g * p.G + n - tok * p.G;
-                const long at = sg.row0 + tok;
-                if (GQA_IN_BOUNDS(at, p.bounds.total, p.status, kSite | 10)) {
-                    to = reinterpret_cast<uint64_t>(p.o + at * p.o_stride + head * kD);
-                    if (p.lse && cw == 0)
-                        p.lse[(long)head * p.bounds.total + at] =
-                            (m + __log2f(sum)) * 0.69314718055994531f;
-                }
+            change[lane] = make_float2(mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift - m)),
+                                       sg.slot >= 0 ? 1.f : 1.0f / sum);
+            void *to = places[kRows * member + lane].sum;
+            if (cw == 0 && to) {
+                if (sg.slot >= 0) *reinterpret_cast<float2 *>(to) = make_float2(m, sum);
+                else *reinterpret_cast<float *>(to) = (m + __log2f(sum)) * 0.69314718055994531f;
             }
-            rowf[lane] = make_float4(f, sg.slot >= 0 ? 1.f : 1.0f / sum,
-                                     __uint_as_float(static_cast<uint32_t>(to)),
-                                     __uint_as_float(static_cast<uint32_t>(to >> 32)));
         }
         if (!products_done()) ok = false;
         __syncwarp();
@@ -686,9 +694,9 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         const bool nans = *const_cast<volatile int *>(&bars->nan_any[group][turn]) != 0;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            const float4 f = rowf[r];
-            const uint64_t to = static_cast<uint64_t>(__float_as_uint(f.w)) << 32 | __float_as_uint(f.z);
-            if (to == 0) continue;
+            const float2 f = change[r];
+            void *to = places[kRows * member + r].o;
+            if (!to) continue;
             float x = (__uint_as_float(a[r]) + (__uint_as_float(b[r]) + __uint_as_float(c[r]))) * f.x *
                       f.x * f.y;
             if (nans && nan_row(turn, kRows * member + r)[t / 32] >> (t & 31) & 1) x = CUDART_NAN_F;
@@ -735,6 +743,7 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
         for (int i = 0; i < 2; ++i) mbar_init(&bars->drained[i], 1);
         mbar_init(&bars->gathered, L::kGroups * kConsumers);
         mbar_init(&bars->taken, L::kGroups * kConsumers);
+        mbar_init(&bars->q_raw, 1);
         mbar_init(&bars->clc_full, 1);
         fence_mbar_init();
     }

@@ -36,7 +36,7 @@ template <int TEAM, bool SHARE>   // groups of a team; the teams take a pair's s
 struct Q8Stream {
     static constexpr bool kQ8 = true;
     static constexpr int kGroups = 4, kTeams = kGroups / TEAM, kEnds = SHARE ? 1 : kTeams;
-    static constexpr int kUnit = 128, kStages = SHARE || TEAM == 4 ? 5 : 6, kSegSlots = 8;
+    static constexpr int kUnit = 128, kStages = 5, kSegSlots = 8;
     static constexpr int kProducer = kGroups * kConsumers, kThreads = 32 * (kProducer + 4);
     __device__ static int full_of(int, int) { return 0; }
 };
