@@ -307,16 +307,17 @@ class PagedQ8:
         self.q[:first] = math.nan
         self.q[self.cu[-1]:] = math.nan
         self.kq, self.vq, self.sc, self.table = q8.pools(len(t), s, Hkv, page, D, gen)
-        self.rows = []
-        for i, n in enumerate(s):
-            x = []
-            for _ in range(2):
-                y = _randn(gen, n, Hkv, D)
-                # powers of two of their own for every vector, over `spread` binades
-                up = torch.randint(0, spread + 1, (n, Hkv, 1), generator=gen).cuda() - spread
-                x += list(q8.quantise(y.double() * torch.exp2(up.double())))
-            self.rows.append(x)          # key numbers, key bytes, value numbers, value bytes
-            self.put(i)
+        n, x = sum(s), []
+        for _ in range(2):
+            y = _randn(gen, n, Hkv, D)
+            # powers of two of their own for every vector, over `spread` binades
+            up = torch.randint(0, spread + 1, (n, Hkv, 1), generator=gen).cuda() - spread
+            x += list(q8.quantise(y.double() * torch.exp2(up.double())))
+        # of each sequence: key numbers, key bytes, value numbers, value bytes
+        self.rows = [list(parts) for parts in zip(*(y.split(s) for y in x))]
+        seq = torch.repeat_interleave(torch.arange(len(s)), torch.tensor(s)).cuda()
+        at = torch.cat([torch.arange(n) for n in s]).cuda()
+        self.write(self.table.long()[seq, at // page], at % page, x)
         self.max_q, self.max_kv = max_q or max(t), max_kv or max(s)
         self.cu_d, self.s_d = pu.i32(self.cu), pu.i32(s)
         self.cache = q8.cache_of(self.kq, self.vq, self.sc, self.table, self.s_d)
@@ -327,11 +328,13 @@ class PagedQ8:
         self.o = torch.full((self.total, Hq * D + 8), -7.0, dtype=torch.bfloat16, device="cuda")
         self.L = torch.full((Hq, self.total), -7.0, device="cuda")
 
+    def write(self, pg, slot, x):
+        self.kq[pg, :, slot], self.vq[pg, :, slot] = x[0], x[2]
+        self.sc[pg, :, slot, 0], self.sc[pg, :, slot, 1] = x[1], x[3]
+
     def put(self, i):
         n = self.rows[i][0].shape[0]
-        pg, slot = q8.places(self.table, i, self.page, torch.arange(n, device="cuda"))
-        self.kq[pg, :, slot], self.vq[pg, :, slot] = self.rows[i][0], self.rows[i][2]
-        self.sc[pg, :, slot, 0], self.sc[pg, :, slot, 1] = self.rows[i][1], self.rows[i][3]
+        self.write(*q8.places(self.table, i, self.page, torch.arange(n, device="cuda")), self.rows[i])
 
     def run(self, window=0, scale=D ** -0.5, stream=None):
         gqa.gqa_attn_paged_q8(self.q, self.Hq * D, self.cache, self.cu_d, len(self.t), self.total,

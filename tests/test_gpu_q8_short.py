@@ -29,9 +29,9 @@ def _lens(t, most=512):
     return [max(n, 1 + (37 * i) % most) for i, n in enumerate(t)]
 
 
-@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (3, 1), (1, 1), (4, 2)])
-@pytest.mark.parametrize("page", [16, 32, 64, 128])
-@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("Hq,Hkv,page,window", [
+    (8, 1, 16, 0), (8, 1, 64, 70), (3, 1, 16, 70), (3, 1, 128, 0), (1, 1, 32, 70), (1, 1, 128, 70),
+    (4, 2, 32, 0), (4, 2, 64, 0)])
 def test_decode(Hq, Hkv, page, window):
     t = [0 if i % 11 == 5 else 1 for i in range(N)]
     _paged(t, _lens(t), Hq, Hkv, page, window, 700 + Hq + page, first=2, behind=3,
