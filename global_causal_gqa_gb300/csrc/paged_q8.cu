@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kRows = 8;             // of a group
 constexpr int kScoreTiles = 2;       // of a team, in tensor memory
+constexpr int kWeightTiles = 2;      // of a team, in shared memory
 constexpr int kScoreCols = 2 * kRows, kValueCols = 3 * kRows;   // columns of a group
 constexpr float kGrow = 3.0f, kShift = 12.0f, kLargest = 32768.0f;   // log2 units; 2^(3 + 12)
 // Values below 2^-100 count as 2^-100 in mo, so that 2^(m - mo) stays within fp32.
@@ -47,7 +48,7 @@ constexpr float kLeast = -100.0f;
 struct Q8Bars : StreamBars {
     uint64_t q_full[4], q_free[4], q_raw;
     uint64_t s_full[4][kScoreTiles], s_free[4][kScoreTiles];   // of a team
-    uint64_t p_full[4], pv_done[4];
+    uint64_t p_full[4][kWeightTiles], pv_done[4][kWeightTiles];   // of a team
     uint64_t gathered, taken;        // the teams' shares of a pair: written; read
     uint64_t drained[2];
     float2 share[4][8];              // (m, l) of a group's rows
@@ -82,8 +83,8 @@ struct Layout {
     static constexpr int kQuery = kScoreN * kD, kWeights = kValueN * kD;   // bytes of a tile
     static constexpr int kQ = S::kStages * kStageBytes;
     static constexpr int kP = kQ + kQuerySlots * kQuery;
-    static constexpr int kScales = kP + kTeams * kWeights;        // two bytes per key of a stage
-    static constexpr int kRowFactors = kScales + S::kStages * 2 * S::kUnit;   // float4 [warp][row]
+    static constexpr int kScales = kP + kTeams * kWeightTiles * kWeights;        // two bytes per key of a stage
+    static constexpr int kRowFactors = kScales + S::kStages * 2 * S::kUnit;   // float4 [warp][8]
     static constexpr int kChanges = kRowFactors + kGroups * kConsumers * kRows * 16;   // float2
     static constexpr int kMost = kChanges + kGroups * kConsumers * kRows * 8;          // float2
     static constexpr int kSums = kMost + kGroups * kConsumers * kRows * 8;   // float [group][row][warp]
@@ -299,7 +300,7 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
     const uint64_t vd0 = sdesc_sw128(ring + (!p.joint ? kTileBytes : p.v_first ? 0 : 1024), 16, step);
     const uint64_t pd0 = sdesc_sw128(ring + L::kP, 16, 1024);
     constexpr uint32_t idesc = idesc_f8_f32(128, L::kValueN, 1, 1);
-    uint32_t parity = 0;               // of each team's weights, a bit each
+    uint32_t parity = 0, next = 0;     // of each team's tiles of weights, a bit each; its next tile
     for (int k = 0, u = 0;; ++k) {
         const int slot = k % kSegSlots;
         if (!mbar_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
@@ -312,10 +313,12 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
         bool ok = true;
         for (int j = 0; j < stages; ++j, ++u) {
             const int team = (SHARE ? u : k) % L::kTeams;
-            const uint64_t pd = pd0 + team * (L::kWeights >> 4);
-            ok = mbar_wait(&bars->p_full[team], parity >> team & 1);
+            const int tile = next >> team & 1, at = team * kWeightTiles + tile;
+            const uint64_t pd = pd0 + at * (L::kWeights >> 4);
+            ok = mbar_wait(&bars->p_full[team][tile], parity >> at & 1);
             if (!ok) break;
-            parity ^= 1u << team;
+            parity ^= 1u << at;
+            next ^= 1u << team;
             tc_fence_after();
             const int st = u % kStages;
             const uint64_t vd = vd0 + st * (kStageBytes >> 4);
@@ -323,7 +326,7 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
             for (int kk = 0; kk < 4; ++kk)
                 umma_f8_ss(tmem + L::kOutputs + team * L::kValueN, vd + kk * (step >> 2), pd + 2 * kk,
                            idesc, kk > 0 || j >= (SHARE ? L::kTeams : 1));
-            umma_commit(&bars->pv_done[team]);
+            umma_commit(&bars->pv_done[team][tile]);
             umma_commit(&bars->empty[st]);
         }
         if (!ok) {
@@ -345,11 +348,12 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
     const int t = 32 * cw + lane;      // the thread's key of a stage, and its dim of the outputs
     tmem += static_cast<uint32_t>(32 * cw) << 16;
     const uint32_t outputs = tmem + L::kOutputs + team * L::kValueN + member * kValueCols;
+    // factors and -m of two rows each, and then the products' factors of four
     float4 *rowf = reinterpret_cast<float4 *>(smem + L::kRowFactors) + warp * kRows;
     float2 *change = reinterpret_cast<float2 *>(smem + L::kChanges) + warp * kRows;
     float2 *most = reinterpret_cast<float2 *>(smem + L::kMost) + group * kConsumers * kRows;
     float *sums = reinterpret_cast<float *>(smem + L::kSums) + group * kRows * kConsumers;
-    uint8_t *weights = smem + L::kP + team * L::kWeights + member * kValueCols * kD;
+    uint8_t *weights = smem + L::kP + team * kWeightTiles * L::kWeights + member * kValueCols * kD;
     // (of its team's and group's barriers alone a warp sees every phase: a parity two phases back
     // reads as done, so tiles that the teams shared would be read too early)
     int scored = 0;                    // score tiles read
@@ -359,7 +363,10 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
     bool ok = true;
     auto any = [&](bool mine) { return group_any(group + 1, 32 * kConsumers, mine); };
     auto products_done = [&]() {       // of all weights handed over
-        return handed == 0 || warp_wait(&bars->pv_done[team], (handed - 1) & 1);
+        return handed == 0 || warp_wait(&bars->pv_done[team][handed - 1 & 1], (handed - 1 >> 1) & 1);
+    };
+    auto tile_read = [&]() {           // the weights that lie where the next ones go
+        return handed < kWeightTiles || warp_wait(&bars->pv_done[team][handed & 1], (handed - 2 >> 1) & 1);
     };
     auto fail = [&](int barrier, int n) { expired(p.status, kRoleConsumer, barrier, n); };
 #pragma unroll 1
@@ -421,8 +428,15 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_free[team][si]);
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
-                    y[r] = fmaf(__uint_as_float(s[kRows + r]), kl, __uint_as_float(s[r]) * kf);
+                for (int r = 0; r < kRows; r += 2) {
+                    const float2 h = make_float2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])),
+                                 lo16 = make_float2(__uint_as_float(s[kRows + r]),
+                                                    __uint_as_float(s[kRows + r + 1])),
+                                 x = __ffma2_rn(lo16, make_float2(kl, kl),
+                                                __fmul2_rn(h, make_float2(kf, kf)));
+                    y[r] = x.x;
+                    y[r + 1] = x.y;
+                }
                 if (edge) {
 #pragma unroll
                     for (int r = 0; r < kRows; ++r)
@@ -461,9 +475,11 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                                             mo == -CUDART_INF_F ? 1.f : ex2_approx(mo - mno));
                             m = mn;
                             mo = mno;
-                            rowf[lane] = make_float4(
-                                factors[lane], -fmaxf(mn, -3.0e38f),
-                                mn == -CUDART_INF_F ? 0.f : ex2_approx(mn - mno + kShift), 0.f);
+                            float *mine = reinterpret_cast<float *>(rowf + lane / 2) + (lane & 1);
+                            mine[0] = factors[lane];
+                            mine[2] = -fmaxf(mn, -3.0e38f);
+                            reinterpret_cast<float *>(rowf + kRows / 2)[lane] =
+                                mn == -CUDART_INF_F ? 0.f : ex2_approx(mn - mno + kShift);
                             if (!SHARE && fresh && cw == 0 && bars->nan_any[group][turn ^ 1]) {
                                 // the last pair's bits have been read
                                 *reinterpret_cast<uint4 *>(nan_row(turn ^ 1, kRows * member + lane)) =
@@ -493,41 +509,50 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                     }
                     float top = -CUDART_INF_F, largest = 0.f;
 #pragma unroll
-                    for (int r = 0; r < kRows; r += 2) {
-                        float x[2];
+                    for (int r = 0; r < kRows; r += 4) {
+                        const float4 z = rowf[kRows / 2 + r / 4];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float4 f = rowf[r + i];
-                            x[i] = fmaf(y[r + i], f.x, f.y);
-                            w[r + i] = ex2_approx(x[i]);
-                            pw[r + i] = w[r + i] * f.z * vf;
+                        for (int i = r; i < r + 4; i += 2) {
+                            const float4 f = rowf[i / 2];
+                            const float2 x = __ffma2_rn(make_float2(y[i], y[i + 1]), make_float2(f.x, f.y),
+                                                        make_float2(f.z, f.w));
+                            w[i] = ex2_approx(x.x);
+                            w[i + 1] = ex2_approx(x.y);
+                            const float2 b = __fmul2_rn(
+                                __fmul2_rn(make_float2(w[i], w[i + 1]),
+                                           i == r ? make_float2(z.x, z.y) : make_float2(z.z, z.w)),
+                                make_float2(vf, vf));
+                            pw[i] = b.x;
+                            pw[i + 1] = b.y;
+                            top = fmax3(top, x.x, x.y);
+                            largest = fmax3(largest, b.x, b.y);
                         }
-                        top = fmax3(top, x[0], x[1]);
-                        largest = fmax3(largest, pw[r], pw[r + 1]);
                     }
                     if (update || !any(top > kGrow || largest > kLargest || !ok)) break;
                     update = true;
                 }
                 // ---- P, a byte per column, row and key
-                if (!products_done()) ok = false;           // the last ones have been read
+                if (!tile_read()) ok = false;
                 if (edge) {
                     // (a hidden key's value may have a NaN for a power)
 #pragma unroll
                     for (int r = 0; r < kRows; ++r)
                         if (hidden >> r & 1) pw[r] = 0.f;
                 }
+                uint8_t *to = weights + (handed & 1) * L::kWeights;
 #pragma unroll
                 for (int r = 0; r < kRows; r += 2) {
-                    l[r] += w[r];
-                    l[r + 1] += w[r + 1];
+                    const float2 lr = __fadd2_rn(make_float2(l[r], l[r + 1]), make_float2(w[r], w[r + 1]));
+                    l[r] = lr.x;
+                    l[r + 1] = lr.y;
                     const __half2 x = __floats2half2_rn(pw[r], pw[r + 1]);
                     const uint32_t c = *reinterpret_cast<const uint32_t *>(&x) & 0xff00ff00u;
                     const __half2 x1 = __hsub2(x, *reinterpret_cast<const __half2 *>(&c));
                     const uint32_t d = *reinterpret_cast<const uint32_t *>(&x1) & 0xff00ff00u;
                     const __half2 x2 = __hsub2(x1, *reinterpret_cast<const __half2 *>(&d));
                     const uint32_t f = to_e5m2x2(x2);
-                    uint8_t *at = weights + r * kD + (t ^ (r << 4));
-                    uint8_t *at1 = weights + (r + 1) * kD + (t ^ (r + 1 << 4));
+                    uint8_t *at = to + r * kD + (t ^ (r << 4));
+                    uint8_t *at1 = to + (r + 1) * kD + (t ^ (r + 1 << 4));
                     at[0] = static_cast<uint8_t>(c >> 8);
                     at1[0] = static_cast<uint8_t>(c >> 24);
                     at[kRows * kD] = static_cast<uint8_t>(d >> 8);
@@ -538,7 +563,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
             } else {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_free[team][si]);
-                if (!products_done()) ok = false;          // (sees every phase)
+                if (!tile_read()) ok = false;              // (sees every phase)
             }
             // ---- values that the mask hides: 0 * NaN is NaN
             if (edge && member == 0) {
@@ -574,7 +599,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[team]);
+            if (lane == 0) mbar_arrive(&bars->p_full[team][handed & 1]);
             ++handed;
             fresh = false;
         }
@@ -736,8 +761,10 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
                 mbar_init(&bars->s_full[g][i], 2);
                 mbar_init(&bars->s_free[g][i], TEAM * kConsumers);
             }
-            mbar_init(&bars->p_full[g], TEAM * kConsumers);
-            mbar_init(&bars->pv_done[g], 1);
+            for (int i = 0; i < kWeightTiles; ++i) {
+                mbar_init(&bars->p_full[g][i], TEAM * kConsumers);
+                mbar_init(&bars->pv_done[g][i], 1);
+            }
             for (int i = 0; i < 2; ++i) bars->nan_any[g][i] = 0;
         }
         for (int i = 0; i < 2; ++i) mbar_init(&bars->drained[i], 1);
@@ -748,7 +775,7 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
         fence_mbar_init();
     }
     // columns of P that no weight is written to, and the NaN bits
-    for (int i = threadIdx.x; i < L::kTeams * L::kWeights / 16; i += S::kThreads)
+    for (int i = threadIdx.x; i < L::kTeams * kWeightTiles * L::kWeights / 16; i += S::kThreads)
         reinterpret_cast<uint4 *>(smem + L::kP)[i] = make_uint4(0, 0, 0, 0);
     for (int i = threadIdx.x; i < L::kTeams * 2 * L::kTeamRows; i += S::kThreads)
         reinterpret_cast<uint4 *>(smem + L::kNan)[i] = make_uint4(0, 0, 0, 0);
@@ -845,8 +872,11 @@ int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, const Plan &pla
 bool paged_q8_counts_fit(int nseq, int total, int max_q, int max_kv, int Hq, int Hkv) {
     const Plan plan = plan_of(max_q, Hq, Hkv);
     if (plan.team)
+        // (in the cut a pair's end counts as 6 units at most)
         return (long)Hkv * plan.blocks <= 0x7fffffffL &&
-               paged_decode_counts_fit(nseq, max_kv, Hkv * plan.blocks);
+               paged_decode_counts_fit(nseq, max_kv, Hkv * plan.blocks) &&
+               (long)nseq * Hkv * plan.blocks * ((max_kv - 1) / kStreamUnit + 1 + 6) <=
+                   0x7fffffffL - 2 * kSMs;
     return paged_expand_counts_fit(nseq, max_kv, Hkv) &&
            packed_prefill_counts_fit(nseq, total, max_kv, Hq, Hkv);
 }

@@ -28,6 +28,7 @@ struct FewStream {
     static constexpr bool kQ8 = true;
     static constexpr int kUnit = 128, kStages = 5, kSegSlots = 4, kTeams = 2, kEnds = BOTH ? 1 : 2;
     static constexpr int kProducer = kTeams * kConsumers, kThreads = 32 * (kProducer + 1);
+    static constexpr int kEndCost = 4;
     // the barrier of a stage's load: its group's, so that a group sees every phase of its own
     __device__ static int full_of(int turn, int j) { return (BOTH ? j : turn) % kTeams; }
 };

@@ -25,10 +25,14 @@ constexpr int kScaleCopies = 16;                // lanes that copy an 8-bit stag
 
 // What the kernels differ in.  kUnit: keys of a stage.  kStages: of the ring.  kTeams: groups of
 // consumers, or teams of groups, that take the pairs in turn.  kEnds: records of the end.  kProducer:
-// the producer's warp.  full_of: which of its barriers a stage's load completes.
+// the producer's warp.  full_of: which of its barriers a stage's load completes.  kEndCost: units
+// that a pair's end counts as when the batch is cut (24 caches of 700-6000 tokens, 8 KV heads: 16 to
+// 48 rows 99.5 us at 0, 88 to 92 at 3 to 8; 16 rows 67 at 0, 53 at 6; 8 rows 65 us for windows of 2048
+// at 0, 61 at 4).
 struct Bf16Stream {
     static constexpr bool kQ8 = false;
     static constexpr int kUnit = 64, kStages = 6, kSegSlots = 4, kTeams = 2, kEnds = kTeams;
+    static constexpr int kEndCost = 0;
     static constexpr int kProducer = kTeams * kConsumers, kThreads = 32 * (kProducer + 1);
     __device__ static int full_of(int turn, int) { return turn % kTeams; }
 };
@@ -37,6 +41,7 @@ struct Q8Stream {
     static constexpr bool kQ8 = true;
     static constexpr int kGroups = 4, kTeams = kGroups / TEAM, kEnds = SHARE ? 1 : kTeams;
     static constexpr int kUnit = 128, kStages = 5, kSegSlots = 8;
+    static constexpr int kEndCost = TEAM == 4 ? 4 : 6;
     static constexpr int kProducer = kGroups * kConsumers, kThreads = 32 * (kProducer + 4);
     __device__ static int full_of(int, int) { return 0; }
 };
@@ -218,7 +223,7 @@ __device__ __forceinline__ void scan_units(const Params &p, StreamBars *bars) {
         for (int i = s0; i < s0 + m && i < p.nseq; ++i) {
             const PackedSeq s = packed_seq(p.cu, p.kv_lens, i, p.bounds, p.status);
             const int n = count_units<S::kUnit>(s, p.window);
-            mine += p.Hkv * blocks_of<S>(p, s.T) * n;
+            mine += p.Hkv * blocks_of<S>(p, s.T) * (n > 0 ? n + S::kEndCost : 0);
             most = max(most, n);
         }
 #pragma unroll
@@ -300,7 +305,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         int first = 32 * m * w, incl;
         while (true) {
             load_items(first);
-            incl = s_units * s_heads;
+            incl = (s_units > 0 ? s_units + S::kEndCost : 0) * s_heads;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, incl, d);
@@ -313,11 +318,20 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         }
         const uint32_t behind = __ballot_sync(0xffffffffu, before + incl > pos);
         at = behind ? __ffs(behind) - 1 : 31;
-        const int n = max(1, __shfl_sync(0xffffffffu, s_units, at));
+        const int n = max(1, __shfl_sync(0xffffffffu, s_units, at)) + S::kEndCost;
         const int heads = S::kQ8 ? __shfl_sync(0xffffffffu, s_heads, at) : s_heads;
         const int rel = pos - before - (__shfl_sync(0xffffffffu, incl, at) - n * heads);
         head = rel / n;
         in = rel - head * n;
+        if (S::kEndCost > 0 && in >= n - S::kEndCost) {   // within a pair's end: from the next one on
+            pos += n - in;
+            run = max(0, run - (n - in));
+            in = 0;
+            if (++head == heads) {
+                head = 0;
+                ++at;
+            }
+        }
     };
     int claims = 0;
     // Claims chunks until one has work; run = 0: there is none.
@@ -387,6 +401,10 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         }
         in += sg.stages;
         if (in == n) {
+            if (S::kEndCost > 0 && !p.whole) {
+                run = max(0, run - S::kEndCost);
+                pos += S::kEndCost;
+            }
             in = 0;
             if (++head == heads) {
                 head = 0;
