@@ -38,9 +38,11 @@ using namespace stream;
 namespace {
 
 constexpr int kRows = 8;             // of a group
+constexpr int kStreamUnit = 128;
 constexpr int kScoreTiles = 2;       // of a team, in tensor memory
 constexpr int kWeightTiles = 2;      // of a team, in shared memory
 constexpr int kScoreCols = 2 * kRows, kValueCols = 3 * kRows;   // columns of a group
+constexpr int kChunk = 16 * kStreamUnit;      // bytes of 16 columns of the weights
 constexpr float kGrow = 3.0f, kShift = 12.0f, kLargest = 32768.0f;   // log2 units; 2^(3 + 12)
 // Values below 2^-100 count as 2^-100 in mo, so that 2^(m - mo) stays within fp32.
 constexpr float kLeast = -100.0f;
@@ -109,6 +111,13 @@ __device__ __forceinline__ bool group_any(int id, int threads, bool mine) {
         : "r"(static_cast<uint32_t>(mine)), "r"(id), "r"(threads)
         : "memory");
     return r != 0;
+}
+
+// Two f16 numbers less their upper bytes as such, exactly.
+__device__ __forceinline__ uint32_t less_upper(uint32_t x) {
+    const uint32_t u = x & 0xff00ff00u;
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&u));
+    return *reinterpret_cast<const uint32_t *>(&y);
 }
 
 // Bytes of a stage from 8 keys (or values) to the next 8.
@@ -249,7 +258,7 @@ __device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint
     const uint32_t ring = smem_u32(smem);
     const uint64_t kd0 = sdesc_sw128(ring + (p.joint && p.v_first ? 1024 : 0), 16, key_step(p));
     const uint64_t qd0 = sdesc_sw128(ring + L::kQ, 16, 1024);
-    constexpr uint32_t idesc = idesc_f8_f32(128, L::kScoreN, 0, 0);
+    constexpr uint32_t idesc = idesc_f8_f32(128, L::kScoreN, 0, 0, 0);
     uint32_t counts = 0;               // scores of each team's stages, mod 256
     for (int k = 0, u = 0;; ++k) {
         const int slot = k % kSegSlots, b = k % L::kQuerySlots;
@@ -298,8 +307,8 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
     constexpr int kStages = L::S::kStages, kSegSlots = L::S::kSegSlots;
     const uint32_t ring = smem_u32(smem), step = key_step(p);
     const uint64_t vd0 = sdesc_sw128(ring + (!p.joint ? kTileBytes : p.v_first ? 0 : 1024), 16, step);
-    const uint64_t pd0 = sdesc_sw128(ring + L::kP, 16, 1024);
-    constexpr uint32_t idesc = idesc_f8_f32(128, L::kValueN, 1, 1);
+    const uint64_t pd0 = sdesc_mn(ring + L::kP, 128, kChunk);
+    constexpr uint32_t idesc = idesc_f8_f32(128, L::kValueN, 1, 1, 1);
     uint32_t parity = 0, next = 0;     // of each team's tiles of weights, a bit each; its next tile
     for (int k = 0, u = 0;; ++k) {
         const int slot = k % kSegSlots;
@@ -324,7 +333,7 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
             const uint64_t vd = vd0 + st * (kStageBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                umma_f8_ss(tmem + L::kOutputs + team * L::kValueN, vd + kk * (step >> 2), pd + 2 * kk,
+                umma_f8_ss(tmem + L::kOutputs + team * L::kValueN, vd + kk * (step >> 2), pd + 32 * kk,
                            idesc, kk > 0 || j >= (SHARE ? L::kTeams : 1));
             umma_commit(&bars->pv_done[team][tile]);
             umma_commit(&bars->empty[st]);
@@ -353,7 +362,11 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
     float2 *change = reinterpret_cast<float2 *>(smem + L::kChanges) + warp * kRows;
     float2 *most = reinterpret_cast<float2 *>(smem + L::kMost) + group * kConsumers * kRows;
     float *sums = reinterpret_cast<float *>(smem + L::kSums) + group * kRows * kConsumers;
-    uint8_t *weights = smem + L::kP + team * kWeightTiles * L::kWeights + member * kValueCols * kD;
+    // A key's weights of 8 rows, each of their three bytes together (MN-major tiles of 16 columns, so
+    // that a thread has 3 stores for 24 bytes).
+    uint8_t *weights = smem + L::kP + team * kWeightTiles * L::kWeights + t * 16 +
+                       member * kValueCols / 16 * kChunk + member * kValueCols % 16;
+    const int second = member * kValueCols % 16 == 0 ? 8 : kChunk - 8;
     // (of its team's and group's barriers alone a warp sees every phase: a parity two phases back
     // reads as done, so tiles that the teams shared would be read too early)
     int scored = 0;                    // score tiles read
@@ -539,27 +552,32 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                     for (int r = 0; r < kRows; ++r)
                         if (hidden >> r & 1) pw[r] = 0.f;
                 }
-                uint8_t *to = weights + (handed & 1) * L::kWeights;
+                uint2 c, d, f;
 #pragma unroll
-                for (int r = 0; r < kRows; r += 2) {
-                    const float2 lr = __fadd2_rn(make_float2(l[r], l[r + 1]), make_float2(w[r], w[r + 1]));
-                    l[r] = lr.x;
-                    l[r + 1] = lr.y;
-                    const __half2 x = __floats2half2_rn(pw[r], pw[r + 1]);
-                    const uint32_t c = *reinterpret_cast<const uint32_t *>(&x) & 0xff00ff00u;
-                    const __half2 x1 = __hsub2(x, *reinterpret_cast<const __half2 *>(&c));
-                    const uint32_t d = *reinterpret_cast<const uint32_t *>(&x1) & 0xff00ff00u;
-                    const __half2 x2 = __hsub2(x1, *reinterpret_cast<const __half2 *>(&d));
-                    const uint32_t f = to_e5m2x2(x2);
-                    uint8_t *at = to + r * kD + (t ^ (r << 4));
-                    uint8_t *at1 = to + (r + 1) * kD + (t ^ (r + 1 << 4));
-                    at[0] = static_cast<uint8_t>(c >> 8);
-                    at1[0] = static_cast<uint8_t>(c >> 24);
-                    at[kRows * kD] = static_cast<uint8_t>(d >> 8);
-                    at1[kRows * kD] = static_cast<uint8_t>(d >> 24);
-                    at[2 * kRows * kD] = static_cast<uint8_t>(f);
-                    at1[2 * kRows * kD] = static_cast<uint8_t>(f >> 8);
+                for (int r = 0; r < kRows; r += 4) {
+                    uint32_t x[2], x1[2], x2[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int k = r + 2 * i;
+                        const float2 lk = __fadd2_rn(make_float2(l[k], l[k + 1]),
+                                                     make_float2(w[k], w[k + 1]));
+                        l[k] = lk.x;
+                        l[k + 1] = lk.y;
+                        const __half2 y = __floats2half2_rn(pw[k], pw[k + 1]);
+                        x[i] = *reinterpret_cast<const uint32_t *>(&y);
+                        x1[i] = less_upper(x[i]);
+                        const uint32_t rest = less_upper(x1[i]);
+                        x2[i] = to_e5m2x2(*reinterpret_cast<const __half2 *>(&rest));
+                    }
+                    // the upper bytes of four, of what is left of them, and the rest
+                    (r ? c.y : c.x) = __byte_perm(x[0], x[1], 0x7531);
+                    (r ? d.y : d.x) = __byte_perm(x1[0], x1[1], 0x7531);
+                    (r ? f.y : f.x) = __byte_perm(x2[0], x2[1], 0x5410);
                 }
+                uint8_t *to = weights + (handed & 1) * L::kWeights;
+                *reinterpret_cast<uint2 *>(to) = c;
+                *reinterpret_cast<uint2 *>(to + second) = d;
+                *reinterpret_cast<uint2 *>(to + kChunk) = f;
             } else {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_free[team][si]);
@@ -808,7 +826,7 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
 struct Plan {
     int team, blocks;
 };
-constexpr int kMostBlocks = 2, kStreamUnit = 128;
+constexpr int kMostBlocks = 2;
 Plan plan_of(int max_q, int Hq, int Hkv) {
     const long n = static_cast<long>(max_q) * (Hq / Hkv);
     if (n <= kRows) return {1, 1};

@@ -287,6 +287,13 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
     return d;
 }
 
+// The same without a swizzle, for an MN-major matrix: 16 bytes of 8 rows behind one another; `rows`:
+// from 8 rows to the next 8, `chunks`: from 16 bytes to the next 16.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t rows, uint32_t chunks) {
+    return (saddr >> 4 & 0x3FFFu) | static_cast<uint64_t>(rows >> 4 & 0x3FFFu) << 16 |
+           static_cast<uint64_t>(chunks >> 4 & 0x3FFFu) << 32 | 1ull << 46;
+}
+
 // Instruction descriptor for kind::f16 with bf16 A and B and an fp32 accumulator.
 // a_mn / b_mn: 1 if that operand is MN-major (transposed), 0 if K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, int b_mn) {
@@ -298,10 +305,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, in
 }
 
 // Instruction descriptor for kind::f8f6f4 with an e4m3 A, a B of e4m3 (b_e5m2 = 0) or e5m2, and an
-// fp32 accumulator; a_mn: 1 if A is MN-major, B is K-major.
-__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, int a_mn, int b_e5m2) {
+// fp32 accumulator; a_mn, b_mn as above.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, int a_mn, int b_mn, int b_e5m2) {
     return (1u << 4)                       // D format: f32
            | (static_cast<uint32_t>(b_e5m2) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+           (static_cast<uint32_t>(b_mn) << 16) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
