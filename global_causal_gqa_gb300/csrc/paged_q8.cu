@@ -4,32 +4,38 @@
 // keys 2^a_j y_j and values 2^b_j z_j of e4m3 numbers y, z (q8.cuh):
 //   o = sum_j softmax_j(scale 2^a_j q . y_j) 2^b_j z_j  over j <= i (and i - j < W with a window).
 //
-// Up to 32 rows (tokens x heads of a KV group) per sequence: the streaming kernel below, bound by
-// memory, 258 bytes per key and KV head.  More: all keys that the call sees are expanded to bf16
-// pages in the workspace (paged_read.cu) and the tile kernel (packed_prefill.cu) takes them from
-// there.
+// By the rows (tokens x heads of a KV group) that a sequence may have: up to 8, paged_q8_few.cu, or
+// paged_q8_short.cu for many short caches; 9 to 64, the kernel below, bound by memory at 16 rows
+// (32 caches of 8k-64k tokens 437 us, 6.2 TB/s) and by its warps at 32 (603 us; blocks of 32 rows
+// read the pages again, from L2 for the most part: 24 drafts of 2-6 tokens of 8 rows 84 us).  More:
+// all keys that the call sees are expanded to bf16 pages in the workspace (paged_read.cu) and the
+// tile kernel (packed_prefill.cu) takes them from there (96 rows: 186 us so, 246 in three blocks).
 //
-// The streaming kernel is cut and fed as the bf16 one (paged_decode.cu; paged_stream.cuh), in
-// stages of 128 keys.  Its products run on tcgen05 with the numbers as they lie in the pages:
+// The kernel is cut and fed as the bf16 one (paged_decode.cu; paged_stream.cuh), in stages of 128
+// keys.  Its products run on tcgen05 with the numbers as they lie in the pages:
 //   S^T [128 keys x columns] = Y Q'^T,   O^T [128 dims x columns] += Z^T P'^T,
-// e4m3 A operands straight from the stage, so that no thread ever touches a key's number (with
-// mma.sync, whose 8-bit form is slower than its 16-bit one, the 64 conversions and 8 ldmatrix of
-// 16 keys and 8 rows alone took more than the copies; 12 rows over 700-6000 keys 88 us).  The
-// operands that are not 8-bit are sums of 8-bit columns:
+// e4m3 A operands straight from the stage, so that no thread ever touches a key's number (by
+// mma.sync, 16 rows of these caches took 575 us: the conversions alone were more than the copies).
+// The operands that are not 8-bit are sums of 8-bit columns:
 //   q 2^u = h + l / 16 (e4m3, the row's largest element brought to [2^7, 2^8)): bf16's 8 bits, but
 //     for elements below 2^-3, which lose at most 2^-14, 2^-21 of the largest;
 //   P = c + m + f (e5m2, a weight times its value's 2^b): of P in f16 the upper byte, the upper byte
 //     of what is left, and the rest rounded: off by 2^-9 + 2^-11 of P, or 2^-17.
-// A thread has one key and all rows: its key's and value's powers of two are its own, the rows'
+// A thread has one key and 8 rows: its key's and value's powers of two are its own, the rows'
 // factors are read from shared memory.  l sums the weights relative to 2^m, O the products P
 // relative to 2^(mo - 12), mo the largest score plus its value's exponent: either range alone may
 // be far from the other's.  Both references move, for all keys of a stage together, when something
 // exceeds them by 2^3, so that P stays within e5m2's range and 2^-17 is 2^-29 of its largest.
 //
-// Warps: two groups of four (softmax, a quarter of a stage's keys each; the groups take the pairs
-// in turn, so that one's ends pass while the other streams, or with 17 to 32 rows 16 of them
-// each), the producer, two that issue the products, and one that brings the queries into operands a
-// pair ahead.
+// Warps: four groups of four for the softmax (8 rows; a warp a quarter of a stage's keys), the
+// producer, one that issues the score products and one the value products (one thread for both
+// took 1500 cycles a stage), and one that brings the queries into operands a pair ahead.  Two
+// groups are a team for up to 16 rows, and the teams take the pairs in turn, so that one's ends
+// pass while the other streams, or (SHARE, where a CTA has few pairs) each pair's stages; four for
+// up to 32.  A stage of 32 rows takes 2200 cycles, of 24 nearly as many: it is a warp's own chain
+// of some 300 instructions, with five warps on a scheduler, that counts.  So the threads' stores
+// count (weights key by key, 24 bytes in 3 stores, instead of a byte per column: 671 -> 603 us),
+// and paired fp32 arithmetic.
 #include "paged_stream.cuh"
 #include "q8.cuh"
 
@@ -836,9 +842,9 @@ Plan plan_of(int max_q, int Hq, int Hkv) {
 }
 
 // The call's tensor maps, in p what they come to: {128 numbers, 8 keys, the two pools, groups of 8
-// keys, (page, KV head)}, a box of `most` keys of a page at most.  A map takes a stride from pool to pool below 2^40, and then a page's keys
-// and values come as one copy, 8 of either in turn (32 caches of 8k-64k tokens in pages of 16: 577 us
-// with two copies, 458 with one); else as two.
+// keys, (page, KV head)}, a box of `most` keys of a page at most.  A map takes a stride from pool to
+// pool below 2^40, and then a page's keys and values come as one copy, 8 of either in turn (32 caches
+// of 8k-64k tokens in pages of 16: 577 us with two copies, 449 with one); else as two.
 bool make_maps(const gqa_paged_kv_q8 &c, int most, Params &p, CUtensorMap *mk, CUtensorMap *mv) {
     const uint64_t kp = reinterpret_cast<uint64_t>(c.k), vp = reinterpret_cast<uint64_t>(c.v);
     const uint64_t apart = kp < vp ? vp - kp : kp - vp, page = c.page_size;
@@ -847,7 +853,8 @@ bool make_maps(const gqa_paged_kv_q8 &c, int most, Params &p, CUtensorMap *mk, C
     const uint32_t pools = p.joint ? 2 : 1;
     const uint64_t dims[5] = {kD, 8, pools, page / 8, (uint64_t)c.num_pages * c.Hkv};
     const uint64_t strides[4] = {kD, p.joint ? apart : kD, 8 * kD, page * kD};
-    const uint32_t box[5] = {kD, 8, pools, static_cast<uint32_t>(c.page_size < most ? page : most) / 8, 1};
+    const uint32_t box[5] = {kD, 8, pools,
+                             static_cast<uint32_t>(c.page_size < most ? page : most) / 8, 1};
     return make_byte_map(mk, p.v_first ? c.v : c.k, 5, dims, strides, box) &&
            make_byte_map(mv, c.v, 5, dims, strides, box);
 }

@@ -108,7 +108,7 @@ class LayerStack:
 @dataclass
 class PagedLayer:
     """One attention layer's caller-owned device tensors for a packed batch of `total` tokens."""
-    k_pool: object         # [num_pages, Hkv, page_size, d] bf16, keys after RoPE
+    k_pool: object         # [num_pages, Hkv, page_size, d] bf16 (or 8-bit), keys after RoPE
     v_pool: object         # the same shape
     qkv: object            # [total, (Hq + 2 Hkv) d] bf16, rows of the fused projection
     o: object              # [total, Hq, d] bf16, the attention output
@@ -123,12 +123,13 @@ class PagedLayer:
 
 class PagedStack:
     """A serving step over paged caches: per layer one gqa_packed_rope_append and one
-    gqa_attn_paged, or, for a layer with `scales`, their 8-bit forms.  cu_seqlens (int32 [nseq + 1]), kv_lens (int32 [nseq], counted with the new
-    tokens) and page_table (int32 [nseq, max_pages], used by every layer with its own pools)
-    are device tensors read when the kernels run: a captured step follows what the caller
-    writes to them between replays, up to max_q new tokens and max_kv tokens of a sequence.
-    Chunks run fastest with a max_kv near the longest sequence.  A stack has one workspace and
-    one tensor of rotated queries: its steps, eager or replayed, must not overlap."""
+    gqa_attn_paged, or, for a layer with `scales`, their 8-bit forms.  cu_seqlens (int32
+    [nseq + 1]), kv_lens (int32 [nseq], counted with the new tokens) and page_table (int32 [nseq,
+    max_pages], used by every layer with its own pools) are device tensors read when the kernels
+    run: a captured step follows what the caller writes to them between replays, up to max_q new
+    tokens and max_kv tokens of a sequence.  Chunks run fastest with a max_kv near the longest
+    sequence, which also sizes the workspace of 8-bit layers.  A stack has one workspace and one
+    tensor of rotated queries: its steps, eager or replayed, must not overlap."""
 
     def __init__(self, layers: List[PagedLayer], cu_seqlens, kv_lens, page_table, max_q: int,
                  max_kv: int, Hq: int, Hkv: int, d: int, scale: float, eps: float = 1e-6):

@@ -437,10 +437,12 @@ gqa_status gqa_packed_rope_append_q8(const void *q, int64_t q_stride, const void
                                      void *k_out, const gqa_paged_kv_q8 *cache,
                                      gqa_stream_t stream);
 
-/* As gqa_attn_paged over an 8-bit cache: the same arguments, masks, limits, flags and NaN rules,
- * applied to the numbers that the cache stands for.  gqa_attn_paged_q8_workspace_bytes sizes its
- * own workspace (with the arguments of the call), which may include room for every key that the
- * bounds allow in bf16: pass a max_kv near the longest sequence. */
+/* As gqa_attn_paged over an 8-bit cache: the same arguments, masks, limits and flags, applied to the
+ * numbers that the cache stands for.  A key that reads back as NaN makes every row that sees it NaN,
+ * a NaN value those rows' elements; a query row with an infinity or a NaN is NaN.
+ * gqa_attn_paged_q8_workspace_bytes sizes its own workspace (with the arguments of the call).  With
+ * more than 64 rows (max_q * Hq / Hkv) it has room for every key that nseq and max_kv allow in bf16:
+ * pass a max_kv near the longest sequence. */
 size_t gqa_attn_paged_q8_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
                                          int Hkv, int d);
 gqa_status gqa_attn_paged_q8(const void *q, int64_t q_stride, const gqa_paged_kv_q8 *cache,
