@@ -47,6 +47,7 @@ constexpr int kRows = 8;             // of a group
 constexpr int kStreamUnit = 128;
 constexpr int kScoreTiles = 2;       // of a team, in tensor memory
 constexpr int kWeightTiles = 2;      // of a team, in shared memory
+static_assert(kWeightTiles == kScoreTiles, "a stage's scores and weights have tiles of one number");
 constexpr int kScoreCols = 2 * kRows, kValueCols = 3 * kRows;   // columns of a group
 constexpr int kChunk = 16 * kStreamUnit;      // bytes of 16 columns of the weights
 constexpr float kGrow = 3.0f, kShift = 12.0f, kLargest = 32768.0f;   // log2 units; 2^(3 + 12)
@@ -55,7 +56,8 @@ constexpr float kLeast = -100.0f;
 
 struct Q8Bars : StreamBars {
     uint64_t q_full[4], q_free[4], q_raw;
-    uint64_t s_full[4][kScoreTiles], s_free[4][kScoreTiles];   // of a team
+    // of a team: a stage's scores are there, and the weights before its own read; the scores read
+    uint64_t s_full[4][kScoreTiles], s_free[4][kScoreTiles];
     uint64_t p_full[4][kWeightTiles], pv_done[4][kWeightTiles];   // of a team
     uint64_t gathered, taken;        // the teams' shares of a pair: written; read
     uint64_t drained[2];
@@ -126,6 +128,13 @@ __device__ __forceinline__ uint32_t less_upper(uint32_t x) {
     return *reinterpret_cast<const uint32_t *>(&y);
 }
 
+// A warp's wait for a phase that is mostly over: one test, and the loop out of line (the loops of
+// every such wait are a large part of the code, and the caches of instructions are small).
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity); }
+__device__ __forceinline__ bool quick_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_on(bar, parity);
+}
+
 // Bytes of a stage from 8 keys (or values) to the next 8.
 __device__ __forceinline__ uint32_t key_step(const Params &p) { return p.joint ? 2048 : 1024; }
 
@@ -162,7 +171,7 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
     const int lane = threadIdx.x & 31;
     for (int k = 0;; ++k) {
         const int slot = k % kSegSlots, b = k % L::kQuerySlots;
-        if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
+        if (!quick_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
             expired(p.status, kRoleQueries, 0, k);
             return;
         }
@@ -170,7 +179,7 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->seg_free[slot]);
         if (sg.stages < 0) return;
-        if (k >= L::kQuerySlots && !warp_wait(&bars->q_free[b], (k / L::kQuerySlots - 1) & 1)) {
+        if (k >= L::kQuerySlots && !quick_wait(&bars->q_free[b], (k / L::kQuerySlots - 1) & 1)) {
             expired(p.status, kRoleQueries, 1, k);
             return;
         }
@@ -207,7 +216,7 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
             }
             reinterpret_cast<Place *>(smem + L::kPlaces)[k % L::kFactorSlots * L::kTeamRows + lane] = to;
         }
-        if (!warp_wait(&bars->q_raw, k & 1)) {
+        if (!quick_wait(&bars->q_raw, k & 1)) {
             expired(p.status, kRoleQueries, 2, k);
             return;
         }
@@ -316,6 +325,9 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
     const uint64_t pd0 = sdesc_mn(ring + L::kP, 128, kChunk);
     constexpr uint32_t idesc = idesc_f8_f32(128, L::kValueN, 1, 1, 1);
     uint32_t parity = 0, next = 0;     // of each team's tiles of weights, a bit each; its next tile
+    // (no weights before a tile's first)
+    for (int i = 0; i < L::kTeams * kWeightTiles; ++i)
+        mbar_arrive(&bars->s_full[i / kWeightTiles][i % kWeightTiles]);
     for (int k = 0, u = 0;; ++k) {
         const int slot = k % kSegSlots;
         if (!mbar_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
@@ -342,6 +354,7 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
                 umma_f8_ss(tmem + L::kOutputs + team * L::kValueN, vd + kk * (step >> 2), pd + 32 * kk,
                            idesc, kk > 0 || j >= (SHARE ? L::kTeams : 1));
             umma_commit(&bars->pv_done[team][tile]);
+            umma_commit(&bars->s_full[team][tile]);   // of the stage whose weights go there next
             umma_commit(&bars->empty[st]);
         }
         if (!ok) {
@@ -382,16 +395,13 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
     bool ok = true;
     auto any = [&](bool mine) { return group_any(group + 1, 32 * kConsumers, mine); };
     auto products_done = [&]() {       // of all weights handed over
-        return handed == 0 || warp_wait(&bars->pv_done[team][handed - 1 & 1], (handed - 1 >> 1) & 1);
-    };
-    auto tile_read = [&]() {           // the weights that lie where the next ones go
-        return handed < kWeightTiles || warp_wait(&bars->pv_done[team][handed & 1], (handed - 2 >> 1) & 1);
+        return handed == 0 || quick_wait(&bars->pv_done[team][handed - 1 & 1], (handed - 1 >> 1) & 1);
     };
     auto fail = [&](int barrier, int n) { expired(p.status, kRoleConsumer, barrier, n); };
 #pragma unroll 1
     for (int k = SHARE ? 0 : team, turn = 0;; k += SHARE ? 1 : L::kTeams, turn ^= 1) {
         const int slot = k % kSegSlots;
-        if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) ok = false;
+        if (!quick_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) ok = false;
         if (any(!ok)) return fail(0, k);
         const Segment sg = bars->seg[slot];
         __syncwarp();
@@ -418,7 +428,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         for (int j = 0, u = sg.u0; j < sg.stages; ++j, ++u) {
             if (SHARE && u % L::kTeams != team) continue;
             const int st = u % kStages, si = scored % kScoreTiles;
-            if (!warp_wait(&bars->s_full[team][si], (scored / kScoreTiles) & 1)) ok = false;
+            if (!quick_wait(&bars->s_full[team][si], (scored / kScoreTiles) & 1)) ok = false;
             ++scored;
             const int kb = (sg.unit0 + j) * kUnit, key = kb + t;
             const bool edge = kb + kUnit - 1 > q_first || kb < lo_all;   // of the mask
@@ -551,7 +561,6 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                     update = true;
                 }
                 // ---- P, a byte per column, row and key
-                if (!tile_read()) ok = false;
                 if (edge) {
                     // (a hidden key's value may have a NaN for a power)
 #pragma unroll
@@ -587,7 +596,6 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
             } else {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_free[team][si]);
-                if (!tile_read()) ok = false;              // (sees every phase)
             }
             // ---- values that the mask hides: 0 * NaN is NaN
             if (edge && member == 0) {
@@ -637,7 +645,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                 if ((lane & 3) == 0) sums[row * kConsumers + cw] = l[0];
                 if (any(!ok)) return fail(2, k);
                 if (!products_done()) ok = false;
-                if (k > 0 && !warp_wait(&bars->taken, k - 1 & 1)) ok = false;
+                if (k > 0 && !quick_wait(&bars->taken, k - 1 & 1)) ok = false;
                 if (lane < kRows) {
                     const float4 s = *reinterpret_cast<const float4 *>(sums + lane * kConsumers);
                     change[lane].x = mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift - m));
@@ -661,12 +669,12 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                         x = CUDART_NAN_F;
                     shares[(group * kRows + r) * kD + t] = fresh ? 0.f : x;
                 }
-            } else if (k > 0 && !warp_wait(&bars->taken, k - 1 & 1)) {   // (sees every phase)
+            } else if (k > 0 && !quick_wait(&bars->taken, k - 1 & 1)) {   // (sees every phase)
                 ok = false;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->gathered);
-            if (!warp_wait(&bars->gathered, k & 1)) ok = false;
+            if (!quick_wait(&bars->gathered, k & 1)) ok = false;
             if (nans && cw == 0) {     // the bits have been read
                 if (lane < kRows)
                     *reinterpret_cast<uint4 *>(nan_row(turn, kRows * member + lane)) =
@@ -782,7 +790,7 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
             mbar_init(&bars->q_full[g], 1);
             mbar_init(&bars->q_free[g], 1);
             for (int i = 0; i < kScoreTiles; ++i) {
-                mbar_init(&bars->s_full[g][i], 2);
+                mbar_init(&bars->s_full[g][i], 3);
                 mbar_init(&bars->s_free[g][i], TEAM * kConsumers);
             }
             for (int i = 0; i < kWeightTiles; ++i) {
