@@ -5,11 +5,13 @@
 //   o = sum_j softmax_j(scale 2^a_j q . y_j) 2^b_j z_j  over j <= i (and i - j < W with a window).
 //
 // By the rows (tokens x heads of a KV group) that a sequence may have: up to 8, paged_q8_few.cu, or
-// paged_q8_short.cu for many short caches; 9 to 64, the kernel below, bound by memory at 16 rows
-// (32 caches of 8k-64k tokens 437 us, 6.2 TB/s) and by its warps at 32 (603 us; blocks of 32 rows
-// read the pages again, from L2 for the most part: 24 drafts of 2-6 tokens of 8 rows 84 us).  More:
+// paged_q8_short.cu for many short caches; 9 to 96, the kernel below, bound by memory at 16 rows
+// (32 caches of 8k-64k tokens 434 us, 6.3 TB/s) and by its warps at 32 (557 us; blocks of 32 rows
+// read the pages again, from L2 for the most part: 24 drafts of 2-6 tokens of 8 rows 80 us).  More:
 // all keys that the call sees are expanded to bf16 pages in the workspace (paged_read.cu) and the
-// tile kernel (packed_prefill.cu) takes them from there (96 rows: 186 us so, 246 in three blocks).
+// tile kernel (packed_prefill.cu) takes them from there (24 times 72, 96 and 128 rows over 700-6000 tokens: 184, 186
+// and 190 us so, 158, 169 and 220 in blocks; 16 to 96 rows 179 and 106; 8 times 96 over 20k-60k 605
+// and 439).
 //
 // The kernel is cut and fed as the bf16 one (paged_decode.cu; paged_stream.cuh), in stages of 128
 // keys.  Its products run on tcgen05 with the numbers as they lie in the pages:
@@ -32,10 +34,12 @@
 // took 1500 cycles a stage), and one that brings the queries into operands a pair ahead.  Two
 // groups are a team for up to 16 rows, and the teams take the pairs in turn, so that one's ends
 // pass while the other streams, or (SHARE, where a CTA has few pairs) each pair's stages; four for
-// up to 32.  A stage of 32 rows takes 2200 cycles, of 24 nearly as many: it is a warp's own chain
-// of some 300 instructions, with five warps on a scheduler, that counts.  So the threads' stores
-// count (weights key by key, 24 bytes in 3 stores, instead of a byte per column: 671 -> 603 us),
-// and paired fp32 arithmetic.
+// up to 32.  A stage of 32 rows takes 2000 cycles, of 24 nearly as many: it is a warp's own chain
+// of some 300 instructions, with five warps on a scheduler, that counts (scores out of tensor
+// memory 330 cycles, weights 450, the vote 250, their bytes 340, each wait about 150 although what
+// it waits for is there).  So the threads' stores count (weights key by key, 24 bytes in 3 stores,
+// instead of a byte per column: 32 rows 671 -> 603 us), waits (one for a stage's scores and for the
+// tile that its weights go to: 557), and paired fp32 arithmetic.
 #include "paged_stream.cuh"
 #include "q8.cuh"
 
@@ -126,13 +130,6 @@ __device__ __forceinline__ uint32_t less_upper(uint32_t x) {
     const uint32_t u = x & 0xff00ff00u;
     const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&u));
     return *reinterpret_cast<const uint32_t *>(&y);
-}
-
-// A warp's wait for a phase that is mostly over: one test, and the loop out of line (the loops of
-// every such wait are a large part of the code, and the caches of instructions are small).
-__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity); }
-__device__ __forceinline__ bool quick_wait(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_on(bar, parity);
 }
 
 // Bytes of a stage from 8 keys (or values) to the next 8.
@@ -840,7 +837,7 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
 struct Plan {
     int team, blocks;
 };
-constexpr int kMostBlocks = 2;
+constexpr int kMostBlocks = 3;
 Plan plan_of(int max_q, int Hq, int Hkv) {
     const long n = static_cast<long>(max_q) * (Hq / Hkv);
     if (n <= kRows) return {1, 1};

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(FewStream<BOTH>::kThreads, 1)
         __syncwarp();
         uint64_t *bar = &bars->merge[BOTH ? 0 : group];
         if (lane == 0) mbar_arrive(bar);
-        if (warp_wait(bar, meets++ & 1)) return true;
+        if (quick_wait(bar, meets++ & 1)) return true;
         expired(p.status, 2, meets);
         return false;
     };
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(FewStream<BOTH>::kThreads, 1)
     Segment sg;
     auto next_segment = [&](int k) {
         const int slot = k % kSegSlots;
-        if (!warp_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
+        if (!quick_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) {
             expired(p.status, 0, k);
             return false;
         }
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(FewStream<BOTH>::kThreads, 1)
         x.clear();
         for (int j = BOTH ? group : 0; j < sg.stages; j += BOTH ? kGroups : 1) {
             const int u = sg.u0 + j, st = u % kStages;
-            if (!warp_wait(&bars->full[group][st], phases >> st & 1)) {
+            if (!quick_wait(&bars->full[group][st], phases >> st & 1)) {
                 expired(p.status, 1, u);
                 return;
             }

@@ -26,9 +26,9 @@ constexpr int kScaleCopies = 16;                // lanes that copy an 8-bit stag
 // What the kernels differ in.  kUnit: keys of a stage.  kStages: of the ring.  kTeams: groups of
 // consumers, or teams of groups, that take the pairs in turn.  kEnds: records of the end.  kProducer:
 // the producer's warp.  full_of: which of its barriers a stage's load completes.  kEndCost: units
-// that a pair's end counts as when the batch is cut (24 caches of 700-6000 tokens, 8 KV heads: 16 to
-// 48 rows 99.5 us at 0, 88 to 92 at 3 to 8; 16 rows 67 at 0, 53 at 6; 8 rows 65 us for windows of 2048
-// at 0, 61 at 4).
+// that a pair's end counts as when the batch is cut (24 caches of 700-6000 tokens, 8 KV heads, before
+// other steps: 16 to 48 rows 99.5 us at 0, 88 to 92 at 3 to 8; 16 rows 67 at 0, 53 at 6; 8 rows over
+// windows of 2048 65 at 0, 61 at 4).
 struct Bf16Stream {
     static constexpr bool kQ8 = false;
     static constexpr int kUnit = 64, kStages = 6, kSegSlots = 4, kTeams = 2, kEnds = kTeams;
@@ -176,6 +176,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
+// A warp's wait for a phase that is mostly over: one test, and the loop out of line (the loops of
+// every such wait are a large part of the code, and the caches of instructions are small).
+static __device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity); }
+__device__ __forceinline__ bool quick_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_on(bar, parity);
+}
+
 __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
@@ -248,6 +255,9 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
+    auto wait = [](uint64_t *bar, uint32_t parity) {
+        return S::kQ8 ? quick_wait(bar, parity) : warp_wait(bar, parity);
+    };
     bool ok = true;
     int u = 0;   // stages issued
     uint32_t owner = 0, phases = 0;   // a place's last group; bits 8 group + place: full's
@@ -344,7 +354,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
                 mbar_arrive_expect_tx(&bars->clc_full, 16);
                 clc_try_cancel(&bars->clc_resp, &bars->clc_full);
             }
-            if (!warp_wait(&bars->clc_full, claims++ & 1)) {
+            if (!wait(&bars->clc_full, claims++ & 1)) {
                 set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 3, claims);
                 ok = false;
                 return;
@@ -425,7 +435,7 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         const int records = ahead.stages < 0 ? S::kEnds : 1;
         for (int i = 0; i < records; ++i, ++k) {
             const int slot = k & (kSegSlots - 1);
-            if (k >= kSegSlots && !warp_wait(&bars->seg_free[slot], (k / kSegSlots - 1) & 1)) {
+            if (k >= kSegSlots && !wait(&bars->seg_free[slot], (k / kSegSlots - 1) & 1)) {
                 set_timeout(p.status, kDiagPagedDecode, kRoleProducer, 0, k);
                 ok = false;
                 return;

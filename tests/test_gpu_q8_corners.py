@@ -23,10 +23,11 @@ def _gpu():
 
 
 @pytest.mark.parametrize("Hq,Hkv,most", [(40, 1, 1), (24, 1, 2), (64, 2, 2), (33, 1, 1), (48, 4, 5),
-                                         (9, 1, 7), (12, 1, 1), (64, 1, 1), (22, 2, 3)])
+                                         (9, 1, 7), (12, 1, 1), (64, 1, 1), (22, 2, 3),
+                                         (24, 1, 4), (64, 4, 5), (7, 1, 13)])
 @pytest.mark.parametrize("s_most,window", [(400, 0), (900, 0), (900, 130)])
 def test_rows_in_blocks(Hq, Hkv, most, s_most, window):
-    """9 to 64 rows: teams of two and four groups, one block or two, sequences with fewer rows."""
+    """9 to 96 rows: teams of two and four groups, up to three blocks, sequences with fewer rows."""
     t = [(3 * i + 1) % (most + 1) for i in range(11)]
     t[4] = most
     s = [max(n, 1 + (131 * i) % s_most) for i, n in enumerate(t)]
@@ -65,7 +66,7 @@ def test_places_of_the_pools(t, n, how):
     p.check(only=None if n == 2 else range(0, n, 17))
 
 
-@pytest.mark.parametrize("t", [1, 3, 30])
+@pytest.mark.parametrize("t", [1, 3, 6, 30])
 def test_captured_calls_that_share_a_workspace(t):
     """Two captured calls of different batches with one workspace, replayed in turn on one stream."""
     ps = [PagedQ8([t] * 5, [3000, 30 + 7 * i, 1000, 512, 64], 8, 2, 16, 820 + i, max_kv=4000)

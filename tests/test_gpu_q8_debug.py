@@ -47,7 +47,7 @@ def test_short_and_blocks(debug_lib):
     t_sh.test_drafts(2, 1, 4, 33)
     for what, code in (("page", -1), ("lens", -1), ("bound", -4)):
         t_sh.test_bad_device_contents(what, code)
-    for Hq, Hkv, most in ((40, 1, 1), (24, 1, 2), (12, 1, 1)):
+    for Hq, Hkv, most in ((40, 1, 1), (24, 1, 2), (12, 1, 1), (7, 1, 13)):
         t_co.test_rows_in_blocks(Hq, Hkv, most, 900, 130)
     for cu in t_co.FEW:
         t_co.test_attention_with_contradictory_offsets(cu, 6, 64, 64, 64)
