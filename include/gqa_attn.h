@@ -442,7 +442,8 @@ gqa_status gqa_packed_rope_append_q8(const void *q, int64_t q_stride, const void
  * a NaN value those rows' elements; a query row with an infinity or a NaN is NaN.
  * gqa_attn_paged_q8_workspace_bytes sizes its own workspace (with the arguments of the call).  With
  * more than 96 rows (max_q * Hq / Hkv) it has room for every key that nseq and max_kv allow in bf16:
- * pass a max_kv near the longest sequence. */
+ * pass a max_kv near the longest sequence, and decode steps over long caches in a call of their own,
+ * not next to a chunk that brings the whole batch over 96 rows. */
 size_t gqa_attn_paged_q8_workspace_bytes(int nseq, int total, int max_q, int max_kv, int Hq,
                                          int Hkv, int d);
 gqa_status gqa_attn_paged_q8(const void *q, int64_t q_stride, const gqa_paged_kv_q8 *cache,
