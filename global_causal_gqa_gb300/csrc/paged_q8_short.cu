@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     __syncwarp();
     const int pairs = p.nseq * p.Hkv;
     int *claimed = reinterpret_cast<int *>(smem + kClaimed);   // of the CTA's pairs
-    const int box = min(p.page_size, kKeys), boxes = kKeys / box;
+    static_assert(kKeys == 32, "box_shift");
+    const int box = min(p.page_size, kKeys), box_shift = min(p.page_shift, 5), boxes = kKeys >> box_shift;
     if (threadIdx.x == 0) *claimed = 0;
     __syncthreads();
     // ---- the pair whose copies are issued, an entry of its page table per lane (max_kv <= 512: at
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
             if (!p.joint) tma_load_5d(dst + kKeys * kD, &tmV, full, 0, 0, 0, group, slab);
         }
         const int bkey = 8 * (lane & (kByteCopies - 1));
-        const int at = __shfl_sync(0xffffffffu, slab, bkey / box);
+        const int at = __shfl_sync(0xffffffffu, slab, bkey >> box_shift);
         if (lane < kByteCopies)
             copy_async16(ring_bytes + (slot * kKeys + bkey) * 2,
                          p.scales + ((long)max(at, 0) * p.page_size + (kb + bkey & (p.page_size - 1))) * 2,

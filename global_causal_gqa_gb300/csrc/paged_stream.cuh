@@ -496,12 +496,12 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
                 }
             }
             if constexpr (S::kQ8) {
-                // the bytes of 8 keys per lane
+                // the bytes of 8 keys per lane (a page is a box: it has kUnit keys at most)
                 const int key = 8 * lane & (kUnit - 1);
-                const int at = __shfl_sync(0xffffffffu, slab, key / box);
+                const int at = __shfl_sync(0xffffffffu, slab, key >> p.page_shift);
                 if (free && lane < kScaleCopies)
                     copy_async16(scales + (st * kUnit + key) * 2,
-                                 p.scales + ((long)max(at, 0) * p.page_size + key % box) * 2,
+                                 p.scales + ((long)max(at, 0) * p.page_size + (key & (p.page_size - 1))) * 2,
                                  at >= 0 ? 16 : 0, full);
             }
             if (!__all_sync(0xffffffffu, free)) {
