@@ -849,7 +849,7 @@ Plan plan_of(int max_q, int Hq, int Hkv) {
 // The call's tensor maps, in p what they come to: {128 numbers, 8 keys, the two pools, groups of 8
 // keys, (page, KV head)}, a box of `most` keys of a page at most.  A map takes a stride from pool to
 // pool below 2^40, and then a page's keys and values come as one copy, 8 of either in turn (32 caches
-// of 8k-64k tokens in pages of 16: 577 us with two copies, 449 with one); else as two.
+// of 8k-64k tokens in pages of 16: 577 us with two copies, 426 with one); else as two.
 bool make_maps(const gqa_paged_kv_q8 &c, int most, Params &p, CUtensorMap *mk, CUtensorMap *mv) {
     const uint64_t kp = reinterpret_cast<uint64_t>(c.k), vp = reinterpret_cast<uint64_t>(c.v);
     const uint64_t apart = kp < vp ? vp - kp : kp - vp, page = c.page_size;
