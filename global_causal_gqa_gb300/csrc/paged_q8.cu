@@ -125,6 +125,11 @@ __device__ __forceinline__ bool group_any(int id, int threads, bool mine) {
     return r != 0;
 }
 
+// 255 in the bytes that are NaN among the four e4m3 in x.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
+    return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
 // Two f16 numbers less their upper bytes as such, exactly.
 __device__ __forceinline__ uint32_t less_upper(uint32_t x) {
     const uint32_t u = x & 0xff00ff00u;
@@ -215,41 +220,57 @@ __device__ __forceinline__ void bring_queries(const Params &p, Q8Bars *bars, uin
         }
         if (!quick_wait(&bars->q_raw, k & 1)) {
             expired(p.status, kRoleQueries, 2, k);
+            quick_wait(&bars->q_raw, k & 1);   // never leave the CTA with copies in flight
             return;
         }
-        // two rows at a time: half a warp has a row, 8 dims per lane
-        const int half = lane >> 4, c = lane & 15;
-#pragma unroll 2
-        for (int i0 = 0; i0 < L::kTeamRows; i0 += 2) {
-            const int row = i0 + half, n = row % kRows;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (row < n_rows) w = *reinterpret_cast<const uint4 *>(smem + L::kRaw + row * kD * 2 + 16 * c);
-            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+        // A group's rows at a time, four lanes to a row, 4 x 8 dims each (a group without rows reads
+        // nothing of its tile; two rows at a time took 5200 cycles for 32, which a kernel's first pair
+        // waits for).
+        const int n = lane >> 2, part = lane & 3;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n_rows; i0 += kRows) {
+            const int row = i0 + n;
+            uint4 w[4];
             uint32_t most = 0;         // (magnitudes compare as their bits do, NaN above all)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                most = max(most, max(words[e] << 16 & 0x7fffffffu, words[e] & 0x7fff0000u));
+            for (int j = 0; j < 4; ++j) {
+                w[j] = make_uint4(0, 0, 0, 0);
+                if (row < n_rows)
+                    w[j] = *reinterpret_cast<const uint4 *>(smem + L::kRaw + row * kD * 2 +
+                                                            16 * (part + 4 * j));
+            }
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1)
-                most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t words[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    most = max(most, max(words[e] << 16 & 0x7fffffffu, words[e] & 0x7fff0000u));
+            }
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
             const uint32_t ex = max(most >> 23, 8u);
             const float up = __uint_as_float((261 - ex) << 23);   // 2^(7 - exponent)
-            uint32_t h[2] = {0, 0}, l[2] = {0, 0};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x0 = bf16lo(words[e]) * up, x1 = bf16hi(words[e]) * up;
-                const uint32_t y = to_e4m3x2(x0, x1), back = e4m3x2_f16x2(y);
-                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-                h[e >> 1] |= y << (16 * (e & 1));
-                l[e >> 1] |= to_e4m3x2((x0 - z.x) * 16.f, (x1 - z.y) * 16.f) << (16 * (e & 1));
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t words[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                uint32_t h[2] = {0, 0}, l[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x0 = bf16lo(words[e]) * up, x1 = bf16hi(words[e]) * up;
+                    const uint32_t y = to_e4m3x2(x0, x1), back = e4m3x2_f16x2(y);
+                    const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                    h[e >> 1] |= y << (16 * (e & 1));
+                    l[e >> 1] |= to_e4m3x2((x0 - z.x) * 16.f, (x1 - z.y) * 16.f) << (16 * (e & 1));
+                }
+                // row n of its group: h in the tile's row 16 g + n, l in row 16 g + 8 + n; a row with
+                // an infinity or NaN: NaN
+                const int c = part + 4 * j;
+                uint8_t *at = tile + (2 * i0 + n) * kD + ((c >> 1 ^ n) << 4) + 8 * (c & 1);
+                *reinterpret_cast<uint2 *>(at) =
+                    ex == 255 ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : make_uint2(h[0], h[1]);
+                *reinterpret_cast<uint2 *>(at + kRows * kD) = make_uint2(l[0], l[1]);
             }
-            // row n of its group: h in the tile's row 16 g + n, l in row 16 g + 8 + n; a row with an
-            // infinity or NaN: NaN
-            uint8_t *at = tile + (row / kRows * kScoreCols + n) * kD + ((c >> 1 ^ n) << 4) + 8 * (c & 1);
-            *reinterpret_cast<uint2 *>(at) =
-                ex == 255 ? make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu) : make_uint2(h[0], h[1]);
-            *reinterpret_cast<uint2 *>(at + kRows * kD) = make_uint2(l[0], l[1]);
-            if (c == 0) factors[row] = __uint_as_float((ex - 7) << 23) * p.scale_log2;
+            if (part == 0) factors[row] = __uint_as_float((ex - 7) << 23) * p.scale_log2;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -604,11 +625,19 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                     for (int i = 0; i < 8; ++i)
                         reinterpret_cast<uint4 *>(vr)[i] = make_uint4(0, 0, 0, 0);
                 } else if (key > q_first || key < lo_all) {
-                    // some rows see it: its NaN are taken out, and noted for the rows that do
+                    // some rows see it: its NaN are taken out, and noted for the rows that do (all
+                    // numbers are looked over first, together: one after the other they took 4000
+                    // cycles)
+                    uint32_t nan = 0;
+#pragma unroll 2
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 x = reinterpret_cast<const uint4 *>(vr)[i];
+                        nan |= nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w);
+                    }
 #pragma unroll 1
-                    for (int i = 0; i < kD / 4; ++i) {
+                    for (int i = 0; nan && i < kD / 4; ++i) {
                         uint32_t *at = reinterpret_cast<uint32_t *>(vr) + i;
-                        const uint32_t x = *at, bad = __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        const uint32_t x = *at, bad = nan_bytes(x);
                         if (!bad) continue;
                         *at = x & ~bad;
                         const int dim = 16 * (i >> 2 ^ (t & 7)) + 4 * (i & 3);
@@ -765,8 +794,6 @@ template <int TEAM, bool SHARE>
 __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
     paged_q8_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const Params p) {
-    griddep_wait();
-    griddep_launch_dependents();
     using L = Layout<TEAM, SHARE>;
     using S = typename L::S;
     extern __shared__ uint8_t smem_raw[];
@@ -809,6 +836,8 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
     for (int i = threadIdx.x; i < L::kTeams * 2 * L::kTeamRows; i += S::kThreads)
         reinterpret_cast<uint4 *>(smem + L::kNan)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
+    griddep_wait();                    // nothing before it reads or writes global memory
+    griddep_launch_dependents();
     if (warp == L::kScoreWarp) {
         tmem_alloc(&bars->tmem, L::kColumns);
         tmem_relinquish();
