@@ -304,7 +304,7 @@ __device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint
         if (stages < 0) break;
         bool ok = mbar_wait(&bars->q_full[b], (k / L::kQuerySlots) & 1);
         for (int j = 0; ok && j < stages; ++j, ++u) {
-            const int team = (SHARE ? u : k) % L::kTeams, st = u % kStages;
+            const int team = (SHARE ? j : k) % L::kTeams, st = u % kStages;
             const uint32_t n = counts >> (8 * team) & 255, tile = n % kScoreTiles;
             counts = (counts & ~(255u << (8 * team))) | (n + 1 & 255) << (8 * team);
             // (a tile's first use waits for the phase before its first, which reads as done)
@@ -357,7 +357,7 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
         if (stages < 0) break;
         bool ok = true;
         for (int j = 0; j < stages; ++j, ++u) {
-            const int team = (SHARE ? u : k) % L::kTeams;
+            const int team = (SHARE ? j : k) % L::kTeams;
             const int tile = next >> team & 1, at = team * kWeightTiles + tile;
             const uint64_t pd = pd0 + at * (L::kWeights >> 4);
             ok = mbar_wait(&bars->p_full[team][tile], parity >> at & 1);
@@ -444,7 +444,8 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         for (int r = 0; r < kRows; ++r) l[r] = 0.f;
 #pragma unroll 1
         for (int j = 0, u = sg.u0; j < sg.stages; ++j, ++u) {
-            if (SHARE && u % L::kTeams != team) continue;
+            // (the first to team 0, whatever the CTA had before: the shares are added up in order)
+            if (SHARE && j % L::kTeams != team) continue;
             const int st = u % kStages, si = scored % kScoreTiles;
             if (!quick_wait(&bars->s_full[team][si], (scored / kScoreTiles) & 1)) ok = false;
             ++scored;
