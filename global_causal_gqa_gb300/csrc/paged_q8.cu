@@ -795,6 +795,8 @@ template <int TEAM, bool SHARE>
 __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
     paged_q8_kernel(const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const Params p) {
+    griddep_wait();
+    griddep_launch_dependents();
     using L = Layout<TEAM, SHARE>;
     using S = typename L::S;
     extern __shared__ uint8_t smem_raw[];
@@ -837,8 +839,6 @@ __global__ void __launch_bounds__((Q8Stream<TEAM, SHARE>::kThreads), 1)
     for (int i = threadIdx.x; i < L::kTeams * 2 * L::kTeamRows; i += S::kThreads)
         reinterpret_cast<uint4 *>(smem + L::kNan)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
-    griddep_wait();                    // nothing before it reads or writes global memory
-    griddep_launch_dependents();
     if (warp == L::kScoreWarp) {
         tmem_alloc(&bars->tmem, L::kColumns);
         tmem_relinquish();

@@ -55,6 +55,8 @@ template <bool BOTH>
 __global__ void __launch_bounds__(FewStream<BOTH>::kThreads, 1)
     paged_q8_few_kernel(const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const Params p) {
+    griddep_wait();
+    griddep_launch_dependents();
     using S = FewStream<BOTH>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -76,8 +78,6 @@ __global__ void __launch_bounds__(FewStream<BOTH>::kThreads, 1)
         mbar_init(&bars->clc_full, 1);
         fence_mbar_init();
     }
-    griddep_wait();                           // nothing before it reads or writes global memory
-    griddep_launch_dependents();
     scan_units<S>(p, bars);
     __syncthreads();
     if (warp == S::kProducer) {

@@ -36,6 +36,8 @@ constexpr int kSmemBytes = kClaimed + 16 + 1024;
 __global__ void __launch_bounds__(32 * kWarps, 1)
     paged_q8_short_kernel(const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const Params p) {
+    griddep_wait();
+    griddep_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -54,8 +56,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     const int box = min(p.page_size, kKeys), box_shift = min(p.page_shift, 5), boxes = kKeys >> box_shift;
     if (threadIdx.x == 0) *claimed = 0;
     __syncthreads();
-    griddep_wait();                          // nothing before it reads or writes global memory
-    griddep_launch_dependents();
     // ---- the pair whose copies are issued, an entry of its page table per lane (max_kv <= 512: at
     // most 32 pages; entries behind its last page are read but not used)
     PackedSeq s{0, 0, 0};
