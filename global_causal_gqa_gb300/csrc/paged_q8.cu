@@ -137,9 +137,6 @@ __device__ __forceinline__ uint32_t less_upper(uint32_t x) {
     return *reinterpret_cast<const uint32_t *>(&y);
 }
 
-// Bytes of a stage from 8 keys (or values) to the next 8.
-__device__ __forceinline__ uint32_t key_step(const Params &p) { return p.joint ? 2048 : 1024; }
-
 // (Out of line: the records of expired waits are never run in earnest.)
 __device__ __noinline__ void expired(int *status, int role, int barrier, int n) {
     set_timeout(status, kDiagPagedDecode, role, barrier, n);
@@ -289,7 +286,7 @@ __device__ __forceinline__ void issue_scores(const Params &p, Q8Bars *bars, uint
     using L = Layout<TEAM, SHARE>;
     constexpr int kStages = L::S::kStages, kSegSlots = L::S::kSegSlots;
     const uint32_t ring = smem_u32(smem);
-    const uint64_t kd0 = sdesc_sw128(ring + (p.joint && p.v_first ? 1024 : 0), 16, key_step(p));
+    const uint64_t kd0 = sdesc_sw128(ring, 16, kKeyStep);
     const uint64_t qd0 = sdesc_sw128(ring + L::kQ, 16, 1024);
     constexpr uint32_t idesc = idesc_f8_f32(128, L::kScoreN, 0, 0, 0);
     uint32_t counts = 0;               // scores of each team's stages, mod 256
@@ -338,8 +335,8 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
                                              uint32_t tmem) {
     using L = Layout<TEAM, SHARE>;
     constexpr int kStages = L::S::kStages, kSegSlots = L::S::kSegSlots;
-    const uint32_t ring = smem_u32(smem), step = key_step(p);
-    const uint64_t vd0 = sdesc_sw128(ring + (!p.joint ? kTileBytes : p.v_first ? 0 : 1024), 16, step);
+    const uint32_t ring = smem_u32(smem);
+    const uint64_t vd0 = sdesc_sw128(ring + kTileBytes, 16, kKeyStep);
     const uint64_t pd0 = sdesc_mn(ring + L::kP, 128, kChunk);
     constexpr uint32_t idesc = idesc_f8_f32(128, L::kValueN, 1, 1, 1);
     uint32_t parity = 0, next = 0;     // of each team's tiles of weights, a bit each; its next tile
@@ -369,7 +366,7 @@ __device__ __forceinline__ void issue_values(const Params &p, Q8Bars *bars, uint
             const uint64_t vd = vd0 + st * (kStageBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                umma_f8_ss(tmem + L::kOutputs + team * L::kValueN, vd + kk * (step >> 2), pd + 32 * kk,
+                umma_f8_ss(tmem + L::kOutputs + team * L::kValueN, vd + kk * (kKeyStep >> 2), pd + 32 * kk,
                            idesc, kk > 0 || j >= (SHARE ? L::kTeams : 1));
             umma_commit(&bars->pv_done[team][tile]);
             umma_commit(&bars->s_full[team][tile]);   // of the stage whose weights go there next
@@ -618,9 +615,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
             }
             // ---- values that the mask hides: 0 * NaN is NaN
             if (edge && member == 0) {
-                uint8_t *vr = smem + st * kStageBytes +
-                              (!p.joint ? kTileBytes + t * kD
-                                        : (t >> 3) * 2048 + (p.v_first ? 0 : 1024) + (t & 7) * kD);
+                uint8_t *vr = smem + st * kStageBytes + kTileBytes + t * kD;
                 if (key >= sg.S || key < lo) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -876,22 +871,16 @@ Plan plan_of(int max_q, int Hq, int Hkv) {
     return blocks <= kMostBlocks ? Plan{4, static_cast<int>(blocks)} : Plan{0, 0};
 }
 
-// The call's tensor maps, in p what they come to: {128 numbers, 8 keys, the two pools, groups of 8
-// keys, (page, KV head)}, a box of `most` keys of a page at most.  A map takes a stride from pool to
-// pool below 2^40, and then a page's keys and values come as one copy, 8 of either in turn (32 caches
-// of 8k-64k tokens in pages of 16: 577 us with two copies, 426 with one); else as two.
-bool make_maps(const gqa_paged_kv_q8 &c, int most, Params &p, CUtensorMap *mk, CUtensorMap *mv) {
-    const uint64_t kp = reinterpret_cast<uint64_t>(c.k), vp = reinterpret_cast<uint64_t>(c.v);
-    const uint64_t apart = kp < vp ? vp - kp : kp - vp, page = c.page_size;
-    p.joint = apart > 0 && apart < (1ull << 40);
-    p.v_first = p.joint && vp < kp;
-    const uint32_t pools = p.joint ? 2 : 1;
-    const uint64_t dims[5] = {kD, 8, pools, page / 8, (uint64_t)c.num_pages * c.Hkv};
-    const uint64_t strides[4] = {kD, p.joint ? apart : kD, 8 * kD, page * kD};
-    const uint32_t box[5] = {kD, 8, pools,
-                             static_cast<uint32_t>(c.page_size < most ? page : most) / 8, 1};
-    return make_byte_map(mk, p.v_first ? c.v : c.k, 5, dims, strides, box) &&
-           make_byte_map(mv, c.v, 5, dims, strides, box);
+// The call's tensor maps, {128 numbers, keys of a page, (page, KV head)}, a box of `most` keys of a page
+// at most.  (One map over both pools, their distance as a dimension's stride, brought a page's keys and
+// values by one copy, in pages of 16 tokens 426 instead of 522 us over 32 caches of 8k-64k.  But strides
+// that are not multiples of the ones before are outside what the encoder's description allows, and two
+// runs of random cases ended in a fault, small pools far apart.)
+bool make_maps(const gqa_paged_kv_q8 &c, int most, CUtensorMap *mk, CUtensorMap *mv) {
+    const uint64_t page = c.page_size;
+    const uint64_t dims[3] = {kD, page, (uint64_t)c.num_pages * c.Hkv}, strides[2] = {kD, page * kD};
+    const uint32_t box[3] = {kD, static_cast<uint32_t>(c.page_size < most ? c.page_size : most), 1};
+    return make_byte_map(mk, c.k, 3, dims, strides, box) && make_byte_map(mv, c.v, 3, dims, strides, box);
 }
 
 template <int TEAM, bool SHARE>
@@ -916,7 +905,7 @@ int launch_stream(const PackedAttn &a, const gqa_paged_kv_q8 &c, const Plan &pla
     // of 20-40 tokens 8 and 13).
     const bool each = plan.team == 1 && p.whole &&
                       pairs >= (a.max_kv <= 2 * kShortKeys ? 1 : 6) * static_cast<long>(kSMs);
-    if (!make_maps(c, each ? kShortKeys : kStreamUnit, p, &mk, &mv)) return GQA_ERR_CUDA;
+    if (!make_maps(c, each ? kShortKeys : kStreamUnit, &mk, &mv)) return GQA_ERR_CUDA;
     if (each) return launch_q8_short(mk, mv, p, s);
     const long grid = !p.whole ? p.chunks : pairs < kSMs ? pairs : kSMs;
     const int rc = plan.team == 1   ? launch_q8_few(mk, mv, p, grid, s)

@@ -14,7 +14,8 @@
 // A stage takes a warp 1800 cycles, the copies of a stage 1365: with few pairs per CTA both groups
 // of four warps take a pair's stages in turn (BOTH; 32 caches of 8k-64k tokens 529 -> 399 us, 6.8
 // TB/s, which is HBM), else the pairs, so that one's ends pass while the other streams (64
-// windows of 2048, pages of 16: 58 us, 4.5 TB/s, of them 5 of start and 5 of the merge).  The
+// windows of 2048: 57 us in pages of 64, 4.6 TB/s, of them 5 of start and 5 of the merge; 69 in pages
+// of 16, whose 16 copies a stage the producer issues one after the other).  The
 // tcgen05 kernel of paged_q8.cu takes 425 us: it holds a stage 2.5 us, through a score product, a
 // softmax and a value product in different warps, where this one holds it 1 us.
 #include "paged_q8_few.cuh"
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(FewStream<BOTH>::kThreads, 1)
     const int group = warp / kConsumers, cw = warp % kConsumers;
     float *xchg = reinterpret_cast<float *>(smem + kXchg) + group * kConsumers * kRows * kD;
     const int part = 32 * cw;                 // first of this warp's keys in a stage
-    const FewAt at(p, part, kTileBytes);
+    const FewAt at(part, kTileBytes);
     FewRows x;
     int meets = 0;
     auto meet = [&]() {

@@ -38,7 +38,7 @@ __device__ __forceinline__ bool strip_nan(uint32_t &w) {
 }
 
 // Where a lane finds its parts of a warp's 32 keys, relative to the stage.
-// Rows of 128 bytes, 128-byte swizzled; `step` bytes from 8 keys to the next.  A block of 16
+// Rows of 128 bytes, 128-byte swizzled.  A block of 16
 // keys has the keys 0-7 and 8 + (0-7 ^ 4) as the rows 0-7 and 8-15 of the score product's A
 // operand.  There each four numbers of a lane are two of the product's k-steps' pairs: the
 // queries' dims are taken in the same order.  V's 16 x 16 matrices, transposed, bring a lane
@@ -46,24 +46,21 @@ __device__ __forceinline__ bool strip_nan(uint32_t &w) {
 // 4i .. 4i + 3 are the score rows 2i, 2i + 1, 8 + 2i, 8 + 2i + 1.  (The ^ 4: eight rows of either
 // operand lie in eight different swizzled columns.)
 struct FewAt {
-    uint32_t step, keys0, values0, k[2], v;
+    uint32_t values0, k[2], v;               // values0: bytes from keys to values
     int part;                                // the first of the 32 keys within the stage
-    // `apart`: bytes from keys to values where no copy brings both
-    __device__ __forceinline__ FewAt(const Params &p, int first, uint32_t apart) {
+    __device__ __forceinline__ FewAt(int first, uint32_t apart) {
         const int lane = threadIdx.x & 31, mat = lane >> 3, l7 = lane & 7;
         part = first;
-        step = p.joint ? 2048 : 1024;
-        keys0 = p.joint && p.v_first ? 1024 : 0;
-        values0 = !p.joint ? apart : p.v_first ? 0 : 1024;
+        values0 = apart;
         const int kk = mat & 1 ? 8 + (l7 ^ 4) : l7;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-            k[b] = keys0 + row(16 * b + kk) + (((mat >> 1) ^ (kk & 7)) << 4);
+            k[b] = row(16 * b + kk) + (((mat >> 1) ^ (kk & 7)) << 4);
         const int rho = lane & 15, i = 2 * (rho >> 2) + (rho & 1), vk = rho & 2 ? 8 + (i ^ 4) : i;
         v = values0 + row(16 * (lane >> 4) + vk) + ((vk & 7) << 4);
     }
     __device__ __forceinline__ uint32_t row(int key) const {
-        return (part + key >> 3) * step + (key & 7) * kD;
+        return (part + key) * kD;
     }
     __device__ __forceinline__ uint32_t values(int key) const { return values0 + row(key); }
 };

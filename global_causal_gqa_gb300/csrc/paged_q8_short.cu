@@ -6,7 +6,7 @@
 // eight warps share it, and the code that only the ends run misses the instruction caches: 256 chats
 // of 20-450 tokens, 8 heads, 57 us.  Here a warp takes a whole pair, 32 keys at a time, issues its
 // own copies, a few steps ahead and over the ends of pairs, and writes the result from its
-// registers: no warp waits for another (38 us, 3.3 TB/s; 1024 such chats 97 us, 5.4 TB/s; twelve
+// registers: no warp waits for another (39 us, 3.2 TB/s; 1024 such chats 97 us, 5.4 TB/s; twelve
 // warps with two steps in flight each: eight with three 45 us, nine with three 44).  It needs as many
 // pairs as warps to fill the GPU.
 #include "paged_q8_few.cuh"
@@ -98,10 +98,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
         __syncwarp();
         uint8_t *dst = ring + slot * kStepBytes;
         if (lane < boxes) {
-            const int group = (key & (p.page_size - 1)) >> 3;
-            dst += lane * box * (p.joint ? 2 * kD : kD);
-            tma_load_5d(dst, &tmK, full, 0, 0, 0, group, slab);
-            if (!p.joint) tma_load_5d(dst + kKeys * kD, &tmV, full, 0, 0, 0, group, slab);
+            const int row = key & (p.page_size - 1);
+            dst += lane * box * kD;
+            tma_load_3d(dst, &tmK, full, 0, row, slab);
+            tma_load_3d(dst + kKeys * kD, &tmV, full, 0, row, slab);
         }
         const int bkey = 8 * (lane & (kByteCopies - 1));
         const int at = __shfl_sync(0xffffffffu, slab, bkey >> box_shift);
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 #pragma unroll 1
     for (int i = 0; i < kDepth; ++i) issue();
 
-    const FewAt at(p, 0, kKeys * kD);
+    const FewAt at(0, kKeys * kD);
     FewRows x;
 #pragma unroll 1
     for (int taken = 0; done < issued; ++taken) {

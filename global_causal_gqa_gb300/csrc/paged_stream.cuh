@@ -21,6 +21,7 @@ constexpr int kMostStages = 6;
 constexpr int kConsumers = 4;                   // warps of a group of consumers
 constexpr int kSMs = 152;
 constexpr int kMinRun = 128;                    // units per SM from which chunks come in levels
+constexpr int kKeyStep = 1024;                  // 8-bit stages: bytes of 8 keys (or values)
 constexpr int kScaleCopies = 16;                // lanes that copy an 8-bit stage's scale bytes
 
 // What the kernels differ in.  kUnit: keys of a stage.  kStages: of the ring.  kTeams: groups of
@@ -80,7 +81,6 @@ struct Params {
     int chunks, rec_rows;          // rows that a partial has room for
     const int32_t *cu, *kv_lens, *pages;
     const uint8_t *scales;         // of 8-bit pages
-    int joint, v_first;            // 8-bit pages: a copy has keys and values, these first
     int *status;
     long q_stride, o_stride;
     PackedBounds bounds;
@@ -478,17 +478,15 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
             }
             const int st = u % kStages, group = S::full_of(turn, j);
             uint64_t *full = &bars->full[group][st];
-            // (8-bit pages: a box has keys and values where one copy brings both)
-            uint8_t *dst = smem + st * kStageBytes +
-                           lane * box * (S::kQ8 && !p.joint ? kD : 2 * kD);
+            uint8_t *dst = smem + st * kStageBytes + lane * box * (S::kQ8 ? kD : 2 * kD);
             const int row = unit_key & (p.page_size - 1);
             // every lane with a box waits, announces its bytes and loads for itself
             const bool free = u < kStages || mbar_wait(&bars->empty[st], (u / kStages - 1) & 1);
             if (free && lane < boxes) {
                 if constexpr (S::kQ8) {
                     mbar_arrive_expect_tx(full, 2 * box * kD);
-                    tma_load_5d(dst, &tmK, full, 0, 0, 0, 0, slab);
-                    if (!p.joint) tma_load_5d(dst + kTileBytes, &tmV, full, 0, 0, 0, 0, slab);
+                    tma_load_3d(dst, &tmK, full, 0, 0, slab);
+                    tma_load_3d(dst + kTileBytes, &tmV, full, 0, 0, slab);
                 } else {
                     mbar_arrive_expect_tx(full, 2 * box * kD * 2);
                     tma_load_4d(dst, &tmK, full, 0, row, 0, slab);

@@ -46,15 +46,21 @@ def test_no_lse(t, n):
 
 
 @pytest.mark.parametrize("t,n", [(1, 2), (1, 930), (2, 2), (7, 2)])
-@pytest.mark.parametrize("how", ["values first", "one pool"])
+@pytest.mark.parametrize("how", ["values first", "one pool", "far apart"])
 def test_places_of_the_pools(t, n, how):
-    """Values that lie before the keys, and values that are the keys, which takes two copies of a
-    page, as pools farther apart than a copy can bring together do."""
+    """Values that lie before the keys, values that are the keys, and small pools 12 GB apart."""
     p = PagedQ8([t] * n, [300 if n == 2 else 90] * n, 8, 1, 16, 812 + t)
     if how == "values first":
         both = torch.empty(2, *p.kq.shape, dtype=torch.uint8, device="cuda")
         both[0], both[1] = p.vq, p.kq
         p.vq, p.kq = both[0], both[1]
+    elif how == "far apart":
+        room = torch.empty(12 << 30, dtype=torch.uint8, device="cuda")
+        n = p.kq.numel()
+        ends = [x.reshape(p.kq.shape) for x in (room[:n], room[-n:])]
+        ends[0].copy_(p.kq)
+        ends[1].copy_(p.vq)
+        p.kq, p.vq = ends
     else:
         p.vq = p.kq
         p.sc[..., 1] = p.sc[..., 0]
