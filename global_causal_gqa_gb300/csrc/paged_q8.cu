@@ -9,9 +9,9 @@
 // (32 caches of 8k-64k tokens 430 us, 6.3 TB/s) and by its warps at 32 (557 us; blocks of 32 rows
 // read the pages again, from L2 for the most part: 24 drafts of 2-6 tokens of 8 rows 76 us).  More:
 // all keys that the call sees are expanded to bf16 pages in the workspace (paged_read.cu) and the
-// tile kernel (packed_prefill.cu) takes them from there (24 times 72, 96 and 128 rows over 700-6000 tokens: 184, 186
-// and 190 us so, 158, 169 and 220 in blocks; 16 to 96 rows 179 and 106; 8 times 96 over 20k-60k 605
-// and 439).
+// tile kernel (packed_prefill.cu) takes them from there (24 times 72, 96 and 128 rows over 700-6000
+// tokens: 184, 186 and 190 us so, 158, 169 and 220 in blocks; 16 to 96 rows 179 and 106; 8 times 96
+// over 20k-60k 605 and 439).
 //
 // The kernel is cut and fed as the bf16 one (paged_decode.cu; paged_stream.cuh), in stages of 128
 // keys.  Its products run on tcgen05 with the numbers as they lie in the pages:
