@@ -418,6 +418,21 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         const int slot = k % kSegSlots;
         if (!quick_wait(&bars->seg_full[slot], (k / kSegSlots) & 1)) ok = false;
         if (any(!ok)) return fail(0, k);
+        // NaN among the values' numbers: a bit per row and dim of this pair (turn), and of the last
+        auto nan_row = [&](int which, int r) {    // r: of the team's rows
+            return reinterpret_cast<uint32_t *>(smem + L::kNan) +
+                   ((2 * team + which) * L::kTeamRows + r) * 4;
+        };
+        if (!SHARE && cw == 0 && bars->nan_any[group][turn ^ 1]) {
+            // The last pair's bits: all warps of the group have read them, and the team's first group,
+            // which sets them, is not past this pair before this group has handed over its stages.
+            // Here, where groups that have no rows of this pair come by, too.
+            if (lane < kRows)
+                *reinterpret_cast<uint4 *>(nan_row(turn ^ 1, kRows * member + lane)) =
+                    make_uint4(0, 0, 0, 0);
+            __syncwarp();
+            if (lane == 0) bars->nan_any[group][turn ^ 1] = 0;
+        }
         const Segment sg = bars->seg[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->seg_free[slot]);
@@ -429,11 +444,6 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         const int q_first = sg.S - sg.T;          // keys beyond are hidden from some
         const int lo = p.window > 0 ? max(0, q_first - p.window + 1) : 0;
         const int lo_all = p.window > 0 ? max(0, sg.S - p.window) : 0;
-        // NaN among the values' numbers: a bit per row and dim of this pair (turn), and of the last
-        auto nan_row = [&](int which, int r) {    // r: of the team's rows
-            return reinterpret_cast<uint32_t *>(smem + L::kNan) +
-                   ((2 * team + which) * L::kTeamRows + r) * 4;
-        };
         float m = -CUDART_INF_F, mo = -CUDART_INF_F;   // of row `lane`
         bool fresh = true;             // no stage of this pair yet
         float l[kRows];
@@ -525,14 +535,8 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                             mine[2] = -fmaxf(mn, -3.0e38f);
                             reinterpret_cast<float *>(rowf + kRows / 2)[lane] =
                                 mn == -CUDART_INF_F ? 0.f : ex2_approx(mn - mno + kShift);
-                            if (!SHARE && fresh && cw == 0 && bars->nan_any[group][turn ^ 1]) {
-                                // the last pair's bits have been read
-                                *reinterpret_cast<uint4 *>(nan_row(turn ^ 1, kRows * member + lane)) =
-                                    make_uint4(0, 0, 0, 0);
-                            }
                         }
                         __syncwarp();
-                        if (!SHARE && fresh && cw == 0 && lane == 0) bars->nan_any[group][turn ^ 1] = 0;
                         if (!fresh) {
                             if (!products_done()) ok = false;
                             tc_fence_after();
