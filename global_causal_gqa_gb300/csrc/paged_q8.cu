@@ -98,8 +98,8 @@ struct Layout {
     static constexpr int kQ = S::kStages * kStageBytes;
     static constexpr int kP = kQ + kQuerySlots * kQuery;
     static constexpr int kScales = kP + kTeams * kWeightTiles * kWeights;        // two bytes per key of a stage
-    static constexpr int kRowFactors = kScales + S::kStages * 2 * S::kUnit;   // float4 [warp][8]
-    static constexpr int kChanges = kRowFactors + kGroups * kConsumers * kRows * 16;   // float2
+    static constexpr int kRowFactors = kScales + S::kStages * 2 * S::kUnit;   // float [warp][2][8]
+    static constexpr int kChanges = kRowFactors + kGroups * kConsumers * kRows * 8;    // float2
     static constexpr int kMost = kChanges + kGroups * kConsumers * kRows * 8;          // float2
     static constexpr int kSums = kMost + kGroups * kConsumers * kRows * 8;   // float [group][row][warp]
     static constexpr int kFactors = kSums + kGroups * kRows * kConsumers * 4;   // float [pair][row]
@@ -391,8 +391,8 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
     const int t = 32 * cw + lane;      // the thread's key of a stage, and its dim of the outputs
     tmem += static_cast<uint32_t>(32 * cw) << 16;
     const uint32_t outputs = tmem + L::kOutputs + team * L::kValueN + member * kValueCols;
-    // factors and -m of two rows each, and then the products' factors of four
-    float4 *rowf = reinterpret_cast<float4 *>(smem + L::kRowFactors) + warp * kRows;
+    // the rows' -m, and then their products' factors
+    float *rowf = reinterpret_cast<float *>(smem + L::kRowFactors) + warp * 2 * kRows;
     float2 *change = reinterpret_cast<float2 *>(smem + L::kChanges) + warp * kRows;
     float2 *most = reinterpret_cast<float2 *>(smem + L::kMost) + group * kConsumers * kRows;
     float *sums = reinterpret_cast<float *>(smem + L::kSums) + group * kRows * kConsumers;
@@ -465,7 +465,19 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                 tmem_ld16(tmem + (team * kScoreTiles + si) * L::kScoreN + member * kScoreCols, s);
                 const uint32_t bytes =
                     reinterpret_cast<const uint16_t *>(smem + L::kScales)[st * kUnit + t];
-                const float kf = scale_of(bytes & 255u), kl = kf * 0.0625f, vf = scale_of(bytes >> 8);
+                const float kf = scale_of(bytes & 255u), vf = scale_of(bytes >> 8);
+                // The scores' factors, the row's times the key's: a score multiplied by one after the
+                // other may leave fp32's range on the way, or, by a 0, take a hidden one to NaN.
+                // (Formed while the scores are on their way: 32 rows 565 us, after them 575.)
+                const float4 *factors = reinterpret_cast<const float4 *>(
+                    smem + L::kFactors + (k % L::kFactorSlots * L::kTeamRows + member * kRows) * 4);
+                float2 sf[kRows / 2];
+#pragma unroll
+                for (int i = 0; i < kRows / 2; i += 2) {
+                    const float4 f = factors[i / 2];
+                    sf[i] = __fmul2_rn(make_float2(f.x, f.y), make_float2(kf, kf));
+                    sf[i + 1] = __fmul2_rn(make_float2(f.z, f.w), make_float2(kf, kf));
+                }
                 uint32_t hidden = 0;       // a bit per row
                 if (edge) {
                     // a token's rows at a time
@@ -487,8 +499,8 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                     const float2 h = make_float2(__uint_as_float(s[r]), __uint_as_float(s[r + 1])),
                                  lo16 = make_float2(__uint_as_float(s[kRows + r]),
                                                     __uint_as_float(s[kRows + r + 1])),
-                                 x = __ffma2_rn(lo16, make_float2(kl, kl),
-                                                __fmul2_rn(h, make_float2(kf, kf)));
+                                 x = __fmul2_rn(__ffma2_rn(lo16, make_float2(0.0625f, 0.0625f), h),
+                                                sf[r / 2]);
                     y[r] = x.x;
                     y[r + 1] = x.y;
                 }
@@ -504,12 +516,10 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                 while (true) {
                     if (update) {
                         const float ev = fmaxf(exponent_of(bytes >> 8), kLeast);
-                        const float *factors = reinterpret_cast<const float *>(smem + L::kFactors) +
-                                               k % L::kFactorSlots * L::kTeamRows + member * kRows;
                         float a[kRows], b[kRows];
 #pragma unroll
                         for (int r = 0; r < kRows; ++r) {
-                            a[r] = y[r] * factors[r];
+                            a[r] = y[r];
                             b[r] = a[r] + ev;
                         }
                         auto larger = [](float c, float d) { return fmaxf(c, d); };
@@ -530,10 +540,8 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                                             mo == -CUDART_INF_F ? 1.f : ex2_approx(mo - mno));
                             m = mn;
                             mo = mno;
-                            float *mine = reinterpret_cast<float *>(rowf + lane / 2) + (lane & 1);
-                            mine[0] = factors[lane];
-                            mine[2] = -fmaxf(mn, -3.0e38f);
-                            reinterpret_cast<float *>(rowf + kRows / 2)[lane] =
+                            rowf[lane] = -fmaxf(mn, -3.0e38f);
+                            rowf[kRows + lane] =
                                 mn == -CUDART_INF_F ? 0.f : ex2_approx(mn - mno + kShift);
                         }
                         __syncwarp();
@@ -559,12 +567,13 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                     float top = -CUDART_INF_F, largest = 0.f;
 #pragma unroll
                     for (int r = 0; r < kRows; r += 4) {
-                        const float4 z = rowf[kRows / 2 + r / 4];
+                        const float4 ref = reinterpret_cast<const float4 *>(rowf)[r / 4],
+                                     z = reinterpret_cast<const float4 *>(rowf + kRows)[r / 4];
 #pragma unroll
                         for (int i = r; i < r + 4; i += 2) {
-                            const float4 f = rowf[i / 2];
-                            const float2 x = __ffma2_rn(make_float2(y[i], y[i + 1]), make_float2(f.x, f.y),
-                                                        make_float2(f.z, f.w));
+                            const float2 x = __fadd2_rn(make_float2(y[i], y[i + 1]),
+                                                        i == r ? make_float2(ref.x, ref.y)
+                                                               : make_float2(ref.z, ref.w));
                             w[i] = ex2_approx(x.x);
                             w[i + 1] = ex2_approx(x.y);
                             const float2 b = __fmul2_rn(

@@ -154,7 +154,9 @@ struct FewRows {
                                  e4m3x2_f16x2(w[2 * s + 1] >> 16), qb[2 * i + s][0],
                                  qb[2 * i + s][1]);
             }
-        // x[b]: keys kb + 16b + gq (rows 2tq, + 1) and + 8 + (gq ^ 4)
+        // x[b]: keys kb + 16b + gq (rows 2tq, + 1) and + 8 + (gq ^ 4).  (The key's and the row's
+        // factors make one first: either alone may take a finite score out of fp32's range, or, as
+        // 0, a hidden one to NaN.)
         float ev[2][2];   // the values' exponents
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -165,7 +167,7 @@ struct FewRows {
                 ev[b][f] = exponent_of(w >> 8);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    x[b][2 * f + c] = (xs[0][b][2 * f + c] + xs[1][b][2 * f + c]) * kf;
+                    x[b][2 * f + c] = (xs[0][b][2 * f + c] + xs[1][b][2 * f + c]) * (kf * sl[c]);
             }
         const bool edge = kb + 31 > mask.q_first || kb < mask.lo_all;   // of the mask
         uint32_t hidden = 0;   // bits 4b + e
@@ -193,9 +195,9 @@ struct FewRows {
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
                     t = fmaxf(t, x[b][2 * f + c]);
-                    to = fmaxf(to, fmaf(x[b][2 * f + c], sl[c], ev[b][f]));
+                    to = fmaxf(to, x[b][2 * f + c] + ev[b][f]);
                 }
-            top[c] = t * sl[c];
+            top[c] = t;
             topo[c] = to;
             grow |= top[c] > m[c] + kGrow || to > mo[c] + kGrow;
         }
@@ -231,8 +233,8 @@ struct FewRows {
             for (int e = 0; e < 4; ++e) {
                 const int c = e & 1;
                 const float ro = mo[c] == -CUDART_INF_F ? 0.f : mo[c] - kShift;
-                w[e] = ex2_approx(fmaf(x[b][e], sl[c], -mr[c]));
-                wv[e] = ex2_approx(fmaf(x[b][e], sl[c], ev[b][e >> 1] - ro));
+                w[e] = ex2_approx(x[b][e] - mr[c]);
+                wv[e] = ex2_approx(x[b][e] + (ev[b][e >> 1] - ro));
             }
             if (edge) {
 #pragma unroll
