@@ -25,9 +25,10 @@
 //     of what is left, and the rest rounded: off by 2^-9 + 2^-11 of P, or 2^-17.
 // A thread has one key and 8 rows: its key's and value's powers of two are its own, the rows'
 // factors are read from shared memory.  l sums the weights relative to 2^m, O the products P
-// relative to 2^(mo - 12), mo the largest score plus its value's exponent: either range alone may
-// be far from the other's.  Both references move, for all keys of a stage together, when something
-// exceeds them by 2^3, so that P stays within e5m2's range and 2^-17 is 2^-29 of its largest.
+// relative to 2^(m + mo - 12), mo the largest score plus its value's exponent, less m: either range
+// alone may be far from the other's.  Both references move, for all keys of a stage together, when
+// something exceeds them by 2^3, so that P stays within e5m2's range and 2^-17 is 2^-29 of its
+// largest.
 //
 // Warps: four groups of four for the softmax (8 rows; a warp a quarter of a stage's keys), the
 // producer, one that issues the score products and one the value products (one thread for both
@@ -55,7 +56,7 @@ static_assert(kWeightTiles == kScoreTiles, "a stage's scores and weights have ti
 constexpr int kScoreCols = 2 * kRows, kValueCols = 3 * kRows;   // columns of a group
 constexpr int kChunk = 16 * kStreamUnit;      // bytes of 16 columns of the weights
 constexpr float kGrow = 3.0f, kShift = 12.0f, kLargest = 32768.0f;   // log2 units; 2^(3 + 12)
-// Values below 2^-100 count as 2^-100 in mo, so that 2^(m - mo) stays within fp32.
+// Values below 2^-100 count as 2^-100 in mo, so that 2^-mo stays within fp32.
 constexpr float kLeast = -100.0f;
 
 struct Q8Bars : StreamBars {
@@ -141,6 +142,9 @@ __device__ __forceinline__ uint32_t less_upper(uint32_t x) {
 __device__ __noinline__ void expired(int *status, int role, int barrier, int n) {
     set_timeout(status, kDiagPagedDecode, role, barrier, n);
 }
+
+// A score that others are taken relative to.
+__device__ __forceinline__ float finite(float m) { return fmaxf(m, -3.0e38f); }
 
 // The rows' a[i] of all lanes brought together by `op`, in 9 exchanges: of halves, then whole.
 // Returns the row whose value the lane has in a[0].
@@ -518,31 +522,36 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                         const float ev = fmaxf(exponent_of(bytes >> 8), kLeast);
                         float a[kRows], b[kRows];
 #pragma unroll
-                        for (int r = 0; r < kRows; ++r) {
-                            a[r] = y[r];
-                            b[r] = a[r] + ev;
-                        }
+                        for (int r = 0; r < kRows; ++r) a[r] = y[r];
+                        // (the score and exponent less the warp's largest score: next to a score of
+                        // 2^24 an exponent is lost in fp32)
                         auto larger = [](float c, float d) { return fmaxf(c, d); };
                         const int row = gather_rows(a, larger);
+#pragma unroll
+                        for (int r = 0; r < kRows; ++r)
+                            b[r] = y[r] - finite(__shfl_sync(0xffffffffu, a[0], 4 * r)) + ev;
                         gather_rows(b, larger);
                         if ((lane & 3) == 0) most[cw * kRows + row] = make_float2(a[0], b[0]);
                         if (any(!ok)) return fail(1, u);
                         if (lane < kRows) {
-                            float mn = m, mno = mo;
+                            float mn = m;
+#pragma unroll
+                            for (int c = 0; c < kConsumers; ++c)
+                                mn = fmaxf(mn, most[c * kRows + lane].x);
+                            const float base = finite(mn), was = mo + (finite(m) - base);
+                            float mno = was;
 #pragma unroll
                             for (int c = 0; c < kConsumers; ++c) {
                                 const float2 x = most[c * kRows + lane];
-                                mn = fmaxf(mn, x.x);
-                                mno = fmaxf(mno, x.y);
+                                mno = fmaxf(mno, x.y + (finite(x.x) - base));
                             }
                             change[lane] =
                                 make_float2(m == -CUDART_INF_F ? 0.f : ex2_approx(m - mn),
-                                            mo == -CUDART_INF_F ? 1.f : ex2_approx(mo - mno));
+                                            mo == -CUDART_INF_F ? 1.f : ex2_approx(was - mno));
                             m = mn;
                             mo = mno;
-                            rowf[lane] = -fmaxf(mn, -3.0e38f);
-                            rowf[kRows + lane] =
-                                mn == -CUDART_INF_F ? 0.f : ex2_approx(mn - mno + kShift);
+                            rowf[lane] = -base;
+                            rowf[kRows + lane] = mn == -CUDART_INF_F ? 0.f : ex2_approx(kShift - mno);
                         }
                         __syncwarp();
                         if (!fresh) {
@@ -674,8 +683,8 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
             float *shares = reinterpret_cast<float *>(smem + L::kShares);
             bool nans = false;
             if (rows > 0) {
-                // this team's share, O relative to m (times 2^(mo - 12 - m), in two steps as that
-                // may be 2^-138)
+                // this team's share, O relative to m (times 2^(mo - 12), in two steps as that may be
+                // 2^-138)
                 const int row = gather_rows(l, [](float a, float b) { return a + b; });
                 if ((lane & 3) == 0) sums[row * kConsumers + cw] = l[0];
                 if (any(!ok)) return fail(2, k);
@@ -683,7 +692,7 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
                 if (k > 0 && !quick_wait(&bars->taken, k - 1 & 1)) ok = false;
                 if (lane < kRows) {
                     const float4 s = *reinterpret_cast<const float4 *>(sums + lane * kConsumers);
-                    change[lane].x = mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift - m));
+                    change[lane].x = mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift));
                     if (cw == 0) bars->share[group][lane] = make_float2(m, (s.x + s.y) + (s.z + s.w));
                 }
                 __syncwarp();
@@ -762,11 +771,10 @@ __device__ __forceinline__ void softmax(const Params &p, Q8Bars *bars, uint8_t *
         if ((lane & 3) == 0) sums[row * kConsumers + cw] = l[0];
         if (any(!ok)) return fail(2, k);
         if (lane < kRows) {
-            // A row's factors.  O relative to m: times 2^(mo - 12 - m), in two steps as that may be
-            // 2^-138.
+            // A row's factors.  O relative to m: times 2^(mo - 12), in two steps as that may be 2^-138.
             const float4 s = *reinterpret_cast<const float4 *>(sums + lane * kConsumers);
             const float sum = (s.x + s.y) + (s.z + s.w);
-            change[lane] = make_float2(mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift - m)),
+            change[lane] = make_float2(mo == -CUDART_INF_F ? 1.f : ex2_approx(0.5f * (mo - kShift)),
                                        sg.slot >= 0 ? 1.f : 1.0f / sum);
             void *to = places[kRows * member + lane].sum;
             if (cw == 0 && to) {

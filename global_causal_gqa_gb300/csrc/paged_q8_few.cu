@@ -5,10 +5,10 @@
 // which a warp takes 32.  S^T = Y Q^T and O^T += Z^T P^T are m16n8k16 f16 MMAs with the keys, and
 // then the dims, as M and the rows as N.  The e4m3 numbers become f16 exactly, two per instruction
 // in registers (mma.sync's own 8-bit form takes longer than the 16-bit one: 33 cycles against 22 in
-// a chain).  A query row is brought to f16 by a power of two of its own; P = 2^(x + b - mo + 9) with
-// b its value's exponent, so a value's power of two is in its weight and the numbers multiply as
-// they are.  l sums the weights relative to 2^m, O relative to 2^(mo - 9), mo the largest x + b seen:
-// either range alone may be far from the other's.  Both references move when something exceeds them
+// a chain).  A query row is brought to f16 by a power of two of its own; P = 2^(x - m + b - mo + 9)
+// with b its value's exponent, so a value's power of two is in its weight and the numbers multiply as
+// they are.  l sums the weights relative to 2^m, O relative to 2^(m + mo - 9), mo the largest x - m + b
+// seen: either range alone may be far from the other's.  Both references move when something exceeds them
 // by 2^6; P lies between 2^15 and 2^-24, 2^-33 of the reference.
 //
 // A stage takes a warp 1800 cycles, the copies of a stage 1365: with few pairs per CTA both groups

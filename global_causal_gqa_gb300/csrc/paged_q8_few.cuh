@@ -83,7 +83,9 @@ struct FewRows {
     uint32_t qb[8][2];
     float sl[2];                              // the factor of a score of rows 2tq, + 1, log2 units
     float o[8][4];                            // dims 16 i + gq (+ 8 for the second pair)
-    float m[2], mr[2], mo[2], l[2];           // mr: m, or 0 while m is -inf
+    // mr: m, or 0 while m is -inf.  mo: the largest score plus its value's exponent, less mr (kept
+    // relative: next to a score of 2^24 an exponent is lost in fp32).
+    float m[2], mr[2], mo[2], l[2];
 
     // This lane's part of the queries: row gq, zero past the last one, in f16 with the row's largest
     // element brought to [2^14, 2^15); what that leaves of a number below 2^-14 is a multiple of
@@ -186,7 +188,7 @@ struct FewRows {
         }
         // ---- online softmax
         bool grow = false;
-        float top[2], topo[2];
+        float top[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             float t = -CUDART_INF_F, to = -CUDART_INF_F;
@@ -195,26 +197,30 @@ struct FewRows {
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
                     t = fmaxf(t, x[b][2 * f + c]);
-                    to = fmaxf(to, x[b][2 * f + c] + ev[b][f]);
+                    to = fmaxf(to, x[b][2 * f + c] - mr[c] + ev[b][f]);
                 }
             top[c] = t;
-            topo[c] = to;
-            grow |= top[c] > m[c] + kGrow || to > mo[c] + kGrow;
+            grow |= t > m[c] + kGrow || to > mo[c] + kGrow;
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float mx = top[c], mxo = topo[c];
+                float mx = top[c], mxo = -CUDART_INF_F;
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                const float mn = fmaxf(m[c], mx), mrn = mn == -CUDART_INF_F ? 0.f : mn;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) mxo = fmaxf(mxo, x[b][2 * f + c] - mrn + ev[b][f]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
                     mxo = fmaxf(mxo, __shfl_xor_sync(0xffffffffu, mxo, d));
-                }
-                const float mn = fmaxf(m[c], mx), mno = fmaxf(mo[c], mxo);
+                const float was = mo[c] + (mr[c] - mrn), mno = fmaxf(was, mxo);
                 const float f = m[c] == -CUDART_INF_F ? 0.f : ex2_approx(m[c] - mn);
-                const float fo = mo[c] == -CUDART_INF_F ? 1.f : ex2_approx(mo[c] - mno);
+                const float fo = mo[c] == -CUDART_INF_F ? 1.f : ex2_approx(was - mno);
                 m[c] = mn;
-                mr[c] = mn == -CUDART_INF_F ? 0.f : mn;
+                mr[c] = mrn;
                 l[c] *= f;
                 mo[c] = mno;
 #pragma unroll
@@ -233,8 +239,9 @@ struct FewRows {
             for (int e = 0; e < 4; ++e) {
                 const int c = e & 1;
                 const float ro = mo[c] == -CUDART_INF_F ? 0.f : mo[c] - kShift;
-                w[e] = ex2_approx(x[b][e] - mr[c]);
-                wv[e] = ex2_approx(x[b][e] + (ev[b][e >> 1] - ro));
+                const float d = x[b][e] - mr[c];
+                w[e] = ex2_approx(d);
+                wv[e] = ex2_approx(d + (ev[b][e >> 1] - ro));
             }
             if (edge) {
 #pragma unroll
@@ -303,12 +310,12 @@ struct FewRows {
         }
     }
 
-    // O relative to m: times 2^(mo - 9 - m), in two steps as that may be 2^-135.
+    // O relative to m: times 2^(mo - 9), in two steps as that may be 2^-135.
     __device__ __forceinline__ void finish() {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             if (mo[c] == -CUDART_INF_F) continue;   // O is 0, or NaN
-            const float f = ex2_approx(0.5f * (mo[c] - kShift - m[c]));
+            const float f = ex2_approx(0.5f * (mo[c] - kShift));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 o[i][c] = o[i][c] * f * f;
