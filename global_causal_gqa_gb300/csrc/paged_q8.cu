@@ -56,8 +56,9 @@ static_assert(kWeightTiles == kScoreTiles, "a stage's scores and weights have ti
 constexpr int kScoreCols = 2 * kRows, kValueCols = 3 * kRows;   // columns of a group
 constexpr int kChunk = 16 * kStreamUnit;      // bytes of 16 columns of the weights
 constexpr float kGrow = 3.0f, kShift = 12.0f, kLargest = 32768.0f;   // log2 units; 2^(3 + 12)
-// Values below 2^-100 count as 2^-100 in mo, so that 2^-mo stays within fp32.
-constexpr float kLeast = -100.0f;
+// Values of powers below 2^-112 count as 2^-112 in mo, so that a weight of up to 2^3 times 2^(12 - mo)
+// stays within fp32: the products of the smallest, 2^-126, are 2^-2, and lose 2^-15 of that.
+constexpr float kLeast = -112.0f;
 
 struct Q8Bars : StreamBars {
     uint64_t q_full[4], q_free[4], q_raw;

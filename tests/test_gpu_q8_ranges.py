@@ -1,6 +1,6 @@
 """The 8-bit paged attention at the ends of its numbers' ranges: queries and keys of opposite powers
-of two, factors that vanish, scores far from zero.  By every kernel: a warp per pair (many short
-caches), up to 8 rows, two and four groups, the tile kernel."""
+of two, factors that vanish, scores far from zero, values of tiny powers.  By every kernel: a warp
+per pair (many short caches), up to 8 rows, two and four groups, the tile kernel."""
 import math
 
 import pytest
@@ -98,3 +98,15 @@ def test_scores_far_from_zero(t, n, s, up, far):
             z = 2.0 ** (far + 3) + math.log(m)
             pu.check(p.L[:, p.cu[i] + r], torch.full((8,), z, dtype=torch.float64, device="cuda"),
                      torch.full((8,), z * 2.0 ** -21, dtype=torch.float64, device="cuda"), "lse")
+
+
+@pytest.mark.parametrize("t,n,s", KERNELS[:-1])
+def test_values_of_tiny_powers(t, n, s):
+    """Values of the format's last two powers of two: what is lost of a weight is relative to them,
+    not to a larger value that is not there.  (Not by the tile kernel, to which many of them are
+    below bf16's normal numbers.)"""
+    p = _batch(t, n, s, 953, spread=3)
+    for i in range(n):
+        p.rows[i][3] = (p.rows[i][3].int() - 118).clamp_min(1).to(torch.uint8)
+        p.put(i)
+    _checked(p)
