@@ -895,9 +895,9 @@ Plan plan_of(int max_q, int Hq, int Hkv) {
 
 // The call's tensor maps, {128 numbers, keys of a page, (page, KV head)}, a box of `most` keys of a page
 // at most.  (One map over both pools, their distance as a dimension's stride, brought a page's keys and
-// values by one copy, in pages of 16 tokens 426 instead of 522 us over 32 caches of 8k-64k.  But strides
-// that are not multiples of the ones before are outside what the encoder's description allows, and two
-// runs of random cases ended in a fault, small pools far apart.)
+// values by one copy, in pages of 16 tokens 426 instead of 522 us over 32 caches of 8k-64k.  Two runs of
+// random cases with it ended in a fault, the pools small and far apart.  What in the copy did it is not
+// known; what no other map here does is to span memory that is not its tensor's.)
 bool make_maps(const gqa_paged_kv_q8 &c, int most, CUtensorMap *mk, CUtensorMap *mv) {
     const uint64_t page = c.page_size;
     const uint64_t dims[3] = {kD, page, (uint64_t)c.num_pages * c.Hkv}, strides[2] = {kD, page * kD};
