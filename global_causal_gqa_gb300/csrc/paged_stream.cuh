@@ -452,8 +452,8 @@ __device__ __forceinline__ void produce(const CUtensorMap &tmK, const CUtensorMa
         walk_ahead = PageWalk(p.pages + (long)ahead.seq * p.max_pages,
                               ahead.unit0 * kUnit >> p.page_shift,
                               (ahead.S - 1 >> p.page_shift) + 1);
-        // its queries on their way to L2: two 128-byte lines a row (8-bit: a
-        // warp of their own loads them)
+        // its queries on their way to L2: two 128-byte lines a row (8-bit: they are read a
+        // pair ahead, by a warp of their own or by the consumers before they merge the last)
         if (!S::kQ8 && lane < 2 * ahead.T * p.G) {
             const int r = lane >> 1, t = token_of(p, r);
             prefetch_l2(p.q + (long)(ahead.row0 + t) * p.q_stride +
