@@ -6,8 +6,8 @@
 //
 // By the rows (tokens x heads of a KV group) that a sequence may have: up to 8, paged_q8_few.cu, or
 // paged_q8_short.cu for many short caches; 9 to 96, the kernel below, bound by memory at 16 rows
-// (32 caches of 8k-64k tokens 430 us, 6.3 TB/s) and by its warps at 32 (557 us; blocks of 32 rows
-// read the pages again, from L2 for the most part: 24 drafts of 2-6 tokens of 8 rows 76 us).  More:
+// (32 caches of 8k-64k tokens 435 us, 6.3 TB/s) and by its warps at 32 (557 us; blocks of 32 rows
+// read the pages again, from L2 for the most part: 24 drafts of 2-6 tokens of 8 rows 77 us).  More:
 // all keys that the call sees are expanded to bf16 pages in the workspace (paged_read.cu) and the
 // tile kernel (packed_prefill.cu) takes them from there (24 times 72, 96 and 128 rows over 700-6000
 // tokens: 184, 186 and 190 us so, 158, 169 and 220 in blocks; 16 to 96 rows 179 and 106; 8 times 96

@@ -12,7 +12,7 @@
 // by 2^6; P lies between 2^15 and 2^-24, 2^-33 of the reference.
 //
 // A stage takes a warp 1800 cycles, the copies of a stage 1365: with few pairs per CTA both groups
-// of four warps take a pair's stages in turn (BOTH; 32 caches of 8k-64k tokens 529 -> 399 us, 6.8
+// of four warps take a pair's stages in turn (BOTH; 32 caches of 8k-64k tokens 529 -> 401 us, 6.8
 // TB/s, which is HBM), else the pairs, so that one's ends pass while the other streams (64
 // windows of 2048: 57 us in pages of 64, 4.6 TB/s, of them 5 of start and 5 of the merge; 69 in pages
 // of 16, whose 16 copies a stage the producer issues one after the other).  The

@@ -6,7 +6,7 @@
 // eight warps share it, and the code that only the ends run misses the instruction caches: 256 chats
 // of 20-450 tokens, 8 heads, 57 us.  Here a warp takes a whole pair, 32 keys at a time, issues its
 // own copies, a few steps ahead and over the ends of pairs, and writes the result from its
-// registers: no warp waits for another (39 us, 3.2 TB/s; 1024 such chats 97 us, 5.4 TB/s; twelve
+// registers: no warp waits for another (39 us, 3.2 TB/s; 1024 such chats 99 us, 5.3 TB/s; twelve
 // warps with two steps in flight each: eight with three 45 us, nine with three 44).  It needs as many
 // pairs as warps to fill the GPU.
 #include "paged_q8_few.cuh"
